@@ -251,8 +251,9 @@ def _plain_decode(s):
 def _plain_store(s):
     x = s["state"]
     amax = x.abs().amax(-1, keepdim=True)
-    scale = amax / 127.0
-    inverse = torch.where(amax > 0, 127.0 / amax, 0.0)
+    top = torch.full_like(amax, 127.0)                                    # tensors on both sides: one IEEE division each
+    scale = amax / top
+    inverse = torch.where(amax > 0, top / amax, 0.0)
     codes = (x * inverse).round().clamp(-127, 127).to(torch.int8)
     keep = s["slots"] >= 0
     at = s["slots"][keep].long()
