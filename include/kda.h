@@ -58,9 +58,10 @@ typedef enum {
                                 exceeded 6e4 in magnitude (or was not finite) */
     KDA_ERR_SCRATCH_TOO_SMALL = 8, /* kda_chunk_fwd_static_scratch: the problem needs more
                                       scratch than KDA_STATIC_SCRATCH_BYTES */
-    KDA_ERR_BOUNDS = 9 /* device, only in a library compiled with -DKDA_DEBUG_BOUNDS: an
+    KDA_ERR_BOUNDS = 9, /* device, only in a library compiled with -DKDA_DEBUG_BOUNDS: an
                           index checked before a global-memory access fell outside its
                           buffer; that access was skipped (no trap) */
+    KDA_ERR_BAD_SLOT = 10 /* device: a state-cache slot below -1 or not below num_slots */
 } kda_status_t;
 
 #define KDA_HEAD_DIM 128
@@ -449,6 +450,127 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
                             int32_t num_seqs, int32_t tokens_per_seq, int32_t num_heads, int32_t head_dim_k,
                             int32_t head_dim_v, const float *initial_state, float scale, float lower_bound,
                             float *o, float *final_state, int32_t *status_dev, kda_stream_t stream);
+
+/*
+ * kda_linear_chunk_fwd — linear attention with one decay for each head (no
+ * delta rule) over varlen-packed prompts, for layers that share KDA's state
+ * [N,H,128,128], packing and serving path:
+ *       S_t = e^{g_t} S_{t-1} + k_t v_t^T,      o_t = scale * S_t^T q_t
+ * with g_t one number per (token, head), or one per head at every token. It is
+ * computed chunk by chunk (128 tokens) on the tensor cores: with G_i the sum of
+ * the chunk's g up to token i,
+ *       o_i = scale * (e^{G_i} S^T q_i + sum_{j<=i} e^{G_i-G_j} (q_i.k_j) v_j)
+ *       S  <- e^{G_end} S + sum_j e^{G_end-G_j} k_j v_j^T
+ * (every exponent is a sum of g <= 0, so no factor exceeds 1). Sequences of few
+ * tokens run the recurrence itself.
+ * (Not part of the method's pages.)
+ *   q, k          bf16, num_qk_heads heads of 128 channels per token; value head
+ *                 h reads query/key head h / (num_heads / num_qk_heads), so
+ *                 num_qk_heads divides num_heads.
+ *   v             bf16, num_heads heads of 128 channels per token.
+ *   *_token_stride  elements from one token to the next (>= heads x 128, a
+ *                 multiple of 8): q, k and v may be slices of one projection.
+ *   g             fp32 natural-log decay, g <= 0 (-inf forgets everything; a g
+ *                 below -138 counts as -inf): [total_tokens, num_heads] with
+ *                 g_per_token = 1, [num_heads] with 0.
+ *   cu_seqlens    int32 [num_seqs + 1]: cu[0] = 0, nondecreasing, cu[num_seqs] <=
+ *                 total_tokens. Rows of o behind the last sequence are left as
+ *                 they were, and q, k, v, g there are not used.
+ *   initial_state fp32 [num_seqs, num_heads, 128, 128] (key rows) or NULL for zeros.
+ * Outputs:
+ *   o             bf16 [total_tokens, num_heads, 128], contiguous.
+ *   final_state   fp32 [num_seqs, num_heads, 128, 128] or NULL; may be the same
+ *                 pointer as initial_state. An empty sequence's final state is
+ *                 its initial state.
+ *   status_dev    optional device int32, zeroed on the stream, then the first of
+ *                 KDA_ERR_GATE_RANGE (some g > 0 or NaN), KDA_ERR_BAD_SEQLENS (that
+ *                 sequence is skipped), KDA_ERR_TIMEOUT.
+ *   workspace     kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte aligned
+ *                 (NULL when that is 0); not shared by calls that overlap.
+ * Precision: products of bf16 operands with fp32 accumulation; the state is kept
+ * and updated in fp32, its update's operands split into two bf16 terms (relative
+ * error of final_state about 1e-6); the decayed scores and the copy of the state
+ * that q multiplies are rounded to bf16, as o is.
+ * q, k, v must be finite: a non-finite value may reach every output of its
+ * sequence from the start of its chunk on. Alignment: q, k, v, o and the
+ * states 16 bytes (32 for the states), g, cu_seqlens and status_dev 4.
+ */
+kda_status_t kda_linear_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
+                                  const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                  int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
+                                  int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                  int32_t g_per_token, const float *initial_state, float scale, void *o,
+                                  float *final_state, int32_t *status_dev, void *workspace, size_t workspace_bytes,
+                                  kda_stream_t stream);
+
+/* Workspace bytes of kda_linear_chunk_fwd for these sizes on the current device
+ * (0: none needed, or invalid arguments). */
+size_t kda_linear_chunk_fwd_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t num_heads);
+
+/*
+ * kda_linear_decode_fwd — the recurrence of kda_linear_chunk_fwd for
+ * tokens_per_seq (0 .. KDA_DECODE_MAX_TOKENS) tokens of each sequence, state in
+ * and out: token t of sequence n is row n * tokens_per_seq + t of q, k, v, g, o.
+ * Arguments, layouts, aliasing and errors as there; fp32 throughout, o rounded
+ * once to bf16. One launch; the state is read and written once.
+ */
+kda_status_t kda_linear_decode_fwd(const void *q, const void *k, const void *v, const float *g, int32_t num_seqs,
+                                   int32_t tokens_per_seq, int32_t num_heads, int32_t num_qk_heads,
+                                   int32_t head_dim_k, int32_t head_dim_v, int64_t q_token_stride,
+                                   int64_t k_token_stride, int64_t v_token_stride, int32_t g_per_token,
+                                   const float *initial_state, float scale, void *o, float *final_state,
+                                   int32_t *status_dev, kda_stream_t stream);
+
+/*
+ * kda_state_store / kda_state_load — a cache of recurrent states (the state
+ * after a prefix sums that prefix up) in int8 with one fp32 scale per key row:
+ * 16.5 KB per head where the fp32 state takes 64 KB. Both work on the states of
+ * the prefill and decode calls above. (Not part of the method's pages.)
+ *   state   fp32 [num_rows, num_heads, 128, 128]
+ *   slots   int32 [num_rows]: the cache slot of each row; -1: none
+ *   codes   int8 [num_slots, num_heads, 128, 128]
+ *   scales  fp32 [num_slots, num_heads, 128]
+ * store: scale = amax / 127 with amax the largest magnitude of the key row, code =
+ *   round-to-nearest-even(x * (127 / amax)), so that code * scale is off by at
+ *   most amax / 254 (and rounding in fp32). A row with amax < 2^-100 gets scale 0
+ *   and codes 0; a row with a NaN or an infinity gets scale NaN and codes 0, so
+ *   that it reads back as NaN. Rows with slot -1 are skipped, and slots that no row
+ *   names are left as they were; of several rows with one slot the last is stored.
+ * load: state = code * scale; a row with slot -1 becomes zeros (no cached prefix).
+ * A slot below -1 or not below num_slots counts as -1 and sets *status_dev
+ * (optional, zeroed on the stream) to KDA_ERR_BAD_SLOT. Alignment: state 32
+ * bytes, codes 16, the others 4. One launch, asynchronous on `stream`.
+ */
+kda_status_t kda_state_store(const float *state, const int32_t *slots, int32_t num_rows, int32_t num_heads,
+                             int32_t head_dim_k, int32_t head_dim_v, int32_t num_slots, void *codes, float *scales,
+                             int32_t *status_dev, kda_stream_t stream);
+kda_status_t kda_state_load(const void *codes, const float *scales, const int32_t *slots, int32_t num_rows,
+                            int32_t num_heads, int32_t head_dim_k, int32_t head_dim_v, int32_t num_slots,
+                            float *state, int32_t *status_dev, kda_stream_t stream);
+
+/*
+ * kda_add_rms_norm — a layer's input: the residual's addition, the RMS norm and
+ * the rounding to 8 bits for the layer's projections, in one pass:
+ *     h = x + residual;   residual_out = h rounded to the residual's type
+ *     n = h / sqrt(mean(h^2) + eps) * weight          (h not rounded)
+ *     y_scale = max|n| / 448;   y = e4m3(n / y_scale), round to nearest even
+ * per row. (The output end of the layer is kda_chunk_fwd_gated_norm; the pages
+ * leave this end out.)
+ *   x             bf16 [rows, width], width 1 .. 32768
+ *   residual      bf16, or fp32 with residual_fp32 = 1: [rows, width]
+ *   weight        fp32 [width]
+ *   residual_out  like residual; may be the same pointer
+ *   y             e4m3 [rows, width];  y_scale  fp32 [rows]
+ * Sums and norms are fp32. A row whose max|n| is below 2^-100 gets scale 0 and
+ * codes 0; a row with a NaN or an infinity, or whose sum of squares overflows
+ * fp32, gets scale NaN and codes NaN.
+ * Alignment: x, residual, residual_out, weight, y 16 bytes, y_scale 4.
+ * Contiguous rows; one launch, asynchronous on `stream`.
+ */
+#define KDA_NORM_MAX_WIDTH 32768
+kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *weight, int64_t rows, int32_t width,
+                              float eps, int32_t residual_fp32, void *residual_out, void *y, float *y_scale,
+                              kda_stream_t stream);
 
 /* Number of kernel launches one kda_chunk_fwd call makes for these sizes
  * (0 when num_seqs == 0). Host-only, no CUDA call. */

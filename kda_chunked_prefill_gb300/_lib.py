@@ -26,6 +26,7 @@ KDA_ERR_TIMEOUT = 6
 KDA_ERR_VALUE_RANGE = 7
 KDA_ERR_SCRATCH_TOO_SMALL = 8
 KDA_ERR_BOUNDS = 9
+KDA_ERR_BAD_SLOT = 10
 KDA_DEBUG_WITHHOLD_READY = 1
 KDA_DEBUG_WY_PRODUCER = 2  # the producer CTAs form the WY product
 KDA_DEBUG_WY_CONSUMER = 4  # the consumer CTAs form it
@@ -37,9 +38,11 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_stat
             "kda_chunk_fwd_debug", "kda_chunk_fwd_raw_gates", "kda_chunk_fwd_gated_norm", "kda_chunk_fwd_split",
             "kda_chunk_fwd_split_plan", "kda_chunk_fwd_split_workspace_size", "kda_chunk_fwd_host", "kda_chunk_fwd_plan",
             "kda_chunk_fwd_host_buffer_size", "kda_decode_fwd",
-            "kda_chunk_fwd_launches",
+            "kda_chunk_fwd_launches", "kda_linear_chunk_fwd", "kda_linear_chunk_fwd_workspace_size",
+            "kda_linear_decode_fwd", "kda_state_store", "kda_state_load", "kda_add_rms_norm",
             "kda_status_string", "kda_version")
 DECODE_MAX_TOKENS = 64
+NORM_MAX_WIDTH = 32768
 
 _lock = threading.Lock()
 _lib = None
@@ -96,6 +99,20 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_chunk_fwd_host_buffer_size.restype = ctypes.c_size_t
         lib.kda_decode_fwd.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, f32, f32, vp, vp, vp, vp]
         lib.kda_decode_fwd.restype = ctypes.c_int
+        lib.kda_linear_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, i64, i64, i64, i32, vp,
+                                             f32, vp, vp, vp, vp, ctypes.c_size_t, vp]
+        lib.kda_linear_chunk_fwd.restype = ctypes.c_int
+        lib.kda_linear_chunk_fwd_workspace_size.argtypes = [i32, i64, i32]
+        lib.kda_linear_chunk_fwd_workspace_size.restype = ctypes.c_size_t
+        lib.kda_linear_decode_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i64, i64, i32, vp, f32,
+                                              vp, vp, vp, vp]
+        lib.kda_linear_decode_fwd.restype = ctypes.c_int
+        lib.kda_state_store.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]
+        lib.kda_state_store.restype = ctypes.c_int
+        lib.kda_state_load.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+        lib.kda_state_load.restype = ctypes.c_int
+        lib.kda_add_rms_norm.argtypes = [vp, vp, vp, i64, i32, f32, i32, vp, vp, vp, vp]
+        lib.kda_add_rms_norm.restype = ctypes.c_int
         lib.kda_chunk_fwd_workspace_size.argtypes = [i32, i32]
         lib.kda_chunk_fwd_workspace_size.restype = ctypes.c_size_t
         lib.kda_chunk_fwd_launches.argtypes = [i32, i64, i32]
@@ -472,3 +489,282 @@ def decode_fwd(q, k, v, g, beta, num_seqs: int, state=None, scale: Optional[floa
         if code != KDA_OK:
             raise KdaError(code, "kda_decode_fwd (device)")
     return o, fs
+
+
+# ------------------------------------------------------------------ linear attention with one decay per head
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _on(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _heads_view(t, name, tokens, device):
+    """Check a [T, heads, 128] bf16 tensor whose tokens may be strided (a slice
+    of a wider projection); returns its token stride in elements."""
+    if t.dtype != _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens:
+        raise ValueError(f"{name} must have shape ({tokens}, heads, head_dim), got {tuple(t.shape)}")
+    _on(t, name, device)
+    heads, dim = t.shape[1], t.shape[2]
+    if tokens == 0:
+        return heads * dim
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != dim and heads > 1):
+        raise ValueError(f"{name} must hold its heads and channels contiguously within a token")
+    if tokens == 1:
+        return heads * dim
+    if st < heads * dim or st % 8:
+        raise ValueError(f"{name}'s tokens must not overlap and lie a multiple of 8 elements apart")
+    return st
+
+
+def _linear_args(q, k, v, g, o, initial_state, final_state, num_seqs, status):
+    """The checks kda_linear_chunk_fwd and kda_linear_decode_fwd share."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must have shape (tokens, heads, head_dim)")
+    T, Hk, D = q.shape
+    H, V = v.shape[1], v.shape[2]
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    strides = (_heads_view(q, "q", T, dev), _heads_view(k, "k", T, dev), _heads_view(v, "v", T, dev))
+    if k.shape != q.shape:
+        raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"the number of value heads ({H}) must be a multiple of the query/key heads ({Hk})")
+    per_token = g.dim() == 2
+    _check(g, "g", _F32, (T, H) if per_token else (H,), dev)
+    _check(o, "o", _BF16, (T, H, V), dev)
+    for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
+        if t is not None:
+            _check(t, name, _F32, (num_seqs, H, D, V), dev)
+    if status is not None:
+        _check(status, "status", _I32, (1,), dev)
+    return T, H, Hk, D, V, dev, strides, int(per_token)
+
+
+def linear_workspace_size(num_seqs: int, total_tokens: int, num_heads: int) -> int:
+    """Workspace bytes ``kda_linear_chunk_fwd`` needs on the current CUDA device (0: none)."""
+    return int(load_library().kda_linear_chunk_fwd_workspace_size(int(num_seqs), int(total_tokens), int(num_heads)))
+
+
+def _raise(rc, what):
+    raise KdaError(rc, what)
+
+
+def kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale: float, o, final_state, status=None, stream=None,
+                         workspace=None) -> int:
+    """Call the C entry point ``kda_linear_chunk_fwd`` with caller-allocated outputs.
+
+    q, k: bf16 [T,Hk,128]; v: bf16 [T,H,128], H a multiple of Hk (tokens may be
+    strided); g: fp32 log decay [T,H], or [H] for one decay per head; cu_seqlens:
+    int32 [N+1]; initial_state / final_state: fp32 [N,H,128,128] or None (may be
+    the same tensor); o: bf16 [T,H,128]; status: int32 [1] or None; workspace:
+    uint8 tensor of ``linear_workspace_size(N, T, H)`` bytes (default: a new one
+    from torch's allocator for the call's stream). All on one CUDA device.
+    Raises ``KdaError`` on a host-side error; returns ``KDA_OK`` once queued.
+    """
+    N = cu_seqlens.shape[0] - 1
+    T, H, Hk, D, V, dev, (qs, ks, vs), per_token = _linear_args(q, k, v, g, o, initial_state, final_state, N, status)
+    _check(cu_seqlens, "cu_seqlens", _I32, (N + 1,), dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = lib.kda_linear_chunk_fwd_workspace_size(N, T, H)
+            if need:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+        rc = lib.kda_linear_chunk_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, D, V, qs, ks, vs,
+            per_token, _ptr(initial_state), scale, o.data_ptr(), _ptr(final_state), _ptr(status), _ptr(workspace),
+            0 if workspace is None else workspace.numel(), stream.cuda_stream)
+    if rc != KDA_OK:
+        _raise(rc, "kda_linear_chunk_fwd")
+    return rc
+
+
+def _new_on(stream, dev, *specs):
+    """Empty tensors for a call on ``stream`` (None: the current stream)."""
+    if stream is None:
+        return [None if s is None else torch.empty(s[0], dtype=s[1], device=dev) for s in specs]
+    with torch.cuda.stream(stream):
+        return [None if s is None else torch.empty(s[0], dtype=s[1], device=dev) for s in specs]
+
+
+def _raise_device(status, stream, what):
+    if stream is not None:
+        stream.synchronize()
+    code = int(status.item())
+    if code != KDA_OK:
+        raise KdaError(code, f"{what} (device)")
+
+
+def linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, scale: Optional[float] = None,
+                     output_final_state: bool = True, check: bool = False, stream=None):
+    """Allocate ``o`` (and ``final_state``) and run ``kda_linear_chunk_fwd``.
+
+    Returns ``(o, final_state)``; ``final_state`` is None when not requested. With
+    ``check=True`` the device status word is read back (a synchronising copy)
+    and a device-detected error raises ``KdaError``. Rows of ``o`` behind the last
+    sequence are not written.
+    """
+    dev, H, N = q.device, v.shape[1], cu_seqlens.shape[0] - 1
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+    o, fs, status = _new_on(stream, dev, (v.shape, _BF16),
+                            ((N, H, q.shape[2], v.shape[2]), _F32) if output_final_state else None,
+                            ((1,), _I32) if check else None)
+    kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale, o, fs, status, stream)
+    if check:
+        _raise_device(status, stream, "kda_linear_chunk_fwd")
+    return o, fs
+
+
+def kda_linear_decode_fwd(q, k, v, g, num_seqs: int, initial_state, scale: float, o, final_state, status=None,
+                          stream=None) -> int:
+    """Call the C entry point ``kda_linear_decode_fwd`` with caller-allocated
+    outputs: sequence n's tokens are rows n*Tn .. n*Tn+Tn-1 of q, k, v, g and o;
+    tensors as in ``kda_linear_chunk_fwd``."""
+    N = int(num_seqs)
+    T = q.shape[0]
+    if N < 0 or (N == 0 and T != 0) or (N > 0 and T % N != 0):
+        raise ValueError("q must hold the same number of tokens for every sequence")
+    T, H, Hk, D, V, dev, (qs, ks, vs), per_token = _linear_args(q, k, v, g, o, initial_state, final_state, N, status)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        rc = load_library().kda_linear_decode_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), N, T // N if N else 0, H, Hk, D, V, qs, ks, vs,
+            per_token, _ptr(initial_state), scale, o.data_ptr(), _ptr(final_state), _ptr(status), stream.cuda_stream)
+    if rc != KDA_OK:
+        _raise(rc, "kda_linear_decode_fwd")
+    return rc
+
+
+def linear_decode_fwd(q, k, v, g, num_seqs: int, state=None, scale: Optional[float] = None, in_place: bool = False,
+                      check: bool = False, stream=None):
+    """Run ``kda_linear_decode_fwd``; returns ``(o, final_state)``. With
+    ``in_place`` the given ``state`` tensor is updated and returned as ``final_state``."""
+    dev, H, N = q.device, v.shape[1], int(num_seqs)
+    if scale is None:
+        scale = q.shape[2] ** -0.5
+    if in_place and state is None:
+        raise ValueError("in_place needs a state tensor")
+    o, fs, status = _new_on(stream, dev, (v.shape, _BF16),
+                            None if in_place else ((N, H, q.shape[2], v.shape[2]), _F32), ((1,), _I32) if check else None)
+    fs = state if in_place else fs
+    kda_linear_decode_fwd(q, k, v, g, N, state, scale, o, fs, status, stream)
+    if check:
+        _raise_device(status, stream, "kda_linear_decode_fwd")
+    return o, fs
+
+
+# ------------------------------------------------------------------ the int8 cache of states
+def _cache_args(state, slots, codes, scales, status):
+    if state.dim() != 4:
+        raise ValueError("state must have shape (rows, heads, 128, 128)")
+    M, H, K, V = state.shape
+    dev = state.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    slots_n = codes.shape[0]
+    _check(state, "state", _F32, (M, H, K, V), dev)
+    _check(slots, "slots", _I32, (M,), dev)
+    _check(codes, "codes", torch.int8, (slots_n, H, K, V), dev)
+    _check(scales, "scales", _F32, (slots_n, H, K), dev)
+    if status is not None:
+        _check(status, "status", _I32, (1,), dev)
+    return M, H, K, V, slots_n, dev
+
+
+def kda_state_store(state, slots, codes, scales, status=None, stream=None) -> int:
+    """Call the C entry point ``kda_state_store``: quantise state (fp32
+    [M,H,128,128]) into the slots (int32 [M], -1: none) of the cache codes (int8
+    [S,H,128,128]) and scales (fp32 [S,H,128])."""
+    M, H, K, V, S, dev = _cache_args(state, slots, codes, scales, status)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        rc = load_library().kda_state_store(state.data_ptr(), slots.data_ptr(), M, H, K, V, S, codes.data_ptr(),
+                                            scales.data_ptr(), _ptr(status), stream.cuda_stream)
+    if rc != KDA_OK:
+        _raise(rc, "kda_state_store")
+    return rc
+
+
+def kda_state_load(codes, scales, slots, state, status=None, stream=None) -> int:
+    """Call the C entry point ``kda_state_load``: read the slots of the cache
+    back into ``state`` (a row with slot -1 becomes zeros)."""
+    M, H, K, V, S, dev = _cache_args(state, slots, codes, scales, status)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        rc = load_library().kda_state_load(codes.data_ptr(), scales.data_ptr(), slots.data_ptr(), M, H, K, V, S,
+                                           state.data_ptr(), _ptr(status), stream.cuda_stream)
+    if rc != KDA_OK:
+        _raise(rc, "kda_state_load")
+    return rc
+
+
+def state_store(state, slots, codes, scales, check: bool = False, stream=None) -> None:
+    """Run ``kda_state_store``; with ``check`` a bad slot raises ``KdaError``."""
+    status = _new_on(stream, state.device, ((1,), _I32))[0] if check else None
+    kda_state_store(state, slots, codes, scales, status, stream)
+    if check:
+        _raise_device(status, stream, "kda_state_store")
+
+
+def state_load(codes, scales, slots, check: bool = False, stream=None):
+    """Allocate the states fp32 [M,H,128,128] and run ``kda_state_load``."""
+    state, status = _new_on(stream, codes.device, ((slots.shape[0], *codes.shape[1:]), _F32), ((1,), _I32) if check else None)
+    kda_state_load(codes, scales, slots, state, status, stream)
+    if check:
+        _raise_device(status, stream, "kda_state_load")
+    return state
+
+
+# ------------------------------------------------------------------ residual addition, RMS norm, e4m3 output
+def kda_add_rms_norm(x, residual, weight, eps: float, residual_out, y, y_scale, stream=None) -> int:
+    """Call the C entry point ``kda_add_rms_norm``: x bf16 [..., d]; residual and
+    residual_out (may be the same tensor) bf16 or fp32 like x; weight fp32 [d];
+    y float8_e4m3fn like x; y_scale fp32 [...]."""
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    shape, d = x.shape, x.shape[-1]
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be CUDA tensors")
+    if residual.dtype not in (_BF16, _F32):
+        raise TypeError(f"residual must be {_BF16} or {_F32}, got {residual.dtype}")
+    _check(x, "x", _BF16, shape, dev)
+    _check(residual, "residual", residual.dtype, shape, dev)
+    _check(residual_out, "residual_out", residual.dtype, shape, dev)
+    _check(weight, "weight", _F32, (d,), dev)
+    _check(y, "y", torch.float8_e4m3fn, shape, dev)
+    _check(y_scale, "y_scale", _F32, shape[:-1], dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.device(dev):
+        rc = load_library().kda_add_rms_norm(x.data_ptr(), residual.data_ptr(), weight.data_ptr(), y_scale.numel(), d,
+                                             eps, int(residual.dtype == _F32), residual_out.data_ptr(), y.data_ptr(),
+                                             y_scale.data_ptr(), stream.cuda_stream)
+    if rc != KDA_OK:
+        _raise(rc, "kda_add_rms_norm")
+    return rc
+
+
+def add_rms_norm(x, residual, weight, eps: float = 1e-6, in_place: bool = False, stream=None):
+    """Run ``kda_add_rms_norm``; returns ``(y, y_scale, residual_out)``. With
+    ``in_place`` the given ``residual`` is updated and returned."""
+    y, y_scale, res = _new_on(stream, x.device, (x.shape, torch.float8_e4m3fn), (x.shape[:-1], _F32),
+                              None if in_place else (residual.shape, residual.dtype))
+    res = residual if in_place else res
+    kda_add_rms_norm(x, residual, weight, eps, res, y, y_scale, stream)
+    return y, y_scale, res

@@ -1,0 +1,128 @@
+// kda_linear_decode_fwd: the recurrence of the linear attention with one decay
+// per head, token after token, state in and out:
+//     S <- e^{g_t} S + k_t v_t^T ;  o_t = scale S^T q_t
+//
+// One CTA per (sequence, head, quarter of the value columns), state in
+// registers. Unlike the delta rule the update needs no k^T S, so a token costs
+// one reduction: every thread updates its 8 key rows x 4 columns and adds up
+// q_c S_cv over them, lanes that share columns add by shuffles, the four warps
+// through shared memory. Everything is fp32; o is rounded once.
+//
+// Bound by memory: 64 KB of state read and written per (sequence, head) and
+// call. A warp reads 4 key rows x 128 bytes per access, 8 accesses in flight.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kda.h"
+#include "kda_checks.h"
+#include "kda_common.cuh"
+#include "kda_linear.h"
+
+namespace kda {
+namespace lin {
+namespace dec {
+
+constexpr int THREADS = 128;
+constexpr int QUARTERS = 4;
+constexpr int COLS = DV / QUARTERS;
+constexpr int BATCH = 4;  // tokens staged in shared memory at a time
+
+template <bool VARLEN>
+__global__ void __launch_bounds__(THREADS) kda_linear_recurrent_kernel(const Params p) {
+    __shared__ float sk[BATCH][DK], sq[BATCH][DK], sv[BATCH][COLS], sd[BATCH];
+    __shared__ float part[2][4][COLS];
+    const int quarter = blockIdx.x % QUARTERS;
+    const int64_t chain = blockIdx.x / QUARTERS;  // n * H + h
+    const int n = static_cast<int>(chain / p.H), h = static_cast<int>(chain % p.H), hk = h / p.rep;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int col = COLS * quarter + 4 * (lane & 7);
+    const int row0 = 32 * warp + (lane >> 3);  // and every 4th row up to row0 + 28
+
+    int64_t bos, len;
+    if (VARLEN) {
+        const int64_t b = p.cu[n], e = p.cu[n + 1];
+        if (b < 0 || e < b || e > p.T || p.cu[0] != 0) {
+            if (tid == 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
+            return;
+        }
+        bos = b;
+        len = e - b;
+    } else {
+        bos = static_cast<int64_t>(n) * p.steps;
+        len = p.steps;
+    }
+
+    const size_t sbase = static_cast<size_t>(chain) * (DK * DV) + static_cast<size_t>(row0) * DV + col;
+    float4 S[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        S[r] = p.s0 ? *reinterpret_cast<const float4 *>(p.s0 + sbase + 4 * r * DV) : make_float4(0.f, 0.f, 0.f, 0.f);
+
+    bool gate_bad = false;
+    for (int64_t t0 = 0; t0 < len; t0 += BATCH) {
+        const int steps = static_cast<int>(len - t0 < BATCH ? len - t0 : BATCH);
+        if (t0) __syncthreads();  // the last batch has been read
+        for (int u = 0; u < steps; ++u) {
+            const int64_t t = bos + t0 + u;
+            sk[u][tid] = __bfloat162float(p.k[t * p.ks + hk * DK + tid]);
+            sq[u][tid] = __bfloat162float(p.q[t * p.qs + hk * DK + tid]);
+            if (tid < COLS) sv[u][tid] = __bfloat162float(p.v[t * p.vs + h * DV + COLS * quarter + tid]);
+            if (tid == 0) {
+                const float g = p.g[p.g_per_token ? t * p.H + h : h];
+                gate_bad |= !(g <= 0.f);
+                sd[u] = g < G_FLOOR ? 0.f : expf(g);
+            }
+        }
+        __syncthreads();
+        for (int u = 0; u < steps; ++u) {
+            const float d = sd[u];
+            const float4 v = *reinterpret_cast<const float4 *>(&sv[u][4 * (lane & 7)]);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float kk = sk[u][row0 + 4 * r], qq = sq[u][row0 + 4 * r];
+                S[r].x = fmaf(kk, v.x, d * S[r].x);
+                S[r].y = fmaf(kk, v.y, d * S[r].y);
+                S[r].z = fmaf(kk, v.z, d * S[r].z);
+                S[r].w = fmaf(kk, v.w, d * S[r].w);
+                a.x = fmaf(qq, S[r].x, a.x);
+                a.y = fmaf(qq, S[r].y, a.y);
+                a.z = fmaf(qq, S[r].z, a.z);
+                a.w = fmaf(qq, S[r].w, a.w);
+            }
+#pragma unroll
+            for (int s = 8; s <= 16; s <<= 1) {
+                a.x += __shfl_xor_sync(0xffffffffu, a.x, s);
+                a.y += __shfl_xor_sync(0xffffffffu, a.y, s);
+                a.z += __shfl_xor_sync(0xffffffffu, a.z, s);
+                a.w += __shfl_xor_sync(0xffffffffu, a.w, s);
+            }
+            float(*mine)[COLS] = part[u & 1];
+            if (lane < 8) *reinterpret_cast<float4 *>(&mine[warp][4 * lane]) = a;
+            __syncthreads();  // (the other half of part[] is read before the next token's barrier)
+            if (tid < COLS) {
+                const float o = p.scale * ((mine[0][tid] + mine[1][tid]) + (mine[2][tid] + mine[3][tid]));
+                p.o[((bos + t0 + u) * p.H + h) * DV + COLS * quarter + tid] = __float2bfloat16_rn(o);
+            }
+        }
+    }
+    if (p.sT) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) *reinterpret_cast<float4 *>(p.sT + sbase + 4 * r * DV) = S[r];
+    }
+    if (gate_bad) set_status(p.status, KDA_ERR_GATE_RANGE);
+}
+
+}  // namespace dec
+
+cudaError_t launch_recurrent(const Params &p, cudaStream_t stream) {
+    const int grid = p.N * p.H * dec::QUARTERS;  // the caller has checked that this fits
+    if (p.cu)
+        dec::kda_linear_recurrent_kernel<true><<<grid, dec::THREADS, 0, stream>>>(p);
+    else
+        dec::kda_linear_recurrent_kernel<false><<<grid, dec::THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace lin
+}  // namespace kda

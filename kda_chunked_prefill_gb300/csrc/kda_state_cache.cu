@@ -1,0 +1,180 @@
+// kda_state_store / kda_state_load: recurrent states in int8 with one fp32
+// scale per key row, written to and read from the slots of a cache.
+//
+//     scale_i = max_j |S_ij| / 127,  code_ij = rint(S_ij * (127 / max_j |S_ij|)),  S'_ij = code_ij * scale_i
+//
+// A key row has one size (its channel's decays), rows of one state differ: hence
+// a scale per row. Eight bits on a linear grid: for the near-normal entries of
+// a row the error is about 0.6 % of the row's size where e4m3 gives 2.6 %.
+//
+// Both are bound by memory: 64 KB of fp32 and 16.5 KB of codes and scales per
+// state and head, each touched once. 16 lanes hold a row, 8 columns each (32-byte
+// fp32 and 8-byte code accesses, whole sectors); a warp keeps eight rows in flight.
+#include <cuda_runtime.h>
+
+#include "kda.h"
+#include "kda_checks.h"
+#include "kda_common.cuh"
+
+namespace kda {
+namespace cache {
+
+constexpr int THREADS = 256;
+constexpr int ROWS_PER_CTA = 64;  // key rows: 8 warps x 8 rows
+constexpr int PARTS = DK / ROWS_PER_CTA;
+constexpr float TINY = 7.888609052210118e-31f;  // 2^-100: below it a row counts as zero
+
+struct F8 {
+    float v[8];
+};
+__device__ __forceinline__ F8 ld8(const float *p) {
+    F8 r;
+    asm volatile("ld.global.nc.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r.v[0]), "=f"(r.v[1]), "=f"(r.v[2]), "=f"(r.v[3]), "=f"(r.v[4]), "=f"(r.v[5]), "=f"(r.v[6]),
+                   "=f"(r.v[7])
+                 : "l"(p));
+    return r;
+}
+__device__ __forceinline__ void st8(float *p, const F8 &r) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(r.v[0]), "f"(r.v[1]), "f"(r.v[2]),
+                 "f"(r.v[3]), "f"(r.v[4]), "f"(r.v[5]), "f"(r.v[6]), "f"(r.v[7])
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_s8(const float *x, float inv) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u |= (static_cast<uint32_t>(__float2int_rn(x[i] * inv)) & 0xffu) << (8 * i);
+    return u;
+}
+
+__global__ void __launch_bounds__(THREADS) kda_state_store_kernel(const float *__restrict__ state,
+                                                                  const int32_t *__restrict__ slots, int32_t M,
+                                                                  int32_t H, int32_t num_slots,
+                                                                  int8_t *__restrict__ codes,
+                                                                  float *__restrict__ scales, int32_t *status) {
+    const int part = blockIdx.x % PARTS;
+    const int64_t mh = blockIdx.x / PARTS;
+    const int m = static_cast<int>(mh / H), h = static_cast<int>(mh % H);
+    const int slot = slots[m];
+    if (slot < 0 || slot >= num_slots) {
+        if (slot != -1 && threadIdx.x == 0) set_status(status, KDA_ERR_BAD_SLOT);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 15;
+    const int row0 = part * ROWS_PER_CTA + warp * 8 + (lane >> 4);
+    const float *src = state + (mh * DK + row0) * DV + 8 * sub;
+    F8 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = ld8(src + 2 * i * DV);
+    // of several rows with this slot only the last is stored (no order of writes decides)
+    bool later = false;
+    for (int i = m + 1 + static_cast<int>(threadIdx.x); i < M; i += THREADS) later |= slots[i] == slot;
+    if (__syncthreads_or(later)) return;
+    const int64_t dst = (static_cast<int64_t>(slot) * H + h) * DK + row0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a = max_abs_nan(a, x[i].v[j]);
+#pragma unroll
+        for (int s = 8; s; s >>= 1) a = max_abs_nan(a, __shfl_xor_sync(0xffffffffu, a, s));
+        const bool finite = a <= 3.402823466e38f;  // false for NaN too
+        const float inv = finite && a >= TINY ? __fdiv_rn(127.f, a) : 0.f;
+        uint2 c;
+        c.x = inv == 0.f ? 0u : pack_s8(x[i].v, inv);
+        c.y = inv == 0.f ? 0u : pack_s8(x[i].v + 4, inv);
+        *reinterpret_cast<uint2 *>(codes + (dst + 2 * i) * DV + 8 * sub) = c;
+        if (sub == 0)
+            scales[dst + 2 * i] = !finite ? __int_as_float(0x7fc00000) : a >= TINY ? __fdiv_rn(a, 127.f) : 0.f;
+    }
+}
+
+__global__ void __launch_bounds__(THREADS) kda_state_load_kernel(const int8_t *__restrict__ codes,
+                                                                 const float *__restrict__ scales,
+                                                                 const int32_t *__restrict__ slots, int32_t H,
+                                                                 int32_t num_slots, float *__restrict__ state,
+                                                                 int32_t *status) {
+    const int part = blockIdx.x % PARTS;
+    const int64_t mh = blockIdx.x / PARTS;
+    const int m = static_cast<int>(mh / H), h = static_cast<int>(mh % H);
+    const int slot = slots[m];
+    const bool have = slot >= 0 && slot < num_slots;
+    if (!have && slot != -1 && threadIdx.x == 0) set_status(status, KDA_ERR_BAD_SLOT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane & 15;
+    const int row0 = part * ROWS_PER_CTA + warp * 8 + (lane >> 4);
+    const int64_t src = (static_cast<int64_t>(have ? slot : 0) * H + h) * DK + row0;
+    float *dst = state + (mh * DK + row0) * DV + 8 * sub;
+    uint2 c[4];
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = have ? __ldg(reinterpret_cast<const uint2 *>(codes + (src + 2 * i) * DV + 8 * sub)) : make_uint2(0, 0);
+        s[i] = have ? __ldg(scales + src + 2 * i) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        F8 x;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w = j < 4 ? c[i].x : c[i].y;
+            x.v[j] = static_cast<float>(static_cast<int8_t>((w >> (8 * (j & 3))) & 0xffu)) * s[i];
+        }
+        st8(dst + 2 * i * DV, x);
+    }
+}
+
+}  // namespace cache
+}  // namespace kda
+
+namespace {
+// KDA_OK when there is something to launch; *grid 0 when there is nothing to do
+kda_status_t cache_args(const void *state, const void *slots, int32_t num_rows, int32_t num_heads, int32_t dk,
+                        int32_t dv, int32_t num_slots, const void *codes, const void *scales, const void *status,
+                        int *grid) {
+    using kda::checks::aligned;
+    *grid = 0;
+    if (dk != KDA_HEAD_DIM || dv != KDA_HEAD_DIM) return KDA_ERR_UNSUPPORTED;
+    if (num_rows < 0 || num_heads < 1 || num_slots < 0) return KDA_ERR_INVALID_ARG;
+    const int64_t ctas = static_cast<int64_t>(num_rows) * num_heads * kda::cache::PARTS;
+    if (ctas > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+    if (status && !aligned(status, 4)) return KDA_ERR_INVALID_ARG;
+    if (num_rows == 0) return KDA_OK;
+    if (!state || !slots || !aligned(state, 32) || !aligned(slots, 4)) return KDA_ERR_INVALID_ARG;
+    if (num_slots > 0 && (!codes || !scales)) return KDA_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 4)) return KDA_ERR_INVALID_ARG;
+    *grid = static_cast<int>(ctas);
+    return KDA_OK;
+}
+kda_status_t queued() { return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+}  // namespace
+
+extern "C" kda_status_t kda_state_store(const float *state, const int32_t *slots, int32_t num_rows, int32_t num_heads,
+                                        int32_t head_dim_k, int32_t head_dim_v, int32_t num_slots, void *codes,
+                                        float *scales, int32_t *status_dev, kda_stream_t stream) {
+    int grid;
+    const kda_status_t rc = cache_args(state, slots, num_rows, num_heads, head_dim_k, head_dim_v, num_slots, codes,
+                                       scales, status_dev, &grid);
+    if (rc != KDA_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (!grid) return KDA_OK;
+    kda::cache::kda_state_store_kernel<<<grid, kda::cache::THREADS, 0, s>>>(
+        state, slots, num_rows, num_heads, num_slots, static_cast<int8_t *>(codes), scales, status_dev);
+    return queued();
+}
+
+extern "C" kda_status_t kda_state_load(const void *codes, const float *scales, const int32_t *slots, int32_t num_rows,
+                                       int32_t num_heads, int32_t head_dim_k, int32_t head_dim_v, int32_t num_slots,
+                                       float *state, int32_t *status_dev, kda_stream_t stream) {
+    int grid;
+    const kda_status_t rc = cache_args(state, slots, num_rows, num_heads, head_dim_k, head_dim_v, num_slots, codes,
+                                       scales, status_dev, &grid);
+    if (rc != KDA_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (!grid) return KDA_OK;
+    kda::cache::kda_state_load_kernel<<<grid, kda::cache::THREADS, 0, s>>>(
+        static_cast<const int8_t *>(codes), scales, slots, num_heads, num_slots, state, status_dev);
+    return queued();
+}

@@ -1,0 +1,243 @@
+"""GPU tests of the linear attention with one decay per head (chunked and recurrent forms) against the fp64 recurrence.
+
+Bounds, from the number of roundings (u = 2^-8 for bf16, half a step; 2^-24 for fp32; A = the same sums over magnitudes):
+  o (both)       u |o| for its own rounding; the chunked form also rounds each decayed score and the state that q multiplies
+                 once to bf16: u A.
+  final state    the chunked form's update operands are two bf16 terms: u^2 A. All fp32 sums: at most 128 terms a chunk and one
+                 step a chunk, taken as 600 roundings of 2^-24, truncations counted double: together below 8e-5 A.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kda_chunked_prefill_gb300 as kda
+from kda_chunked_prefill_gb300 import _lib
+from oracle import linear as ref
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+FP32 = 1200 * 2.0 ** -24
+D = 128
+
+
+def make(lens, H, Hk, seed, state=True, decay="token", extra=0, rate=1.0):
+    rng = np.random.default_rng(seed)
+    T = sum(lens) + extra
+    unit = lambda x: x / np.linalg.norm(x, axis=-1, keepdims=True)
+    q, k = (torch.from_numpy(unit(rng.standard_normal((T, Hk, D)))).to(torch.bfloat16) for _ in range(2))
+    v = torch.from_numpy(rng.standard_normal((T, H, D))).to(torch.bfloat16)
+    g = -rate * np.log1p(np.exp(rng.standard_normal((T, H) if decay == "token" else (H,)))) * np.exp(-4 * rng.random(H))
+    return {"q": q, "k": k, "v": v, "g": torch.from_numpy(g).float(), "lens": lens,
+            "cu": torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32), "scale": D ** -0.5,
+            "s0": torch.from_numpy(rng.standard_normal((len(lens), H, D, D)) * 0.3).float() if state else None}
+
+
+def oracle_of(x):
+    f = lambda t: None if t is None else t.double().numpy()
+    return ref.recurrence(f(x["q"]), f(x["k"]), f(x["v"]), f(x["g"]), x["lens"], f(x["s0"]), x["scale"])
+
+
+def check(x, o, fs, want=None, chunked=True):
+    ro, size, rs, rsize = oracle_of(x) if want is None else want
+    n = sum(x["lens"])
+    o = o[:n].double().cpu().numpy()
+    err, tol = np.abs(o - ro[:n]), U * np.abs(ro[:n]) * 1.01 + ((U * 1.05 if chunked else 0) + FP32) * size[:n] + 1e-30
+    assert np.isfinite(o).all() and (err <= tol).all(), f"o: {np.max(err / tol):.3g} of the bound"
+    if fs is not None:
+        s = fs.double().cpu().numpy()
+        err, tol = np.abs(s - rs), ((U * U if chunked else 0) + FP32) * rsize + 1e-30
+        assert np.isfinite(s).all() and (err <= tol).all(), f"final state: {np.max(err / tol):.3g} of the bound"
+
+
+def dev(x):
+    return {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in x.items()}
+
+
+def chunk(x, **kw):
+    d = dev(x)
+    return kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], scale=x["scale"], check=True, **kw)
+
+
+CHUNK = {
+    "one_token": ([1], 1, 1, False, "token"),
+    "one_chunk": ([128], 2, 2, False, "token"),
+    "one_over": ([129], 2, 1, True, "token"),
+    "two_chunks": ([256], 2, 2, True, "head"),
+    "ragged": ([130, 0, 64, 1, 127, 128, 383, 0, 5], 3, 3, True, "token"),
+    "ragged_no_state": ([33, 400, 0, 17], 4, 2, False, "token"),
+    "shared_heads": ([200, 70], 6, 2, True, "head"),
+    "long": ([1500], 2, 2, True, "token"),
+    "few_tokens_each": ([1, 2, 3, 0, 4] * 5, 3, 1, True, "token"),
+    "all_empty": ([0, 0, 0], 2, 2, True, "token"),
+    "many_heads": ([300, 40], 96, 32, True, "head"),
+}
+
+
+@pytest.mark.parametrize("name", list(CHUNK))
+def test_chunk(name):
+    lens, H, Hk, state, decay = CHUNK[name]
+    x = make(lens, H, Hk, seed=sum(lens) + H, state=state, decay=decay)
+    o, fs = chunk(x)
+    check(x, o, fs)
+
+
+@pytest.mark.parametrize("lens,H", [([4000, 9], 1), ([2600, 1, 0, 3100], 2)])
+def test_chunk_few_long_chains(lens, H):
+    """Few (sequence, head) chains of many chunks, with slow decays: old tokens matter to the end."""
+    x = make(lens, H, H, seed=77, rate=0.02)
+    o, fs = chunk(x)
+    check(x, o, fs)
+
+
+@pytest.mark.parametrize("g", [0.0, -1e-6, -5.0, -60.0, -138.5, float("-inf")])
+def test_chunk_extreme_decays(g):
+    x = make([300, 20], 2, 2, seed=5)
+    x["g"].fill_(g)
+    o, fs = chunk(x)
+    check(x, o, fs)
+
+
+def test_chunk_resets_inside_a_sequence():
+    """-inf at some tokens forgets what was before; the rest decays slowly."""
+    x = make([500, 77], 2, 2, seed=6, rate=0.05)
+    x["g"][[3, 130, 131, 255, 256, 400, 510], :] = float("-inf")
+    o, fs = chunk(x)
+    check(x, o, fs)
+
+
+def test_chunk_strided_projection():
+    x = make([190, 33], 4, 2, seed=9)
+    d = dev(x)
+    qkv = torch.full((223, 2 * 2 * D + 4 * D + 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q, k, v = qkv[:, :2 * D].view(223, 2, D), qkv[:, 2 * D:4 * D].view(223, 2, D), qkv[:, 4 * D:8 * D].view(223, 4, D)
+    q.copy_(d["q"]), k.copy_(d["k"]), v.copy_(d["v"])
+    o, fs = kda.linear_chunk_fwd(q, k, v, d["g"], d["cu"], d["s0"], check=True)
+    check(x, o, fs)
+    o2, fs2 = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], check=True)
+    assert torch.equal(o, o2) and torch.equal(fs, fs2)
+
+
+@pytest.mark.parametrize("lens", [[130, 20], [3, 1], [2000, 5]])
+def test_rows_behind_the_last_sequence(lens):
+    """Padding rows hold NaN on the way in and keep their values on the way out."""
+    x = make(lens, 2, 2, seed=13, extra=150)
+    n = sum(lens)
+    want = oracle_of(x)
+    for key in ("q", "k", "v", "g"):
+        x[key][n:] = float("nan")
+    d = dev(x)
+    o = torch.full((n + 150, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    fs = torch.empty_like(d["s0"])
+    status = torch.ones(1, dtype=torch.int32, device="cuda")
+    kda.kda_linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], x["scale"], o, fs, status)
+    check(x, o, fs, want)
+    assert int(status) == 0 and bool((o[n:] == 7.0).all())
+
+
+def test_sequences_do_not_see_each_other():
+    """NaN in one sequence (its last chunk shares rows with the next one's tile) stays in that sequence."""
+    x = make([100, 70, 300], 2, 2, seed=14)
+    clean = chunk(x)
+    bad = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+    for key in ("q", "k", "v"):
+        bad[key][100:170] = float("nan")
+    d = dev(bad)
+    o, fs = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], scale=x["scale"])
+    for part in (slice(0, 100), slice(170, 470)):
+        assert torch.equal(o[part], clean[0][part])
+    assert torch.equal(fs[[0, 2]], clean[1][[0, 2]])
+
+
+def test_chunk_in_place_state_and_no_state_out():
+    x = make([150, 0, 90], 2, 2, seed=15)
+    d = dev(x)
+    o = torch.empty_like(d["v"])
+    kda.kda_linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], x["scale"], o, d["s0"])
+    check(x, o, d["s0"])
+    o2, none = chunk(x, output_final_state=False)
+    assert none is None and torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("lens,H", [([700, 300], 2), ([5000], 1), ([2, 1, 3], 2)])
+def test_chunk_is_deterministic_on_any_stream(lens, H):
+    x = make(lens, H, H, seed=16)
+    d = dev(x)
+    a = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"])
+    s = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], stream=s[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    for o, fs in got:
+        assert torch.equal(o, a[0]) and torch.equal(fs, a[1])
+
+
+def test_chunk_in_two_captured_graphs():
+    """Two captured calls with workspaces of their own, replayed on two streams at once."""
+    runs = []
+    for seed, lens in ((21, [3000, 40]), (22, [900, 2500])):
+        x = make(lens, 2, 2, seed=seed)
+        d = dev(x)
+        kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"])
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            out = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], scale=x["scale"])
+        runs.append((x, d, graph, side, out))
+    for _ in range(3):
+        for _, _, graph, side, _ in runs:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    for x, _, _, _, (o, fs) in runs:
+        check(x, o, fs)
+
+
+def test_device_errors():
+    x = make([130, 20], 2, 2, seed=17)
+    for bad in (1e-3, float("nan"), float("inf")):
+        y = dict(x, g=x["g"].clone())
+        y["g"][140, 1] = bad
+        with pytest.raises(kda.KdaError) as e:
+            chunk(y)
+        assert e.value.code == kda.KDA_ERR_GATE_RANGE
+    for cu in ([0, 151, 150], [0, 130, 151], [1, 130, 150], [0, -5, 150]):
+        with pytest.raises(kda.KdaError) as e:
+            chunk(dict(x, cu=torch.tensor(cu, dtype=torch.int32)))
+        assert e.value.code == kda.KDA_ERR_BAD_SEQLENS
+
+
+# ------------------------------------------------------------------ decode
+@pytest.mark.parametrize("N,Tn,H,Hk,state,decay", [
+    (1, 1, 1, 1, True, "token"), (7, 1, 16, 8, True, "head"), (64, 1, 16, 16, False, "token"), (5, 3, 4, 1, True, "token"),
+    (3, 4, 16, 8, True, "head"), (2, 64, 2, 2, True, "token"), (3, 5, 5, 5, False, "head"), (2, 0, 3, 3, True, "token")])
+def test_decode(N, Tn, H, Hk, state, decay):
+    x = make([Tn] * N, H, Hk, seed=N + 10 * Tn + H, state=state, decay=decay)
+    d = dev(x)
+    o, fs = kda.linear_decode_fwd(d["q"], d["k"], d["v"], d["g"], N, d["s0"], check=True)
+    check(x, o, fs, chunked=False)
+    if state:
+        o2, fs2 = kda.linear_decode_fwd(d["q"], d["k"], d["v"], d["g"], N, d["s0"], in_place=True)
+        assert fs2 is d["s0"] and torch.equal(o, o2) and torch.equal(fs, fs2)
+
+
+def test_decode_reports_bad_gates():
+    x = make([1] * 3, 2, 2, seed=3)
+    x["g"][1, 1] = 0.5
+    d = dev(x)
+    with pytest.raises(kda.KdaError) as e:
+        kda.linear_decode_fwd(d["q"], d["k"], d["v"], d["g"], 3, d["s0"], check=True)
+    assert e.value.code == kda.KDA_ERR_GATE_RANGE
+
+
+def test_prompt_then_tokens():
+    """Prefill 200 tokens, then decode two steps of two tokens from its state: the recurrence over all of them."""
+    x = make([204, 204], 4, 2, seed=31)
+    take = lambda t, a, b: torch.cat([t[:204][a:b], t[204:][a:b]]).cuda().contiguous()
+    cu = torch.tensor([0, 200, 400], dtype=torch.int32, device="cuda")
+    part = lambda a, b: [take(x[k], a, b) for k in ("q", "k", "v", "g")]
+    o, s = kda.linear_chunk_fwd(*part(0, 200), cu, x["s0"].cuda(), check=True)
+    outs = [o.view(2, 200, 4, D)]
+    for a in (200, 202):
+        o, s = kda.linear_decode_fwd(*part(a, a + 2), 2, s, in_place=True)
+        outs.append(o.view(2, 2, 4, D))
+    check(x, torch.cat(outs, 1).reshape(408, 4, D), s)
