@@ -1,0 +1,747 @@
+// Chunked form of the linear attention with one decay per head (kda_linear_chunk_fwd) on tcgen05.
+//
+// For a chunk of 128 tokens with G_i the sum of its g up to token i (all g <= 0):
+//     A   = q k^T                                 MMA  [128 x 128 x 128]
+//     P_ij = [j <= i] e^{G_i - G_j} A_ij          warpgroup 0, bf16 into tensor memory
+//     O1  = q S,  O2 = P v                        MMA, MMA
+//     o_i = scale (e^{G_i} O1_i + O2_i)           warpgroup 0
+//     U   = k^T v~,  v~_j = e^{G_end - G_j} v_j   warpgroup 1 forms v~, MMA
+//     S   = e^{G_end} S + U                       warpgroup 1, fp32 registers
+//
+// One CTA per SM walks (segment, head) tasks: a segment is a sequence or a part
+// of one. Warp 8 loads q, k and v tiles by TMA into a ring of five 32 KB tiles,
+// warp 9 issues the MMAs, the two warpgroups work on the accumulators.
+//
+// Why this split. U does not depend on S, so the recurrence from chunk to chunk
+// is one fused multiply-add per state element and its rounding to bf16 for the
+// next q S: S stays in fp32 registers (128 per thread, one key row each), is
+// never accumulated by the tensor cores over many chunks, and a chunk's MMAs
+// are all off the critical path. v~ is split in two bf16 terms (hi + lo, both
+// multiplied by the exact bf16 k), which keeps the final state within about
+// 1e-6; P and the copy of S that q multiplies are rounded once to bf16, like o.
+//
+// Decays: every factor is 2^x with x a sum of same-signed terms that starts at
+// the nearer end (prefixes within 32 tokens, suffixes within 32 tokens plus
+// whole-block totals), so its absolute error is a few units in the last place of
+// x itself, never of the chunk's total, and no factor exceeds 1.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "kda.h"
+#include "kda_linear.cuh"
+#include "kda_linear.h"
+
+namespace kda {
+namespace lin {
+
+namespace {
+
+constexpr int C = CHUNK;
+constexpr int TILE = C * DK * 2;  // one 128 x 128 bf16 tile: two panels of 64 channels, 128-byte rows, swizzled
+constexpr int PANEL = TILE / 2;
+constexpr int TILES = 5;
+constexpr int OFF_S = TILES * TILE;   // bf16 copy of S: [key][value], two panels of 64 values
+constexpr int OFF_VT = OFF_S + TILE;  // v~ of 64 tokens: hi (two panels), lo (two panels)
+constexpr int VT_TERM = TILE / 2, VT_PANEL = TILE / 4;
+constexpr int OFF_MISC = OFF_VT + TILE;
+
+struct ChunkParams {
+    Params a;
+    CUtensorMap tq, tk, tv;
+    int32_t tasks;  // WHOLE: (sequence, head) pairs
+    // the rest only with segments (device memory in the workspace)
+    int32_t seg_chunks;
+    int32_t most_segs;  // that the workspace holds
+    int32_t *num_segs;
+    int2 *first;     // [N] first segment and number of segments
+    Segment *segs;
+    float *decays;   // [segment][head]
+    float *states;   // [segment][head][128][128]
+};
+
+struct Misc {
+    uint64_t full[TILES], empty[TILES];
+    uint64_t qk, u0, u1, o;               // tensor core -> warpgroups (commits)
+    uint64_t vt0, vt1, s, p, ofree;       // warpgroups -> tensor core (128 arrivals)
+    alignas(16) float tab[3][C];          // [a - 1][j]: 2^(sum of g after j up to the start of block a), a = 1..3
+    alignas(16) float pre[C];             // log2 prefix of j within its block of 32
+    float w[C];                           // 2^(sum of g after j up to the chunk's end)
+    float tot0[4], tot1[4];               // the blocks' totals, for each warpgroup
+    uint32_t tmem;
+    int32_t abort;
+};
+static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && OFF_MISC % 16 == 0, "read as float4");
+constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc));
+static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
+
+constexpr uint32_t COL_QK = 0, COL_O1 = 128, COL_O2 = 256, COL_U = 384;  // tensor memory columns (P over A)
+constexpr int THREADS = 320;
+constexpr long long SPINS = 1ll << 24;
+
+struct Task {
+    int64_t t0;
+    int32_t len, h;
+    const float *sin;  // NULL: zeros
+    float *sout;       // NULL: not wanted
+    float *decay;      // NULL, or where the segment's log2 decay goes
+    bool skip;
+};
+
+template <Pass PASS>
+__device__ __forceinline__ int tasks_of(const ChunkParams &p) {
+    return PASS == Pass::WHOLE ? p.tasks : *p.num_segs * p.a.H;
+}
+
+template <Pass PASS>
+__device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
+    const Params &a = p.a;
+    Task t;
+    const int seg = id / a.H;
+    t.h = id % a.H;
+    t.decay = nullptr;
+    constexpr size_t SZ = static_cast<size_t>(DK) * DV;
+    if (PASS == Pass::WHOLE) {
+        const int64_t b = a.cu[seg], e = a.cu[seg + 1];
+        t.skip = b < 0 || e < b || e > a.T || a.cu[0] != 0;
+        t.t0 = b;
+        t.len = static_cast<int32_t>(e - b);
+        const size_t at = static_cast<size_t>(id) * SZ;
+        t.sin = a.s0 ? a.s0 + at : nullptr;
+        t.sout = a.sT ? a.sT + at : nullptr;
+        return t;
+    }
+    const Segment sg = p.segs[seg];
+    t.t0 = sg.t0;
+    t.len = sg.len;
+    const size_t at = (static_cast<size_t>(sg.seq) * a.H + t.h) * SZ, ws = static_cast<size_t>(id) * SZ;
+    const bool last = sg.index == sg.count - 1;
+    // With the states updated in place, a cut sequence's entry state is read by one
+    // CTA and overwritten by another: the last segment's slot, else unused, keeps it.
+    const bool keep = sg.count > 1 && a.s0 && a.s0 == a.sT;
+    if (PASS == Pass::STATES) {
+        t.skip = last && !keep;
+        if (last) t.len = 0;
+        t.sin = (last || sg.index == 0) && a.s0 ? a.s0 + at : nullptr;
+        t.sout = p.states + ws;
+        t.decay = p.decays + id;
+    } else {
+        const size_t row = static_cast<size_t>(a.H) * SZ;
+        t.skip = false;
+        t.sin = sg.index > 0 ? p.states + ws - row : keep ? p.states + ws + (sg.count - 1) * row : a.s0 ? a.s0 + at : nullptr;
+        t.sout = last && a.sT ? a.sT + at : nullptr;
+    }
+    return t;
+}
+
+// a bounded wait; false: it ran out, or another role has given up
+__device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
+    for (long long i = 0; i < SPINS; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 1023) == 1023 && *reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
+    }
+    set_status(status, KDA_ERR_TIMEOUT);
+    *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
+    return false;
+}
+
+// the same for a whole warp, with one answer
+__device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
+    return __all_sync(0xffffffffu, wait(m, bar, parity, status));
+}
+
+// the chunk's log2 decay of token `row` (0 behind the segment), and whether its gate is bad
+__device__ __forceinline__ float gate_raw(const Params &a, int64_t t0, int row, int left, int h) {
+    if (row >= left) return 0.f;
+    return __ldg(a.g + (a.g_per_token ? (t0 + row) * a.H + h : h));
+}
+__device__ __forceinline__ float log2_decay(float g) { return fmaxf(g * LOG2E, -200.f); }  // 2^-200 is 0 in fp32
+// inclusive prefix and exclusive suffix within the warp, and the warp's total
+__device__ __forceinline__ void warp_sums(float x, int lane, float &pre, float &suf, float &tot) {
+    pre = x;
+    suf = x;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const float a = __shfl_up_sync(0xffffffffu, pre, s), b = __shfl_down_sync(0xffffffffu, suf, s);
+        if (lane >= s) pre += a;
+        if (lane + s < 32) suf += b;
+    }
+    tot = __shfl_sync(0xffffffffu, suf, 0);
+    suf = __shfl_down_sync(0xffffffffu, suf, 1);
+    if (lane == 31) suf = 0.f;
+}
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {  // K-major: 128 rows, k in the panels
+    return umma_desc_sw128(tile + (kk >> 2) * PANEL + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk, uint32_t panel) {  // MN-major: rows are k
+    return umma_desc_sw128(tile + kk * 2048, panel, 1024);
+}
+
+// ---- warp 8: tile loads
+template <Pass PASS>
+__device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m) {
+    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+    int n = 0;  // tiles issued
+    bool ok = true;
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; ok && id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) continue;
+        const int hk = t.h / p.a.rep;
+        for (int c = 0; ok && c < t.len; c += C) {
+            const int row = static_cast<int>(t.t0 + c);
+            for (int i = 3 - PER; ok && i < 3; ++i, ++n) {
+                const int slot = n % TILES;
+                if (n >= TILES) ok = wait(m, &m->empty[slot], ((n / TILES) - 1) & 1, p.a.status);
+                if (!ok) break;
+                unsigned char *dst = smem + slot * TILE;
+                const CUtensorMap *map = i == 0 ? &p.tq : i == 1 ? &p.tk : &p.tv;
+                const int head = i == 2 ? t.h : hk;
+                mbar_arrive_expect_tx(&m->full[slot], TILE);
+                tma_load_3d(dst, map, 0, head, row, &m->full[slot]);
+                tma_load_3d(dst + PANEL, map, 64, head, row, &m->full[slot]);
+            }
+        }
+    }
+    // no copy and no commit of this CTA is in flight when it ends
+    for (int k = n > TILES ? n - TILES : 0; k < n; ++k) {
+        if (ok) ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1, p.a.status);
+        for (long long i = 0; !ok && i < SPINS; ++i)
+            if (mbar_try_wait(&m->full[k % TILES], (k / TILES) & 1)) break;
+    }
+}
+
+// ---- warp 9, one thread: MMAs
+template <Pass PASS>
+__device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+    constexpr uint32_t ID_QK = idesc_bf16(false, false, C, C), ID_QS = idesc_bf16(false, true, C, DV),
+                       ID_U = idesc_bf16(true, true, DK, DV), ID_PV = idesc_bf16(false, true, C, DV);
+    int32_t *status = p.a.status;
+    int n = 0;
+    uint32_t it = 0;
+    const uint32_t sS = smem_u32(smem + OFF_S), sVT = smem_u32(smem + OFF_VT);
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) continue;
+        for (int c = 0; c < t.len; c += C, n += PER, ++it) {
+            const uint32_t ph = it & 1;
+            const int iq = n % TILES, ik = (n + PER - 2) % TILES, iv = (n + PER - 1) % TILES;
+            const uint32_t tq = smem_u32(smem + iq * TILE), tk = smem_u32(smem + ik * TILE), tv = smem_u32(smem + iv * TILE);
+            if (!wait(m, &m->full[ik], ((n + PER - 2) / TILES) & 1, status)) return;
+            if (PASS != Pass::STATES) {
+                if (!wait(m, &m->full[iq], (n / TILES) & 1, status)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, desc_k(tq, kk), desc_k(tk, kk), ID_QK, kk > 0);
+                umma_commit(&m->qk);
+                if (!wait(m, &m->s, ph, status)) return;
+                if (it > 0 && !wait(m, &m->ofree, ph ^ 1, status)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk)
+                    umma_f16(tmem + COL_O1, desc_k(tq, kk), desc_mn(sS, kk, PANEL), ID_QS, kk > 0);
+                umma_commit(&m->empty[iq]);
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!wait(m, half ? &m->vt1 : &m->vt0, ph, status)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    umma_f16(tmem + COL_U, desc_mn(tk, 4 * half + kk, PANEL), desc_mn(sVT, kk, VT_PANEL), ID_U,
+                             half > 0 || kk > 0);
+                    umma_f16(tmem + COL_U, desc_mn(tk, 4 * half + kk, PANEL), desc_mn(sVT + VT_TERM, kk, VT_PANEL), ID_U, 1);
+                }
+                umma_commit(half ? &m->u1 : &m->u0);
+            }
+            umma_commit(&m->empty[ik]);
+            if (PASS != Pass::STATES) {
+                if (!wait(m, &m->full[iv], ((n + PER - 1) / TILES) & 1, status)) return;
+                if (!wait(m, &m->p, ph, status)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    umma_ts(tmem + COL_O2, tmem + COL_QK + 8 * kk, desc_mn(tv, kk, PANEL), ID_PV, kk > 0);
+                umma_commit(&m->o);
+            }
+            umma_commit(&m->empty[iv]);
+        }
+    }
+}
+
+// ---- warpgroup 0: decayed scores and the output (thread = token row)
+template <Pass PASS>
+__device__ __forceinline__ void role_scores(const ChunkParams &p, Misc *m, uint32_t tmem) {
+    const Params &a = p.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
+    uint32_t it = 0;
+    bool bad = false, fail = false;  // (a warp that gives up tells the others at the next barrier)
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) continue;
+        float graw = gate_raw(a, t.t0, tid, t.len, t.h);
+        for (int c = 0; c < t.len; c += C, ++it) {
+            const uint32_t ph = it & 1;
+            const int left = t.len - c;  // tokens from this chunk on
+            bad |= !(graw <= 0.f);
+            const float x = log2_decay(graw);
+            if (left > C) graw = gate_raw(a, t.t0 + c + C, tid, left - C, t.h);
+            float pre, suf, tot;
+            warp_sums(x, lane, pre, suf, tot);
+            if (lane == 0) m->tot0[warp] = tot;
+            if (named_bar_or(1, 128, fail)) return;
+            float upto = pre, after = suf;
+#pragma unroll
+            for (int b = 0; b < 3; ++b)
+                if (b < warp) upto += m->tot0[b];
+#pragma unroll
+            for (int b = 1; b < 4; ++b) {  // anchor: the start of block b
+                if (b > warp) {
+                    m->tab[b - 1][tid] = ex2(after);
+                    after += m->tot0[b];
+                }
+            }
+            m->pre[tid] = pre;
+            const float row = ex2(pre), entry = a.scale * ex2(upto);
+            named_bar_sync(1, 128);
+            if (!wait_warp(m, &m->qk, ph, a.status)) {
+                fail = true;
+                continue;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {  // key blocks of 32
+                uint32_t out[16];
+                if (b > warp) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) out[j] = 0;
+                } else {
+                    uint32_t s[32];
+                    tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
+                    tmem_wait_ld();
+                    if (b < warp) {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[warp - 1][32 * b]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
+                            out[2 * j] = pack_bf16(__uint_as_float(s[4 * j]) * (row * w.x), __uint_as_float(s[4 * j + 1]) * (row * w.y));
+                            out[2 * j + 1] = pack_bf16(__uint_as_float(s[4 * j + 2]) * (row * w.z), __uint_as_float(s[4 * j + 3]) * (row * w.w));
+                        }
+                    } else {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
+                            // (selected, not multiplied by zero: a score behind the row may be anything)
+                            const float s0 = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
+                            const float s1 = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
+                            const float s2 = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
+                            const float s3 = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
+                            out[2 * j] = pack_bf16(s0, s1);
+                            out[2 * j + 1] = pack_bf16(s2, s3);
+                        }
+                    }
+                }
+                tmem_st16(tmem + lanes + COL_QK + 16 * b, out);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&m->p);
+            if (!wait_warp(m, &m->o, ph, a.status)) {
+                fail = true;
+                continue;
+            }
+            tc_fence_after();
+            __nv_bfloat16 *dst = a.o + ((t.t0 + c + tid) * a.H + t.h) * DV;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                uint32_t o1[16], o2[16], w[8];
+                tmem_ld16(tmem + lanes + COL_O1 + 16 * b, o1);
+                tmem_ld16(tmem + lanes + COL_O2 + 16 * b, o2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = pack_bf16(fmaf(entry, __uint_as_float(o1[2 * j]), a.scale * __uint_as_float(o2[2 * j])),
+                                     fmaf(entry, __uint_as_float(o1[2 * j + 1]), a.scale * __uint_as_float(o2[2 * j + 1])));
+                if (tid < left) {
+                    reinterpret_cast<uint4 *>(dst)[2 * b] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4 *>(dst)[2 * b + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&m->ofree);
+        }
+    }
+    if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
+}
+
+// ---- warpgroup 1: v~ and the state (thread = key row of S)
+template <Pass PASS>
+__device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+    const Params &a = p.a;
+    const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
+    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+    unsigned char *sS = smem + OFF_S, *sVT = smem + OFF_VT;
+    uint32_t it = 0;
+    int n = 0;
+    bool fail = false;
+    float S[DV];
+    auto publish = [&]() {  // the bf16 copy that q multiplies
+#pragma unroll
+        for (int j = 0; j < DV / 8; ++j) {
+            const uint4 u = make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
+                                       pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
+            *reinterpret_cast<uint4 *>(sS + (j >> 3) * PANEL + tid * 128 + (((j & 7) ^ (tid & 7)) << 4)) = u;
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(&m->s);
+    };
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) {
+            if (PASS == Pass::WHOLE && tid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            continue;
+        }
+        if (t.sin) {
+#pragma unroll
+            for (int j = 0; j < DV; j += 8) ld_f8(S + j, t.sin + static_cast<size_t>(tid) * DV + j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < DV; ++j) S[j] = 0.f;
+        }
+        float sum = 0.f;  // log2 decay of the segment
+        float graw = gate_raw(a, t.t0, tid, t.len, t.h);
+        if (PASS != Pass::STATES && t.len > 0) publish();
+        for (int c = 0; c < t.len; c += C, n += PER, ++it) {
+            const uint32_t ph = it & 1;
+            const int left = t.len - c;
+            const int nk = n + PER - 2, nv = n + PER - 1;
+            unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
+            const float x = log2_decay(graw);
+            if (left > C) graw = gate_raw(a, t.t0 + c + C, tid, left - C, t.h);
+            float pre, suf, tot;
+            warp_sums(x, lane, pre, suf, tot);
+            if (lane == 0) m->tot1[warp] = tot;
+            if (named_bar_or(2, 128, fail)) return;
+#pragma unroll
+            for (int b = 1; b < 4; ++b)
+                if (b > warp) suf += m->tot1[b];
+            m->w[tid] = ex2(suf);
+            const float total = (m->tot1[0] + m->tot1[1]) + (m->tot1[2] + m->tot1[3]);
+            sum += total;
+            fail = !wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1, a.status);
+            if (left < C) {  // rows behind the segment belong to someone else: zeros in k and v
+                fail |= !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1, a.status);
+                if (tid >= left && !fail) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int off = (j >> 3) * PANEL + tid * 128 + ((j & 7) << 4);
+                        *reinterpret_cast<uint4 *>(tk + off) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(tv + off) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            if (named_bar_or(2, 128, fail)) return;  // weights (and zeros) written
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (half && !wait_warp(m, &m->u0, ph, a.status)) {
+                    fail = true;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // 16-byte pieces: 64 rows x 8 of each panel
+                    const int piece = i * 128 + tid, panel = piece >> 9, in = piece & 511, r = in >> 3;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(tv + panel * PANEL + half * VT_PANEL + in * 16);
+                    const float wr = m->w[64 * half + r];
+                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = unpack_bf16(v[j]);
+                        const float y0 = f.x * wr, y1 = f.y * wr;
+                        hi[j] = pack_bf16(y0, y1);
+                        const float2 b = unpack_bf16(hi[j]);
+                        lo[j] = pack_bf16(y0 - b.x, y1 - b.y);
+                    }
+                    *reinterpret_cast<uint4 *>(sVT + panel * VT_PANEL + in * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sVT + VT_TERM + panel * VT_PANEL + in * 16) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_shared();
+                mbar_arrive(half ? &m->vt1 : &m->vt0);
+            }
+            if (fail || !wait_warp(m, &m->u1, ph, a.status)) {
+                fail = true;
+                continue;
+            }
+            tc_fence_after();
+            // S e^total + U, with e^total - 1 so that a slow decay is not rounded away chunk after chunk
+            const float dm1 = expm1f(total * (1.f / LOG2E));
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t u[32];
+                tmem_ld32(tmem + lanes + COL_U + 32 * b, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[32 * b + j] = fmaf(S[32 * b + j], dm1, S[32 * b + j]) + __uint_as_float(u[j]);
+            }
+            tc_fence_before();
+            if (PASS != Pass::STATES && left > C) publish();  // (u1 came after q S: the old copy has been read)
+        }
+        if (t.sout && !fail) {
+#pragma unroll
+            for (int j = 0; j < DV; j += 8) st_f8(t.sout + static_cast<size_t>(tid) * DV + j, S + j);
+        }
+        if (PASS == Pass::STATES && tid == 0) *t.decay = sum;
+    }
+}
+
+template <Pass PASS>
+__global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < TILES; ++i) {
+            mbar_init(&m->full[i], 1);
+            mbar_init(&m->empty[i], 1);
+        }
+        mbar_init(&m->qk, 1);
+        mbar_init(&m->u0, 1);
+        mbar_init(&m->u1, 1);
+        mbar_init(&m->o, 1);
+        mbar_init(&m->vt0, 128);
+        mbar_init(&m->vt1, 128);
+        mbar_init(&m->s, 128);
+        mbar_init(&m->p, 128);
+        mbar_init(&m->ofree, 128);
+        m->abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 9) tmem_alloc(&m->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+    if (warp < 4) {
+        if (PASS == Pass::WHOLE)
+            role_scores<Pass::WHOLE>(p, m, tmem);
+        else if (PASS == Pass::OUTPUT)
+            role_scores<Pass::OUTPUT>(p, m, tmem);
+    } else if (warp < 8) {
+        role_state<PASS>(p, smem, m, tmem);
+    } else if (warp == 8) {
+        if (lane == 0) role_load<PASS>(p, smem, m);
+    } else {
+        if (lane == 0) role_mma<PASS>(p, smem, m, tmem);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ---- segments: one CTA. Sequence n of c chunks gets ceil(c / L) segments of about equal length.
+__global__ void __launch_bounds__(256) kda_linear_plan_kernel(const ChunkParams p) {
+    __shared__ int part[256], total;
+    const Params &a = p.a;
+    const int tid = threadIdx.x;
+    const int per = (a.N + 255) / 256, n0 = tid * per, n1 = n0 + per < a.N ? n0 + per : a.N;
+    const bool start_ok = a.cu[0] == 0;
+    auto chunks = [&](int n) -> int64_t {
+        const int64_t b = a.cu[n], e = a.cu[n + 1];
+        return start_ok && b >= 0 && e >= b && e <= a.T ? (e - b + C - 1) / C : -1;
+    };
+    int mine = 0;
+    for (int n = n0; n < n1; ++n) {
+        const int64_t c = chunks(n);
+        mine += c < 0 ? 0 : c == 0 ? 1 : static_cast<int>((c + p.seg_chunks - 1) / p.seg_chunks);
+    }
+    part[tid] = mine;
+    __syncthreads();
+    if (tid == 0) {
+        int s = 0;
+        for (int i = 0; i < 256; ++i) {
+            const int v = part[i];
+            part[i] = s;
+            s += v;
+        }
+        // more than valid offsets can need: sequences overlap (cu_seqlens goes back), and nothing runs
+        if (s > p.most_segs) {
+            set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            s = -1;
+        }
+        *p.num_segs = s < 0 ? 0 : s;
+        total = s;
+    }
+    __syncthreads();
+    if (total < 0) {
+        for (int n = n0; n < n1; ++n) p.first[n] = make_int2(0, 0);
+        return;
+    }
+    int at = part[tid];
+    for (int n = n0; n < n1; ++n) {
+        const int64_t c = chunks(n);
+        if (c < 0) {
+            set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            p.first[n] = make_int2(at, 0);
+            continue;
+        }
+        const int k = c == 0 ? 1 : static_cast<int>((c + p.seg_chunks - 1) / p.seg_chunks);
+        const int64_t step = (c + k - 1) / k * C, len = a.cu[n + 1] - a.cu[n];
+        p.first[n] = make_int2(at, k);
+        for (int i = 0; i < k; ++i, ++at) {
+            Segment sg;
+            const int64_t b = i * step < len ? i * step : len, e = b + step < len ? b + step : len;
+            sg.t0 = static_cast<int32_t>(a.cu[n] + b);
+            sg.len = static_cast<int32_t>(e - b);
+            sg.seq = n;
+            sg.index = i;
+            sg.count = k;
+            p.segs[at] = sg;
+        }
+    }
+}
+
+// ---- entry states: E_{s+1} = 2^{decay_s} E_s + N_s along a sequence, in place over the segments' states N_s
+__global__ void __launch_bounds__(256) kda_linear_join_kernel(const ChunkParams p) {
+    constexpr int PARTS = DK * DV / 1024;
+    const int part = blockIdx.x % PARTS, chain = blockIdx.x / PARTS, n = chain / p.a.H, h = chain % p.a.H;
+    const int2 f = p.first[n];
+    if (f.y < 3) return;  // the first segment's state is whole already, and the last one's is not needed
+    const size_t step = static_cast<size_t>(p.a.H) * DK * DV / 4;
+    float4 *s = reinterpret_cast<float4 *>(p.states) + (static_cast<size_t>(f.x) * p.a.H + h) * (DK * DV / 4) + part * 256 + threadIdx.x;
+    float4 e = *s;
+    for (int i = 1; i < f.y - 1; ++i) {
+        s += step;
+        const float4 x = *s;
+        const float d = expm1f(p.decays[(static_cast<int64_t>(f.x) + i) * p.a.H + h] * (1.f / LOG2E));
+        e.x = fmaf(e.x, d, e.x) + x.x;
+        e.y = fmaf(e.y, d, e.y) + x.y;
+        e.z = fmaf(e.z, d, e.z) + x.z;
+        e.w = fmaf(e.w, d, e.w) + x.w;
+        *s = e;
+    }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ host side
+namespace {
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {  // looked up once through the runtime (no link to the driver library)
+    static const EncodeTiledFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return static_cast<EncodeTiledFn>(nullptr);
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+// [tokens][heads][128] bf16 with a token stride; box 64 channels x 1 head x 128 tokens, 128-byte swizzle
+bool encode(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int heads, int64_t stride) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {DK, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {DK * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, 1, C}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(x), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int num_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return sms;
+}
+
+template <Pass PASS>
+cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(kda_linear_chunk_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    kda_linear_chunk_kernel<PASS><<<static_cast<int>(most_tasks < sms ? most_tasks : sms), THREADS, SMEM, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// Sequences of few tokens run the recurrence.
+bool few_tokens(int64_t N, int64_t T) { return T <= 16 * N; }
+
+// Chunks per segment so that every SM gets about one (segment, head); 0 when no
+// sequence can be longer than that.
+int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
+    const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
+    int64_t len = (all + sms - 1) / sms;
+    if (len < 4) len = 4;
+    return longest <= len ? 0 : static_cast<int>(len);
+}
+
+struct Layout {
+    int64_t most;  // segments at most: ceil(c / L) <= c' / L + 1 summed over the sequences
+    size_t first, segs, decays, states, bytes;
+};
+Layout layout_of(int64_t N, int64_t T, int64_t H, int len) {
+    Layout l;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.most = T / (static_cast<int64_t>(C) * len) + N;
+    l.first = 256;
+    l.segs = up(l.first + sizeof(int2) * N);
+    l.decays = up(l.segs + sizeof(Segment) * l.most);
+    l.states = up(l.decays + sizeof(float) * l.most * H);
+    l.bytes = l.states + sizeof(float) * DK * DV * l.most * H;
+    return l;
+}
+}  // namespace
+
+size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
+    if (N < 1 || T < 1 || H < 1 || few_tokens(N, T)) return 0;
+    const int sms = num_sms();
+    const int len = sms > 0 ? segment_chunks(N, T, H, sms) : 0;
+    return len ? layout_of(N, T, H, len).bytes : 0;
+}
+
+cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream) {
+    if (few_tokens(a.N, a.T)) return launch_recurrent(a, stream);
+    const int sms = num_sms();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    ChunkParams p{};
+    p.a = a;
+    const int hk = a.H / a.rep;
+    if (!encode(&p.tq, a.q, a.T, hk, a.qs) || !encode(&p.tk, a.k, a.T, hk, a.ks) || !encode(&p.tv, a.v, a.T, a.H, a.vs))
+        return cudaErrorInvalidValue;
+    p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
+    p.tasks = a.N * a.H;
+    if (!p.seg_chunks) return run<Pass::WHOLE>(p, p.tasks, sms, stream);
+    const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    p.most_segs = static_cast<int32_t>(l.most);
+    p.num_segs = reinterpret_cast<int32_t *>(ws);
+    p.first = reinterpret_cast<int2 *>(ws + l.first);
+    p.segs = reinterpret_cast<Segment *>(ws + l.segs);
+    p.decays = reinterpret_cast<float *>(ws + l.decays);
+    p.states = reinterpret_cast<float *>(ws + l.states);
+    kda_linear_plan_kernel<<<1, 256, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = run<Pass::STATES>(p, l.most * a.H, sms, stream);
+    if (e != cudaSuccess) return e;
+    kda_linear_join_kernel<<<a.N * a.H * (DK * DV / 1024), 256, 0, stream>>>(p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? run<Pass::OUTPUT>(p, l.most * a.H, sms, stream) : e;
+}
+
+}  // namespace lin
+}  // namespace kda

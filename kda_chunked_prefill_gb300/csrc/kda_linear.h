@@ -28,8 +28,26 @@ struct Params {
 // A log decay below this counts as -inf: e^-138 is below 2^-126 times any finite bf16 ratio that could show
 constexpr float G_FLOOR = -138.f;
 
+constexpr int CHUNK = 128;  // tokens
+
+// A part of a sequence that one CTA walks: tokens t0 .. t0 + len - 1 of sequence seq.
+struct Segment {
+    int32_t t0, len, seq, index, count;  // index of the sequence's count segments
+};
+
+// What a launch of the chunk kernel does with a segment.
+enum class Pass {
+    WHOLE,   // segments are whole sequences
+    STATES,  // the states of all segments but a sequence's last, from zeros (the first: from the sequence's entry state)
+    OUTPUT   // the outputs, from the joined states
+};
+
 // the recurrence, token after token (few tokens per sequence)
 cudaError_t launch_recurrent(const Params &p, cudaStream_t stream);
+
+// chunk by chunk on the tensor cores; the recurrence where sequences are short
+cudaError_t launch_chunked(const Params &p, void *workspace, cudaStream_t stream);
+size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H);
 
 }  // namespace lin
 }  // namespace kda

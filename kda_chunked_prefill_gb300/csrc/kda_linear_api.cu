@@ -78,14 +78,11 @@ kda_status_t kda_linear_chunk_fwd(const void *q, const void *k, const void *v, c
     if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     if (num_seqs == 0) return KDA_OK;
     p.cu = cu_seqlens;
-    return kda::lin::launch_recurrent(p, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return kda::lin::launch_chunked(p, workspace, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 size_t kda_linear_chunk_fwd_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t num_heads) {
-    (void)num_seqs;
-    (void)total_tokens;
-    (void)num_heads;
-    return 0;
+    return kda::lin::chunked_workspace_bytes(num_seqs, total_tokens, num_heads);
 }
 
 kda_status_t kda_linear_decode_fwd(const void *q, const void *k, const void *v, const float *g, int32_t num_seqs,
