@@ -9,16 +9,21 @@
 //     S   = e^{G_end} S + U                       warpgroup 1, fp32 registers
 //
 // One CTA per SM walks (segment, head) tasks: a segment is a sequence or a part
-// of one. Warp 8 loads q, k and v tiles by TMA into a ring of five 32 KB tiles,
-// warp 9 issues the MMAs, the two warpgroups work on the accumulators.
+// of one. Six roles run side by side, each a chunk or two ahead of the next:
+//   load    one thread: q, k and v tiles by TMA into a ring of five 32 KB tiles
+//   decays  one warp: the chunk's decay tables from g
+//   v~      4 warps: v~ in stages of 32 tokens
+//   scores  8 warps: P, then o_i into the chunk's v tile
+//   state   8 warps: S
+//   MMA, store   one thread each
 //
 // Why this split. U does not depend on S, so the recurrence from chunk to chunk
 // is one fused multiply-add per state element and its rounding to bf16 for the
-// next q S: S stays in fp32 registers (128 per thread, one key row each), is
+// next q S: S stays in fp32 registers (a key row shared by two threads), is
 // never accumulated by the tensor cores over many chunks, and a chunk's MMAs
 // are all off the critical path. v~ is split in two bf16 terms (hi + lo, both
 // multiplied by the exact bf16 k), which keeps the final state within about
-// 1e-6; P and the copy of S that q multiplies are rounded once to bf16, like o.
+// 3e-6; P and the copy of S that q multiplies are rounded once to bf16, like o.
 //
 // Decays: every factor is 2^x with x a sum of same-signed terms that starts at
 // the nearer end (prefixes within 32 tokens, suffixes within 32 tokens plus
@@ -42,13 +47,14 @@ constexpr int TILE = C * DK * 2;  // one 128 x 128 bf16 tile: two panels of 64 c
 constexpr int PANEL = TILE / 2;
 constexpr int TILES = 5;
 constexpr int OFF_S = TILES * TILE;   // bf16 copy of S: [key][value], two panels of 64 values
-constexpr int OFF_VT = OFF_S + TILE;  // v~ of 64 tokens: hi (two panels), lo (two panels)
-constexpr int VT_TERM = TILE / 2, VT_PANEL = TILE / 4;
+constexpr int OFF_VT = OFF_S + TILE;  // v~: two stages of 32 tokens, each hi (two panels) and lo (two panels)
+constexpr int STAGES = 4, STAGE_ROWS = C / STAGES;  // stages of a chunk
+constexpr int VT_PANEL = STAGE_ROWS * 128, VT_TERM = 2 * VT_PANEL, VT_STAGE = 2 * VT_TERM;
 constexpr int OFF_MISC = OFF_VT + TILE;
 
 struct ChunkParams {
     Params a;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     int32_t tasks;  // WHOLE: (sequence, head) pairs
     // the rest only with segments (device memory in the workspace)
     int32_t seg_chunks;
@@ -62,21 +68,39 @@ struct ChunkParams {
 
 struct Misc {
     uint64_t full[TILES], empty[TILES];
-    uint64_t qk, u0, u1, o;               // tensor core -> warpgroups (commits)
-    uint64_t vt0, vt1, s, p, ofree;       // warpgroups -> tensor core (128 arrivals)
-    alignas(16) float tab[3][C];          // [a - 1][j]: 2^(sum of g after j up to the start of block a), a = 1..3
-    alignas(16) float pre[C];             // log2 prefix of j within its block of 32
-    float w[C];                           // 2^(sum of g after j up to the chunk's end)
-    float tot0[4], tot1[4];               // the blocks' totals, for each warpgroup
+    uint64_t qk, u, o, vfree[2];  // tensor core -> warps (commits)
+    uint64_t dec;                 // decay tables written
+    uint64_t vt[2], s, p;         // v~ stage, bf16 state, scores written
+    uint64_t wfree;               // the weights of v~ read
+    uint64_t ufree, ofree, ostage;  // U read; O1 and O2 read; o in the v tile
+    alignas(16) float tab[192];   // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
+    alignas(16) float pre[C];     // log2 prefix of j within its block of 32
+    float upto[C];                // 2^(sum of g up to j)
+    float w[C];                   // 2^(sum of g after j up to the chunk's end)
+    float dm1[2];                 // 2^(the chunk's sum) - 1, by the chunk's parity
     uint32_t tmem;
     int32_t abort;
 };
+__host__ __device__ constexpr int tab_at(int anchor) { return anchor == 1 ? 0 : anchor == 2 ? 32 : 96; }
 static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && OFF_MISC % 16 == 0, "read as float4");
 constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc));
 static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
 constexpr uint32_t COL_QK = 0, COL_O1 = 128, COL_O2 = 256, COL_U = 384;  // tensor memory columns (P over A)
-constexpr int THREADS = 320;
+// warps: 0-7 scores, 8-15 state, 16-19 v~, then one each
+constexpr int GROUP = 256, VGROUP = 128;
+constexpr int WARP_LOAD = 20, WARP_MMA = 21, WARP_DECAY = 22, WARP_STORE = 23, THREADS = 768;
+// Registers: 24 warps launch with 80; 8 x 72 + 8 x 112 + 4 x 64 + 4 x 48 = 24 x 80.
+constexpr int REGS = 80, REGS_SCORES = 72, REGS_STATE = 112, REGS_V = 64, REGS_AUX = 48;
+static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 4 * REGS_V + 4 * REGS_AUX == 24 * REGS, "the launch's registers");
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr long long SPINS = 1ll << 24;
 
 struct Task {
@@ -134,7 +158,10 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
     return t;
 }
 
-// a bounded wait; false: it ran out, or another role has given up
+// A bounded wait for a barrier's phase. (A parity wait takes the phase before
+// last for the next: every role that waits on a barrier waits for each of its
+// phases in turn, or has seen the one before complete through another wait.)
+// False: it ran out, or another role has given up
 __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
     for (long long i = 0; i < SPINS; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -150,35 +177,29 @@ __device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parit
     return __all_sync(0xffffffffu, wait(m, bar, parity, status));
 }
 
-// the chunk's log2 decay of token `row` (0 behind the segment), and whether its gate is bad
+// g of token `row` of a chunk (0 behind the segment)
 __device__ __forceinline__ float gate_raw(const Params &a, int64_t t0, int row, int left, int h) {
     if (row >= left) return 0.f;
     return __ldg(a.g + (a.g_per_token ? (t0 + row) * a.H + h : h));
 }
 __device__ __forceinline__ float log2_decay(float g) { return fmaxf(g * LOG2E, -200.f); }  // 2^-200 is 0 in fp32
-// inclusive prefix and exclusive suffix within the warp, and the warp's total
-__device__ __forceinline__ void warp_sums(float x, int lane, float &pre, float &suf, float &tot) {
-    pre = x;
-    suf = x;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const float a = __shfl_up_sync(0xffffffffu, pre, s), b = __shfl_down_sync(0xffffffffu, suf, s);
-        if (lane >= s) pre += a;
-        if (lane + s < 32) suf += b;
-    }
-    tot = __shfl_sync(0xffffffffu, suf, 0);
-    suf = __shfl_down_sync(0xffffffffu, suf, 1);
-    if (lane == 31) suf = 0.f;
-}
 
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int kk) {  // K-major: 128 rows, k in the panels
-    return umma_desc_sw128(tile + (kk >> 2) * PANEL + (kk & 3) * 32, 16, 1024);
+// Operand descriptors: a tile's own, and the step to k-block kk of 16 added to
+// its low word (all within 256 KB, so no carry leaves the address field). The
+// low word goes through an empty asm once per use, which keeps the compiler from
+// computing every descriptor ahead of the chunk loop and spilling them.
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return umma_desc_sw128(tile, 16, 1024); }  // K-major
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, uint32_t panel) {  // MN-major: rows are k
+    return umma_desc_sw128(tile, panel, 1024);
 }
-__device__ __forceinline__ uint64_t desc_mn(uint32_t tile, int kk, uint32_t panel) {  // MN-major: rows are k
-    return umma_desc_sw128(tile + kk * 2048, panel, 1024);
+__device__ __forceinline__ uint64_t fresh(uint64_t d) {
+    asm volatile("" : "+l"(d));
+    return d;
 }
+__device__ __forceinline__ constexpr uint64_t step_k(int kk) { return ((kk >> 2) * PANEL + (kk & 3) * 32) >> 4; }
+__device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 2048) >> 4; }
 
-// ---- warp 8: tile loads
+// ---- one thread: tile loads
 template <Pass PASS>
 __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
@@ -212,7 +233,7 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
     }
 }
 
-// ---- warp 9, one thread: MMAs
+// ---- one thread: MMAs
 template <Pass PASS>
 __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
@@ -221,7 +242,7 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
     int32_t *status = p.a.status;
     int n = 0;
     uint32_t it = 0;
-    const uint32_t sS = smem_u32(smem + OFF_S), sVT = smem_u32(smem + OFF_VT);
+    const uint32_t base = smem_u32(smem);
     const int tasks = tasks_of<PASS>(p);
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
@@ -229,108 +250,251 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
         for (int c = 0; c < t.len; c += C, n += PER, ++it) {
             const uint32_t ph = it & 1;
             const int iq = n % TILES, ik = (n + PER - 2) % TILES, iv = (n + PER - 1) % TILES;
-            const uint32_t tq = smem_u32(smem + iq * TILE), tk = smem_u32(smem + ik * TILE), tv = smem_u32(smem + iv * TILE);
             if (!wait(m, &m->full[ik], ((n + PER - 2) / TILES) & 1, status)) return;
             if (PASS != Pass::STATES) {
                 if (!wait(m, &m->full[iq], (n / TILES) & 1, status)) return;
                 tc_fence_after();
+                const uint64_t q = fresh(desc_k(base + iq * TILE)), k = fresh(desc_k(base + ik * TILE));
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, desc_k(tq, kk), desc_k(tk, kk), ID_QK, kk > 0);
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
                 umma_commit(&m->qk);
-                if (!wait(m, &m->s, ph, status)) return;
-                if (it > 0 && !wait(m, &m->ofree, ph ^ 1, status)) return;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk)
-                    umma_f16(tmem + COL_O1, desc_k(tq, kk), desc_mn(sS, kk, PANEL), ID_QS, kk > 0);
-                umma_commit(&m->empty[iq]);
             }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!wait(m, half ? &m->vt1 : &m->vt0, ph, status)) return;
+            if (it > 0 && !wait(m, &m->ufree, ph ^ 1, status)) return;
+            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+#pragma unroll 1
+            for (int st = 0; st < STAGES; ++st) {
+                if (!wait(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1, status)) return;
                 tc_fence_after();
+                const uint64_t k = fresh(kt + st * step_mn(STAGE_ROWS / 16));
+                const uint64_t v = fresh(desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    umma_f16(tmem + COL_U, desc_mn(tk, 4 * half + kk, PANEL), desc_mn(sVT, kk, VT_PANEL), ID_U,
-                             half > 0 || kk > 0);
-                    umma_f16(tmem + COL_U, desc_mn(tk, 4 * half + kk, PANEL), desc_mn(sVT + VT_TERM, kk, VT_PANEL), ID_U, 1);
+                for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
+                    umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk), ID_U, st > 0 || kk > 0);
+                    umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk) + (VT_TERM >> 4), ID_U, 1);
                 }
-                umma_commit(half ? &m->u1 : &m->u0);
-            }
-            umma_commit(&m->empty[ik]);
-            if (PASS != Pass::STATES) {
-                if (!wait(m, &m->full[iv], ((n + PER - 1) / TILES) & 1, status)) return;
-                if (!wait(m, &m->p, ph, status)) return;
-                tc_fence_after();
+                umma_commit(&m->vfree[st & 1]);
+                if (PASS != Pass::STATES && st == 1) {
+                    if (!wait(m, &m->s, ph, status)) return;
+                    if (it > 0 && !wait(m, &m->ofree, ph ^ 1, status)) return;
+                    tc_fence_after();
+                    const uint64_t q = fresh(desc_k(base + iq * TILE)), s = fresh(desc_mn(base + OFF_S, PANEL));
 #pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    umma_ts(tmem + COL_O2, tmem + COL_QK + 8 * kk, desc_mn(tv, kk, PANEL), ID_PV, kk > 0);
-                umma_commit(&m->o);
+                    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
+                    umma_commit(&m->empty[iq]);
+                }
             }
-            umma_commit(&m->empty[iv]);
+            umma_commit(&m->u);
+            umma_commit(&m->empty[ik]);
+            if (PASS == Pass::STATES) {
+                umma_commit(&m->empty[iv]);
+                continue;
+            }
+            // P v comes last: zeros behind a segment's end are in v by now, and v~ has been made of it (o goes into its tile)
+            if (!wait(m, &m->full[iv], ((n + PER - 1) / TILES) & 1, status)) return;
+            if (!wait(m, &m->p, ph, status)) return;
+            tc_fence_after();
+            const uint64_t vv = fresh(desc_mn(base + iv * TILE, PANEL));
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk)
+                umma_ts(tmem + COL_O2, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), vv + step_mn(kk), ID_PV, kk > 0);
+            umma_commit(&m->o);
         }
     }
 }
 
-// ---- warpgroup 0: decayed scores and the output (thread = token row)
+// ---- one warp: decay tables. Lane l has token l of each block of 32.
 template <Pass PASS>
-__device__ __forceinline__ void role_scores(const ChunkParams &p, Misc *m, uint32_t tmem) {
+__device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
     const Params &a = p.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
+    const int lane = threadIdx.x & 31;
     uint32_t it = 0;
-    bool bad = false, fail = false;  // (a warp that gives up tells the others at the next barrier)
+    bool bad = false;
     const int tasks = tasks_of<PASS>(p);
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) continue;
-        float graw = gate_raw(a, t.t0, tid, t.len, t.h);
+        float raw[4], sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) raw[b] = gate_raw(a, t.t0, 32 * b + lane, t.len, t.h);
         for (int c = 0; c < t.len; c += C, ++it) {
-            const uint32_t ph = it & 1;
-            const int left = t.len - c;  // tokens from this chunk on
-            bad |= !(graw <= 0.f);
-            const float x = log2_decay(graw);
-            if (left > C) graw = gate_raw(a, t.t0 + c + C, tid, left - C, t.h);
-            float pre, suf, tot;
-            warp_sums(x, lane, pre, suf, tot);
-            if (lane == 0) m->tot0[warp] = tot;
-            if (named_bar_or(1, 128, fail)) return;
-            float upto = pre, after = suf;
+            float pre[4], suf[4], tot[4];
 #pragma unroll
-            for (int b = 0; b < 3; ++b)
-                if (b < warp) upto += m->tot0[b];
+            for (int b = 0; b < 4; ++b) {
+                bad |= !(raw[b] <= 0.f);
+                pre[b] = suf[b] = log2_decay(raw[b]);
+                raw[b] = gate_raw(a, t.t0 + c + C, 32 * b + lane, t.len - c - C, t.h);
+            }
 #pragma unroll
-            for (int b = 1; b < 4; ++b) {  // anchor: the start of block b
-                if (b > warp) {
-                    m->tab[b - 1][tid] = ex2(after);
-                    after += m->tot0[b];
+            for (int s = 1; s < 32; s <<= 1) {  // inclusive sums from either end of the block
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const float x = __shfl_up_sync(0xffffffffu, pre[b], s), y = __shfl_down_sync(0xffffffffu, suf[b], s);
+                    if (lane >= s) pre[b] += x;
+                    if (lane + s < 32) suf[b] += y;
                 }
             }
-            m->pre[tid] = pre;
-            const float row = ex2(pre), entry = a.scale * ex2(upto);
-            named_bar_sync(1, 128);
-            if (!wait_warp(m, &m->qk, ph, a.status)) {
-                fail = true;
-                continue;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                tot[b] = __shfl_sync(0xffffffffu, suf[b], 0);
+                suf[b] = __shfl_down_sync(0xffffffffu, suf[b], 1);  // after the token
+                if (lane == 31) suf[b] = 0.f;
             }
-            tc_fence_after();
+            // the last chunk's tables have been read
+            if (it > 0) {
+                if (PASS != Pass::STATES && !wait_warp(m, &m->p, (it - 1) & 1, a.status)) return;
+                if (!wait_warp(m, &m->wfree, (it - 1) & 1, a.status)) return;
+            }
+            float before = 0.f;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {  // key blocks of 32
-                uint32_t out[16];
-                if (b > warp) {
+            for (int b = 0; b < 4; ++b) {
+                float after = suf[b];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[j] = 0;
-                } else {
-                    uint32_t s[32];
-                    tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
-                    tmem_wait_ld();
-                    if (b < warp) {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[warp - 1][32 * b]);
+                for (int x = b + 1; x < 4; ++x) {
+                    if (PASS != Pass::STATES) m->tab[tab_at(x) + 32 * b + lane] = ex2(after);
+                    after += tot[x];
+                }
+                m->w[32 * b + lane] = ex2(after);
+                if (PASS != Pass::STATES) {
+                    m->pre[32 * b + lane] = pre[b];
+                    m->upto[32 * b + lane] = ex2(pre[b] + before);
+                    before += tot[b];
+                }
+            }
+            const float total = (tot[0] + tot[1]) + (tot[2] + tot[3]);
+            sum += total;
+            // (minus one, so that a slow decay is not rounded away chunk after chunk)
+            if (lane == 0) m->dm1[it & 1] = expm1f(total * (1.f / LOG2E));
+            mbar_arrive(&m->dec);
+        }
+        if (PASS == Pass::STATES && lane == 0) *t.decay = sum;
+    }
+    if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
+}
+
+// ---- warps 16-19: v~ = 2^(sum of g after j) v in two bf16 terms, 16-byte pieces in the tile's own order
+template <Pass PASS>
+__device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m) {
+    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+    int32_t *status = p.a.status;
+    const int tid = threadIdx.x & (VGROUP - 1);
+    uint32_t it = 0;
+    int n = 0;
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) continue;
+        for (int c = 0; c < t.len; c += C, n += PER, ++it) {
+            const int left = t.len - c, nk = n + PER - 2, nv = n + PER - 1;
+            unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
+            if (!wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1, status)) return;
+            if (left < C && !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1, status)) return;
+            if (!wait_warp(m, &m->dec, it & 1, status)) return;
+#pragma unroll 1
+            for (int st = 0; st < STAGES; ++st) {
+                const uint32_t use = 2 * it + (st >> 1);
+                if (use && !wait_warp(m, &m->vfree[st & 1], (use - 1) & 1, status)) return;
+                unsigned char *vt = smem + OFF_VT + (st & 1) * VT_STAGE;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int panel = i >> 1, off = ((i & 1) * VGROUP + tid) * 16;  // 32 rows x 8 pieces a panel
+                    const int row = STAGE_ROWS * st + (off >> 7);
+                    const int at = panel * PANEL + st * VT_PANEL + off;
+                    uint4 u = *reinterpret_cast<const uint4 *>(tv + at);
+                    const float wr = m->w[row];
+                    if (row >= left) {  // behind the segment, someone else's rows: zeros in k, v and v~
+                        u = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(tv + at) = u;
+                        *reinterpret_cast<uint4 *>(tk + at) = u;
+                    }
+                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = unpack_bf16(v[j]);
+                        const float y0 = f.x * wr, y1 = f.y * wr;
+                        hi[j] = pack_bf16(y0, y1);
+                        const float2 b = unpack_bf16(hi[j]);
+                        lo[j] = pack_bf16(y0 - b.x, y1 - b.y);
+                    }
+                    *reinterpret_cast<uint4 *>(vt + panel * VT_PANEL + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(vt + VT_TERM + panel * VT_PANEL + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                fence_proxy_async_shared();
+                mbar_arrive(&m->vt[st & 1]);
+            }
+            mbar_arrive(&m->wfree);
+        }
+    }
+}
+
+// ---- one thread: o from the chunk's v tile to memory, then the tile is free
+template <Pass PASS>
+__device__ __forceinline__ void role_store(const ChunkParams &p, unsigned char *smem, Misc *m) {
+    int n = 0;
+    uint32_t it = 0;
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) continue;
+        for (int c = 0; c < t.len; c += C, n += 3, ++it) {
+            if (!wait(m, &m->ostage, it & 1, p.a.status)) return;
+            if (t.len - c >= C) {
+                const unsigned char *src = smem + (n + 2) % TILES * TILE;
+                tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c));
+                tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c));
+                bulk_commit();
+                bulk_wait_read();
+            }
+            mbar_arrive(&m->empty[(n + 2) % TILES]);
+        }
+    }
+    bulk_wait_all();
+}
+
+// ---- warps 0-7: decayed scores and the output. Two threads share a token row: key blocks 0 and 3 or 1 and 2 of the scores, one
+// half of the values of the output.
+template <Pass PASS>
+__device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+    const Params &a = p.a;
+    const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
+    uint32_t it = 0;
+    int n = 0;
+    bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
+    const int tasks = tasks_of<PASS>(p);
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        if (t.skip) continue;
+        for (int c = 0; c < t.len; c += C, n += 3, ++it) {
+            const uint32_t ph = it & 1;
+            const int left = t.len - c;  // tokens from this chunk on
+            unsigned char *tile = smem + (n + 2) % TILES * TILE + half * PANEL;  // o goes where v was
+            fail = fail || !wait_warp(m, &m->dec, ph, a.status) || !wait_warp(m, &m->qk, ph, a.status);
+            float entry = 0.f;
+            if (!fail) {
+                tc_fence_after();
+                const float pre = m->pre[tid], row = ex2(pre);
+                entry = a.scale * m->upto[tid];
+                const int b0 = half ? 1 : 0, b1 = half ? 2 : 3;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {  // key blocks of 32
+                    const int b = i ? b1 : b0;
+                    uint32_t s[32], out[16];
+                    if (b <= warp) {
+                        tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
+                        tmem_wait_ld();
+                    }
+                    if (b > warp) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) out[j] = 0;
+                    } else if (b < warp) {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float4 w = f[j];
                             out[2 * j] = pack_bf16(__uint_as_float(s[4 * j]) * (row * w.x), __uint_as_float(s[4 * j + 1]) * (row * w.y));
-                            out[2 * j + 1] = pack_bf16(__uint_as_float(s[4 * j + 2]) * (row * w.z), __uint_as_float(s[4 * j + 3]) * (row * w.w));
+                            out[2 * j + 1] =
+                                pack_bf16(__uint_as_float(s[4 * j + 2]) * (row * w.z), __uint_as_float(s[4 * j + 3]) * (row * w.w));
                         }
                     } else {
                         const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
@@ -346,58 +510,66 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, Misc *m, uint3
                             out[2 * j + 1] = pack_bf16(s2, s3);
                         }
                     }
+                    tmem_st16(tmem + lanes + COL_QK + 32 * b, out);  // over the scores it comes from
                 }
-                tmem_st16(tmem + lanes + COL_QK + 16 * b, out);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&m->p);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&m->p);
-            if (!wait_warp(m, &m->o, ph, a.status)) {
-                fail = true;
-                continue;
-            }
-            tc_fence_after();
-            __nv_bfloat16 *dst = a.o + ((t.t0 + c + tid) * a.H + t.h) * DV;
+            fail = fail || !wait_warp(m, &m->o, ph, a.status);
+            if (!fail) {
+                tc_fence_after();
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                uint32_t o1[16], o2[16], w[8];
-                tmem_ld16(tmem + lanes + COL_O1 + 16 * b, o1);
-                tmem_ld16(tmem + lanes + COL_O2 + 16 * b, o2);
-                tmem_wait_ld();
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t o1[16], o2[16], w[8];
+                    tmem_ld16(tmem + lanes + COL_O1 + 64 * half + 16 * b, o1);
+                    tmem_ld16(tmem + lanes + COL_O2 + 64 * half + 16 * b, o2);
+                    tmem_wait_ld();
+                    if (b == 3) {
+                        tc_fence_before();
+                        mbar_arrive(&m->ofree);
+                    }
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    w[j] = pack_bf16(fmaf(entry, __uint_as_float(o1[2 * j]), a.scale * __uint_as_float(o2[2 * j])),
-                                     fmaf(entry, __uint_as_float(o1[2 * j + 1]), a.scale * __uint_as_float(o2[2 * j + 1])));
-                if (tid < left) {
-                    reinterpret_cast<uint4 *>(dst)[2 * b] = make_uint4(w[0], w[1], w[2], w[3]);
-                    reinterpret_cast<uint4 *>(dst)[2 * b + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = pack_bf16(fmaf(entry, __uint_as_float(o1[2 * j]), a.scale * __uint_as_float(o2[2 * j])),
+                                         fmaf(entry, __uint_as_float(o1[2 * j + 1]), a.scale * __uint_as_float(o2[2 * j + 1])));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)  // the tile's swizzle: 16-byte piece ^ row % 8
+                        *reinterpret_cast<uint4 *>(tile + tid * 128 + (((2 * b + j) ^ (tid & 7)) << 4)) =
+                            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&m->ofree);
+            if (left < C) {  // rows behind the segment are not written
+                if (named_bar_or(1, GROUP, fail)) return;
+                for (int i = tid; i < left * 8; i += 128) {
+                    const int r = i >> 3, j = i & 7;
+                    *reinterpret_cast<uint4 *>(a.o + ((t.t0 + c + r) * a.H + t.h) * DV + 64 * half + 8 * j) =
+                        *reinterpret_cast<const uint4 *>(tile + r * 128 + ((j ^ (r & 7)) << 4));
+                }
+            } else {
+                fence_proxy_async_shared();
+            }
+            mbar_arrive(&m->ostage);
         }
     }
-    if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- warpgroup 1: v~ and the state (thread = key row of S)
+// ---- warps 8-15: the state. Two threads share a key row of S, one half of its values each.
 template <Pass PASS>
 __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
-    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+    constexpr int NV = DV / 2;
     const Params &a = p.a;
-    const int tid = threadIdx.x - 128, warp = tid >> 5, lane = tid & 31;
+    const int gtid = threadIdx.x - GROUP, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
-    unsigned char *sS = smem + OFF_S, *sVT = smem + OFF_VT;
+    unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
-    int n = 0;
-    bool fail = false;
-    float S[DV];
+    float S[NV];
     auto publish = [&]() {  // the bf16 copy that q multiplies
 #pragma unroll
-        for (int j = 0; j < DV / 8; ++j) {
+        for (int j = 0; j < NV / 8; ++j) {
             const uint4 u = make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
                                        pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
-            *reinterpret_cast<uint4 *>(sS + (j >> 3) * PANEL + tid * 128 + (((j & 7) ^ (tid & 7)) << 4)) = u;
+            *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) = u;
         }
         fence_proxy_async_shared();
         mbar_arrive(&m->s);
@@ -406,100 +578,40 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) {
-            if (PASS == Pass::WHOLE && tid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            if (PASS == Pass::WHOLE && gtid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
             continue;
         }
+        const size_t at = static_cast<size_t>(tid) * DV + half * NV;
         if (t.sin) {
 #pragma unroll
-            for (int j = 0; j < DV; j += 8) ld_f8(S + j, t.sin + static_cast<size_t>(tid) * DV + j);
+            for (int j = 0; j < NV; j += 8) ld_f8(S + j, t.sin + at + j);
         } else {
 #pragma unroll
-            for (int j = 0; j < DV; ++j) S[j] = 0.f;
+            for (int j = 0; j < NV; ++j) S[j] = 0.f;
         }
-        float sum = 0.f;  // log2 decay of the segment
-        float graw = gate_raw(a, t.t0, tid, t.len, t.h);
         if (PASS != Pass::STATES && t.len > 0) publish();
-        for (int c = 0; c < t.len; c += C, n += PER, ++it) {
-            const uint32_t ph = it & 1;
-            const int left = t.len - c;
-            const int nk = n + PER - 2, nv = n + PER - 1;
-            unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
-            const float x = log2_decay(graw);
-            if (left > C) graw = gate_raw(a, t.t0 + c + C, tid, left - C, t.h);
-            float pre, suf, tot;
-            warp_sums(x, lane, pre, suf, tot);
-            if (lane == 0) m->tot1[warp] = tot;
-            if (named_bar_or(2, 128, fail)) return;
-#pragma unroll
-            for (int b = 1; b < 4; ++b)
-                if (b > warp) suf += m->tot1[b];
-            m->w[tid] = ex2(suf);
-            const float total = (m->tot1[0] + m->tot1[1]) + (m->tot1[2] + m->tot1[3]);
-            sum += total;
-            fail = !wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1, a.status);
-            if (left < C) {  // rows behind the segment belong to someone else: zeros in k and v
-                fail |= !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1, a.status);
-                if (tid >= left && !fail) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int off = (j >> 3) * PANEL + tid * 128 + ((j & 7) << 4);
-                        *reinterpret_cast<uint4 *>(tk + off) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(tv + off) = make_uint4(0, 0, 0, 0);
-                    }
-                }
-            }
-            if (named_bar_or(2, 128, fail)) return;  // weights (and zeros) written
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (half && !wait_warp(m, &m->u0, ph, a.status)) {
-                    fail = true;
-                    break;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {  // 16-byte pieces: 64 rows x 8 of each panel
-                    const int piece = i * 128 + tid, panel = piece >> 9, in = piece & 511, r = in >> 3;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(tv + panel * PANEL + half * VT_PANEL + in * 16);
-                    const float wr = m->w[64 * half + r];
-                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack_bf16(v[j]);
-                        const float y0 = f.x * wr, y1 = f.y * wr;
-                        hi[j] = pack_bf16(y0, y1);
-                        const float2 b = unpack_bf16(hi[j]);
-                        lo[j] = pack_bf16(y0 - b.x, y1 - b.y);
-                    }
-                    *reinterpret_cast<uint4 *>(sVT + panel * VT_PANEL + in * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(sVT + VT_TERM + panel * VT_PANEL + in * 16) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                fence_proxy_async_shared();
-                mbar_arrive(half ? &m->vt1 : &m->vt0);
-            }
-            if (fail || !wait_warp(m, &m->u1, ph, a.status)) {
-                fail = true;
-                continue;
-            }
+        for (int c = 0; c < t.len; c += C, ++it) {
+            if (!wait_warp(m, &m->u, it & 1, a.status)) return;
             tc_fence_after();
-            // S e^total + U, with e^total - 1 so that a slow decay is not rounded away chunk after chunk
-            const float dm1 = expm1f(total * (1.f / LOG2E));
+            const float dm1 = m->dm1[it & 1];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < NV / 32; ++b) {
                 uint32_t u[32];
-                tmem_ld32(tmem + lanes + COL_U + 32 * b, u);
+                tmem_ld32(tmem + lanes + COL_U + NV * half + 32 * b, u);
                 tmem_wait_ld();
+                if (b == NV / 32 - 1) {
+                    tc_fence_before();
+                    mbar_arrive(&m->ufree);
+                }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) S[32 * b + j] = fmaf(S[32 * b + j], dm1, S[32 * b + j]) + __uint_as_float(u[j]);
             }
-            tc_fence_before();
-            if (PASS != Pass::STATES && left > C) publish();  // (u1 came after q S: the old copy has been read)
+            if (PASS != Pass::STATES && c + C < t.len) publish();  // (u came after q S: the old copy has been read)
         }
-        if (t.sout && !fail) {
+        if (t.sout) {
 #pragma unroll
-            for (int j = 0; j < DV; j += 8) st_f8(t.sout + static_cast<size_t>(tid) * DV + j, S + j);
+            for (int j = 0; j < NV; j += 8) st_f8(t.sout + at + j, S + j);
         }
-        if (PASS == Pass::STATES && tid == 0) *t.decay = sum;
     }
 }
 
@@ -514,38 +626,52 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
             mbar_init(&m->empty[i], 1);
         }
         mbar_init(&m->qk, 1);
-        mbar_init(&m->u0, 1);
-        mbar_init(&m->u1, 1);
+        mbar_init(&m->u, 1);
         mbar_init(&m->o, 1);
-        mbar_init(&m->vt0, 128);
-        mbar_init(&m->vt1, 128);
-        mbar_init(&m->s, 128);
-        mbar_init(&m->p, 128);
-        mbar_init(&m->ofree, 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&m->vfree[i], 1);
+            mbar_init(&m->vt[i], VGROUP);
+        }
+        mbar_init(&m->dec, 32);
+        mbar_init(&m->wfree, VGROUP);
+        mbar_init(&m->s, GROUP);
+        mbar_init(&m->p, GROUP);
+        mbar_init(&m->ufree, GROUP);
+        mbar_init(&m->ofree, GROUP);
+        mbar_init(&m->ostage, GROUP);
         m->abort = 0;
         mbar_fence_init();
     }
-    if (warp == 9) tmem_alloc(&m->tmem, 512);
+    if (warp == WARP_MMA) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    if (warp < 4) {
-        if (PASS == Pass::WHOLE)
-            role_scores<Pass::WHOLE>(p, m, tmem);
-        else if (PASS == Pass::OUTPUT)
-            role_scores<Pass::OUTPUT>(p, m, tmem);
-    } else if (warp < 8) {
+    if (warp < 8) {
+        fewer_registers<REGS_SCORES>();
+        if (PASS != Pass::STATES) role_scores<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m, tmem);
+    } else if (warp < 16) {
+        more_registers<REGS_STATE>();
         role_state<PASS>(p, smem, m, tmem);
-    } else if (warp == 8) {
-        if (lane == 0) role_load<PASS>(p, smem, m);
+    } else if (warp < 20) {
+        fewer_registers<REGS_V>();
+        role_v<PASS>(p, smem, m);
     } else {
-        if (lane == 0) role_mma<PASS>(p, smem, m, tmem);
+        fewer_registers<REGS_AUX>();
+        if (warp == WARP_LOAD) {
+            if (lane == 0) role_load<PASS>(p, smem, m);
+        } else if (warp == WARP_MMA) {
+            if (lane == 0) role_mma<PASS>(p, smem, m, tmem);
+        } else if (warp == WARP_DECAY) {
+            role_decay<PASS>(p, m);
+        } else if (PASS != Pass::STATES) {
+            if (lane == 0) role_store<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m);
+        }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
 }
 
 // ---- segments: one CTA. Sequence n of c chunks gets ceil(c / L) segments of about equal length.
@@ -672,8 +798,13 @@ int num_sms() {
 
 template <Pass PASS>
 cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(kda_linear_chunk_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kda_linear_chunk_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
+    static const int regs = [] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<PASS>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
     kda_linear_chunk_kernel<PASS><<<static_cast<int>(most_tasks < sms ? most_tasks : sms), THREADS, SMEM, stream>>>(p);
     return cudaGetLastError();
 }
@@ -721,7 +852,8 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     ChunkParams p{};
     p.a = a;
     const int hk = a.H / a.rep;
-    if (!encode(&p.tq, a.q, a.T, hk, a.qs) || !encode(&p.tk, a.k, a.T, hk, a.ks) || !encode(&p.tv, a.v, a.T, a.H, a.vs))
+    if (!encode(&p.tq, a.q, a.T, hk, a.qs) || !encode(&p.tk, a.k, a.T, hk, a.ks) || !encode(&p.tv, a.v, a.T, a.H, a.vs) ||
+        !encode(&p.to, a.o, a.T, a.H, static_cast<int64_t>(a.H) * DV))
         return cudaErrorInvalidValue;
     p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
