@@ -12,7 +12,7 @@
 // of one. Six roles run side by side, each a chunk or two ahead of the next:
 //   load    one thread: q, k and v tiles by TMA into a ring of five 32 KB tiles
 //   decays  one warp: the chunk's decay tables from g
-//   v~      4 warps: v~ in stages of 32 tokens
+//   v~      8 warps: v~ in stages of 32 tokens
 //   scores  8 warps: P, then o_i into the chunk's v tile
 //   state   8 warps: S
 //   MMA, store   one thread each
@@ -87,12 +87,12 @@ constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc));
 static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
 constexpr uint32_t COL_QK = 0, COL_O1 = 128, COL_O2 = 256, COL_U = 384;  // tensor memory columns (P over A)
-// warps: 0-7 scores, 8-15 state, 16-19 v~, then one each
-constexpr int GROUP = 256, VGROUP = 128;
-constexpr int WARP_LOAD = 20, WARP_MMA = 21, WARP_DECAY = 22, WARP_STORE = 23, THREADS = 768;
-// Registers: 24 warps launch with 80; 8 x 72 + 8 x 112 + 4 x 64 + 4 x 48 = 24 x 80.
-constexpr int REGS = 80, REGS_SCORES = 72, REGS_STATE = 112, REGS_V = 64, REGS_AUX = 48;
-static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 4 * REGS_V + 4 * REGS_AUX == 24 * REGS, "the launch's registers");
+// warps: 0-7 scores, 8-15 state, 16-23 v~, then one each
+constexpr int GROUP = 256;
+constexpr int WARP_LOAD = 24, WARP_MMA = 25, WARP_DECAY = 26, WARP_STORE = 27, THREADS = 896;
+// Registers: 28 warps launch with 72; the roles' shares add up to no more.
+constexpr int REGS = 72, REGS_SCORES = 72, REGS_STATE = 104, REGS_V = 48, REGS_AUX = 56;
+static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 8 * REGS_V + 4 * REGS_AUX <= 28 * REGS, "the launch's registers");
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -101,7 +101,7 @@ template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-constexpr long long SPINS = 1ll << 24;
+constexpr int WAITS = 20000;  // waits of up to WAIT_NS each before a role gives up
 
 struct Task {
     int64_t t0;
@@ -163,18 +163,23 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
 // phases in turn, or has seen the one before complete through another wait.)
 // False: it ran out, or another role has given up
 __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
-    for (long long i = 0; i < SPINS; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 1023) == 1023 && *reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
+#pragma unroll 1
+    for (int i = 0; i < WAITS; ++i) {
+        if (mbar_wait_some(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
     }
     set_status(status, KDA_ERR_TIMEOUT);
     *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
     return false;
 }
-
 // the same for a whole warp, with one answer
 __device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
     return __all_sync(0xffffffffu, wait(m, bar, parity, status));
+}
+// one arrival for the whole warp
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    mbar_arrive_if(bar, (threadIdx.x & 31) == 0);
 }
 
 // g of token `row` of a chunk (0 behind the segment)
@@ -184,56 +189,64 @@ __device__ __forceinline__ float gate_raw(const Params &a, int64_t t0, int row, 
 }
 __device__ __forceinline__ float log2_decay(float g) { return fmaxf(g * LOG2E, -200.f); }  // 2^-200 is 0 in fp32
 
-// Operand descriptors: a tile's own, and the step to k-block kk of 16 added to
-// its low word (all within 256 KB, so no carry leaves the address field). The
-// low word goes through an empty asm once per use, which keeps the compiler from
-// computing every descriptor ahead of the chunk loop and spilling them.
+// Operand descriptors: a tile's own, and the step to k-block kk of 16 added to it (within the address field: no carry leaves it).
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return umma_desc_sw128(tile, 16, 1024); }  // K-major
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, uint32_t panel) {  // MN-major: rows are k
     return umma_desc_sw128(tile, panel, 1024);
 }
-__device__ __forceinline__ uint64_t fresh(uint64_t d) {
-    asm volatile("" : "+l"(d));
-    return d;
-}
 __device__ __forceinline__ constexpr uint64_t step_k(int kk) { return ((kk >> 2) * PANEL + (kk & 3) * 32) >> 4; }
 __device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 2048) >> 4; }
 
-// ---- one thread: tile loads
+// ---- one thread: tile loads. A chunk's tiles take slots in the order q, v, k: the third waits for the slot of the chunk
+// before's first, so the first is the one that is free soonest (q) and the third not the one that is needed first (v). They are
+// issued in the order v, q, k, since q's slot waits for an output to be stored.
 template <Pass PASS>
 __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
-    int n = 0;  // tiles issued
+    int n = 0, part = 0;  // tiles of whole chunks issued, and which of a chunk that was given up
     bool ok = true;
     const int tasks = tasks_of<PASS>(p);
+#pragma unroll 1
     for (int id = blockIdx.x; ok && id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) continue;
         const int hk = t.h / p.a.rep;
+#pragma unroll 1
         for (int c = 0; ok && c < t.len; c += C) {
             const int row = static_cast<int>(t.t0 + c);
-            for (int i = 3 - PER; ok && i < 3; ++i, ++n) {
-                const int slot = n % TILES;
-                if (n >= TILES) ok = wait(m, &m->empty[slot], ((n / TILES) - 1) & 1, p.a.status);
-                if (!ok) break;
+            part = 0;
+#pragma unroll 1
+            for (int i = 0; i < PER; ++i) {
+                const int at = PER == 2 ? i : i == 0 ? 1 : i == 1 ? 0 : 2;  // tile of the chunk: (q,) v, k
+                const int slot = (n + at) % TILES;
+                if (n + at >= TILES && !wait(m, &m->empty[slot], ((n + at) / TILES - 1) & 1, p.a.status)) {
+                    ok = false;
+                    break;
+                }
                 unsigned char *dst = smem + slot * TILE;
-                const CUtensorMap *map = i == 0 ? &p.tq : i == 1 ? &p.tk : &p.tv;
-                const int head = i == 2 ? t.h : hk;
+                const bool is_v = at == PER - 2;
+                const CUtensorMap *map = is_v ? &p.tv : at == PER - 1 ? &p.tk : &p.tq;
+                const int head = is_v ? t.h : hk;
                 mbar_arrive_expect_tx(&m->full[slot], TILE);
                 tma_load_3d(dst, map, 0, head, row, &m->full[slot]);
                 tma_load_3d(dst + PANEL, map, 64, head, row, &m->full[slot]);
+                part |= 1 << at;
             }
+            if (ok) n += PER;
         }
     }
     // no copy and no commit of this CTA is in flight when it ends
-    for (int k = n > TILES ? n - TILES : 0; k < n; ++k) {
-        if (ok) ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1, p.a.status);
-        for (long long i = 0; !ok && i < SPINS; ++i)
-            if (mbar_try_wait(&m->full[k % TILES], (k / TILES) & 1)) break;
-    }
+#pragma unroll 1
+    for (int k = n > TILES ? n - TILES : 0; ok && k < n; ++k)
+        ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1, p.a.status);
+    if (ok) return;
+#pragma unroll 1
+    for (int k = n > TILES ? n - TILES : 0; k < n + PER; ++k)
+        if (k < n || (part >> (k - n) & 1)) (void)mbar_wait_some(&m->full[k % TILES], (k / TILES) & 1);
 }
 
-// ---- one thread: MMAs
+// ---- one warp: MMAs. The whole warp walks the tasks, with everything that makes an address the same in all lanes, and one
+// lane issues: from a single-lane loop each MMA took 140-190 cycles to issue, more than the 70 it runs.
 template <Pass PASS>
 __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
@@ -243,61 +256,72 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
     int n = 0;
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
-    const int tasks = tasks_of<PASS>(p);
+    const int tasks = __shfl_sync(0xffffffffu, tasks_of<PASS>(p), 0);
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
+#pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
-        if (t.skip) continue;
-        for (int c = 0; c < t.len; c += C, n += PER, ++it) {
-            const uint32_t ph = it & 1;
-            const int iq = n % TILES, ik = (n + PER - 2) % TILES, iv = (n + PER - 1) % TILES;
-            if (!wait(m, &m->full[ik], ((n + PER - 2) / TILES) & 1, status)) return;
-            if (PASS != Pass::STATES) {
-                if (!wait(m, &m->full[iq], (n / TILES) & 1, status)) return;
-                tc_fence_after();
-                const uint64_t q = fresh(desc_k(base + iq * TILE)), k = fresh(desc_k(base + ik * TILE));
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
-                umma_commit(&m->qk);
-            }
-            if (it > 0 && !wait(m, &m->ufree, ph ^ 1, status)) return;
-            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+        const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
-            for (int st = 0; st < STAGES; ++st) {
-                if (!wait(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1, status)) return;
+        for (int c = 0; c < len; c += C, n += PER, ++it) {
+            const uint32_t ph = it & 1;
+            const int iq = n % TILES, iv = (n + PER - 2) % TILES, ik = (n + PER - 1) % TILES;
+            if (!wait_warp(m, &m->full[ik], ((n + PER - 1) / TILES) & 1, status)) return;
+            if (PASS != Pass::STATES) {
+                if (!wait_warp(m, &m->full[iq], (n / TILES) & 1, status)) return;
                 tc_fence_after();
-                const uint64_t k = fresh(kt + st * step_mn(STAGE_ROWS / 16));
-                const uint64_t v = fresh(desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL));
+                const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
-                    umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk), ID_U, st > 0 || kk > 0);
-                    umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk) + (VT_TERM >> 4), ID_U, 1);
+                    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
+                    umma_commit(&m->qk);
                 }
-                umma_commit(&m->vfree[st & 1]);
+            }
+            if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1, status)) return;
+            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+#pragma unroll
+            for (int st = 0; st < STAGES; ++st) {
+                if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1, status)) return;
+                tc_fence_after();
+                const uint64_t k = kt + st * step_mn(STAGE_ROWS / 16);
+                const uint64_t v = desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
+                        umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk), ID_U, st > 0 || kk > 0);
+                        umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk) + (VT_TERM >> 4), ID_U, 1);
+                    }
+                    umma_commit(&m->vfree[st & 1]);
+                    if (st == STAGES - 1) {
+                        umma_commit(&m->u);
+                        umma_commit(&m->empty[ik]);
+                        if (PASS == Pass::STATES) umma_commit(&m->empty[iv]);
+                    }
+                }
                 if (PASS != Pass::STATES && st == 1) {
-                    if (!wait(m, &m->s, ph, status)) return;
-                    if (it > 0 && !wait(m, &m->ofree, ph ^ 1, status)) return;
+                    if (!wait_warp(m, &m->s, ph, status)) return;
+                    if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1, status)) return;
                     tc_fence_after();
-                    const uint64_t q = fresh(desc_k(base + iq * TILE)), s = fresh(desc_mn(base + OFF_S, PANEL));
+                    const uint64_t q = desc_k(base + iq * TILE), s = desc_mn(base + OFF_S, PANEL);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
-                    umma_commit(&m->empty[iq]);
+                        for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
+                        umma_commit(&m->empty[iq]);
+                    }
                 }
             }
-            umma_commit(&m->u);
-            umma_commit(&m->empty[ik]);
-            if (PASS == Pass::STATES) {
-                umma_commit(&m->empty[iv]);
-                continue;
-            }
+            if (PASS == Pass::STATES) continue;
             // P v comes last: zeros behind a segment's end are in v by now, and v~ has been made of it (o goes into its tile)
-            if (!wait(m, &m->full[iv], ((n + PER - 1) / TILES) & 1, status)) return;
-            if (!wait(m, &m->p, ph, status)) return;
+            if (!wait_warp(m, &m->full[iv], ((n + PER - 2) / TILES) & 1, status)) return;
+            if (!wait_warp(m, &m->p, ph, status)) return;
             tc_fence_after();
-            const uint64_t vv = fresh(desc_mn(base + iv * TILE, PANEL));
+            const uint64_t vv = desc_mn(base + iv * TILE, PANEL);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk)
-                umma_ts(tmem + COL_O2, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), vv + step_mn(kk), ID_PV, kk > 0);
-            umma_commit(&m->o);
+                for (int kk = 0; kk < C / 16; ++kk)
+                    umma_ts(tmem + COL_O2, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), vv + step_mn(kk), ID_PV, kk > 0);
+                umma_commit(&m->o);
+            }
         }
     }
 }
@@ -310,12 +334,14 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
     uint32_t it = 0;
     bool bad = false;
     const int tasks = tasks_of<PASS>(p);
+#pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) continue;
         float raw[4], sum = 0.f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) raw[b] = gate_raw(a, t.t0, 32 * b + lane, t.len, t.h);
+#pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             float pre[4], suf[4], tot[4];
 #pragma unroll
@@ -364,27 +390,29 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
             sum += total;
             // (minus one, so that a slow decay is not rounded away chunk after chunk)
             if (lane == 0) m->dm1[it & 1] = expm1f(total * (1.f / LOG2E));
-            mbar_arrive(&m->dec);
+            arrive_warp(&m->dec);
         }
         if (PASS == Pass::STATES && lane == 0) *t.decay = sum;
     }
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- warps 16-19: v~ = 2^(sum of g after j) v in two bf16 terms, 16-byte pieces in the tile's own order
+// ---- warps 16-23: v~ = 2^(sum of g after j) v in two bf16 terms, 16-byte pieces in the tile's own order
 template <Pass PASS>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
     int32_t *status = p.a.status;
-    const int tid = threadIdx.x & (VGROUP - 1);
+    const int tid = threadIdx.x & (GROUP - 1);
     uint32_t it = 0;
     int n = 0;
     const int tasks = tasks_of<PASS>(p);
+#pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) continue;
+#pragma unroll 1
         for (int c = 0; c < t.len; c += C, n += PER, ++it) {
-            const int left = t.len - c, nk = n + PER - 2, nv = n + PER - 1;
+            const int left = t.len - c, nk = n + PER - 1, nv = n + PER - 2;
             unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
             if (!wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1, status)) return;
             if (left < C && !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1, status)) return;
@@ -395,8 +423,8 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 if (use && !wait_warp(m, &m->vfree[st & 1], (use - 1) & 1, status)) return;
                 unsigned char *vt = smem + OFF_VT + (st & 1) * VT_STAGE;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int panel = i >> 1, off = ((i & 1) * VGROUP + tid) * 16;  // 32 rows x 8 pieces a panel
+                for (int panel = 0; panel < 2; ++panel) {
+                    const int off = tid * 16;  // 32 rows x 8 pieces a panel
                     const int row = STAGE_ROWS * st + (off >> 7);
                     const int at = panel * PANEL + st * VT_PANEL + off;
                     uint4 u = *reinterpret_cast<const uint4 *>(tv + at);
@@ -420,9 +448,9 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                     *reinterpret_cast<uint4 *>(vt + VT_TERM + panel * VT_PANEL + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 fence_proxy_async_shared();
-                mbar_arrive(&m->vt[st & 1]);
+                arrive_warp(&m->vt[st & 1]);
             }
-            mbar_arrive(&m->wfree);
+            arrive_warp(&m->wfree);
         }
     }
 }
@@ -433,19 +461,21 @@ __device__ __forceinline__ void role_store(const ChunkParams &p, unsigned char *
     int n = 0;
     uint32_t it = 0;
     const int tasks = tasks_of<PASS>(p);
+#pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) continue;
+#pragma unroll 1
         for (int c = 0; c < t.len; c += C, n += 3, ++it) {
             if (!wait(m, &m->ostage, it & 1, p.a.status)) return;
             if (t.len - c >= C) {
-                const unsigned char *src = smem + (n + 2) % TILES * TILE;
+                const unsigned char *src = smem + (n + 1) % TILES * TILE;
                 tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c));
                 tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c));
                 bulk_commit();
                 bulk_wait_read();
             }
-            mbar_arrive(&m->empty[(n + 2) % TILES]);
+            mbar_arrive(&m->empty[(n + 1) % TILES]);
         }
     }
     bulk_wait_all();
@@ -462,13 +492,15 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
     int n = 0;
     bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
     const int tasks = tasks_of<PASS>(p);
+#pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) continue;
+#pragma unroll 1
         for (int c = 0; c < t.len; c += C, n += 3, ++it) {
             const uint32_t ph = it & 1;
             const int left = t.len - c;  // tokens from this chunk on
-            unsigned char *tile = smem + (n + 2) % TILES * TILE + half * PANEL;  // o goes where v was
+            unsigned char *tile = smem + (n + 1) % TILES * TILE + half * PANEL;  // o goes where v was
             fail = fail || !wait_warp(m, &m->dec, ph, a.status) || !wait_warp(m, &m->qk, ph, a.status);
             float entry = 0.f;
             if (!fail) {
@@ -514,7 +546,7 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&m->p);
+                arrive_warp(&m->p);
             }
             fail = fail || !wait_warp(m, &m->o, ph, a.status);
             if (!fail) {
@@ -527,7 +559,7 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                     tmem_wait_ld();
                     if (b == 3) {
                         tc_fence_before();
-                        mbar_arrive(&m->ofree);
+                        arrive_warp(&m->ofree);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -541,6 +573,7 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
             }
             if (left < C) {  // rows behind the segment are not written
                 if (named_bar_or(1, GROUP, fail)) return;
+#pragma unroll 1
                 for (int i = tid; i < left * 8; i += 128) {
                     const int r = i >> 3, j = i & 7;
                     *reinterpret_cast<uint4 *>(a.o + ((t.t0 + c + r) * a.H + t.h) * DV + 64 * half + 8 * j) =
@@ -549,7 +582,7 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
             } else {
                 fence_proxy_async_shared();
             }
-            mbar_arrive(&m->ostage);
+            arrive_warp(&m->ostage);
         }
     }
 }
@@ -572,9 +605,10 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) = u;
         }
         fence_proxy_async_shared();
-        mbar_arrive(&m->s);
+        arrive_warp(&m->s);
     };
     const int tasks = tasks_of<PASS>(p);
+#pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<PASS>(p, id);
         if (t.skip) {
@@ -590,6 +624,7 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             for (int j = 0; j < NV; ++j) S[j] = 0.f;
         }
         if (PASS != Pass::STATES && t.len > 0) publish();
+#pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             if (!wait_warp(m, &m->u, it & 1, a.status)) return;
             tc_fence_after();
@@ -601,7 +636,7 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
                 tmem_wait_ld();
                 if (b == NV / 32 - 1) {
                     tc_fence_before();
-                    mbar_arrive(&m->ufree);
+                    arrive_warp(&m->ufree);
                 }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) S[32 * b + j] = fmaf(S[32 * b + j], dm1, S[32 * b + j]) + __uint_as_float(u[j]);
@@ -630,15 +665,15 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
         mbar_init(&m->o, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->vfree[i], 1);
-            mbar_init(&m->vt[i], VGROUP);
+            mbar_init(&m->vt[i], GROUP / 32);
         }
-        mbar_init(&m->dec, 32);
-        mbar_init(&m->wfree, VGROUP);
-        mbar_init(&m->s, GROUP);
-        mbar_init(&m->p, GROUP);
-        mbar_init(&m->ufree, GROUP);
-        mbar_init(&m->ofree, GROUP);
-        mbar_init(&m->ostage, GROUP);
+        mbar_init(&m->dec, 1);
+        mbar_init(&m->wfree, GROUP / 32);
+        mbar_init(&m->s, GROUP / 32);
+        mbar_init(&m->p, GROUP / 32);
+        mbar_init(&m->ufree, GROUP / 32);
+        mbar_init(&m->ofree, GROUP / 32);
+        mbar_init(&m->ostage, GROUP / 32);
         m->abort = 0;
         mbar_fence_init();
     }
@@ -648,12 +683,11 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = m->tmem;
     if (warp < 8) {
-        fewer_registers<REGS_SCORES>();
         if (PASS != Pass::STATES) role_scores<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m, tmem);
     } else if (warp < 16) {
         more_registers<REGS_STATE>();
         role_state<PASS>(p, smem, m, tmem);
-    } else if (warp < 20) {
+    } else if (warp < 24) {
         fewer_registers<REGS_V>();
         role_v<PASS>(p, smem, m);
     } else {
@@ -661,7 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
         if (warp == WARP_LOAD) {
             if (lane == 0) role_load<PASS>(p, smem, m);
         } else if (warp == WARP_MMA) {
-            if (lane == 0) role_mma<PASS>(p, smem, m, tmem);
+            role_mma<PASS>(p, smem, m, tmem);
         } else if (warp == WARP_DECAY) {
             role_decay<PASS>(p, m);
         } else if (PASS != Pass::STATES) {

@@ -14,6 +14,12 @@ __device__ __forceinline__ constexpr uint32_t idesc_bf16(bool a_mn_major, bool b
            (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
 }
+// true in one lane of a converged warp, the same one every time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 // D[tmem] (+)= A[tmem] B[smem]
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -38,6 +44,26 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_if(uint64_t *bar, bool yes) {  // (no branch)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 st;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(static_cast<uint32_t>(yes))
+        : "memory");
+}
+// A wait that lets the warp sleep until the phase completes, WAIT_NS at most. (With
+// the default time, a few hundred cycles, the polls of a CTA's waiting warps
+// slow its working ones down.)
+constexpr uint32_t WAIT_NS = 100000;
+__device__ __forceinline__ bool mbar_wait_some(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(WAIT_NS)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
