@@ -69,20 +69,20 @@ struct ChunkParams {
 struct Misc {
     uint64_t full[TILES], empty[TILES];
     uint64_t qk, u, o, vfree[2];  // tensor core -> warps (commits)
-    uint64_t dec;                 // decay tables written
+    uint64_t decw[2], dect;       // decay tables written: w and dm1; tab, pre and upto
     uint64_t vt[2], s, p;         // v~ stage, bf16 state, scores written
-    uint64_t wfree;               // the weights of v~ read
+    uint64_t wfree[2];            // w read
     uint64_t ufree, ofree, ostage;  // U read; O1 and O2 read; o in the v tile
     alignas(16) float tab[192];   // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
     alignas(16) float pre[C];     // log2 prefix of j within its block of 32
-    float upto[C];                // 2^(sum of g up to j)
-    float w[C];                   // 2^(sum of g after j up to the chunk's end)
-    float dm1[2];                 // 2^(the chunk's sum) - 1, by the chunk's parity
+    alignas(16) float upto[C];    // 2^(sum of g up to j)
+    alignas(16) float w[2][C];    // 2^(sum of g after j up to the chunk's end), a chunk ahead
+    float dm1[4];                 // 2^(the chunk's sum) - 1, of the last four chunks
     uint32_t tmem;
     int32_t abort;
 };
 __host__ __device__ constexpr int tab_at(int anchor) { return anchor == 1 ? 0 : anchor == 2 ? 32 : 96; }
-static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && OFF_MISC % 16 == 0, "read as float4");
+static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && offsetof(Misc, upto) % 16 == 0 && offsetof(Misc, w) % 16 == 0 && OFF_MISC % 16 == 0, "read as float4");
 constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc));
 static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
@@ -162,19 +162,18 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
 // last for the next: every role that waits on a barrier waits for each of its
 // phases in turn, or has seen the one before complete through another wait.)
 // False: it ran out, or another role has given up
-__device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
+__device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
+    int i = 0;
 #pragma unroll 1
-    for (int i = 0; i < WAITS; ++i) {
-        if (mbar_wait_some(bar, parity)) return true;
+    while (!mbar_wait_some(bar, parity)) {
+        if (++i == WAITS) *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
         if (*reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
     }
-    set_status(status, KDA_ERR_TIMEOUT);
-    *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
-    return false;
+    return true;
 }
 // the same for a whole warp, with one answer
-__device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity, int32_t *status) {
-    return __all_sync(0xffffffffu, wait(m, bar, parity, status));
+__device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(m, bar, parity));
 }
 // one arrival for the whole warp
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
@@ -219,7 +218,7 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
             for (int i = 0; i < PER; ++i) {
                 const int at = PER == 2 ? i : i == 0 ? 1 : i == 1 ? 0 : 2;  // tile of the chunk: (q,) v, k
                 const int slot = (n + at) % TILES;
-                if (n + at >= TILES && !wait(m, &m->empty[slot], ((n + at) / TILES - 1) & 1, p.a.status)) {
+                if (n + at >= TILES && !wait(m, &m->empty[slot], ((n + at) / TILES - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -238,7 +237,7 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
     // no copy and no commit of this CTA is in flight when it ends
 #pragma unroll 1
     for (int k = n > TILES ? n - TILES : 0; ok && k < n; ++k)
-        ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1, p.a.status);
+        ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1);
     if (ok) return;
 #pragma unroll 1
     for (int k = n > TILES ? n - TILES : 0; k < n + PER; ++k)
@@ -252,7 +251,6 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
     constexpr uint32_t ID_QK = idesc_bf16(false, false, C, C), ID_QS = idesc_bf16(false, true, C, DV),
                        ID_U = idesc_bf16(true, true, DK, DV), ID_PV = idesc_bf16(false, true, C, DV);
-    int32_t *status = p.a.status;
     int n = 0;
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
@@ -266,9 +264,9 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
         for (int c = 0; c < len; c += C, n += PER, ++it) {
             const uint32_t ph = it & 1;
             const int iq = n % TILES, iv = (n + PER - 2) % TILES, ik = (n + PER - 1) % TILES;
-            if (!wait_warp(m, &m->full[ik], ((n + PER - 1) / TILES) & 1, status)) return;
+            if (!wait_warp(m, &m->full[ik], ((n + PER - 1) / TILES) & 1)) return;
             if (PASS != Pass::STATES) {
-                if (!wait_warp(m, &m->full[iq], (n / TILES) & 1, status)) return;
+                if (!wait_warp(m, &m->full[iq], (n / TILES) & 1)) return;
                 tc_fence_after();
                 const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
                 if (elect_one()) {
@@ -276,12 +274,21 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
                     for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
                     umma_commit(&m->qk);
                 }
-            }
-            if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1, status)) return;
-            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+                if (!wait_warp(m, &m->s, ph)) return;
+                if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+                tc_fence_after();
+                const uint64_t s = desc_mn(base + OFF_S, PANEL);
+                if (elect_one()) {
 #pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
+                    umma_commit(&m->empty[iq]);
+                }
+            }
+            if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
+            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+#pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
-                if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1, status)) return;
+                if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1)) return;
                 tc_fence_after();
                 const uint64_t k = kt + st * step_mn(STAGE_ROWS / 16);
                 const uint64_t v = desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL);
@@ -298,22 +305,11 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
                         if (PASS == Pass::STATES) umma_commit(&m->empty[iv]);
                     }
                 }
-                if (PASS != Pass::STATES && st == 1) {
-                    if (!wait_warp(m, &m->s, ph, status)) return;
-                    if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1, status)) return;
-                    tc_fence_after();
-                    const uint64_t q = desc_k(base + iq * TILE), s = desc_mn(base + OFF_S, PANEL);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
-                        umma_commit(&m->empty[iq]);
-                    }
-                }
             }
             if (PASS == Pass::STATES) continue;
             // P v comes last: zeros behind a segment's end are in v by now, and v~ has been made of it (o goes into its tile)
-            if (!wait_warp(m, &m->full[iv], ((n + PER - 2) / TILES) & 1, status)) return;
-            if (!wait_warp(m, &m->p, ph, status)) return;
+            if (!wait_warp(m, &m->full[iv], ((n + PER - 2) / TILES) & 1)) return;
+            if (!wait_warp(m, &m->p, ph)) return;
             tc_fence_after();
             const uint64_t vv = desc_mn(base + iv * TILE, PANEL);
             if (elect_one()) {
@@ -326,11 +322,11 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
     }
 }
 
-// ---- one warp: decay tables. Lane l has token l of each block of 32.
+// ---- one warp: decay tables. Lane l has tokens 4 l .. 4 l + 3, eight lanes a block of 32.
 template <Pass PASS>
 __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
     const Params &a = p.a;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, in = lane & 7, block = lane >> 3;
     uint32_t it = 0;
     bool bad = false;
     const int tasks = tasks_of<PASS>(p);
@@ -340,57 +336,66 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
         if (t.skip) continue;
         float raw[4], sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) raw[b] = gate_raw(a, t.t0, 32 * b + lane, t.len, t.h);
+        for (int j = 0; j < 4; ++j) raw[j] = gate_raw(a, t.t0, 4 * lane + j, t.len, t.h);
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
-            float pre[4], suf[4], tot[4];
+            float pre[4], suf[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                bad |= !(raw[b] <= 0.f);
-                pre[b] = suf[b] = log2_decay(raw[b]);
-                raw[b] = gate_raw(a, t.t0 + c + C, 32 * b + lane, t.len - c - C, t.h);
+            for (int j = 0; j < 4; ++j) {
+                bad |= !(raw[j] <= 0.f);
+                pre[j] = log2_decay(raw[j]);
             }
 #pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {  // inclusive sums from either end of the block
+            for (int j = 0; j < 4; ++j) raw[j] = gate_raw(a, t.t0 + c + C, 4 * lane + j, t.len - c - C, t.h);
+            suf[3] = 0.f;  // after the token, within the lane
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const float x = __shfl_up_sync(0xffffffffu, pre[b], s), y = __shfl_down_sync(0xffffffffu, suf[b], s);
-                    if (lane >= s) pre[b] += x;
-                    if (lane + s < 32) suf[b] += y;
-                }
-            }
+            for (int j = 2; j >= 0; --j) suf[j] = suf[j + 1] + pre[j + 1];
+            const float own = suf[0] + pre[0];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                tot[b] = __shfl_sync(0xffffffffu, suf[b], 0);
-                suf[b] = __shfl_down_sync(0xffffffffu, suf[b], 1);  // after the token
-                if (lane == 31) suf[b] = 0.f;
-            }
-            // the last chunk's tables have been read
-            if (it > 0) {
-                if (PASS != Pass::STATES && !wait_warp(m, &m->p, (it - 1) & 1, a.status)) return;
-                if (!wait_warp(m, &m->wfree, (it - 1) & 1, a.status)) return;
-            }
-            float before = 0.f;
+            for (int j = 1; j < 4; ++j) pre[j] += pre[j - 1];
+            float up = own, down = own;  // sums over the block's lanes up to this one, from this one on
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float after = suf[b];
-#pragma unroll
-                for (int x = b + 1; x < 4; ++x) {
-                    if (PASS != Pass::STATES) m->tab[tab_at(x) + 32 * b + lane] = ex2(after);
-                    after += tot[x];
-                }
-                m->w[32 * b + lane] = ex2(after);
-                if (PASS != Pass::STATES) {
-                    m->pre[32 * b + lane] = pre[b];
-                    m->upto[32 * b + lane] = ex2(pre[b] + before);
-                    before += tot[b];
-                }
+            for (int s = 1; s < 8; s <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, up, s), y = __shfl_down_sync(0xffffffffu, down, s);
+                if (in >= s) up += x;
+                if (in + s < 8) down += y;
             }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+            if (in == 0) before = 0.f;  // the block's lanes before this one
+            if (in == 7) after = 0.f;   // and behind it
+            float tot[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, down, 8 * b);
             const float total = (tot[0] + tot[1]) + (tot[2] + tot[3]);
             sum += total;
-            // (minus one, so that a slow decay is not rounded away chunk after chunk)
-            if (lane == 0) m->dm1[it & 1] = expm1f(total * (1.f / LOG2E));
-            arrive_warp(&m->dec);
+            float to_end = after, from_start = before;  // whole blocks added one by one, the nearer first
+#pragma unroll
+            for (int b = 1; b < 4; ++b) {
+                if (b > block) to_end += tot[b];
+                if (3 - b < block) from_start += tot[3 - b];
+            }
+            const int buf = it & 1;
+            if (it > 1 && !wait_warp(m, &m->wfree[buf], ((it >> 1) - 1) & 1)) return;
+            *reinterpret_cast<float4 *>(&m->w[buf][4 * lane]) =
+                make_float4(ex2(suf[0] + to_end), ex2(suf[1] + to_end), ex2(suf[2] + to_end), ex2(suf[3] + to_end));
+            // (minus one, so that a slow decay is not rounded away chunk after chunk; the state's warps have read the
+            // entry of four chunks ago: the scores of two chunks ago came after their read)
+            if (lane == 0) m->dm1[it & 3] = expm1f(total * (1.f / LOG2E));
+            arrive_warp(&m->decw[buf]);
+            if (PASS == Pass::STATES) continue;
+            if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
+#pragma unroll 1
+            for (int x = block + 1; x < 4; ++x) {
+                *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
+                    make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
+                after += x == 1 ? tot[1] : tot[2];
+            }
+            *reinterpret_cast<float4 *>(&m->pre[4 * lane]) =
+                make_float4(pre[0] + before, pre[1] + before, pre[2] + before, pre[3] + before);
+            *reinterpret_cast<float4 *>(&m->upto[4 * lane]) =
+                make_float4(ex2(pre[0] + from_start), ex2(pre[1] + from_start), ex2(pre[2] + from_start), ex2(pre[3] + from_start));
+            __syncwarp();
+            arrive_warp(&m->dect);
         }
         if (PASS == Pass::STATES && lane == 0) *t.decay = sum;
     }
@@ -401,7 +406,6 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
 template <Pass PASS>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
-    int32_t *status = p.a.status;
     const int tid = threadIdx.x & (GROUP - 1);
     uint32_t it = 0;
     int n = 0;
@@ -414,21 +418,21 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
         for (int c = 0; c < t.len; c += C, n += PER, ++it) {
             const int left = t.len - c, nk = n + PER - 1, nv = n + PER - 2;
             unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
-            if (!wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1, status)) return;
-            if (left < C && !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1, status)) return;
-            if (!wait_warp(m, &m->dec, it & 1, status)) return;
+            if (!wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1)) return;
+            if (left < C && !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1)) return;
+            if (!wait_warp(m, &m->decw[it & 1], (it >> 1) & 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
                 const uint32_t use = 2 * it + (st >> 1);
-                if (use && !wait_warp(m, &m->vfree[st & 1], (use - 1) & 1, status)) return;
+                if (use && !wait_warp(m, &m->vfree[st & 1], (use - 1) & 1)) return;
                 unsigned char *vt = smem + OFF_VT + (st & 1) * VT_STAGE;
-#pragma unroll
+                const int off = tid * 16, row = STAGE_ROWS * st + (off >> 7);  // 32 rows x 8 pieces a panel
+                const float wr = m->w[it & 1][row];
+                const f2 w2 = pair(wr, wr), minus = pair(-1.f, -1.f);
+#pragma unroll 1
                 for (int panel = 0; panel < 2; ++panel) {
-                    const int off = tid * 16;  // 32 rows x 8 pieces a panel
-                    const int row = STAGE_ROWS * st + (off >> 7);
                     const int at = panel * PANEL + st * VT_PANEL + off;
                     uint4 u = *reinterpret_cast<const uint4 *>(tv + at);
-                    const float wr = m->w[row];
                     if (row >= left) {  // behind the segment, someone else's rows: zeros in k, v and v~
                         u = make_uint4(0, 0, 0, 0);
                         *reinterpret_cast<uint4 *>(tv + at) = u;
@@ -438,11 +442,9 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack_bf16(v[j]);
-                        const float y0 = f.x * wr, y1 = f.y * wr;
-                        hi[j] = pack_bf16(y0, y1);
-                        const float2 b = unpack_bf16(hi[j]);
-                        lo[j] = pack_bf16(y0 - b.x, y1 - b.y);
+                        const f2 y = mul2(of_bf16(v[j]), w2);
+                        hi[j] = bf16_of(y);
+                        lo[j] = bf16_of(fma2(of_bf16(hi[j]), minus, y));
                     }
                     *reinterpret_cast<uint4 *>(vt + panel * VT_PANEL + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(vt + VT_TERM + panel * VT_PANEL + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -450,7 +452,7 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 fence_proxy_async_shared();
                 arrive_warp(&m->vt[st & 1]);
             }
-            arrive_warp(&m->wfree);
+            arrive_warp(&m->wfree[it & 1]);
         }
     }
 }
@@ -467,7 +469,7 @@ __device__ __forceinline__ void role_store(const ChunkParams &p, unsigned char *
         if (t.skip) continue;
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, n += 3, ++it) {
-            if (!wait(m, &m->ostage, it & 1, p.a.status)) return;
+            if (!wait(m, &m->ostage, it & 1)) return;
             if (t.len - c >= C) {
                 const unsigned char *src = smem + (n + 1) % TILES * TILE;
                 tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c));
@@ -501,75 +503,73 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
             const uint32_t ph = it & 1;
             const int left = t.len - c;  // tokens from this chunk on
             unsigned char *tile = smem + (n + 1) % TILES * TILE + half * PANEL;  // o goes where v was
-            fail = fail || !wait_warp(m, &m->dec, ph, a.status) || !wait_warp(m, &m->qk, ph, a.status);
+            fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
             float entry = 0.f;
             if (!fail) {
                 tc_fence_after();
                 const float pre = m->pre[tid], row = ex2(pre);
                 entry = a.scale * m->upto[tid];
-                const int b0 = half ? 1 : 0, b1 = half ? 2 : 3;
+                // key blocks of 32, half a block at a time: blocks 0 and 3, or 1 and 2
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {  // key blocks of 32
-                    const int b = i ? b1 : b0;
-                    uint32_t s[32], out[16];
-                    if (b <= warp) {
-                        tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
-                        tmem_wait_ld();
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const int b = (i & 2) ? 3 - half : half, j0 = 16 * (i & 1);
+                    uint32_t s[16], out[8];
                     if (b > warp) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) out[j] = 0;
-                    } else if (b < warp) {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            out[2 * j] = pack_bf16(__uint_as_float(s[4 * j]) * (row * w.x), __uint_as_float(s[4 * j + 1]) * (row * w.y));
-                            out[2 * j + 1] =
-                                pack_bf16(__uint_as_float(s[4 * j + 2]) * (row * w.z), __uint_as_float(s[4 * j + 3]) * (row * w.w));
-                        }
+                        for (int j = 0; j < 8; ++j) out[j] = 0;
                     } else {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
+                        tmem_ld16(tmem + lanes + COL_QK + 32 * b + j0, s);
+                        const float4 *f = reinterpret_cast<const float4 *>((b < warp ? &m->tab[tab_at(warp)] : m->pre) + 32 * b + j0);
+                        float4 w[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            // (selected, not multiplied by zero: a score behind the row may be anything)
-                            const float s0 = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
-                            const float s1 = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
-                            const float s2 = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
-                            const float s3 = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
-                            out[2 * j] = pack_bf16(s0, s1);
-                            out[2 * j + 1] = pack_bf16(s2, s3);
+                        for (int j = 0; j < 4; ++j) {
+                            w[j] = f[j];
+                            if (b < warp) {
+                                w[j].x *= row, w[j].y *= row, w[j].z *= row, w[j].w *= row;
+                            } else {
+                                w[j].x = ex2(pre - w[j].x), w[j].y = ex2(pre - w[j].y);
+                                w[j].z = ex2(pre - w[j].z), w[j].w = ex2(pre - w[j].w);
+                            }
+                        }
+                        tmem_wait_ld();
+                        const int upto = b < warp ? 16 : lane - j0;  // the last key this row may see
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            // (selected, not multiplied by zero: a score behind the row, and its weight, may be anything)
+                            const float x = 4 * j <= upto ? __uint_as_float(s[4 * j]) * w[j].x : 0.f;
+                            const float y = 4 * j + 1 <= upto ? __uint_as_float(s[4 * j + 1]) * w[j].y : 0.f;
+                            const float z = 4 * j + 2 <= upto ? __uint_as_float(s[4 * j + 2]) * w[j].z : 0.f;
+                            const float q = 4 * j + 3 <= upto ? __uint_as_float(s[4 * j + 3]) * w[j].w : 0.f;
+                            out[2 * j] = pack_bf16(x, y);
+                            out[2 * j + 1] = pack_bf16(z, q);
                         }
                     }
-                    tmem_st16(tmem + lanes + COL_QK + 32 * b, out);  // over the scores it comes from
+                    tmem_st8(tmem + lanes + COL_QK + 32 * b + (j0 >> 1), out);  // over the scores they come from
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&m->p);
             }
-            fail = fail || !wait_warp(m, &m->o, ph, a.status);
+            fail = fail || !wait_warp(m, &m->o, ph);
             if (!fail) {
                 tc_fence_after();
-#pragma unroll
+                const f2 e2 = pair(entry, entry), s2 = pair(a.scale, a.scale);
+#pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     uint32_t o1[16], o2[16], w[8];
                     tmem_ld16(tmem + lanes + COL_O1 + 64 * half + 16 * b, o1);
                     tmem_ld16(tmem + lanes + COL_O2 + 64 * half + 16 * b, o2);
                     tmem_wait_ld();
-                    if (b == 3) {
-                        tc_fence_before();
-                        arrive_warp(&m->ofree);
-                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        w[j] = pack_bf16(fmaf(entry, __uint_as_float(o1[2 * j]), a.scale * __uint_as_float(o2[2 * j])),
-                                         fmaf(entry, __uint_as_float(o1[2 * j + 1]), a.scale * __uint_as_float(o2[2 * j + 1])));
+                        w[j] = bf16_of(fma2(e2, pair(o1[2 * j], o1[2 * j + 1]), mul2(s2, pair(o2[2 * j], o2[2 * j + 1]))));
 #pragma unroll
                     for (int j = 0; j < 2; ++j)  // the tile's swizzle: 16-byte piece ^ row % 8
                         *reinterpret_cast<uint4 *>(tile + tid * 128 + (((2 * b + j) ^ (tid & 7)) << 4)) =
                             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                 }
+                tc_fence_before();
+                arrive_warp(&m->ofree);
             }
             if (left < C) {  // rows behind the segment are not written
                 if (named_bar_or(1, GROUP, fail)) return;
@@ -596,12 +596,11 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
-    float S[NV];
+    f2 S[NV / 2];
     auto publish = [&]() {  // the bf16 copy that q multiplies
 #pragma unroll
         for (int j = 0; j < NV / 8; ++j) {
-            const uint4 u = make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
-                                       pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
+            const uint4 u = make_uint4(bf16_of(S[4 * j]), bf16_of(S[4 * j + 1]), bf16_of(S[4 * j + 2]), bf16_of(S[4 * j + 3]));
             *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) = u;
         }
         fence_proxy_async_shared();
@@ -618,34 +617,43 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
         const size_t at = static_cast<size_t>(tid) * DV + half * NV;
         if (t.sin) {
 #pragma unroll
-            for (int j = 0; j < NV; j += 8) ld_f8(S + j, t.sin + at + j);
+            for (int j = 0; j < NV; j += 8) {
+                float x[8];
+                ld_f8(x, t.sin + at + j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[j / 2 + i] = pair(x[2 * i], x[2 * i + 1]);
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) S[j] = 0.f;
+            for (int j = 0; j < NV / 2; ++j) S[j] = 0;
         }
         if (PASS != Pass::STATES && t.len > 0) publish();
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
-            if (!wait_warp(m, &m->u, it & 1, a.status)) return;
+            if (!wait_warp(m, &m->u, it & 1)) return;
             tc_fence_after();
-            const float dm1 = m->dm1[it & 1];
+            const float dm1 = m->dm1[it & 3];
+            const f2 d2 = pair(dm1, dm1);
 #pragma unroll
             for (int b = 0; b < NV / 32; ++b) {
                 uint32_t u[32];
                 tmem_ld32(tmem + lanes + COL_U + NV * half + 32 * b, u);
                 tmem_wait_ld();
-                if (b == NV / 32 - 1) {
-                    tc_fence_before();
-                    arrive_warp(&m->ufree);
-                }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[32 * b + j] = fmaf(S[32 * b + j], dm1, S[32 * b + j]) + __uint_as_float(u[j]);
+                for (int j = 0; j < 16; ++j) S[16 * b + j] = add2(fma2(S[16 * b + j], d2, S[16 * b + j]), pair(u[2 * j], u[2 * j + 1]));
             }
+            tc_fence_before();
+            arrive_warp(&m->ufree);
             if (PASS != Pass::STATES && c + C < t.len) publish();  // (u came after q S: the old copy has been read)
         }
         if (t.sout) {
 #pragma unroll
-            for (int j = 0; j < NV; j += 8) st_f8(t.sout + at + j, S + j);
+            for (int j = 0; j < NV; j += 8) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split(S[j / 2 + i], x[2 * i], x[2 * i + 1]);
+                st_f8(t.sout + at + j, x);
+            }
         }
     }
 }
@@ -666,9 +674,10 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
         for (int i = 0; i < 2; ++i) {
             mbar_init(&m->vfree[i], 1);
             mbar_init(&m->vt[i], GROUP / 32);
+            mbar_init(&m->decw[i], 1);
+            mbar_init(&m->wfree[i], GROUP / 32);
         }
-        mbar_init(&m->dec, 1);
-        mbar_init(&m->wfree, GROUP / 32);
+        mbar_init(&m->dect, 1);
         mbar_init(&m->s, GROUP / 32);
         mbar_init(&m->p, GROUP / 32);
         mbar_init(&m->ufree, GROUP / 32);
@@ -705,6 +714,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && m->abort) set_status(p.a.status, KDA_ERR_TIMEOUT);
     if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
 }
 
