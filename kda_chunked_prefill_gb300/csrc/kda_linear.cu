@@ -9,13 +9,13 @@
 //     S   = e^{G_end} S + U                       warpgroup 1, fp32 registers
 //
 // One CTA per SM walks (segment, head) tasks: a segment is a sequence or a part
-// of one. Six roles run side by side, each a chunk or two ahead of the next:
+// of one. Roles run side by side, each a chunk or two ahead of the next:
 //   load    one thread: q, k and v tiles by TMA into a ring of five 32 KB tiles
 //   decays  one warp: the chunk's decay tables from g
 //   v~      8 warps: v~ in stages of 32 tokens
 //   scores  8 warps: P, then o_i into the chunk's v tile
 //   state   8 warps: S
-//   MMA, store   one thread each
+//   MMAs    one warp for q k^T, q S and P v, one for U
 //
 // Why this split. U does not depend on S, so the recurrence from chunk to chunk
 // is one fused multiply-add per state element and its rounding to bf16 for the
@@ -67,19 +67,21 @@ struct ChunkParams {
 };
 
 struct Misc {
-    uint64_t full[TILES], empty[TILES];
-    uint64_t qk, u, o, vfree[2];  // tensor core -> warps (commits)
+    uint64_t full[6];             // a tile has come, by its kind and its chunk's number
+    uint64_t empty[TILES];        // a slot is free
+    uint64_t qk, qs, u, o, vfree[2];  // tensor core -> warps (commits)
     uint64_t decw[2], dect;       // decay tables written: w and dm1; tab, pre and upto
     uint64_t vt[2], s, p;         // v~ stage, bf16 state, scores written
     uint64_t wfree[2];            // w read
-    uint64_t ufree, ofree, ostage;  // U read; O1 and O2 read; o in the v tile
+    uint64_t go;                  // the first g have been read
+    uint64_t ufree, ofree;        // U read; O1 and O2 read
+    uint32_t tmem;                // address of the tensor memory
+    int32_t abort;                // a wait ran out
     alignas(16) float tab[192];   // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
     alignas(16) float pre[C];     // log2 prefix of j within its block of 32
     alignas(16) float upto[C];    // 2^(sum of g up to j)
     alignas(16) float w[2][C];    // 2^(sum of g after j up to the chunk's end), a chunk ahead
     float dm1[4];                 // 2^(the chunk's sum) - 1, of the last four chunks
-    uint32_t tmem;
-    int32_t abort;
 };
 __host__ __device__ constexpr int tab_at(int anchor) { return anchor == 1 ? 0 : anchor == 2 ? 32 : 96; }
 static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && offsetof(Misc, upto) % 16 == 0 && offsetof(Misc, w) % 16 == 0 && OFF_MISC % 16 == 0, "read as float4");
@@ -89,7 +91,8 @@ static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 constexpr uint32_t COL_QK = 0, COL_O1 = 128, COL_O2 = 256, COL_U = 384;  // tensor memory columns (P over A)
 // warps: 0-7 scores, 8-15 state, 16-23 v~, then one each
 constexpr int GROUP = 256;
-constexpr int WARP_LOAD = 24, WARP_MMA = 25, WARP_DECAY = 26, WARP_STORE = 27, THREADS = 896;
+constexpr int WARP_LOAD = 24, WARP_DECAY = 25, WARP_MMA_OUT = 26, WARP_MMA_U = 27, THREADS = 896;
+constexpr int WARP_STORE = 4;  // of the scores' warps, the one with only masked scores
 // Registers: 28 warps launch with 72; the roles' shares add up to no more.
 constexpr int REGS = 72, REGS_SCORES = 72, REGS_STATE = 104, REGS_V = 48, REGS_AUX = 56;
 static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 8 * REGS_V + 4 * REGS_AUX <= 28 * REGS, "the launch's registers");
@@ -158,6 +161,19 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
     return t;
 }
 
+constexpr int TQ = 0, TV = 1, TK = 2;
+// (Barriers by kind of tile and not by slot: who waits for one kind only then
+// waits for each phase of its barriers in turn. Five slots hold tiles of three
+// chunks where a chunk has two, of two otherwise.)
+template <Pass PASS>
+__device__ __forceinline__ uint64_t *full_of(Misc *m, int kind, uint32_t it) {
+    return PASS == Pass::STATES ? &m->full[3 * (kind - TV) + it % 3] : &m->full[2 * kind + it % 2];
+}
+template <Pass PASS>
+__device__ __forceinline__ uint32_t full_phase(uint32_t it) {
+    return (PASS == Pass::STATES ? it / 3 : it / 2) & 1;
+}
+
 // A bounded wait for a barrier's phase. (A parity wait takes the phase before
 // last for the next: every role that waits on a barrier waits for each of its
 // phases in turn, or has seen the one before complete through another wait.)
@@ -202,7 +218,8 @@ __device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 204
 template <Pass PASS>
 __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m) {
     constexpr int PER = PASS == Pass::STATES ? 2 : 3;
-    int n = 0, part = 0;  // tiles of whole chunks issued, and which of a chunk that was given up
+    int n = 0, part = 0;  // tiles of whole chunks issued, and which kinds of a chunk that was given up
+    uint32_t it = 0;
     bool ok = true;
     const int tasks = tasks_of<PASS>(p);
 #pragma unroll 1
@@ -214,24 +231,29 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
         for (int c = 0; ok && c < t.len; c += C) {
             const int row = static_cast<int>(t.t0 + c);
             part = 0;
+            // the first decay table waits for a few bytes of g: they go ahead of all SMs' first tiles
+            if (n == 0 && !wait(m, &m->go, 0)) {
+                ok = false;
+                break;
+            }
 #pragma unroll 1
             for (int i = 0; i < PER; ++i) {
-                const int at = PER == 2 ? i : i == 0 ? 1 : i == 1 ? 0 : 2;  // tile of the chunk: (q,) v, k
-                const int slot = (n + at) % TILES;
+                const int kind = PER == 2 ? i + 1 : i == 0 ? TV : i == 1 ? TQ : TK;
+                const int at = kind - (3 - PER), slot = (n + at) % TILES;
                 if (n + at >= TILES && !wait(m, &m->empty[slot], ((n + at) / TILES - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 unsigned char *dst = smem + slot * TILE;
-                const bool is_v = at == PER - 2;
-                const CUtensorMap *map = is_v ? &p.tv : at == PER - 1 ? &p.tk : &p.tq;
-                const int head = is_v ? t.h : hk;
-                mbar_arrive_expect_tx(&m->full[slot], TILE);
-                tma_load_3d(dst, map, 0, head, row, &m->full[slot]);
-                tma_load_3d(dst + PANEL, map, 64, head, row, &m->full[slot]);
-                part |= 1 << at;
+                const CUtensorMap *map = kind == TV ? &p.tv : kind == TK ? &p.tk : &p.tq;
+                const int head = kind == TV ? t.h : hk;
+                uint64_t *full = full_of<PASS>(m, kind, it);
+                mbar_arrive_expect_tx(full, TILE);
+                tma_load_3d(dst, map, 0, head, row, full);
+                tma_load_3d(dst + PANEL, map, 64, head, row, full);
+                part |= 1 << kind;
             }
-            if (ok) n += PER;
+            if (ok) n += PER, ++it;
         }
     }
     // no copy and no commit of this CTA is in flight when it ends
@@ -240,17 +262,71 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
         ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1);
     if (ok) return;
 #pragma unroll 1
-    for (int k = n > TILES ? n - TILES : 0; k < n + PER; ++k)
-        if (k < n || (part >> (k - n) & 1)) (void)mbar_wait_some(&m->full[k % TILES], (k / TILES) & 1);
+    for (int kind = 0; kind < 3; ++kind) {
+        if (it > 0 && kind >= 3 - PER) (void)mbar_wait_some(full_of<PASS>(m, kind, it - 1), full_phase<PASS>(it - 1));
+        if (part >> kind & 1) (void)mbar_wait_some(full_of<PASS>(m, kind, it), full_phase<PASS>(it));
+    }
 }
 
-// ---- one warp: MMAs. The whole warp walks the tasks, with everything that makes an address the same in all lanes, and one
-// lane issues: from a single-lane loop each MMA took 140-190 cycles to issue, more than the 70 it runs.
+// ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, with
+// everything that makes an address the same in all lanes, and one lane issues. (A 128 x 128 x 16 MMA runs 70 cycles; from one
+// warp the waits and descriptors between groups of four or eight cost as much again.)
 template <Pass PASS>
-__device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
-    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+__device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr uint32_t ID_QK = idesc_bf16(false, false, C, C), ID_QS = idesc_bf16(false, true, C, DV),
-                       ID_U = idesc_bf16(true, true, DK, DV), ID_PV = idesc_bf16(false, true, C, DV);
+                       ID_PV = idesc_bf16(false, true, C, DV);
+    int n = 0;
+    uint32_t it = 0;
+    const uint32_t base = smem_u32(smem);
+    const int tasks = __shfl_sync(0xffffffffu, tasks_of<PASS>(p), 0);
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
+#pragma unroll 1
+    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+        const Task t = task_of<PASS>(p, id);
+        const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
+#pragma unroll 1
+        for (int c = 0; c < len; c += C, n += 3, ++it) {
+            const uint32_t ph = it & 1;
+            const int iq = n % TILES, iv = (n + 1) % TILES, ik = (n + 2) % TILES;
+            const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
+            if (!wait_warp(m, full_of<PASS>(m, TQ, it), full_phase<PASS>(it))) return;
+            if (!wait_warp(m, full_of<PASS>(m, TK, it), full_phase<PASS>(it))) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
+                umma_commit(&m->qk);
+                umma_commit(&m->empty[ik]);
+            }
+            const uint64_t s = desc_mn(base + OFF_S, PANEL);
+            if (!wait_warp(m, &m->s, ph)) return;
+            if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
+                umma_commit(&m->qs);
+                umma_commit(&m->empty[iq]);  // (twice: a k tile has two readers, and any slot may hold one)
+                umma_commit(&m->empty[iq]);
+            }
+            // P v comes after U: by then zeros behind a segment's end are in v, and v~ has been made of it (o goes into its tile)
+            const uint64_t v = desc_mn(base + iv * TILE, PANEL);
+            if (!wait_warp(m, &m->u, ph)) return;
+            if (!wait_warp(m, &m->p, ph)) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    umma_ts(tmem + COL_O2, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), ID_PV, kk > 0);
+                umma_commit(&m->o);
+            }
+        }
+    }
+}
+template <Pass PASS>
+__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+    constexpr uint32_t ID_U = idesc_bf16(true, true, DK, DV);
     int n = 0;
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
@@ -263,35 +339,18 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
 #pragma unroll 1
         for (int c = 0; c < len; c += C, n += PER, ++it) {
             const uint32_t ph = it & 1;
-            const int iq = n % TILES, iv = (n + PER - 2) % TILES, ik = (n + PER - 1) % TILES;
-            if (!wait_warp(m, &m->full[ik], ((n + PER - 1) / TILES) & 1)) return;
-            if (PASS != Pass::STATES) {
-                if (!wait_warp(m, &m->full[iq], (n / TILES) & 1)) return;
-                tc_fence_after();
-                const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
-                    umma_commit(&m->qk);
-                }
-                if (!wait_warp(m, &m->s, ph)) return;
-                if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
-                tc_fence_after();
-                const uint64_t s = desc_mn(base + OFF_S, PANEL);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
-                    umma_commit(&m->empty[iq]);
-                }
-            }
-            if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
+            const int iv = (n + PER - 2) % TILES, ik = (n + PER - 1) % TILES;
             const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+            if (!wait_warp(m, full_of<PASS>(m, TK, it), full_phase<PASS>(it))) return;
+            if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
-                if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1)) return;
-                tc_fence_after();
                 const uint64_t k = kt + st * step_mn(STAGE_ROWS / 16);
                 const uint64_t v = desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL);
+                if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1)) return;
+                // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
+                if (PASS != Pass::STATES && st == STAGES - 1 && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+                tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
@@ -305,18 +364,6 @@ __device__ __forceinline__ void role_mma(const ChunkParams &p, unsigned char *sm
                         if (PASS == Pass::STATES) umma_commit(&m->empty[iv]);
                     }
                 }
-            }
-            if (PASS == Pass::STATES) continue;
-            // P v comes last: zeros behind a segment's end are in v by now, and v~ has been made of it (o goes into its tile)
-            if (!wait_warp(m, &m->full[iv], ((n + PER - 2) / TILES) & 1)) return;
-            if (!wait_warp(m, &m->p, ph)) return;
-            tc_fence_after();
-            const uint64_t vv = desc_mn(base + iv * TILE, PANEL);
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    umma_ts(tmem + COL_O2, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), vv + step_mn(kk), ID_PV, kk > 0);
-                umma_commit(&m->o);
             }
         }
     }
@@ -344,6 +391,10 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
             for (int j = 0; j < 4; ++j) {
                 bad |= !(raw[j] <= 0.f);
                 pre[j] = log2_decay(raw[j]);
+            }
+            if (it == 0) {
+                bad = __any_sync(0xffffffffu, bad);  // (they have come)
+                arrive_warp(&m->go);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) raw[j] = gate_raw(a, t.t0 + c + C, 4 * lane + j, t.len - c - C, t.h);
@@ -418,8 +469,8 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
         for (int c = 0; c < t.len; c += C, n += PER, ++it) {
             const int left = t.len - c, nk = n + PER - 1, nv = n + PER - 2;
             unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
-            if (!wait_warp(m, &m->full[nv % TILES], (nv / TILES) & 1)) return;
-            if (left < C && !wait_warp(m, &m->full[nk % TILES], (nk / TILES) & 1)) return;
+            if (!wait_warp(m, full_of<PASS>(m, TV, it), full_phase<PASS>(it))) return;
+            if (left < C && !wait_warp(m, full_of<PASS>(m, TK, it), full_phase<PASS>(it))) return;
             if (!wait_warp(m, &m->decw[it & 1], (it >> 1) & 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
@@ -455,32 +506,6 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
             arrive_warp(&m->wfree[it & 1]);
         }
     }
-}
-
-// ---- one thread: o from the chunk's v tile to memory, then the tile is free
-template <Pass PASS>
-__device__ __forceinline__ void role_store(const ChunkParams &p, unsigned char *smem, Misc *m) {
-    int n = 0;
-    uint32_t it = 0;
-    const int tasks = tasks_of<PASS>(p);
-#pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
-        if (t.skip) continue;
-#pragma unroll 1
-        for (int c = 0; c < t.len; c += C, n += 3, ++it) {
-            if (!wait(m, &m->ostage, it & 1)) return;
-            if (t.len - c >= C) {
-                const unsigned char *src = smem + (n + 1) % TILES * TILE;
-                tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c));
-                tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c));
-                bulk_commit();
-                bulk_wait_read();
-            }
-            mbar_arrive(&m->empty[(n + 1) % TILES]);
-        }
-    }
-    bulk_wait_all();
 }
 
 // ---- warps 0-7: decayed scores and the output. Two threads share a token row: key blocks 0 and 3 or 1 and 2 of the scores, one
@@ -582,9 +607,29 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
             } else {
                 fence_proxy_async_shared();
             }
-            arrive_warp(&m->ostage);
+            // one warp stores a whole chunk's o and frees the tile; the others go on (none of them comes here again before
+            // that warp's scores of the next chunk)
+            if (threadIdx.x >> 5 != WARP_STORE) {
+                named_bar_arrive(2, GROUP);
+            } else {
+                named_bar_sync(2, GROUP);
+                if (lane == 0) {
+                    const int slot = (n + 1) % TILES;
+                    if (left >= C && !fail) {
+                        const unsigned char *src = smem + slot * TILE;
+                        tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c));
+                        tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c));
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                    mbar_arrive(&m->empty[slot]);
+                    mbar_arrive(&m->empty[slot]);
+                }
+                __syncwarp();
+            }
         }
     }
+    if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
 }
 
 // ---- warps 8-15: the state. Two threads share a key row of S, one half of its values each.
@@ -644,7 +689,10 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             }
             tc_fence_before();
             arrive_warp(&m->ufree);
-            if (PASS != Pass::STATES && c + C < t.len) publish();  // (u came after q S: the old copy has been read)
+            if (PASS != Pass::STATES) {
+                if (!wait_warp(m, &m->qs, it & 1)) return;  // the old copy has been read
+                if (c + C < t.len) publish();
+            }
         }
         if (t.sout) {
 #pragma unroll
@@ -664,11 +712,10 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < TILES; ++i) {
-            mbar_init(&m->full[i], 1);
-            mbar_init(&m->empty[i], 1);
-        }
+        for (int i = 0; i < 6; ++i) mbar_init(&m->full[i], 1);
+        for (int i = 0; i < TILES; ++i) mbar_init(&m->empty[i], PASS == Pass::STATES ? 1 : 2);
         mbar_init(&m->qk, 1);
+        mbar_init(&m->qs, 1);
         mbar_init(&m->u, 1);
         mbar_init(&m->o, 1);
         for (int i = 0; i < 2; ++i) {
@@ -678,15 +725,15 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
             mbar_init(&m->wfree[i], GROUP / 32);
         }
         mbar_init(&m->dect, 1);
+        mbar_init(&m->go, 1);
         mbar_init(&m->s, GROUP / 32);
         mbar_init(&m->p, GROUP / 32);
         mbar_init(&m->ufree, GROUP / 32);
         mbar_init(&m->ofree, GROUP / 32);
-        mbar_init(&m->ostage, GROUP / 32);
         m->abort = 0;
         mbar_fence_init();
     }
-    if (warp == WARP_MMA) tmem_alloc(&m->tmem, 512);
+    if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -703,19 +750,19 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
         fewer_registers<REGS_AUX>();
         if (warp == WARP_LOAD) {
             if (lane == 0) role_load<PASS>(p, smem, m);
-        } else if (warp == WARP_MMA) {
-            role_mma<PASS>(p, smem, m, tmem);
         } else if (warp == WARP_DECAY) {
             role_decay<PASS>(p, m);
+        } else if (warp == WARP_MMA_U) {
+            role_mma_state<PASS>(p, smem, m, tmem);
         } else if (PASS != Pass::STATES) {
-            if (lane == 0) role_store<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m);
+            role_mma_out<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m, tmem);
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && m->abort) set_status(p.a.status, KDA_ERR_TIMEOUT);
-    if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
+    if (warp == WARP_MMA_U) tmem_dealloc(tmem, 512);
 }
 
 // ---- segments: one CTA. Sequence n of c chunks gets ceil(c / L) segments of about equal length.
