@@ -534,42 +534,41 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                 tc_fence_after();
                 const float pre = m->pre[tid], row = ex2(pre);
                 entry = a.scale * m->upto[tid];
-                // key blocks of 32, half a block at a time: blocks 0 and 3, or 1 and 2
+                // key blocks of 32: 0 and 3, or 1 and 2
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int b = (i & 2) ? 3 - half : half, j0 = 16 * (i & 1);
-                    uint32_t s[16], out[8];
+                for (int i = 0; i < 2; ++i) {
+                    const int b = i ? 3 - half : half;
+                    uint32_t s[32];
+                    if (b <= warp) tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
                     if (b > warp) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) out[j] = 0;
-                    } else {
-                        tmem_ld16(tmem + lanes + COL_QK + 32 * b + j0, s);
-                        const float4 *f = reinterpret_cast<const float4 *>((b < warp ? &m->tab[tab_at(warp)] : m->pre) + 32 * b + j0);
-                        float4 w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            w[j] = f[j];
-                            if (b < warp) {
-                                w[j].x *= row, w[j].y *= row, w[j].z *= row, w[j].w *= row;
-                            } else {
-                                w[j].x = ex2(pre - w[j].x), w[j].y = ex2(pre - w[j].y);
-                                w[j].z = ex2(pre - w[j].z), w[j].w = ex2(pre - w[j].w);
-                            }
-                        }
+                        for (int j = 0; j < 16; ++j) s[j] = 0;
+                    } else if (b < warp) {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
+                        const f2 r2 = pair(row, row);
                         tmem_wait_ld();
-                        const int upto = b < warp ? 16 : lane - j0;  // the last key this row may see
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
+                            s[2 * j] = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), mul2(r2, pair(w.x, w.y))));
+                            s[2 * j + 1] = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), mul2(r2, pair(w.z, w.w))));
+                        }
+                    } else {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
                             // (selected, not multiplied by zero: a score behind the row, and its weight, may be anything)
-                            const float x = 4 * j <= upto ? __uint_as_float(s[4 * j]) * w[j].x : 0.f;
-                            const float y = 4 * j + 1 <= upto ? __uint_as_float(s[4 * j + 1]) * w[j].y : 0.f;
-                            const float z = 4 * j + 2 <= upto ? __uint_as_float(s[4 * j + 2]) * w[j].z : 0.f;
-                            const float q = 4 * j + 3 <= upto ? __uint_as_float(s[4 * j + 3]) * w[j].w : 0.f;
-                            out[2 * j] = pack_bf16(x, y);
-                            out[2 * j + 1] = pack_bf16(z, q);
+                            const float x = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
+                            const float y = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
+                            const float z = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
+                            const float q = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
+                            s[2 * j] = pack_bf16(x, y);
+                            s[2 * j + 1] = pack_bf16(z, q);
                         }
                     }
-                    tmem_st8(tmem + lanes + COL_QK + 32 * b + (j0 >> 1), out);  // over the scores they come from
+                    tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -581,17 +580,17 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                 const f2 e2 = pair(entry, entry), s2 = pair(a.scale, a.scale);
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
-                    uint32_t o1[16], o2[16], w[8];
+                    uint32_t o1[16], o2[16];
                     tmem_ld16(tmem + lanes + COL_O1 + 64 * half + 16 * b, o1);
                     tmem_ld16(tmem + lanes + COL_O2 + 64 * half + 16 * b, o2);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        w[j] = bf16_of(fma2(e2, pair(o1[2 * j], o1[2 * j + 1]), mul2(s2, pair(o2[2 * j], o2[2 * j + 1]))));
+                        o1[j] = bf16_of(fma2(e2, pair(o1[2 * j], o1[2 * j + 1]), mul2(s2, pair(o2[2 * j], o2[2 * j + 1]))));
 #pragma unroll
                     for (int j = 0; j < 2; ++j)  // the tile's swizzle: 16-byte piece ^ row % 8
                         *reinterpret_cast<uint4 *>(tile + tid * 128 + (((2 * b + j) ^ (tid & 7)) << 4)) =
-                            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                            make_uint4(o1[4 * j], o1[4 * j + 1], o1[4 * j + 2], o1[4 * j + 3]);
                 }
                 tc_fence_before();
                 arrive_warp(&m->ofree);
