@@ -59,7 +59,7 @@ struct ChunkParams {
     // the rest only with segments (device memory in the workspace)
     int32_t seg_chunks;
     int32_t most_segs;  // that the workspace holds
-    int32_t *num_segs;
+    int32_t *num_segs;  // and, behind it, the count of the launch's barrier
     int2 *first;     // [N] first segment and number of segments
     Segment *segs;
     float *decays;   // [segment][head]
@@ -104,6 +104,7 @@ template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+constexpr int GRID_POLLS = 1 << 24;
 constexpr int WAITS = 20000;  // waits of up to WAIT_NS each before a role gives up
 
 struct Task {
@@ -705,32 +706,127 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
     }
 }
 
+// ---- segments: between the two passes of one launch
+// all threads of the CTA (from whichever role)
+__device__ __forceinline__ void cta_sync() { named_bar_sync(0, THREADS); }
+// all CTAs of the launch (one thread of each; all are resident); false: a wait ran out
+__device__ __forceinline__ bool grid_sync(int32_t *count, int32_t target) {
+    __threadfence();
+    atomicAdd(count, 1);
+#pragma unroll 1
+    for (int i = 0; i < GRID_POLLS; ++i) {
+        if (ld_acquire(count) >= target) {
+            __threadfence();
+            return true;
+        }
+        __nanosleep(64);
+    }
+    return false;
+}
+
+// Entry states: E_{s+1} = 2^{decay_s} E_s + N_s along a sequence, in place over the segments' states N_s. Each of the launch's
+// 256 x CTAs threads takes W values at a time through all segments of a chain, with BATCH loads in flight.
+template <int W>
+__device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
+    constexpr int BATCH = W == 1 ? 16 : 4;
+    constexpr int UNITS = DK * DV / W;
+    const int H = p.a.H;
+    const int64_t all = static_cast<int64_t>(p.a.N) * H * UNITS, stride = static_cast<int64_t>(gridDim.x) * GROUP;
+    const size_t step = static_cast<size_t>(H) * DK * DV;
+#pragma unroll 1
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * GROUP + gtid; u < all; u += stride) {
+        const int chain = static_cast<int>(u / UNITS), n = chain / H, h = chain % H;
+        const int2 f = p.first[n];
+        if (f.y < 3) continue;  // the first segment's state is whole already, and the last one's is not needed
+        float *s = p.states + (static_cast<size_t>(f.x) * H + h) * (DK * DV) + (u % UNITS) * W;
+        const float *d = p.decays + static_cast<int64_t>(f.x) * H + h;
+        float e[W];
+#pragma unroll
+        for (int w = 0; w < W; ++w) e[w] = __ldcg(s + w);
+#pragma unroll 1
+        for (int i = 1; i < f.y - 1; i += BATCH) {
+            float x[BATCH][W], dd[BATCH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                if (i + j >= f.y - 1) continue;
+                dd[j] = __ldcg(d + (i + j) * H);
+#pragma unroll
+                for (int w = 0; w < W; ++w) x[j][w] = __ldcg(s + (i + j) * step + w);
+            }
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+                if (i + j >= f.y - 1) continue;
+                const float m1 = expm1f(dd[j] * (1.f / LOG2E));
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    e[w] = fmaf(e[w], m1, e[w]) + x[j][w];
+                    s[(i + j) * step + w] = e[w];
+                }
+            }
+        }
+    }
+}
+
 template <Pass PASS>
+__device__ __forceinline__ void init_barriers(Misc *m) {  // one thread
+    for (int i = 0; i < 6; ++i) mbar_init(&m->full[i], 1);
+    for (int i = 0; i < TILES; ++i) mbar_init(&m->empty[i], PASS == Pass::STATES ? 1 : 2);
+    mbar_init(&m->qk, 1);
+    mbar_init(&m->qs, 1);
+    mbar_init(&m->u, 1);
+    mbar_init(&m->o, 1);
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&m->vfree[i], 1);
+        mbar_init(&m->vt[i], GROUP / 32);
+        mbar_init(&m->decw[i], 1);
+        mbar_init(&m->wfree[i], GROUP / 32);
+    }
+    mbar_init(&m->dect, 1);
+    mbar_init(&m->go, 1);
+    mbar_init(&m->s, GROUP / 32);
+    mbar_init(&m->p, GROUP / 32);
+    mbar_init(&m->ufree, GROUP / 32);
+    mbar_init(&m->ofree, GROUP / 32);
+    mbar_fence_init();
+}
+
+__device__ __forceinline__ void end_barriers(Misc *m) {
+    constexpr int N = offsetof(Misc, tmem) / sizeof(uint64_t);  // the barriers come first in Misc
+    for (int i = 0; i < N; ++i) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);
+}
+
+// from the pass over the states to the pass over the outputs; false: the launch has given up
+template <bool JOINS>
+__device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
+    cta_sync();
+    if (threadIdx.x == 0 && !grid_sync(p.num_segs + 1, gridDim.x)) m->abort = 1;
+    cta_sync();
+    if (JOINS) {
+        if (p.a.N * p.a.H >= 32)
+            join_states<4>(p, threadIdx.x - GROUP);
+        else
+            join_states<1>(p, threadIdx.x - GROUP);
+    }
+    cta_sync();
+    if (threadIdx.x == 0) {
+        if (!grid_sync(p.num_segs + 1, 2 * gridDim.x)) m->abort = 1;
+        end_barriers(m);  // (every arrival of the first pass has come)
+        init_barriers<Pass::OUTPUT>(m);
+    }
+    cta_sync();
+    return *reinterpret_cast<volatile int32_t *>(&m->abort) == 0;
+}
+
+// SEGMENTS: sequences in segments, states first (a cooperative launch); else every sequence as a whole
+template <bool SEGMENTS>
 __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr Pass OUT = SEGMENTS ? Pass::OUTPUT : Pass::WHOLE;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 6; ++i) mbar_init(&m->full[i], 1);
-        for (int i = 0; i < TILES; ++i) mbar_init(&m->empty[i], PASS == Pass::STATES ? 1 : 2);
-        mbar_init(&m->qk, 1);
-        mbar_init(&m->qs, 1);
-        mbar_init(&m->u, 1);
-        mbar_init(&m->o, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&m->vfree[i], 1);
-            mbar_init(&m->vt[i], GROUP / 32);
-            mbar_init(&m->decw[i], 1);
-            mbar_init(&m->wfree[i], GROUP / 32);
-        }
-        mbar_init(&m->dect, 1);
-        mbar_init(&m->go, 1);
-        mbar_init(&m->s, GROUP / 32);
-        mbar_init(&m->p, GROUP / 32);
-        mbar_init(&m->ufree, GROUP / 32);
-        mbar_init(&m->ofree, GROUP / 32);
+        init_barriers<SEGMENTS ? Pass::STATES : Pass::WHOLE>(m);
         m->abort = 0;
-        mbar_fence_init();
     }
     if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
@@ -738,23 +834,29 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = m->tmem;
     if (warp < 8) {
-        if (PASS != Pass::STATES) role_scores<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m, tmem);
+        if (!SEGMENTS || next_pass<false>(p, m)) role_scores<OUT>(p, smem, m, tmem);
     } else if (warp < 16) {
         more_registers<REGS_STATE>();
-        role_state<PASS>(p, smem, m, tmem);
+        if (SEGMENTS) role_state<Pass::STATES>(p, smem, m, tmem);
+        if (!SEGMENTS || next_pass<true>(p, m)) role_state<OUT>(p, smem, m, tmem);
     } else if (warp < 24) {
         fewer_registers<REGS_V>();
-        role_v<PASS>(p, smem, m);
+        if (SEGMENTS) role_v<Pass::STATES>(p, smem, m);
+        if (!SEGMENTS || next_pass<false>(p, m)) role_v<OUT>(p, smem, m);
     } else {
         fewer_registers<REGS_AUX>();
         if (warp == WARP_LOAD) {
-            if (lane == 0) role_load<PASS>(p, smem, m);
+            if (SEGMENTS && lane == 0) role_load<Pass::STATES>(p, smem, m);
+            __syncwarp();
+            if ((!SEGMENTS || next_pass<false>(p, m)) && lane == 0) role_load<OUT>(p, smem, m);
         } else if (warp == WARP_DECAY) {
-            role_decay<PASS>(p, m);
+            if (SEGMENTS) role_decay<Pass::STATES>(p, m);
+            if (!SEGMENTS || next_pass<false>(p, m)) role_decay<OUT>(p, m);
         } else if (warp == WARP_MMA_U) {
-            role_mma_state<PASS>(p, smem, m, tmem);
-        } else if (PASS != Pass::STATES) {
-            role_mma_out<PASS == Pass::STATES ? Pass::OUTPUT : PASS>(p, smem, m, tmem);
+            if (SEGMENTS) role_mma_state<Pass::STATES>(p, smem, m, tmem);
+            if (!SEGMENTS || next_pass<false>(p, m)) role_mma_state<OUT>(p, smem, m, tmem);
+        } else {
+            if (!SEGMENTS || next_pass<false>(p, m)) role_mma_out<OUT>(p, smem, m, tmem);
         }
     }
     __syncwarp();
@@ -794,7 +896,8 @@ __global__ void __launch_bounds__(256) kda_linear_plan_kernel(const ChunkParams 
             set_status(a.status, KDA_ERR_BAD_SEQLENS);
             s = -1;
         }
-        *p.num_segs = s < 0 ? 0 : s;
+        p.num_segs[0] = s < 0 ? 0 : s;
+        p.num_segs[1] = 0;
         total = s;
     }
     __syncthreads();
@@ -823,27 +926,6 @@ __global__ void __launch_bounds__(256) kda_linear_plan_kernel(const ChunkParams 
             sg.count = k;
             p.segs[at] = sg;
         }
-    }
-}
-
-// ---- entry states: E_{s+1} = 2^{decay_s} E_s + N_s along a sequence, in place over the segments' states N_s
-__global__ void __launch_bounds__(256) kda_linear_join_kernel(const ChunkParams p) {
-    constexpr int PARTS = DK * DV / 1024;
-    const int part = blockIdx.x % PARTS, chain = blockIdx.x / PARTS, n = chain / p.a.H, h = chain % p.a.H;
-    const int2 f = p.first[n];
-    if (f.y < 3) return;  // the first segment's state is whole already, and the last one's is not needed
-    const size_t step = static_cast<size_t>(p.a.H) * DK * DV / 4;
-    float4 *s = reinterpret_cast<float4 *>(p.states) + (static_cast<size_t>(f.x) * p.a.H + h) * (DK * DV / 4) + part * 256 + threadIdx.x;
-    float4 e = *s;
-    for (int i = 1; i < f.y - 1; ++i) {
-        s += step;
-        const float4 x = *s;
-        const float d = expm1f(p.decays[(static_cast<int64_t>(f.x) + i) * p.a.H + h] * (1.f / LOG2E));
-        e.x = fmaf(e.x, d, e.x) + x.x;
-        e.y = fmaf(e.y, d, e.y) + x.y;
-        e.z = fmaf(e.z, d, e.z) + x.z;
-        e.w = fmaf(e.w, d, e.w) + x.w;
-        *s = e;
     }
 }
 
@@ -886,16 +968,22 @@ int num_sms() {
     return sms;
 }
 
-template <Pass PASS>
+template <bool SEGMENTS>
 cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(kda_linear_chunk_kernel<PASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    const auto kernel = kda_linear_chunk_kernel<SEGMENTS>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     static const int regs = [] {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<PASS>) == cudaSuccess ? at.numRegs : 0;
+        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<SEGMENTS>) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
-    kda_linear_chunk_kernel<PASS><<<static_cast<int>(most_tasks < sms ? most_tasks : sms), THREADS, SMEM, stream>>>(p);
+    const int grid = static_cast<int>(most_tasks < sms ? most_tasks : sms);
+    if (SEGMENTS) {
+        void *args[] = {const_cast<ChunkParams *>(&p)};
+        return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(THREADS), args, SMEM, stream);
+    }
+    kernel<<<grid, THREADS, SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -947,7 +1035,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
         return cudaErrorInvalidValue;
     p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
-    if (!p.seg_chunks) return run<Pass::WHOLE>(p, p.tasks, sms, stream);
+    if (!p.seg_chunks) return run<false>(p, p.tasks, sms, stream);
     const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.most_segs = static_cast<int32_t>(l.most);
@@ -957,12 +1045,8 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.decays = reinterpret_cast<float *>(ws + l.decays);
     p.states = reinterpret_cast<float *>(ws + l.states);
     kda_linear_plan_kernel<<<1, 256, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = run<Pass::STATES>(p, l.most * a.H, sms, stream);
-    if (e != cudaSuccess) return e;
-    kda_linear_join_kernel<<<a.N * a.H * (DK * DV / 1024), 256, 0, stream>>>(p);
-    e = cudaGetLastError();
-    return e == cudaSuccess ? run<Pass::OUTPUT>(p, l.most * a.H, sms, stream) : e;
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? run<true>(p, l.most * a.H, sms, stream) : e;
 }
 
 }  // namespace lin

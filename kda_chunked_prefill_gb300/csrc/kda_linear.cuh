@@ -52,6 +52,9 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t *bar, bool yes) {  // (n
         "r"(static_cast<uint32_t>(yes))
         : "memory");
 }
+__device__ __forceinline__ void mbar_inval(uint64_t *bar) {
+    asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // A wait that lets the warp sleep until the phase completes, WAIT_NS at most. (With
 // the default time, a few hundred cycles, the polls of a CTA's waiting warps
 // slow its working ones down.)
