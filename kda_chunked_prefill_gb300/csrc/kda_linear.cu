@@ -62,7 +62,7 @@ struct ChunkParams {
     int32_t *num_segs;  // and, behind it, the count of the launch's barrier
     int2 *first;     // [N] first segment and number of segments
     Segment *segs;
-    float *decays;   // [segment][head]
+    float *decays;   // [segment][head], minus one
     float *states;   // [segment][head][128][128]
 };
 
@@ -112,24 +112,27 @@ struct Task {
     int32_t len, h;
     const float *sin;  // NULL: zeros
     float *sout;       // NULL: not wanted
-    float *decay;      // NULL, or where the segment's log2 decay goes
+    float *decay;      // NULL, or where the segment's decay minus one goes
     bool skip;
 };
 
-template <Pass PASS>
+// The roles' code is shared by the two passes of a segmented launch (SEG): `states` is true in the first. One copy of each:
+// an SM's instruction cache holds about one copy of all roles, and a role's first run through cold code costs as much as
+// two chunks.
+template <bool SEG>
 __device__ __forceinline__ int tasks_of(const ChunkParams &p) {
-    return PASS == Pass::WHOLE ? p.tasks : *p.num_segs * p.a.H;
+    return SEG ? *p.num_segs * p.a.H : p.tasks;
 }
 
-template <Pass PASS>
-__device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
+template <bool SEG>
+__device__ __forceinline__ Task task_of(const ChunkParams &p, int id, bool states) {
     const Params &a = p.a;
     Task t;
     const int seg = id / a.H;
-    t.h = id % a.H;
+    t.h = id - seg * a.H;
     t.decay = nullptr;
     constexpr size_t SZ = static_cast<size_t>(DK) * DV;
-    if (PASS == Pass::WHOLE) {
+    if (!SEG) {
         const int64_t b = a.cu[seg], e = a.cu[seg + 1];
         t.skip = b < 0 || e < b || e > a.T || a.cu[0] != 0;
         t.t0 = b;
@@ -147,7 +150,7 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id) {
     // With the states updated in place, a cut sequence's entry state is read by one
     // CTA and overwritten by another: the last segment's slot, else unused, keeps it.
     const bool keep = sg.count > 1 && a.s0 && a.s0 == a.sT;
-    if (PASS == Pass::STATES) {
+    if (states) {
         t.skip = last && !keep;
         if (last) t.len = 0;
         t.sin = (last || sg.index == 0) && a.s0 ? a.s0 + at : nullptr;
@@ -166,14 +169,10 @@ constexpr int TQ = 0, TV = 1, TK = 2;
 // (Barriers by kind of tile and not by slot: who waits for one kind only then
 // waits for each phase of its barriers in turn. Five slots hold tiles of three
 // chunks where a chunk has two, of two otherwise.)
-template <Pass PASS>
-__device__ __forceinline__ uint64_t *full_of(Misc *m, int kind, uint32_t it) {
-    return PASS == Pass::STATES ? &m->full[3 * (kind - TV) + it % 3] : &m->full[2 * kind + it % 2];
+__device__ __forceinline__ uint64_t *full_of(Misc *m, int kind, uint32_t it, bool states) {
+    return states ? &m->full[3 * (kind - TV) + it % 3] : &m->full[2 * kind + it % 2];
 }
-template <Pass PASS>
-__device__ __forceinline__ uint32_t full_phase(uint32_t it) {
-    return (PASS == Pass::STATES ? it / 3 : it / 2) & 1;
-}
+__device__ __forceinline__ uint32_t full_phase(uint32_t it, bool states) { return (states ? it / 3 : it / 2) & 1; }
 
 // A bounded wait for a barrier's phase. (A parity wait takes the phase before
 // last for the next: every role that waits on a barrier waits for each of its
@@ -216,16 +215,17 @@ __device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 204
 // ---- one thread: tile loads. A chunk's tiles take slots in the order q, v, k: the third waits for the slot of the chunk
 // before's first, so the first is the one that is free soonest (q) and the third not the one that is needed first (v). They are
 // issued in the order v, q, k, since q's slot waits for an output to be stored.
-template <Pass PASS>
-__device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m) {
-    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+template <bool SEG>
+__device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m, bool states) {
+    const int PER = states ? 2 : 3;
+    const uint64_t policy = evict_first();
     int n = 0, part = 0;  // tiles of whole chunks issued, and which kinds of a chunk that was given up
     uint32_t it = 0;
     bool ok = true;
-    const int tasks = tasks_of<PASS>(p);
+    const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; ok && id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
         const int hk = t.h / p.a.rep;
 #pragma unroll 1
@@ -248,10 +248,10 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
                 unsigned char *dst = smem + slot * TILE;
                 const CUtensorMap *map = kind == TV ? &p.tv : kind == TK ? &p.tk : &p.tq;
                 const int head = kind == TV ? t.h : hk;
-                uint64_t *full = full_of<PASS>(m, kind, it);
+                uint64_t *full = full_of(m, kind, it, states);
                 mbar_arrive_expect_tx(full, TILE);
-                tma_load_3d(dst, map, 0, head, row, full);
-                tma_load_3d(dst + PANEL, map, 64, head, row, full);
+                tma_load_3d(dst, map, 0, head, row, full, policy);
+                tma_load_3d(dst + PANEL, map, 64, head, row, full, policy);
                 part |= 1 << kind;
             }
             if (ok) n += PER, ++it;
@@ -264,34 +264,35 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
     if (ok) return;
 #pragma unroll 1
     for (int kind = 0; kind < 3; ++kind) {
-        if (it > 0 && kind >= 3 - PER) (void)mbar_wait_some(full_of<PASS>(m, kind, it - 1), full_phase<PASS>(it - 1));
-        if (part >> kind & 1) (void)mbar_wait_some(full_of<PASS>(m, kind, it), full_phase<PASS>(it));
+        if (it > 0 && kind >= 3 - PER) (void)mbar_wait_some(full_of(m, kind, it - 1, states), full_phase(it - 1, states));
+        if (part >> kind & 1) (void)mbar_wait_some(full_of(m, kind, it, states), full_phase(it, states));
     }
 }
 
 // ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, with
 // everything that makes an address the same in all lanes, and one lane issues. (A 128 x 128 x 16 MMA runs 70 cycles; from one
 // warp the waits and descriptors between groups of four or eight cost as much again.)
-template <Pass PASS>
+template <bool SEG>
 __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+    constexpr bool states = false;
     constexpr uint32_t ID_QK = idesc_bf16(false, false, C, C), ID_QS = idesc_bf16(false, true, C, DV),
                        ID_PV = idesc_bf16(false, true, C, DV);
     int n = 0;
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
-    const int tasks = __shfl_sync(0xffffffffu, tasks_of<PASS>(p), 0);
+    const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
     tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
         for (int c = 0; c < len; c += C, n += 3, ++it) {
             const uint32_t ph = it & 1;
             const int iq = n % TILES, iv = (n + 1) % TILES, ik = (n + 2) % TILES;
             const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
-            if (!wait_warp(m, full_of<PASS>(m, TQ, it), full_phase<PASS>(it))) return;
-            if (!wait_warp(m, full_of<PASS>(m, TK, it), full_phase<PASS>(it))) return;
+            if (!wait_warp(m, full_of(m, TQ, it, states), full_phase(it, states))) return;
+            if (!wait_warp(m, full_of(m, TK, it, states), full_phase(it, states))) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -324,25 +325,25 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
         }
     }
 }
-template <Pass PASS>
-__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
-    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+template <bool SEG>
+__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
+    const int PER = states ? 2 : 3;
     constexpr uint32_t ID_U = idesc_bf16(true, true, DK, DV);
     int n = 0;
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
-    const int tasks = __shfl_sync(0xffffffffu, tasks_of<PASS>(p), 0);
+    const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
     tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
         for (int c = 0; c < len; c += C, n += PER, ++it) {
             const uint32_t ph = it & 1;
             const int iv = (n + PER - 2) % TILES, ik = (n + PER - 1) % TILES;
             const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
-            if (!wait_warp(m, full_of<PASS>(m, TK, it), full_phase<PASS>(it))) return;
+            if (!wait_warp(m, full_of(m, TK, it, states), full_phase(it, states))) return;
             if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
@@ -350,7 +351,7 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
                 const uint64_t v = desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL);
                 if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1)) return;
                 // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
-                if (PASS != Pass::STATES && st == STAGES - 1 && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+                if (!states && st == STAGES - 1 && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -362,7 +363,7 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
                     if (st == STAGES - 1) {
                         umma_commit(&m->u);
                         umma_commit(&m->empty[ik]);
-                        if (PASS == Pass::STATES) umma_commit(&m->empty[iv]);
+                        if (states) umma_commit(&m->empty[iv]);
                     }
                 }
             }
@@ -371,16 +372,16 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
 }
 
 // ---- one warp: decay tables. Lane l has tokens 4 l .. 4 l + 3, eight lanes a block of 32.
-template <Pass PASS>
-__device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
+template <bool SEG>
+__device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool states) {
     const Params &a = p.a;
     const int lane = threadIdx.x & 31, in = lane & 7, block = lane >> 3;
     uint32_t it = 0;
     bool bad = false;
-    const int tasks = tasks_of<PASS>(p);
+    const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
         float raw[4], sum = 0.f;
 #pragma unroll
@@ -434,7 +435,7 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
             // entry of four chunks ago: the scores of two chunks ago came after their read)
             if (lane == 0) m->dm1[it & 3] = expm1f(total * (1.f / LOG2E));
             arrive_warp(&m->decw[buf]);
-            if (PASS == Pass::STATES) continue;
+            if (states) continue;
             if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
 #pragma unroll 1
             for (int x = block + 1; x < 4; ++x) {
@@ -449,29 +450,29 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m) {
             __syncwarp();
             arrive_warp(&m->dect);
         }
-        if (PASS == Pass::STATES && lane == 0) *t.decay = sum;
+        if (states && lane == 0) *t.decay = expm1f(sum * (1.f / LOG2E));
     }
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
 // ---- warps 16-23: v~ = 2^(sum of g after j) v in two bf16 terms, 16-byte pieces in the tile's own order
-template <Pass PASS>
-__device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m) {
-    constexpr int PER = PASS == Pass::STATES ? 2 : 3;
+template <bool SEG>
+__device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, bool states) {
+    const int PER = states ? 2 : 3;
     const int tid = threadIdx.x & (GROUP - 1);
     uint32_t it = 0;
     int n = 0;
-    const int tasks = tasks_of<PASS>(p);
+    const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, n += PER, ++it) {
             const int left = t.len - c, nk = n + PER - 1, nv = n + PER - 2;
             unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
-            if (!wait_warp(m, full_of<PASS>(m, TV, it), full_phase<PASS>(it))) return;
-            if (left < C && !wait_warp(m, full_of<PASS>(m, TK, it), full_phase<PASS>(it))) return;
+            if (!wait_warp(m, full_of(m, TV, it, states), full_phase(it, states))) return;
+            if (left < C && !wait_warp(m, full_of(m, TK, it, states), full_phase(it, states))) return;
             if (!wait_warp(m, &m->decw[it & 1], (it >> 1) & 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
@@ -511,18 +512,19 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
 
 // ---- warps 0-7: decayed scores and the output. Two threads share a token row: key blocks 0 and 3 or 1 and 2 of the scores, one
 // half of the values of the output.
-template <Pass PASS>
+template <bool SEG>
 __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+    constexpr bool states = false;
     const Params &a = p.a;
     const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
     uint32_t it = 0;
     int n = 0;
     bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
-    const int tasks = tasks_of<PASS>(p);
+    const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, n += 3, ++it) {
@@ -617,8 +619,8 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                     const int slot = (n + 1) % TILES;
                     if (left >= C && !fail) {
                         const unsigned char *src = smem + slot * TILE;
-                        tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c));
-                        tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c));
+                        tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c), evict_first());
+                        tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c), evict_first());
                         bulk_commit();
                         bulk_wait_read();
                     }
@@ -633,8 +635,8 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
 }
 
 // ---- warps 8-15: the state. Two threads share a key row of S, one half of its values each.
-template <Pass PASS>
-__device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+template <bool SEG>
+__device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
     constexpr int NV = DV / 2;
     const Params &a = p.a;
     const int gtid = threadIdx.x - GROUP, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
@@ -642,21 +644,12 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
     f2 S[NV / 2];
-    auto publish = [&]() {  // the bf16 copy that q multiplies
-#pragma unroll
-        for (int j = 0; j < NV / 8; ++j) {
-            const uint4 u = make_uint4(bf16_of(S[4 * j]), bf16_of(S[4 * j + 1]), bf16_of(S[4 * j + 2]), bf16_of(S[4 * j + 3]));
-            *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) = u;
-        }
-        fence_proxy_async_shared();
-        arrive_warp(&m->s);
-    };
-    const int tasks = tasks_of<PASS>(p);
+    const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
-        const Task t = task_of<PASS>(p, id);
+        const Task t = task_of<SEG>(p, id, states);
         if (t.skip) {
-            if (PASS == Pass::WHOLE && gtid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            if (!SEG && gtid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
             continue;
         }
         const size_t at = static_cast<size_t>(tid) * DV + half * NV;
@@ -672,9 +665,17 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
 #pragma unroll
             for (int j = 0; j < NV / 2; ++j) S[j] = 0;
         }
-        if (PASS != Pass::STATES && t.len > 0) publish();
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
+            if (!states) {  // the bf16 copy that q multiplies, once q has been multiplied by the last one
+                if (c > 0 && !wait_warp(m, &m->qs, (it - 1) & 1)) return;
+#pragma unroll
+                for (int j = 0; j < NV / 8; ++j)
+                    *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) =
+                        make_uint4(bf16_of(S[4 * j]), bf16_of(S[4 * j + 1]), bf16_of(S[4 * j + 2]), bf16_of(S[4 * j + 3]));
+                fence_proxy_async_shared();
+                arrive_warp(&m->s);
+            }
             if (!wait_warp(m, &m->u, it & 1)) return;
             tc_fence_after();
             const float dm1 = m->dm1[it & 3];
@@ -689,11 +690,8 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             }
             tc_fence_before();
             arrive_warp(&m->ufree);
-            if (PASS != Pass::STATES) {
-                if (!wait_warp(m, &m->qs, it & 1)) return;  // the old copy has been read
-                if (c + C < t.len) publish();
-            }
         }
+        if (!states && t.len > 0 && !wait_warp(m, &m->qs, (it - 1) & 1)) return;
         if (t.sout) {
 #pragma unroll
             for (int j = 0; j < NV; j += 8) {
@@ -724,94 +722,70 @@ __device__ __forceinline__ bool grid_sync(int32_t *count, int32_t target) {
     return false;
 }
 
-// Entry states: E_{s+1} = 2^{decay_s} E_s + N_s along a sequence, in place over the segments' states N_s. Each of the launch's
-// 256 x CTAs threads takes W values at a time through all segments of a chain, with BATCH loads in flight.
-template <int W>
+// Entry states: E_{s+1} = decay_s E_s + N_s along a sequence, in place over the segments' states N_s. Each of the launch's
+// 256 x CTAs threads takes a pair of values through all segments of a head, with BATCH loads in flight. (The first segment's
+// state is whole already, and the last one's is not needed.)
 __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
-    constexpr int BATCH = W == 1 ? 16 : 4;
-    constexpr int UNITS = DK * DV / W;
+    constexpr int BATCH = 8, UNITS = DK * DV / 2;
     const int H = p.a.H;
-    const int64_t all = static_cast<int64_t>(p.a.N) * H * UNITS, stride = static_cast<int64_t>(gridDim.x) * GROUP;
-    const size_t step = static_cast<size_t>(H) * DK * DV;
+    const size_t step = static_cast<size_t>(H) * UNITS;  // from segment to segment
 #pragma unroll 1
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * GROUP + gtid; u < all; u += stride) {
-        const int chain = static_cast<int>(u / UNITS), n = chain / H, h = chain % H;
+    for (int n = 0; n < p.a.N; ++n) {
         const int2 f = p.first[n];
-        if (f.y < 3) continue;  // the first segment's state is whole already, and the last one's is not needed
-        float *s = p.states + (static_cast<size_t>(f.x) * H + h) * (DK * DV) + (u % UNITS) * W;
-        const float *d = p.decays + static_cast<int64_t>(f.x) * H + h;
-        float e[W];
-#pragma unroll
-        for (int w = 0; w < W; ++w) e[w] = __ldcg(s + w);
 #pragma unroll 1
-        for (int i = 1; i < f.y - 1; i += BATCH) {
-            float x[BATCH][W], dd[BATCH];
+        for (uint32_t u = blockIdx.x * GROUP + gtid; f.y > 2 && u < static_cast<uint32_t>(H) * UNITS; u += gridDim.x * GROUP) {
+            f2 *s = reinterpret_cast<f2 *>(p.states) + f.x * step + u;
+            const float *d = p.decays + static_cast<int64_t>(f.x) * H + u / UNITS;
+            f2 e = __ldcg(s);
+#pragma unroll 1
+            for (int left = f.y - 2; left > 0; left -= BATCH) {
+                f2 x[BATCH];
+                float dd[BATCH];
 #pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                if (i + j >= f.y - 1) continue;
-                dd[j] = __ldcg(d + (i + j) * H);
-#pragma unroll
-                for (int w = 0; w < W; ++w) x[j][w] = __ldcg(s + (i + j) * step + w);
-            }
-#pragma unroll
-            for (int j = 0; j < BATCH; ++j) {
-                if (i + j >= f.y - 1) continue;
-                const float m1 = expm1f(dd[j] * (1.f / LOG2E));
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    e[w] = fmaf(e[w], m1, e[w]) + x[j][w];
-                    s[(i + j) * step + w] = e[w];
+                for (int j = 0; j < BATCH; ++j) {
+                    const int at = 1 + (j < left ? j : 0);
+                    x[j] = __ldcg(s + at * step);
+                    dd[j] = __ldcg(d + at * H);
                 }
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    e = add2(fma2(e, pair(dd[j], dd[j]), e), x[j]);
+                    if (j < left) s[(1 + j) * step] = e;
+                }
+                s += BATCH * step;
+                d += BATCH * H;
             }
         }
     }
 }
 
-template <Pass PASS>
-__device__ __forceinline__ void init_barriers(Misc *m) {  // one thread
-    for (int i = 0; i < 6; ++i) mbar_init(&m->full[i], 1);
-    for (int i = 0; i < TILES; ++i) mbar_init(&m->empty[i], PASS == Pass::STATES ? 1 : 2);
-    mbar_init(&m->qk, 1);
-    mbar_init(&m->qs, 1);
-    mbar_init(&m->u, 1);
-    mbar_init(&m->o, 1);
-    for (int i = 0; i < 2; ++i) {
-        mbar_init(&m->vfree[i], 1);
-        mbar_init(&m->vt[i], GROUP / 32);
-        mbar_init(&m->decw[i], 1);
-        mbar_init(&m->wfree[i], GROUP / 32);
-    }
-    mbar_init(&m->dect, 1);
-    mbar_init(&m->go, 1);
-    mbar_init(&m->s, GROUP / 32);
-    mbar_init(&m->p, GROUP / 32);
-    mbar_init(&m->ufree, GROUP / 32);
-    mbar_init(&m->ofree, GROUP / 32);
+constexpr int BARRIERS = offsetof(Misc, tmem) / sizeof(uint64_t);  // they come first in Misc
+__device__ __forceinline__ int arrivals_of(int i, bool states) {
+    constexpr int E0 = offsetof(Misc, empty) / 8, V0 = offsetof(Misc, vt) / 8, W0 = offsetof(Misc, wfree) / 8,
+                  F0 = offsetof(Misc, ufree) / 8;
+    if (i >= E0 && i < E0 + TILES) return states ? 1 : 2;                                  // readers of a tile (see the k tile's)
+    return ((i >= V0 && i < V0 + 4) || (i >= W0 && i < W0 + 2) || i >= F0) ? GROUP / 32 : 1;  // warps of a group
+}
+__device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // one thread
+#pragma unroll 1
+    for (int i = 0; i < BARRIERS; ++i) mbar_init(reinterpret_cast<uint64_t *>(m) + i, arrivals_of(i, states));
     mbar_fence_init();
 }
 
-__device__ __forceinline__ void end_barriers(Misc *m) {
-    constexpr int N = offsetof(Misc, tmem) / sizeof(uint64_t);  // the barriers come first in Misc
-    for (int i = 0; i < N; ++i) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);
-}
-
-// from the pass over the states to the pass over the outputs; false: the launch has given up
-template <bool JOINS>
+// From the pass over the states to the pass over the outputs, for the role of thread 0 (LEADS), the state's (JOINS) and the
+// others; false: the launch has given up.
+template <bool LEADS, bool JOINS>
 __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
     cta_sync();
-    if (threadIdx.x == 0 && !grid_sync(p.num_segs + 1, gridDim.x)) m->abort = 1;
+    if (LEADS && threadIdx.x == 0 && !grid_sync(p.num_segs + 1, gridDim.x)) m->abort = 1;
     cta_sync();
-    if (JOINS) {
-        if (p.a.N * p.a.H >= 32)
-            join_states<4>(p, threadIdx.x - GROUP);
-        else
-            join_states<1>(p, threadIdx.x - GROUP);
-    }
+    if (JOINS) join_states(p, threadIdx.x - GROUP);
     cta_sync();
-    if (threadIdx.x == 0) {
+    if (LEADS && threadIdx.x == 0) {
         if (!grid_sync(p.num_segs + 1, 2 * gridDim.x)) m->abort = 1;
-        end_barriers(m);  // (every arrival of the first pass has come)
-        init_barriers<Pass::OUTPUT>(m);
+#pragma unroll 1
+        for (int i = 0; i < BARRIERS; ++i) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
+        init_barriers(m, false);
     }
     cta_sync();
     return *reinterpret_cast<volatile int32_t *>(&m->abort) == 0;
@@ -820,12 +794,11 @@ __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
 // SEGMENTS: sequences in segments, states first (a cooperative launch); else every sequence as a whole
 template <bool SEGMENTS>
 __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr Pass OUT = SEGMENTS ? Pass::OUTPUT : Pass::WHOLE;
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        init_barriers<SEGMENTS ? Pass::STATES : Pass::WHOLE>(m);
+        init_barriers(m, SEGMENTS);
         m->abort = 0;
     }
     if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
@@ -833,30 +806,39 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
+    // every role: the pass over the states, the join, the pass over the outputs; or the last alone
     if (warp < 8) {
-        if (!SEGMENTS || next_pass<false>(p, m)) role_scores<OUT>(p, smem, m, tmem);
+        if (!SEGMENTS || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
     } else if (warp < 16) {
         more_registers<REGS_STATE>();
-        if (SEGMENTS) role_state<Pass::STATES>(p, smem, m, tmem);
-        if (!SEGMENTS || next_pass<true>(p, m)) role_state<OUT>(p, smem, m, tmem);
+#pragma unroll 1
+        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
+            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
+        }
     } else if (warp < 24) {
         fewer_registers<REGS_V>();
-        if (SEGMENTS) role_v<Pass::STATES>(p, smem, m);
-        if (!SEGMENTS || next_pass<false>(p, m)) role_v<OUT>(p, smem, m);
+#pragma unroll 1
+        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
+            role_v<SEGMENTS>(p, smem, m, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
+        }
     } else {
         fewer_registers<REGS_AUX>();
-        if (warp == WARP_LOAD) {
-            if (SEGMENTS && lane == 0) role_load<Pass::STATES>(p, smem, m);
+#pragma unroll 1
+        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
+            const bool states = SEGMENTS && pass == 0;
+            if (warp == WARP_LOAD) {
+                if (lane == 0) role_load<SEGMENTS>(p, smem, m, states);
+            } else if (warp == WARP_DECAY) {
+                role_decay<SEGMENTS>(p, m, states);
+            } else if (warp == WARP_MMA_U) {
+                role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
+            } else if (!states) {
+                role_mma_out<SEGMENTS>(p, smem, m, tmem);
+            }
             __syncwarp();
-            if ((!SEGMENTS || next_pass<false>(p, m)) && lane == 0) role_load<OUT>(p, smem, m);
-        } else if (warp == WARP_DECAY) {
-            if (SEGMENTS) role_decay<Pass::STATES>(p, m);
-            if (!SEGMENTS || next_pass<false>(p, m)) role_decay<OUT>(p, m);
-        } else if (warp == WARP_MMA_U) {
-            if (SEGMENTS) role_mma_state<Pass::STATES>(p, smem, m, tmem);
-            if (!SEGMENTS || next_pass<false>(p, m)) role_mma_state<OUT>(p, smem, m, tmem);
-        } else {
-            if (!SEGMENTS || next_pass<false>(p, m)) role_mma_out<OUT>(p, smem, m, tmem);
+            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
         }
     }
     __syncwarp();

@@ -35,13 +35,6 @@ struct Segment {
     int32_t t0, len, seq, index, count;  // index of the sequence's count segments
 };
 
-// What a launch of the chunk kernel does with a segment.
-enum class Pass {
-    WHOLE,   // segments are whole sequences
-    STATES,  // the states of all segments but a sequence's last, from zeros (the first: from the sequence's entry state)
-    OUTPUT   // the outputs, from the joined states
-};
-
 // the recurrence, token after token (few tokens per sequence)
 cudaError_t launch_recurrent(const Params &p, cudaStream_t stream);
 
