@@ -706,14 +706,19 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
 
 // ---- segments: between the two passes of one launch
 // all threads of the CTA (from whichever role)
-__device__ __forceinline__ void cta_sync() { named_bar_sync(0, THREADS); }
+__device__ __forceinline__ void cta_sync() {
+    __syncwarp();  // (a warp comes to a barrier as a whole)
+    named_bar_sync(0, THREADS);
+}
 // all CTAs of the launch (one thread of each; all are resident); false: a wait ran out
 __device__ __forceinline__ bool grid_sync(int32_t *count, int32_t target) {
     __threadfence();
     atomicAdd(count, 1);
 #pragma unroll 1
     for (int i = 0; i < GRID_POLLS; ++i) {
-        if (ld_acquire(count) >= target) {
+        // (relaxed polls, one fence: an acquire load per poll invalidates the L1 cache each time, and the SM's next loads
+        // wait for all of them)
+        if (ld_relaxed(count) >= target) {
             __threadfence();
             return true;
         }
@@ -759,6 +764,32 @@ __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
     }
 }
 
+// Touches the pages that this CTA's part of the join and its first output task begin in, from warps that the pass over the
+// states leaves idle: an SM's first access to a page costs microseconds when all SMs make theirs at once.
+__device__ __forceinline__ void touch(const void *p) {
+    uint32_t x;
+    asm volatile("ld.volatile.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void touch_ahead(const ChunkParams &p) {
+    const int tid = threadIdx.x;
+    const int tasks = tasks_of<true>(p), id = blockIdx.x;
+    constexpr size_t SZ = static_cast<size_t>(DK) * DV;
+    if (id >= tasks) return;
+    const Task t = task_of<true>(p, id, false);
+    if (t.len > 0) {
+        const int hk = t.h / p.a.rep;
+        if (tid == 0) touch(p.a.q + t.t0 * p.a.qs + hk * DK);
+        if (tid == 1) touch(p.a.o + (t.t0 * p.a.H + t.h) * DV);
+        if (tid == 2) touch(p.a.g + (p.a.g_per_token ? t.t0 * p.a.H + t.h : t.h));
+    }
+    if (tid == 3 && t.sin) touch(t.sin);
+    if (tid == 4 && t.sout) touch(t.sout);
+    if (tid < 64) {
+        const size_t all = static_cast<size_t>(tasks) * SZ, at = static_cast<size_t>(tid) << 19;  // every 2 MB of the states
+        if (at < all) touch(p.states + at);
+    }
+}
+
 constexpr int BARRIERS = offsetof(Misc, tmem) / sizeof(uint64_t);  // they come first in Misc
 __device__ __forceinline__ int arrivals_of(int i, bool states) {
     constexpr int E0 = offsetof(Misc, empty) / 8, V0 = offsetof(Misc, vt) / 8, W0 = offsetof(Misc, wfree) / 8,
@@ -766,9 +797,8 @@ __device__ __forceinline__ int arrivals_of(int i, bool states) {
     if (i >= E0 && i < E0 + TILES) return states ? 1 : 2;                                  // readers of a tile (see the k tile's)
     return ((i >= V0 && i < V0 + 4) || (i >= W0 && i < W0 + 2) || i >= F0) ? GROUP / 32 : 1;  // warps of a group
 }
-__device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // one thread
-#pragma unroll 1
-    for (int i = 0; i < BARRIERS; ++i) mbar_init(reinterpret_cast<uint64_t *>(m) + i, arrivals_of(i, states));
+__device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // warp 0
+    for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_init(reinterpret_cast<uint64_t *>(m) + i, arrivals_of(i, states));
     mbar_fence_init();
 }
 
@@ -781,11 +811,11 @@ __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
     cta_sync();
     if (JOINS) join_states(p, threadIdx.x - GROUP);
     cta_sync();
-    if (LEADS && threadIdx.x == 0) {
-        if (!grid_sync(p.num_segs + 1, 2 * gridDim.x)) m->abort = 1;
-#pragma unroll 1
-        for (int i = 0; i < BARRIERS; ++i) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
+    if (LEADS && threadIdx.x < 32) {
+        for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
         init_barriers(m, false);
+        __syncwarp();
+        if (threadIdx.x == 0 && !grid_sync(p.num_segs + 1, 2 * gridDim.x)) m->abort = 1;
     }
     cta_sync();
     return *reinterpret_cast<volatile int32_t *>(&m->abort) == 0;
@@ -797,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
         init_barriers(m, SEGMENTS);
         m->abort = 0;
     }
@@ -808,6 +838,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     const uint32_t tmem = m->tmem;
     // every role: the pass over the states, the join, the pass over the outputs; or the last alone
     if (warp < 8) {
+        if (SEGMENTS) touch_ahead(p);
         if (!SEGMENTS || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
     } else if (warp < 16) {
         more_registers<REGS_STATE>();
