@@ -45,12 +45,10 @@ namespace {
 constexpr int C = CHUNK;
 constexpr int TILE = C * DK * 2;  // one 128 x 128 bf16 tile: two panels of 64 channels, 128-byte rows, swizzled
 constexpr int PANEL = TILE / 2;
-constexpr int TILES = 5;
-constexpr int OFF_S = TILES * TILE;   // bf16 copy of S: [key][value], two panels of 64 values
-constexpr int OFF_VT = OFF_S + TILE;  // v~: two stages of 32 tokens, each hi (two panels) and lo (two panels)
-constexpr int STAGES = 4, STAGE_ROWS = C / STAGES;  // stages of a chunk
-constexpr int VT_PANEL = STAGE_ROWS * 128, VT_TERM = 2 * VT_PANEL, VT_STAGE = 2 * VT_TERM;
-constexpr int OFF_MISC = OFF_VT + TILE;
+constexpr int TILES = 6;
+constexpr int OFF_S = TILES * TILE;   // bf16 copy of S: [value][key], two panels of 64 keys
+constexpr int STAGES = 4, STAGE_ROWS = C / STAGES;  // stages of a chunk's v~
+constexpr int OFF_MISC = OFF_S + TILE;
 
 struct ChunkParams {
     Params a;
@@ -67,28 +65,30 @@ struct ChunkParams {
 };
 
 struct Misc {
-    uint64_t full[6];             // a tile has come, by its kind and its chunk's number
-    uint64_t empty[TILES];        // a slot is free
-    uint64_t qk, qs, u, o, vfree[2];  // tensor core -> warps (commits)
-    uint64_t decw[2], dect;       // decay tables written: w and dm1; tab, pre and upto
-    uint64_t vt[2], s, p;         // v~ stage, bf16 state, scores written
-    uint64_t wfree[2];            // w read
-    uint64_t go;                  // the first g have been read
-    uint64_t ufree, ofree;        // U read; O1 and O2 read
-    uint32_t tmem;                // address of the tensor memory
-    int32_t abort;                // a wait ran out
-    alignas(16) float tab[192];   // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
-    alignas(16) float pre[C];     // log2 prefix of j within its block of 32
-    alignas(16) float upto[C];    // 2^(sum of g up to j)
-    alignas(16) float w[2][C];    // 2^(sum of g after j up to the chunk's end), a chunk ahead
-    float dm1[4];                 // 2^(the chunk's sum) - 1, of the last four chunks
+    uint64_t full[6];                 // a tile has come, by its kind and its chunk's number
+    uint64_t empty[TILES];            // a slot is free
+    uint64_t qk, qs, u, o, vfree[STAGES];  // tensor core -> warps (commits)
+    uint64_t decw[2], dect;           // decay tables written: w and dm1; tab, pre and start
+    uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled)
+    uint64_t wfree[2];                // w read
+    uint64_t go;                      // the first g have been read
+    uint64_t ufree, ofree;            // U read; O read
+    uint32_t tmem;                    // address of the tensor memory
+    int32_t abort;                    // a wait ran out
+    alignas(16) float tab[192];       // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
+    alignas(16) float pre[C];         // log2 prefix of j within its block of 32
+    alignas(16) float w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
+    float start[4];                   // log2 sum of g up to the start of each block
+    float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
 };
 __host__ __device__ constexpr int tab_at(int anchor) { return anchor == 1 ? 0 : anchor == 2 ? 32 : 96; }
-static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && offsetof(Misc, upto) % 16 == 0 && offsetof(Misc, w) % 16 == 0 && OFF_MISC % 16 == 0, "read as float4");
+static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && offsetof(Misc, w) % 16 == 0 && OFF_MISC % 16 == 0,
+              "read as float4");
 constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc));
 static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
-constexpr uint32_t COL_QK = 0, COL_O1 = 128, COL_O2 = 256, COL_U = 384;  // tensor memory columns (P over A)
+// tensor memory columns: q k^T, and P in the first half of each block's; the outputs; U; v~ (hi of 128 tokens, then lo)
+constexpr uint32_t COL_QK = 0, COL_O = 128, COL_U = 256, COL_VT = 384;
 // warps: 0-7 scores, 8-15 state, 16-23 v~, then one each
 constexpr int GROUP = 256;
 constexpr int WARP_LOAD = 24, WARP_DECAY = 25, WARP_MMA_OUT = 26, WARP_MMA_U = 27, THREADS = 896;
@@ -166,13 +166,12 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id, bool state
 }
 
 constexpr int TQ = 0, TV = 1, TK = 2;
-// (Barriers by kind of tile and not by slot: who waits for one kind only then
-// waits for each phase of its barriers in turn. Five slots hold tiles of three
-// chunks where a chunk has two, of two otherwise.)
-__device__ __forceinline__ uint64_t *full_of(Misc *m, int kind, uint32_t it, bool states) {
-    return states ? &m->full[3 * (kind - TV) + it % 3] : &m->full[2 * kind + it % 2];
+// The six slots hold the three tiles of two chunks, or the two (v, k) of three. A slot's barriers are numbered by the chunks
+// that have used it.
+__device__ __forceinline__ int slot_of(int kind, uint32_t it, bool states) {
+    return states ? 2 * static_cast<int>(it % 3) + kind - TV : 3 * static_cast<int>(it % 2) + kind;
 }
-__device__ __forceinline__ uint32_t full_phase(uint32_t it, bool states) { return (states ? it / 3 : it / 2) & 1; }
+__device__ __forceinline__ uint32_t use_of(uint32_t it, bool states) { return states ? it / 3 : it / 2; }
 
 // A bounded wait for a barrier's phase. (A parity wait takes the phase before
 // last for the next: every role that waits on a barrier waits for each of its
@@ -212,17 +211,13 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t tile, uint32_t panel) {  //
 __device__ __forceinline__ constexpr uint64_t step_k(int kk) { return ((kk >> 2) * PANEL + (kk & 3) * 32) >> 4; }
 __device__ __forceinline__ constexpr uint64_t step_mn(int kk) { return (kk * 2048) >> 4; }
 
-// ---- one thread: tile loads. A chunk's tiles take slots in the order q, v, k: the third waits for the slot of the chunk
-// before's first, so the first is the one that is free soonest (q) and the third not the one that is needed first (v). They are
-// issued in the order v, q, k, since q's slot waits for an output to be stored.
+// ---- one thread: tile loads, a chunk ahead (two in the pass over the states)
 template <bool SEG>
 __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *smem, Misc *m, bool states) {
-    const int PER = states ? 2 : 3;
     const uint64_t policy = evict_first();
-    int n = 0, part = 0;  // tiles of whole chunks issued, and which kinds of a chunk that was given up
-    uint32_t it = 0;
+    uint32_t it = 0, part = 0;  // whole chunks issued, and which kinds of a chunk that was given up
     bool ok = true;
-    const int tasks = tasks_of<SEG>(p);
+    const int tasks = tasks_of<SEG>(p), first = states ? TV : TQ;
 #pragma unroll 1
     for (int id = blockIdx.x; ok && id < tasks; id += gridDim.x) {
         const Task t = task_of<SEG>(p, id, states);
@@ -233,39 +228,40 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
             const int row = static_cast<int>(t.t0 + c);
             part = 0;
             // the first decay table waits for a few bytes of g: they go ahead of all SMs' first tiles
-            if (n == 0 && !wait(m, &m->go, 0)) {
+            if (it == 0 && !wait(m, &m->go, 0)) {
                 ok = false;
                 break;
             }
+            const uint32_t use = use_of(it, states);
 #pragma unroll 1
-            for (int i = 0; i < PER; ++i) {
-                const int kind = PER == 2 ? i + 1 : i == 0 ? TV : i == 1 ? TQ : TK;
-                const int at = kind - (3 - PER), slot = (n + at) % TILES;
-                if (n + at >= TILES && !wait(m, &m->empty[slot], ((n + at) / TILES - 1) & 1)) {
+            for (int kind = first; kind < 3; ++kind) {
+                const int slot = slot_of(kind, it, states);
+                if (use > 0 && !wait(m, &m->empty[slot], (use - 1) & 1)) {
                     ok = false;
                     break;
                 }
                 unsigned char *dst = smem + slot * TILE;
                 const CUtensorMap *map = kind == TV ? &p.tv : kind == TK ? &p.tk : &p.tq;
                 const int head = kind == TV ? t.h : hk;
-                uint64_t *full = full_of(m, kind, it, states);
-                mbar_arrive_expect_tx(full, TILE);
-                tma_load_3d(dst, map, 0, head, row, full, policy);
-                tma_load_3d(dst + PANEL, map, 64, head, row, full, policy);
-                part |= 1 << kind;
+                mbar_arrive_expect_tx(&m->full[slot], TILE);
+                tma_load_3d(dst, map, 0, head, row, &m->full[slot], policy);
+                tma_load_3d(dst + PANEL, map, 64, head, row, &m->full[slot], policy);
+                part |= 1u << kind;
             }
-            if (ok) n += PER, ++it;
+            if (ok) ++it;
         }
     }
     // no copy and no commit of this CTA is in flight when it ends
+    const uint32_t back = states ? 3 : 2;
 #pragma unroll 1
-    for (int k = n > TILES ? n - TILES : 0; ok && k < n; ++k)
-        ok = wait(m, &m->empty[k % TILES], (k / TILES) & 1);
+    for (uint32_t k = it > back ? it - back : 0; k < it; ++k)
+#pragma unroll 1
+        for (int kind = first; ok && kind < 3; ++kind) ok = wait(m, &m->empty[slot_of(kind, k, states)], use_of(k, states) & 1);
     if (ok) return;
 #pragma unroll 1
-    for (int kind = 0; kind < 3; ++kind) {
-        if (it > 0 && kind >= 3 - PER) (void)mbar_wait_some(full_of(m, kind, it - 1, states), full_phase(it - 1, states));
-        if (part >> kind & 1) (void)mbar_wait_some(full_of(m, kind, it, states), full_phase(it, states));
+    for (int kind = first; kind < 3; ++kind) {
+        if (it > 0) (void)mbar_wait_some(&m->full[slot_of(kind, it - 1, states)], use_of(it - 1, states) & 1);
+        if (part >> kind & 1) (void)mbar_wait_some(&m->full[slot_of(kind, it, states)], use_of(it, states) & 1);
     }
 }
 
@@ -275,11 +271,10 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
 template <bool SEG>
 __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
-    constexpr uint32_t ID_QK = idesc_bf16(false, false, C, C), ID_QS = idesc_bf16(false, true, C, DV),
-                       ID_PV = idesc_bf16(false, true, C, DV);
-    int n = 0;
+    constexpr uint32_t ID_KK = idesc_bf16(false, false, C, C), ID_PV = idesc_bf16(false, true, C, DV);
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
+    const uint64_t s = desc_k(base + OFF_S);
     const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
     tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
@@ -287,31 +282,29 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
         const Task t = task_of<SEG>(p, id, states);
         const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
-        for (int c = 0; c < len; c += C, n += 3, ++it) {
-            const uint32_t ph = it & 1;
-            const int iq = n % TILES, iv = (n + 1) % TILES, ik = (n + 2) % TILES;
+        for (int c = 0; c < len; c += C, ++it) {
+            const uint32_t ph = it & 1, up = use_of(it, states) & 1;
+            const int iq = slot_of(TQ, it, states), iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
             const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
-            if (!wait_warp(m, full_of(m, TQ, it, states), full_phase(it, states))) return;
-            if (!wait_warp(m, full_of(m, TK, it, states), full_phase(it, states))) return;
+            if (!wait_warp(m, &m->full[iq], up)) return;
+            if (!wait_warp(m, &m->full[ik], up)) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_QK, kk > 0);
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_KK, kk > 0);
                 umma_commit(&m->qk);
                 umma_commit(&m->empty[ik]);
             }
-            const uint64_t s = desc_mn(base + OFF_S, PANEL);
             if (!wait_warp(m, &m->s, ph)) return;
             if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O1, q + step_k(kk), s + step_mn(kk), ID_QS, kk > 0);
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O, q + step_k(kk), s + step_k(kk), ID_KK, kk > 0);
                 umma_commit(&m->qs);
-                umma_commit(&m->empty[iq]);  // (twice: a k tile has two readers, and any slot may hold one)
                 umma_commit(&m->empty[iq]);
             }
-            // P v comes after U: by then zeros behind a segment's end are in v, and v~ has been made of it (o goes into its tile)
+            // P v onto the scaled q S; after U: by then v~ has been made of v (o goes into its tile)
             const uint64_t v = desc_mn(base + iv * TILE, PANEL);
             if (!wait_warp(m, &m->u, ph)) return;
             if (!wait_warp(m, &m->p, ph)) return;
@@ -319,7 +312,7 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < C / 16; ++kk)
-                    umma_ts(tmem + COL_O2, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), ID_PV, kk > 0);
+                    umma_ts(tmem + COL_O, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), ID_PV, 1);
                 umma_commit(&m->o);
             }
         }
@@ -327,9 +320,7 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
 }
 template <bool SEG>
 __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    const int PER = states ? 2 : 3;
-    constexpr uint32_t ID_U = idesc_bf16(true, true, DK, DV);
-    int n = 0;
+    constexpr uint32_t ID_U = idesc_bf16(false, true, DV, DK);
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
     const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
@@ -339,27 +330,27 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
         const Task t = task_of<SEG>(p, id, states);
         const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
-        for (int c = 0; c < len; c += C, n += PER, ++it) {
+        for (int c = 0; c < len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            const int iv = (n + PER - 2) % TILES, ik = (n + PER - 1) % TILES;
+            const int iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
             const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
-            if (!wait_warp(m, full_of(m, TK, it, states), full_phase(it, states))) return;
+            if (!wait_warp(m, &m->full[ik], use_of(it, states) & 1)) return;
             if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
                 const uint64_t k = kt + st * step_mn(STAGE_ROWS / 16);
-                const uint64_t v = desc_mn(base + OFF_VT + (st & 1) * VT_STAGE, VT_PANEL);
-                if (!wait_warp(m, &m->vt[st & 1], (2 * it + (st >> 1)) & 1)) return;
+                const uint32_t vt = tmem + COL_VT + st * (STAGE_ROWS / 2);
+                if (!wait_warp(m, &m->vt[st], ph)) return;
                 // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
                 if (!states && st == STAGES - 1 && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
-                        umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk), ID_U, st > 0 || kk > 0);
-                        umma_f16(tmem + COL_U, k + step_mn(kk), v + step_mn(kk) + (VT_TERM >> 4), ID_U, 1);
+                        umma_ts(tmem + COL_U, vt + 8 * kk, k + step_mn(kk), ID_U, st > 0 || kk > 0);
+                        umma_ts(tmem + COL_U, vt + C / 2 + 8 * kk, k + step_mn(kk), ID_U, 1);
                     }
-                    umma_commit(&m->vfree[st & 1]);
+                    umma_commit(&m->vfree[st]);
                     if (st == STAGES - 1) {
                         umma_commit(&m->u);
                         umma_commit(&m->empty[ik]);
@@ -421,12 +412,10 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, down, 8 * b);
             const float total = (tot[0] + tot[1]) + (tot[2] + tot[3]);
             sum += total;
-            float to_end = after, from_start = before;  // whole blocks added one by one, the nearer first
+            float to_end = after;  // whole blocks added one by one, the nearer first
 #pragma unroll
-            for (int b = 1; b < 4; ++b) {
+            for (int b = 1; b < 4; ++b)
                 if (b > block) to_end += tot[b];
-                if (3 - b < block) from_start += tot[3 - b];
-            }
             const int buf = it & 1;
             if (it > 1 && !wait_warp(m, &m->wfree[buf], ((it >> 1) - 1) & 1)) return;
             *reinterpret_cast<float4 *>(&m->w[buf][4 * lane]) =
@@ -445,9 +434,14 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             }
             *reinterpret_cast<float4 *>(&m->pre[4 * lane]) =
                 make_float4(pre[0] + before, pre[1] + before, pre[2] + before, pre[3] + before);
-            *reinterpret_cast<float4 *>(&m->upto[4 * lane]) =
-                make_float4(ex2(pre[0] + from_start), ex2(pre[1] + from_start), ex2(pre[2] + from_start), ex2(pre[3] + from_start));
-            __syncwarp();
+            if (lane == 0) {
+                float from = 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    m->start[b] = from;
+                    from += tot[b];
+                }
+            }
             arrive_warp(&m->dect);
         }
         if (states && lane == 0) *t.decay = expm1f(sum * (1.f / LOG2E));
@@ -455,55 +449,67 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- warps 16-23: v~ = 2^(sum of g after j) v in two bf16 terms, 16-byte pieces in the tile's own order
+// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A thread has one value
+// channel (the lane of its warp's quarter) and every other 16 tokens.
 template <bool SEG>
-__device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, bool states) {
-    const int PER = states ? 2 : 3;
-    const int tid = threadIdx.x & (GROUP - 1);
+__device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
+    const int gtid = threadIdx.x & (GROUP - 1), half = gtid >> 7, ch = gtid & 127;
+    const uint32_t dst = tmem + (static_cast<uint32_t>(ch >> 5) << 21) + COL_VT + 8 * half;
+    const uint32_t row0 = (ch >> 6) * PANEL + half * 16 * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
+    const f2 minus = pair(-1.f, -1.f);
     uint32_t it = 0;
-    int n = 0;
     const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
 #pragma unroll 1
-        for (int c = 0; c < t.len; c += C, n += PER, ++it) {
-            const int left = t.len - c, nk = n + PER - 1, nv = n + PER - 2;
-            unsigned char *tk = smem + (nk % TILES) * TILE, *tv = smem + (nv % TILES) * TILE;
-            if (!wait_warp(m, full_of(m, TV, it, states), full_phase(it, states))) return;
-            if (left < C && !wait_warp(m, full_of(m, TK, it, states), full_phase(it, states))) return;
+        for (int c = 0; c < t.len; c += C, ++it) {
+            const int left = t.len - c, iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
+            const uint32_t up = use_of(it, states) & 1;
+            unsigned char *tv = smem + iv * TILE;
+            if (!wait_warp(m, &m->full[iv], up)) return;
+            if (left < C) {  // rows behind the segment are someone else's: zeros in v, k and v~
+                if (!wait_warp(m, &m->full[ik], up)) return;
+                unsigned char *tk = smem + ik * TILE;
+#pragma unroll 1
+                for (int i = gtid; i < (C - left) * 16; i += GROUP) {
+                    const int at = (i & 8 ? PANEL : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16;
+                    *reinterpret_cast<uint4 *>(tv + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(tk + at) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_shared();
+            }
             if (!wait_warp(m, &m->decw[it & 1], (it >> 1) & 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
-                const uint32_t use = 2 * it + (st >> 1);
-                if (use && !wait_warp(m, &m->vfree[st & 1], (use - 1) & 1)) return;
-                unsigned char *vt = smem + OFF_VT + (st & 1) * VT_STAGE;
-                const int off = tid * 16, row = STAGE_ROWS * st + (off >> 7);  // 32 rows x 8 pieces a panel
-                const float wr = m->w[it & 1][row];
-                const f2 w2 = pair(wr, wr), minus = pair(-1.f, -1.f);
-#pragma unroll 1
-                for (int panel = 0; panel < 2; ++panel) {
-                    const int at = panel * PANEL + st * VT_PANEL + off;
-                    uint4 u = *reinterpret_cast<const uint4 *>(tv + at);
-                    if (row >= left) {  // behind the segment, someone else's rows: zeros in k, v and v~
-                        u = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(tv + at) = u;
-                        *reinterpret_cast<uint4 *>(tk + at) = u;
-                    }
-                    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t hi[4], lo[4];
+                if (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1)) return;
+                tc_fence_after();
+                const unsigned char *src = tv + row0 + st * (STAGE_ROWS * 128);
+                const int j0 = STAGE_ROWS * st + 16 * half;  // this thread's 16 tokens
+                const float4 *w4 = reinterpret_cast<const float4 *>(&m->w[it & 1][j0]);
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f2 y = mul2(of_bf16(v[j]), w2);
-                        hi[j] = bf16_of(y);
-                        lo[j] = bf16_of(fma2(of_bf16(hi[j]), minus, y));
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w = w4[j];
+                    uint32_t x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // the tile's swizzle: 16-byte piece ^ row % 8
+                        const int r = 4 * j + i;
+                        x[i] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(src + r * 128 + ((piece ^ (r & 7)) << 4))) << 16;
+                        if (j0 + r >= left) x[i] = 0;
                     }
-                    *reinterpret_cast<uint4 *>(vt + panel * VT_PANEL + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(vt + VT_TERM + panel * VT_PANEL + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const f2 y0 = mul2(pair(x[0], x[1]), pair(w.x, w.y)), y1 = mul2(pair(x[2], x[3]), pair(w.z, w.w));
+                    hi[2 * j] = bf16_of(y0);
+                    hi[2 * j + 1] = bf16_of(y1);
+                    lo[2 * j] = bf16_of(fma2(of_bf16(hi[2 * j]), minus, y0));
+                    lo[2 * j + 1] = bf16_of(fma2(of_bf16(hi[2 * j + 1]), minus, y1));
                 }
-                fence_proxy_async_shared();
-                arrive_warp(&m->vt[st & 1]);
+                tmem_st8(dst + st * (STAGE_ROWS / 2), hi);
+                tmem_st8(dst + st * (STAGE_ROWS / 2) + C / 2, lo);
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(&m->vt[st]);
             }
             arrive_warp(&m->wfree[it & 1]);
         }
@@ -519,7 +525,6 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
     const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
     uint32_t it = 0;
-    int n = 0;
     bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
     const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
@@ -527,16 +532,15 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
 #pragma unroll 1
-        for (int c = 0; c < t.len; c += C, n += 3, ++it) {
+        for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
             const int left = t.len - c;  // tokens from this chunk on
-            unsigned char *tile = smem + (n + 1) % TILES * TILE + half * PANEL;  // o goes where v was
+            const int slot = slot_of(TV, it, states);
+            unsigned char *tile = smem + slot * TILE + half * PANEL;  // o goes where v was
             fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
-            float entry = 0.f;
             if (!fail) {
                 tc_fence_after();
-                const float pre = m->pre[tid], row = ex2(pre);
-                entry = a.scale * m->upto[tid];
+                const float pre = m->pre[tid], row = ex2(pre), entry = ex2(pre + m->start[warp]);
                 // key blocks of 32: 0 and 3, or 1 and 2
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
@@ -573,27 +577,46 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                     }
                     tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(&m->p);
+                // q S by the row's decay since the chunk began; P v is added onto it
+                fail = !wait_warp(m, &m->qs, ph);
+                if (!fail) {
+                    tc_fence_after();
+                    const f2 e2 = pair(entry, entry);
+#pragma unroll 1
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t s[32];
+                        tmem_ld32(tmem + lanes + COL_O + 64 * half + 32 * b, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float x, y;
+                            split(mul2(e2, pair(s[2 * j], s[2 * j + 1])), x, y);
+                            s[2 * j] = __float_as_uint(x);
+                            s[2 * j + 1] = __float_as_uint(y);
+                        }
+                        tmem_st32(tmem + lanes + COL_O + 64 * half + 32 * b, s);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive_warp(&m->p);
+                }
             }
             fail = fail || !wait_warp(m, &m->o, ph);
             if (!fail) {
                 tc_fence_after();
-                const f2 e2 = pair(entry, entry), s2 = pair(a.scale, a.scale);
+                const f2 s2 = pair(a.scale, a.scale);
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    uint32_t o1[16], o2[16];
-                    tmem_ld16(tmem + lanes + COL_O1 + 64 * half + 16 * b, o1);
-                    tmem_ld16(tmem + lanes + COL_O2 + 64 * half + 16 * b, o2);
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + lanes + COL_O + 64 * half + 32 * b, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        o1[j] = bf16_of(fma2(e2, pair(o1[2 * j], o1[2 * j + 1]), mul2(s2, pair(o2[2 * j], o2[2 * j + 1]))));
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)  // the tile's swizzle: 16-byte piece ^ row % 8
-                        *reinterpret_cast<uint4 *>(tile + tid * 128 + (((2 * b + j) ^ (tid & 7)) << 4)) =
-                            make_uint4(o1[4 * j], o1[4 * j + 1], o1[4 * j + 2], o1[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j) {  // the tile's swizzle: 16-byte piece ^ row % 8
+                        const int i = 8 * j;
+                        *reinterpret_cast<uint4 *>(tile + tid * 128 + (((4 * b + j) ^ (tid & 7)) << 4)) =
+                            make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
+                                       bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
+                    }
                 }
                 tc_fence_before();
                 arrive_warp(&m->ofree);
@@ -616,7 +639,6 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
             } else {
                 named_bar_sync(2, GROUP);
                 if (lane == 0) {
-                    const int slot = (n + 1) % TILES;
                     if (left >= C && !fail) {
                         const unsigned char *src = smem + slot * TILE;
                         tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c), evict_first());
@@ -624,7 +646,6 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                         bulk_commit();
                         bulk_wait_read();
                     }
-                    mbar_arrive(&m->empty[slot]);
                     mbar_arrive(&m->empty[slot]);
                 }
                 __syncwarp();
@@ -634,16 +655,16 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
 }
 
-// ---- warps 8-15: the state. Two threads share a key row of S, one half of its values each.
+// ---- warps 8-15: the state, transposed as U is. Two threads share a value column of S, one half of its keys each.
 template <bool SEG>
 __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    constexpr int NV = DV / 2;
+    constexpr int NK = DK / 2;
     const Params &a = p.a;
     const int gtid = threadIdx.x - GROUP, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
-    f2 S[NV / 2];
+    f2 S[NK / 2];
     const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
@@ -652,25 +673,20 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             if (!SEG && gtid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
             continue;
         }
-        const size_t at = static_cast<size_t>(tid) * DV + half * NV;
+        const size_t at = static_cast<size_t>(half * NK) * DV + tid;  // and every 128th value behind it
         if (t.sin) {
 #pragma unroll
-            for (int j = 0; j < NV; j += 8) {
-                float x[8];
-                ld_f8(x, t.sin + at + j);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[j / 2 + i] = pair(x[2 * i], x[2 * i + 1]);
-            }
+            for (int j = 0; j < NK / 2; ++j) S[j] = pair(__ldcg(t.sin + at + 2 * j * DV), __ldcg(t.sin + at + (2 * j + 1) * DV));
         } else {
 #pragma unroll
-            for (int j = 0; j < NV / 2; ++j) S[j] = 0;
+            for (int j = 0; j < NK / 2; ++j) S[j] = 0;
         }
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             if (!states) {  // the bf16 copy that q multiplies, once q has been multiplied by the last one
                 if (c > 0 && !wait_warp(m, &m->qs, (it - 1) & 1)) return;
 #pragma unroll
-                for (int j = 0; j < NV / 8; ++j)
+                for (int j = 0; j < NK / 8; ++j)
                     *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) =
                         make_uint4(bf16_of(S[4 * j]), bf16_of(S[4 * j + 1]), bf16_of(S[4 * j + 2]), bf16_of(S[4 * j + 3]));
                 fence_proxy_async_shared();
@@ -681,9 +697,9 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             const float dm1 = m->dm1[it & 3];
             const f2 d2 = pair(dm1, dm1);
 #pragma unroll
-            for (int b = 0; b < NV / 32; ++b) {
+            for (int b = 0; b < NK / 32; ++b) {
                 uint32_t u[32];
-                tmem_ld32(tmem + lanes + COL_U + NV * half + 32 * b, u);
+                tmem_ld32(tmem + lanes + COL_U + NK * half + 32 * b, u);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) S[16 * b + j] = add2(fma2(S[16 * b + j], d2, S[16 * b + j]), pair(u[2 * j], u[2 * j + 1]));
@@ -694,11 +710,11 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
         if (!states && t.len > 0 && !wait_warp(m, &m->qs, (it - 1) & 1)) return;
         if (t.sout) {
 #pragma unroll
-            for (int j = 0; j < NV; j += 8) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) split(S[j / 2 + i], x[2 * i], x[2 * i + 1]);
-                st_f8(t.sout + at + j, x);
+            for (int j = 0; j < NK / 2; ++j) {
+                float x, y;
+                split(S[j], x, y);
+                t.sout[at + 2 * j * DV] = x;
+                t.sout[at + (2 * j + 1) * DV] = y;
             }
         }
     }
@@ -767,8 +783,7 @@ __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
 // Touches the pages that this CTA's part of the join and its first output task begin in, from warps that the pass over the
 // states leaves idle: an SM's first access to a page costs microseconds when all SMs make theirs at once.
 __device__ __forceinline__ void touch(const void *p) {
-    uint32_t x;
-    asm volatile("ld.volatile.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    asm volatile("{\n\t.reg .b32 x;\n\tld.volatile.global.u32 x, [%0];\n\t}" ::"l"(p) : "memory");
 }
 __device__ __forceinline__ void touch_ahead(const ChunkParams &p) {
     const int tid = threadIdx.x;
@@ -794,8 +809,8 @@ constexpr int BARRIERS = offsetof(Misc, tmem) / sizeof(uint64_t);  // they come 
 __device__ __forceinline__ int arrivals_of(int i, bool states) {
     constexpr int E0 = offsetof(Misc, empty) / 8, V0 = offsetof(Misc, vt) / 8, W0 = offsetof(Misc, wfree) / 8,
                   F0 = offsetof(Misc, ufree) / 8;
-    if (i >= E0 && i < E0 + TILES) return states ? 1 : 2;                                  // readers of a tile (see the k tile's)
-    return ((i >= V0 && i < V0 + 4) || (i >= W0 && i < W0 + 2) || i >= F0) ? GROUP / 32 : 1;  // warps of a group
+    if (i >= E0 && i < E0 + TILES) return !states && (i - E0) % 3 == TK ? 2 : 1;  // a k tile is read by q k^T and by U
+    return ((i >= V0 && i < V0 + STAGES + 2) || (i >= W0 && i < W0 + 2) || i >= F0) ? GROUP / 32 : 1;  // warps of a group
 }
 __device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // warp 0
     for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_init(reinterpret_cast<uint64_t *>(m) + i, arrivals_of(i, states));
@@ -851,7 +866,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
         fewer_registers<REGS_V>();
 #pragma unroll 1
         for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
-            role_v<SEGMENTS>(p, smem, m, SEGMENTS && pass == 0);
+            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
             if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
         }
     } else {
@@ -865,7 +880,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
                 role_decay<SEGMENTS>(p, m, states);
             } else if (warp == WARP_MMA_U) {
                 role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
-            } else if (!states) {
+            } else if (warp == WARP_MMA_OUT && !states) {
                 role_mma_out<SEGMENTS>(p, smem, m, tmem);
             }
             __syncwarp();
