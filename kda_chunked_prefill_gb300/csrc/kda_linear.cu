@@ -13,8 +13,8 @@
 //   load    one thread: q, k and v tiles by TMA into a ring of five 32 KB tiles
 //   decays  one warp: the chunk's decay tables from g
 //   v~      8 warps: v~ in stages of 32 tokens
-//   scores  8 warps: P, then o_i into the chunk's v tile
-//   state   8 warps: S
+//   scores  8 warps: P, half of o_i
+//   state   8 warps: S, the other half of o_i; o leaves from the chunk's q tile
 //   MMAs    one warp for q k^T, q S and P v, one for U
 //
 // Why this split. U does not depend on S, so the recurrence from chunk to chunk
@@ -234,7 +234,8 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
             }
             const uint32_t use = use_of(it, states);
 #pragma unroll 1
-            for (int kind = first; kind < 3; ++kind) {
+            for (int i = first; i < 3; ++i) {  // v, k, q: q's slot is free last, when an output has been stored
+                const int kind = states ? i : i == 2 ? TQ : i + 1;
                 const int slot = slot_of(kind, it, states);
                 if (use > 0 && !wait(m, &m->empty[slot], (use - 1) & 1)) {
                     ok = false;
@@ -302,9 +303,8 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
 #pragma unroll
                 for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O, q + step_k(kk), s + step_k(kk), ID_KK, kk > 0);
                 umma_commit(&m->qs);
-                umma_commit(&m->empty[iq]);
             }
-            // P v onto the scaled q S; after U: by then v~ has been made of v (o goes into its tile)
+            // P v onto the scaled q S; after U: by then v~ has been made of v
             const uint64_t v = desc_mn(base + iv * TILE, PANEL);
             if (!wait_warp(m, &m->u, ph)) return;
             if (!wait_warp(m, &m->p, ph)) return;
@@ -314,6 +314,7 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
                 for (int kk = 0; kk < C / 16; ++kk)
                     umma_ts(tmem + COL_O, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), ID_PV, 1);
                 umma_commit(&m->o);
+                umma_commit(&m->empty[iv]);
             }
         }
     }
@@ -457,6 +458,7 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
     const uint32_t dst = tmem + (static_cast<uint32_t>(ch >> 5) << 21) + COL_VT + 8 * half;
     const uint32_t row0 = (ch >> 6) * PANEL + half * 16 * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
     const f2 minus = pair(-1.f, -1.f);
+    bool fail = false;  // (a warp that gives up still comes to the barriers)
     uint32_t it = 0;
     const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
@@ -468,22 +470,24 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
             const int left = t.len - c, iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
             const uint32_t up = use_of(it, states) & 1;
             unsigned char *tv = smem + iv * TILE;
-            if (!wait_warp(m, &m->full[iv], up)) return;
-            if (left < C) {  // rows behind the segment are someone else's: zeros in v, k and v~
-                if (!wait_warp(m, &m->full[ik], up)) return;
+            fail = fail || !wait_warp(m, &m->full[iv], up);
+            if (left < C) {  // rows behind the segment are someone else's: zeros in v and k
+                fail = fail || !wait_warp(m, &m->full[ik], up);
                 unsigned char *tk = smem + ik * TILE;
 #pragma unroll 1
-                for (int i = gtid; i < (C - left) * 16; i += GROUP) {
+                for (int i = gtid; !fail && i < (C - left) * 16; i += GROUP) {
                     const int at = (i & 8 ? PANEL : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16;
                     *reinterpret_cast<uint4 *>(tv + at) = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4 *>(tk + at) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_shared();
+                if (named_bar_or(3, GROUP, fail)) return;
             }
-            if (!wait_warp(m, &m->decw[it & 1], (it >> 1) & 1)) return;
+            fail = fail || !wait_warp(m, &m->decw[it & 1], (it >> 1) & 1);
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
-                if (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1)) return;
+                fail = fail || (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1));
+                if (fail) break;
                 tc_fence_after();
                 const unsigned char *src = tv + row0 + st * (STAGE_ROWS * 128);
                 const int j0 = STAGE_ROWS * st + 16 * half;  // this thread's 16 tokens
@@ -497,7 +501,6 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                     for (int i = 0; i < 4; ++i) {  // the tile's swizzle: 16-byte piece ^ row % 8
                         const int r = 4 * j + i;
                         x[i] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(src + r * 128 + ((piece ^ (r & 7)) << 4))) << 16;
-                        if (j0 + r >= left) x[i] = 0;
                     }
                     const f2 y0 = mul2(pair(x[0], x[1]), pair(w.x, w.y)), y1 = mul2(pair(x[2], x[3]), pair(w.z, w.w));
                     hi[2 * j] = bf16_of(y0);
@@ -511,17 +514,72 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 tc_fence_before();
                 arrive_warp(&m->vt[st]);
             }
-            arrive_warp(&m->wfree[it & 1]);
+            if (!fail) arrive_warp(&m->wfree[it & 1]);
         }
     }
 }
 
-// ---- warps 0-7: decayed scores and the output. Two threads share a token row: key blocks 0 and 3 or 1 and 2 of the scores, one
-// half of the values of the output.
+// A chunk's output from tensor memory into the q tile, and out. The scores' and the state's warps share it: four threads a token
+// row, 32 values each (half, part). True: some warp has given up. (A warp that gives up still comes to the barriers.)
+__device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
+                                            int slot, int tid, int half, int part, bool fail) {
+    unsigned char *tile = smem + slot * TILE + half * PANEL;
+    const int left = t.len - c, lane = threadIdx.x & 31;
+    if (!fail) {
+        tc_fence_after();
+        const f2 s2 = pair(p.a.scale, p.a.scale);
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+            uint32_t o[16];
+            tmem_ld16(tmem_lanes + COL_O + 64 * half + 32 * part + 16 * b, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // the tile's swizzle: 16-byte piece ^ row % 8
+                const int i = 8 * j;
+                *reinterpret_cast<uint4 *>(tile + tid * 128 + (((4 * part + 2 * b + j) ^ (tid & 7)) << 4)) =
+                    make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
+                               bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
+            }
+        }
+        tc_fence_before();
+        arrive_warp(&m->ofree);
+    }
+    if (left < C) {  // rows behind the segment are not written
+        if (named_bar_or(1, 2 * GROUP, fail)) return true;
+#pragma unroll 1
+        for (int i = 128 * part + tid; i < left * 8; i += 256) {
+            const int r = i >> 3, j = i & 7;
+            *reinterpret_cast<uint4 *>(p.a.o + ((t.t0 + c + r) * p.a.H + t.h) * DV + 64 * half + 8 * j) =
+                *reinterpret_cast<const uint4 *>(tile + r * 128 + ((j ^ (r & 7)) << 4));
+        }
+    } else {
+        fence_proxy_async_shared();
+    }
+    // one warp stores a whole chunk's o and frees the tile; the others go on (none of them comes here again before that warp's
+    // scores of the next chunk)
+    if (threadIdx.x >> 5 != WARP_STORE) {
+        named_bar_arrive(2, 2 * GROUP);
+    } else {
+        named_bar_sync(2, 2 * GROUP);
+        if (lane == 0) {
+            if (left >= C && !fail) {
+                const unsigned char *src = smem + slot * TILE;
+                tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c), evict_first());
+                tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c), evict_first());
+                bulk_commit();
+                bulk_wait_read();
+            }
+            mbar_arrive(&m->empty[slot]);
+        }
+        __syncwarp();
+    }
+    return false;
+}
+
+// ---- warps 0-7: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
 template <bool SEG>
 __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
-    const Params &a = p.a;
     const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
     uint32_t it = 0;
@@ -534,13 +592,10 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            const int left = t.len - c;  // tokens from this chunk on
-            const int slot = slot_of(TV, it, states);
-            unsigned char *tile = smem + slot * TILE + half * PANEL;  // o goes where v was
             fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
             if (!fail) {
                 tc_fence_after();
-                const float pre = m->pre[tid], row = ex2(pre), entry = ex2(pre + m->start[warp]);
+                const float pre = m->pre[tid], row = ex2(pre);
                 // key blocks of 32: 0 and 3, or 1 and 2
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
@@ -577,79 +632,12 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                     }
                     tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
                 }
-                // q S by the row's decay since the chunk began; P v is added onto it
-                fail = !wait_warp(m, &m->qs, ph);
-                if (!fail) {
-                    tc_fence_after();
-                    const f2 e2 = pair(entry, entry);
-#pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t s[32];
-                        tmem_ld32(tmem + lanes + COL_O + 64 * half + 32 * b, s);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float x, y;
-                            split(mul2(e2, pair(s[2 * j], s[2 * j + 1])), x, y);
-                            s[2 * j] = __float_as_uint(x);
-                            s[2 * j + 1] = __float_as_uint(y);
-                        }
-                        tmem_st32(tmem + lanes + COL_O + 64 * half + 32 * b, s);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    arrive_warp(&m->p);
-                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(&m->p);
             }
             fail = fail || !wait_warp(m, &m->o, ph);
-            if (!fail) {
-                tc_fence_after();
-                const f2 s2 = pair(a.scale, a.scale);
-#pragma unroll 1
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t o[32];
-                    tmem_ld32(tmem + lanes + COL_O + 64 * half + 32 * b, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // the tile's swizzle: 16-byte piece ^ row % 8
-                        const int i = 8 * j;
-                        *reinterpret_cast<uint4 *>(tile + tid * 128 + (((4 * b + j) ^ (tid & 7)) << 4)) =
-                            make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
-                                       bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
-                    }
-                }
-                tc_fence_before();
-                arrive_warp(&m->ofree);
-            }
-            if (left < C) {  // rows behind the segment are not written
-                if (named_bar_or(1, GROUP, fail)) return;
-#pragma unroll 1
-                for (int i = tid; i < left * 8; i += 128) {
-                    const int r = i >> 3, j = i & 7;
-                    *reinterpret_cast<uint4 *>(a.o + ((t.t0 + c + r) * a.H + t.h) * DV + 64 * half + 8 * j) =
-                        *reinterpret_cast<const uint4 *>(tile + r * 128 + ((j ^ (r & 7)) << 4));
-                }
-            } else {
-                fence_proxy_async_shared();
-            }
-            // one warp stores a whole chunk's o and frees the tile; the others go on (none of them comes here again before
-            // that warp's scores of the next chunk)
-            if (threadIdx.x >> 5 != WARP_STORE) {
-                named_bar_arrive(2, GROUP);
-            } else {
-                named_bar_sync(2, GROUP);
-                if (lane == 0) {
-                    if (left >= C && !fail) {
-                        const unsigned char *src = smem + slot * TILE;
-                        tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c), evict_first());
-                        tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c), evict_first());
-                        bulk_commit();
-                        bulk_wait_read();
-                    }
-                    mbar_arrive(&m->empty[slot]);
-                }
-                __syncwarp();
-            }
+            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, fail)) return;
         }
     }
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
@@ -664,6 +652,7 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
+    bool fail = false;
     f2 S[NK / 2];
     const int tasks = tasks_of<SEG>(p);
 #pragma unroll 1
@@ -681,33 +670,66 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
 #pragma unroll
             for (int j = 0; j < NK / 2; ++j) S[j] = 0;
         }
+        auto publish = [&]() {  // the bf16 copy that q multiplies
+#pragma unroll
+            for (int j = 0; j < NK / 8; ++j)
+                *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) =
+                    make_uint4(bf16_of(S[4 * j]), bf16_of(S[4 * j + 1]), bf16_of(S[4 * j + 2]), bf16_of(S[4 * j + 3]));
+            fence_proxy_async_shared();
+            arrive_warp(&m->s);
+        };
+        if (!states && t.len > 0) publish();
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
-            if (!states) {  // the bf16 copy that q multiplies, once q has been multiplied by the last one
-                if (c > 0 && !wait_warp(m, &m->qs, (it - 1) & 1)) return;
+            const uint32_t ph = it & 1;
+            if (!states) {  // q S by the row's decay since the chunk began; P v is added onto it
+                fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qs, ph);
+                if (!fail) {
+                    tc_fence_after();
+                    const float entry = ex2(m->pre[tid] + m->start[warp]);
+                    const f2 e2 = pair(entry, entry);
+#pragma unroll 1
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t x[16];
+                        tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < NK / 8; ++j)
-                    *reinterpret_cast<uint4 *>(sS + ((j ^ (tid & 7)) << 4)) =
-                        make_uint4(bf16_of(S[4 * j]), bf16_of(S[4 * j + 1]), bf16_of(S[4 * j + 2]), bf16_of(S[4 * j + 3]));
-                fence_proxy_async_shared();
-                arrive_warp(&m->s);
+                        for (int j = 0; j < 8; ++j) {
+                            float y, z;
+                            split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
+                            x[2 * j] = __float_as_uint(y);
+                            x[2 * j + 1] = __float_as_uint(z);
+                        }
+                        tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive_warp(&m->p);
+                }
             }
-            if (!wait_warp(m, &m->u, it & 1)) return;
-            tc_fence_after();
-            const float dm1 = m->dm1[it & 3];
-            const f2 d2 = pair(dm1, dm1);
+            fail = fail || !wait_warp(m, &m->u, ph);
+            if (!fail) {
+                tc_fence_after();
+                const float dm1 = m->dm1[it & 3];
+                const f2 d2 = pair(dm1, dm1);
 #pragma unroll
-            for (int b = 0; b < NK / 32; ++b) {
-                uint32_t u[32];
-                tmem_ld32(tmem + lanes + COL_U + NK * half + 32 * b, u);
-                tmem_wait_ld();
+                for (int b = 0; b < NK / 16; ++b) {
+                    uint32_t u[16];
+                    tmem_ld16(tmem + lanes + COL_U + NK * half + 16 * b, u);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) S[16 * b + j] = add2(fma2(S[16 * b + j], d2, S[16 * b + j]), pair(u[2 * j], u[2 * j + 1]));
+                    for (int j = 0; j < 8; ++j) S[8 * b + j] = add2(fma2(S[8 * b + j], d2, S[8 * b + j]), pair(u[2 * j], u[2 * j + 1]));
+                }
+                tc_fence_before();
+                arrive_warp(&m->ufree);
+                if (!states && c + C < t.len) publish();  // (q S of this chunk is done)
             }
-            tc_fence_before();
-            arrive_warp(&m->ufree);
+            if (!states) {
+                fail = fail || !wait_warp(m, &m->o, ph);
+                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, fail)) return;
+            }
         }
-        if (!states && t.len > 0 && !wait_warp(m, &m->qs, (it - 1) & 1)) return;
+        if (fail) return;
         if (t.sout) {
 #pragma unroll
             for (int j = 0; j < NK / 2; ++j) {
@@ -807,10 +829,11 @@ __device__ __forceinline__ void touch_ahead(const ChunkParams &p) {
 
 constexpr int BARRIERS = offsetof(Misc, tmem) / sizeof(uint64_t);  // they come first in Misc
 __device__ __forceinline__ int arrivals_of(int i, bool states) {
-    constexpr int E0 = offsetof(Misc, empty) / 8, V0 = offsetof(Misc, vt) / 8, W0 = offsetof(Misc, wfree) / 8,
-                  F0 = offsetof(Misc, ufree) / 8;
+    constexpr int E0 = offsetof(Misc, empty) / 8, V0 = offsetof(Misc, vt) / 8, P0 = offsetof(Misc, p) / 8,
+                  W0 = offsetof(Misc, wfree) / 8, U0 = offsetof(Misc, ufree) / 8;
     if (i >= E0 && i < E0 + TILES) return !states && (i - E0) % 3 == TK ? 2 : 1;  // a k tile is read by q k^T and by U
-    return ((i >= V0 && i < V0 + STAGES + 2) || (i >= W0 && i < W0 + 2) || i >= F0) ? GROUP / 32 : 1;  // warps of a group
+    if (i == P0 || i == U0 + 1) return 2 * GROUP / 32;                              // warps of the scores' and the state's groups
+    return ((i >= V0 && i < P0) || (i >= W0 && i < W0 + 2) || i == U0) ? GROUP / 32 : 1;  // warps of one group
 }
 __device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // warp 0
     for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_init(reinterpret_cast<uint64_t *>(m) + i, arrivals_of(i, states));

@@ -92,6 +92,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+using kda::tmem_st16;
 // 16 columns from the first half of r
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
