@@ -47,7 +47,7 @@ constexpr int TILE = C * DK * 2;  // one 128 x 128 bf16 tile: two panels of 64 c
 constexpr int PANEL = TILE / 2;
 constexpr int TILES = 6;
 constexpr int OFF_S = TILES * TILE;   // bf16 copy of S: [value][key], two panels of 64 keys
-constexpr int STAGES = 4, STAGE_ROWS = C / STAGES;  // stages of a chunk's v~
+constexpr int STAGES = 2, STAGE_ROWS = C / STAGES;  // stages of a chunk's v~
 constexpr int OFF_MISC = OFF_S + TILE;
 
 struct ChunkParams {
@@ -69,14 +69,17 @@ struct Misc {
     uint64_t empty[TILES];            // a slot is free
     uint64_t qk, qs, u, o, vfree[STAGES];  // tensor core -> warps (commits)
     uint64_t decw[2], dect;           // decay tables written: w and dm1; tab, pre and start
-    uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled)
+    uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled, if need be)
     uint64_t wfree[2];                // w read
     uint64_t go;                      // the first g have been read
     uint64_t ufree, ofree;            // U read; O read
     uint32_t tmem;                    // address of the tensor memory
     int32_t abort;                    // a wait ran out
-    alignas(16) float tab[192];       // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
-    alignas(16) float pre[C];         // log2 prefix of j within its block of 32
+    int32_t easy, pad;                // this chunk's decay is above EASY
+    // slow chunks (EASY): tab[j] = 2^-(sum of g up to j), pre[j] = log2 sum of g up to j, start = 0; others: tab, for anchors
+    // 1..3 from tab_at(), 2^(sum of g after j up to the start of block a), j before it, and pre the log2 prefix within j's block
+    alignas(16) float tab[192];
+    alignas(16) float pre[C];
     alignas(16) float w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
     float start[4];                   // log2 sum of g up to the start of each block
     float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
@@ -104,6 +107,9 @@ template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+// A chunk whose whole decay is above 2^EASY needs no anchors: its scores are A_ij 2^-(sum of g up to j), at most 2^80 times
+// their size, and the row's 2^(sum of g up to i) is left to the output, so that q S and P v add up as they are.
+constexpr float EASY = -80.f;
 constexpr int GRID_POLLS = 1 << 24;
 constexpr int WAITS = 20000;  // waits of up to WAIT_NS each before a role gives up
 
@@ -266,18 +272,62 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
     }
 }
 
-// ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, with
-// everything that makes an address the same in all lanes, and one lane issues. (A 128 x 128 x 16 MMA runs 70 cycles; from one
-// warp the waits and descriptors between groups of four or eight cost as much again.)
+// ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, and one
+// lane issues. Tile addresses are constants, by the slot as a template argument: with addresses from registers an MMA takes 140
+// to 280 cycles to issue, with constants 61, and a 128 x 128 x 16 MMA runs 70.
+template <int SLOT>
+__device__ __forceinline__ void issue_qk(uint32_t base, Misc *m) {
+    const uint64_t q = desc_k(base + SLOT * TILE), k = desc_k(base + (SLOT + TK) * TILE);
+#pragma unroll
+    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(COL_QK, q + step_k(kk), k + step_k(kk), idesc_bf16(false, false, C, C), kk > 0);
+    umma_commit(&m->qk);
+    umma_commit(&m->empty[SLOT + TK]);
+}
+template <int SLOT>
+__device__ __forceinline__ void issue_qs(uint32_t base, Misc *m) {
+    const uint64_t q = desc_k(base + SLOT * TILE), s = desc_k(base + OFF_S);
+#pragma unroll
+    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(COL_O, q + step_k(kk), s + step_k(kk), idesc_bf16(false, false, C, DV), kk > 0);
+    umma_commit(&m->qs);
+}
+template <int SLOT>
+__device__ __forceinline__ void issue_pv(uint32_t base, Misc *m) {
+    const uint64_t v = desc_mn(base + (SLOT + TV) * TILE, PANEL);
+#pragma unroll
+    for (int kk = 0; kk < C / 16; ++kk)
+        umma_ts(COL_O, COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), idesc_bf16(false, true, C, DV), 1);
+    umma_commit(&m->o);
+    umma_commit(&m->empty[SLOT + TV]);
+}
+template <int SLOT, int ST>
+__device__ __forceinline__ void issue_u(uint32_t base, Misc *m) {
+    const uint64_t k = desc_mn(base + SLOT * TILE, PANEL) + step_mn(ST * STAGE_ROWS / 16);
+    constexpr uint32_t VT = COL_VT + ST * (STAGE_ROWS / 2), ID = idesc_bf16(false, true, DV, DK);
+#pragma unroll
+    for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
+        umma_ts(COL_U, VT + 8 * kk, k + step_mn(kk), ID, ST > 0 || kk > 0);
+        umma_ts(COL_U, VT + C / 2 + 8 * kk, k + step_mn(kk), ID, 1);
+    }
+    umma_commit(&m->vfree[ST]);
+}
+template <int ST>
+__device__ __forceinline__ void issue_u(uint32_t base, Misc *m, int slot) {  // a k tile's slot
+    if (slot == 2)
+        issue_u<2, ST>(base, m);
+    else if (slot == 5)
+        issue_u<5, ST>(base, m);
+    else if (slot == 1)
+        issue_u<1, ST>(base, m);
+    else
+        issue_u<3, ST>(base, m);
+}
+
 template <bool SEG>
-__device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+__device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m) {
     constexpr bool states = false;
-    constexpr uint32_t ID_KK = idesc_bf16(false, false, C, C), ID_PV = idesc_bf16(false, true, C, DV);
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
-    const uint64_t s = desc_k(base + OFF_S);
     const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
-    tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<SEG>(p, id, states);
@@ -285,47 +335,45 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
 #pragma unroll 1
         for (int c = 0; c < len; c += C, ++it) {
             const uint32_t ph = it & 1, up = use_of(it, states) & 1;
-            const int iq = slot_of(TQ, it, states), iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
-            const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
-            if (!wait_warp(m, &m->full[iq], up)) return;
-            if (!wait_warp(m, &m->full[ik], up)) return;
+            if (!wait_warp(m, &m->full[slot_of(TQ, it, states)], up)) return;
+            if (!wait_warp(m, &m->full[slot_of(TK, it, states)], up)) return;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_KK, kk > 0);
-                umma_commit(&m->qk);
-                umma_commit(&m->empty[ik]);
+                if (ph)
+                    issue_qk<3>(base, m);
+                else
+                    issue_qk<0>(base, m);
             }
+            __syncwarp();
             if (!wait_warp(m, &m->s, ph)) return;
             if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O, q + step_k(kk), s + step_k(kk), ID_KK, kk > 0);
-                umma_commit(&m->qs);
+                if (ph)
+                    issue_qs<3>(base, m);
+                else
+                    issue_qs<0>(base, m);
             }
-            // P v onto the scaled q S; after U: by then v~ has been made of v
-            const uint64_t v = desc_mn(base + iv * TILE, PANEL);
+            __syncwarp();
+            // P v onto q S; after U: by then v~ has been made of v
             if (!wait_warp(m, &m->u, ph)) return;
             if (!wait_warp(m, &m->p, ph)) return;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < C / 16; ++kk)
-                    umma_ts(tmem + COL_O, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), ID_PV, 1);
-                umma_commit(&m->o);
-                umma_commit(&m->empty[iv]);
+                if (ph)
+                    issue_pv<3>(base, m);
+                else
+                    issue_pv<0>(base, m);
             }
+            __syncwarp();
         }
     }
 }
 template <bool SEG>
-__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    constexpr uint32_t ID_U = idesc_bf16(false, true, DV, DK);
+__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, bool states) {
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
     const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
-    tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
     for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
         const Task t = task_of<SEG>(p, id, states);
@@ -333,35 +381,28 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
 #pragma unroll 1
         for (int c = 0; c < len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            const int iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
-            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
+            const int ik = slot_of(TK, it, states);
             if (!wait_warp(m, &m->full[ik], use_of(it, states) & 1)) return;
             if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
-#pragma unroll 1
-            for (int st = 0; st < STAGES; ++st) {
-                const uint64_t k = kt + st * step_mn(STAGE_ROWS / 16);
-                const uint32_t vt = tmem + COL_VT + st * (STAGE_ROWS / 2);
-                if (!wait_warp(m, &m->vt[st], ph)) return;
-                // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
-                if (!states && st == STAGES - 1 && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
-                        umma_ts(tmem + COL_U, vt + 8 * kk, k + step_mn(kk), ID_U, st > 0 || kk > 0);
-                        umma_ts(tmem + COL_U, vt + C / 2 + 8 * kk, k + step_mn(kk), ID_U, 1);
-                    }
-                    umma_commit(&m->vfree[st]);
-                    if (st == STAGES - 1) {
-                        umma_commit(&m->u);
-                        umma_commit(&m->empty[ik]);
-                        if (states) umma_commit(&m->empty[iv]);
-                    }
-                }
+            if (!wait_warp(m, &m->vt[0], ph)) return;
+            tc_fence_after();
+            if (elect_one()) issue_u<0>(base, m, ik);
+            __syncwarp();
+            if (!wait_warp(m, &m->vt[1], ph)) return;
+            // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
+            if (!states && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+            tc_fence_after();
+            if (elect_one()) {
+                issue_u<1>(base, m, ik);
+                umma_commit(&m->u);
+                umma_commit(&m->empty[ik]);
+                if (states) umma_commit(&m->empty[slot_of(TV, it, states)]);
             }
+            __syncwarp();
         }
     }
 }
+static_assert(STAGES == 2, "role_mma_state");
 
 // ---- one warp: decay tables. Lane l has tokens 4 l .. 4 l + 3, eight lanes a block of 32.
 template <bool SEG>
@@ -427,11 +468,22 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             arrive_warp(&m->decw[buf]);
             if (states) continue;
             if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
+            const bool easy = total > EASY;
+            if (easy) {
+                float from = before;  // this block's earlier lanes, then the blocks before it
+#pragma unroll
+                for (int b = 2; b >= 0; --b)
+                    if (b < block) from += tot[b];
+                *reinterpret_cast<float4 *>(&m->tab[4 * lane]) =
+                    make_float4(ex2(-pre[0] - from), ex2(-pre[1] - from), ex2(-pre[2] - from), ex2(-pre[3] - from));
+                before = from;
+            } else {
 #pragma unroll 1
-            for (int x = block + 1; x < 4; ++x) {
-                *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
-                    make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
-                after += x == 1 ? tot[1] : tot[2];
+                for (int x = block + 1; x < 4; ++x) {
+                    *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
+                        make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
+                    after += x == 1 ? tot[1] : tot[2];
+                }
             }
             *reinterpret_cast<float4 *>(&m->pre[4 * lane]) =
                 make_float4(pre[0] + before, pre[1] + before, pre[2] + before, pre[3] + before);
@@ -439,9 +491,10 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
                 float from = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    m->start[b] = from;
+                    m->start[b] = easy ? 0.f : from;
                     from += tot[b];
                 }
+                m->easy = easy;
             }
             arrive_warp(&m->dect);
         }
@@ -450,13 +503,16 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A thread has one value
-// channel (the lane of its warp's quarter) and every other 16 tokens.
+// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
+// (its quarter of the lanes) and 16 of every 32 tokens: ldmatrix transposes 8 x 8 blocks, and a tensor-memory store of the same
+// fragment shape puts each pair of tokens into its channel's lane.
 template <bool SEG>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    const int gtid = threadIdx.x & (GROUP - 1), half = gtid >> 7, ch = gtid & 127;
-    const uint32_t dst = tmem + (static_cast<uint32_t>(ch >> 5) << 21) + COL_VT + 8 * half;
-    const uint32_t row0 = (ch >> 6) * PANEL + half * 16 * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
+    const int gtid = threadIdx.x & (GROUP - 1), lane = gtid & 31, quad = (gtid >> 5) & 3, half = gtid >> 7;
+    const uint32_t dst = tmem + (static_cast<uint32_t>(quad) << 21) + COL_VT + 8 * half;
+    // this lane's row of the blocks: token lane % 8, channels 8 (lane / 8) .. of the quarter; swizzle: 16-byte piece ^ row % 8
+    const uint32_t row0 = (quad >> 1) * PANEL + (16 * half + (lane & 7)) * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);
+    const int pair0 = 16 * half + 2 * (lane & 3);  // the fragments' tokens
     const f2 minus = pair(-1.f, -1.f);
     bool fail = false;  // (a warp that gives up still comes to the barriers)
     uint32_t it = 0;
@@ -489,27 +545,28 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 fail = fail || (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1));
                 if (fail) break;
                 tc_fence_after();
-                const unsigned char *src = tv + row0 + st * (STAGE_ROWS * 128);
-                const int j0 = STAGE_ROWS * st + 16 * half;  // this thread's 16 tokens
-                const float4 *w4 = reinterpret_cast<const float4 *>(&m->w[it & 1][j0]);
-                uint32_t hi[8], lo[8];
+#pragma unroll 1
+                for (int t0 = STAGE_ROWS * st; t0 < STAGE_ROWS * (st + 1); t0 += 32) {
+                    uint32_t hi[8], lo[8];  // [8 tokens][8 channels]
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 w = w4[j];
-                    uint32_t x[4];
+                    for (int g = 0; g < 2; ++g) {
+                        uint32_t x[4];
+                        ldsm_x4_t(x, tv + row0 + t0 * 128 + g * 1024);
+                        const f2 w2 = *reinterpret_cast<const f2 *>(&m->w[it & 1][t0 + 8 * g + pair0]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // the tile's swizzle: 16-byte piece ^ row % 8
-                        const int r = 4 * j + i;
-                        x[i] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(src + r * 128 + ((piece ^ (r & 7)) << 4))) << 16;
+                        for (int i = 0; i < 4; ++i) {
+                            const f2 y = mul2(of_bf16(x[i]), w2);
+                            hi[4 * g + i] = bf16_of(y);
+                            lo[4 * g + i] = bf16_of(fma2(of_bf16(hi[4 * g + i]), minus, y));
+                        }
                     }
-                    const f2 y0 = mul2(pair(x[0], x[1]), pair(w.x, w.y)), y1 = mul2(pair(x[2], x[3]), pair(w.z, w.w));
-                    hi[2 * j] = bf16_of(y0);
-                    hi[2 * j + 1] = bf16_of(y1);
-                    lo[2 * j] = bf16_of(fma2(of_bf16(hi[2 * j]), minus, y0));
-                    lo[2 * j + 1] = bf16_of(fma2(of_bf16(hi[2 * j + 1]), minus, y1));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 16 lanes each
+                        const uint32_t at = dst + (h << 20) + t0 / 2;
+                        tmem_st_frag2(at, hi[2 * h], hi[2 * h + 1], hi[4 + 2 * h], hi[5 + 2 * h]);
+                        tmem_st_frag2(at + C / 2, lo[2 * h], lo[2 * h + 1], lo[4 + 2 * h], lo[5 + 2 * h]);
+                    }
                 }
-                tmem_st8(dst + st * (STAGE_ROWS / 2), hi);
-                tmem_st8(dst + st * (STAGE_ROWS / 2) + C / 2, lo);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&m->vt[st]);
@@ -522,12 +579,12 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
 // A chunk's output from tensor memory into the q tile, and out. The scores' and the state's warps share it: four threads a token
 // row, 32 values each (half, part). True: some warp has given up. (A warp that gives up still comes to the barriers.)
 __device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
-                                            int slot, int tid, int half, int part, bool fail) {
+                                            int slot, int tid, int half, int part, float factor, bool fail) {
     unsigned char *tile = smem + slot * TILE + half * PANEL;
     const int left = t.len - c, lane = threadIdx.x & 31;
     if (!fail) {
         tc_fence_after();
-        const f2 s2 = pair(p.a.scale, p.a.scale);
+        const f2 s2 = pair(factor, factor);
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
             uint32_t o[16];
@@ -593,51 +650,54 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
             fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
+            float out = 0.f;  // what the row's output is multiplied by
             if (!fail) {
                 tc_fence_after();
-                const float pre = m->pre[tid], row = ex2(pre);
-                // key blocks of 32: 0 and 3, or 1 and 2
+                const float pre = m->pre[tid];
+                const bool easy = m->easy;
+                out = p.a.scale * (easy ? ex2(pre) : 1.f);
+                const float row = easy ? 1.f : ex2(pre);
+                // key blocks of 32, half a block at a time: blocks 0 and 3, or 1 and 2 (small loop bodies: with six roles
+                // on it, a scheduler fetches most instructions it meets once a chunk from beyond its own cache)
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    const int b = i ? 3 - half : half;
-                    uint32_t s[32];
-                    if (b <= warp) tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
+                for (int i = 0; i < 4; ++i) {
+                    const int b = (i & 2) ? 3 - half : half, j0 = 32 * b + 16 * (i & 1);
+                    uint32_t s[16], x[8];
                     if (b > warp) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) s[j] = 0;
-                    } else if (b < warp) {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
-                        const f2 r2 = pair(row, row);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            s[2 * j] = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), mul2(r2, pair(w.x, w.y))));
-                            s[2 * j + 1] = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), mul2(r2, pair(w.z, w.w))));
-                        }
+                        for (int j = 0; j < 8; ++j) x[j] = 0;
                     } else {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
-                        tmem_wait_ld();
+                        tmem_ld16(tmem + lanes + COL_QK + j0, s);
+                        if (easy) {
+                            const f2 *f = reinterpret_cast<const f2 *>(&m->tab[j0]);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            // (selected, not multiplied by zero: a score behind the row, and its weight, may be anything)
-                            const float x = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
-                            const float y = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
-                            const float z = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
-                            const float q = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
-                            s[2 * j] = pack_bf16(x, y);
-                            s[2 * j + 1] = pack_bf16(z, q);
+                            for (int j = 0; j < 8; ++j) x[j] = bf16_of(mul2(pair(s[2 * j], s[2 * j + 1]), f[j]));
+                        } else {
+                            const bool near = b == warp;
+                            const float2 *f = reinterpret_cast<const float2 *>((near ? m->pre : m->tab + tab_at(warp)) + j0);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float2 w = f[j];
+                                w = near ? make_float2(ex2(pre - w.x), ex2(pre - w.y)) : make_float2(row * w.x, row * w.y);
+                                x[j] = bf16_of(mul2(pair(s[2 * j], s[2 * j + 1]), pair(w.x, w.y)));
+                            }
+                        }
+                        if (b == warp) {  // (cleared, not multiplied by zero: a score behind the row, and its weight, may be anything)
+                            const int see = lane + 1 - 16 * (i & 1);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) x[j] = 2 * j + 1 < see ? x[j] : 2 * j < see ? x[j] & 0xffffu : 0u;
                         }
                     }
-                    tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
+                    tmem_st8(tmem + lanes + COL_QK + 32 * b + 8 * (i & 1), x);  // over the scores they come from
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&m->p);
             }
             fail = fail || !wait_warp(m, &m->o, ph);
-            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, fail)) return;
+            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out, fail)) return;
         }
     }
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
@@ -682,28 +742,35 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            if (!states) {  // q S by the row's decay since the chunk began; P v is added onto it
-                fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qs, ph);
+            float out = a.scale;  // what the row's output is multiplied by
+            if (!states) {
+                fail = fail || !wait_warp(m, &m->dect, ph);
                 if (!fail) {
-                    tc_fence_after();
                     const float entry = ex2(m->pre[tid] + m->start[warp]);
-                    const f2 e2 = pair(entry, entry);
+                    if (m->easy) {
+                        out *= entry;
+                    } else if (wait_warp(m, &m->qs, ph)) {  // q S by the row's decay since the chunk began; P v is added onto it
+                        tc_fence_after();
+                        const f2 e2 = pair(entry, entry);
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t x[16];
-                        tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
-                        tmem_wait_ld();
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t x[16];
+                            tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float y, z;
-                            split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
-                            x[2 * j] = __float_as_uint(y);
-                            x[2 * j + 1] = __float_as_uint(z);
+                            for (int j = 0; j < 8; ++j) {
+                                float y, z;
+                                split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
+                                x[2 * j] = __float_as_uint(y);
+                                x[2 * j + 1] = __float_as_uint(z);
+                            }
+                            tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
                         }
-                        tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        tmem_wait_st();
+                        tc_fence_before();
+                    } else {
+                        fail = true;
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
                     arrive_warp(&m->p);
                 }
             }
@@ -722,11 +789,14 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
                 }
                 tc_fence_before();
                 arrive_warp(&m->ufree);
-                if (!states && c + C < t.len) publish();  // (q S of this chunk is done)
+                if (!states) {
+                    fail = !wait_warp(m, &m->qs, ph);  // q has been multiplied by the last copy
+                    if (!fail && c + C < t.len) publish();
+                }
             }
             if (!states) {
                 fail = fail || !wait_warp(m, &m->o, ph);
-                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, fail)) return;
+                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out, fail)) return;
             }
         }
         if (fail) return;
@@ -873,7 +943,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = m->tmem;
+    constexpr uint32_t tmem = 0;  // all 512 columns were allocated: they begin at column 0
     // every role: the pass over the states, the join, the pass over the outputs; or the last alone
     if (warp < 8) {
         if (SEGMENTS) touch_ahead(p);
@@ -902,9 +972,9 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
             } else if (warp == WARP_DECAY) {
                 role_decay<SEGMENTS>(p, m, states);
             } else if (warp == WARP_MMA_U) {
-                role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
+                role_mma_state<SEGMENTS>(p, smem, m, states);
             } else if (warp == WARP_MMA_OUT && !states) {
-                role_mma_out<SEGMENTS>(p, smem, m, tmem);
+                role_mma_out<SEGMENTS>(p, smem, m);
             }
             __syncwarp();
             if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
