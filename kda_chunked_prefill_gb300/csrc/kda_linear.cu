@@ -92,10 +92,10 @@ static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
 // tensor memory columns: q k^T, and P in the first half of each block's; the outputs; U; v~ (hi of 128 tokens, then lo)
 constexpr uint32_t COL_QK = 0, COL_O = 128, COL_U = 256, COL_VT = 384;
-// warps: 0-7 scores, 8-15 state, 16-23 v~, then one each
-constexpr int GROUP = 256;
-constexpr int WARP_LOAD = 24, WARP_DECAY = 25, WARP_MMA_OUT = 26, WARP_MMA_U = 27, THREADS = 896;
-constexpr int WARP_STORE = 4;  // of the scores' warps, the one with only masked scores
+// threads: four warps with a role each, then three groups of eight
+constexpr int WARP_LOAD = 0, WARP_DECAY = 1, WARP_MMA_OUT = 2, WARP_MMA_U = 3;
+constexpr int GROUP = 256, T_SCORES = 128, T_STATE = T_SCORES + GROUP, T_V = T_STATE + GROUP, THREADS = T_V + GROUP;
+constexpr int WARP_STORE = T_SCORES / 32 + 4;  // of the scores' warps, the one with only masked scores
 // Registers: 28 warps launch with 72; the roles' shares add up to no more.
 constexpr int REGS = 72, REGS_SCORES = 72, REGS_STATE = 104, REGS_V = 48, REGS_AUX = 56;
 static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 8 * REGS_V + 4 * REGS_AUX <= 28 * REGS, "the launch's registers");
@@ -503,12 +503,12 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
+// ---- eight warps: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
 // (its quarter of the lanes) and 16 of every 32 tokens: ldmatrix transposes 8 x 8 blocks, and a tensor-memory store of the same
 // fragment shape puts each pair of tokens into its channel's lane.
 template <bool SEG>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    const int gtid = threadIdx.x & (GROUP - 1), lane = gtid & 31, quad = (gtid >> 5) & 3, half = gtid >> 7;
+    const int gtid = threadIdx.x - T_V, lane = gtid & 31, quad = (gtid >> 5) & 3, half = gtid >> 7;
     const uint32_t dst = tmem + (static_cast<uint32_t>(quad) << 21) + COL_VT + 8 * half;
     // this lane's row of the blocks: token lane % 8, channels 8 (lane / 8) .. of the quarter; swizzle: 16-byte piece ^ row % 8
     const uint32_t row0 = (quad >> 1) * PANEL + (16 * half + (lane & 7)) * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);
@@ -633,11 +633,11 @@ __device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char 
     return false;
 }
 
-// ---- warps 0-7: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
+// ---- eight warps: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
 template <bool SEG>
 __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
-    const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+    const int half = (threadIdx.x - T_SCORES) >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
     uint32_t it = 0;
     bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
@@ -703,12 +703,12 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
 }
 
-// ---- warps 8-15: the state, transposed as U is. Two threads share a value column of S, one half of its keys each.
+// ---- eight warps: the state, transposed as U is. Two threads share a value column of S, one half of its keys each.
 template <bool SEG>
 __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
     constexpr int NK = DK / 2;
     const Params &a = p.a;
-    const int gtid = threadIdx.x - GROUP, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
+    const int gtid = threadIdx.x - T_STATE, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
@@ -878,7 +878,7 @@ __device__ __forceinline__ void touch(const void *p) {
     asm volatile("{\n\t.reg .b32 x;\n\tld.volatile.global.u32 x, [%0];\n\t}" ::"l"(p) : "memory");
 }
 __device__ __forceinline__ void touch_ahead(const ChunkParams &p) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x - T_SCORES;
     const int tasks = tasks_of<true>(p), id = blockIdx.x;
     constexpr size_t SZ = static_cast<size_t>(DK) * DV;
     if (id >= tasks) return;
@@ -917,7 +917,7 @@ __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
     cta_sync();
     if (LEADS && threadIdx.x == 0 && !grid_sync(p.num_segs + 1, gridDim.x)) m->abort = 1;
     cta_sync();
-    if (JOINS) join_states(p, threadIdx.x - GROUP);
+    if (JOINS) join_states(p, threadIdx.x - T_STATE);
     cta_sync();
     if (LEADS && threadIdx.x < 32) {
         for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
@@ -945,24 +945,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     tc_fence_after();
     constexpr uint32_t tmem = 0;  // all 512 columns were allocated: they begin at column 0
     // every role: the pass over the states, the join, the pass over the outputs; or the last alone
-    if (warp < 8) {
-        if (SEGMENTS) touch_ahead(p);
-        if (!SEGMENTS || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
-    } else if (warp < 16) {
-        more_registers<REGS_STATE>();
-#pragma unroll 1
-        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
-            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
-            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
-        }
-    } else if (warp < 24) {
-        fewer_registers<REGS_V>();
-#pragma unroll 1
-        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
-            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
-            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
-        }
-    } else {
+    if (threadIdx.x < T_SCORES) {
         fewer_registers<REGS_AUX>();
 #pragma unroll 1
         for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
@@ -977,6 +960,23 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
                 role_mma_out<SEGMENTS>(p, smem, m);
             }
             __syncwarp();
+            if (SEGMENTS && pass == 0 && !next_pass<true, false>(p, m)) break;
+        }
+    } else if (threadIdx.x < T_STATE) {
+        if (SEGMENTS) touch_ahead(p);
+        if (!SEGMENTS || next_pass<false, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
+    } else if (threadIdx.x < T_V) {
+        more_registers<REGS_STATE>();
+#pragma unroll 1
+        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
+            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
+        }
+    } else {
+        fewer_registers<REGS_V>();
+#pragma unroll 1
+        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
+            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
             if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
         }
     }
