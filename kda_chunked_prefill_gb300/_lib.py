@@ -7,6 +7,7 @@ missing or fails to load, these functions raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -61,6 +62,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
     """Load ``libkda.so``; raises ``OSError`` if it is absent (no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -491,68 +494,115 @@ def decode_fwd(q, k, v, g, beta, num_seqs: int, state=None, scale: Optional[floa
     return o, fs
 
 
+# ------------------------------------------------------------------ what the calls below share
+# A call's host time counts where its kernel takes a few microseconds: each tensor is checked by one expression (the detailed
+# message is made only when it fails), the current stream is read as a handle, and the device is switched only if it has to be.
+_BF16, _F32, _I32, _I8, _F8, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.float8_e4m3fn, torch.uint8)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _need(t, name, dtype, shape, index):
+    """``t`` is a contiguous tensor of this dtype and shape on CUDA device ``index``."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _check(t, name, dtype, shape, torch.device("cuda", index))
+
+
+def _device_of(t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("inputs must be CUDA tensors")
+    return index
+
+
+def _call(f, what, index, args, stream):
+    """Call a C entry point whose last argument is the stream, on device ``index``."""
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
+        rc = f(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, handle)
+    if rc != KDA_OK:
+        raise KdaError(rc, what)
+    return rc
+
+
+def _on(stream):
+    """Where a call's own tensors are allocated: on its stream."""
+    return _here if stream is None else torch.cuda.stream(stream)
+
+
+_here = contextlib.nullcontext()
+
+
+def _raise_device(status, stream, what):
+    if stream is not None:
+        stream.synchronize()
+    code = int(status.item())
+    if code != KDA_OK:
+        raise KdaError(code, f"{what} (device)")
+
+
+def _status(check, device):
+    return torch.empty(1, dtype=_I32, device=device) if check else None
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
 # ------------------------------------------------------------------ linear attention with one decay per head
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-
-
-def _on(t, name, device):
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-
-def _heads_view(t, name, tokens, device):
+def _heads_view(t, name, tokens, index):
     """Check a [T, heads, 128] bf16 tensor whose tokens may be strided (a slice
     of a wider projection); returns its token stride in elements."""
-    if t.dtype != _BF16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != tokens:
-        raise ValueError(f"{name} must have shape ({tokens}, heads, head_dim), got {tuple(t.shape)}")
-    _on(t, name, device)
-    heads, dim = t.shape[1], t.shape[2]
-    if tokens == 0:
-        return heads * dim
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens:
+        raise ValueError(f"{name} must have shape ({tokens}, heads, head_dim), got {tuple(shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on CUDA device {index}, got {t.device}")
+    width = shape[1] * shape[2]
+    if tokens == 0 or t.is_contiguous():
+        return width
     st, sh, sd = t.stride()
-    if sd != 1 or (sh != dim and heads > 1):
+    if sd != 1 or (sh != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must hold its heads and channels contiguously within a token")
     if tokens == 1:
-        return heads * dim
-    if st < heads * dim or st % 8:
+        return width
+    if st < width or st % 8:
         raise ValueError(f"{name}'s tokens must not overlap and lie a multiple of 8 elements apart")
     return st
 
 
 def _linear_args(q, k, v, g, o, initial_state, final_state, num_seqs, status):
     """The checks kda_linear_chunk_fwd and kda_linear_decode_fwd share."""
+    index = _device_of(q)
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must have shape (tokens, heads, head_dim)")
     T, Hk, D = q.shape
     H, V = v.shape[1], v.shape[2]
-    dev = q.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
-    strides = (_heads_view(q, "q", T, dev), _heads_view(k, "k", T, dev), _heads_view(v, "v", T, dev))
+    qs, ks, vs = _heads_view(q, "q", T, index), _heads_view(k, "k", T, index), _heads_view(v, "v", T, index)
     if k.shape != q.shape:
         raise ValueError(f"k must have q's shape {tuple(q.shape)}, got {tuple(k.shape)}")
     if Hk < 1 or H % Hk:
         raise ValueError(f"the number of value heads ({H}) must be a multiple of the query/key heads ({Hk})")
     per_token = g.dim() == 2
-    _check(g, "g", _F32, (T, H) if per_token else (H,), dev)
-    _check(o, "o", _BF16, (T, H, V), dev)
-    for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
-        if t is not None:
-            _check(t, name, _F32, (num_seqs, H, D, V), dev)
+    _need(g, "g", _F32, (T, H) if per_token else (H,), index)
+    _need(o, "o", _BF16, (T, H, V), index)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", _F32, (num_seqs, H, D, V), index)
+    if final_state is not None:
+        _need(final_state, "final_state", _F32, (num_seqs, H, D, V), index)
     if status is not None:
-        _check(status, "status", _I32, (1,), dev)
-    return T, H, Hk, D, V, dev, strides, int(per_token)
+        _need(status, "status", _I32, (1,), index)
+    return index, T, H, Hk, D, V, qs, ks, vs, int(per_token)
 
 
 def linear_workspace_size(num_seqs: int, total_tokens: int, num_heads: int) -> int:
     """Workspace bytes ``kda_linear_chunk_fwd`` needs on the current CUDA device (0: none)."""
     return int(load_library().kda_linear_chunk_fwd_workspace_size(int(num_seqs), int(total_tokens), int(num_heads)))
-
-
-def _raise(rc, what):
-    raise KdaError(rc, what)
 
 
 def kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale: float, o, final_state, status=None, stream=None,
@@ -568,42 +618,21 @@ def kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale: float, o,
     Raises ``KdaError`` on a host-side error; returns ``KDA_OK`` once queued.
     """
     N = cu_seqlens.shape[0] - 1
-    T, H, Hk, D, V, dev, (qs, ks, vs), per_token = _linear_args(q, k, v, g, o, initial_state, final_state, N, status)
-    _check(cu_seqlens, "cu_seqlens", _I32, (N + 1,), dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    index, T, H, Hk, D, V, qs, ks, vs, per_token = _linear_args(q, k, v, g, o, initial_state, final_state, N, status)
+    _need(cu_seqlens, "cu_seqlens", _I32, (N + 1,), index)
     lib = load_library()
-    with torch.cuda.device(dev):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(index) if _current_device() != index else _here:
             need = lib.kda_linear_chunk_fwd_workspace_size(N, T, H)
-            if need:
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-        rc = lib.kda_linear_chunk_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, D, V, qs, ks, vs,
-            per_token, _ptr(initial_state), scale, o.data_ptr(), _ptr(final_state), _ptr(status), _ptr(workspace),
-            0 if workspace is None else workspace.numel(), stream.cuda_stream)
-    if rc != KDA_OK:
-        _raise(rc, "kda_linear_chunk_fwd")
-    return rc
-
-
-def _new_on(stream, dev, *specs):
-    """Empty tensors for a call on ``stream`` (None: the current stream)."""
-    if stream is None:
-        return [None if s is None else torch.empty(s[0], dtype=s[1], device=dev) for s in specs]
-    with torch.cuda.stream(stream):
-        return [None if s is None else torch.empty(s[0], dtype=s[1], device=dev) for s in specs]
-
-
-def _raise_device(status, stream, what):
-    if stream is not None:
-        stream.synchronize()
-    code = int(status.item())
-    if code != KDA_OK:
-        raise KdaError(code, f"{what} (device)")
+        if need:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=_U8, device=q.device)
+    elif workspace.get_device() != index or workspace.dtype is not _U8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return _call(lib.kda_linear_chunk_fwd, "kda_linear_chunk_fwd", index,
+                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, D, V, qs, ks,
+                  vs, per_token, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
+                  0 if workspace is None else workspace.numel()), stream)
 
 
 def linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, scale: Optional[float] = None,
@@ -615,12 +644,14 @@ def linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, scale: Optional
     and a device-detected error raises ``KdaError``. Rows of ``o`` behind the last
     sequence are not written.
     """
-    dev, H, N = q.device, v.shape[1], cu_seqlens.shape[0] - 1
+    dev, shape = q.device, v.shape
     if scale is None:
         scale = q.shape[2] ** -0.5
-    o, fs, status = _new_on(stream, dev, (v.shape, _BF16),
-                            ((N, H, q.shape[2], v.shape[2]), _F32) if output_final_state else None,
-                            ((1,), _I32) if check else None)
+    with _on(stream):
+        o = torch.empty(shape, dtype=_BF16, device=dev)
+        fs = (torch.empty((cu_seqlens.shape[0] - 1, shape[1], q.shape[2], shape[2]), dtype=_F32, device=dev)
+              if output_final_state else None)
+        status = _status(check, dev)
     kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale, o, fs, status, stream)
     if check:
         _raise_device(status, stream, "kda_linear_chunk_fwd")
@@ -636,31 +667,26 @@ def kda_linear_decode_fwd(q, k, v, g, num_seqs: int, initial_state, scale: float
     T = q.shape[0]
     if N < 0 or (N == 0 and T != 0) or (N > 0 and T % N != 0):
         raise ValueError("q must hold the same number of tokens for every sequence")
-    T, H, Hk, D, V, dev, (qs, ks, vs), per_token = _linear_args(q, k, v, g, o, initial_state, final_state, N, status)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        rc = load_library().kda_linear_decode_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), N, T // N if N else 0, H, Hk, D, V, qs, ks, vs,
-            per_token, _ptr(initial_state), scale, o.data_ptr(), _ptr(final_state), _ptr(status), stream.cuda_stream)
-    if rc != KDA_OK:
-        _raise(rc, "kda_linear_decode_fwd")
-    return rc
+    index, T, H, Hk, D, V, qs, ks, vs, per_token = _linear_args(q, k, v, g, o, initial_state, final_state, N, status)
+    return _call(load_library().kda_linear_decode_fwd, "kda_linear_decode_fwd", index,
+                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), N, T // N if N else 0, H, Hk, D, V, qs, ks, vs,
+                  per_token, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status)), stream)
 
 
 def linear_decode_fwd(q, k, v, g, num_seqs: int, state=None, scale: Optional[float] = None, in_place: bool = False,
                       check: bool = False, stream=None):
     """Run ``kda_linear_decode_fwd``; returns ``(o, final_state)``. With
     ``in_place`` the given ``state`` tensor is updated and returned as ``final_state``."""
-    dev, H, N = q.device, v.shape[1], int(num_seqs)
+    dev, shape = q.device, v.shape
     if scale is None:
         scale = q.shape[2] ** -0.5
     if in_place and state is None:
         raise ValueError("in_place needs a state tensor")
-    o, fs, status = _new_on(stream, dev, (v.shape, _BF16),
-                            None if in_place else ((N, H, q.shape[2], v.shape[2]), _F32), ((1,), _I32) if check else None)
-    fs = state if in_place else fs
-    kda_linear_decode_fwd(q, k, v, g, N, state, scale, o, fs, status, stream)
+    with _on(stream):
+        o = torch.empty(shape, dtype=_BF16, device=dev)
+        fs = state if in_place else torch.empty((int(num_seqs), shape[1], q.shape[2], shape[2]), dtype=_F32, device=dev)
+        status = _status(check, dev)
+    kda_linear_decode_fwd(q, k, v, g, num_seqs, state, scale, o, fs, status, stream)
     if check:
         _raise_device(status, stream, "kda_linear_decode_fwd")
     return o, fs
@@ -668,54 +694,42 @@ def linear_decode_fwd(q, k, v, g, num_seqs: int, state=None, scale: Optional[flo
 
 # ------------------------------------------------------------------ the int8 cache of states
 def _cache_args(state, slots, codes, scales, status):
-    if state.dim() != 4:
+    index = _device_of(state)
+    shape = state.shape
+    if len(shape) != 4:
         raise ValueError("state must have shape (rows, heads, 128, 128)")
-    M, H, K, V = state.shape
-    dev = state.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
-    slots_n = codes.shape[0]
-    _check(state, "state", _F32, (M, H, K, V), dev)
-    _check(slots, "slots", _I32, (M,), dev)
-    _check(codes, "codes", torch.int8, (slots_n, H, K, V), dev)
-    _check(scales, "scales", _F32, (slots_n, H, K), dev)
+    M, H, K, V = shape
+    S = codes.shape[0]
+    _need(state, "state", _F32, shape, index)
+    _need(slots, "slots", _I32, (M,), index)
+    _need(codes, "codes", _I8, (S, H, K, V), index)
+    _need(scales, "scales", _F32, (S, H, K), index)
     if status is not None:
-        _check(status, "status", _I32, (1,), dev)
-    return M, H, K, V, slots_n, dev
+        _need(status, "status", _I32, (1,), index)
+    return index, M, H, K, V, S
 
 
 def kda_state_store(state, slots, codes, scales, status=None, stream=None) -> int:
     """Call the C entry point ``kda_state_store``: quantise state (fp32
     [M,H,128,128]) into the slots (int32 [M], -1: none) of the cache codes (int8
     [S,H,128,128]) and scales (fp32 [S,H,128])."""
-    M, H, K, V, S, dev = _cache_args(state, slots, codes, scales, status)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        rc = load_library().kda_state_store(state.data_ptr(), slots.data_ptr(), M, H, K, V, S, codes.data_ptr(),
-                                            scales.data_ptr(), _ptr(status), stream.cuda_stream)
-    if rc != KDA_OK:
-        _raise(rc, "kda_state_store")
-    return rc
+    index, M, H, K, V, S = _cache_args(state, slots, codes, scales, status)
+    return _call(load_library().kda_state_store, "kda_state_store", index,
+                 (state.data_ptr(), slots.data_ptr(), M, H, K, V, S, codes.data_ptr(), scales.data_ptr(), _p(status)), stream)
 
 
 def kda_state_load(codes, scales, slots, state, status=None, stream=None) -> int:
     """Call the C entry point ``kda_state_load``: read the slots of the cache
     back into ``state`` (a row with slot -1 becomes zeros)."""
-    M, H, K, V, S, dev = _cache_args(state, slots, codes, scales, status)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        rc = load_library().kda_state_load(codes.data_ptr(), scales.data_ptr(), slots.data_ptr(), M, H, K, V, S,
-                                           state.data_ptr(), _ptr(status), stream.cuda_stream)
-    if rc != KDA_OK:
-        _raise(rc, "kda_state_load")
-    return rc
+    index, M, H, K, V, S = _cache_args(state, slots, codes, scales, status)
+    return _call(load_library().kda_state_load, "kda_state_load", index,
+                 (codes.data_ptr(), scales.data_ptr(), slots.data_ptr(), M, H, K, V, S, state.data_ptr(), _p(status)), stream)
 
 
 def state_store(state, slots, codes, scales, check: bool = False, stream=None) -> None:
     """Run ``kda_state_store``; with ``check`` a bad slot raises ``KdaError``."""
-    status = _new_on(stream, state.device, ((1,), _I32))[0] if check else None
+    with _on(stream):
+        status = _status(check, state.device)
     kda_state_store(state, slots, codes, scales, status, stream)
     if check:
         _raise_device(status, stream, "kda_state_store")
@@ -723,7 +737,10 @@ def state_store(state, slots, codes, scales, check: bool = False, stream=None) -
 
 def state_load(codes, scales, slots, check: bool = False, stream=None):
     """Allocate the states fp32 [M,H,128,128] and run ``kda_state_load``."""
-    state, status = _new_on(stream, codes.device, ((slots.shape[0], *codes.shape[1:]), _F32), ((1,), _I32) if check else None)
+    dev = codes.device
+    with _on(stream):
+        state = torch.empty((slots.shape[0], *codes.shape[1:]), dtype=_F32, device=dev)
+        status = _status(check, dev)
     kda_state_load(codes, scales, slots, state, status, stream)
     if check:
         _raise_device(status, stream, "kda_state_load")
@@ -735,36 +752,30 @@ def kda_add_rms_norm(x, residual, weight, eps: float, residual_out, y, y_scale, 
     """Call the C entry point ``kda_add_rms_norm``: x bf16 [..., d]; residual and
     residual_out (may be the same tensor) bf16 or fp32 like x; weight fp32 [d];
     y float8_e4m3fn like x; y_scale fp32 [...]."""
-    if x.dim() < 1:
+    index, shape = _device_of(x), x.shape
+    if len(shape) < 1:
         raise ValueError("x must have at least one dimension")
-    shape, d = x.shape, x.shape[-1]
-    dev = x.device
-    if dev.type != "cuda":
-        raise ValueError("inputs must be CUDA tensors")
-    if residual.dtype not in (_BF16, _F32):
-        raise TypeError(f"residual must be {_BF16} or {_F32}, got {residual.dtype}")
-    _check(x, "x", _BF16, shape, dev)
-    _check(residual, "residual", residual.dtype, shape, dev)
-    _check(residual_out, "residual_out", residual.dtype, shape, dev)
-    _check(weight, "weight", _F32, (d,), dev)
-    _check(y, "y", torch.float8_e4m3fn, shape, dev)
-    _check(y_scale, "y_scale", _F32, shape[:-1], dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    with torch.cuda.device(dev):
-        rc = load_library().kda_add_rms_norm(x.data_ptr(), residual.data_ptr(), weight.data_ptr(), y_scale.numel(), d,
-                                             eps, int(residual.dtype == _F32), residual_out.data_ptr(), y.data_ptr(),
-                                             y_scale.data_ptr(), stream.cuda_stream)
-    if rc != KDA_OK:
-        _raise(rc, "kda_add_rms_norm")
-    return rc
+    kind = residual.dtype
+    if kind is not _BF16 and kind is not _F32:
+        raise TypeError(f"residual must be {_BF16} or {_F32}, got {kind}")
+    _need(x, "x", _BF16, shape, index)
+    _need(residual, "residual", kind, shape, index)
+    _need(residual_out, "residual_out", kind, shape, index)
+    _need(weight, "weight", _F32, shape[-1:], index)
+    _need(y, "y", _F8, shape, index)
+    _need(y_scale, "y_scale", _F32, shape[:-1], index)
+    return _call(load_library().kda_add_rms_norm, "kda_add_rms_norm", index,
+                 (x.data_ptr(), residual.data_ptr(), weight.data_ptr(), y_scale.numel(), shape[-1], eps,
+                  1 if kind is _F32 else 0, residual_out.data_ptr(), y.data_ptr(), y_scale.data_ptr()), stream)
 
 
 def add_rms_norm(x, residual, weight, eps: float = 1e-6, in_place: bool = False, stream=None):
     """Run ``kda_add_rms_norm``; returns ``(y, y_scale, residual_out)``. With
     ``in_place`` the given ``residual`` is updated and returned."""
-    y, y_scale, res = _new_on(stream, x.device, (x.shape, torch.float8_e4m3fn), (x.shape[:-1], _F32),
-                              None if in_place else (residual.shape, residual.dtype))
-    res = residual if in_place else res
+    dev, shape = x.device, x.shape
+    with _on(stream):
+        y = torch.empty(shape, dtype=_F8, device=dev)
+        y_scale = torch.empty(shape[:-1], dtype=_F32, device=dev)
+        res = residual if in_place else torch.empty_like(residual)
     kda_add_rms_norm(x, residual, weight, eps, res, y, y_scale, stream)
     return y, y_scale, res

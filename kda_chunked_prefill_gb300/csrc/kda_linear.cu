@@ -33,6 +33,8 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <atomic>
+
 #include "kda.h"
 #include "kda_linear.cuh"
 #include "kda_linear.h"
@@ -1080,25 +1082,40 @@ bool encode(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int heads, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int device() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) (void)cudaGetLastError();
+    return dev;
+}
+// SMs of the current device (0: no usable device); asked once for each of the first MAX_DEVICES
+constexpr int MAX_DEVICES = 64;
 int num_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    static std::atomic<int> known[MAX_DEVICES];
+    const int dev = device();
+    if (dev < 0) return 0;
+    int sms = dev < MAX_DEVICES ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
+    if (dev < MAX_DEVICES) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
 template <bool SEGMENTS>
 cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
     const auto kernel = kda_linear_chunk_kernel<SEGMENTS>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
-    static const int regs = [] {
+    static std::atomic<bool> ready[MAX_DEVICES];
+    const int dev = device();
+    if (dev < 0 || dev >= MAX_DEVICES || !ready[dev].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<SEGMENTS>) == cudaSuccess ? at.numRegs : 0;
-    }();
-    if (regs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
+        if (dev >= 0 && dev < MAX_DEVICES) ready[dev].store(true, std::memory_order_release);
+    }
     const int grid = static_cast<int>(most_tasks < sms ? most_tasks : sms);
     if (SEGMENTS) {
         void *args[] = {const_cast<ChunkParams *>(&p)};

@@ -113,7 +113,7 @@ def test_binding_refuses_cpu_tensors_and_bad_views():
         kda.state_load(torch.zeros(2, 1, 128, 128, dtype=torch.int8), torch.zeros(2, 1, 128), torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         kda.add_rms_norm(t, t, torch.ones(128))
-    cpu = torch.device("cpu")
+    cpu = t.get_device()
     assert _lib._heads_view(t, "q", 4, cpu) == 256
     assert _lib._heads_view(torch.zeros(4, 768, dtype=torch.bfloat16)[:, 256:512].view(4, 2, 128), "q", 4, cpu) == 768
     for bad in (t.transpose(0, 1).contiguous().transpose(0, 1), torch.zeros(4, 2, 256, dtype=torch.bfloat16)[:, :, ::2],
