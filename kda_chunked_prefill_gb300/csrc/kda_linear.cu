@@ -33,7 +33,7 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
-#include <atomic>
+#include <cmath>
 
 #include "kda.h"
 #include "kda_linear.cuh"
@@ -49,7 +49,7 @@ constexpr int TILE = C * DK * 2;  // one 128 x 128 bf16 tile: two panels of 64 c
 constexpr int PANEL = TILE / 2;
 constexpr int TILES = 6;
 constexpr int OFF_S = TILES * TILE;   // bf16 copy of S: [value][key], two panels of 64 keys
-constexpr int STAGES = 2, STAGE_ROWS = C / STAGES;  // stages of a chunk's v~
+constexpr int STAGES = 4, STAGE_ROWS = C / STAGES;  // stages of a chunk's v~
 constexpr int OFF_MISC = OFF_S + TILE;
 
 struct ChunkParams {
@@ -57,13 +57,15 @@ struct ChunkParams {
     CUtensorMap tq, tk, tv, to;
     int32_t tasks;  // WHOLE: (sequence, head) pairs
     // the rest only with segments (device memory in the workspace)
-    int32_t seg_chunks;
-    int32_t most_segs;  // that the workspace holds
-    int32_t *num_segs;  // and, behind it, the count of the launch's barrier
-    int2 *first;     // [N] first segment and number of segments
-    Segment *segs;
-    float *decays;   // [segment][head], minus one
-    float *states;   // [segment][head][128][128]
+    int32_t seg_chunks;  // shortest cut that the workspace is sized for
+    int32_t most_segs;   // that the workspace holds
+    int32_t sms;
+    int32_t *counts;     // [0] segments, [1] the launch's barrier, [2] segments of the pass over the states (0: nothing is cut)
+    int2 *first;         // [N] first slot and number of segments
+    Segment *segs;       // the segments, long ones first
+    Segment *segs_s;     // those of the pass over the states, long ones first
+    float *decays;       // [slot][head], minus one
+    float *states;       // [slot][head][128][128]
 };
 
 struct Misc {
@@ -71,17 +73,14 @@ struct Misc {
     uint64_t empty[TILES];            // a slot is free
     uint64_t qk, qs, u, o, vfree[STAGES];  // tensor core -> warps (commits)
     uint64_t decw[2], dect;           // decay tables written: w and dm1; tab, pre and start
-    uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled, if need be)
+    uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled)
     uint64_t wfree[2];                // w read
     uint64_t go;                      // the first g have been read
     uint64_t ufree, ofree;            // U read; O read
     uint32_t tmem;                    // address of the tensor memory
     int32_t abort;                    // a wait ran out
-    int32_t easy, pad;                // this chunk's decay is above EASY
-    // slow chunks (EASY): tab[j] = 2^-(sum of g up to j), pre[j] = log2 sum of g up to j, start = 0; others: tab, for anchors
-    // 1..3 from tab_at(), 2^(sum of g after j up to the start of block a), j before it, and pre the log2 prefix within j's block
-    alignas(16) float tab[192];
-    alignas(16) float pre[C];
+    alignas(16) float tab[192];       // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
+    alignas(16) float pre[C];         // log2 prefix of j within its block of 32
     alignas(16) float w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
     float start[4];                   // log2 sum of g up to the start of each block
     float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
@@ -94,10 +93,10 @@ static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
 // tensor memory columns: q k^T, and P in the first half of each block's; the outputs; U; v~ (hi of 128 tokens, then lo)
 constexpr uint32_t COL_QK = 0, COL_O = 128, COL_U = 256, COL_VT = 384;
-// threads: four warps with a role each, then three groups of eight
-constexpr int WARP_LOAD = 0, WARP_DECAY = 1, WARP_MMA_OUT = 2, WARP_MMA_U = 3;
-constexpr int GROUP = 256, T_SCORES = 128, T_STATE = T_SCORES + GROUP, T_V = T_STATE + GROUP, THREADS = T_V + GROUP;
-constexpr int WARP_STORE = T_SCORES / 32 + 4;  // of the scores' warps, the one with only masked scores
+// warps: 0-7 scores, 8-15 state, 16-23 v~, then one each
+constexpr int GROUP = 256;
+constexpr int WARP_LOAD = 24, WARP_DECAY = 25, WARP_MMA_OUT = 26, WARP_MMA_U = 27, THREADS = 896;
+constexpr int WARP_STORE = 4;  // of the scores' warps, the one with only masked scores
 // Registers: 28 warps launch with 72; the roles' shares add up to no more.
 constexpr int REGS = 72, REGS_SCORES = 72, REGS_STATE = 104, REGS_V = 48, REGS_AUX = 56;
 static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 8 * REGS_V + 4 * REGS_AUX <= 28 * REGS, "the launch's registers");
@@ -109,9 +108,6 @@ template <int N>
 __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
-// A chunk whose whole decay is above 2^EASY needs no anchors: its scores are A_ij 2^-(sum of g up to j), at most 2^80 times
-// their size, and the row's 2^(sum of g up to i) is left to the output, so that q S and P v add up as they are.
-constexpr float EASY = -80.f;
 constexpr int GRID_POLLS = 1 << 24;
 constexpr int WAITS = 20000;  // waits of up to WAIT_NS each before a role gives up
 
@@ -128,8 +124,14 @@ struct Task {
 // an SM's instruction cache holds about one copy of all roles, and a role's first run through cold code costs as much as
 // two chunks.
 template <bool SEG>
-__device__ __forceinline__ int tasks_of(const ChunkParams &p) {
-    return SEG ? *p.num_segs * p.a.H : p.tasks;
+__device__ __forceinline__ int tasks_of(const ChunkParams &p, bool states) {
+    return SEG ? p.counts[states ? 2 : 0] * p.a.H : p.tasks;
+}
+// The CTA's k-th task. Segments are sorted by length: back and forth over the CTAs, each gets about the same number of chunks.
+__device__ __forceinline__ int nth_task(int k, int cta, int ctas) { return k * ctas + (k & 1 ? ctas - 1 - cta : cta); }
+template <bool SEG>
+__device__ __forceinline__ int nth_task(int k) {
+    return SEG ? nth_task(k, blockIdx.x, gridDim.x) : k * gridDim.x + blockIdx.x;
 }
 
 template <bool SEG>
@@ -150,23 +152,23 @@ __device__ __forceinline__ Task task_of(const ChunkParams &p, int id, bool state
         t.sout = a.sT ? a.sT + at : nullptr;
         return t;
     }
-    const Segment sg = p.segs[seg];
+    const Segment sg = (states ? p.segs_s : p.segs)[seg];
     t.t0 = sg.t0;
     t.len = sg.len;
-    const size_t at = (static_cast<size_t>(sg.seq) * a.H + t.h) * SZ, ws = static_cast<size_t>(id) * SZ;
+    t.skip = false;
+    const int own = sg.slot * a.H + t.h;
+    const size_t at = (static_cast<size_t>(sg.seq) * a.H + t.h) * SZ, ws = static_cast<size_t>(own) * SZ;
     const bool last = sg.index == sg.count - 1;
     // With the states updated in place, a cut sequence's entry state is read by one
-    // CTA and overwritten by another: the last segment's slot, else unused, keeps it.
+    // CTA and overwritten by another: the last segment's slot, else unused, keeps it (a task without tokens).
     const bool keep = sg.count > 1 && a.s0 && a.s0 == a.sT;
     if (states) {
-        t.skip = last && !keep;
         if (last) t.len = 0;
         t.sin = (last || sg.index == 0) && a.s0 ? a.s0 + at : nullptr;
         t.sout = p.states + ws;
-        t.decay = p.decays + id;
+        t.decay = p.decays + own;
     } else {
         const size_t row = static_cast<size_t>(a.H) * SZ;
-        t.skip = false;
         t.sin = sg.index > 0 ? p.states + ws - row : keep ? p.states + ws + (sg.count - 1) * row : a.s0 ? a.s0 + at : nullptr;
         t.sout = last && a.sT ? a.sT + at : nullptr;
     }
@@ -225,9 +227,9 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
     const uint64_t policy = evict_first();
     uint32_t it = 0, part = 0;  // whole chunks issued, and which kinds of a chunk that was given up
     bool ok = true;
-    const int tasks = tasks_of<SEG>(p), first = states ? TV : TQ;
+    const int tasks = tasks_of<SEG>(p, states), first = states ? TV : TQ;
 #pragma unroll 1
-    for (int id = blockIdx.x; ok && id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; ok && (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
         const int hk = t.h / p.a.rep;
@@ -274,137 +276,102 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
     }
 }
 
-// ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, and one
-// lane issues. Tile addresses are constants, by the slot as a template argument: with addresses from registers an MMA takes 140
-// to 280 cycles to issue, with constants 61, and a 128 x 128 x 16 MMA runs 70.
-template <int SLOT>
-__device__ __forceinline__ void issue_qk(uint32_t base, Misc *m) {
-    const uint64_t q = desc_k(base + SLOT * TILE), k = desc_k(base + (SLOT + TK) * TILE);
-#pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(COL_QK, q + step_k(kk), k + step_k(kk), idesc_bf16(false, false, C, C), kk > 0);
-    umma_commit(&m->qk);
-    umma_commit(&m->empty[SLOT + TK]);
-}
-template <int SLOT>
-__device__ __forceinline__ void issue_qs(uint32_t base, Misc *m) {
-    const uint64_t q = desc_k(base + SLOT * TILE), s = desc_k(base + OFF_S);
-#pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) umma_f16(COL_O, q + step_k(kk), s + step_k(kk), idesc_bf16(false, false, C, DV), kk > 0);
-    umma_commit(&m->qs);
-}
-template <int SLOT>
-__device__ __forceinline__ void issue_pv(uint32_t base, Misc *m) {
-    const uint64_t v = desc_mn(base + (SLOT + TV) * TILE, PANEL);
-#pragma unroll
-    for (int kk = 0; kk < C / 16; ++kk)
-        umma_ts(COL_O, COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), idesc_bf16(false, true, C, DV), 1);
-    umma_commit(&m->o);
-    umma_commit(&m->empty[SLOT + TV]);
-}
-template <int SLOT, int ST>
-__device__ __forceinline__ void issue_u(uint32_t base, Misc *m) {
-    const uint64_t k = desc_mn(base + SLOT * TILE, PANEL) + step_mn(ST * STAGE_ROWS / 16);
-    constexpr uint32_t VT = COL_VT + ST * (STAGE_ROWS / 2), ID = idesc_bf16(false, true, DV, DK);
-#pragma unroll
-    for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
-        umma_ts(COL_U, VT + 8 * kk, k + step_mn(kk), ID, ST > 0 || kk > 0);
-        umma_ts(COL_U, VT + C / 2 + 8 * kk, k + step_mn(kk), ID, 1);
-    }
-    umma_commit(&m->vfree[ST]);
-}
-template <int ST>
-__device__ __forceinline__ void issue_u(uint32_t base, Misc *m, int slot) {  // a k tile's slot
-    if (slot == 2)
-        issue_u<2, ST>(base, m);
-    else if (slot == 5)
-        issue_u<5, ST>(base, m);
-    else if (slot == 1)
-        issue_u<1, ST>(base, m);
-    else
-        issue_u<3, ST>(base, m);
-}
-
+// ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, with
+// everything that makes an address the same in all lanes, and one lane issues. (A 128 x 128 x 16 MMA runs 70 cycles; from one
+// warp the waits and descriptors between groups of four or eight cost as much again.)
 template <bool SEG>
-__device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m) {
+__device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
+    constexpr uint32_t ID_KK = idesc_bf16(false, false, C, C), ID_PV = idesc_bf16(false, true, C, DV);
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
-    const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
+    const uint64_t s = desc_k(base + OFF_S);
+    const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p, states), 0);
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
         for (int c = 0; c < len; c += C, ++it) {
             const uint32_t ph = it & 1, up = use_of(it, states) & 1;
-            if (!wait_warp(m, &m->full[slot_of(TQ, it, states)], up)) return;
-            if (!wait_warp(m, &m->full[slot_of(TK, it, states)], up)) return;
+            const int iq = slot_of(TQ, it, states), iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
+            const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
+            if (!wait_warp(m, &m->full[iq], up)) return;
+            if (!wait_warp(m, &m->full[ik], up)) return;
             tc_fence_after();
             if (elect_one()) {
-                if (ph)
-                    issue_qk<3>(base, m);
-                else
-                    issue_qk<0>(base, m);
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_QK, q + step_k(kk), k + step_k(kk), ID_KK, kk > 0);
+                umma_commit(&m->qk);
+                umma_commit(&m->empty[ik]);
             }
-            __syncwarp();
             if (!wait_warp(m, &m->s, ph)) return;
             if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
             tc_fence_after();
             if (elect_one()) {
-                if (ph)
-                    issue_qs<3>(base, m);
-                else
-                    issue_qs<0>(base, m);
+#pragma unroll
+                for (int kk = 0; kk < DK / 16; ++kk) umma_f16(tmem + COL_O, q + step_k(kk), s + step_k(kk), ID_KK, kk > 0);
+                umma_commit(&m->qs);
             }
-            __syncwarp();
-            // P v onto q S; after U: by then v~ has been made of v
+            // P v onto the scaled q S; after U: by then v~ has been made of v
+            const uint64_t v = desc_mn(base + iv * TILE, PANEL);
             if (!wait_warp(m, &m->u, ph)) return;
             if (!wait_warp(m, &m->p, ph)) return;
             tc_fence_after();
             if (elect_one()) {
-                if (ph)
-                    issue_pv<3>(base, m);
-                else
-                    issue_pv<0>(base, m);
+#pragma unroll
+                for (int kk = 0; kk < C / 16; ++kk)
+                    umma_ts(tmem + COL_O, tmem + COL_QK + 32 * (kk >> 1) + 8 * (kk & 1), v + step_mn(kk), ID_PV, 1);
+                umma_commit(&m->o);
+                umma_commit(&m->empty[iv]);
             }
-            __syncwarp();
         }
     }
 }
 template <bool SEG>
-__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, bool states) {
+__device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
+    constexpr uint32_t ID_U = idesc_bf16(false, true, DV, DK);
     uint32_t it = 0;
     const uint32_t base = smem_u32(smem);
-    const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p), 0);
+    const int tasks = __shfl_sync(0xffffffffu, tasks_of<SEG>(p, states), 0);
+    tmem = __shfl_sync(0xffffffffu, tmem, 0);
 #pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         const int len = __shfl_sync(0xffffffffu, t.skip ? 0 : t.len, 0);
 #pragma unroll 1
         for (int c = 0; c < len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            const int ik = slot_of(TK, it, states);
+            const int iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
+            const uint64_t kt = desc_mn(base + ik * TILE, PANEL);
             if (!wait_warp(m, &m->full[ik], use_of(it, states) & 1)) return;
             if (it > 0 && !wait_warp(m, &m->ufree, ph ^ 1)) return;
-            if (!wait_warp(m, &m->vt[0], ph)) return;
-            tc_fence_after();
-            if (elect_one()) issue_u<0>(base, m, ik);
-            __syncwarp();
-            if (!wait_warp(m, &m->vt[1], ph)) return;
-            // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
-            if (!states && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
-            tc_fence_after();
-            if (elect_one()) {
-                issue_u<1>(base, m, ik);
-                umma_commit(&m->u);
-                umma_commit(&m->empty[ik]);
-                if (states) umma_commit(&m->empty[slot_of(TV, it, states)]);
+#pragma unroll 1
+            for (int st = 0; st < STAGES; ++st) {
+                const uint64_t k = kt + st * step_mn(STAGE_ROWS / 16);
+                const uint32_t vt = tmem + COL_VT + st * (STAGE_ROWS / 2);
+                if (!wait_warp(m, &m->vt[st], ph)) return;
+                // U is not complete before the last chunk's output is read: nobody that waits for u is a phase late
+                if (!states && st == STAGES - 1 && it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < STAGE_ROWS / 16; ++kk) {
+                        umma_ts(tmem + COL_U, vt + 8 * kk, k + step_mn(kk), ID_U, st > 0 || kk > 0);
+                        umma_ts(tmem + COL_U, vt + C / 2 + 8 * kk, k + step_mn(kk), ID_U, 1);
+                    }
+                    umma_commit(&m->vfree[st]);
+                    if (st == STAGES - 1) {
+                        umma_commit(&m->u);
+                        umma_commit(&m->empty[ik]);
+                        if (states) umma_commit(&m->empty[iv]);
+                    }
+                }
             }
-            __syncwarp();
         }
     }
 }
-static_assert(STAGES == 2, "role_mma_state");
 
 // ---- one warp: decay tables. Lane l has tokens 4 l .. 4 l + 3, eight lanes a block of 32.
 template <bool SEG>
@@ -413,9 +380,9 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     const int lane = threadIdx.x & 31, in = lane & 7, block = lane >> 3;
     uint32_t it = 0;
     bool bad = false;
-    const int tasks = tasks_of<SEG>(p);
+    const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
         float raw[4], sum = 0.f;
@@ -470,22 +437,11 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             arrive_warp(&m->decw[buf]);
             if (states) continue;
             if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
-            const bool easy = total > EASY;
-            if (easy) {
-                float from = before;  // this block's earlier lanes, then the blocks before it
-#pragma unroll
-                for (int b = 2; b >= 0; --b)
-                    if (b < block) from += tot[b];
-                *reinterpret_cast<float4 *>(&m->tab[4 * lane]) =
-                    make_float4(ex2(-pre[0] - from), ex2(-pre[1] - from), ex2(-pre[2] - from), ex2(-pre[3] - from));
-                before = from;
-            } else {
 #pragma unroll 1
-                for (int x = block + 1; x < 4; ++x) {
-                    *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
-                        make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
-                    after += x == 1 ? tot[1] : tot[2];
-                }
+            for (int x = block + 1; x < 4; ++x) {
+                *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
+                    make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
+                after += x == 1 ? tot[1] : tot[2];
             }
             *reinterpret_cast<float4 *>(&m->pre[4 * lane]) =
                 make_float4(pre[0] + before, pre[1] + before, pre[2] + before, pre[3] + before);
@@ -493,10 +449,9 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
                 float from = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    m->start[b] = easy ? 0.f : from;
+                    m->start[b] = from;
                     from += tot[b];
                 }
-                m->easy = easy;
             }
             arrive_warp(&m->dect);
         }
@@ -505,22 +460,19 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- eight warps: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
-// (its quarter of the lanes) and 16 of every 32 tokens: ldmatrix transposes 8 x 8 blocks, and a tensor-memory store of the same
-// fragment shape puts each pair of tokens into its channel's lane.
+// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A thread has one value
+// channel (the lane of its warp's quarter) and every other 16 tokens.
 template <bool SEG>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    const int gtid = threadIdx.x - T_V, lane = gtid & 31, quad = (gtid >> 5) & 3, half = gtid >> 7;
-    const uint32_t dst = tmem + (static_cast<uint32_t>(quad) << 21) + COL_VT + 8 * half;
-    // this lane's row of the blocks: token lane % 8, channels 8 (lane / 8) .. of the quarter; swizzle: 16-byte piece ^ row % 8
-    const uint32_t row0 = (quad >> 1) * PANEL + (16 * half + (lane & 7)) * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);
-    const int pair0 = 16 * half + 2 * (lane & 3);  // the fragments' tokens
+    const int gtid = threadIdx.x & (GROUP - 1), half = gtid >> 7, ch = gtid & 127;
+    const uint32_t dst = tmem + (static_cast<uint32_t>(ch >> 5) << 21) + COL_VT + 8 * half;
+    const uint32_t row0 = (ch >> 6) * PANEL + half * 16 * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
     const f2 minus = pair(-1.f, -1.f);
     bool fail = false;  // (a warp that gives up still comes to the barriers)
     uint32_t it = 0;
-    const int tasks = tasks_of<SEG>(p);
+    const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
 #pragma unroll 1
@@ -547,28 +499,27 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 fail = fail || (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1));
                 if (fail) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int t0 = STAGE_ROWS * st; t0 < STAGE_ROWS * (st + 1); t0 += 32) {
-                    uint32_t hi[8], lo[8];  // [8 tokens][8 channels]
+                const unsigned char *src = tv + row0 + st * (STAGE_ROWS * 128);
+                const int j0 = STAGE_ROWS * st + 16 * half;  // this thread's 16 tokens
+                const float4 *w4 = reinterpret_cast<const float4 *>(&m->w[it & 1][j0]);
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        uint32_t x[4];
-                        ldsm_x4_t(x, tv + row0 + t0 * 128 + g * 1024);
-                        const f2 w2 = *reinterpret_cast<const f2 *>(&m->w[it & 1][t0 + 8 * g + pair0]);
+                for (int j = 0; j < 4; ++j) {
+                    const float4 w = w4[j];
+                    uint32_t x[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const f2 y = mul2(of_bf16(x[i]), w2);
-                            hi[4 * g + i] = bf16_of(y);
-                            lo[4 * g + i] = bf16_of(fma2(of_bf16(hi[4 * g + i]), minus, y));
-                        }
+                    for (int i = 0; i < 4; ++i) {  // the tile's swizzle: 16-byte piece ^ row % 8
+                        const int r = 4 * j + i;
+                        x[i] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(src + r * 128 + ((piece ^ (r & 7)) << 4))) << 16;
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // 16 lanes each
-                        const uint32_t at = dst + (h << 20) + t0 / 2;
-                        tmem_st_frag2(at, hi[2 * h], hi[2 * h + 1], hi[4 + 2 * h], hi[5 + 2 * h]);
-                        tmem_st_frag2(at + C / 2, lo[2 * h], lo[2 * h + 1], lo[4 + 2 * h], lo[5 + 2 * h]);
-                    }
+                    const f2 y0 = mul2(pair(x[0], x[1]), pair(w.x, w.y)), y1 = mul2(pair(x[2], x[3]), pair(w.z, w.w));
+                    hi[2 * j] = bf16_of(y0);
+                    hi[2 * j + 1] = bf16_of(y1);
+                    lo[2 * j] = bf16_of(fma2(of_bf16(hi[2 * j]), minus, y0));
+                    lo[2 * j + 1] = bf16_of(fma2(of_bf16(hi[2 * j + 1]), minus, y1));
                 }
+                tmem_st8(dst + st * (STAGE_ROWS / 2), hi);
+                tmem_st8(dst + st * (STAGE_ROWS / 2) + C / 2, lo);
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&m->vt[st]);
@@ -581,12 +532,12 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
 // A chunk's output from tensor memory into the q tile, and out. The scores' and the state's warps share it: four threads a token
 // row, 32 values each (half, part). True: some warp has given up. (A warp that gives up still comes to the barriers.)
 __device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
-                                            int slot, int tid, int half, int part, float factor, bool fail) {
+                                            int slot, int tid, int half, int part, bool fail) {
     unsigned char *tile = smem + slot * TILE + half * PANEL;
     const int left = t.len - c, lane = threadIdx.x & 31;
     if (!fail) {
         tc_fence_after();
-        const f2 s2 = pair(factor, factor);
+        const f2 s2 = pair(p.a.scale, p.a.scale);
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
             uint32_t o[16];
@@ -635,90 +586,87 @@ __device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char 
     return false;
 }
 
-// ---- eight warps: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
+// ---- warps 0-7: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
 template <bool SEG>
 __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
-    const int half = (threadIdx.x - T_SCORES) >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+    const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
     uint32_t it = 0;
     bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
-    const int tasks = tasks_of<SEG>(p);
+    const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
             fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
-            float out = 0.f;  // what the row's output is multiplied by
             if (!fail) {
                 tc_fence_after();
-                const float pre = m->pre[tid];
-                const bool easy = m->easy;
-                out = p.a.scale * (easy ? ex2(pre) : 1.f);
-                const float row = easy ? 1.f : ex2(pre);
-                // key blocks of 32, half a block at a time: blocks 0 and 3, or 1 and 2 (small loop bodies: with six roles
-                // on it, a scheduler fetches most instructions it meets once a chunk from beyond its own cache)
+                const float pre = m->pre[tid], row = ex2(pre);
+                // key blocks of 32: 0 and 3, or 1 and 2
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int b = (i & 2) ? 3 - half : half, j0 = 32 * b + 16 * (i & 1);
-                    uint32_t s[16], x[8];
+                for (int i = 0; i < 2; ++i) {
+                    const int b = i ? 3 - half : half;
+                    uint32_t s[32];
+                    if (b <= warp) tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
                     if (b > warp) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[j] = 0;
-                    } else {
-                        tmem_ld16(tmem + lanes + COL_QK + j0, s);
-                        if (easy) {
-                            const f2 *f = reinterpret_cast<const f2 *>(&m->tab[j0]);
-                            tmem_wait_ld();
+                        for (int j = 0; j < 16; ++j) s[j] = 0;
+                    } else if (b < warp) {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
+                        const f2 r2 = pair(row, row);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) x[j] = bf16_of(mul2(pair(s[2 * j], s[2 * j + 1]), f[j]));
-                        } else {
-                            const bool near = b == warp;
-                            const float2 *f = reinterpret_cast<const float2 *>((near ? m->pre : m->tab + tab_at(warp)) + j0);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float2 w = f[j];
-                                w = near ? make_float2(ex2(pre - w.x), ex2(pre - w.y)) : make_float2(row * w.x, row * w.y);
-                                x[j] = bf16_of(mul2(pair(s[2 * j], s[2 * j + 1]), pair(w.x, w.y)));
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
+                            s[2 * j] = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), mul2(r2, pair(w.x, w.y))));
+                            s[2 * j + 1] = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), mul2(r2, pair(w.z, w.w))));
                         }
-                        if (b == warp) {  // (cleared, not multiplied by zero: a score behind the row, and its weight, may be anything)
-                            const int see = lane + 1 - 16 * (i & 1);
+                    } else {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) x[j] = 2 * j + 1 < see ? x[j] : 2 * j < see ? x[j] & 0xffffu : 0u;
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
+                            // (selected, not multiplied by zero: a score behind the row, and its weight, may be anything)
+                            const float x = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
+                            const float y = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
+                            const float z = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
+                            const float q = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
+                            s[2 * j] = pack_bf16(x, y);
+                            s[2 * j + 1] = pack_bf16(z, q);
                         }
                     }
-                    tmem_st8(tmem + lanes + COL_QK + 32 * b + 8 * (i & 1), x);  // over the scores they come from
+                    tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&m->p);
             }
             fail = fail || !wait_warp(m, &m->o, ph);
-            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out, fail)) return;
+            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, fail)) return;
         }
     }
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
 }
 
-// ---- eight warps: the state, transposed as U is. Two threads share a value column of S, one half of its keys each.
+// ---- warps 8-15: the state, transposed as U is. Two threads share a value column of S, one half of its keys each.
 template <bool SEG>
 __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
     constexpr int NK = DK / 2;
     const Params &a = p.a;
-    const int gtid = threadIdx.x - T_STATE, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
+    const int gtid = threadIdx.x - GROUP, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
     bool fail = false;
     f2 S[NK / 2];
-    const int tasks = tasks_of<SEG>(p);
+    const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
-    for (int id = blockIdx.x; id < tasks; id += gridDim.x) {
+    for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) {
             if (!SEG && gtid == 0 && t.h == 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
@@ -744,35 +692,28 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            float out = a.scale;  // what the row's output is multiplied by
-            if (!states) {
-                fail = fail || !wait_warp(m, &m->dect, ph);
+            if (!states) {  // q S by the row's decay since the chunk began; P v is added onto it
+                fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qs, ph);
                 if (!fail) {
+                    tc_fence_after();
                     const float entry = ex2(m->pre[tid] + m->start[warp]);
-                    if (m->easy) {
-                        out *= entry;
-                    } else if (wait_warp(m, &m->qs, ph)) {  // q S by the row's decay since the chunk began; P v is added onto it
-                        tc_fence_after();
-                        const f2 e2 = pair(entry, entry);
+                    const f2 e2 = pair(entry, entry);
 #pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            uint32_t x[16];
-                            tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
-                            tmem_wait_ld();
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t x[16];
+                        tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float y, z;
-                                split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
-                                x[2 * j] = __float_as_uint(y);
-                                x[2 * j + 1] = __float_as_uint(z);
-                            }
-                            tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        for (int j = 0; j < 8; ++j) {
+                            float y, z;
+                            split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
+                            x[2 * j] = __float_as_uint(y);
+                            x[2 * j + 1] = __float_as_uint(z);
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                    } else {
-                        fail = true;
+                        tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
                     }
+                    tmem_wait_st();
+                    tc_fence_before();
                     arrive_warp(&m->p);
                 }
             }
@@ -791,14 +732,11 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
                 }
                 tc_fence_before();
                 arrive_warp(&m->ufree);
-                if (!states) {
-                    fail = !wait_warp(m, &m->qs, ph);  // q has been multiplied by the last copy
-                    if (!fail && c + C < t.len) publish();
-                }
+                if (!states && c + C < t.len) publish();  // (q S of this chunk is done)
             }
             if (!states) {
                 fail = fail || !wait_warp(m, &m->o, ph);
-                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out, fail)) return;
+                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, fail)) return;
             }
         }
         if (fail) return;
@@ -880,8 +818,8 @@ __device__ __forceinline__ void touch(const void *p) {
     asm volatile("{\n\t.reg .b32 x;\n\tld.volatile.global.u32 x, [%0];\n\t}" ::"l"(p) : "memory");
 }
 __device__ __forceinline__ void touch_ahead(const ChunkParams &p) {
-    const int tid = threadIdx.x - T_SCORES;
-    const int tasks = tasks_of<true>(p), id = blockIdx.x;
+    const int tid = threadIdx.x;
+    const int tasks = tasks_of<true>(p, false), id = blockIdx.x;
     constexpr size_t SZ = static_cast<size_t>(DK) * DV;
     if (id >= tasks) return;
     const Task t = task_of<true>(p, id, false);
@@ -917,15 +855,15 @@ __device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // warp 0
 template <bool LEADS, bool JOINS>
 __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
     cta_sync();
-    if (LEADS && threadIdx.x == 0 && !grid_sync(p.num_segs + 1, gridDim.x)) m->abort = 1;
+    if (LEADS && threadIdx.x == 0 && !grid_sync(p.counts + 1, gridDim.x)) m->abort = 1;
     cta_sync();
-    if (JOINS) join_states(p, threadIdx.x - T_STATE);
+    if (JOINS) join_states(p, threadIdx.x - GROUP);
     cta_sync();
     if (LEADS && threadIdx.x < 32) {
         for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
         init_barriers(m, false);
         __syncwarp();
-        if (threadIdx.x == 0 && !grid_sync(p.num_segs + 1, 2 * gridDim.x)) m->abort = 1;
+        if (threadIdx.x == 0 && !grid_sync(p.counts + 1, 2 * gridDim.x)) m->abort = 1;
     }
     cta_sync();
     return *reinterpret_cast<volatile int32_t *>(&m->abort) == 0;
@@ -937,48 +875,49 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     extern __shared__ __align__(1024) unsigned char smem[];
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool cut = SEGMENTS && p.counts[2] > 0;  // two passes
     if (warp == 0) {
-        init_barriers(m, SEGMENTS);
+        init_barriers(m, cut);
         m->abort = 0;
     }
     if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    constexpr uint32_t tmem = 0;  // all 512 columns were allocated: they begin at column 0
+    const uint32_t tmem = m->tmem;
     // every role: the pass over the states, the join, the pass over the outputs; or the last alone
-    if (threadIdx.x < T_SCORES) {
+    if (warp < 8) {
+        if (cut) touch_ahead(p);
+        if (!cut || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
+    } else if (warp < 16) {
+        more_registers<REGS_STATE>();
+#pragma unroll 1
+        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
+            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
+        }
+    } else if (warp < 24) {
+        fewer_registers<REGS_V>();
+#pragma unroll 1
+        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
+            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
+        }
+    } else {
         fewer_registers<REGS_AUX>();
 #pragma unroll 1
-        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
+        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
             const bool states = SEGMENTS && pass == 0;
             if (warp == WARP_LOAD) {
                 if (lane == 0) role_load<SEGMENTS>(p, smem, m, states);
             } else if (warp == WARP_DECAY) {
                 role_decay<SEGMENTS>(p, m, states);
             } else if (warp == WARP_MMA_U) {
-                role_mma_state<SEGMENTS>(p, smem, m, states);
+                role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
             } else if (warp == WARP_MMA_OUT && !states) {
-                role_mma_out<SEGMENTS>(p, smem, m);
+                role_mma_out<SEGMENTS>(p, smem, m, tmem);
             }
             __syncwarp();
-            if (SEGMENTS && pass == 0 && !next_pass<true, false>(p, m)) break;
-        }
-    } else if (threadIdx.x < T_STATE) {
-        if (SEGMENTS) touch_ahead(p);
-        if (!SEGMENTS || next_pass<false, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
-    } else if (threadIdx.x < T_V) {
-        more_registers<REGS_STATE>();
-#pragma unroll 1
-        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
-            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
-            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
-        }
-    } else {
-        fewer_registers<REGS_V>();
-#pragma unroll 1
-        for (int pass = SEGMENTS ? 0 : 1; pass < 2; ++pass) {
-            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
             if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
         }
     }
@@ -989,66 +928,203 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     if (warp == WARP_MMA_U) tmem_dealloc(tmem, 512);
 }
 
-// ---- segments: one CTA. Sequence n of c chunks gets ceil(c / L) segments of about equal length.
-__global__ void __launch_bounds__(256) kda_linear_plan_kernel(const ChunkParams p) {
-    __shared__ int part[256], total;
+// ---- segments: one CTA decides whether and how to cut, and sorts. Sequence n of c chunks gets ceil(c / L) segments of about
+// equal length, for the L of a few that is estimated to be fastest with these lengths. The estimate of a cut into no more than
+// SORTED segments is that of the busiest SM under the order in which the segments will be taken, found by sorting them; more
+// segments stay in the order of the sequences, and are taken to be of average length.
+constexpr int CUTS = 6, SORTED = 384, PLAN_GROUP = 128, PLAN_THREADS = CUTS * PLAN_GROUP;
+// Fitted to 90 timings on GB300 (15 batches, each with the six cuts), in microseconds: a chunk and a task of the pass over the
+// outputs and of that over the states, the outputs' chunks when memory bounds all SMs, the join and its barriers, and the join of
+// a segment. Each of the 15 was within 1 % of the best of its six. (A task costs this much where tasks are few: its first chunk
+// goes alone through all roles.)
+constexpr float T_OUT = 2.7f, T_OUT_TASK = 9.f, T_STATES = 1.7f, T_STATES_TASK = 6.f, T_OUT_ALL = 3.2f, T_CUT = 8.f, T_JOIN = 0.2f,
+                T_PLAN = 5.f;
+
+__host__ __device__ inline int cut_length(int i, int shortest) {  // candidates: no cut, then 1, 1.5, 2, 3, 4 times the shortest
+    return i == 0 ? 0x3fffffff : i == 1 ? shortest : i == 2 ? shortest + (shortest + 1) / 2 : shortest * (i - 1);
+}
+__host__ __device__ inline int pieces(int c, int len) { return c <= len ? 1 : (c + len - 1) / len; }
+struct Cut {
+    int longest, most, tasks, all, tasks_s, all_s;  // longest segment, most segments of a sequence; segments and their chunks in either pass
+};
+__host__ __device__ inline float pass_time(int longest, float all, float tasks, int sms, float chunk, float task) {
+    const float mean = all / fmaxf(tasks, 1.f) * chunk + task, rounds = tasks / sms;
+    return fmaxf(longest * chunk + task + fmaxf(floorf(rounds) - 1.f, 0.f) * mean, ceilf(rounds) * mean);
+}
+__host__ __device__ inline float cut_time(const Cut &c, int H, int sms, float out, float states) {
+    out = fmaxf(out, static_cast<float>(c.all) * H / sms * T_OUT_ALL);
+    return c.tasks_s > 0 ? out + states + T_CUT + T_JOIN * c.most : out;
+}
+__host__ __device__ inline float cut_time(const Cut &c, int H, int sms) {
+    const float h = static_cast<float>(H);
+    return cut_time(c, H, sms, pass_time(c.longest, c.all * h, c.tasks * h, sms, T_OUT, T_OUT_TASK),
+                    pass_time(c.longest, c.all_s * h, c.tasks_s * h, sms, T_STATES, T_STATES_TASK));
+}
+
+// the segments of a candidate, by slot, and the slots in order of length (tables of both passes)
+struct Sorted {
+    alignas(16) uint32_t key[2][SORTED];  // in either pass (outputs, states): chunks << 16 | 0xffff - slot, larger ones first; 0: not in it
+    uint16_t seq[SORTED], index[SORTED];
+    uint16_t order[2][SORTED];            // the slots by key
+};
+struct PlanShared {
+    Sorted sorted[CUTS];
+    Cut cuts[CUTS];
+    int time[CUTS][2];  // of the passes: bits of a positive float
+    int warps[CUTS][PLAN_GROUP / 32];
+    int count[CUTS], total_s, best;  // segments of the pass over the states
+};
+
+__global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const ChunkParams p) {
+    __shared__ PlanShared m;
     const Params &a = p.a;
-    const int tid = threadIdx.x;
-    const int per = (a.N + 255) / 256, n0 = tid * per, n1 = n0 + per < a.N ? n0 + per : a.N;
+    const int tid = threadIdx.x, i = tid / PLAN_GROUP, x0 = tid % PLAN_GROUP;  // candidate, and thread of its group
+    const int len = cut_length(i, p.seg_chunks);
     const bool start_ok = a.cu[0] == 0;
-    auto chunks = [&](int n) -> int64_t {
+    const bool keep = a.s0 && a.s0 == a.sT;
+    auto chunks = [&](int n) -> int {
         const int64_t b = a.cu[n], e = a.cu[n + 1];
-        return start_ok && b >= 0 && e >= b && e <= a.T ? (e - b + C - 1) / C : -1;
+        return start_ok && b >= 0 && e >= b && e <= a.T ? static_cast<int>((e - b + C - 1) / C) : -1;
     };
-    int mine = 0;
+    if (tid < CUTS) m.cuts[tid] = Cut{};
+    if (tid < 2 * CUTS) m.time[tid >> 1][tid & 1] = 0;
+    if (tid < CUTS) m.count[tid] = 0;
+    if (tid == 0) m.total_s = 0;
+    __syncthreads();
+    // each group: its candidate's segments, and the first slot of each thread's sequences
+    const int per = (a.N + PLAN_GROUP - 1) / PLAN_GROUP, n0 = x0 * per, n1 = n0 + per < a.N ? n0 + per : a.N;
+    int mine = 0;  // (saturating: offsets that are no offsets can add up to anything)
     for (int n = n0; n < n1; ++n) {
-        const int64_t c = chunks(n);
-        mine += c < 0 ? 0 : c == 0 ? 1 : static_cast<int>((c + p.seg_chunks - 1) / p.seg_chunks);
-    }
-    part[tid] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        int s = 0;
-        for (int i = 0; i < 256; ++i) {
-            const int v = part[i];
-            part[i] = s;
-            s += v;
+        const int c = chunks(n);
+        if (c < 0) continue;
+        const int k = pieces(c, len), one = (c + k - 1) / k;
+        mine = min(mine + k, p.most_segs + 1);
+        atomicMax(&m.cuts[i].longest, one);
+        atomicMax(&m.cuts[i].most, k);
+        atomicAdd(&m.cuts[i].all, c);
+        if (k > 1) {
+            atomicAdd(&m.cuts[i].tasks_s, k - 1);
+            atomicAdd(&m.cuts[i].all_s, c - one);
         }
-        // more than valid offsets can need: sequences overlap (cu_seqlens goes back), and nothing runs
-        if (s > p.most_segs) {
+    }
+    int upto = mine;  // sums over the threads up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if ((tid & 31) >= o) upto = min(upto + y, p.most_segs + 1);
+    }
+    if ((tid & 31) == 31) m.warps[i][x0 >> 5] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_GROUP / 32; ++w) {
+        if (w == x0 >> 5) upto += total;
+        total = min(total + m.warps[i][w], p.most_segs + 1);
+    }
+    const int first = upto - mine;
+    // more than valid offsets can need: sequences overlap (cu_seqlens goes back), and nothing runs
+    const bool overlap = __syncthreads_or(total > p.most_segs);
+    if (overlap) {
+        if (tid == 0) {
             set_status(a.status, KDA_ERR_BAD_SEQLENS);
-            s = -1;
+            p.counts[0] = p.counts[1] = p.counts[2] = 0;
         }
-        p.num_segs[0] = s < 0 ? 0 : s;
-        p.num_segs[1] = 0;
-        total = s;
-    }
-    __syncthreads();
-    if (total < 0) {
-        for (int n = n0; n < n1; ++n) p.first[n] = make_int2(0, 0);
         return;
     }
-    int at = part[tid];
+    if (x0 == 0) m.cuts[i].tasks = total;
+    Sorted &t = m.sorted[i];
+    const bool sort = total <= SORTED;
+    if (sort) {
+        int at = first;
+        for (int n = n0; n < n1; ++n) {
+            const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
+            for (int j = 0; j < k; ++j, ++at) t.seq[at] = static_cast<uint16_t>(n), t.index[at] = static_cast<uint16_t>(j);
+        }
+    }
+    __syncthreads();
+    // the first chunk of segment j of k; and a segment's chunks in the pass over the states, where the last one of a cut sequence
+    // comes without tokens, if at all, to keep the sequence's entry state
+    auto begin = [](int c, int k, int j) { return j * (c / k) + min(j, c % k); };
+    auto states_len = [&](int l, int k, int j) { return j < k - 1 ? l : k > 1 && keep ? 0 : -1; };
+    if (sort)
+        for (int x = x0; x < (total + 3 & ~3); x += PLAN_GROUP) {
+            const int c = x < total ? chunks(t.seq[x]) : 0, k = pieces(c, len), j = t.index[x];
+            const int l = x < total ? min(begin(c, k, j + 1) - begin(c, k, j), 0x7fff) : -1, ls = l < 0 ? -1 : states_len(l, k, j);
+            t.key[0][x] = l < 0 ? 0 : l << 16 | 0xffff - x;
+            t.key[1][x] = ls < 0 ? 0 : ls << 16 | 0xffff - x;
+            if (ls >= 0) atomicAdd(&m.count[i], 1);
+        }
+    __syncthreads();
+    if (sort)
+        for (int x = x0; x < total; x += PLAN_GROUP)
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                const uint32_t own = t.key[pass][x];
+                int rank = 0;
+#pragma unroll 4
+                for (int y = 0; y < total; y += 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(&t.key[pass][y]);
+                    rank += (v.x > own) + (v.y > own) + (v.z > own) + (v.w > own);
+                }
+                if (own) t.order[pass][rank] = static_cast<uint16_t>(x);
+            }
+    __syncthreads();
+    if (sort)
+        for (int b = x0; b < 2 * p.sms; b += PLAN_GROUP) {  // both passes' tasks of every SM
+            const int pass = b >= p.sms, sm = b - pass * p.sms, tasks = (pass ? m.count[i] : total) * a.H;
+            float time = 0.f;
+            for (int k = 0, id; (id = nth_task(k, sm, p.sms)) < tasks; ++k)
+                time += (t.key[pass][t.order[pass][id / a.H]] >> 16) * (pass ? T_STATES : T_OUT) + (pass ? T_STATES_TASK : T_OUT_TASK);
+            atomicMax(&m.time[i][pass], __float_as_int(time));
+        }
+    __syncthreads();
+    if (tid == 0) {
+        float least = 3.0e38f;
+        m.best = 0;
+        for (int j = 0; j < CUTS; ++j) {
+            const Cut &c = m.cuts[j];
+            const float time = c.tasks <= SORTED ? cut_time(c, a.H, p.sms, __int_as_float(m.time[j][0]), __int_as_float(m.time[j][1]))
+                                                 : cut_time(c, a.H, p.sms);
+            if (time < least) least = time, m.best = j;
+        }
+    }
+    __syncthreads();
+    if (i != m.best) return;  // the chosen candidate's group writes
+    auto segment = [&](int n, int j, int slot) {
+        const int64_t from = a.cu[n], to = a.cu[n + 1];
+        const int c = static_cast<int>((to - from + C - 1) / C), k = pieces(c, len);
+        Segment s;
+        s.t0 = static_cast<int32_t>(from + static_cast<int64_t>(begin(c, k, j)) * C);
+        s.len = static_cast<int32_t>(j == k - 1 ? to - s.t0 : (begin(c, k, j + 1) - begin(c, k, j)) * C);
+        s.seq = n;
+        s.index = j;
+        s.count = k;
+        s.slot = slot;
+        return s;
+    };
+    int at = first;
     for (int n = n0; n < n1; ++n) {
-        const int64_t c = chunks(n);
-        if (c < 0) {
-            set_status(a.status, KDA_ERR_BAD_SEQLENS);
-            p.first[n] = make_int2(at, 0);
-            continue;
-        }
-        const int k = c == 0 ? 1 : static_cast<int>((c + p.seg_chunks - 1) / p.seg_chunks);
-        const int64_t step = (c + k - 1) / k * C, len = a.cu[n + 1] - a.cu[n];
+        const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
+        if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
         p.first[n] = make_int2(at, k);
-        for (int i = 0; i < k; ++i, ++at) {
-            Segment sg;
-            const int64_t b = i * step < len ? i * step : len, e = b + step < len ? b + step : len;
-            sg.t0 = static_cast<int32_t>(a.cu[n] + b);
-            sg.len = static_cast<int32_t>(e - b);
-            sg.seq = n;
-            sg.index = i;
-            sg.count = k;
-            p.segs[at] = sg;
+        for (int j = 0; !sort && j < k; ++j) {
+            const Segment s = segment(n, j, at + j);
+            p.segs[at + j] = s;
+            if (states_len(0, k, j) >= 0) p.segs_s[atomicAdd(&m.total_s, 1)] = s;
         }
+        at += k;
+    }
+    if (sort)
+        for (int r = x0; r < total; r += PLAN_GROUP) {
+            const int x = t.order[0][r], y = r < m.count[i] ? t.order[1][r] : -1;
+            p.segs[r] = segment(t.seq[x], t.index[x], x);
+            if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], y);
+        }
+    named_bar_sync(1, PLAN_GROUP);  // (the others have left)
+    if (x0 == 0) {
+        p.counts[0] = total;
+        p.counts[1] = 0;
+        p.counts[2] = sort ? m.count[i] : m.total_s;
     }
 }
 
@@ -1082,40 +1158,25 @@ bool encode(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int heads, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int device() {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) (void)cudaGetLastError();
-    return dev;
-}
-// SMs of the current device (0: no usable device); asked once for each of the first MAX_DEVICES
-constexpr int MAX_DEVICES = 64;
 int num_sms() {
-    static std::atomic<int> known[MAX_DEVICES];
-    const int dev = device();
-    if (dev < 0) return 0;
-    int sms = dev < MAX_DEVICES ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (sms) return sms;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         (void)cudaGetLastError();
         return 0;
     }
-    if (dev < MAX_DEVICES) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
 template <bool SEGMENTS>
 cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
     const auto kernel = kda_linear_chunk_kernel<SEGMENTS>;
-    static std::atomic<bool> ready[MAX_DEVICES];
-    const int dev = device();
-    if (dev < 0 || dev >= MAX_DEVICES || !ready[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    static const int regs = [] {
         cudaFuncAttributes at{};
-        if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
-        if (e != cudaSuccess) return e;
-        if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
-        if (dev >= 0 && dev < MAX_DEVICES) ready[dev].store(true, std::memory_order_release);
-    }
+        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<SEGMENTS>) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
     const int grid = static_cast<int>(most_tasks < sms ? most_tasks : sms);
     if (SEGMENTS) {
         void *args[] = {const_cast<ChunkParams *>(&p)};
@@ -1128,18 +1189,32 @@ cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t 
 // Sequences of few tokens run the recurrence.
 bool few_tokens(int64_t N, int64_t T) { return T <= 16 * N; }
 
-// Chunks per segment so that every SM gets about one (segment, head); 0 when no
-// sequence can be longer than that.
+// The shortest cut of sequences worth a try, about half an SM's share of the chunks; 0 when nothing is to be cut: no sequence can
+// be longer, or they can all be of one length (tokens a multiple of sequences) and are estimated to be as fast whole. (A batch
+// of unequal lengths that passes for equal runs correctly, only perhaps slower.)
 int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
     const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
-    int64_t len = (all + sms - 1) / sms;
+    int64_t len = (all + 2 * sms - 1) / (2 * sms);
     if (len < 4) len = 4;
-    return longest <= len ? 0 : static_cast<int>(len);
+    if (longest <= len) return 0;
+    if (T % N == 0) {
+        const int64_t each = (T / N + C - 1) / C;
+        auto time_of = [&](int64_t cut) {
+            const int64_t k = (each + cut - 1) / cut, one = (each + k - 1) / k;
+            return cut_time({static_cast<int>(one), static_cast<int>(k), static_cast<int>(k * N), static_cast<int>(each * N),
+                             static_cast<int>((k - 1) * N), static_cast<int>((each - one) * N)}, static_cast<int>(H), sms);
+        };
+        const float whole = time_of(each);
+        float best = 3.0e38f;
+        for (int i = 1; i < CUTS; ++i) best = std::fmin(best, time_of(cut_length(i, static_cast<int>(len))));
+        if (whole <= best + T_PLAN) return 0;
+    }
+    return static_cast<int>(len);
 }
 
 struct Layout {
     int64_t most;  // segments at most: ceil(c / L) <= c' / L + 1 summed over the sequences
-    size_t first, segs, decays, states, bytes;
+    size_t first, segs, segs_s, decays, states, bytes;
 };
 Layout layout_of(int64_t N, int64_t T, int64_t H, int len) {
     Layout l;
@@ -1147,7 +1222,8 @@ Layout layout_of(int64_t N, int64_t T, int64_t H, int len) {
     l.most = T / (static_cast<int64_t>(C) * len) + N;
     l.first = 256;
     l.segs = up(l.first + sizeof(int2) * N);
-    l.decays = up(l.segs + sizeof(Segment) * l.most);
+    l.segs_s = up(l.segs + sizeof(Segment) * l.most);
+    l.decays = up(l.segs_s + sizeof(Segment) * l.most);
     l.states = up(l.decays + sizeof(float) * l.most * H);
     l.bytes = l.states + sizeof(float) * DK * DV * l.most * H;
     return l;
@@ -1177,12 +1253,14 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.most_segs = static_cast<int32_t>(l.most);
-    p.num_segs = reinterpret_cast<int32_t *>(ws);
+    p.sms = sms;
+    p.counts = reinterpret_cast<int32_t *>(ws);
     p.first = reinterpret_cast<int2 *>(ws + l.first);
     p.segs = reinterpret_cast<Segment *>(ws + l.segs);
+    p.segs_s = reinterpret_cast<Segment *>(ws + l.segs_s);
     p.decays = reinterpret_cast<float *>(ws + l.decays);
     p.states = reinterpret_cast<float *>(ws + l.states);
-    kda_linear_plan_kernel<<<1, 256, 0, stream>>>(p);
+    kda_linear_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? run<true>(p, l.most * a.H, sms, stream) : e;
 }

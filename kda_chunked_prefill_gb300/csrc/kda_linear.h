@@ -30,9 +30,10 @@ constexpr float G_FLOOR = -138.f;
 
 constexpr int CHUNK = 128;  // tokens
 
-// A part of a sequence that one CTA walks: tokens t0 .. t0 + len - 1 of sequence seq.
+// A part of a sequence that one CTA walks: tokens t0 .. t0 + len - 1 of sequence seq, its index-th of count segments; slot: where
+// its state goes.
 struct Segment {
-    int32_t t0, len, seq, index, count;  // index of the sequence's count segments
+    int32_t t0, len, seq, index, count, slot;
 };
 
 // the recurrence, token after token (few tokens per sequence)
