@@ -79,8 +79,11 @@ struct Misc {
     uint64_t ufree, ofree;            // U read; O read
     uint32_t tmem;                    // address of the tensor memory
     int32_t abort;                    // a wait ran out
-    alignas(16) float tab[192];       // anchors 1..3, from tab_at(): 2^(sum of g after j up to the start of block a), j before it
-    alignas(16) float pre[C];         // log2 prefix of j within its block of 32
+    int32_t easy, pad;                // this chunk's decay is above EASY
+    // slow chunks (EASY): tab[j] = 2^-(sum of g up to j), pre[j] = log2 sum of g up to j, start = 0; others: tab, for anchors
+    // 1..3 from tab_at(), 2^(sum of g after j up to the start of block a), j before it, and pre the log2 prefix within j's block
+    alignas(16) float tab[192];
+    alignas(16) float pre[C];
     alignas(16) float w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
     float start[4];                   // log2 sum of g up to the start of each block
     float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
@@ -100,6 +103,9 @@ constexpr int WARP_STORE = 4;  // of the scores' warps, the one with only masked
 // Registers: 28 warps launch with 72; the roles' shares add up to no more.
 constexpr int REGS = 72, REGS_SCORES = 72, REGS_STATE = 104, REGS_V = 48, REGS_AUX = 56;
 static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 8 * REGS_V + 4 * REGS_AUX <= 28 * REGS, "the launch's registers");
+// A chunk whose whole decay is above 2^EASY needs no anchors: its scores are A_ij 2^-(sum of g up to j), at most 2^80 times
+// their size, and the row's 2^(sum of g up to i) is left to the output, so that q S and P v add up as they are.
+constexpr float EASY = -80.f;
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -437,11 +443,22 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             arrive_warp(&m->decw[buf]);
             if (states) continue;
             if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
+            const bool easy = total > EASY;
+            if (easy) {
+                float from = before;  // this block's earlier lanes, then the blocks before it
+#pragma unroll
+                for (int b = 2; b >= 0; --b)
+                    if (b < block) from += tot[b];
+                *reinterpret_cast<float4 *>(&m->tab[4 * lane]) =
+                    make_float4(ex2(-pre[0] - from), ex2(-pre[1] - from), ex2(-pre[2] - from), ex2(-pre[3] - from));
+                before = from;
+            } else {
 #pragma unroll 1
-            for (int x = block + 1; x < 4; ++x) {
-                *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
-                    make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
-                after += x == 1 ? tot[1] : tot[2];
+                for (int x = block + 1; x < 4; ++x) {
+                    *reinterpret_cast<float4 *>(&m->tab[tab_at(x) + 4 * lane]) =
+                        make_float4(ex2(suf[0] + after), ex2(suf[1] + after), ex2(suf[2] + after), ex2(suf[3] + after));
+                    after += x == 1 ? tot[1] : tot[2];
+                }
             }
             *reinterpret_cast<float4 *>(&m->pre[4 * lane]) =
                 make_float4(pre[0] + before, pre[1] + before, pre[2] + before, pre[3] + before);
@@ -449,9 +466,10 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
                 float from = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    m->start[b] = from;
+                    m->start[b] = easy ? 0.f : from;
                     from += tot[b];
                 }
+                m->easy = easy;
             }
             arrive_warp(&m->dect);
         }
@@ -532,12 +550,12 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
 // A chunk's output from tensor memory into the q tile, and out. The scores' and the state's warps share it: four threads a token
 // row, 32 values each (half, part). True: some warp has given up. (A warp that gives up still comes to the barriers.)
 __device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
-                                            int slot, int tid, int half, int part, bool fail) {
+                                            int slot, int tid, int half, int part, float factor, bool fail) {
     unsigned char *tile = smem + slot * TILE + half * PANEL;
     const int left = t.len - c, lane = threadIdx.x & 31;
     if (!fail) {
         tc_fence_after();
-        const f2 s2 = pair(p.a.scale, p.a.scale);
+        const f2 s2 = pair(factor, factor);
 #pragma unroll 1
         for (int b = 0; b < 2; ++b) {
             uint32_t o[16];
@@ -603,9 +621,12 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
             fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
+            float out = 0.f;  // what the row's output is multiplied by
             if (!fail) {
                 tc_fence_after();
                 const float pre = m->pre[tid], row = ex2(pre);
+                const bool easy = m->easy;
+                out = p.a.scale * (easy ? row : 1.f);
                 // key blocks of 32: 0 and 3, or 1 and 2
 #pragma unroll 1
                 for (int i = 0; i < 2; ++i) {
@@ -615,6 +636,18 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                     if (b > warp) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) s[j] = 0;
+                    } else if (easy) {
+                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[32 * b]);
+                        const int see = b == warp ? lane : 32;
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = f[j];
+                            const uint32_t x = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), pair(w.x, w.y)));
+                            const uint32_t y = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), pair(w.z, w.w)));
+                            s[2 * j] = 4 * j + 1 <= see ? x : 4 * j <= see ? x & 0xffffu : 0u;
+                            s[2 * j + 1] = 4 * j + 3 <= see ? y : 4 * j + 2 <= see ? y & 0xffffu : 0u;
+                        }
                     } else if (b < warp) {
                         const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
                         const f2 r2 = pair(row, row);
@@ -647,7 +680,7 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
                 arrive_warp(&m->p);
             }
             fail = fail || !wait_warp(m, &m->o, ph);
-            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, fail)) return;
+            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out, fail)) return;
         }
     }
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
@@ -692,28 +725,35 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            if (!states) {  // q S by the row's decay since the chunk began; P v is added onto it
-                fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qs, ph);
+            float out = a.scale;  // what the row's output is multiplied by
+            if (!states) {
+                fail = fail || !wait_warp(m, &m->dect, ph);
                 if (!fail) {
-                    tc_fence_after();
                     const float entry = ex2(m->pre[tid] + m->start[warp]);
-                    const f2 e2 = pair(entry, entry);
+                    if (m->easy) {
+                        out *= entry;
+                    } else if (wait_warp(m, &m->qs, ph)) {  // q S by the row's decay since the chunk began; P v is added onto it
+                        tc_fence_after();
+                        const f2 e2 = pair(entry, entry);
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t x[16];
-                        tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
-                        tmem_wait_ld();
+                        for (int b = 0; b < 4; ++b) {
+                            uint32_t x[16];
+                            tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float y, z;
-                            split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
-                            x[2 * j] = __float_as_uint(y);
-                            x[2 * j + 1] = __float_as_uint(z);
+                            for (int j = 0; j < 8; ++j) {
+                                float y, z;
+                                split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
+                                x[2 * j] = __float_as_uint(y);
+                                x[2 * j + 1] = __float_as_uint(z);
+                            }
+                            tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
                         }
-                        tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        tmem_wait_st();
+                        tc_fence_before();
+                    } else {
+                        fail = true;
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
                     arrive_warp(&m->p);
                 }
             }
@@ -732,11 +772,14 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
                 }
                 tc_fence_before();
                 arrive_warp(&m->ufree);
-                if (!states && c + C < t.len) publish();  // (q S of this chunk is done)
+                if (!states) {
+                    fail = !wait_warp(m, &m->qs, ph);  // q has been multiplied by the last copy
+                    if (!fail && c + C < t.len) publish();
+                }
             }
             if (!states) {
                 fail = fail || !wait_warp(m, &m->o, ph);
-                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, fail)) return;
+                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out, fail)) return;
             }
         }
         if (fail) return;
