@@ -84,7 +84,7 @@ struct Misc {
     // 1..3 from tab_at(), 2^(sum of g after j up to the start of block a), j before it, and pre the log2 prefix within j's block
     alignas(16) float tab[192];
     alignas(16) float pre[C];
-    alignas(16) float w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
+    alignas(16) uint32_t w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
     float start[4];                   // log2 sum of g up to the start of each block
     float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
 };
@@ -435,8 +435,11 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
                 if (b > block) to_end += tot[b];
             const int buf = it & 1;
             if (it > 1 && !wait_warp(m, &m->wfree[buf], ((it >> 1) - 1) & 1)) return;
-            *reinterpret_cast<float4 *>(&m->w[buf][4 * lane]) =
-                make_float4(ex2(suf[0] + to_end), ex2(suf[1] + to_end), ex2(suf[2] + to_end), ex2(suf[3] + to_end));
+            const f2 w0 = pair(ex2(suf[0] + to_end), ex2(suf[1] + to_end)), w1 = pair(ex2(suf[2] + to_end), ex2(suf[3] + to_end));
+            const uint32_t h0 = bf16_of(w0), h1 = bf16_of(w1);
+            const f2 minus = pair(-1.f, -1.f);
+            *reinterpret_cast<uint4 *>(&m->w[buf][4 * lane]) =
+                make_uint4(h0, bf16_of(fma2(of_bf16(h0), minus, w0)), h1, bf16_of(fma2(of_bf16(h1), minus, w1)));
             // (minus one, so that a slow decay is not rounded away chunk after chunk; the state's warps have read the
             // entry of four chunks ago: the scores of two chunks ago came after their read)
             if (lane == 0) m->dm1[it & 3] = expm1f(total * (1.f / LOG2E));
@@ -478,14 +481,16 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A thread has one value
-// channel (the lane of its warp's quarter) and every other 16 tokens.
+// ---- eight warps: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
+// (its quarter of the lanes) and 16 of every 32 tokens: ldmatrix transposes 8 x 8 blocks, and a tensor-memory store of the same
+// fragment shape puts each pair of tokens into its channel's lane.
 template <bool SEG>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
-    const int gtid = threadIdx.x & (GROUP - 1), half = gtid >> 7, ch = gtid & 127;
-    const uint32_t dst = tmem + (static_cast<uint32_t>(ch >> 5) << 21) + COL_VT + 8 * half;
-    const uint32_t row0 = (ch >> 6) * PANEL + half * 16 * 128 + (ch & 7) * 2, piece = (ch & 63) >> 3;
-    const f2 minus = pair(-1.f, -1.f);
+    const int gtid = threadIdx.x & (GROUP - 1), lane = gtid & 31, quad = (gtid >> 5) & 3, half = gtid >> 7;
+    const uint32_t dst = tmem + (static_cast<uint32_t>(quad) << 21) + COL_VT + 8 * half;
+    // this lane's row of the blocks: token lane % 8, channels 8 (lane / 8) .. of the quarter; swizzle: 16-byte piece ^ row % 8
+    const uint32_t row0 = (quad >> 1) * PANEL + (16 * half + (lane & 7)) * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);
+    const int pair0 = 16 * half + 2 * (lane & 3);  // the fragments' tokens
     bool fail = false;  // (a warp that gives up still comes to the barriers)
     uint32_t it = 0;
     const int tasks = tasks_of<SEG>(p, states);
@@ -517,27 +522,25 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 fail = fail || (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1));
                 if (fail) break;
                 tc_fence_after();
-                const unsigned char *src = tv + row0 + st * (STAGE_ROWS * 128);
-                const int j0 = STAGE_ROWS * st + 16 * half;  // this thread's 16 tokens
-                const float4 *w4 = reinterpret_cast<const float4 *>(&m->w[it & 1][j0]);
-                uint32_t hi[8], lo[8];
+                uint32_t hi[8], lo[8];  // [8 tokens][8 channels]
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 w = w4[j];
+                for (int g = 0; g < 2; ++g) {
                     uint32_t x[4];
+                    ldsm_x4_t(x, tv + row0 + st * (STAGE_ROWS * 128) + g * 1024);
+                    const uint2 w2 = *reinterpret_cast<const uint2 *>(&m->w[it & 1][STAGE_ROWS * st + 8 * g + pair0]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // the tile's swizzle: 16-byte piece ^ row % 8
-                        const int r = 4 * j + i;
-                        x[i] = static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(src + r * 128 + ((piece ^ (r & 7)) << 4))) << 16;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t y = mul_bf16(x[i], w2.x);
+                        hi[4 * g + i] = y;
+                        lo[4 * g + i] = fma_bf16(x[i], w2.y, fma_bf16(x[i], w2.x, y ^ 0x80008000u));
                     }
-                    const f2 y0 = mul2(pair(x[0], x[1]), pair(w.x, w.y)), y1 = mul2(pair(x[2], x[3]), pair(w.z, w.w));
-                    hi[2 * j] = bf16_of(y0);
-                    hi[2 * j + 1] = bf16_of(y1);
-                    lo[2 * j] = bf16_of(fma2(of_bf16(hi[2 * j]), minus, y0));
-                    lo[2 * j + 1] = bf16_of(fma2(of_bf16(hi[2 * j + 1]), minus, y1));
                 }
-                tmem_st8(dst + st * (STAGE_ROWS / 2), hi);
-                tmem_st8(dst + st * (STAGE_ROWS / 2) + C / 2, lo);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // 16 lanes each
+                    const uint32_t at = dst + (h << 20) + st * (STAGE_ROWS / 2);
+                    tmem_st_frag2(at, hi[2 * h], hi[2 * h + 1], hi[4 + 2 * h], hi[5 + 2 * h]);
+                    tmem_st_frag2(at + C / 2, lo[2 * h], lo[2 * h + 1], lo[4 + 2 * h], lo[5 + 2 * h]);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(&m->vt[st]);

@@ -77,6 +77,11 @@ __device__ __forceinline__ bool mbar_wait_some(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// 16 lanes x 8 columns: register 2 g + i of thread T is lane T / 4 + 8 i, column 4 g + T % 4 (what ldmatrix's fragments are)
+__device__ __forceinline__ void tmem_st_frag2(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -143,6 +148,16 @@ __device__ __forceinline__ uint32_t bf16_of(f2 a) {
     float x, y;
     split(a, x, y);
     return pack_bf16(x, y);
+}
+__device__ __forceinline__ uint32_t mul_bf16(uint32_t a, uint32_t b) {  // two of them
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
 }
 __device__ __forceinline__ f2 of_bf16(uint32_t u) { return pair(u << 16, u & 0xffff0000u); }
 // `n` threads meet at named barrier `id`; whether any of them says so
