@@ -8,6 +8,8 @@
 // Bound by memory: 7 bytes per element (2 + 2 in, 2 + 1 out; 11 with an fp32
 // residual).
 //
+// 8192 rows of 2048 with a bf16 residual: 20.5 us, 5.7 TB/s (85 % of a copy).
+//
 // Rows are cut at multiples of 8 elements of the whole tensor, not of the row:
 // with 16-byte-aligned tensors every such group is one aligned access of x, r, r'
 // and y whatever the width; a group that two rows share is handled element by
@@ -24,6 +26,7 @@ namespace addnorm {
 
 constexpr float TINY = 7.888609052210118e-31f;  // 2^-100: below it a row counts as zero
 constexpr float E4M3_MAX = 448.f;
+constexpr int NARROW = 4;  // rows of a CTA where a warp takes one
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;  // saturating, round to nearest even; NaN stays NaN
@@ -32,18 +35,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-__device__ __forceinline__ void load_bf16(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_bf16(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void load_res(const __nv_bfloat16 *p, float (&v)[8]) { load_bf16(p, v); }
-__device__ __forceinline__ void load_res(const float *p, float (&v)[8]) {
+__device__ __forceinline__ void load_weight(const float *p, float (&v)[8]) {
     const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
@@ -55,39 +47,79 @@ __device__ __forceinline__ void store_res(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+template <typename R>
+struct Raw {  // eight elements as they lie in memory
+    uint4 u[sizeof(R) / 2];
+};
+template <typename R>
+__device__ __forceinline__ void load_raw(Raw<R> &r, const R *p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(R) / 2); ++i) r.u[i] = reinterpret_cast<const uint4 *>(p)[i];
+}
+__device__ __forceinline__ void add_raw(float (&v)[8], const Raw<__nv_bfloat16> &r) {
+    const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_bf16(w[i]);
+        v[2 * i] += f.x;
+        v[2 * i + 1] += f.y;
+    }
+}
+__device__ __forceinline__ void add_raw(float (&v)[8], const Raw<float> &r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] += __uint_as_float(r.u[i].x);
+        v[4 * i + 1] += __uint_as_float(r.u[i].y);
+        v[4 * i + 2] += __uint_as_float(r.u[i].z);
+        v[4 * i + 3] += __uint_as_float(r.u[i].w);
+    }
+}
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 
-// One CTA of THREADS threads per row; a thread holds NV groups of 8 elements.
+// THREADS threads per row, a warp or whole CTAs; a thread holds NV groups of 8 elements.
 // ALIGNED: width is a multiple of 8 (no shared groups, weight loads are vectors).
 template <typename R, int THREADS, int NV, bool ALIGNED>
-__global__ void __launch_bounds__(THREADS) kda_add_rms_norm_kernel(const __nv_bfloat16 *__restrict__ x, const R *res,
-                                                                   const float *__restrict__ weight, int32_t width,
-                                                                   float eps, R *res_out, uint8_t *__restrict__ y,
-                                                                   float *__restrict__ y_scale) {
+__global__ void __launch_bounds__(THREADS == 32 ? 32 * NARROW : THREADS)
+    kda_add_rms_norm_kernel(const __nv_bfloat16 *__restrict__ x, const R *res, const float *__restrict__ weight, int32_t rows,
+                            int32_t width, float eps, R *res_out, uint8_t *__restrict__ y, float *__restrict__ y_scale) {
     constexpr int WARPS = THREADS / 32;
     __shared__ float s_sum[WARPS], s_max[WARPS];
-    const int tid = threadIdx.x;
-    const int64_t f0 = static_cast<int64_t>(blockIdx.x) * width, f1 = f0 + width;
+    const int tid = threadIdx.x % THREADS;
+    const int64_t row = THREADS == 32 ? static_cast<int64_t>(blockIdx.x) * NARROW + threadIdx.x / 32 : blockIdx.x;
+    if (row >= rows) return;
+    const int64_t f0 = row * width, f1 = f0 + width;
     const int64_t v0 = f0 >> 3;
     float h[NV][8];
     float sum = 0.f, mx = 0.f;
+    // All loads before the first store, where the registers hold them: the residual may be updated in place, and no load moves
+    // past a store by itself.
+    constexpr bool AHEAD = THREADS <= 512;
+    Raw<__nv_bfloat16> xr[NV];
+    Raw<R> rr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t f = (v0 + tid + i * THREADS) << 3;
-        if (f >= f1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
-            continue;
+        if (AHEAD && f + 8 <= f1 && (ALIGNED || f >= f0)) {
+            load_raw(xr[i], x + f);
+            load_raw(rr[i], res + f);
         }
-        float r[8];
-        if (ALIGNED || (f >= f0 && f + 8 <= f1)) {
-            load_bf16(x + f, h[i]);
-            load_res(res + f, r);
+    }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[i][j] += r[j];
+    for (int i = 0; i < NV; ++i) {
+        const int64_t f = (v0 + tid + i * THREADS) << 3;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = 0.f;
+        if (f >= f1) continue;
+        if (ALIGNED || (f >= f0 && f + 8 <= f1)) {
+            if (!AHEAD) {
+                load_raw(xr[i], x + f);
+                load_raw(rr[i], res + f);
+            }
+            add_raw(h[i], xr[i]);
+            add_raw(h[i], rr[i]);
             store_res(res_out + f, h[i]);
         } else {
 #pragma unroll
@@ -105,7 +137,7 @@ __global__ void __launch_bounds__(THREADS) kda_add_rms_norm_kernel(const __nv_bf
         if (f >= f1) continue;
         float w[8];
         if (ALIGNED) {
-            load_res(weight + (f - f0), w);
+            load_weight(weight + (f - f0), w);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = (f + j >= f0 && f + j < f1) ? __ldg(weight + (f + j - f0)) : 0.f;
@@ -141,7 +173,7 @@ __global__ void __launch_bounds__(THREADS) kda_add_rms_norm_kernel(const __nv_bf
     const float amax = max_abs_nan(0.f, mx * rstd);  // max|n|; NaN once anything in the row is not finite
     const bool tiny = amax < TINY;
     const float mul = tiny ? 0.f : rstd * (E4M3_MAX / amax);
-    if (tid == 0) y_scale[blockIdx.x] = tiny ? 0.f : amax / E4M3_MAX;
+    if (tid == 0) y_scale[row] = tiny ? 0.f : amax / E4M3_MAX;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t f = (v0 + tid + i * THREADS) << 3;
@@ -161,28 +193,40 @@ __global__ void __launch_bounds__(THREADS) kda_add_rms_norm_kernel(const __nv_bf
 template <typename R, int THREADS, int NV>
 void launch_width(bool al, const __nv_bfloat16 *x, const R *res, const float *w, int rows, int width, float eps,
                   R *res_out, uint8_t *y, float *ys, cudaStream_t s) {
+    constexpr int PER_CTA = THREADS == 32 ? NARROW : 1;
+    const int grid = (rows - 1) / PER_CTA + 1;
     if (al)
-        kda_add_rms_norm_kernel<R, THREADS, NV, true><<<rows, THREADS, 0, s>>>(x, res, w, width, eps, res_out, y, ys);
+        kda_add_rms_norm_kernel<R, THREADS, NV, true><<<grid, THREADS * PER_CTA, 0, s>>>(x, res, w, rows, width, eps, res_out, y, ys);
     else
-        kda_add_rms_norm_kernel<R, THREADS, NV, false><<<rows, THREADS, 0, s>>>(x, res, w, width, eps, res_out, y, ys);
+        kda_add_rms_norm_kernel<R, THREADS, NV, false><<<grid, THREADS * PER_CTA, 0, s>>>(x, res, w, rows, width, eps, res_out, y, ys);
 }
 template <typename R>
 void launch(const __nv_bfloat16 *x, const R *res, const float *w, int rows, int width, float eps, R *res_out,
             uint8_t *y, float *ys, cudaStream_t s) {
     const bool al = width % 8 == 0;
     const int groups = al ? width / 8 : width / 8 + 2;  // groups a row may touch
+    // Two groups a thread or three, as far as that is a warp to 512 threads a row. Measured with 8192 rows of 2048 (bf16 residual): 20.5
+    // us, with one group 22.4 and four 23.8; 2048 rows of 12288: three groups 31.5, two (1024 threads) 45.1, six 38.7.
     if (groups <= 32)
         launch_width<R, 32, 1>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
+    else if (groups <= 64)
+        launch_width<R, 32, 2>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
     else if (groups <= 128)
-        launch_width<R, 128, 1>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
+        launch_width<R, 64, 2>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
     else if (groups <= 256)
         launch_width<R, 128, 2>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
+    else if (groups <= 384)
+        launch_width<R, 128, 3>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
     else if (groups <= 512)
         launch_width<R, 256, 2>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
+    else if (groups <= 768)
+        launch_width<R, 256, 3>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
     else if (groups <= 1024)
         launch_width<R, 512, 2>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
+    else if (groups <= 1536)
+        launch_width<R, 512, 3>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
     else if (groups <= 2048)
-        launch_width<R, 1024, 2>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
+        launch_width<R, 512, 4>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
     else
         launch_width<R, 1024, 5>(al, x, res, w, rows, width, eps, res_out, y, ys, s);
 }
