@@ -461,8 +461,9 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
  * the chunk's g up to token i,
  *       o_i = scale * (e^{G_i} S^T q_i + sum_{j<=i} e^{G_i-G_j} (q_i.k_j) v_j)
  *       S  <- e^{G_end} S + sum_j e^{G_end-G_j} k_j v_j^T
- * (every exponent is a sum of g <= 0, so no factor exceeds 1). Sequences of few
- * tokens run the recurrence itself.
+ * (every exponent is a sum of g <= 0). Sequences of few tokens (16 on average)
+ * run the recurrence itself. Long sequences are cut where there are few: two
+ * launches then, the first to plan the cut, else one.
  * (Not part of the method's pages.)
  *   q, k          bf16, num_qk_heads heads of 128 channels per token; value head
  *                 h reads query/key head h / (num_heads / num_qk_heads), so
@@ -489,8 +490,9 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
  *                 (NULL when that is 0); not shared by calls that overlap.
  * Precision: products of bf16 operands with fp32 accumulation; the state is kept
  * and updated in fp32, its update's operands split into two bf16 terms (relative
- * error of final_state about 1e-6); the decayed scores and the copy of the state
- * that q multiplies are rounded to bf16, as o is.
+ * error of final_state about 4e-6); the decayed scores and the copy of the state
+ * that q multiplies are rounded to bf16, as o is. A chunk's scores are held at up
+ * to 2^48 times their size: (q.k) v must stay below 2^79.
  * q, k, v must be finite: a non-finite value may reach every output of its
  * sequence from the start of its chunk on. Alignment: q, k, v, o and the
  * states 16 bytes (32 for the states), g, cu_seqlens and status_dev 4.

@@ -1,34 +1,38 @@
 // Chunked form of the linear attention with one decay per head (kda_linear_chunk_fwd) on tcgen05.
 //
 // For a chunk of 128 tokens with G_i the sum of its g up to token i (all g <= 0):
-//     A   = q k^T                                 MMA  [128 x 128 x 128]
-//     P_ij = [j <= i] e^{G_i - G_j} A_ij          warpgroup 0, bf16 into tensor memory
-//     O1  = q S,  O2 = P v                        MMA, MMA
-//     o_i = scale (e^{G_i} O1_i + O2_i)           warpgroup 0
-//     U   = k^T v~,  v~_j = e^{G_end - G_j} v_j   warpgroup 1 forms v~, MMA
-//     S   = e^{G_end} S + U                       warpgroup 1, fp32 registers
+//     A    = q k^T                                MMA, 128 x 128 x 128, into tensor memory
+//     P_ij = [j <= i] e^{G_i - G_j} A_ij          bf16, over A
+//     O    = diag(e^G) q S + P v                  two MMAs into one accumulator, S in bf16
+//     U^T  = v~^T k,  v~_j = e^{G_end - G_j} v_j  MMA, v~ in two bf16 terms
+//     S    = e^{G_end} S + U                      fp32 registers
 //
-// One CTA per SM walks (segment, head) tasks: a segment is a sequence or a part
-// of one. Roles run side by side, each a chunk or two ahead of the next:
-//   load    one thread: q, k and v tiles by TMA into a ring of five 32 KB tiles
+// A CTA per SM walks (segment, head) tasks: a segment is a sequence or, where there are few, a part of one. Roles run side by
+// side, each a chunk or two ahead of the next:
+//   load    one thread: q, k and v tiles by TMA into a ring of six 32 KB tiles, two chunks of the three kinds
 //   decays  one warp: the chunk's decay tables from g
-//   v~      8 warps: v~ in stages of 32 tokens
-//   scores  8 warps: P, half of o_i
-//   state   8 warps: S, the other half of o_i; o leaves from the chunk's q tile
+//   v~      8 warps: v~, transposed into tensor memory, in stages of 32 tokens
+//   scores  8 warps: P, and half of o
+//   state   8 warps: S, and the other half of o; o leaves by TMA from the chunk's q tile
 //   MMAs    one warp for q k^T, q S and P v, one for U
 //
-// Why this split. U does not depend on S, so the recurrence from chunk to chunk
-// is one fused multiply-add per state element and its rounding to bf16 for the
-// next q S: S stays in fp32 registers (a key row shared by two threads), is
-// never accumulated by the tensor cores over many chunks, and a chunk's MMAs
-// are all off the critical path. v~ is split in two bf16 terms (hi + lo, both
-// multiplied by the exact bf16 k), which keeps the final state within about
-// 3e-6; P and the copy of S that q multiplies are rounded once to bf16, like o.
+// Why this split. U does not depend on S, so the recurrence from chunk to chunk is one fused multiply-add per state element and
+// its rounding to bf16 for the next q S: S stays in fp32 registers (two threads share a value column) and is never accumulated
+// by the tensor cores over many chunks. v~ in two bf16 terms, both multiplied by the exact bf16 k, keeps the final state within
+// 4e-6 (relative, against 64 bits; one term: 2e-3, and a third would cost 8 MMAs of 40 a chunk); P and the copy of S that q
+// multiplies are rounded once to bf16, like o.
 //
-// Decays: every factor is 2^x with x a sum of same-signed terms that starts at
-// the nearer end (prefixes within 32 tokens, suffixes within 32 tokens plus
-// whole-block totals), so its absolute error is a few units in the last place of
-// x itself, never of the chunk's total, and no factor exceeds 1.
+// Decays: every factor is 2^x with x a sum of same-signed terms that starts at the nearer end (prefixes within 32 tokens,
+// suffixes within 32 tokens plus whole-block totals), so its absolute error is a few units in the last place of x itself, never
+// of the chunk's total, and no factor exceeds 1 (but see EASY).
+//
+// Cut sequences (one or few long prompts): a launch makes the segments' states from zero (v, k and g alone), joins them to entry
+// states, E' = decay E + N, and then makes the outputs. That reads k and v twice, and takes 1.7 us more a chunk.
+//
+// Bound by latency: one chunk takes an SM 2.6 us, of 1.5 us of MMAs and 0.8 us of memory at an SM's share; the chain is
+// q S -> P v -> o -> next q S, with P (1.1 us) waiting for q k^T, which waits for the last P v: tensor memory holds no second
+// score tile beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 52 us; 8 of 2048: 59 us, 2.8 TB/s; one of 65536, 4
+// heads (cut in 37): 103 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -60,7 +64,9 @@ struct ChunkParams {
     int32_t seg_chunks;  // shortest cut that the workspace is sized for
     int32_t most_segs;   // that the workspace holds
     int32_t sms;
-    int32_t *counts;     // [0] segments, [1] the launch's barrier, [2] segments of the pass over the states (0: nothing is cut)
+    int32_t equal;       // leave sequences of equal lengths whole
+    int32_t *counts;     // [0] segments, [1] barrier between the passes, [2] segments of the pass over the states (0: nothing is cut),
+                         // [3] whether there is a plan
     int2 *first;         // [N] first slot and number of segments
     Segment *segs;       // the segments, long ones first
     Segment *segs_s;     // those of the pass over the states, long ones first
@@ -84,7 +90,8 @@ struct Misc {
     // 1..3 from tab_at(), 2^(sum of g after j up to the start of block a), j before it, and pre the log2 prefix within j's block
     alignas(16) float tab[192];
     alignas(16) float pre[C];
-    alignas(16) uint32_t w[2][C];        // 2^(sum of g after j up to the chunk's end), a chunk ahead
+    alignas(16) uint32_t w[2][C];     // 2^(sum of g after j up to the chunk's end), a chunk ahead: for a pair of tokens two bf16
+                                      // values and what they leave, in bf16
     float start[4];                   // log2 sum of g up to the start of each block
     float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
 };
@@ -103,9 +110,10 @@ constexpr int WARP_STORE = 4;  // of the scores' warps, the one with only masked
 // Registers: 28 warps launch with 72; the roles' shares add up to no more.
 constexpr int REGS = 72, REGS_SCORES = 72, REGS_STATE = 104, REGS_V = 48, REGS_AUX = 56;
 static_assert(8 * REGS_SCORES + 8 * REGS_STATE + 8 * REGS_V + 4 * REGS_AUX <= 28 * REGS, "the launch's registers");
-// A chunk whose whole decay is above 2^EASY needs no anchors: its scores are A_ij 2^-(sum of g up to j), at most 2^80 times
+// A chunk whose whole decay is above 2^EASY needs no anchors: its scores are A_ij 2^-(sum of g up to j), at most 2^48 times
 // their size, and the row's 2^(sum of g up to i) is left to the output, so that q S and P v add up as they are.
-constexpr float EASY = -80.f;
+// (A_ij v_j must stay below 2^79 then. Without this, q S is scaled in tensor memory between the two MMAs: 4 % more a chunk.)
+constexpr float EASY = -48.f;
 template <int N>
 __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -126,9 +134,9 @@ struct Task {
     bool skip;
 };
 
-// The roles' code is shared by the two passes of a segmented launch (SEG): `states` is true in the first. One copy of each:
-// an SM's instruction cache holds about one copy of all roles, and a role's first run through cold code costs as much as
-// two chunks.
+// The roles' code is shared by the two passes of a launch with segments (SEG): `states` is true in the first. One copy of each:
+// an SM's instruction cache holds about one copy of all roles, and a role's first run through cold code costs as much as two
+// chunks.
 template <bool SEG>
 __device__ __forceinline__ int tasks_of(const ChunkParams &p, bool states) {
     return SEG ? p.counts[states ? 2 : 0] * p.a.H : p.tasks;
@@ -481,9 +489,12 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
 
-// ---- eight warps: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
+// ---- warps 16-23: v~_j = 2^(sum of g after j) v_j in two bf16 terms, transposed into tensor memory. A warp has 32 value channels
 // (its quarter of the lanes) and 16 of every 32 tokens: ldmatrix transposes 8 x 8 blocks, and a tensor-memory store of the same
 // fragment shape puts each pair of tokens into its channel's lane.
+// With w = a + b in bf16, off by 2^-16 w at most: h = bf16(v a), and l = bf16(v b + (v a - h)), where v a - h has no more than 8
+// bits and is exact, and l, of 2^-7 v w at most, is rounded by 2^-8 of itself. So h + l is off by 3 / 2^16 of v w at most (4e-6 of
+// a state in all), in three instructions for a pair of tokens; from fp32 products it took eight, and 2.3e-6.
 template <bool SEG>
 __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
     const int gtid = threadIdx.x & (GROUP - 1), lane = gtid & 31, quad = (gtid >> 5) & 3, half = gtid >> 7;
@@ -858,31 +869,6 @@ __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
     }
 }
 
-// Touches the pages that this CTA's part of the join and its first output task begin in, from warps that the pass over the
-// states leaves idle: an SM's first access to a page costs microseconds when all SMs make theirs at once.
-__device__ __forceinline__ void touch(const void *p) {
-    asm volatile("{\n\t.reg .b32 x;\n\tld.volatile.global.u32 x, [%0];\n\t}" ::"l"(p) : "memory");
-}
-__device__ __forceinline__ void touch_ahead(const ChunkParams &p) {
-    const int tid = threadIdx.x;
-    const int tasks = tasks_of<true>(p, false), id = blockIdx.x;
-    constexpr size_t SZ = static_cast<size_t>(DK) * DV;
-    if (id >= tasks) return;
-    const Task t = task_of<true>(p, id, false);
-    if (t.len > 0) {
-        const int hk = t.h / p.a.rep;
-        if (tid == 0) touch(p.a.q + t.t0 * p.a.qs + hk * DK);
-        if (tid == 1) touch(p.a.o + (t.t0 * p.a.H + t.h) * DV);
-        if (tid == 2) touch(p.a.g + (p.a.g_per_token ? t.t0 * p.a.H + t.h : t.h));
-    }
-    if (tid == 3 && t.sin) touch(t.sin);
-    if (tid == 4 && t.sout) touch(t.sout);
-    if (tid < 64) {
-        const size_t all = static_cast<size_t>(tasks) * SZ, at = static_cast<size_t>(tid) << 19;  // every 2 MB of the states
-        if (at < all) touch(p.states + at);
-    }
-}
-
 constexpr int BARRIERS = offsetof(Misc, tmem) / sizeof(uint64_t);  // they come first in Misc
 __device__ __forceinline__ int arrivals_of(int i, bool states) {
     constexpr int E0 = offsetof(Misc, empty) / 8, V0 = offsetof(Misc, vt) / 8, P0 = offsetof(Misc, p) / 8,
@@ -915,78 +901,18 @@ __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
     return *reinterpret_cast<volatile int32_t *>(&m->abort) == 0;
 }
 
-// SEGMENTS: sequences in segments, states first (a cooperative launch); else every sequence as a whole
-template <bool SEGMENTS>
-__global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
-    extern __shared__ __align__(1024) unsigned char smem[];
-    Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool cut = SEGMENTS && p.counts[2] > 0;  // two passes
-    if (warp == 0) {
-        init_barriers(m, cut);
-        m->abort = 0;
-    }
-    if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = m->tmem;
-    // every role: the pass over the states, the join, the pass over the outputs; or the last alone
-    if (warp < 8) {
-        if (cut) touch_ahead(p);
-        if (!cut || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
-    } else if (warp < 16) {
-        more_registers<REGS_STATE>();
-#pragma unroll 1
-        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
-            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
-            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
-        }
-    } else if (warp < 24) {
-        fewer_registers<REGS_V>();
-#pragma unroll 1
-        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
-            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
-            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
-        }
-    } else {
-        fewer_registers<REGS_AUX>();
-#pragma unroll 1
-        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
-            const bool states = SEGMENTS && pass == 0;
-            if (warp == WARP_LOAD) {
-                if (lane == 0) role_load<SEGMENTS>(p, smem, m, states);
-            } else if (warp == WARP_DECAY) {
-                role_decay<SEGMENTS>(p, m, states);
-            } else if (warp == WARP_MMA_U) {
-                role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
-            } else if (warp == WARP_MMA_OUT && !states) {
-                role_mma_out<SEGMENTS>(p, smem, m, tmem);
-            }
-            __syncwarp();
-            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
-        }
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    if (threadIdx.x == 0 && m->abort) set_status(p.a.status, KDA_ERR_TIMEOUT);
-    if (warp == WARP_MMA_U) tmem_dealloc(tmem, 512);
-}
-
 // ---- segments: one CTA decides whether and how to cut, and sorts. Sequence n of c chunks gets ceil(c / L) segments of about
 // equal length, for the L of a few that is estimated to be fastest with these lengths. The estimate of a cut into no more than
 // SORTED segments is that of the busiest SM under the order in which the segments will be taken, found by sorting them; more
 // segments stay in the order of the sequences, and are taken to be of average length.
-constexpr int CUTS = 6, SORTED = 384, PLAN_GROUP = 128, PLAN_THREADS = CUTS * PLAN_GROUP;
+constexpr int CUTS = 7, SORTED = 384, PLAN_GROUP = 128, PLAN_THREADS = CUTS * PLAN_GROUP;
 // Fitted to 90 timings on GB300 (15 batches, each with the six cuts), in microseconds: a chunk and a task of the pass over the
 // outputs and of that over the states, the outputs' chunks when memory bounds all SMs, the join and its barriers, and the join of
 // a segment. Each of the 15 was within 1 % of the best of its six. (A task costs this much where tasks are few: its first chunk
 // goes alone through all roles.)
-constexpr float T_OUT = 2.7f, T_OUT_TASK = 9.f, T_STATES = 1.7f, T_STATES_TASK = 6.f, T_OUT_ALL = 3.2f, T_CUT = 8.f, T_JOIN = 0.2f,
-                T_PLAN = 5.f;
+constexpr float T_OUT = 2.7f, T_OUT_TASK = 9.f, T_STATES = 1.7f, T_STATES_TASK = 6.f, T_OUT_ALL = 3.2f, T_CUT = 8.f, T_JOIN = 0.2f;
 
-__host__ __device__ inline int cut_length(int i, int shortest) {  // candidates: no cut, then 1, 1.5, 2, 3, 4 times the shortest
+__host__ __device__ inline int cut_length(int i, int shortest) {  // candidates: no cut, then 1, 1.5, 2, 3, 4, 5 times the shortest
     return i == 0 ? 0x3fffffff : i == 1 ? shortest : i == 2 ? shortest + (shortest + 1) / 2 : shortest * (i - 1);
 }
 __host__ __device__ inline int pieces(int c, int len) { return c <= len ? 1 : (c + len - 1) / len; }
@@ -1021,7 +947,7 @@ struct PlanShared {
     int count[CUTS], total_s, best;  // segments of the pass over the states
 };
 
-__global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const __grid_constant__ ChunkParams p) {
     __shared__ PlanShared m;
     const Params &a = p.a;
     const int tid = threadIdx.x, i = tid / PLAN_GROUP, x0 = tid % PLAN_GROUP;  // candidate, and thread of its group
@@ -1032,6 +958,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const Chu
         const int64_t b = a.cu[n], e = a.cu[n + 1];
         return start_ok && b >= 0 && e >= b && e <= a.T ? static_cast<int>((e - b + C - 1) / C) : -1;
     };
+    if (p.equal) {
+        const int64_t each = a.T / a.N;
+        bool equal = true;
+        for (int n = tid; n <= a.N; n += PLAN_THREADS) equal = equal && a.cu[n] == n * each;
+        if (__syncthreads_and(equal)) {
+            if (tid == 0) p.counts[3] = 0;
+            return;
+        }
+    }
     if (tid < CUTS) m.cuts[tid] = Cut{};
     if (tid < 2 * CUTS) m.time[tid >> 1][tid & 1] = 0;
     if (tid < CUTS) m.count[tid] = 0;
@@ -1074,6 +1009,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const Chu
         if (tid == 0) {
             set_status(a.status, KDA_ERR_BAD_SEQLENS);
             p.counts[0] = p.counts[1] = p.counts[2] = 0;
+            p.counts[3] = 1;
         }
         return;
     }
@@ -1135,43 +1071,111 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const Chu
         }
     }
     __syncthreads();
-    if (i != m.best) return;  // the chosen candidate's group writes
-    auto segment = [&](int n, int j, int slot) {
-        const int64_t from = a.cu[n], to = a.cu[n + 1];
-        const int c = static_cast<int>((to - from + C - 1) / C), k = pieces(c, len);
-        Segment s;
-        s.t0 = static_cast<int32_t>(from + static_cast<int64_t>(begin(c, k, j)) * C);
-        s.len = static_cast<int32_t>(j == k - 1 ? to - s.t0 : (begin(c, k, j + 1) - begin(c, k, j)) * C);
-        s.seq = n;
-        s.index = j;
-        s.count = k;
-        s.slot = slot;
-        return s;
-    };
-    int at = first;
-    for (int n = n0; n < n1; ++n) {
-        const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
-        if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
-        p.first[n] = make_int2(at, k);
-        for (int j = 0; !sort && j < k; ++j) {
-            const Segment s = segment(n, j, at + j);
-            p.segs[at + j] = s;
-            if (states_len(0, k, j) >= 0) p.segs_s[atomicAdd(&m.total_s, 1)] = s;
+    if (i == m.best) {  // the chosen candidate's group writes
+        auto segment = [&](int n, int j, int slot) {
+            const int64_t from = a.cu[n], to = a.cu[n + 1];
+            const int c = static_cast<int>((to - from + C - 1) / C), k = pieces(c, len);
+            Segment s;
+            s.t0 = static_cast<int32_t>(from + static_cast<int64_t>(begin(c, k, j)) * C);
+            s.len = static_cast<int32_t>(j == k - 1 ? to - s.t0 : (begin(c, k, j + 1) - begin(c, k, j)) * C);
+            s.seq = n;
+            s.index = j;
+            s.count = k;
+            s.slot = slot;
+            return s;
+        };
+        int at = first;
+        for (int n = n0; n < n1; ++n) {
+            const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
+            if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            p.first[n] = make_int2(at, k);
+            for (int j = 0; !sort && j < k; ++j) {
+                const Segment s = segment(n, j, at + j);
+                p.segs[at + j] = s;
+                if (states_len(0, k, j) >= 0) p.segs_s[atomicAdd(&m.total_s, 1)] = s;
+            }
+            at += k;
         }
-        at += k;
-    }
-    if (sort)
-        for (int r = x0; r < total; r += PLAN_GROUP) {
-            const int x = t.order[0][r], y = r < m.count[i] ? t.order[1][r] : -1;
-            p.segs[r] = segment(t.seq[x], t.index[x], x);
-            if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], y);
+        if (sort)
+            for (int r = x0; r < total; r += PLAN_GROUP) {
+                const int x = t.order[0][r], y = r < m.count[i] ? t.order[1][r] : -1;
+                p.segs[r] = segment(t.seq[x], t.index[x], x);
+                if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], y);
+            }
+        named_bar_sync(1, PLAN_GROUP);  // (the others have left)
+        if (x0 == 0) {
+            p.counts[0] = total;
+            p.counts[1] = 0;
+            p.counts[2] = sort ? m.count[i] : m.total_s;
+            p.counts[3] = 1;
         }
-    named_bar_sync(1, PLAN_GROUP);  // (the others have left)
-    if (x0 == 0) {
-        p.counts[0] = total;
-        p.counts[1] = 0;
-        p.counts[2] = sort ? m.count[i] : m.total_s;
     }
+}
+
+// SEGMENTS: the plan's segments, states first if something is cut; else every sequence as a whole
+template <bool SEGMENTS>
+__device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *smem) {
+    Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool cut = SEGMENTS && p.counts[2] > 0;  // two passes
+    if (warp == 0) {
+        init_barriers(m, cut);
+        m->abort = 0;
+    }
+    if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+    // every role: the pass over the states, the join, the pass over the outputs; or the last alone
+    if (warp < 8) {
+        if (!cut || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
+    } else if (warp < 16) {
+        more_registers<REGS_STATE>();
+#pragma unroll 1
+        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
+            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
+        }
+    } else if (warp < 24) {
+        fewer_registers<REGS_V>();
+#pragma unroll 1
+        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
+            role_v<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
+        }
+    } else {
+        fewer_registers<REGS_AUX>();
+#pragma unroll 1
+        for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
+            const bool states = SEGMENTS && pass == 0;
+            if (warp == WARP_LOAD) {
+                if (lane == 0) role_load<SEGMENTS>(p, smem, m, states);
+            } else if (warp == WARP_DECAY) {
+                role_decay<SEGMENTS>(p, m, states);
+            } else if (warp == WARP_MMA_U) {
+                role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
+            } else if (warp == WARP_MMA_OUT && !states) {
+                role_mma_out<SEGMENTS>(p, smem, m, tmem);
+            }
+            __syncwarp();
+            if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && m->abort) set_status(p.a.status, KDA_ERR_TIMEOUT);
+    if (warp == WARP_MMA_U) tmem_dealloc(tmem, 512);
+}
+
+// Two copies of the roles, one runs: in the code with both passes, whole sequences take 10 % longer.
+__global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    if (p.seg_chunks && p.counts[3])
+        run_roles<true>(p, smem);
+    else
+        run_roles<false>(p, smem);
 }
 
 }  // namespace
@@ -1213,18 +1217,17 @@ int num_sms() {
     return sms;
 }
 
-template <bool SEGMENTS>
 cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
-    const auto kernel = kda_linear_chunk_kernel<SEGMENTS>;
+    const auto kernel = kda_linear_chunk_kernel;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     static const int regs = [] {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<SEGMENTS>) == cudaSuccess ? at.numRegs : 0;
+        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
     const int grid = static_cast<int>(most_tasks < sms ? most_tasks : sms);
-    if (SEGMENTS) {
+    if (p.seg_chunks) {
         void *args[] = {const_cast<ChunkParams *>(&p)};
         return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(THREADS), args, SMEM, stream);
     }
@@ -1235,27 +1238,26 @@ cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t 
 // Sequences of few tokens run the recurrence.
 bool few_tokens(int64_t N, int64_t T) { return T <= 16 * N; }
 
-// The shortest cut of sequences worth a try, about half an SM's share of the chunks; 0 when nothing is to be cut: no sequence can
-// be longer, or they can all be of one length (tokens a multiple of sequences) and are estimated to be as fast whole. (A batch
-// of unequal lengths that passes for equal runs correctly, only perhaps slower.)
+// The shortest cut of sequences worth a try, about half an SM's share of the chunks; 0 when no sequence can be longer.
 int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
     const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
     int64_t len = (all + 2 * sms - 1) / (2 * sms);
     if (len < 4) len = 4;
-    if (longest <= len) return 0;
-    if (T % N == 0) {
-        const int64_t each = (T / N + C - 1) / C;
-        auto time_of = [&](int64_t cut) {
-            const int64_t k = (each + cut - 1) / cut, one = (each + k - 1) / k;
-            return cut_time({static_cast<int>(one), static_cast<int>(k), static_cast<int>(k * N), static_cast<int>(each * N),
-                             static_cast<int>((k - 1) * N), static_cast<int>((each - one) * N)}, static_cast<int>(H), sms);
-        };
-        const float whole = time_of(each);
-        float best = 3.0e38f;
-        for (int i = 1; i < CUTS; ++i) best = std::fmin(best, time_of(cut_length(i, static_cast<int>(len))));
-        if (whole <= best + T_PLAN) return 0;
-    }
-    return static_cast<int>(len);
+    return longest <= len ? 0 : static_cast<int>(len);
+}
+// Sequences of equal lengths are estimated to be as fast whole as cut (4 x 2048, 16 heads: 52 us, cut 60). The plan kernel then
+// looks whether they are equal, and makes no plan if so: the host does not know, and a padded batch looks the same to it.
+bool whole_if_equal(int64_t N, int64_t T, int64_t H, int len, int sms) {
+    if (T % N) return false;
+    const int64_t each = (T / N + C - 1) / C;
+    auto time_of = [&](int64_t cut) {
+        const int64_t k = (each + cut - 1) / cut, one = (each + k - 1) / k;
+        return cut_time({static_cast<int>(one), static_cast<int>(k), static_cast<int>(k * N), static_cast<int>(each * N),
+                         static_cast<int>((k - 1) * N), static_cast<int>((each - one) * N)}, static_cast<int>(H), sms);
+    };
+    float best = 3.0e38f;
+    for (int i = 1; i < CUTS; ++i) best = std::fmin(best, time_of(cut_length(i, len)));
+    return time_of(each) <= best;
 }
 
 struct Layout {
@@ -1295,7 +1297,8 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
         return cudaErrorInvalidValue;
     p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
-    if (!p.seg_chunks) return run<false>(p, p.tasks, sms, stream);
+    if (!p.seg_chunks) return run(p, p.tasks, sms, stream);
+    p.equal = whole_if_equal(a.N, a.T, a.H, p.seg_chunks, sms);
     const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.most_segs = static_cast<int32_t>(l.most);
@@ -1308,7 +1311,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.states = reinterpret_cast<float *>(ws + l.states);
     kda_linear_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? run<true>(p, l.most * a.H, sms, stream) : e;
+    return e == cudaSuccess ? run(p, l.most * a.H, sms, stream) : e;
 }
 
 }  // namespace lin
