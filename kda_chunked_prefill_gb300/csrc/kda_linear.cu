@@ -31,12 +31,13 @@
 //
 // Bound by latency: one chunk takes an SM 2.6 us, of 1.5 us of MMAs and 0.8 us of memory at an SM's share; the chain is
 // q S -> P v -> o -> next q S, with P (1.1 us) waiting for q k^T, which waits for the last P v: tensor memory holds no second
-// score tile beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 52 us; 8 of 2048: 59 us, 2.8 TB/s; one of 65536, 4
+// score tile beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 50 us; 8 of 2048: 57 us, 4.9 TB/s; one of 65536, 4
 // heads (cut in 37): 103 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "kda.h"
@@ -64,9 +65,9 @@ struct ChunkParams {
     int32_t seg_chunks;  // shortest cut that the workspace is sized for
     int32_t most_segs;   // that the workspace holds
     int32_t sms;
-    int32_t equal;       // leave sequences of equal lengths whole
     int32_t *counts;     // [0] segments, [1] barrier between the passes, [2] segments of the pass over the states (0: nothing is cut),
-                         // [3] whether there is a plan
+                         // [3] CTAs that have the plan
+    unsigned long long *go, token;  // the plan is there
     int2 *first;         // [N] first slot and number of segments
     Segment *segs;       // the segments, long ones first
     Segment *segs_s;     // those of the pass over the states, long ones first
@@ -905,7 +906,8 @@ __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
 // equal length, for the L of a few that is estimated to be fastest with these lengths. The estimate of a cut into no more than
 // SORTED segments is that of the busiest SM under the order in which the segments will be taken, found by sorting them; more
 // segments stay in the order of the sequences, and are taken to be of average length.
-constexpr int CUTS = 7, SORTED = 384, PLAN_GROUP = 128, PLAN_THREADS = CUTS * PLAN_GROUP;
+constexpr int CUTS = 7, SORTED = 384, PLAN_GROUP = THREADS / CUTS;
+static_assert(PLAN_GROUP == 128, "four warps a candidate");
 // Fitted to 90 timings on GB300 (15 batches, each with the six cuts), in microseconds: a chunk and a task of the pass over the
 // outputs and of that over the states, the outputs' chunks when memory bounds all SMs, the join and its barriers, and the join of
 // a segment. Each of the 15 was within 1 % of the best of its six. (A task costs this much where tasks are few: its first chunk
@@ -947,8 +949,16 @@ struct PlanShared {
     int count[CUTS], total_s, best;  // segments of the pass over the states
 };
 
-__global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const __grid_constant__ ChunkParams p) {
-    __shared__ PlanShared m;
+// every sequence as long as the next
+__device__ __forceinline__ bool equal_lengths(const ChunkParams &p) {
+    const int64_t each = p.a.T / p.a.N;
+    bool equal = true;
+    for (int n = threadIdx.x; n <= p.a.N; n += THREADS) equal = equal && p.a.cu[n] == n * each;
+    return __syncthreads_and(equal);
+}
+
+// all threads of one CTA; the others wait for it
+__device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     const Params &a = p.a;
     const int tid = threadIdx.x, i = tid / PLAN_GROUP, x0 = tid % PLAN_GROUP;  // candidate, and thread of its group
     const int len = cut_length(i, p.seg_chunks);
@@ -958,15 +968,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const __g
         const int64_t b = a.cu[n], e = a.cu[n + 1];
         return start_ok && b >= 0 && e >= b && e <= a.T ? static_cast<int>((e - b + C - 1) / C) : -1;
     };
-    if (p.equal) {
-        const int64_t each = a.T / a.N;
-        bool equal = true;
-        for (int n = tid; n <= a.N; n += PLAN_THREADS) equal = equal && a.cu[n] == n * each;
-        if (__syncthreads_and(equal)) {
-            if (tid == 0) p.counts[3] = 0;
-            return;
-        }
-    }
     if (tid < CUTS) m.cuts[tid] = Cut{};
     if (tid < 2 * CUTS) m.time[tid >> 1][tid & 1] = 0;
     if (tid < CUTS) m.count[tid] = 0;
@@ -1009,7 +1010,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const __g
         if (tid == 0) {
             set_status(a.status, KDA_ERR_BAD_SEQLENS);
             p.counts[0] = p.counts[1] = p.counts[2] = 0;
-            p.counts[3] = 1;
         }
         return;
     }
@@ -1102,14 +1102,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) kda_linear_plan_kernel(const __g
                 p.segs[r] = segment(t.seq[x], t.index[x], x);
                 if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], y);
             }
-        named_bar_sync(1, PLAN_GROUP);  // (the others have left)
+        named_bar_sync(1, PLAN_GROUP);
         if (x0 == 0) {
             p.counts[0] = total;
             p.counts[1] = 0;
             p.counts[2] = sort ? m.count[i] : m.total_s;
-            p.counts[3] = 1;
         }
     }
+    fence_proxy_async_shared();  // the tiles come to the same place
 }
 
 // SEGMENTS: the plan's segments, states first if something is cut; else every sequence as a whole
@@ -1169,13 +1169,49 @@ __device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *s
     if (warp == WARP_MMA_U) tmem_dealloc(tmem, 512);
 }
 
-// Two copies of the roles, one runs: in the code with both passes, whole sequences take 10 % longer.
+// CTA 0 plans, and the others wait for the launch's token in the workspace, which the last of them takes away again: the memory
+// may hold anything, or what an earlier launch with the same arguments left (a replayed graph). False: the wait ran out.
+__device__ __forceinline__ bool wait_for_plan(const ChunkParams &p, unsigned char *smem) {
+    if (blockIdx.x == 0) {
+        plan(p, *reinterpret_cast<PlanShared *>(smem));
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            p.counts[3] = 0;
+            __threadfence();
+            *reinterpret_cast<volatile unsigned long long *>(p.go) = gridDim.x > 1 ? p.token : 0;
+        }
+        __syncthreads();
+        return true;
+    }
+    bool ok = true;
+    if (threadIdx.x == 0) {
+        ok = false;
+#pragma unroll 1
+        for (int i = 0; !ok && i < GRID_POLLS; ++i) {
+            ok = *reinterpret_cast<volatile unsigned long long *>(p.go) == p.token;
+            if (!ok) __nanosleep(64);
+        }
+        __threadfence();
+        if (ok && atomicAdd(p.counts + 3, 1) == gridDim.x - 2) *reinterpret_cast<volatile unsigned long long *>(p.go) = 0;
+    }
+    return __syncthreads_and(ok);
+}
+
+static_assert(sizeof(PlanShared) <= OFF_MISC, "the plan lies where the tiles will");
+// What a launch may turn out to be. Two copies of the roles where it may be either: in the code with both passes, whole sequences
+// take 10 % longer. A kernel with only one of them takes 1 to 5 % less than one with both.
+enum Mode { WHOLE, PLANNED, EITHER };
+template <Mode MODE>
 __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __grid_constant__ ChunkParams p) {
     extern __shared__ __align__(1024) unsigned char smem[];
-    if (p.seg_chunks && p.counts[3])
-        run_roles<true>(p, smem);
-    else
-        run_roles<false>(p, smem);
+    if (MODE == WHOLE || (MODE == EITHER && equal_lengths(p))) {
+        if (MODE != PLANNED) run_roles<false>(p, smem);
+    } else if (MODE != WHOLE) {
+        if (wait_for_plan(p, smem))
+            run_roles<true>(p, smem);
+        else if (threadIdx.x == 0)
+            set_status(p.a.status, KDA_ERR_TIMEOUT);
+    }
 }
 
 }  // namespace
@@ -1217,17 +1253,18 @@ int num_sms() {
     return sms;
 }
 
+template <Mode MODE>
 cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t stream) {
-    const auto kernel = kda_linear_chunk_kernel;
+    const auto kernel = kda_linear_chunk_kernel<MODE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     static const int regs = [] {
         cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel) == cudaSuccess ? at.numRegs : 0;
+        return cudaFuncGetAttributes(&at, kda_linear_chunk_kernel<MODE>) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != REGS) return cudaErrorInvalidConfiguration;  // the roles' register split adds up to this
     const int grid = static_cast<int>(most_tasks < sms ? most_tasks : sms);
-    if (p.seg_chunks) {
+    if (MODE != WHOLE) {
         void *args[] = {const_cast<ChunkParams *>(&p)};
         return cudaLaunchCooperativeKernel(reinterpret_cast<const void *>(kernel), dim3(grid), dim3(THREADS), args, SMEM, stream);
     }
@@ -1245,8 +1282,8 @@ int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
     if (len < 4) len = 4;
     return longest <= len ? 0 : static_cast<int>(len);
 }
-// Sequences of equal lengths are estimated to be as fast whole as cut (4 x 2048, 16 heads: 52 us, cut 60). The plan kernel then
-// looks whether they are equal, and makes no plan if so: the host does not know, and a padded batch looks the same to it.
+// Sequences of equal lengths are estimated to be as fast whole as cut (4 x 2048, 16 heads: 50 us, cut 60). Every CTA
+// then looks whether they are equal, and none plans if so: the host does not know, and a padded batch looks the same to it.
 bool whole_if_equal(int64_t N, int64_t T, int64_t H, int len, int sms) {
     if (T % N) return false;
     const int64_t each = (T / N + C - 1) / C;
@@ -1297,8 +1334,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
         return cudaErrorInvalidValue;
     p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
-    if (!p.seg_chunks) return run(p, p.tasks, sms, stream);
-    p.equal = whole_if_equal(a.N, a.T, a.H, p.seg_chunks, sms);
+    if (!p.seg_chunks) return run<WHOLE>(p, p.tasks, sms, stream);
     const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.most_segs = static_cast<int32_t>(l.most);
@@ -1309,9 +1345,11 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.segs_s = reinterpret_cast<Segment *>(ws + l.segs_s);
     p.decays = reinterpret_cast<float *>(ws + l.decays);
     p.states = reinterpret_cast<float *>(ws + l.states);
-    kda_linear_plan_kernel<<<1, PLAN_THREADS, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? run(p, l.most * a.H, sms, stream) : e;
+    p.go = reinterpret_cast<unsigned long long *>(ws + 32);
+    static std::atomic<unsigned long long> calls{0};
+    p.token = (++calls + static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(&calls))) * 0x9e3779b97f4a7c15ull;
+    return whole_if_equal(a.N, a.T, a.H, p.seg_chunks, sms) ? run<EITHER>(p, l.most * a.H, sms, stream)
+                                                            : run<PLANNED>(p, l.most * a.H, sms, stream);
 }
 
 }  // namespace lin
