@@ -29,10 +29,10 @@
 // Cut sequences (one or few long prompts): a launch makes the segments' states from zero (v, k and g alone), joins them to entry
 // states, E' = decay E + N, and then makes the outputs. That reads k and v twice, and takes 1.7 us more a chunk.
 //
-// Bound by latency: one chunk takes an SM 2.6 us, of 1.5 us of MMAs and 0.8 us of memory at an SM's share; the chain is
-// q S -> P v -> o -> next q S, with P (1.1 us) waiting for q k^T, which waits for the last P v: tensor memory holds no second
-// score tile beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 50 us; 8 of 2048: 57 us, 4.9 TB/s; one of 65536, 4
-// heads (cut in 37): 103 us.
+// Bound by latency: one chunk takes an SM 2.6 us, with 1.5 us of MMAs and 0.8 us of memory at an SM's share. The chain is
+// q k^T -> P (1.2 us) -> P v (0.6) -> o (0.4) -> q k^T of the next chunk (0.4), because tensor memory holds no second score tile
+// beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 50 us; 8 of 2048: 56 us, 4.9 TB/s; one of 65536, 4 heads (cut in
+// 37): 104 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -1272,8 +1272,10 @@ cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t 
     return cudaGetLastError();
 }
 
-// Sequences of few tokens run the recurrence.
-bool few_tokens(int64_t N, int64_t T) { return T <= 16 * N; }
+// Sequences of few tokens run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 128.
+// 16 heads, 17 tokens each: 4 sequences 17.3 us and as chunks 8.7, 64 sequences 103 and 50, 256 sequences 352 and 178; a token
+// more or less is 0.8, 4.9 and 17.6 us of the recurrence, so they meet at 6 to 7 tokens.
+bool few_tokens(int64_t N, int64_t T) { return T <= 6 * N; }
 
 // The shortest cut of sequences worth a try, about half an SM's share of the chunks; 0 when no sequence can be longer.
 int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
