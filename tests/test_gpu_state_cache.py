@@ -140,8 +140,56 @@ def test_serving_run():
         got = torch.cat([o1[cuts[i]:cuts[i + 1]], o2[2 * i:2 * i + 2]]).double().cpu().numpy()
         want, sz = ro[first[i]:first[i + 1]], size[first[i]:first[i + 1]]
         assert (np.abs(got - want) <= 2.0 ** -8 * (1.01 * np.abs(want) + 1.1 * sz) + 1e-30).all()
-    assert (np.abs(s2.double().cpu().numpy() - rs) <= (2.0 ** -16 + 1200 * 2.0 ** -24) * rsize).all()
+    # 3.03 u^2, u = 2^-8: the two-term operands of the state's update (derived in test_gpu_linear.py)
+    assert (np.abs(s2.double().cpu().numpy() - rs) <= (3.03 * 2.0 ** -16 + 1200 * 2.0 ** -24) * rsize).all()
     kda.state_store(s2, torch.tensor([6, 0, 2], dtype=torch.int32, device="cuda"), codes, scales, check=True)
     again = kda.state_load(codes, scales, torch.tensor([6, 0, 2], dtype=torch.int32, device="cuda"))
     amax = s2.abs().amax(-1, keepdim=True)
     assert bool(((again - s2).abs() <= amax / 254 + amax * 2.0 ** -20).all())
+
+
+def test_layer_run_in_a_graph():
+    """Norm, projection, load, prompt, store, captured once and replayed on new inputs: as the same calls made one by one, and the
+    prompt as the recurrence over what the projection made."""
+    H, Hk, width, lens = 4, 2, 256, [300, 20, 129]
+    T = sum(lens)
+    gen = torch.Generator().manual_seed(50)
+    rand = lambda *shape: torch.randn(*shape, generator=gen)
+    x, residual, weight = rand(T, width).bfloat16().cuda(), rand(T, width).cuda(), (1 + 0.1 * rand(width)).cuda()
+    w_qkv = (rand(width, (2 * Hk + H) * D) * 0.01).bfloat16().cuda()
+    g = (-torch.rand(H, generator=gen) * 0.2).cuda()
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    codes, scales = cache(6, H)
+    kda.state_store(states(3, H, 51).cuda() * 0.1, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), codes, scales)
+    slots_in, slots_out = (torch.tensor(i, dtype=torch.int32, device="cuda") for i in ([2, -1, 0], [3, 4, 5]))
+
+    def layer():
+        y, y_scale, res = kda.add_rms_norm(x, residual, weight, 1e-6)
+        qkv = (y.float() * y_scale[:, None]).bfloat16() @ w_qkv
+        q, k, v = (t.view(T, -1, D) for t in qkv.split([Hk * D, Hk * D, H * D], dim=1))
+        s0 = kda.state_load(codes, scales, slots_in)
+        o, state = kda.linear_chunk_fwd(q, k, v, g, cu, s0)
+        kda.state_store(state, slots_out, codes, scales)
+        return q, k, v, s0, o, state, res
+
+    layer()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer()
+    for _ in range(2):
+        x.copy_(rand(T, width).bfloat16())
+        residual.copy_(rand(T, width))
+        graph.replay()
+        torch.cuda.synchronize()
+        got, stored = [t.clone() for t in out], (codes.clone(), scales.clone())
+        codes[3:], scales[3:] = 0, 0
+        want = layer()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(codes, stored[0]) and torch.equal(scales, stored[1])
+        q, k, v, s0, o, state, res = (t.double().cpu().numpy() for t in got)
+        assert np.array_equal(res, (x.float() + residual).double().cpu().numpy())
+        ro, size, rs, rsize = ref.recurrence(q, k, v, np.broadcast_to(g.double().cpu().numpy(), (T, H)), lens, s0, D ** -0.5)
+        # as in test_gpu_linear.py: one rounding of o, one of each score and of the state's copy, fp32 sums
+        assert (np.abs(o - ro) <= 2.0 ** -8 * (1.01 * np.abs(ro) + 1.05 * size) + 1200 * 2.0 ** -24 * size + 1e-30).all()
+        assert (np.abs(state - rs) <= (3.03 * 2.0 ** -16 + 1200 * 2.0 ** -24) * rsize).all()
