@@ -66,9 +66,9 @@ struct ChunkParams {
     int32_t most_segs;   // that the workspace holds
     int32_t sms;
     int32_t *counts;     // [0] segments, [1] barrier between the passes, [2] segments of the pass over the states (0: nothing is cut),
-                         // [3] CTAs that have the plan
+                         // [3] CTAs that have the plan, [6] sequences to join
     unsigned long long *go, token;  // the plan is there
-    int2 *first;         // [N] first slot and number of segments
+    int2 *first;         // first slot and number of segments of each sequence to join
     Segment *segs;       // the segments, long ones first
     Segment *segs_s;     // those of the pass over the states, long ones first
     float *decays;       // [slot][head], minus one
@@ -841,10 +841,10 @@ __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
     const int H = p.a.H;
     const size_t step = static_cast<size_t>(H) * UNITS;  // from segment to segment
 #pragma unroll 1
-    for (int n = 0; n < p.a.N; ++n) {
+    for (int n = 0; n < p.counts[6]; ++n) {
         const int2 f = p.first[n];
 #pragma unroll 1
-        for (uint32_t u = blockIdx.x * GROUP + gtid; f.y > 2 && u < static_cast<uint32_t>(H) * UNITS; u += gridDim.x * GROUP) {
+        for (uint32_t u = blockIdx.x * GROUP + gtid; u < static_cast<uint32_t>(H) * UNITS; u += gridDim.x * GROUP) {
             f2 *s = reinterpret_cast<f2 *>(p.states) + f.x * step + u;
             const float *d = p.decays + static_cast<int64_t>(f.x) * H + u / UNITS;
             f2 e = __ldcg(s);
@@ -946,7 +946,7 @@ struct PlanShared {
     Cut cuts[CUTS];
     int time[CUTS][2];  // of the passes: bits of a positive float
     int warps[CUTS][PLAN_GROUP / 32];
-    int count[CUTS], total_s, best;  // segments of the pass over the states
+    int count[CUTS], total_s, best, cut;  // segments of the pass over the states; sequences cut in more than two
 };
 
 // every sequence as long as the next
@@ -971,23 +971,29 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     if (tid < CUTS) m.cuts[tid] = Cut{};
     if (tid < 2 * CUTS) m.time[tid >> 1][tid & 1] = 0;
     if (tid < CUTS) m.count[tid] = 0;
-    if (tid == 0) m.total_s = 0;
+    if (tid == 0) m.total_s = m.cut = 0;
     __syncthreads();
     // each group: its candidate's segments, and the first slot of each thread's sequences
     const int per = (a.N + PLAN_GROUP - 1) / PLAN_GROUP, n0 = x0 * per, n1 = n0 + per < a.N ? n0 + per : a.N;
+    Cut own{};
     int mine = 0;  // (saturating: offsets that are no offsets can add up to anything)
     for (int n = n0; n < n1; ++n) {
         const int c = chunks(n);
         if (c < 0) continue;
         const int k = pieces(c, len), one = (c + k - 1) / k;
         mine = min(mine + k, p.most_segs + 1);
-        atomicMax(&m.cuts[i].longest, one);
-        atomicMax(&m.cuts[i].most, k);
-        atomicAdd(&m.cuts[i].all, c);
-        if (k > 1) {
-            atomicAdd(&m.cuts[i].tasks_s, k - 1);
-            atomicAdd(&m.cuts[i].all_s, c - one);
-        }
+        own.longest = max(own.longest, one);
+        own.most = max(own.most, k);
+        own.all += c;
+        own.tasks_s += k - 1;
+        own.all_s += c - one;  // (0 of a sequence that is not cut)
+    }
+    if (n0 < n1) {
+        atomicMax(&m.cuts[i].longest, own.longest);
+        atomicMax(&m.cuts[i].most, own.most);
+        atomicAdd(&m.cuts[i].all, own.all);
+        atomicAdd(&m.cuts[i].tasks_s, own.tasks_s);
+        atomicAdd(&m.cuts[i].all_s, own.all_s);
     }
     int upto = mine;  // sums over the threads up to this one
 #pragma unroll
@@ -1015,7 +1021,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     }
     if (x0 == 0) m.cuts[i].tasks = total;
     Sorted &t = m.sorted[i];
-    const bool sort = total <= SORTED;
+    const bool sort = total <= SORTED && a.N <= 0xffff;  // (a table's entry has 16 bits)
     if (sort) {
         int at = first;
         for (int n = n0; n < n1; ++n) {
@@ -1065,7 +1071,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
         m.best = 0;
         for (int j = 0; j < CUTS; ++j) {
             const Cut &c = m.cuts[j];
-            const float time = c.tasks <= SORTED ? cut_time(c, a.H, p.sms, __int_as_float(m.time[j][0]), __int_as_float(m.time[j][1]))
+            const float time = c.tasks <= SORTED && a.N <= 0xffff ? cut_time(c, a.H, p.sms, __int_as_float(m.time[j][0]), __int_as_float(m.time[j][1]))
                                                  : cut_time(c, a.H, p.sms);
             if (time < least) least = time, m.best = j;
         }
@@ -1088,7 +1094,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
         for (int n = n0; n < n1; ++n) {
             const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
             if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
-            p.first[n] = make_int2(at, k);
+            if (k > 2) p.first[atomicAdd(&m.cut, 1)] = make_int2(at, k);
             for (int j = 0; !sort && j < k; ++j) {
                 const Segment s = segment(n, j, at + j);
                 p.segs[at + j] = s;
@@ -1107,6 +1113,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
             p.counts[0] = total;
             p.counts[1] = 0;
             p.counts[2] = sort ? m.count[i] : m.total_s;
+            p.counts[6] = m.cut;
         }
     }
     fence_proxy_async_shared();  // the tiles come to the same place

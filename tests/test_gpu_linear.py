@@ -156,6 +156,22 @@ def test_cut_sequences_with_states_in_place():
     assert torch.equal(o, want[0]) and torch.equal(d["s0"], want[1])
 
 
+def test_invalid_sequences_by_the_thousand():
+    """Most of 70000 offsets out of range: those sequences are skipped and reported, the others computed."""
+    N, T = 70000, 420010
+    x = make([100, 2500], 1, 1, seed=37)
+    d = dev(x)
+    wide = lambda t: torch.cat([t, torch.zeros((T - 2600, *t.shape[1:]), dtype=t.dtype, device="cuda")])
+    cu = torch.full((N + 1,), -1, dtype=torch.int32, device="cuda")
+    cu[:2] = torch.tensor([0, 100])
+    cu[-2:] = torch.tensor([100, 2600])
+    o = torch.full((T, 1, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_linear_chunk_fwd(wide(d["q"]), wide(d["k"]), wide(d["v"]), wide(d["g"]), cu, None, x["scale"], o, None, status)
+    assert int(status) == kda.KDA_ERR_BAD_SEQLENS and bool((o[2600:] == 7.0).all())
+    check(dict(x, s0=None), o[:2600], None)
+
+
 def test_sequences_that_overlap_are_refused():
     """Offsets that go back and cover the rows several times: an error, and nothing is written."""
     x = make([3000], 1, 1, seed=36)
