@@ -248,6 +248,7 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
         const Task t = task_of<SEG>(p, id, states);
         if (t.skip) continue;
         const int hk = t.h / p.a.rep;
+        if (t.sin) prefetch_l2(t.sin, DK * DV * sizeof(float));  // (the state's warps come for it a chunk or two later)
 #pragma unroll 1
         for (int c = 0; ok && c < t.len; c += C) {
             const int row = static_cast<int>(t.t0 + c);

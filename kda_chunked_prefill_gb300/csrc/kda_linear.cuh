@@ -64,6 +64,10 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t *bar, bool yes) {  // (n
 __device__ __forceinline__ void mbar_inval(uint64_t *bar) {
     asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// a multiple of 16 bytes, on its way to L2
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 // A wait that lets the warp sleep until the phase completes, WAIT_NS at most. (With
 // the default time, a few hundred cycles, the polls of a CTA's waiting warps
 // slow its working ones down.)
