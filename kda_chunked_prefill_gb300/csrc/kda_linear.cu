@@ -1285,13 +1285,6 @@ cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t 
 // more or less is 0.8, 4.9 and 17.6 us of the recurrence, so they meet at 6 to 7 tokens.
 bool few_tokens(int64_t N, int64_t T) { return T <= 6 * N; }
 
-// The shortest cut of sequences worth a try, about half an SM's share of the chunks; 0 when no sequence can be longer.
-int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
-    const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
-    int64_t len = (all + 2 * sms - 1) / (2 * sms);
-    if (len < 4) len = 4;
-    return longest <= len ? 0 : static_cast<int>(len);
-}
 // Sequences of equal lengths are estimated to be as fast whole as cut (4 x 2048, 16 heads: 50 us, cut 60). Every CTA
 // then looks whether they are equal, and none plans if so: the host does not know, and a padded batch looks the same to it.
 bool whole_if_equal(int64_t N, int64_t T, int64_t H, int len, int sms) {
@@ -1305,6 +1298,15 @@ bool whole_if_equal(int64_t N, int64_t T, int64_t H, int len, int sms) {
     float best = 3.0e38f;
     for (int i = 1; i < CUTS; ++i) best = std::fmin(best, time_of(cut_length(i, len)));
     return time_of(each) <= best;
+}
+// The shortest cut of sequences worth a try, about half an SM's share of the chunks; 0 when no sequence can be longer, or there
+// is one, as fast whole.
+int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
+    const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
+    int64_t len = (all + 2 * sms - 1) / (2 * sms);
+    if (len < 4) len = 4;
+    if (longest <= len || (N == 1 && whole_if_equal(N, T, H, static_cast<int>(len), sms))) return 0;
+    return static_cast<int>(len);
 }
 
 struct Layout {
