@@ -19,7 +19,7 @@
 // Why this split. U does not depend on S, so the recurrence from chunk to chunk is one fused multiply-add per state element and
 // its rounding to bf16 for the next q S: S stays in fp32 registers (two threads share a value column) and is never accumulated
 // by the tensor cores over many chunks. v~ in two bf16 terms, both multiplied by the exact bf16 k, keeps the final state within
-// 4e-6 (relative, against 64 bits; one term: 2e-3, and a third would cost 8 MMAs of 40 a chunk); P and the copy of S that q
+// 4e-6 (relative, against 64 bits; one term: 2e-3, and for a third tensor memory has no room); P and the copy of S that q
 // multiplies are rounded once to bf16, like o.
 //
 // Decays: every factor is 2^x with x a sum of same-signed terms that starts at the nearer end (prefixes within 32 tokens,
@@ -32,7 +32,7 @@
 // Bound by latency: one chunk takes an SM 2.6 us, with 1.5 us of MMAs and 0.8 us of memory at an SM's share. The chain is
 // q k^T -> P (1.2 us) -> P v (0.6) -> o (0.4) -> q k^T of the next chunk (0.4), because tensor memory holds no second score tile
 // beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 50 us; 8 of 2048: 56 us, 4.9 TB/s; one of 65536, 4 heads (cut in
-// 37): 104 us.
+// 37): 105 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
