@@ -461,7 +461,7 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
  * the chunk's g up to token i,
  *       o_i = scale * (e^{G_i} S^T q_i + sum_{j<=i} e^{G_i-G_j} (q_i.k_j) v_j)
  *       S  <- e^{G_end} S + sum_j e^{G_end-G_j} k_j v_j^T
- * (every exponent is a sum of g <= 0). Sequences of few tokens (6 on average)
+ * (every exponent is a sum of g <= 0). Sequences of few tokens (9 on average)
  * run the recurrence itself. Long sequences are cut where there are few, in one
  * cooperative launch.
  * (Not part of the method's pages.)

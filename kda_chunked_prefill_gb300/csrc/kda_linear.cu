@@ -1281,9 +1281,9 @@ cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t 
 }
 
 // Sequences of few tokens run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 128.
-// 16 heads, 17 tokens each: 4 sequences 17.3 us and as chunks 8.7, 64 sequences 103 and 50, 256 sequences 352 and 178; a token
-// more or less is 0.8, 4.9 and 17.6 us of the recurrence, so they meet at 6 to 7 tokens.
-bool few_tokens(int64_t N, int64_t T) { return T <= 6 * N; }
+// 16 heads, 17 tokens each: 16 sequences 21 us and as chunks 14, 64 sequences 78 and 50, 256 sequences 276 and 178; a token
+// more or less is 1.0, 3.7 and 13.5 us of the recurrence, so they meet at 9 to 10 tokens.
+bool few_tokens(int64_t N, int64_t T) { return T <= 9 * N; }
 
 // Sequences of equal lengths are estimated to be as fast whole as cut (4 x 2048, 16 heads: 50 us, cut 60). Every CTA
 // then looks whether they are equal, and none plans if so: the host does not know, and a padded batch looks the same to it.

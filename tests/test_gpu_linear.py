@@ -158,7 +158,7 @@ def test_cut_sequences_with_states_in_place():
 
 def test_invalid_sequences_by_the_thousand():
     """Most of 70000 offsets out of range: those sequences are skipped and reported, the others computed."""
-    N, T = 70000, 420010
+    N, T = 70000, 640010
     x = make([100, 2500], 1, 1, seed=37)
     d = dev(x)
     wide = lambda t: torch.cat([t, torch.zeros((T - 2600, *t.shape[1:]), dtype=t.dtype, device="cuda")])
