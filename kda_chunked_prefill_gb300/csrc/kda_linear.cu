@@ -71,7 +71,7 @@ struct ChunkParams {
     int2 *first;         // first slot and number of segments of each sequence to join
     Segment *segs;       // the segments, long ones first
     Segment *segs_s;     // those of the pass over the states, long ones first
-    float *decays;       // [slot][head], minus one
+    float *decays;       // [slot][head], as decay_factor() gives them
     float *states;       // [slot][head][128][128]
 };
 
@@ -79,7 +79,7 @@ struct Misc {
     uint64_t full[6];                 // a tile has come, by its kind and its chunk's number
     uint64_t empty[TILES];            // a slot is free
     uint64_t qk, qs, u, o, vfree[STAGES];  // tensor core -> warps (commits)
-    uint64_t decw[2], dect;           // decay tables written: w and dm1; tab, pre and start
+    uint64_t decw[2], dect;           // decay tables written: w and factor; tab, pre and start
     uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled)
     uint64_t wfree[2];                // w read
     uint64_t go;                      // the first g have been read
@@ -94,7 +94,7 @@ struct Misc {
     alignas(16) uint32_t w[2][C];     // 2^(sum of g after j up to the chunk's end), a chunk ahead: for a pair of tokens two bf16
                                       // values and what they leave, in bf16
     float start[4];                   // log2 sum of g up to the start of each block
-    float dm1[4];                     // 2^(the chunk's sum) - 1, of the last four chunks
+    float factor[4];                  // the chunk's decay as decay_factor() gives it, of the last four chunks
 };
 __host__ __device__ constexpr int tab_at(int anchor) { return anchor == 1 ? 0 : anchor == 2 ? 32 : 96; }
 static_assert(offsetof(Misc, tab) % 16 == 0 && offsetof(Misc, pre) % 16 == 0 && offsetof(Misc, w) % 16 == 0 && OFF_MISC % 16 == 0,
@@ -131,7 +131,7 @@ struct Task {
     int32_t len, h;
     const float *sin;  // NULL: zeros
     float *sout;       // NULL: not wanted
-    float *decay;      // NULL, or where the segment's decay minus one goes
+    float *decay;      // NULL, or where the segment's decay_factor() goes
     bool skip;
 };
 
@@ -227,6 +227,13 @@ __device__ __forceinline__ float gate_raw(const Params &a, int64_t t0, int row, 
     return __ldg(a.g + (a.g_per_token ? (t0 + row) * a.H + h : h));
 }
 __device__ __forceinline__ float log2_decay(float g) { return fmaxf(g * LOG2E, -200.f); }  // 2^-200 is 0 in fp32
+// The decay 2^x of a state that many steps multiply, with all of fp32's relative precision: up to 1/2 (and at 0, which is -1) the
+// positive factor itself, above it the negative factor minus one. (Minus one, so that a slow decay is not rounded away step after
+// step; not for a fast one, whose difference from 1 has lost its last bits: at 2^-13 3 % of them, below 2^-24 all.)
+__device__ __forceinline__ float decay_factor(float x) {
+    const float less = expm1f(x * (1.f / LOG2E)), whole = ex2(x);
+    return less < -0.5f && whole > 0.f ? whole : less;
+}
 
 // Operand descriptors: a tile's own, and the step to k-block kk of 16 added to it (within the address field: no carry leaves it).
 __device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return umma_desc_sw128(tile, 16, 1024); }  // K-major
@@ -450,9 +457,9 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             const f2 minus = pair(-1.f, -1.f);
             *reinterpret_cast<uint4 *>(&m->w[buf][4 * lane]) =
                 make_uint4(h0, bf16_of(fma2(of_bf16(h0), minus, w0)), h1, bf16_of(fma2(of_bf16(h1), minus, w1)));
-            // (minus one, so that a slow decay is not rounded away chunk after chunk; the state's warps have read the
-            // entry of four chunks ago: the scores of two chunks ago came after their read)
-            if (lane == 0) m->dm1[it & 3] = expm1f(total * (1.f / LOG2E));
+            // (the state's warps have read the entry of four chunks ago: U of three chunks ago came after their read, and v~ of two
+            // chunks ago, whose end wfree tells, after it)
+            if (lane == 0) m->factor[it & 3] = decay_factor(total);
             arrive_warp(&m->decw[buf]);
             if (states) continue;
             if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
@@ -486,7 +493,7 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             }
             arrive_warp(&m->dect);
         }
-        if (states && lane == 0) *t.decay = expm1f(sum * (1.f / LOG2E));
+        if (states && lane == 0) *t.decay = decay_factor(sum);
     }
     if (bad) set_status(a.status, KDA_ERR_GATE_RANGE);
 }
@@ -776,8 +783,14 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             fail = fail || !wait_warp(m, &m->u, ph);
             if (!fail) {
                 tc_fence_after();
-                const float dm1 = m->dm1[it & 3];
-                const f2 d2 = pair(dm1, dm1);
+                float less = m->factor[it & 3];
+                if (less > 0.f) {  // a fast decay, by itself
+                    const f2 w2 = pair(less, less);
+#pragma unroll
+                    for (int j = 0; j < NK / 2; ++j) S[j] = mul2(S[j], w2);
+                    less = 0.f;
+                }
+                const f2 d2 = pair(less, less);
 #pragma unroll
                 for (int b = 0; b < NK / 16; ++b) {
                     uint32_t u[16];
@@ -861,7 +874,8 @@ __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
                 }
 #pragma unroll
                 for (int j = 0; j < BATCH; ++j) {
-                    e = add2(fma2(e, pair(dd[j], dd[j]), e), x[j]);
+                    const float keep = dd[j] > 0.f ? 0.f : 1.f;
+                    e = add2(fma2(e, pair(dd[j], dd[j]), mul2(e, pair(keep, keep))), x[j]);
                     if (j < left) s[(1 + j) * step] = e;
                 }
                 s += BATCH * step;

@@ -109,6 +109,29 @@ def test_chunk_decay_of_a_whole_chunk(g):
     check(x, o, fs)
 
 
+@pytest.mark.parametrize("total", [-0.6, -0.75, -5.0, -9.0, -13.0, -20.0, -40.0])
+@pytest.mark.parametrize("lens,H", [([384, 128, 70], 3), ([5000], 1)])
+@pytest.mark.parametrize("size", [0.0, 1e-7])
+def test_states_that_only_decay(lens, H, total, size):
+    """Values of (almost) nothing: what is left of the initial state, to the end, is its decay alone. `total`: a chunk's, or, with
+    one long sequence (cut into segments of four chunks and more), four chunks'."""
+    x = make(lens, H, H, seed=38)
+    x["v"] = x["v"] * size
+    x["g"].fill_(total / 128 if H > 1 else total / 512)
+    o, fs = chunk(x)
+    check(x, o, fs)
+
+
+def test_a_state_decays_at_once():
+    """One strong decay in the middle of a chunk, no values: sums of a strong and of slow decays."""
+    for g in (-3.0, -12.8, -17.0, -30.0, -100.0):
+        x = make([140, 300], 2, 2, seed=39, rate=0.01)
+        x["v"] = x["v"] * 0.0
+        x["g"][[60, 250, 400], :] = g
+        o, fs = chunk(x)
+        check(x, o, fs)
+
+
 def test_chunk_large_values():
     """Scores and outputs of 2^30 and more, with decays close to where chunks stop being computed without anchors."""
     x = make([400, 50], 2, 2, seed=32)
