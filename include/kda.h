@@ -484,7 +484,8 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
  *                 pointer as initial_state. An empty sequence's final state is
  *                 its initial state.
  *   status_dev    optional device int32, zeroed on the stream, then the first of
- *                 KDA_ERR_GATE_RANGE (some g > 0 or NaN), KDA_ERR_BAD_SEQLENS (that
+ *                 KDA_ERR_GATE_RANGE (some g > 0 or NaN; from a NaN on, o and the final
+ *                 state of its sequence and head are NaN), KDA_ERR_BAD_SEQLENS (that
  *                 sequence is skipped), KDA_ERR_TIMEOUT.
  *   workspace     kda_linear_chunk_fwd_workspace_size(...) bytes, 256-byte aligned
  *                 (NULL when that is 0); not shared by calls that overlap.

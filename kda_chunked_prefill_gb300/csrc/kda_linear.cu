@@ -226,7 +226,11 @@ __device__ __forceinline__ float gate_raw(const Params &a, int64_t t0, int row, 
     if (row >= left) return 0.f;
     return __ldg(a.g + (a.g_per_token ? (t0 + row) * a.H + h : h));
 }
-__device__ __forceinline__ float log2_decay(float g) { return fmaxf(g * LOG2E, -200.f); }  // 2^-200 is 0 in fp32
+__device__ __forceinline__ float log2_decay(float g) {  // 2^-200 is 0 in fp32; a NaN stays one and shows in what it decays
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g * LOG2E), "f"(-200.f));
+    return r;
+}
 // The decay 2^x of a state that many steps multiply, with all of fp32's relative precision: up to 1/2 (and at 0, which is -1) the
 // positive factor itself, above it the negative factor minus one. (Minus one, so that a slow decay is not rounded away step after
 // step; not for a fast one, whose difference from 1 has lost its last bits: at 2^-13 3 % of them, below 2^-24 all.)

@@ -316,6 +316,28 @@ def test_device_errors():
         assert e.value.code == kda.KDA_ERR_BAD_SEQLENS
 
 
+@pytest.mark.parametrize("lens,at", [([300, 70, 129], 45), ([300, 70, 129], 200), ([300, 70, 129], 359), ([40, 6000], 3000),
+                                     ([3, 5, 9], 5)])
+def test_a_gate_that_is_no_number_shows(lens, at):
+    """From the token of a NaN gate on its sequence and head are NaN, in every form; nothing else is touched by it."""
+    x = make(lens, 2, 2, seed=40, rate=0.3)
+    clean = chunk(x)
+    want = oracle_of(x)
+    x["g"][at, 1] = float("nan")
+    d = dev(x)
+    o, fs = kda.linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], scale=x["scale"])
+    n = int(np.searchsorted(np.cumsum(lens), at, side="right"))
+    end = sum(lens[:n + 1])
+    assert bool(o[at:end, 1].isnan().all()) and bool(fs[n, 1].isnan().all())
+    same = torch.ones(sum(lens), 2, dtype=torch.bool)
+    same[end - lens[n]:end, 1] = False
+    assert torch.equal(o[same.cuda()], clean[0][same.cuda()])
+    o, fs = o.clone(), fs.clone()
+    o[at:end, 1], fs[n, 1] = clean[0][at:end, 1], clean[1][n, 1]
+    assert torch.equal(fs, clean[1])
+    check(x, o, fs, want)  # its chunk's tokens in front of it, too
+
+
 # ------------------------------------------------------------------ decode
 @pytest.mark.parametrize("N,Tn,H,Hk,state,decay", [
     (1, 1, 1, 1, True, "token"), (7, 1, 16, 8, True, "head"), (64, 1, 16, 16, False, "token"), (5, 3, 4, 1, True, "token"),
