@@ -506,6 +506,27 @@ kda_status_t kda_linear_chunk_fwd(const void *q, const void *k, const void *v, c
                                   float *final_state, int32_t *status_dev, void *workspace, size_t workspace_bytes,
                                   kda_stream_t stream);
 
+/*
+ * kda_linear_chunk_fwd_debug — kda_linear_chunk_fwd for testing the failure
+ * detection without a GPU fault. withhold_outputs (and, in the first of the two
+ * passes over cut sequences, withhold_states) is the number of a chunk, counted
+ * from 0 in each thread block, whose decays are not handed on to its values'
+ * warps (-1: none withheld; below that KDA_ERR_INVALID_ARG). What waits for them
+ * gives up after 20000 waits of up to 0.1 ms each, the device reports
+ * KDA_ERR_TIMEOUT in status_dev, every block leaves and the context stays usable;
+ * o and final_state are then unspecified. Blocks with fewer chunks, and batches
+ * that run the recurrence, withhold nothing. With -1 twice it is
+ * kda_linear_chunk_fwd.
+ */
+kda_status_t kda_linear_chunk_fwd_debug(const void *q, const void *k, const void *v, const float *g,
+                                        const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                        int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k,
+                                        int32_t head_dim_v, int64_t q_token_stride, int64_t k_token_stride,
+                                        int64_t v_token_stride, int32_t g_per_token, const float *initial_state,
+                                        float scale, void *o, float *final_state, int32_t *status_dev,
+                                        void *workspace, size_t workspace_bytes, kda_stream_t stream,
+                                        int32_t withhold_states, int32_t withhold_outputs);
+
 /* Workspace bytes of kda_linear_chunk_fwd for these sizes on the current device
  * (0: none needed, or invalid arguments). */
 size_t kda_linear_chunk_fwd_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t num_heads);

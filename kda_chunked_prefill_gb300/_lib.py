@@ -39,7 +39,7 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_stat
             "kda_chunk_fwd_debug", "kda_chunk_fwd_raw_gates", "kda_chunk_fwd_gated_norm", "kda_chunk_fwd_split",
             "kda_chunk_fwd_split_plan", "kda_chunk_fwd_split_workspace_size", "kda_chunk_fwd_host", "kda_chunk_fwd_plan",
             "kda_chunk_fwd_host_buffer_size", "kda_decode_fwd",
-            "kda_chunk_fwd_launches", "kda_linear_chunk_fwd", "kda_linear_chunk_fwd_workspace_size",
+            "kda_chunk_fwd_launches", "kda_linear_chunk_fwd", "kda_linear_chunk_fwd_debug", "kda_linear_chunk_fwd_workspace_size",
             "kda_linear_decode_fwd", "kda_state_store", "kda_state_load", "kda_add_rms_norm",
             "kda_status_string", "kda_version")
 DECODE_MAX_TOKENS = 64
@@ -105,6 +105,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_linear_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, i64, i64, i64, i32, vp,
                                              f32, vp, vp, vp, vp, ctypes.c_size_t, vp]
         lib.kda_linear_chunk_fwd.restype = ctypes.c_int
+        lib.kda_linear_chunk_fwd_debug.argtypes = lib.kda_linear_chunk_fwd.argtypes + [i32, i32]
+        lib.kda_linear_chunk_fwd_debug.restype = ctypes.c_int
         lib.kda_linear_chunk_fwd_workspace_size.argtypes = [i32, i64, i32]
         lib.kda_linear_chunk_fwd_workspace_size.restype = ctypes.c_size_t
         lib.kda_linear_decode_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i64, i64, i32, vp, f32,
@@ -606,7 +608,7 @@ def linear_workspace_size(num_seqs: int, total_tokens: int, num_heads: int) -> i
 
 
 def kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale: float, o, final_state, status=None, stream=None,
-                         workspace=None) -> int:
+                         workspace=None, withhold: Optional[Tuple[int, int]] = None) -> int:
     """Call the C entry point ``kda_linear_chunk_fwd`` with caller-allocated outputs.
 
     q, k: bf16 [T,Hk,128]; v: bf16 [T,H,128], H a multiple of Hk (tokens may be
@@ -615,6 +617,7 @@ def kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale: float, o,
     the same tensor); o: bf16 [T,H,128]; status: int32 [1] or None; workspace:
     uint8 tensor of ``linear_workspace_size(N, T, H)`` bytes (default: a new one
     from torch's allocator for the call's stream). All on one CUDA device.
+    ``withhold`` calls ``kda_linear_chunk_fwd_debug`` with these two numbers.
     Raises ``KdaError`` on a host-side error; returns ``KDA_OK`` once queued.
     """
     N = cu_seqlens.shape[0] - 1
@@ -629,10 +632,13 @@ def kda_linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state, scale: float, o,
                 workspace = torch.empty(need, dtype=_U8, device=q.device)
     elif workspace.get_device() != index or workspace.dtype is not _U8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    return _call(lib.kda_linear_chunk_fwd, "kda_linear_chunk_fwd", index,
-                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, D, V, qs, ks,
-                  vs, per_token, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
-                  0 if workspace is None else workspace.numel()), stream)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, D, V, qs, ks,
+            vs, per_token, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
+            0 if workspace is None else workspace.numel())
+    if withhold is not None:
+        debug = lib.kda_linear_chunk_fwd_debug
+        return _call(lambda *a: debug(*a, *withhold), "kda_linear_chunk_fwd_debug", index, args, stream)
+    return _call(lib.kda_linear_chunk_fwd, "kda_linear_chunk_fwd", index, args, stream)
 
 
 def linear_chunk_fwd(q, k, v, g, cu_seqlens, initial_state=None, scale: Optional[float] = None,

@@ -61,6 +61,7 @@ struct ChunkParams {
     Params a;
     CUtensorMap tq, tk, tv, to;
     int32_t tasks;  // WHOLE: (sequence, head) pairs
+    Withhold withhold;
     // the rest only with segments (device memory in the workspace)
     int32_t seg_chunks;  // shortest cut that the workspace is sized for
     int32_t most_segs;   // that the workspace holds
@@ -81,12 +82,15 @@ struct Misc {
     uint64_t qk, qs, u, o, vfree[STAGES];  // tensor core -> warps (commits)
     uint64_t decw[2], dect;           // decay tables written: w and factor; tab, pre and start
     uint64_t vt[STAGES], s, p;        // v~ stage, bf16 state, scores written (and q S scaled)
-    uint64_t wfree[2];                // w read
+    uint64_t wfree[2], zeroed;        // w read; rows behind a segment zeroed
     uint64_t go;                      // the first g have been read
-    uint64_t ufree, ofree;            // U read; O read
+    uint64_t ufree;                   // U read
+    uint64_t ofree;                   // O read
+    uint64_t drained[2];              // tensor core -> an MMA warp at its end
     uint32_t tmem;                    // address of the tensor memory
     int32_t abort;                    // a wait ran out
-    int32_t easy, pad;                // this chunk's decay is above EASY
+    int32_t easy;                     // this chunk's decay is above EASY
+    int32_t products;                 // -1, or how many chunks' P v have been issued in all (their warp has ended)
     // slow chunks (EASY): tab[j] = 2^-(sum of g up to j), pre[j] = log2 sum of g up to j, start = 0; others: tab, for anchors
     // 1..3 from tab_at(), 2^(sum of g after j up to the start of block a), j before it, and pre the log2 prefix within j's block
     alignas(16) float tab[192];
@@ -124,7 +128,8 @@ __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr int GRID_POLLS = 1 << 24;
-constexpr int WAITS = 20000;  // waits of up to WAIT_NS each before a role gives up
+// waits of up to WAIT_NS each before a role gives up; and before one that is to leave takes its own copies or MMAs for complete
+constexpr int WAITS = 20000, WAITS_DRAIN = 100;
 
 struct Task {
     int64_t t0;
@@ -201,7 +206,8 @@ __device__ __forceinline__ uint32_t use_of(uint32_t it, bool states) { return st
 // A bounded wait for a barrier's phase. (A parity wait takes the phase before
 // last for the next: every role that waits on a barrier waits for each of its
 // phases in turn, or has seen the one before complete through another wait.)
-// False: it ran out, or another role has given up
+// False: it ran out, or another role has given up. A warp that gets false leaves its role at once: roles meet at these barriers
+// alone (but see give_up), where those that stay behind give up in their turn, until all threads have come to the end of the pass.
 __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
     int i = 0;
 #pragma unroll 1
@@ -211,7 +217,13 @@ __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
     }
     return true;
 }
-// the same for a whole warp, with one answer
+// a role that leaves waits for what it has in flight
+__device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < WAITS_DRAIN && !mbar_wait_some(bar, parity); ++i) {
+    }
+}
+// a wait() of a whole warp, with one answer
 __device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(m, bar, parity));
 }
@@ -286,7 +298,7 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
                 tma_load_3d(dst + PANEL, map, 64, head, row, &m->full[slot], policy);
                 part |= 1u << kind;
             }
-            if (ok) ++it;
+            if (ok) ++it, part = 0;
         }
     }
     // no copy and no commit of this CTA is in flight when it ends
@@ -297,17 +309,19 @@ __device__ __forceinline__ void role_load(const ChunkParams &p, unsigned char *s
         for (int kind = first; ok && kind < 3; ++kind) ok = wait(m, &m->empty[slot_of(kind, k, states)], use_of(k, states) & 1);
     if (ok) return;
 #pragma unroll 1
-    for (int kind = first; kind < 3; ++kind) {
-        if (it > 0) (void)mbar_wait_some(&m->full[slot_of(kind, it - 1, states)], use_of(it - 1, states) & 1);
-        if (part >> kind & 1) (void)mbar_wait_some(&m->full[slot_of(kind, it, states)], use_of(it, states) & 1);
-    }
+    for (uint32_t k = it > back ? it - back : 0; k <= it; ++k)
+#pragma unroll 1
+        for (int kind = first; kind < 3; ++kind) {
+            const bool again = part >> kind & 1;  // chunk `it` has this kind's tile, where that of `it - back` was
+            if (k == it ? again : !(again && k + back == it)) wait_drain(&m->full[slot_of(kind, k, states)], use_of(k, states) & 1);
+        }
 }
 
 // ---- two warps: MMAs, one the scores' and the outputs' (q k^T, q S, P v), one U. Each walks the tasks as a whole warp, with
 // everything that makes an address the same in all lanes, and one lane issues. (A 128 x 128 x 16 MMA runs 70 cycles; from one
 // warp the waits and descriptors between groups of four or eight cost as much again.)
 template <bool SEG>
-__device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+__device__ __forceinline__ uint32_t role_mma_out(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
     constexpr uint32_t ID_KK = idesc_bf16(false, false, C, C), ID_PV = idesc_bf16(false, true, C, DV);
     uint32_t it = 0;
@@ -324,8 +338,8 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
             const uint32_t ph = it & 1, up = use_of(it, states) & 1;
             const int iq = slot_of(TQ, it, states), iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
             const uint64_t q = desc_k(base + iq * TILE), k = desc_k(base + ik * TILE);
-            if (!wait_warp(m, &m->full[iq], up)) return;
-            if (!wait_warp(m, &m->full[ik], up)) return;
+            if (!wait_warp(m, &m->full[iq], up)) return it;
+            if (!wait_warp(m, &m->full[ik], up)) return it;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -333,8 +347,8 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
                 umma_commit(&m->qk);
                 umma_commit(&m->empty[ik]);
             }
-            if (!wait_warp(m, &m->s, ph)) return;
-            if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return;
+            if (!wait_warp(m, &m->s, ph)) return it;
+            if (it > 0 && !wait_warp(m, &m->ofree, ph ^ 1)) return it;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -343,8 +357,8 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
             }
             // P v onto the scaled q S; after U: by then v~ has been made of v
             const uint64_t v = desc_mn(base + iv * TILE, PANEL);
-            if (!wait_warp(m, &m->u, ph)) return;
-            if (!wait_warp(m, &m->p, ph)) return;
+            if (!wait_warp(m, &m->u, ph)) return it;
+            if (!wait_warp(m, &m->p, ph)) return it;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -355,6 +369,7 @@ __device__ __forceinline__ void role_mma_out(const ChunkParams &p, unsigned char
             }
         }
     }
+    return it;
 }
 template <bool SEG>
 __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
@@ -398,6 +413,14 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
             }
         }
     }
+}
+// The end of either: what the warp has issued is through with the CTA's memory (also where somebody has given up, and a role that
+// would have waited for it has left).
+__device__ __forceinline__ void drain_mma(uint64_t *bar) {
+    if (elect_one()) umma_commit(bar);
+    __syncwarp();
+    wait_drain(bar, 0);
+    __syncwarp();
 }
 
 // ---- one warp: decay tables. Lane l has tokens 4 l .. 4 l + 3, eight lanes a block of 32.
@@ -464,7 +487,7 @@ __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool s
             // (the state's warps have read the entry of four chunks ago: U of three chunks ago came after their read, and v~ of two
             // chunks ago, whose end wfree tells, after it)
             if (lane == 0) m->factor[it & 3] = decay_factor(total);
-            arrive_warp(&m->decw[buf]);
+            if (it != static_cast<uint32_t>(states ? p.withhold.states : p.withhold.outputs)) arrive_warp(&m->decw[buf]);
             if (states) continue;
             if (it > 0 && !wait_warp(m, &m->p, (it - 1) & 1)) return;
             const bool easy = total > EASY;
@@ -515,8 +538,7 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
     // this lane's row of the blocks: token lane % 8, channels 8 (lane / 8) .. of the quarter; swizzle: 16-byte piece ^ row % 8
     const uint32_t row0 = (quad >> 1) * PANEL + (16 * half + (lane & 7)) * 128 + (((4 * (quad & 1) + (lane >> 3)) ^ (lane & 7)) << 4);
     const int pair0 = 16 * half + 2 * (lane & 3);  // the fragments' tokens
-    bool fail = false;  // (a warp that gives up still comes to the barriers)
-    uint32_t it = 0;
+    uint32_t it = 0, ends = 0;  // chunks, and those that a segment does not fill
     const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
     for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
@@ -527,24 +549,24 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
             const int left = t.len - c, iv = slot_of(TV, it, states), ik = slot_of(TK, it, states);
             const uint32_t up = use_of(it, states) & 1;
             unsigned char *tv = smem + iv * TILE;
-            fail = fail || !wait_warp(m, &m->full[iv], up);
+            if (!wait_warp(m, &m->full[iv], up)) return;
             if (left < C) {  // rows behind the segment are someone else's: zeros in v and k
-                fail = fail || !wait_warp(m, &m->full[ik], up);
+                if (!wait_warp(m, &m->full[ik], up)) return;
                 unsigned char *tk = smem + ik * TILE;
 #pragma unroll 1
-                for (int i = gtid; !fail && i < (C - left) * 16; i += GROUP) {
+                for (int i = gtid; i < (C - left) * 16; i += GROUP) {
                     const int at = (i & 8 ? PANEL : 0) + (left + (i >> 4)) * 128 + (i & 7) * 16;
                     *reinterpret_cast<uint4 *>(tv + at) = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4 *>(tk + at) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_shared();
-                if (named_bar_or(3, GROUP, fail)) return;
+                arrive_warp(&m->zeroed);
+                if (!wait_warp(m, &m->zeroed, ends++ & 1)) return;
             }
-            fail = fail || !wait_warp(m, &m->decw[it & 1], (it >> 1) & 1);
+            if (!wait_warp(m, &m->decw[it & 1], (it >> 1) & 1)) return;
 #pragma unroll 1
             for (int st = 0; st < STAGES; ++st) {
-                fail = fail || (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1));
-                if (fail) break;
+                if (it > 0 && !wait_warp(m, &m->vfree[st], (it - 1) & 1)) return;
                 tc_fence_after();
                 uint32_t hi[8], lo[8];  // [8 tokens][8 channels]
 #pragma unroll
@@ -569,55 +591,67 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
                 tc_fence_before();
                 arrive_warp(&m->vt[st]);
             }
-            if (!fail) arrive_warp(&m->wfree[it & 1]);
+            arrive_warp(&m->wfree[it & 1]);
         }
     }
 }
 
+// The scores' and the state's warps meet at one named barrier, which has no limit, and where the storing warp alone waits: for a full
+// chunk's output tile. It comes there after that chunk's P v, so every other warp has arrived at the chunk's p by then, and none can
+// pass the next chunk's o before it is back. So a warp that gives up behind p still arrives for a chunk whose P v is issued, and
+// for no other, and the storing warp finds just the arrivals that it waits for.
+// at: what the role returned, the number of the full chunk behind whose p it gave up, plus one, or 0
+__device__ __forceinline__ void give_up(Misc *m, uint32_t at) {
+    if (at == 0 || threadIdx.x >> 5 == WARP_STORE) return;
+#pragma unroll 1
+    for (int i = 0; i < GRID_POLLS; ++i) {  // (the warp of P v gives up in its turn)
+        const int products = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&m->products), 0);
+        if (products >= 0) {
+            if (static_cast<int>(at) <= products) named_bar_arrive(2, 2 * GROUP);
+            return;
+        }
+        __nanosleep(64);
+    }
+}
+
 // A chunk's output from tensor memory into the q tile, and out. The scores' and the state's warps share it: four threads a token
-// row, 32 values each (half, part). True: some warp has given up. (A warp that gives up still comes to the barriers.)
-__device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
-                                            int slot, int tid, int half, int part, float factor, bool fail) {
-    unsigned char *tile = smem + slot * TILE + half * PANEL;
-    const int left = t.len - c, lane = threadIdx.x & 31;
-    if (!fail) {
-        tc_fence_after();
-        const f2 s2 = pair(factor, factor);
+// row, 32 values each (half, part).
+__device__ __forceinline__ void output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
+                                            int slot, int tid, int half, int part, float factor) {
+    const int left = t.len - c;
+    // A full chunk's row goes into the tile, its 16-byte pieces swizzled by row % 8; another's straight out, as far as it is one.
+    unsigned char *row = left >= C ? smem + slot * TILE + half * PANEL + tid * 128
+                                   : reinterpret_cast<unsigned char *>(p.a.o + ((t.t0 + c + tid) * p.a.H + t.h) * DV + 64 * half);
+    const int swizzle = left >= C ? tid & 7 : 0;
+    tc_fence_after();
+    const f2 s2 = pair(factor, factor);
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-            uint32_t o[16];
-            tmem_ld16(tmem_lanes + COL_O + 64 * half + 32 * part + 16 * b, o);
-            tmem_wait_ld();
+    for (int b = 0; b < 2; ++b) {
+        uint32_t o[16];
+        tmem_ld16(tmem_lanes + COL_O + 64 * half + 32 * part + 16 * b, o);
+        tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // the tile's swizzle: 16-byte piece ^ row % 8
-                const int i = 8 * j;
-                *reinterpret_cast<uint4 *>(tile + tid * 128 + (((4 * part + 2 * b + j) ^ (tid & 7)) << 4)) =
-                    make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
-                               bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
-            }
+        for (int j = 0; j < 2; ++j) {
+            const int i = 8 * j;
+            const uint4 x = make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
+                                       bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
+            if (tid < left) *reinterpret_cast<uint4 *>(row + (((4 * part + 2 * b + j) ^ swizzle) << 4)) = x;
         }
-        tc_fence_before();
-        arrive_warp(&m->ofree);
     }
-    if (left < C) {  // rows behind the segment are not written
-        if (named_bar_or(1, 2 * GROUP, fail)) return true;
-#pragma unroll 1
-        for (int i = 128 * part + tid; i < left * 8; i += 256) {
-            const int r = i >> 3, j = i & 7;
-            *reinterpret_cast<uint4 *>(p.a.o + ((t.t0 + c + r) * p.a.H + t.h) * DV + 64 * half + 8 * j) =
-                *reinterpret_cast<const uint4 *>(tile + r * 128 + ((j ^ (r & 7)) << 4));
-        }
-    } else {
+    tc_fence_before();
+    arrive_warp(&m->ofree);
+    const bool stores = threadIdx.x >> 5 == WARP_STORE;
+    if (left >= C) {
         fence_proxy_async_shared();
+        // one warp stores a whole chunk's o and frees the tile; the others go on
+        if (!stores)
+            named_bar_arrive(2, 2 * GROUP);
+        else
+            named_bar_sync(2, 2 * GROUP);
     }
-    // one warp stores a whole chunk's o and frees the tile; the others go on (none of them comes here again before that warp's
-    // scores of the next chunk)
-    if (threadIdx.x >> 5 != WARP_STORE) {
-        named_bar_arrive(2, 2 * GROUP);
-    } else {
-        named_bar_sync(2, 2 * GROUP);
-        if (lane == 0) {
-            if (left >= C && !fail) {
+    if (stores) {
+        if ((threadIdx.x & 31) == 0) {
+            if (left >= C) {
                 const unsigned char *src = smem + slot * TILE;
                 tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c), evict_first());
                 tma_store_3d(&p.to, src + PANEL, 64, t.h, static_cast<int>(t.t0 + c), evict_first());
@@ -628,17 +662,15 @@ __device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char 
         }
         __syncwarp();
     }
-    return false;
 }
 
 // ---- warps 0-7: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
 template <bool SEG>
-__device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
+__device__ __forceinline__ uint32_t role_scores(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem) {
     constexpr bool states = false;
     const int half = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // TMEM lane offset 32 * warp in bits 16..31
     uint32_t it = 0;
-    bool fail = false;  // (a warp that gives up still comes to the barriers and tells the others there)
     const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
     for (int nth = 0, id; (id = nth_task<SEG>(nth)) < tasks; ++nth) {
@@ -647,82 +679,79 @@ __device__ __forceinline__ void role_scores(const ChunkParams &p, unsigned char 
 #pragma unroll 1
         for (int c = 0; c < t.len; c += C, ++it) {
             const uint32_t ph = it & 1;
-            fail = fail || !wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph);
-            float out = 0.f;  // what the row's output is multiplied by
-            if (!fail) {
-                tc_fence_after();
-                const float pre = m->pre[tid], row = ex2(pre);
-                const bool easy = m->easy;
-                out = p.a.scale * (easy ? row : 1.f);
-                // key blocks of 32: 0 and 3, or 1 and 2
+            if (!wait_warp(m, &m->dect, ph) || !wait_warp(m, &m->qk, ph)) return 0;
+            tc_fence_after();
+            const float pre = m->pre[tid], row = ex2(pre);
+            const bool easy = m->easy;
+            const float out = p.a.scale * (easy ? row : 1.f);  // what the row's output is multiplied by
+            // key blocks of 32: 0 and 3, or 1 and 2
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {
-                    const int b = i ? 3 - half : half;
-                    uint32_t s[32];
-                    if (b <= warp) tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
-                    if (b > warp) {
+            for (int i = 0; i < 2; ++i) {
+                const int b = i ? 3 - half : half;
+                uint32_t s[32];
+                if (b <= warp) tmem_ld32(tmem + lanes + COL_QK + 32 * b, s);
+                if (b > warp) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) s[j] = 0;
-                    } else if (easy) {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[32 * b]);
-                        const int see = b == warp ? lane : 32;
-                        tmem_wait_ld();
+                    for (int j = 0; j < 16; ++j) s[j] = 0;
+                } else if (easy) {
+                    const float4 *f = reinterpret_cast<const float4 *>(&m->tab[32 * b]);
+                    const int see = b == warp ? lane : 32;
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            const uint32_t x = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), pair(w.x, w.y)));
-                            const uint32_t y = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), pair(w.z, w.w)));
-                            s[2 * j] = 4 * j + 1 <= see ? x : 4 * j <= see ? x & 0xffffu : 0u;
-                            s[2 * j + 1] = 4 * j + 3 <= see ? y : 4 * j + 2 <= see ? y & 0xffffu : 0u;
-                        }
-                    } else if (b < warp) {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
-                        const f2 r2 = pair(row, row);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            s[2 * j] = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), mul2(r2, pair(w.x, w.y))));
-                            s[2 * j + 1] = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), mul2(r2, pair(w.z, w.w))));
-                        }
-                    } else {
-                        const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 w = f[j];
-                            // (selected, not multiplied by zero: a score behind the row, and its weight, may be anything)
-                            const float x = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
-                            const float y = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
-                            const float z = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
-                            const float q = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
-                            s[2 * j] = pack_bf16(x, y);
-                            s[2 * j + 1] = pack_bf16(z, q);
-                        }
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 w = f[j];
+                        const uint32_t x = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), pair(w.x, w.y)));
+                        const uint32_t y = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), pair(w.z, w.w)));
+                        s[2 * j] = 4 * j + 1 <= see ? x : 4 * j <= see ? x & 0xffffu : 0u;
+                        s[2 * j + 1] = 4 * j + 3 <= see ? y : 4 * j + 2 <= see ? y & 0xffffu : 0u;
                     }
-                    tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
+                } else if (b < warp) {
+                    const float4 *f = reinterpret_cast<const float4 *>(&m->tab[tab_at(warp) + 32 * b]);
+                    const f2 r2 = pair(row, row);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 w = f[j];
+                        s[2 * j] = bf16_of(mul2(pair(s[4 * j], s[4 * j + 1]), mul2(r2, pair(w.x, w.y))));
+                        s[2 * j + 1] = bf16_of(mul2(pair(s[4 * j + 2], s[4 * j + 3]), mul2(r2, pair(w.z, w.w))));
+                    }
+                } else {
+                    const float4 *f = reinterpret_cast<const float4 *>(&m->pre[32 * b]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 w = f[j];
+                        // (selected, not multiplied by zero: a score behind the row, and its weight, may be anything)
+                        const float x = 4 * j <= lane ? __uint_as_float(s[4 * j]) * ex2(pre - w.x) : 0.f;
+                        const float y = 4 * j + 1 <= lane ? __uint_as_float(s[4 * j + 1]) * ex2(pre - w.y) : 0.f;
+                        const float z = 4 * j + 2 <= lane ? __uint_as_float(s[4 * j + 2]) * ex2(pre - w.z) : 0.f;
+                        const float q = 4 * j + 3 <= lane ? __uint_as_float(s[4 * j + 3]) * ex2(pre - w.w) : 0.f;
+                        s[2 * j] = pack_bf16(x, y);
+                        s[2 * j + 1] = pack_bf16(z, q);
+                    }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(&m->p);
+                tmem_st16(tmem + lanes + COL_QK + 32 * b, s);  // over the scores they come from
             }
-            fail = fail || !wait_warp(m, &m->o, ph);
-            if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out, fail)) return;
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&m->p);
+            if (!wait_warp(m, &m->o, ph)) return t.len - c >= C ? it + 1 : 0;
+            output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out);
         }
     }
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
+    return 0;
 }
 
 // ---- warps 8-15: the state, transposed as U is. Two threads share a value column of S, one half of its keys each.
 template <bool SEG>
-__device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
+__device__ __forceinline__ uint32_t role_state(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem, bool states) {
     constexpr int NK = DK / 2;
     const Params &a = p.a;
     const int gtid = threadIdx.x - GROUP, half = gtid >> 7, tid = gtid & 127, warp = tid >> 5;
     const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
     unsigned char *sS = smem + OFF_S + half * PANEL + tid * 128;
     uint32_t it = 0;
-    bool fail = false;
     f2 S[NK / 2];
     const int tasks = tasks_of<SEG>(p, states);
 #pragma unroll 1
@@ -754,68 +783,60 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             const uint32_t ph = it & 1;
             float out = a.scale;  // what the row's output is multiplied by
             if (!states) {
-                fail = fail || !wait_warp(m, &m->dect, ph);
-                if (!fail) {
-                    const float entry = ex2(m->pre[tid] + m->start[warp]);
-                    if (m->easy) {
-                        out *= entry;
-                    } else if (wait_warp(m, &m->qs, ph)) {  // q S by the row's decay since the chunk began; P v is added onto it
-                        tc_fence_after();
-                        const f2 e2 = pair(entry, entry);
+                if (!wait_warp(m, &m->dect, ph)) return 0;
+                const float entry = ex2(m->pre[tid] + m->start[warp]);
+                if (m->easy) {
+                    out *= entry;
+                } else {  // q S by the row's decay since the chunk began; P v is added onto it
+                    if (!wait_warp(m, &m->qs, ph)) return 0;
+                    tc_fence_after();
+                    const f2 e2 = pair(entry, entry);
 #pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            uint32_t x[16];
-                            tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
-                            tmem_wait_ld();
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t x[16];
+                        tmem_ld16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float y, z;
-                                split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
-                                x[2 * j] = __float_as_uint(y);
-                                x[2 * j + 1] = __float_as_uint(z);
-                            }
-                            tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
+                        for (int j = 0; j < 8; ++j) {
+                            float y, z;
+                            split(mul2(e2, pair(x[2 * j], x[2 * j + 1])), y, z);
+                            x[2 * j] = __float_as_uint(y);
+                            x[2 * j + 1] = __float_as_uint(z);
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                    } else {
-                        fail = true;
+                        tmem_st16(tmem + lanes + COL_O + 64 * half + 16 * b, x);
                     }
-                    arrive_warp(&m->p);
+                    tmem_wait_st();
+                    tc_fence_before();
                 }
+                arrive_warp(&m->p);
             }
-            fail = fail || !wait_warp(m, &m->u, ph);
-            if (!fail) {
-                tc_fence_after();
-                float less = m->factor[it & 3];
-                if (less > 0.f) {  // a fast decay, by itself
-                    const f2 w2 = pair(less, less);
+            if (!wait_warp(m, &m->u, ph)) return t.len - c >= C ? it + 1 : 0;
+            tc_fence_after();
+            float less = m->factor[it & 3];
+            if (less > 0.f) {  // a fast decay, by itself
+                const f2 w2 = pair(less, less);
 #pragma unroll
-                    for (int j = 0; j < NK / 2; ++j) S[j] = mul2(S[j], w2);
-                    less = 0.f;
-                }
-                const f2 d2 = pair(less, less);
-#pragma unroll
-                for (int b = 0; b < NK / 16; ++b) {
-                    uint32_t u[16];
-                    tmem_ld16(tmem + lanes + COL_U + NK * half + 16 * b, u);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) S[8 * b + j] = add2(fma2(S[8 * b + j], d2, S[8 * b + j]), pair(u[2 * j], u[2 * j + 1]));
-                }
-                tc_fence_before();
-                arrive_warp(&m->ufree);
-                if (!states) {
-                    fail = !wait_warp(m, &m->qs, ph);  // q has been multiplied by the last copy
-                    if (!fail && c + C < t.len) publish();
-                }
+                for (int j = 0; j < NK / 2; ++j) S[j] = mul2(S[j], w2);
+                less = 0.f;
             }
+            const f2 d2 = pair(less, less);
+#pragma unroll
+            for (int b = 0; b < NK / 16; ++b) {
+                uint32_t u[16];
+                tmem_ld16(tmem + lanes + COL_U + NK * half + 16 * b, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) S[8 * b + j] = add2(fma2(S[8 * b + j], d2, S[8 * b + j]), pair(u[2 * j], u[2 * j + 1]));
+            }
+            tc_fence_before();
+            arrive_warp(&m->ufree);
             if (!states) {
-                fail = fail || !wait_warp(m, &m->o, ph);
-                if (output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out, fail)) return;
+                if (!wait_warp(m, &m->qs, ph)) return t.len - c >= C ? it + 1 : 0;  // q has been multiplied by the last copy
+                if (c + C < t.len) publish();
+                if (!wait_warp(m, &m->o, ph)) return t.len - c >= C ? it + 1 : 0;
+                output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out);
             }
         }
-        if (fail) return;
         if (t.sout) {
 #pragma unroll
             for (int j = 0; j < NK / 2; ++j) {
@@ -826,6 +847,7 @@ __device__ __forceinline__ void role_state(const ChunkParams &p, unsigned char *
             }
         }
     }
+    return 0;
 }
 
 // ---- segments: between the two passes of one launch
@@ -895,7 +917,7 @@ __device__ __forceinline__ int arrivals_of(int i, bool states) {
                   W0 = offsetof(Misc, wfree) / 8, U0 = offsetof(Misc, ufree) / 8;
     if (i >= E0 && i < E0 + TILES) return !states && (i - E0) % 3 == TK ? 2 : 1;  // a k tile is read by q k^T and by U
     if (i == P0 || i == U0 + 1) return 2 * GROUP / 32;                              // warps of the scores' and the state's groups
-    return ((i >= V0 && i < P0) || (i >= W0 && i < W0 + 2) || i == U0) ? GROUP / 32 : 1;  // warps of one group
+    return ((i >= V0 && i < P0) || (i >= W0 && i < W0 + 3) || i == U0) ? GROUP / 32 : 1;  // warps of one group
 }
 __device__ __forceinline__ void init_barriers(Misc *m, bool states) {  // warp 0
     for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_init(reinterpret_cast<uint64_t *>(m) + i, arrivals_of(i, states));
@@ -1147,6 +1169,7 @@ __device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *s
     if (warp == 0) {
         init_barriers(m, cut);
         m->abort = 0;
+        m->products = -1;
     }
     if (warp == WARP_MMA_U) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
@@ -1155,12 +1178,13 @@ __device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *s
     const uint32_t tmem = m->tmem;
     // every role: the pass over the states, the join, the pass over the outputs; or the last alone
     if (warp < 8) {
-        if (!cut || next_pass<true, false>(p, m)) role_scores<SEGMENTS>(p, smem, m, tmem);
+        if (!cut || next_pass<true, false>(p, m)) give_up(m, role_scores<SEGMENTS>(p, smem, m, tmem));
     } else if (warp < 16) {
         more_registers<REGS_STATE>();
 #pragma unroll 1
         for (int pass = cut ? 0 : 1; pass < 2; ++pass) {
-            role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            const uint32_t at = role_state<SEGMENTS>(p, smem, m, tmem, SEGMENTS && pass == 0);
+            if (pass == 1) give_up(m, at);
             if (SEGMENTS && pass == 0 && !next_pass<false, true>(p, m)) break;
         }
     } else if (warp < 24) {
@@ -1181,8 +1205,11 @@ __device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *s
                 role_decay<SEGMENTS>(p, m, states);
             } else if (warp == WARP_MMA_U) {
                 role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
+                drain_mma(&m->drained[0]);
             } else if (warp == WARP_MMA_OUT && !states) {
-                role_mma_out<SEGMENTS>(p, smem, m, tmem);
+                const uint32_t products = role_mma_out<SEGMENTS>(p, smem, m, tmem);
+                if (lane == 0) *reinterpret_cast<volatile int32_t *>(&m->products) = static_cast<int32_t>(products);
+                drain_mma(&m->drained[1]);
             }
             __syncwarp();
             if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
@@ -1352,7 +1379,7 @@ size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
     return len ? layout_of(N, T, H, len).bytes : 0;
 }
 
-cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream) {
+cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream, Withhold withhold) {
     if (few_tokens(a.N, a.T)) return launch_recurrent(a, stream);
     const int sms = num_sms();
     if (sms < 1) return cudaErrorInvalidDevice;
@@ -1364,6 +1391,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
         return cudaErrorInvalidValue;
     p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
+    p.withhold = withhold;
     if (!p.seg_chunks) return run<WHOLE>(p, p.tasks, sms, stream);
     const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);

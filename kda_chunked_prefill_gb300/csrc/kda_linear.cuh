@@ -149,15 +149,5 @@ __device__ __forceinline__ uint32_t fma_bf16(uint32_t a, uint32_t b, uint32_t c)
     return r;
 }
 __device__ __forceinline__ f2 of_bf16(uint32_t u) { return pair(u << 16, u & 0xffff0000u); }
-// `n` threads meet at named barrier `id`; whether any of them says so
-__device__ __forceinline__ bool named_bar_or(int id, int n, bool mine) {
-    uint32_t any;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(any)
-        : "r"(id), "r"(n), "r"(static_cast<uint32_t>(mine))
-        : "memory");
-    return any != 0;
-}
 }  // namespace lin
 }  // namespace kda

@@ -30,6 +30,11 @@ constexpr float G_FLOOR = -138.f;
 
 constexpr int CHUNK = 128;  // tokens
 
+// For tests of the failure detection: in each pass, the number of the chunk of each CTA whose v~ does not get its decays (-1: none).
+struct Withhold {
+    int32_t states = -1, outputs = -1;
+};
+
 // A part of a sequence that one CTA walks: tokens t0 .. t0 + len - 1 of sequence seq, its index-th of count segments; slot: where
 // its state goes.
 struct Segment {
@@ -40,7 +45,7 @@ struct Segment {
 cudaError_t launch_recurrent(const Params &p, cudaStream_t stream);
 
 // chunk by chunk on the tensor cores; the recurrence where sequences are short
-cudaError_t launch_chunked(const Params &p, void *workspace, cudaStream_t stream);
+cudaError_t launch_chunked(const Params &p, void *workspace, cudaStream_t stream, Withhold withhold);
 size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H);
 
 }  // namespace lin

@@ -1,4 +1,4 @@
-// Host side of kda_linear_chunk_fwd and kda_linear_decode_fwd: argument checks and launches.
+// Host side of kda_linear_chunk_fwd (and its debug form) and kda_linear_decode_fwd: argument checks and launches.
 #include <cuda_runtime.h>
 
 #include "kda.h"
@@ -55,17 +55,13 @@ kda_status_t linear_args(const void *q, const void *k, const void *v, const floa
     return KDA_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-kda_status_t kda_linear_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
-                                  const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
-                                  int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
-                                  int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
-                                  int32_t g_per_token, const float *initial_state, float scale, void *o,
-                                  float *final_state, int32_t *status_dev, void *workspace, size_t workspace_bytes,
-                                  kda_stream_t stream) {
+kda_status_t chunk_fwd(const void *q, const void *k, const void *v, const float *g,
+                       const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                       int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
+                       int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                       int32_t g_per_token, const float *initial_state, float scale, void *o,
+                       float *final_state, int32_t *status_dev, void *workspace, size_t workspace_bytes,
+                       kda_stream_t stream, kda::lin::Withhold withhold) {
     kda::lin::Params p;
     const kda_status_t rc = linear_args(q, k, v, g, num_seqs, total_tokens, num_heads, num_qk_heads, head_dim_k,
                                         head_dim_v, q_token_stride, k_token_stride, v_token_stride, g_per_token,
@@ -78,7 +74,36 @@ kda_status_t kda_linear_chunk_fwd(const void *q, const void *k, const void *v, c
     if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     if (num_seqs == 0) return KDA_OK;
     p.cu = cu_seqlens;
-    return kda::lin::launch_chunked(p, workspace, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return kda::lin::launch_chunked(p, workspace, s, withhold) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_linear_chunk_fwd(const void *q, const void *k, const void *v, const float *g,
+                                  const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                  int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
+                                  int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                  int32_t g_per_token, const float *initial_state, float scale, void *o,
+                                  float *final_state, int32_t *status_dev, void *workspace, size_t workspace_bytes,
+                                  kda_stream_t stream) {
+    return chunk_fwd(q, k, v, g, cu_seqlens, num_seqs, total_tokens, num_heads, num_qk_heads, head_dim_k, head_dim_v,
+                     q_token_stride, k_token_stride, v_token_stride, g_per_token, initial_state, scale, o, final_state,
+                     status_dev, workspace, workspace_bytes, stream, {});
+}
+
+kda_status_t kda_linear_chunk_fwd_debug(const void *q, const void *k, const void *v, const float *g, const int32_t
+                                        *cu_seqlens, int32_t num_seqs, int64_t total_tokens, int32_t num_heads,
+                                        int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v, int64_t
+                                        q_token_stride, int64_t k_token_stride, int64_t v_token_stride, int32_t
+                                        g_per_token, const float *initial_state, float scale, void *o, float
+                                        *final_state, int32_t *status_dev, void *workspace, size_t workspace_bytes,
+                                        kda_stream_t stream, int32_t withhold_states, int32_t withhold_outputs) {
+    if (withhold_states < -1 || withhold_outputs < -1) return KDA_ERR_INVALID_ARG;
+    return chunk_fwd(q, k, v, g, cu_seqlens, num_seqs, total_tokens, num_heads, num_qk_heads, head_dim_k, head_dim_v,
+                     q_token_stride, k_token_stride, v_token_stride, g_per_token, initial_state, scale, o, final_state,
+                     status_dev, workspace, workspace_bytes, stream, {withhold_states, withhold_outputs});
 }
 
 size_t kda_linear_chunk_fwd_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t num_heads) {

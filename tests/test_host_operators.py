@@ -52,6 +52,12 @@ def test_linear_chunk_refuses(lib, over, code):
     assert _chunk(lib, **over) == code
 
 
+@pytest.mark.parametrize("withhold", [(-2, -1), (-1, -2), (0, -2 ** 31)])
+def test_linear_chunk_debug_refuses(lib, withhold):
+    args = [FAKE] * 5 + [2, 100, 4, 2, 128, 128, 256, 256, 512, 1, None, 0.1, FAKE, None, None, None, 0, None]
+    assert lib.kda_linear_chunk_fwd_debug(*args, *withhold) == kda.KDA_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("over,code", BAD + [({"Tn": -1}, kda.KDA_ERR_INVALID_ARG), ({"Tn": 65}, kda.KDA_ERR_INVALID_ARG)])
 def test_linear_decode_refuses(lib, over, code):
     assert _decode(lib, **over) == code
