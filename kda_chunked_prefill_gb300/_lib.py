@@ -500,8 +500,9 @@ def decode_fwd(q, k, v, g, beta, num_seqs: int, state=None, scale: Optional[floa
 # A call's host time counts where its kernel takes a few microseconds: each tensor is checked by one expression (the detailed
 # message is made only when it fails), the current stream is read as a handle, and the device is switched only if it has to be.
 _BF16, _F32, _I32, _I8, _F8, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int8, torch.float8_e4m3fn, torch.uint8)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (None on a torch without CUDA, which can import this module and make no call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _need(t, name, dtype, shape, index):

@@ -1,6 +1,9 @@
 """Host-side refusals of the linear-attention, state-cache and add-norm entry points (no GPU: validation runs before any CUDA
 call), and the binding's checks of tensors."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -129,6 +132,21 @@ def test_binding_refuses_cpu_tensors_and_bad_views():
             _lib._heads_view(bad, "q", 4, cpu)
     with pytest.raises(TypeError):
         _lib._heads_view(t.float(), "q", 4, cpu)
+
+
+def test_the_package_imports_on_a_torch_without_cuda():
+    """Inputs, constants and the host checks need no CUDA build of torch: there, its private CUDA bindings do not exist."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, name)\n"
+            "import kda_chunked_prefill_gb300 as kda\n"
+            "from kda_chunked_prefill_gb300 import inputs\n"
+            "inputs.make_inputs([3], 1, seed=0)\n"
+            "t = torch.zeros(4, 2, 128, dtype=torch.bfloat16)\n"
+            "try: kda.add_rms_norm(t, t, torch.ones(128))\n"
+            "except ValueError: print('refused')\n")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, 
+                         cwd=os.path.dirname(os.path.dirname(kda.__file__)))
+    assert run.returncode == 0 and run.stdout.strip() == "refused", run.stderr
 
 
 def test_oracle_recurrence_closed_forms():
