@@ -172,7 +172,14 @@ __global__ void __launch_bounds__(THREADS == 32 ? 32 * NARROW : THREADS)
     const float rstd = sum <= 3.402823466e38f ? 1.f / sqrtf(sum / static_cast<float>(width) + eps) : __int_as_float(0x7fc00000);
     const float amax = max_abs_nan(0.f, mx * rstd);  // max|n|; NaN once anything in the row is not finite
     const bool tiny = amax < TINY;
-    const float mul = tiny ? 0.f : rstd * (E4M3_MAX / amax);
+    float mul = tiny ? 0.f : rstd * (E4M3_MAX / amax);
+    if (mul > 3.402823466e38f) {  // small elements and a small eps: in two factors
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[i][j] *= rstd;
+        mul = E4M3_MAX / amax;
+    }
     if (tid == 0) y_scale[row] = tiny ? 0.f : amax / E4M3_MAX;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -77,6 +77,20 @@ def test_neighbours_of_an_odd_row_stay():
     assert bool((y[65].float() == 1.5).all()) and bool((res[65] == 7).all()) and float(scale[65]) == 5
 
 
+@pytest.mark.parametrize("size", [2.0 ** -119, 1.2 * 2.0 ** -120, 2.0 ** -126])
+@pytest.mark.parametrize("d", [64, 1031])
+def test_small_rows_with_a_small_eps(d, size):
+    """n = h / sqrt(eps) * w is of ordinary size where the factor that takes h * w to the codes, 448 / max|h w|, overflows."""
+    x, r, w = make(3, d, 7, fp32=True)
+    x = torch.zeros_like(x)
+    r[:, ::5] = 0
+    r = r / r.abs().amax(1, keepdim=True) * size
+    w = torch.ones_like(w)
+    y, scale, res = kda.add_rms_norm(x.cuda(), r.cuda(), w.cuda(), 1e-16)
+    assert bool((scale > 2.0 ** -109).all())
+    check(x, r, w, float(np.float32(1e-16)), y, scale, res)
+
+
 @pytest.mark.parametrize("d", [64, 1031, 4096])
 def test_zero_tiny_and_no_number_rows(d):
     x = torch.zeros(6, d, dtype=torch.bfloat16)
