@@ -65,6 +65,7 @@ struct ChunkParams {
     // the rest only with segments (device memory in the workspace)
     int32_t seg_chunks;  // shortest cut that the workspace is sized for
     int32_t most_segs;   // that the workspace holds
+    int32_t most_slots;  // states of cut sequences' segments that it holds
     int32_t sms;
     int32_t *counts;     // [0] segments, [1] barrier between the passes, [2] segments of the pass over the states (0: nothing is cut),
                          // [3] CTAs that have the plan, [6] sequences to join
@@ -976,15 +977,18 @@ __host__ __device__ inline float cut_time(const Cut &c, int H, int sms) {
                     pass_time(c.longest, c.all_s * h, c.tasks_s * h, sms, T_STATES, T_STATES_TASK));
 }
 
-// the segments of a candidate, by slot, and the slots in order of length (tables of both passes)
+// the segments of a candidate, by number, and the numbers in order of length (tables of both passes)
 struct Sorted {
-    alignas(16) uint32_t key[2][SORTED];  // in either pass (outputs, states): chunks << 16 | 0xffff - slot, larger ones first; 0: not in it
+    alignas(16) uint32_t key[2][SORTED];  // in either pass (outputs, states): chunks << 16 | 0xffff - number, larger ones first; 0: not in it
     uint16_t seq[SORTED], index[SORTED];
-    uint16_t order[2][SORTED];            // the slots by key
+    uint16_t order[2][SORTED];            // the numbers by key
 };
 struct PlanShared {
     Sorted sorted[CUTS];
     Cut cuts[CUTS];
+    int slots[CUTS];    // segments of cut sequences
+    int slot[SORTED];   // the chosen candidate's segments' states (of cut sequences)
+    int next;           // states that have been given to sequences
     int time[CUTS][2];  // of the passes: bits of a positive float
     int warps[CUTS][PLAN_GROUP / 32];
     int count[CUTS], total_s, best, cut;  // segments of the pass over the states; sequences cut in more than two
@@ -1009,20 +1013,21 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
         const int64_t b = a.cu[n], e = a.cu[n + 1];
         return start_ok && b >= 0 && e >= b && e <= a.T ? static_cast<int>((e - b + C - 1) / C) : -1;
     };
-    if (tid < CUTS) m.cuts[tid] = Cut{};
+    if (tid < CUTS) m.cuts[tid] = Cut{}, m.slots[tid] = 0;
     if (tid < 2 * CUTS) m.time[tid >> 1][tid & 1] = 0;
     if (tid < CUTS) m.count[tid] = 0;
-    if (tid == 0) m.total_s = m.cut = 0;
+    if (tid == 0) m.total_s = m.cut = m.next = 0;
     __syncthreads();
-    // each group: its candidate's segments, and the first slot of each thread's sequences
+    // each group: its candidate's segments, and the number of the first segment of each thread's sequences
     const int per = (a.N + PLAN_GROUP - 1) / PLAN_GROUP, n0 = x0 * per, n1 = n0 + per < a.N ? n0 + per : a.N;
     Cut own{};
-    int mine = 0;  // (saturating: offsets that are no offsets can add up to anything)
+    int mine = 0, kept = 0;  // (saturating: offsets that are no offsets can add up to anything)
     for (int n = n0; n < n1; ++n) {
         const int c = chunks(n);
         if (c < 0) continue;
         const int k = pieces(c, len), one = (c + k - 1) / k;
         mine = min(mine + k, p.most_segs + 1);
+        if (k > 1) kept = min(kept + k, p.most_slots + 1);
         own.longest = max(own.longest, one);
         own.most = max(own.most, k);
         own.all += c;
@@ -1032,6 +1037,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     if (n0 < n1) {
         atomicMax(&m.cuts[i].longest, own.longest);
         atomicMax(&m.cuts[i].most, own.most);
+        atomicAdd(&m.slots[i], kept);
         atomicAdd(&m.cuts[i].all, own.all);
         atomicAdd(&m.cuts[i].tasks_s, own.tasks_s);
         atomicAdd(&m.cuts[i].all_s, own.all_s);
@@ -1052,7 +1058,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     }
     const int first = upto - mine;
     // more than valid offsets can need: sequences overlap (cu_seqlens goes back), and nothing runs
-    const bool overlap = __syncthreads_or(total > p.most_segs);
+    const bool overlap = __syncthreads_or(total > p.most_segs || m.slots[i] > p.most_slots);
     if (overlap) {
         if (tid == 0) {
             set_status(a.status, KDA_ERR_BAD_SEQLENS);
@@ -1135,19 +1141,25 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
         for (int n = n0; n < n1; ++n) {
             const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
             if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
-            if (k > 2) p.first[atomicAdd(&m.cut, 1)] = make_int2(at, k);
-            for (int j = 0; !sort && j < k; ++j) {
-                const Segment s = segment(n, j, at + j);
+            const int slot = k > 1 ? atomicAdd(&m.next, k) : 0;
+            if (k > 2) p.first[atomicAdd(&m.cut, 1)] = make_int2(slot, k);
+            for (int j = 0; j < k; ++j) {
+                if (sort) {
+                    m.slot[at + j] = slot + j;
+                    continue;
+                }
+                const Segment s = segment(n, j, slot + j);
                 p.segs[at + j] = s;
                 if (states_len(0, k, j) >= 0) p.segs_s[atomicAdd(&m.total_s, 1)] = s;
             }
             at += k;
         }
+        named_bar_sync(1, PLAN_GROUP);
         if (sort)
             for (int r = x0; r < total; r += PLAN_GROUP) {
                 const int x = t.order[0][r], y = r < m.count[i] ? t.order[1][r] : -1;
-                p.segs[r] = segment(t.seq[x], t.index[x], x);
-                if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], y);
+                p.segs[r] = segment(t.seq[x], t.index[x], m.slot[x]);
+                if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], m.slot[y]);
             }
         named_bar_sync(1, PLAN_GROUP);
         if (x0 == 0) {
@@ -1355,19 +1367,22 @@ int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
 }
 
 struct Layout {
-    int64_t most;  // segments at most: ceil(c / L) <= c' / L + 1 summed over the sequences
+    int64_t most;   // segments at most: ceil(c / L) <= c' / L + 1 summed over the sequences
+    int64_t slots;  // of cut sequences (c > L): ceil(c / L) <= 2 c' / L
     size_t first, segs, segs_s, decays, states, bytes;
 };
 Layout layout_of(int64_t N, int64_t T, int64_t H, int len) {
     Layout l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l.most = T / (static_cast<int64_t>(C) * len) + N;
+    l.slots = 2 * T / (static_cast<int64_t>(C) * len);
+    if (l.slots > l.most) l.slots = l.most;
     l.first = 256;
     l.segs = up(l.first + sizeof(int2) * N);
     l.segs_s = up(l.segs + sizeof(Segment) * l.most);
     l.decays = up(l.segs_s + sizeof(Segment) * l.most);
-    l.states = up(l.decays + sizeof(float) * l.most * H);
-    l.bytes = l.states + sizeof(float) * DK * DV * l.most * H;
+    l.states = up(l.decays + sizeof(float) * l.slots * H);
+    l.bytes = l.states + sizeof(float) * DK * DV * l.slots * H;
     return l;
 }
 }  // namespace
@@ -1396,6 +1411,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.most_segs = static_cast<int32_t>(l.most);
+    p.most_slots = static_cast<int32_t>(l.slots);
     p.sms = sms;
     p.counts = reinterpret_cast<int32_t *>(ws);
     p.first = reinterpret_cast<int2 *>(ws + l.first);

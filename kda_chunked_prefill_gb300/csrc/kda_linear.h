@@ -36,7 +36,7 @@ struct Withhold {
 };
 
 // A part of a sequence that one CTA walks: tokens t0 .. t0 + len - 1 of sequence seq, its index-th of count segments; slot: where
-// its state goes.
+// its state goes, if the sequence is cut.
 struct Segment {
     int32_t t0, len, seq, index, count, slot;
 };

@@ -179,6 +179,27 @@ def test_cut_sequences_with_states_in_place():
     assert torch.equal(o, want[0]) and torch.equal(d["s0"], want[1])
 
 
+@pytest.mark.parametrize("lens,H", [([17] * 1000, 16), ([0] * 300 + [2100, 1, 700] + [12] * 200, 4), ([5000, 4000, 300], 1),
+                                    ([4000] + [20] * 500, 1)])
+def test_workspace_holds_the_states_of_cut_sequences_alone(lens, H):
+    """Its size does not grow by a state for every sequence, and nothing behind it is written."""
+    T, N = sum(lens), len(lens)
+    need = kda.linear_workspace_size(N, T, H)
+    # a sequence is cut where it is longer than 4 chunks at least, into no more than twice its length over theirs
+    assert need <= 2 * T // 512 * H * 4 * (D * D + 1) + (N + T // 512) * 64 + 4096
+    rep = 4 if H == 16 else 1
+    x = make(lens, H // rep, H // rep, seed=41)
+    d = dev(x)
+    d["g"], d["v"], d["s0"] = (d["g"].repeat(1, rep), d["v"].repeat(1, rep, 1), d["s0"].repeat(1, rep, 1, 1))
+    d["q"], d["k"] = (d[key].repeat(1, rep, 1) for key in ("q", "k"))
+    ws = torch.full((need + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    o, fs = torch.empty_like(d["v"]), torch.empty_like(d["s0"])
+    status = torch.ones(1, dtype=torch.int32, device="cuda")
+    kda.kda_linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], x["scale"], o, fs, status, workspace=ws[:need])
+    assert int(status) == 0 and bool((ws[need:] == 0x5a).all())
+    check(x, o[:, :H // rep], fs[:, :H // rep])
+
+
 def test_invalid_sequences_by_the_thousand():
     """Most of 70000 offsets out of range: those sequences are skipped and reported, the others computed."""
     N, T = 70000, 640010
