@@ -86,8 +86,7 @@ struct Misc {
     uint64_t wfree[2], zeroed;        // w read; rows behind a segment zeroed
     uint64_t go;                      // the first g have been read
     uint64_t ufree;                   // U read
-    uint64_t ofree;                   // O read
-    uint64_t drained[2];              // tensor core -> an MMA warp at its end
+    uint64_t ofree;                   // O read, and written to the q tile
     uint32_t tmem;                    // address of the tensor memory
     int32_t abort;                    // a wait ran out
     int32_t easy;                     // this chunk's decay is above EASY
@@ -129,8 +128,9 @@ __device__ __forceinline__ void more_registers() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr int GRID_POLLS = 1 << 24;
-// waits of up to WAIT_NS each before a role gives up; and before one that is to leave takes its own copies or MMAs for complete
+// waits of up to WAIT_NS each before a role gives up; and before one that has given up takes its own copies for complete
 constexpr int WAITS = 20000, WAITS_DRAIN = 100;
+constexpr int MMAS_END = 200000;  // cycles; a chunk's MMAs, the most that are ever queued, take 3000
 
 struct Task {
     int64_t t0;
@@ -218,7 +218,7 @@ __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
     }
     return true;
 }
-// a role that leaves waits for what it has in flight
+// a role that has given up waits for what it has in flight
 __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
     for (int i = 0; i < WAITS_DRAIN && !mbar_wait_some(bar, parity); ++i) {
@@ -415,15 +415,6 @@ __device__ __forceinline__ void role_mma_state(const ChunkParams &p, unsigned ch
         }
     }
 }
-// The end of either: what the warp has issued is through with the CTA's memory (also where somebody has given up, and a role that
-// would have waited for it has left).
-__device__ __forceinline__ void drain_mma(uint64_t *bar) {
-    if (elect_one()) umma_commit(bar);
-    __syncwarp();
-    wait_drain(bar, 0);
-    __syncwarp();
-}
-
 // ---- one warp: decay tables. Lane l has tokens 4 l .. 4 l + 3, eight lanes a block of 32.
 template <bool SEG>
 __device__ __forceinline__ void role_decay(const ChunkParams &p, Misc *m, bool states) {
@@ -597,11 +588,11 @@ __device__ __forceinline__ void role_v(const ChunkParams &p, unsigned char *smem
     }
 }
 
-// The scores' and the state's warps meet at one named barrier, which has no limit, and where the storing warp alone waits: for a full
-// chunk's output tile. It comes there after that chunk's P v, so every other warp has arrived at the chunk's p by then, and none can
-// pass the next chunk's o before it is back. So a warp that gives up behind p still arrives for a chunk whose P v is issued, and
-// for no other, and the storing warp finds just the arrivals that it waits for.
-// at: what the role returned, the number of the full chunk behind whose p it gave up, plus one, or 0
+// The scores' and the state's warps meet at one named barrier, which has no limit, and where the storing warp alone waits: for a
+// chunk's output in the q tile. It comes there after that chunk's P v, so every other warp has arrived at the chunk's p by then, and
+// none can pass the next chunk's o before it is back. So a warp that gives up behind p still arrives for a chunk whose P v is issued,
+// and for no other, and the storing warp finds just the arrivals that it waits for.
+// at: what the role returned, the number of the chunk behind whose p it gave up, plus one, or 0
 __device__ __forceinline__ void give_up(Misc *m, uint32_t at) {
     if (at == 0 || threadIdx.x >> 5 == WARP_STORE) return;
 #pragma unroll 1
@@ -616,14 +607,11 @@ __device__ __forceinline__ void give_up(Misc *m, uint32_t at) {
 }
 
 // A chunk's output from tensor memory into the q tile, and out. The scores' and the state's warps share it: four threads a token
-// row, 32 values each (half, part).
-__device__ __forceinline__ void output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
-                                            int slot, int tid, int half, int part, float factor) {
-    const int left = t.len - c;
-    // A full chunk's row goes into the tile, its 16-byte pieces swizzled by row % 8; another's straight out, as far as it is one.
-    unsigned char *row = left >= C ? smem + slot * TILE + half * PANEL + tid * 128
-                                   : reinterpret_cast<unsigned char *>(p.a.o + ((t.t0 + c + tid) * p.a.H + t.h) * DV + 64 * half);
-    const int swizzle = left >= C ? tid & 7 : 0;
+// row, 32 values each (half, part). False: given up.
+__device__ __forceinline__ bool output_part(const ChunkParams &p, unsigned char *smem, Misc *m, uint32_t tmem_lanes, const Task &t, int c,
+                                            int slot, int tid, int half, int part, float factor, uint32_t ph) {
+    unsigned char *tile = smem + slot * TILE + half * PANEL;
+    const int left = t.len - c, lane = threadIdx.x & 31;
     tc_fence_after();
     const f2 s2 = pair(factor, factor);
 #pragma unroll 1
@@ -632,26 +620,32 @@ __device__ __forceinline__ void output_part(const ChunkParams &p, unsigned char 
         tmem_ld16(tmem_lanes + COL_O + 64 * half + 32 * part + 16 * b, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j) {  // the tile's swizzle: 16-byte piece ^ row % 8
             const int i = 8 * j;
-            const uint4 x = make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
-                                       bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
-            if (tid < left) *reinterpret_cast<uint4 *>(row + (((4 * part + 2 * b + j) ^ swizzle) << 4)) = x;
+            *reinterpret_cast<uint4 *>(tile + tid * 128 + (((4 * part + 2 * b + j) ^ (tid & 7)) << 4)) =
+                make_uint4(bf16_of(mul2(s2, pair(o[i], o[i + 1]))), bf16_of(mul2(s2, pair(o[i + 2], o[i + 3]))),
+                           bf16_of(mul2(s2, pair(o[i + 4], o[i + 5]))), bf16_of(mul2(s2, pair(o[i + 6], o[i + 7]))));
         }
     }
     tc_fence_before();
     arrive_warp(&m->ofree);
-    const bool stores = threadIdx.x >> 5 == WARP_STORE;
-    if (left >= C) {
+    if (left < C) {  // rows behind the segment are not written
+        if (!wait_warp(m, &m->ofree, ph)) return false;
+#pragma unroll 1
+        for (int i = 128 * part + tid; i < left * 8; i += 256) {
+            const int r = i >> 3, j = i & 7;
+            *reinterpret_cast<uint4 *>(p.a.o + ((t.t0 + c + r) * p.a.H + t.h) * DV + 64 * half + 8 * j) =
+                *reinterpret_cast<const uint4 *>(tile + r * 128 + ((j ^ (r & 7)) << 4));
+        }
+    } else {
         fence_proxy_async_shared();
-        // one warp stores a whole chunk's o and frees the tile; the others go on
-        if (!stores)
-            named_bar_arrive(2, 2 * GROUP);
-        else
-            named_bar_sync(2, 2 * GROUP);
     }
-    if (stores) {
-        if ((threadIdx.x & 31) == 0) {
+    // one warp stores a whole chunk's o and frees the tile; the others go on
+    if (threadIdx.x >> 5 != WARP_STORE) {
+        named_bar_arrive(2, 2 * GROUP);
+    } else {
+        named_bar_sync(2, 2 * GROUP);
+        if (lane == 0) {
             if (left >= C) {
                 const unsigned char *src = smem + slot * TILE;
                 tma_store_3d(&p.to, src, 0, t.h, static_cast<int>(t.t0 + c), evict_first());
@@ -663,6 +657,7 @@ __device__ __forceinline__ void output_part(const ChunkParams &p, unsigned char 
         }
         __syncwarp();
     }
+    return true;
 }
 
 // ---- warps 0-7: decayed scores. Two threads share a token row: key blocks 0 and 3, or 1 and 2.
@@ -736,8 +731,8 @@ __device__ __forceinline__ uint32_t role_scores(const ChunkParams &p, unsigned c
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&m->p);
-            if (!wait_warp(m, &m->o, ph)) return t.len - c >= C ? it + 1 : 0;
-            output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out);
+            if (!wait_warp(m, &m->o, ph)) return it + 1;
+            if (!output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 0, out, ph)) return it + 1;
         }
     }
     if (threadIdx.x == 32 * WARP_STORE) bulk_wait_all();
@@ -811,7 +806,7 @@ __device__ __forceinline__ uint32_t role_state(const ChunkParams &p, unsigned ch
                 }
                 arrive_warp(&m->p);
             }
-            if (!wait_warp(m, &m->u, ph)) return t.len - c >= C ? it + 1 : 0;
+            if (!wait_warp(m, &m->u, ph)) return it + 1;
             tc_fence_after();
             float less = m->factor[it & 3];
             if (less > 0.f) {  // a fast decay, by itself
@@ -832,10 +827,10 @@ __device__ __forceinline__ uint32_t role_state(const ChunkParams &p, unsigned ch
             tc_fence_before();
             arrive_warp(&m->ufree);
             if (!states) {
-                if (!wait_warp(m, &m->qs, ph)) return t.len - c >= C ? it + 1 : 0;  // q has been multiplied by the last copy
+                if (!wait_warp(m, &m->qs, ph)) return it + 1;  // q has been multiplied by the last copy
                 if (c + C < t.len) publish();
-                if (!wait_warp(m, &m->o, ph)) return t.len - c >= C ? it + 1 : 0;
-                output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out);
+                if (!wait_warp(m, &m->o, ph)) return it + 1;
+                if (!output_part(p, smem, m, tmem + lanes, t, c, slot_of(TQ, it, states), tid, half, 1, out, ph)) return it + 1;
             }
         }
         if (t.sout) {
@@ -935,8 +930,10 @@ __device__ __forceinline__ bool next_pass(const ChunkParams &p, Misc *m) {
     if (JOINS) join_states(p, threadIdx.x - GROUP);
     cta_sync();
     if (LEADS && threadIdx.x < 32) {
-        for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
-        init_barriers(m, false);
+        if (*reinterpret_cast<volatile int32_t *>(&m->abort) == 0) {
+            for (int i = threadIdx.x; i < BARRIERS; i += 32) mbar_inval(reinterpret_cast<uint64_t *>(m) + i);  // (every arrival has come)
+            init_barriers(m, false);
+        }
         __syncwarp();
         if (threadIdx.x == 0 && !grid_sync(p.counts + 1, 2 * gridDim.x)) m->abort = 1;
     }
@@ -987,7 +984,7 @@ struct PlanShared {
     Sorted sorted[CUTS];
     Cut cuts[CUTS];
     int slots[CUTS];    // segments of cut sequences
-    int slot[SORTED];   // the chosen candidate's segments' states (of cut sequences)
+    int slot[SORTED];   // of the chosen candidate: the first state of the (cut) sequence whose first segment has this number
     int next;           // states that have been given to sequences
     int time[CUTS][2];  // of the passes: bits of a positive float
     int warps[CUTS][PLAN_GROUP / 32];
@@ -1143,11 +1140,8 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
             if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
             const int slot = k > 1 ? atomicAdd(&m.next, k) : 0;
             if (k > 2) p.first[atomicAdd(&m.cut, 1)] = make_int2(slot, k);
-            for (int j = 0; j < k; ++j) {
-                if (sort) {
-                    m.slot[at + j] = slot + j;
-                    continue;
-                }
+            if (sort && k > 0) m.slot[at] = slot;
+            for (int j = 0; !sort && j < k; ++j) {
                 const Segment s = segment(n, j, slot + j);
                 p.segs[at + j] = s;
                 if (states_len(0, k, j) >= 0) p.segs_s[atomicAdd(&m.total_s, 1)] = s;
@@ -1155,11 +1149,14 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
             at += k;
         }
         named_bar_sync(1, PLAN_GROUP);
+        auto numbered = [&](int x) {
+            const int j = t.index[x];
+            return segment(t.seq[x], j, m.slot[x - j] + j);
+        };
         if (sort)
             for (int r = x0; r < total; r += PLAN_GROUP) {
-                const int x = t.order[0][r], y = r < m.count[i] ? t.order[1][r] : -1;
-                p.segs[r] = segment(t.seq[x], t.index[x], m.slot[x]);
-                if (y >= 0) p.segs_s[r] = segment(t.seq[y], t.index[y], m.slot[y]);
+                p.segs[r] = numbered(t.order[0][r]);
+                if (r < m.count[i]) p.segs_s[r] = numbered(t.order[1][r]);
             }
         named_bar_sync(1, PLAN_GROUP);
         if (x0 == 0) {
@@ -1217,11 +1214,9 @@ __device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *s
                 role_decay<SEGMENTS>(p, m, states);
             } else if (warp == WARP_MMA_U) {
                 role_mma_state<SEGMENTS>(p, smem, m, tmem, states);
-                drain_mma(&m->drained[0]);
             } else if (warp == WARP_MMA_OUT && !states) {
                 const uint32_t products = role_mma_out<SEGMENTS>(p, smem, m, tmem);
                 if (lane == 0) *reinterpret_cast<volatile int32_t *>(&m->products) = static_cast<int32_t>(products);
-                drain_mma(&m->drained[1]);
             }
             __syncwarp();
             if (SEGMENTS && pass == 0 && !next_pass<false, false>(p, m)) break;
@@ -1231,7 +1226,12 @@ __device__ __forceinline__ void run_roles(const ChunkParams &p, unsigned char *s
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && m->abort) set_status(p.a.status, KDA_ERR_TIMEOUT);
-    if (warp == WARP_MMA_U) tmem_dealloc(tmem, 512);
+    if (warp == WARP_MMA_U) {
+        if (m->abort)  // what has been issued may have nobody left that waited for it: it ends, then the CTA does
+            for (const long long from = clock64(); clock64() - from < MMAS_END;) __nanosleep(1000);
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
 // CTA 0 plans, and the others wait for the launch's token in the workspace, which the last of them takes away again: the memory
