@@ -461,9 +461,10 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
  * the chunk's g up to token i,
  *       o_i = scale * (e^{G_i} S^T q_i + sum_{j<=i} e^{G_i-G_j} (q_i.k_j) v_j)
  *       S  <- e^{G_end} S + sum_j e^{G_end-G_j} k_j v_j^T
- * (every exponent is a sum of g <= 0). Sequences of few tokens (9 on average)
- * run the recurrence itself. Long sequences are cut where there are few, in one
- * cooperative launch.
+ * (every exponent is a sum of g <= 0). Where sequences have few tokens (9 on
+ * average) those of up to 64 run the recurrence itself, in a launch of its own.
+ * Long sequences are cut where there are few, in one cooperative launch. So the
+ * last bits of a sequence's results depend on what is beside it in the batch.
  * (Not part of the method's pages.)
  *   q, k          bf16, num_qk_heads heads of 128 channels per token; value head
  *                 h reads query/key head h / (num_heads / num_qk_heads), so

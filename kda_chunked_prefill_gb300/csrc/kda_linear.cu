@@ -999,6 +999,13 @@ __device__ __forceinline__ bool equal_lengths(const ChunkParams &p) {
     return __syncthreads_and(equal);
 }
 
+// some sequence is not left out (or its offsets say so, valid or not)
+__device__ __forceinline__ bool some_longer(const ChunkParams &p) {
+    bool longer = false;
+    for (int n = threadIdx.x; n < p.a.N; n += THREADS) longer = longer || static_cast<int64_t>(p.a.cu[n + 1]) - p.a.cu[n] > p.a.longest;
+    return __syncthreads_or(longer);
+}
+
 // all threads of one CTA; the others wait for it
 __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     const Params &a = p.a;
@@ -1006,9 +1013,10 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
     const int len = cut_length(i, p.seg_chunks);
     const bool start_ok = a.cu[0] == 0;
     const bool keep = a.s0 && a.s0 == a.sT;
-    auto chunks = [&](int n) -> int {
+    auto chunks = [&](int n) -> int {  // -1: no valid offsets; -2: left out
         const int64_t b = a.cu[n], e = a.cu[n + 1];
-        return start_ok && b >= 0 && e >= b && e <= a.T ? static_cast<int>((e - b + C - 1) / C) : -1;
+        if (!(start_ok && b >= 0 && e >= b && e <= a.T)) return -1;
+        return e - b <= a.longest ? -2 : static_cast<int>((e - b + C - 1) / C);
     };
     if (tid < CUTS) m.cuts[tid] = Cut{}, m.slots[tid] = 0;
     if (tid < 2 * CUTS) m.time[tid >> 1][tid & 1] = 0;
@@ -1137,7 +1145,7 @@ __device__ __forceinline__ void plan(const ChunkParams &p, PlanShared &m) {
         int at = first;
         for (int n = n0; n < n1; ++n) {
             const int c = chunks(n), k = c < 0 ? 0 : pieces(c, len);
-            if (c < 0) set_status(a.status, KDA_ERR_BAD_SEQLENS);
+            if (c == -1) set_status(a.status, KDA_ERR_BAD_SEQLENS);
             const int slot = k > 1 ? atomicAdd(&m.next, k) : 0;
             if (k > 2) p.first[atomicAdd(&m.cut, 1)] = make_int2(slot, k);
             if (sort && k > 0) m.slot[at] = slot;
@@ -1272,6 +1280,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_linear_chunk_kernel(const __gr
     if (MODE == WHOLE || (MODE == EITHER && equal_lengths(p))) {
         if (MODE != PLANNED) run_roles<false>(p, smem);
     } else if (MODE != WHOLE) {
+        if (MODE == PLANNED && p.a.longest >= 0 && !some_longer(p)) return;
         if (wait_for_plan(p, smem))
             run_roles<true>(p, smem);
         else if (threadIdx.x == 0)
@@ -1340,7 +1349,13 @@ cudaError_t run(const ChunkParams &p, int64_t most_tasks, int sms, cudaStream_t 
 // Sequences of few tokens run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 128.
 // 16 heads, 17 tokens each: 16 sequences 21 us and as chunks 14, 64 sequences 78 and 50, 256 sequences 276 and 178; a token
 // more or less is 1.0, 3.7 and 13.5 us of the recurrence, so they meet at 9 to 10 tokens.
+//
+// That is for sequences of like lengths. A batch of so few tokens on average may hold long sequences beside many short ones (prompts
+// among single tokens), and the host does not know. Those of more than FEW_LONGEST tokens then run as chunks, in a second launch that
+// ends at once where there are none. 256 sequences of one token, 16 heads: 83.3 us with it, 81.6 without; 255 of one token and one of
+// 2049: 136 us, and 1660 by the recurrence alone.
 bool few_tokens(int64_t N, int64_t T) { return T <= 9 * N; }
+constexpr int FEW_LONGEST = KDA_DECODE_MAX_TOKENS;  // what the recurrence's own entry point takes
 
 // Sequences of equal lengths are estimated to be as fast whole as cut (4 x 2048, 16 heads: 50 us, cut 60). Every CTA
 // then looks whether they are equal, and none plans if so: the host does not know, and a padded batch looks the same to it.
@@ -1366,6 +1381,13 @@ int segment_chunks(int64_t N, int64_t T, int64_t H, int sms) {
     return static_cast<int>(len);
 }
 
+// The same for what a batch of few tokens on average holds of long sequences, at most long_sequences(): always planned.
+int64_t long_sequences(int64_t N, int64_t T) { return T / (FEW_LONGEST + 1) < N ? T / (FEW_LONGEST + 1) : N; }
+int segment_chunks_of_long(int64_t longer, int64_t T, int64_t H, int sms) {
+    const int len = segment_chunks(longer, T, H, sms);
+    return len ? len : static_cast<int>((T + C - 1) / C);
+}
+
 struct Layout {
     int64_t most;   // segments at most: ceil(c / L) <= c' / L + 1 summed over the sequences
     int64_t slots;  // of cut sequences (c > L): ceil(c / L) <= 2 c' / L
@@ -1388,27 +1410,38 @@ Layout layout_of(int64_t N, int64_t T, int64_t H, int len) {
 }  // namespace
 
 size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
-    if (N < 1 || T < 1 || H < 1 || few_tokens(N, T)) return 0;
+    if (N < 1 || T < 1 || H < 1) return 0;
+    const bool few = few_tokens(N, T);
+    if (few && T <= FEW_LONGEST) return 0;
     const int sms = num_sms();
-    const int len = sms > 0 ? segment_chunks(N, T, H, sms) : 0;
+    if (sms < 1) return 0;
+    if (few) N = long_sequences(N, T);
+    const int len = few ? segment_chunks_of_long(N, T, H, sms) : segment_chunks(N, T, H, sms);
     return len ? layout_of(N, T, H, len).bytes : 0;
 }
 
 cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream, Withhold withhold) {
-    if (few_tokens(a.N, a.T)) return launch_recurrent(a, stream);
+    const bool few = few_tokens(a.N, a.T);
+    if (few && a.T <= FEW_LONGEST) return launch_recurrent(a, stream);
     const int sms = num_sms();
     if (sms < 1) return cudaErrorInvalidDevice;
     ChunkParams p{};
     p.a = a;
+    if (few) {
+        p.a.longest = FEW_LONGEST;
+        const cudaError_t e = launch_recurrent(p.a, stream);
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t N = few ? long_sequences(a.N, a.T) : a.N;
     const int hk = a.H / a.rep;
     if (!encode(&p.tq, a.q, a.T, hk, a.qs) || !encode(&p.tk, a.k, a.T, hk, a.ks) || !encode(&p.tv, a.v, a.T, a.H, a.vs) ||
         !encode(&p.to, a.o, a.T, a.H, static_cast<int64_t>(a.H) * DV))
         return cudaErrorInvalidValue;
-    p.seg_chunks = segment_chunks(a.N, a.T, a.H, sms);
+    p.seg_chunks = few ? segment_chunks_of_long(N, a.T, a.H, sms) : segment_chunks(N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
     p.withhold = withhold;
     if (!p.seg_chunks) return run<WHOLE>(p, p.tasks, sms, stream);
-    const Layout l = layout_of(a.N, a.T, a.H, p.seg_chunks);
+    const Layout l = layout_of(N, a.T, a.H, p.seg_chunks);
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.most_segs = static_cast<int32_t>(l.most);
     p.most_slots = static_cast<int32_t>(l.slots);
@@ -1422,7 +1455,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.go = reinterpret_cast<unsigned long long *>(ws + 32);
     static std::atomic<unsigned long long> calls{0};
     p.token = (++calls + static_cast<unsigned long long>(reinterpret_cast<uintptr_t>(&calls))) * 0x9e3779b97f4a7c15ull;
-    return whole_if_equal(a.N, a.T, a.H, p.seg_chunks, sms) ? run<EITHER>(p, l.most * a.H, sms, stream)
+    return !few && whole_if_equal(a.N, a.T, a.H, p.seg_chunks, sms) ? run<EITHER>(p, l.most * a.H, sms, stream)
                                                             : run<PLANNED>(p, l.most * a.H, sms, stream);
 }
 

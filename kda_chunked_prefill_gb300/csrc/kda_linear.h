@@ -17,6 +17,7 @@ struct Params {
     int32_t steps;
     int32_t N;
     int64_t T;
+    int64_t longest;  // with cu: sequences of more tokens are left out (the recurrence), of no more (chunks; negative: none is)
     int32_t H, rep;  // value heads; value heads per query/key head
     const float *s0;
     float scale;

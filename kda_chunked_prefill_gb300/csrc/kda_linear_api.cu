@@ -45,6 +45,7 @@ kda_status_t linear_args(const void *q, const void *k, const void *v, const floa
     p->steps = 0;
     p->N = num_seqs;
     p->T = tokens;
+    p->longest = -1;
     p->H = num_heads;
     p->rep = num_heads / num_qk_heads;
     p->s0 = s0;

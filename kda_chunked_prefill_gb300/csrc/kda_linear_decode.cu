@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_linear_recurrent_kernel(c
         }
         bos = b;
         len = e - b;
+        if (p.longest >= 0 && len > p.longest) return;  // runs in chunks
     } else {
         bos = static_cast<int64_t>(n) * p.steps;
         len = p.steps;

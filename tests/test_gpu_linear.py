@@ -179,6 +179,47 @@ def test_cut_sequences_with_states_in_place():
     assert torch.equal(o, want[0]) and torch.equal(d["s0"], want[1])
 
 
+@pytest.mark.parametrize("lens,H", [([1] * 255 + [2049], 2), ([0] * 60 + [300, 64, 65, 1] + [2] * 5, 3), ([7] * 30 + [0, 90] + [1] * 3, 2),
+                                    ([9] * 20, 2), ([64, 0, 0, 0, 0, 0, 0, 0], 2), ([0] * 7 + [65, 0], 2),
+                                    ([0] * 800 + [6000, 1, 900], 1)])
+def test_long_sequences_among_short_ones(lens, H):
+    """Few tokens a sequence on average, but not in every one."""
+    x = make(lens, H, H, seed=42, extra=5)
+    x["g"][sum(lens):] = float("nan")
+    d = dev(x)
+    o = torch.full_like(d["v"], 7.0)
+    status = torch.ones(1, dtype=torch.int32, device="cuda")
+    kda.kda_linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], x["scale"], o, d["s0"], status)  # states in place
+    x["g"][sum(lens):] = 0
+    check(x, o, d["s0"])
+    assert int(status) == 0 and bool((o[sum(lens):] == 7.0).all())
+
+
+def test_a_sequence_decides_its_form_by_its_own_length():
+    """A prompt among single tokens gives what it gives alone, and so do they: chunks and the recurrence round differently."""
+    x = make([1] * 40 + [300], 2, 2, seed=43)
+    d = dev(x)
+    cut = lambda a, b: [d[key][a:b] for key in ("q", "k", "v", "g")]
+    cu = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+    o, fs = kda.linear_chunk_fwd(*cut(0, 340), d["cu"], d["s0"], check=True)
+    a = kda.linear_chunk_fwd(*cut(0, 40), cu(*range(41)), d["s0"][:40].contiguous(), check=True)
+    b = kda.linear_chunk_fwd(*cut(40, 340), cu(0, 300), d["s0"][40:].contiguous(), check=True)
+    assert torch.equal(o, torch.cat([a[0], b[0]])) and torch.equal(fs, torch.cat([a[1], b[1]]))
+
+
+@pytest.mark.parametrize("cu", [[0] + [100] * 40 + [90, 200], [0, 150] + [100] * 40, [0] * 40 + [-5, 200], [0] * 40 + [210]])
+def test_bad_offsets_of_a_batch_of_few_tokens(cu):
+    """Reported, whatever form the valid ones run; rows of no valid sequence are left."""
+    x = make([200], 2, 2, seed=44)
+    d = dev(x)
+    s0 = torch.zeros(len(cu) - 1, 2, D, D, device="cuda")
+    o = torch.full_like(d["v"], 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], torch.tensor(cu, dtype=torch.int32, device="cuda"), s0, x["scale"], o,
+                             torch.empty_like(s0), status)
+    assert int(status) == kda.KDA_ERR_BAD_SEQLENS
+
+
 @pytest.mark.parametrize("lens,H", [([17] * 1000, 16), ([0] * 300 + [2100, 1, 700] + [12] * 200, 4), ([5000, 4000, 300], 1),
                                     ([4000] + [20] * 500, 1)])
 def test_workspace_holds_the_states_of_cut_sequences_alone(lens, H):
