@@ -473,7 +473,8 @@ kda_status_t kda_decode_fwd(const void *q, const void *k, const void *v, const f
  *   *_token_stride  elements from one token to the next (>= heads x 128, a
  *                 multiple of 8): q, k and v may be slices of one projection.
  *   g             fp32 natural-log decay, g <= 0 (-inf forgets everything; a g
- *                 below -138 counts as -inf): [total_tokens, num_heads] with
+ *                 below -138 counts as -inf, and a decay over several tokens
+ *                 below 2^-126 may count as 0): [total_tokens, num_heads] with
  *                 g_per_token = 1, [num_heads] with 0.
  *   cu_seqlens    int32 [num_seqs + 1]: cu[0] = 0, nondecreasing, cu[num_seqs] <=
  *                 total_tokens. Rows of o behind the last sequence are left as

@@ -8,7 +8,8 @@
 // Bound by memory: 7 bytes per element (2 + 2 in, 2 + 1 out; 11 with an fp32
 // residual).
 //
-// 8192 rows of 2048 with a bf16 residual: 20.5 us, 5.7 TB/s (85 % of a copy).
+// 8192 rows of 2048 (calls replayed from a graph): with a bf16 residual 20.5 us, 5.7 TB/s (86 % of a copy); with an fp32 residual
+// 30.8 us, 6.0 TB/s (90 %).
 //
 // Rows are cut at multiples of 8 elements of the whole tensor, not of the row:
 // with 16-byte-aligned tensors every such group is one aligned access of x, r, r'

@@ -19,20 +19,22 @@
 // Why this split. U does not depend on S, so the recurrence from chunk to chunk is one fused multiply-add per state element and
 // its rounding to bf16 for the next q S: S stays in fp32 registers (two threads share a value column) and is never accumulated
 // by the tensor cores over many chunks. v~ in two bf16 terms, both multiplied by the exact bf16 k, keeps the final state within
-// 4e-6 (relative, against 64 bits; one term: 2e-3, and for a third tensor memory has no room); P and the copy of S that q
+// 4e-6 (relative, against 64 bits; one term: 2e-3; three: 2e-7, and 10 to 13 % more time); P and the copy of S that q
 // multiplies are rounded once to bf16, like o.
 //
 // Decays: every factor is 2^x with x a sum of same-signed terms that starts at the nearer end (prefixes within 32 tokens,
 // suffixes within 32 tokens plus whole-block totals), so its absolute error is a few units in the last place of x itself, never
-// of the chunk's total, and no factor exceeds 1 (but see EASY).
+// of the chunk's total, and no factor exceeds 1 (but see EASY). Scores between tokens of one block of 32 are the exception: their x
+// is the difference of two prefixes from the block's start, off by a few units in the last place of those. That is 1e-5 where the
+// block forgets once, and 5e-4 at most (32 tokens of -inf): below the rounding of P.
 //
 // Cut sequences (one or few long prompts): a launch makes the segments' states from zero (v, k and g alone), joins them to entry
 // states, E' = decay E + N, and then makes the outputs. That reads k and v twice, and takes 1.7 us more a chunk.
 //
 // Bound by latency: one chunk takes an SM 2.6 us, with 1.5 us of MMAs and 0.8 us of memory at an SM's share. The chain is
-// q k^T -> P (1.2 us) -> P v (0.6) -> o (0.4) -> q k^T of the next chunk (0.4), because tensor memory holds no second score tile
-// beside O, U and v~. 4 sequences of 2048, 16 heads (64 tasks): 50 us; 8 of 2048: 56 us, 4.9 TB/s; one of 65536, 4 heads (cut in
-// 37): 105 us.
+// q k^T -> P (1.2 us) -> P v (0.6) -> o (0.4) -> q k^T of the next chunk (0.4), because P lies over the scores: q k^T waits behind P v.
+// (Columns of P's own would need v~ in two stages instead of four.) 4 sequences of 2048, 16 heads (64 tasks): 50 us; 8 of 2048: 56 us,
+// 4.9 TB/s; one of 65536, 4 heads (cut in 37): 105 us; one of 16384, 96 heads: 356 us, 4.6 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
