@@ -246,12 +246,18 @@ __device__ __forceinline__ float log2_decay(float g) {  // 2^-200 is 0 in fp32; 
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g * LOG2E), "f"(-200.f));
     return r;
 }
-// The decay 2^x of a state that many steps multiply, with all of fp32's relative precision: up to 1/2 (and at 0, which is -1) the
-// positive factor itself, above it the negative factor minus one. (Minus one, so that a slow decay is not rounded away step after
-// step; not for a fast one, whose difference from 1 has lost its last bits: at 2^-13 3 % of them, below 2^-24 all.)
+// The decay 2^x of a state that many steps multiply, with all of fp32's relative precision: down to 1/2 (and for growth, which a
+// gate above 0 gives) 2^x - 1, below -2^-x. (Minus one, so that a slow decay is not rounded away step after step; not for a fast one,
+// whose difference from 1 has lost its last bits: at 2^-13 3 % of them, below 2^-24 all.)
 __device__ __forceinline__ float decay_factor(float x) {
-    const float less = expm1f(x * (1.f / LOG2E)), whole = ex2(x);
-    return less < -0.5f && whole > 0.f ? whole : less;
+    const float less = expm1f(x * (1.f / LOG2E));
+    return less < -0.5f ? -ex2(-x) : less;
+}
+__device__ __forceinline__ bool is_fast(float factor) { return factor < -0.5f; }
+__device__ __forceinline__ float fast_decay(float factor) {  // (one instruction, off by one unit in the last place)
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(-factor));
+    return r;
 }
 
 // Operand descriptors: a tile's own, and the step to k-block kk of 16 added to it (within the address field: no carry leaves it).
@@ -811,8 +817,9 @@ __device__ __forceinline__ uint32_t role_state(const ChunkParams &p, unsigned ch
             if (!wait_warp(m, &m->u, ph)) return it + 1;
             tc_fence_after();
             float less = m->factor[it & 3];
-            if (less > 0.f) {  // a fast decay, by itself
-                const f2 w2 = pair(less, less);
+            if (is_fast(less)) {  // by itself
+                const float whole = fast_decay(less);
+                const f2 w2 = pair(whole, whole);
 #pragma unroll
                 for (int j = 0; j < NK / 2; ++j) S[j] = mul2(S[j], w2);
                 less = 0.f;
@@ -898,8 +905,8 @@ __device__ __forceinline__ void join_states(const ChunkParams &p, int gtid) {
                 }
 #pragma unroll
                 for (int j = 0; j < BATCH; ++j) {
-                    const float keep = dd[j] > 0.f ? 0.f : 1.f;
-                    e = add2(fma2(e, pair(dd[j], dd[j]), mul2(e, pair(keep, keep))), x[j]);
+                    const float keep = is_fast(dd[j]) ? 0.f : 1.f, times = is_fast(dd[j]) ? fast_decay(dd[j]) : dd[j];
+                    e = add2(fma2(e, pair(times, times), mul2(e, pair(keep, keep))), x[j]);
                     if (j < left) s[(1 + j) * step] = e;
                 }
                 s += BATCH * step;
@@ -1429,16 +1436,16 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     if (sms < 1) return cudaErrorInvalidDevice;
     ChunkParams p{};
     p.a = a;
-    if (few) {
-        p.a.longest = FEW_LONGEST;
-        const cudaError_t e = launch_recurrent(p.a, stream);
-        if (e != cudaSuccess) return e;
-    }
     const int64_t N = few ? long_sequences(a.N, a.T) : a.N;
     const int hk = a.H / a.rep;
     if (!encode(&p.tq, a.q, a.T, hk, a.qs) || !encode(&p.tk, a.k, a.T, hk, a.ks) || !encode(&p.tv, a.v, a.T, a.H, a.vs) ||
         !encode(&p.to, a.o, a.T, a.H, static_cast<int64_t>(a.H) * DV))
         return cudaErrorInvalidValue;
+    if (few) {
+        p.a.longest = FEW_LONGEST;
+        const cudaError_t e = launch_recurrent(p.a, stream);
+        if (e != cudaSuccess) return e;
+    }
     p.seg_chunks = few ? segment_chunks_of_long(N, a.T, a.H, sms) : segment_chunks(N, a.T, a.H, sms);
     p.tasks = a.N * a.H;
     p.withhold = withhold;

@@ -378,6 +378,19 @@ def test_device_errors():
         assert e.value.code == kda.KDA_ERR_BAD_SEQLENS
 
 
+@pytest.mark.parametrize("lens,H", [([300, 128, 70], 2), ([5000], 1)])
+@pytest.mark.parametrize("g", [1e-9, 1e-6, 1e-3])
+def test_a_gate_a_little_above_zero_is_reported_and_no_more(lens, H, g):
+    """States grow by e^g then, as the formula has it: a rounding error in g does not lose them."""
+    x = make(lens, H, H, seed=45)
+    x["g"].fill_(g)
+    d = dev(x)
+    o, fs, status = torch.empty_like(d["v"]), torch.empty_like(d["s0"]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_linear_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["cu"], d["s0"], x["scale"], o, fs, status)
+    assert int(status) == kda.KDA_ERR_GATE_RANGE
+    check(x, o, fs)
+
+
 @pytest.mark.parametrize("lens,at", [([300, 70, 129], 45), ([300, 70, 129], 200), ([300, 70, 129], 359), ([40, 6000], 3000),
                                      ([3, 5, 9], 5)])
 def test_a_gate_that_is_no_number_shows(lens, at):
