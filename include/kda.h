@@ -598,6 +598,112 @@ kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *
                               float eps, int32_t residual_fp32, void *residual_out, void *y, float *y_scale,
                               kda_stream_t stream);
 
+/*
+ * kda_gated_delta_chunk_fwd — the delta rule with one decay for each token and
+ * head (KDA's recurrence where a head's channels share their gate) over
+ * varlen-packed prompts, for layers that share KDA's state [N,H,128,128],
+ * packing and serving path:
+ *       S <- e^{g_t} S;   S <- S + beta_t k_t (v_t - S^T k_t)^T;   o_t = scale * S^T q_t
+ * (Not part of the method's pages.)
+ *   q, k          bf16, num_qk_heads heads of 128 channels per token; value head
+ *                 h reads query/key head h / (num_heads / num_qk_heads), so
+ *                 num_qk_heads divides num_heads. As with KDA, normalising the
+ *                 keys is the caller's: beta |k|^2 above 2 makes the state grow.
+ *   v             bf16, num_heads heads of 128 channels per token.
+ *   *_token_stride  elements from one token to the next (>= heads x 128, a
+ *                 multiple of 8): q, k and v may be slices of one projection.
+ *   g, beta       fp32 [total_tokens, num_heads]: natural-log decay, g <= 0 (-inf
+ *                 forgets everything), and the strength of erasing and writing.
+ *   cu_seqlens    int32 [num_seqs + 1]: cu[0] = 0, nondecreasing, cu[num_seqs] <=
+ *                 total_tokens. Rows of o behind the last sequence are left as
+ *                 they were, and q, k, v, g, beta there are not used.
+ *   initial_state fp32 [num_seqs, num_heads, 128, 128] (key rows) or NULL for zeros.
+ * Outputs:
+ *   o             bf16 [total_tokens, num_heads, 128], contiguous.
+ *   final_state   fp32 [num_seqs, num_heads, 128, 128] or NULL; may be the same
+ *                 pointer as initial_state. An empty sequence's final state is
+ *                 its initial state.
+ *   status_dev    optional device int32, zeroed on the stream, then the first of
+ *                 KDA_ERR_GATE_RANGE (some g > 0 or NaN), KDA_ERR_BAD_SEQLENS (that
+ *                 sequence is skipped), KDA_ERR_TIMEOUT.
+ *   workspace     kda_gated_delta_chunk_fwd_workspace_size(...) bytes, 256-byte
+ *                 aligned (NULL when that is 0); not shared by calls that overlap.
+ * q, k, v, g, beta must be finite (g may be -inf): another value may reach every
+ * output of its sequence and head from the start of its chunk on. Alignment: q, k, v, o and the
+ * states 16 bytes, g, beta, cu_seqlens and status_dev 4.
+ */
+kda_status_t kda_gated_delta_chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                       const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                       int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
+                                       int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                       const float *initial_state, float scale, void *o, float *final_state,
+                                       int32_t *status_dev, void *workspace, size_t workspace_bytes,
+                                       kda_stream_t stream);
+
+/* Workspace bytes of kda_gated_delta_chunk_fwd for these sizes on the current
+ * device (0: none needed, or invalid arguments). */
+size_t kda_gated_delta_chunk_fwd_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t num_heads);
+
+/*
+ * kda_gated_delta_decode_fwd — the recurrence of kda_gated_delta_chunk_fwd for
+ * tokens_per_seq (0 .. KDA_DECODE_MAX_TOKENS) tokens of each sequence, state in
+ * and out: token t of sequence n is row n * tokens_per_seq + t of q, k, v, g,
+ * beta, o. Arguments, layouts, aliasing and errors as there; fp32 throughout, o
+ * rounded once to bf16. One launch; the state is read and written once.
+ */
+kda_status_t kda_gated_delta_decode_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                        int32_t num_seqs, int32_t tokens_per_seq, int32_t num_heads,
+                                        int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
+                                        int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                        const float *initial_state, float scale, void *o, float *final_state,
+                                        int32_t *status_dev, kda_stream_t stream);
+
+/*
+ * kda_gated_rms_norm — a layer's output: the RMS norm of each head's row, its
+ * gate, and the rounding to 8 bits for the output projection, in one pass:
+ *     n = x / sqrt(mean(x^2) + eps) * weight * act(gate)     over the 128 channels of a head
+ *     y_scale = max|n| / 448;   y = e4m3(n / y_scale), round to nearest even
+ * per token and head. (kda_chunk_fwd_gated_norm fuses the norm into KDA's prefill
+ * and leaves it in fp32; this call takes the output of any of the attention
+ * calls here.)
+ *   x             bf16, or fp32 with x_fp32 = 1: [tokens, num_heads, 128]
+ *   gate          bf16, num_heads heads of 128 channels per token, gate_token_stride
+ *                 elements from one token to the next (>= heads x 128, a multiple of 8)
+ *   weight        fp32 [128]
+ *   silu          act(gate): 0 sigmoid(gate), 1 gate * sigmoid(gate)
+ *   y             e4m3 [tokens, num_heads, 128];  y_scale  fp32 [tokens, num_heads]
+ * y and y_scale are the activations of kda_scaled_matmul with one scale per 128
+ * channels. Sums and norms are fp32. A row whose max|n| is below 2^-100 gets scale
+ * 0 and codes 0; a row with a NaN or an infinite n, or whose sum of squares
+ * overflows fp32, gets scale NaN and codes NaN. Alignment: x, gate, weight, y 16 bytes,
+ * y_scale 4. One launch, asynchronous on `stream`.
+ */
+kda_status_t kda_gated_rms_norm(const void *x, const void *gate, int64_t gate_token_stride, const float *weight,
+                                int64_t tokens, int32_t num_heads, int32_t head_dim_v, float eps, int32_t x_fp32,
+                                int32_t silu, void *y, float *y_scale, kda_stream_t stream);
+
+/*
+ * kda_scaled_matmul — a layer's projections on 8-bit operands with fp32 scales:
+ *     y[t, n] = sum_b x_scale[t, b] * weight_scale[n / 128, b] * sum_{k in block b} x[t, k] * weight[n, k]
+ * with block b the channels 128 b .. 128 b + 127 (the last may be shorter). It
+ * takes kda_add_rms_norm's rows (one scale a row) and kda_gated_rms_norm's (one
+ * a head). (Not part of the method's pages.)
+ *   x             e4m3 [rows, width], width a multiple of 16, at most KDA_MATMUL_MAX
+ *   x_scale       fp32 [rows], or [rows, ceil(width / 128)] with x_scale_per_block = 1
+ *   weight        e4m3 [outs, width], outs at most KDA_MATMUL_MAX
+ *   weight_scale  fp32 [ceil(outs / 128), ceil(width / 128)]
+ *   y             bf16 [rows, outs]
+ *   status_dev    optional device int32, zeroed on the stream; KDA_ERR_TIMEOUT
+ * Products and sums of a block on the tensor cores in fp32, over the blocks in
+ * fp32 registers; y is rounded once. A NaN code or scale makes NaN what it
+ * enters. All tensors contiguous. Alignment: x, weight, y 16 bytes, the others 4.
+ * One launch, asynchronous on `stream`, no workspace; the same inputs give the same bits.
+ */
+#define KDA_MATMUL_MAX 16777216
+kda_status_t kda_scaled_matmul(const void *x, const float *x_scale, int32_t x_scale_per_block, const void *weight,
+                               const float *weight_scale, int64_t rows, int32_t width, int32_t outs, void *y,
+                               int32_t *status_dev, kda_stream_t stream);
+
 /* Number of kernel launches one kda_chunk_fwd call makes for these sizes
  * (0 when num_seqs == 0). Host-only, no CUDA call. */
 int32_t kda_chunk_fwd_launches(int32_t num_seqs, int64_t total_tokens, int32_t num_heads);

@@ -13,6 +13,8 @@ from ._lib import (KDA_DEBUG_SPLIT_COLUMNS, KDA_DEBUG_WHOLE_COLUMNS, KDA_DEBUG_W
                    kda_chunk_fwd_split, add_rms_norm, kda_add_rms_norm, kda_linear_chunk_fwd, kda_linear_decode_fwd,
                    kda_state_load, kda_state_store, library_path, linear_chunk_fwd, linear_decode_fwd,
                    linear_workspace_size, state_load, state_store,
+                   gated_delta_chunk_fwd, gated_delta_decode_fwd, gated_delta_workspace_size, gated_rms_norm, scaled_matmul,
+                   kda_gated_delta_chunk_fwd, kda_gated_delta_decode_fwd, kda_gated_rms_norm, kda_scaled_matmul,
                    load_library, split_plan, split_workspace_size, status_string, version, workspace_for,
                    workspace_size)
 
@@ -26,4 +28,7 @@ __all__ = [
     "kda_chunk_fwd_host", "host_buffer_size", "KDA_ERR_BAD_SLOT", "linear_chunk_fwd", "kda_linear_chunk_fwd",
     "linear_workspace_size", "linear_decode_fwd", "kda_linear_decode_fwd", "state_store", "kda_state_store",
     "state_load", "kda_state_load", "add_rms_norm", "kda_add_rms_norm",
+    "gated_delta_chunk_fwd", "kda_gated_delta_chunk_fwd", "gated_delta_workspace_size", "gated_delta_decode_fwd",
+    "kda_gated_delta_decode_fwd", "gated_rms_norm", "kda_gated_rms_norm", "scaled_matmul",
+    "kda_scaled_matmul",
 ]

@@ -1,0 +1,526 @@
+// kda_scaled_matmul on tcgen05: e4m3 activations times an e4m3 weight, with fp32 scales.
+//
+//     y[t, n] = sum over blocks b of 128 channels:  xs[t, b] ws[n / 128, b] sum_{k in b} x[t, k] w[n, k]      bf16, rounded once
+//
+// The scales are any fp32 numbers, so the tensor core cannot apply them. It forms each block's inner sum (four MMAs of 32 channels)
+// in one of two accumulators in tensor memory; eight warps read it while it forms the next block's in the other, and add it,
+// times its scale, to their fp32 registers: acc += (xs ws) D.
+//
+// A CTA makes tiles of 128 lanes x BN columns of the accumulator. Roles:
+//   load    one thread: 128-byte wide tiles of both operands by TMA into a ring of stages
+//   MMAs    one thread
+//   scales  one warp: xs ws of each block, to shared memory, a few blocks ahead
+//   sums    eight warps: a lane and half of the columns each; then y
+//
+// Which operand takes the lanes. For more than 64 rows the rows of x do, columns are outputs: a thread needs one scale a block
+// (its 128 columns share the weight's), and y leaves by tiled stores. For up to 64 rows (decode) the weight's rows do and x's are
+// the columns, as few as 16: no lane of the tensor core idles, and the weight, which is what bounds these calls, is read by
+// as many CTAs as there are. Where tiles are fewer than the SMs, the CTAs of a cluster share a tile: each takes a part of the
+// channels, and they add up their sums through distributed shared memory, in the order of their ranks.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kda.h"
+#include "kda_checks.h"
+#include "kda_linear.cuh"
+#include "kda_tensor_map.h"
+
+namespace kda {
+namespace mm {
+
+using lin::f2;
+using lin::fma2;
+using lin::mbar_arrive;
+using lin::mbar_wait_some;
+using lin::pair;
+using lin::split;
+
+constexpr int LANES = 128;  // of an accumulator
+constexpr int KB = 128;     // channels of a block: a row of a stage's tile is 128 bytes
+constexpr int THREADS = 384;
+constexpr int SUM_WARPS = 8, FIRST_SUM_WARP = 4;
+constexpr int SCALES = 8;   // blocks' scales in shared memory
+constexpr int AHEAD = 4;    // of them loaded at a time
+constexpr int MAX_SPLITS = 8;
+constexpr int SWAP_ROWS = 64;
+// waits of up to 0.1 ms each before a role gives up; and before one that has given up takes its own copies for complete
+constexpr int WAITS = 20000, WAITS_DRAIN = 100;
+
+template <int BN, bool SWAP>
+struct Cfg {
+    static constexpr int A_BYTES = LANES * KB, B_BYTES = BN * KB, STAGE = A_BYTES + B_BYTES;
+    static constexpr int CTAS = BN <= 64 ? 2 : 1;  // per SM
+    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : SWAP ? (BN == 64 ? 4 : 5) : 3;
+    static constexpr int GROUPS = BN == 256 ? 2 : 1;  // column groups with a weight scale of their own
+    static constexpr int SCALE_FLOATS = SWAP ? BN : GROUPS * LANES;
+    static constexpr int STAGING = SWAP ? 0 : LANES * BN * 2;  // y's tile
+    static constexpr int COLS = BN / 2;                        // of a thread
+    static constexpr int RED_LD = LANES + 1;                   // a column of the sums that a cluster adds up
+    static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int OFF_STAGING = STAGES * STAGE, OFF_SCALES = OFF_STAGING + STAGING;
+    static constexpr int OFF_MISC = OFF_SCALES + SCALES * SCALE_FLOATS * 4;
+    // registers of the sums' warps and the others, where an even share is too few
+    static constexpr bool UNEVEN = BN == 256;
+    static constexpr int REGS_SUM = 208, REGS_AUX = 80, REGS = 168;
+    static_assert(!UNEVEN || 8 * REGS_SUM + 4 * REGS_AUX <= 12 * REGS, "the launch's registers");
+};
+
+struct Misc {
+    uint64_t full[5], empty[5];              // a stage
+    uint64_t tfull[2], tempty[2];            // an accumulator
+    uint64_t sfull[SCALES], sempty[SCALES];  // a block's scales
+    uint64_t drained;
+    uint32_t tmem;
+    int32_t abort;
+};
+
+struct Params {
+    CUtensorMap a, b, y;  // the lanes' operand, the columns', and (rows in the lanes) the output
+    const float *xs, *ws;
+    int64_t xs_row;   // floats from one row's scales to the next
+    int32_t xs_block; // and from one block's to the next (0: one scale a row)
+    int32_t blocks;   // of channels
+    int32_t rows, outs;
+    int32_t lane_tiles;
+    int64_t tiles;
+    int32_t splits;   // CTAs of a cluster that share a tile
+    int32_t tiled_y;  // y leaves by tiled stores
+    __nv_bfloat16 *out;
+    int32_t *status;
+};
+
+__device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
+    int i = 0;
+#pragma unroll 1
+    while (!mbar_wait_some(bar, parity)) {
+        if (++i == WAITS) *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
+        if (*reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
+    }
+    return true;
+}
+__device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < WAITS_DRAIN && !mbar_wait_some(bar, parity); ++i) {
+    }
+}
+__device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(m, bar, parity));
+}
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(smem_u32(src))
+                 : "memory");
+}
+// kind::f8f6f4 with e4m3 A and B (K-major) and fp32 D: 32 channels
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[8]) { tmem_ld8(t, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) { lin::tmem_ld32(t, r); }
+__device__ __forceinline__ void cluster_sync() {  // all threads of the cluster's CTAs
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
+// Tiles in the order they are made: bands of 16 lane tiles, in a band column after column, so that what runs at one time shares
+// few rows of both operands.
+__device__ __forceinline__ void tile_at(const Params &p, int64_t i, int &lane_tile, int &col_tile) {
+    constexpr int BAND = 16;
+    const int64_t col_tiles = p.tiles / p.lane_tiles;
+    const int64_t band = i / (BAND * col_tiles), in = i - band * BAND * col_tiles;
+    const int first = static_cast<int>(band) * BAND;
+    const int height = p.lane_tiles - first < BAND ? p.lane_tiles - first : BAND;
+    lane_tile = first + static_cast<int>(in % height);
+    col_tile = static_cast<int>(in / height);
+}
+
+template <int BN, bool SWAP>
+__global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmul_kernel(const __grid_constant__ Params p) {
+    using C = Cfg<BN, SWAP>;
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    float *scales = reinterpret_cast<float *>(smem + C::OFF_SCALES);
+    Misc *m = reinterpret_cast<Misc *>(smem + C::OFF_MISC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&m->tfull[i], 1), mbar_init(&m->tempty[i], SUM_WARPS);
+        for (int i = 0; i < SCALES; ++i) mbar_init(&m->sfull[i], 1), mbar_init(&m->sempty[i], SUM_WARPS);
+        mbar_init(&m->drained, 1);
+        m->abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 3) tmem_alloc(&m->tmem, C::TMEM);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+
+    // this CTA's tiles, and its part of their blocks
+    const int splits = p.splits, rank = splits > 1 ? static_cast<int>(blockIdx.x) % splits : 0;
+    const int64_t tile0 = blockIdx.x / splits, tile_step = gridDim.x / splits;
+    const int b0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / splits);
+    const int b1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / splits);
+
+    if (warp < FIRST_SUM_WARP) {
+    if (C::UNEVEN) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
+    if (warp == 0 && lane == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            int lt, ct;
+            tile_at(p, tile, lt, ct);
+            for (int b = b0; b < b1; ++b, ++it) {
+                const uint32_t st = it % C::STAGES, use = it / C::STAGES;
+                if (!(ok = wait(m, &m->empty[st], (use & 1) ^ 1))) break;
+                unsigned char *s = smem + st * C::STAGE;
+                mbar_arrive_expect_tx(&m->full[st], C::STAGE);
+                tma_load_2d(s, &p.a, b * KB, lt * LANES, &m->full[st]);
+                tma_load_2d(s + C::A_BYTES, &p.b, b * KB, ct * BN, &m->full[st]);
+            }
+        }
+        if (!ok)  // what is in flight lands before the CTA ends
+            for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
+                wait_drain(&m->full[i % C::STAGES], (i / C::STAGES) & 1);
+    } else if (warp == 1 && lane == 0) {
+        constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(LANES >> 4) << 24);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            for (int b = b0; b < b1; ++b, ++it) {
+                const uint32_t st = it % C::STAGES, buf = it & 1;
+                if (!(ok = wait(m, &m->full[st], (it / C::STAGES) & 1) && wait(m, &m->tempty[buf], ((it >> 1) & 1) ^ 1))) break;
+                tc_fence_after();
+                const uint32_t s = smem_u32(smem + st * C::STAGE);
+                const uint64_t da = umma_desc_sw128(s, 16, 1024), db = umma_desc_sw128(s + C::A_BYTES, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_e4m3(tmem + buf * BN, da + 2 * k, db + 2 * k, ID, k > 0);
+                umma_commit(&m->empty[st]);
+                umma_commit(&m->tfull[buf]);
+            }
+        }
+        if (!ok) {
+            umma_commit(&m->drained);
+            wait_drain(&m->drained, 0);
+        }
+    } else if (warp == 2) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            int lt, ct;
+            tile_at(p, tile, lt, ct);
+            const int row0 = SWAP ? ct * BN : lt * LANES;
+            const int out_block = SWAP ? lt : ct * BN / KB;
+            const int out_blocks = (p.outs + KB - 1) / KB;
+            constexpr int PER = SWAP ? (BN + 31) / 32 : LANES / 32;  // rows of a lane
+            for (int b = b0; ok && b < b1; b += AHEAD) {
+                float xs[AHEAD][PER], ws[AHEAD][C::GROUPS];
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    const int bb = b + a < b1 ? b + a : b1 - 1;
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int64_t row = row0 + 32 * i + lane;
+                        xs[a][i] = row < p.rows ? __ldg(p.xs + row * p.xs_row + static_cast<int64_t>(bb) * p.xs_block) : 0.f;
+                    }
+#pragma unroll
+                    for (int g = 0; g < C::GROUPS; ++g)
+                        ws[a][g] = out_block + g < out_blocks
+                                       ? __ldg(p.ws + static_cast<int64_t>(out_block + g) * p.blocks + bb) : 0.f;
+                }
+#pragma unroll
+                for (int a = 0; a < AHEAD; ++a) {
+                    if (!ok || b + a >= b1) continue;
+                    const uint32_t slot = it % SCALES;
+                    if (!(ok = wait_warp(m, &m->sempty[slot], ((it / SCALES) & 1) ^ 1))) continue;
+                    float *s = scales + slot * C::SCALE_FLOATS;
+#pragma unroll
+                    for (int g = 0; g < C::GROUPS; ++g)
+#pragma unroll
+                        for (int i = 0; i < PER; ++i)
+                            if (!SWAP || BN >= 32 || lane < BN) s[g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
+                    arrive_warp(&m->sfull[slot]);
+                    ++it;
+                }
+            }
+        }
+    }
+    } else {
+        if (C::UNEVEN) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SUM));
+        const int e = warp - FIRST_SUM_WARP, quad = warp & 3, half = e >> 2;
+        const int my_lane = 32 * quad + lane, col0 = half * C::COLS;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + col0;
+        constexpr int LD = C::COLS < 16 ? C::COLS : C::CTAS == 2 ? 16 : 32;  // columns read at a time
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            int lt, ct;
+            tile_at(p, tile, lt, ct);
+            f2 acc[C::COLS / 2];
+#pragma unroll
+            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
+            for (int b = b0; b < b1; ++b, ++it) {
+                const uint32_t buf = it & 1, slot = it % SCALES;
+                if (!(ok = wait_warp(m, &m->sfull[slot], (it / SCALES) & 1) && wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
+                tc_fence_after();
+                const float *s = scales + slot * C::SCALE_FLOATS;
+                float mine = 0.f;
+                if (!SWAP) mine = s[(col0 / KB) * LANES + my_lane];
+                const f2 mine2 = pair(mine, mine);
+#pragma unroll
+                for (int c = 0; c < C::COLS; c += LD) {
+                    uint32_t d[LD];
+                    tmem_ld(taddr + buf * BN + c, d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < LD; i += 4) {
+                        f2 s0 = mine2, s1 = mine2;
+                        if (SWAP) {
+                            const float4 x = *reinterpret_cast<const float4 *>(s + col0 + c + i);
+                            s0 = pair(x.x, x.y);
+                            s1 = pair(x.z, x.w);
+                        }
+                        acc[(c + i) / 2] = fma2(pair(d[i], d[i + 1]), s0, acc[(c + i) / 2]);
+                        acc[(c + i) / 2 + 1] = fma2(pair(d[i + 2], d[i + 3]), s1, acc[(c + i) / 2 + 1]);
+                    }
+                }
+                tc_fence_before();
+                arrive_warp(&m->tempty[buf]);
+                if (lane == 0) mbar_arrive(&m->sempty[slot]);
+            }
+            if (!ok) break;
+            if (splits > 1) {  // (one tile a CTA; the stages are done with)
+                float *red = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int i = 0; i < C::COLS / 2; ++i) {
+                    float x, y;
+                    split(acc[i], x, y);
+                    red[(col0 + 2 * i) * C::RED_LD + my_lane] = x;
+                    red[(col0 + 2 * i + 1) * C::RED_LD + my_lane] = y;
+                }
+            } else if (SWAP) {
+                const int64_t n = static_cast<int64_t>(lt) * LANES + my_lane;
+#pragma unroll
+                for (int i = 0; i < C::COLS / 2; ++i) {
+                    float v[2];
+                    split(acc[i], v[0], v[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int64_t t = static_cast<int64_t>(ct) * BN + col0 + 2 * i + j;
+                        if (n < p.outs && t < p.rows) p.out[t * p.outs + n] = __float2bfloat16_rn(v[j]);
+                    }
+                }
+            } else {
+                unsigned char *staging = smem + C::OFF_STAGING;  // panels of 64 columns, 128-byte swizzled rows
+                if (e == 0 && lane == 0) bulk_wait_read();       // (the tile before has left)
+                named_bar_sync(1, 32 * SUM_WARPS);
+#pragma unroll
+                for (int c = 0; c < C::COLS; c += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = lin::bf16_of(acc[c / 2 + j]);
+                    const int col = col0 + c;
+                    unsigned char *at = staging + (col / 64) * (LANES * 128) + my_lane * 128 + ((((col % 64) / 8) ^ (my_lane & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_shared();
+                named_bar_sync(1, 32 * SUM_WARPS);
+                if (p.tiled_y) {
+                    if (e == 0 && lane == 0) {
+#pragma unroll
+                        for (int c = 0; c < BN; c += 64)
+                            if (ct * BN + c < p.outs) tma_store_2d(&p.y, staging + (c / 64) * (LANES * 128), ct * BN + c, lt * LANES);
+                        bulk_commit();
+                    }
+                } else {
+#pragma unroll 1
+                    for (int r = e; r < LANES; r += SUM_WARPS) {
+                        const int64_t t = static_cast<int64_t>(lt) * LANES + r;
+                        if (t >= p.rows) break;
+                        for (int c = lane; c < BN && ct * BN + c < p.outs; c += 32)
+                            p.out[t * p.outs + ct * BN + c] = *reinterpret_cast<const __nv_bfloat16 *>(
+                                staging + (c / 64) * (LANES * 128) + r * 128 + ((((c % 64) / 8) ^ (r & 7)) << 4) + (c % 8) * 2);
+                    }
+                    named_bar_sync(1, 32 * SUM_WARPS);
+                }
+            }
+        }
+        if (!SWAP && e == 0 && lane == 0) bulk_wait_read();
+    }
+
+    // (every thread comes here, one that has given up as well)
+    __syncwarp();
+    if (splits > 1) {
+        cluster_sync();
+        if (warp >= FIRST_SUM_WARP) {
+            int lt, ct;
+            tile_at(p, tile0, lt, ct);
+            const int c0 = BN * rank / splits, n = BN * (rank + 1) / splits - c0;
+            const uint32_t red = smem_u32(smem);
+            for (int i = threadIdx.x - 32 * FIRST_SUM_WARP; i < n * LANES; i += 32 * SUM_WARPS) {
+                const int c = c0 + (SWAP ? i / LANES : i % n), l = SWAP ? i % LANES : i / n;
+                const int64_t t = SWAP ? static_cast<int64_t>(ct) * BN + c : static_cast<int64_t>(lt) * LANES + l;
+                const int64_t o = SWAP ? static_cast<int64_t>(lt) * LANES + l : static_cast<int64_t>(ct) * BN + c;
+                if (t >= p.rows || o >= p.outs) continue;
+                float s = 0.f;
+                for (int r = 0; r < splits; ++r) s += ld_cluster(red + 4 * (c * C::RED_LD + l), r);
+                p.out[t * p.outs + o] = __float2bfloat16_rn(s);
+            }
+        }
+        cluster_sync();  // (the others have read this CTA's sums)
+    }
+    if (threadIdx.x == 0 && m->abort) set_status(p.status, KDA_ERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 3) tmem_dealloc(tmem, C::TMEM);
+}
+
+template <int BN, bool SWAP>
+cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int splits, int sms, cudaStream_t stream) {
+    using C = Cfg<BN, SWAP>;
+    constexpr int SMEM = C::OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
+    static_assert(SMEM * C::CTAS <= 227 * 1024, "shared memory");
+    static_assert(SWAP || BN <= 128 ? BN * C::RED_LD * 4 <= C::STAGES * C::STAGE : true, "a cluster's sums lie over the stages");
+    const auto kernel = kda_scaled_matmul_kernel<BN, SWAP>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    const int lanes = SWAP ? p.outs : p.rows, cols = SWAP ? p.rows : p.outs;
+    auto operand = [&](CUtensorMap *m, const void *at, int64_t n, int box_rows) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(n)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width)};
+        const cuuint32_t box[2] = {KB, static_cast<cuuint32_t>(box_rows)};
+        return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, at, 2, dims, strides, box);
+    };
+    if (!operand(&p.a, SWAP ? w : x, lanes, LANES) || !operand(&p.b, SWAP ? x : w, cols, BN)) return cudaErrorInvalidValue;
+    p.tiled_y = 0;
+    if (!SWAP && splits == 1 && p.outs % 8 == 0) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.outs), static_cast<cuuint64_t>(p.rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.outs) * 2};
+        const cuuint32_t box[2] = {64, LANES};
+        if (!encode_map(&p.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 2, dims, strides, box)) return cudaErrorInvalidValue;
+        p.tiled_y = 1;
+    }
+    p.lane_tiles = (lanes - 1) / LANES + 1;
+    p.tiles = static_cast<int64_t>(p.lane_tiles) * ((cols - 1) / BN + 1);
+    p.splits = splits;
+    if (splits == 1) {
+        const int64_t most = static_cast<int64_t>(sms) * C::CTAS;
+        kernel<<<static_cast<int>(p.tiles < most ? p.tiles : most), THREADS, SMEM, stream>>>(p);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * splits));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(splits);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<const Params &>(p));
+}
+
+struct Choice {
+    int bn, splits;
+};
+// The least estimated time over tile widths and splits: waves of CTAs x (a start and an end + blocks x the time of one), in
+// cycles. A block of 256 columns takes the tensor core 512, of 128 its operands' way from shared memory 270, of 64 the same for
+// A alone.
+Choice choose(int64_t rows, int64_t outs, int blocks, int sms) {
+    Choice best{0, 1};
+    double least = 0;
+    auto consider = [&](int bn, int per_sm, int64_t tiles, double block) {
+        for (int s = 1; s <= MAX_SPLITS && s <= blocks; ++s) {
+            if (s > 1 && (bn == 256 || tiles * s > 2 * static_cast<int64_t>(sms) * per_sm)) break;
+            const int64_t slots = static_cast<int64_t>(sms) * per_sm, waves = (tiles * s - 1) / slots + 1;
+            const double each = s == 1 ? 1500 : 4000, t = 3000 + waves * (each + ((blocks - 1) / s + 1) * block * per_sm);
+            if (!best.bn || t < least) best = {bn, s}, least = t;
+        }
+    };
+    auto over = [](int64_t a, int64_t b) { return (a - 1) / b + 1; };
+    if (rows <= SWAP_ROWS) {
+        const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+        consider(bn, 2, over(outs, LANES), 150);
+    } else {
+        consider(256, 1, over(rows, LANES) * over(outs, 256), 530);
+        consider(128, 1, over(rows, LANES) * over(outs, 128), 300);
+        consider(64, 2, over(rows, LANES) * over(outs, 64), 200);
+    }
+    return best;
+}
+
+}  // namespace mm
+}  // namespace kda
+
+extern "C" kda_status_t kda_scaled_matmul(const void *x, const float *x_scale, int32_t x_scale_per_block, const void *weight,
+                                          const float *weight_scale, int64_t rows, int32_t width, int32_t outs, void *y,
+                                          int32_t *status_dev, kda_stream_t stream) {
+    using kda::checks::aligned;
+    if (rows < 0 || width < 1 || outs < 1 || (x_scale_per_block != 0 && x_scale_per_block != 1)) return KDA_ERR_INVALID_ARG;
+    if (width % 16 != 0) return KDA_ERR_UNSUPPORTED;
+    if (rows > 0x7fffffffLL - 128 || width > KDA_MATMUL_MAX || outs > KDA_MATMUL_MAX) return KDA_ERR_UNSUPPORTED;
+    if (status_dev && !aligned(status_dev, 4)) return KDA_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (rows > 0) {
+        if (!x || !x_scale || !weight || !weight_scale || !y) return KDA_ERR_INVALID_ARG;
+        if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(y, 16) || !aligned(x_scale, 4) || !aligned(weight_scale, 4))
+            return KDA_ERR_INVALID_ARG;
+    }
+    if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
+    if (rows == 0) return KDA_OK;
+    const int sms = kda::sm_count();
+    if (sms < 1) return KDA_ERR_CUDA;
+    kda::mm::Params p{};
+    p.xs = x_scale;
+    p.ws = weight_scale;
+    p.blocks = (width - 1) / kda::mm::KB + 1;
+    p.xs_row = x_scale_per_block ? p.blocks : 1;
+    p.xs_block = x_scale_per_block;
+    p.rows = static_cast<int32_t>(rows);
+    p.outs = outs;
+    p.out = static_cast<__nv_bfloat16 *>(y);
+    p.status = status_dev;
+    const kda::mm::Choice c = kda::mm::choose(rows, outs, p.blocks, sms);
+    cudaError_t e;
+    if (rows <= kda::mm::SWAP_ROWS)
+        e = c.bn == 16   ? kda::mm::launch<16, true>(p, x, weight, width, c.splits, sms, s)
+            : c.bn == 32 ? kda::mm::launch<32, true>(p, x, weight, width, c.splits, sms, s)
+                         : kda::mm::launch<64, true>(p, x, weight, width, c.splits, sms, s);
+    else
+        e = c.bn == 64    ? kda::mm::launch<64, false>(p, x, weight, width, c.splits, sms, s)
+            : c.bn == 128 ? kda::mm::launch<128, false>(p, x, weight, width, c.splits, sms, s)
+                          : kda::mm::launch<256, false>(p, x, weight, width, c.splits, sms, s);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
