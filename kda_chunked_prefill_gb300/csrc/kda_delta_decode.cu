@@ -170,9 +170,5 @@ cudaError_t launch_recurrent(const Params &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// (chunks to come: until then the recurrence runs prompts as well)
-cudaError_t launch_chunked(const Params &p, void *, cudaStream_t stream) { return launch_recurrent(p, stream); }
-size_t chunked_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
-
 }  // namespace delta
 }  // namespace kda

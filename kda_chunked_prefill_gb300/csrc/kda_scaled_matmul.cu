@@ -53,8 +53,13 @@ struct Cfg {
     static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : SWAP ? (BN == 64 ? 4 : 5) : 3;
     static constexpr int GROUPS = BN == 256 ? 2 : 1;  // column groups with a weight scale of their own
     static constexpr int SCALE_FLOATS = SWAP ? BN : GROUPS * LANES;
-    static constexpr int STAGING = SWAP ? 0 : LANES * BN * 2;  // y's tile
+    static constexpr int STAGING = SWAP ? 0 : LANES * BN * 2;  // y's tile, a warp's part after another's
     static constexpr int COLS = BN / 2;                        // of a thread
+    static constexpr int PANEL = COLS < 64 ? COLS : 64;        // columns of y's tile that are stored at a time
+    // where columns c .. c + 7 of a warp's row r lie: rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one
+    static __device__ __forceinline__ int staged(int r, int c) {
+        return (c / PANEL) * (32 * PANEL * 2) + r * (PANEL * 2) + ((((c % PANEL) / 8) ^ (PANEL == 64 ? r & 7 : (r >> 1) & 3)) << 4);
+    }
     static constexpr int RED_LD = LANES + 1;                   // a column of the sums that a cluster adds up
     static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int OFF_STAGING = STAGES * STAGE, OFF_SCALES = OFF_STAGING + STAGING;
@@ -340,41 +345,40 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                     }
                 }
             } else {
-                unsigned char *staging = smem + C::OFF_STAGING;  // panels of 64 columns, 128-byte swizzled rows
-                if (e == 0 && lane == 0) bulk_wait_read();       // (the tile before has left)
-                named_bar_sync(1, 32 * SUM_WARPS);
+                // the warp's own 32 rows of y, as panels of PANEL columns, swizzled
+                unsigned char *staging = smem + C::OFF_STAGING + e * (32 * C::COLS * 2);
+                if (lane == 0) bulk_wait_read();  // (the tile before has left)
+                __syncwarp();
 #pragma unroll
                 for (int c = 0; c < C::COLS; c += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w[j] = lin::bf16_of(acc[c / 2 + j]);
-                    const int col = col0 + c;
-                    unsigned char *at = staging + (col / 64) * (LANES * 128) + my_lane * 128 + ((((col % 64) / 8) ^ (my_lane & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(staging + C::staged(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 fence_proxy_async_shared();
-                named_bar_sync(1, 32 * SUM_WARPS);
+                __syncwarp();
+                const int64_t t0 = static_cast<int64_t>(lt) * LANES + 32 * quad;
+                const int n0 = ct * BN + col0;
                 if (p.tiled_y) {
-                    if (e == 0 && lane == 0) {
+                    if (lane == 0) {
 #pragma unroll
-                        for (int c = 0; c < BN; c += 64)
-                            if (ct * BN + c < p.outs) tma_store_2d(&p.y, staging + (c / 64) * (LANES * 128), ct * BN + c, lt * LANES);
+                        for (int c = 0; c < C::COLS; c += C::PANEL)
+                            if (n0 + c < p.outs && t0 < p.rows)
+                                tma_store_2d(&p.y, staging + C::staged(0, c), n0 + c, static_cast<int>(t0));
                         bulk_commit();
                     }
                 } else {
 #pragma unroll 1
-                    for (int r = e; r < LANES; r += SUM_WARPS) {
-                        const int64_t t = static_cast<int64_t>(lt) * LANES + r;
-                        if (t >= p.rows) break;
-                        for (int c = lane; c < BN && ct * BN + c < p.outs; c += 32)
-                            p.out[t * p.outs + ct * BN + c] = *reinterpret_cast<const __nv_bfloat16 *>(
-                                staging + (c / 64) * (LANES * 128) + r * 128 + ((((c % 64) / 8) ^ (r & 7)) << 4) + (c % 8) * 2);
-                    }
-                    named_bar_sync(1, 32 * SUM_WARPS);
+                    for (int r = 0; r < 32 && t0 + r < p.rows; ++r)
+                        for (int c = lane; c < C::COLS && n0 + c < p.outs; c += 32)
+                            p.out[(t0 + r) * p.outs + n0 + c] =
+                                *reinterpret_cast<const __nv_bfloat16 *>(staging + C::staged(r, c & ~7) + (c & 7) * 2);
+                    __syncwarp();
                 }
             }
         }
-        if (!SWAP && e == 0 && lane == 0) bulk_wait_read();
+        if (!SWAP && lane == 0) bulk_wait_read();
     }
 
     // (every thread comes here, one that has given up as well)
@@ -398,10 +402,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         }
         cluster_sync();  // (the others have read this CTA's sums)
     }
-    if (threadIdx.x == 0 && m->abort) set_status(p.status, KDA_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0 && m->abort) set_status(p.status, KDA_ERR_TIMEOUT);
     if (warp == 3) tmem_dealloc(tmem, C::TMEM);
 }
 
@@ -426,8 +430,10 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
     if (!SWAP && splits == 1 && p.outs % 8 == 0) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.outs), static_cast<cuuint64_t>(p.rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.outs) * 2};
-        const cuuint32_t box[2] = {64, LANES};
-        if (!encode_map(&p.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 2, dims, strides, box)) return cudaErrorInvalidValue;
+        const cuuint32_t box[2] = {static_cast<cuuint32_t>(C::PANEL), 32};
+        if (!encode_map(&p.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 2, dims, strides, box,
+                        C::PANEL == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
         p.tiled_y = 1;
     }
     p.lane_tiles = (lanes - 1) / LANES + 1;

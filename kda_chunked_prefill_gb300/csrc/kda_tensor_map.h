@@ -22,15 +22,16 @@ inline EncodeTiledFn encode_tiled_fn() {
     return fn;
 }
 
-// A tensor of up to 3 dimensions (innermost first) with 128-byte swizzled boxes; strides in bytes, from the second dimension on.
+// A tensor of up to 3 dimensions (innermost first) with swizzled boxes; strides in bytes, from the second dimension on.
 // False: the encoder is not there, or refuses.
 inline bool encode_map(CUtensorMap *m, CUtensorMapDataType type, const void *base, int rank, const cuuint64_t *dims,
-                       const cuuint64_t *strides, const cuuint32_t *box) {
+                       const cuuint64_t *strides, const cuuint32_t *box,
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const EncodeTiledFn fn = encode_tiled_fn();
     if (!fn) return false;
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, type, rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 inline int sm_count() {
