@@ -38,7 +38,7 @@ struct Decays {
     float pad[30];
 };
 constexpr int TILE = C * 128;  // 64 x 64 bf16
-constexpr int OFF_T = 0, OFF_PT = TILE, OFF_TLO = 2 * TILE, OFF_DECAYS = 3 * TILE;
+constexpr int OFF_T = 0, OFF_PT = TILE, OFF_TLO = 2 * TILE, OFF_DECAYS = 3 * TILE;  // in this order in a stage, too
 constexpr int IMAGE = OFF_DECAYS + sizeof(Decays);
 static_assert(IMAGE % 128 == 0 && sizeof(Decays) % 16 == 0, "bulk copies");
 
@@ -53,7 +53,6 @@ struct ChunkParams {
     CUtensorMap tq, tk, tv;
     unsigned char *images;  // [slot][head]
     int64_t slots;
-    int32_t wide_o;         // o is aligned to 32 bytes
 };
 
 // ------------------------------------------------------------------ first launch: T, P T and the decays of each chunk
@@ -346,28 +345,28 @@ __global__ void __launch_bounds__(THREADS, 3) kda_gated_delta_prepare_kernel(con
 // ------------------------------------------------------------------ second launch: the state from chunk to chunk
 namespace walk {
 
-constexpr int NV = 64;             // value columns of a CTA
-constexpr int SLICES = DV / NV;
-constexpr int WARPS = 16;          // that hold the state: a key row (lane of the accumulators) x 16 columns a thread
-constexpr int COLS = 16;
+// Everything is transposed: lanes of the accumulators are the 128 value columns. What depends on the state (S, Z, X, each in two bf16
+// terms) is then the operand that tensor memory holds, and never passes through shared memory, whose bandwidth would bound this
+// kernel otherwise; K, Q, T and P T are read from the tiles as they arrive.
+constexpr int WARPS = 16;   // warp = lanes 32 (w % 4) .., part w / 4: 32 keys of the state, 16 tokens of a chunk
+constexpr int KEYS = 32, TOKS = 16;
 constexpr int WARP_LOAD = WARPS, WARP_MMA = WARPS + 1, THREADS = 32 * (WARPS + 2);
-constexpr int STAGES = 2;
-// a stage: [K ; Q] as two panels of 64 channels, 128 rows each; V's columns; [T ; P T]; [second term of T ; zeros]; decays
+constexpr int STAGES = 3;
+// a stage: [K ; Q] and V as panels of 64 channels; [T ; P T]; second term of T; decays
 constexpr int PANEL = 2 * TILE;
-constexpr int OFF_KQ = 0, OFF_V = 2 * PANEL, OFF_TT = OFF_V + TILE, OFF_TL = OFF_TT + 2 * TILE, OFF_D = OFF_TL + 2 * TILE;
+constexpr int OFF_KQ = 0, OFF_V = 2 * PANEL, OFF_TT = OFF_V + 2 * TILE, OFF_TL = OFF_TT + 2 * TILE, OFF_D = OFF_TL + TILE;
 constexpr int STAGE = OFF_D + 1024;
 static_assert(sizeof(Decays) <= 1024, "stage");
-constexpr int STAGE_BYTES = 2 * PANEL + TILE + IMAGE;  // that arrive
-constexpr int OFF_S = STAGES * STAGE;            // two terms of S: [key][value]
-constexpr int OFF_Z = OFF_S + 2 * 2 * TILE;      // of Z: [token][value]
-constexpr int OFF_X = OFF_Z + 2 * TILE;          // of diag(e^{G_end - G}) X
-constexpr int OFF_MISC = OFF_X + 2 * TILE;
-constexpr uint32_t COL_D1 = 0, COL_D2 = 128, COL_D3 = 256;
+constexpr int STAGE_BYTES = 2 * PANEL + 2 * TILE + IMAGE;  // that arrive
+constexpr int OFF_MISC = STAGES * STAGE;
+// Tensor memory columns: S (first terms of 128 keys, then second); (K S)^T, under it Z, and (Q S)^T; X^T, under it X in two terms, and
+// (P T Z)^T; the update (K^T X)^T. Of Z and X, 16 tokens take 8 columns of first terms and 8 of second, over their sums.
+constexpr uint32_t COL_S = 0, COL_KS = 128, COL_QS = 192, COL_X = 256, COL_O = 320, COL_U = 384;
 
 struct Misc {
     uint64_t full[STAGES], empty[STAGES];
-    uint64_t s, z, x;     // written
-    uint64_t d1, d2, d3;  // MMAs complete
+    uint64_t s[2], z, x;           // written; S by halves of the keys
+    uint64_t ks, xs, u;            // MMAs complete: K S and Q S; T Z and P T Z; the update
     uint64_t drained;
     uint32_t tmem;
     int32_t abort;
@@ -398,36 +397,26 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) lin::mbar_arrive(bar);
 }
-// 16 columns of a row in two bf16 terms, to columns c0 .. of tiles `hi` and `lo`
-__device__ __forceinline__ void store_split(unsigned char *hi, unsigned char *lo, int row, int c0, const float (&v)[COLS]) {
-#pragma unroll
-    for (int c = 0; c < COLS; c += 8) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = v[c + 2 * j], y = v[c + 2 * j + 1];
-            h[j] = pack_bf16(x, y);
-            const float2 f = unpack_bf16(h[j]);
-            l[j] = pack_bf16(x - f.x, y - f.y);
-        }
-        const int at = swz(row, (c0 + c) / 8);
-        *reinterpret_cast<uint4 *>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-}
-__device__ __forceinline__ void store_32(void *p, const uint32_t (&w)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-// the sum of 16 columns of an accumulator and 16 of its second half
-__device__ __forceinline__ void load_sum(uint32_t taddr, float (&v)[COLS]) {
-    uint32_t a[16], b[16];
-    tmem_ld16(taddr, a);
-    tmem_ld16(taddr + NV, b);
-    tmem_wait_ld();
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[8]) { tmem_st8(t, r); }
+__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
+// v in two bf16 terms: N columns of pairs at `hi` and at `lo`, and on to the MMAs
+template <int N>
+__device__ __forceinline__ void store_split(uint32_t hi, uint32_t lo, const f2 (&v)[N]) {
+    uint32_t h[N], l[N];
+    const f2 minus = pair(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < COLS; ++i) v[i] = __uint_as_float(a[i]) + __uint_as_float(b[i]);
+    for (int i = 0; i < N; ++i) h[i] = lin::bf16_of(v[i]);
+    tmem_st(hi, h);
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = lin::bf16_of(lin::fma2(lin::of_bf16(h[i]), minus, v[i]));
+    tmem_st(lo, l);
+    tmem_wait_st();
+    tc_fence_before();
 }
 
 __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const __grid_constant__ ChunkParams cp) {
@@ -436,8 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slice = blockIdx.x % SLICES;
-    const int64_t chain = blockIdx.x / SLICES;
+    const int64_t chain = blockIdx.x;
     const int n = static_cast<int>(chain / p.H), h = static_cast<int>(chain % p.H), hk = h / p.rep;
     const int64_t bos = p.cu[n], eos = p.cu[n + 1];
     if (bos < 0 || eos < bos || eos > p.T || p.cu[0] != 0) {
@@ -448,14 +436,12 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], WARPS + 1);
-        mbar_init(&m->s, WARPS), mbar_init(&m->z, WARPS / 2), mbar_init(&m->x, WARPS / 2);
-        mbar_init(&m->d1, 1), mbar_init(&m->d2, 1), mbar_init(&m->d3, 1), mbar_init(&m->drained, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&m->s[i], WARPS / 2);
+        mbar_init(&m->z, WARPS), mbar_init(&m->x, WARPS), mbar_init(&m->ks, 1), mbar_init(&m->xs, 1), mbar_init(&m->u, 1);
+        mbar_init(&m->drained, 1);
         m->abort = 0;
         mbar_fence_init();
     }
-    for (int i = tid; i < STAGES * TILE / 16; i += THREADS)
-        *reinterpret_cast<uint4 *>(smem + (i / (TILE / 16)) * STAGE + OFF_TL + TILE + (i % (TILE / 16)) * 16) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_shared();
     if (warp == WARP_MMA) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -474,30 +460,28 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 uint64_t *bar = &m->full[st];
                 const uint64_t first = lin::evict_first();
                 mbar_arrive_expect_tx(bar, STAGE_BYTES);
-                lin::tma_load_3d(s + OFF_KQ, &cp.tk, 0, hk, t, bar, first);
-                lin::tma_load_3d(s + OFF_KQ + PANEL, &cp.tk, 64, hk, t, bar, first);
-                lin::tma_load_3d(s + OFF_KQ + TILE, &cp.tq, 0, hk, t, bar, first);
-                lin::tma_load_3d(s + OFF_KQ + PANEL + TILE, &cp.tq, 64, hk, t, bar, first);
-                lin::tma_load_3d(s + OFF_V, &cp.tv, NV * slice, h, t, bar, first);
-                const unsigned char *img = images + static_cast<int64_t>(it) * p.H * IMAGE;
-                bulk_g2s(s + OFF_TT, img, 2 * TILE, bar);
-                bulk_g2s(s + OFF_TL, img + OFF_TLO, TILE, bar);
-                bulk_g2s(s + OFF_D, img + OFF_DECAYS, sizeof(Decays), bar);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    lin::tma_load_3d(s + OFF_KQ + c * PANEL, &cp.tk, 64 * c, hk, t, bar, first);
+                    lin::tma_load_3d(s + OFF_KQ + c * PANEL + TILE, &cp.tq, 64 * c, hk, t, bar, first);
+                    lin::tma_load_3d(s + OFF_V + c * TILE, &cp.tv, 64 * c, h, t, bar, first);
+                }
+                bulk_g2s(s + OFF_TT, images + static_cast<int64_t>(it) * p.H * IMAGE, IMAGE, bar);
             }
             if (!ok)  // what is in flight lands before the CTA ends
                 for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) wait_drain(&m->full[i % STAGES], (i / STAGES) & 1);
         }
     } else if (warp == WARP_MMA) {
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t ID1 = lin::idesc_bf16(false, true, 128, 2 * NV), ID2 = lin::idesc_bf16(false, true, 128, NV),
-                           ID3 = lin::idesc_bf16(true, true, 128, 2 * NV);
+        constexpr uint32_t ID = lin::idesc_bf16(false, false, 128, 128), ID_LO = lin::idesc_bf16(false, false, 128, 64),
+                           ID_U = lin::idesc_bf16(false, true, 128, 128);
         bool ok = true;
         for (int it = 0; it < chunks; ++it) {
             const int st = it % STAGES;
             const uint32_t ph = it & 1, s = base + st * STAGE;
             if (!(ok = wait_warp(m, &m->full[st], (it / STAGES) & 1))) break;
             const int64_t left = eos - bos - static_cast<int64_t>(it) * C;
-            if (left < C) {  // the rows behind are another sequence's, or anything: as zeros
+            if (left < C) {  // the rows of K behind are another sequence's, or anything: as zeros
                 unsigned char *kq = smem + st * STAGE + OFF_KQ;
                 for (int i = static_cast<int>(left) * 8 + lane; i < TILE / 16; i += 32) {
                     *reinterpret_cast<uint4 *>(kq + i * 16) = make_uint4(0, 0, 0, 0);
@@ -506,38 +490,48 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 fence_proxy_async_shared();
                 __syncwarp();
             }
-            if (!(ok = wait_warp(m, &m->s, ph))) break;
-            tc_fence_after();
-            if (lane == 0) {
+            auto kq_at = [&](int k) { return umma_desc_sw128(s + OFF_KQ + (k >> 2) * PANEL + (k & 3) * 32, 16, 1024); };
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    umma_f16(tmem + COL_D1, umma_desc_sw128(s + OFF_KQ + (k >> 2) * PANEL + (k & 3) * 32, 16, 1024),
-                             umma_desc_sw128(base + OFF_S + k * 2048, 2 * TILE, 1024), ID1, k > 0);
-                umma_commit(&m->d1);
+            for (int half = 0; half < 2; ++half) {
+                if (!(ok = wait_warp(m, &m->s[half], ph))) break;
+                tc_fence_after();
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 4 * half; k < 4 * half + 4; ++k) {
+                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 8 * k, kq_at(k), ID, k > 0);
+                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 8 * k, kq_at(k), ID, 1);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                umma_commit(&m->ks);
             }
             __syncwarp();
             if (!(ok = wait_warp(m, &m->z, ph))) break;
             tc_fence_after();
             if (lane == 0) {
+                auto t_at = [&](int off, int k) { return umma_desc_sw128(s + off + k * 32, 16, 1024); };
 #pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    umma_f16(tmem + COL_D2, umma_desc_sw128(s + OFF_TT + k * 32, 16, 1024),
-                             umma_desc_sw128(base + OFF_Z + k * 2048, TILE, 1024), ID1, k > 0);
-#pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    umma_f16(tmem + COL_D2, umma_desc_sw128(s + OFF_TL + k * 32, 16, 1024),
-                             umma_desc_sw128(base + OFF_Z + k * 2048, TILE, 1024), ID2, 1);
-                umma_commit(&m->d2);
+                for (int k = 0; k < 4; ++k) {
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, t_at(OFF_TT, k), ID, k > 0);
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k + 8, t_at(OFF_TT, k), ID, 1);
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, t_at(OFF_TL, k), ID_LO, 1);
+                }
+                umma_commit(&m->xs);
             }
             __syncwarp();
             if (!(ok = wait_warp(m, &m->x, ph))) break;
             tc_fence_after();
             if (lane == 0) {
 #pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    umma_f16(tmem + COL_D3, umma_desc_sw128(s + OFF_KQ + k * 2048, PANEL, 1024),
-                             umma_desc_sw128(base + OFF_X + k * 2048, TILE, 1024), ID3, k > 0);
-                umma_commit(&m->d3);
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t b = umma_desc_sw128(s + OFF_KQ + k * 2048, PANEL, 1024);
+                    lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k, b, ID_U, k > 0);
+                    lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k + 8, b, ID_U, 1);
+                }
+                umma_commit(&m->u);
                 umma_commit(&m->empty[st]);
             }
             __syncwarp();
@@ -548,106 +542,111 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
         }
         __syncwarp();
     } else {
-        const int quad = warp & 3, c0 = COLS * (warp >> 2);
-        const int row = 32 * quad + lane;               // key of the state; token of K (below 64) or of Q
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + c0;
-        const bool is_q = quad >= 2;
-        const int tok = row & (C - 1);
-        float S[COLS];
+        const int quad = warp & 3, part = warp >> 2, half = part >> 1;
+        const int val = 32 * quad + lane;  // the value column
+        const uint32_t t = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+        const int k0 = KEYS * part, t0 = TOKS * part;
+        f2 S[KEYS / 2];  // keys k0 + 2 i, k0 + 2 i + 1
         {
-            const float *s0 = p.s0 ? p.s0 + static_cast<size_t>(chain) * (DK * DV) + row * DV + NV * slice + c0 : nullptr;
+            const float *s0 = p.s0 ? p.s0 + static_cast<size_t>(chain) * (DK * DV) + k0 * DV + val : nullptr;
 #pragma unroll
-            for (int c = 0; c < COLS; c += 4) {
-                const float4 x = s0 ? *reinterpret_cast<const float4 *>(s0 + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-                S[c] = x.x, S[c + 1] = x.y, S[c + 2] = x.z, S[c + 3] = x.w;
-            }
+            for (int i = 0; i < KEYS / 2; ++i) S[i] = s0 ? pair(s0[2 * i * DV], s0[(2 * i + 1) * DV]) : 0;
         }
         bool ok = true;
         for (int it = 0; it < chunks; ++it) {
             const int st = it % STAGES;
             const uint32_t ph = it & 1;
-            const int64_t left = eos - bos - static_cast<int64_t>(it) * C;
+            const int64_t rest = eos - bos - static_cast<int64_t>(it) * C;
+            const int left = rest < C ? static_cast<int>(rest) : C;
             const unsigned char *stage = smem + st * STAGE;
             const Decays *d = reinterpret_cast<const Decays *>(stage + OFF_D);
-            store_split(smem + OFF_S, smem + OFF_S + 2 * TILE, row, c0, S);
-            fence_proxy_async_shared();
-            tc_fence_before();
-            arrive_warp(&m->s);
+            store_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
+            arrive_warp(&m->s[half]);
             if (!(ok = wait_warp(m, &m->full[st], (it / STAGES) & 1))) break;
-            const float upto = d->upto[tok], after = d->after[tok], whole = d->whole, less = d->less;
-            float v[COLS], z[COLS];
-            if (!is_q) {
+            f2 z[TOKS / 2], w[TOKS / 2];
+            {
+                const unsigned char *v = stage + OFF_V + (val >> 6) * TILE + t0 * 128 + (val & 7) * 2;
+                const int c = (val & 63) >> 3;
+                auto at = [&](int i) {
+                    return static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(v + i * 128 + ((c ^ (i & 7)) << 4))) << 16;
+                };
 #pragma unroll
-                for (int c = 0; c < COLS; c += 8) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(stage + OFF_V + swz(tok, (c0 + c) / 8));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                for (int i = 0; i < TOKS / 2; ++i) z[i] = pair(at(2 * i), at(2 * i + 1));
+            }
+            const float whole = d->whole, less = d->less;
+            uint32_t r[16];
+            if (!(ok = wait_warp(m, &m->ks, ph))) break;
+            tc_fence_after();
+            tmem_ld16(t + COL_KS + t0, r);
+            tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = unpack_bf16(w[j]);
-                        v[c + 2 * j] = f.x, v[c + 2 * j + 1] = f.y;
-                    }
+            for (int i = 0; i < TOKS / 2; ++i) {
+                const float2 e = *reinterpret_cast<const float2 *>(&d->upto[t0 + 2 * i]);
+                z[i] = lin::fma2(pair(-e.x, -e.y), pair(r[2 * i], r[2 * i + 1]), z[i]);
+            }
+            auto mask = [&](f2(&v)[TOKS / 2]) {  // tokens behind the sequence: zeros, whatever they are
+                if (left == C) return;
+#pragma unroll
+                for (int i = 0; i < TOKS / 2; ++i) {
+                    float x, y;
+                    split(v[i], x, y);
+                    v[i] = pair(t0 + 2 * i < left ? x : 0.f, t0 + 2 * i + 1 < left ? y : 0.f);
+                }
+            };
+            mask(z);
+            store_split(t + COL_KS + t0, t + COL_KS + t0 + 8, z);
+            arrive_warp(&m->z);
+            if (!(ok = wait_warp(m, &m->xs, ph))) break;
+            tc_fence_after();
+            tmem_ld16(t + COL_X + t0, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < TOKS / 2; ++i) {
+                const float2 e = *reinterpret_cast<const float2 *>(&d->after[t0 + 2 * i]);
+                w[i] = lin::mul2(pair(e.x, e.y), pair(r[2 * i], r[2 * i + 1]));
+            }
+            mask(w);
+            store_split(t + COL_X + t0, t + COL_X + t0 + 8, w);
+            arrive_warp(&m->x);
+            {
+                uint32_t q[16];
+                tmem_ld16(t + COL_QS + t0, q);
+                tmem_ld16(t + COL_O + t0, r);
+                tmem_wait_ld();
+                tc_fence_before();
+                __nv_bfloat16 *o = p.o + ((bos + static_cast<int64_t>(it) * C + t0) * p.H + h) * DV + val;
+#pragma unroll
+                for (int i = 0; i < TOKS; ++i) {
+                    const float x = fmaf(p.scale * d->upto[t0 + i], __uint_as_float(q[i]), __uint_as_float(r[i]));
+                    if (t0 + i < left) o[static_cast<int64_t>(i) * p.H * DV] = __float2bfloat16_rn(x);
                 }
             }
             arrive_warp(&m->empty[st]);
-            if (!(ok = wait_warp(m, &m->d1, ph))) break;
+            if (!(ok = wait_warp(m, &m->u, ph))) break;
             tc_fence_after();
-            load_sum(taddr + COL_D1, z);
-            if (!is_q) {
-                const bool in = tok < left;
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) z[c] = in ? fmaf(-upto, z[c], v[c]) : 0.f;
-                store_split(smem + OFF_Z, smem + OFF_Z + TILE, tok, c0, z);
-                fence_proxy_async_shared();
-                tc_fence_before();
-                arrive_warp(&m->z);
-            } else {
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) z[c] *= p.scale * upto;
-                tc_fence_before();
-            }
-            if (!(ok = wait_warp(m, &m->d2, ph))) break;
-            tc_fence_after();
-            load_sum(taddr + COL_D2, v);
-            if (!is_q) {
-                const bool in = tok < left;
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) v[c] = in ? v[c] * after : 0.f;
-                store_split(smem + OFF_X, smem + OFF_X + TILE, tok, c0, v);
-                fence_proxy_async_shared();
-                tc_fence_before();
-                arrive_warp(&m->x);
-            } else {
-                tc_fence_before();
-                uint32_t w[COLS / 2];
-#pragma unroll
-                for (int c = 0; c < COLS; c += 2) w[c / 2] = pack_bf16(z[c] + v[c], z[c + 1] + v[c + 1]);
-                if (tok < left) {
-                    __nv_bfloat16 *o = p.o + ((bos + static_cast<int64_t>(it) * C + tok) * p.H + h) * DV + NV * slice + c0;
-                    if (cp.wide_o) {
-                        store_32(o, w);
-                    } else {
-                        reinterpret_cast<uint4 *>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        reinterpret_cast<uint4 *>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                }
-                __syncwarp();
-            }
-            if (!(ok = wait_warp(m, &m->d3, ph))) break;
-            tc_fence_after();
-            load_sum(taddr + COL_D3, v);
+            uint32_t u[32];
+            lin::tmem_ld32(t + COL_U + k0, u);
+            tmem_wait_ld();
             if (less < -0.5f) {
+                const f2 f = pair(whole, whole);
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) S[c] = fmaf(S[c], whole, v[c]);
+                for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::fma2(S[i], f, pair(u[2 * i], u[2 * i + 1]));
             } else {  // (a slow decay is not rounded away chunk after chunk)
+                const f2 f = pair(less, less);
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) S[c] += fmaf(S[c], less, v[c]);
+                for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::add2(S[i], lin::fma2(S[i], f, pair(u[2 * i], u[2 * i + 1])));
             }
         }
         if (p.sT && ok) {
-            float *sT = p.sT + static_cast<size_t>(chain) * (DK * DV) + row * DV + NV * slice + c0;
+            float *sT = p.sT + static_cast<size_t>(chain) * (DK * DV) + k0 * DV + val;
 #pragma unroll
-            for (int c = 0; c < COLS; c += 4) *reinterpret_cast<float4 *>(sT + c) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+            for (int i = 0; i < KEYS / 2; ++i) {
+                float x, y;
+                split(S[i], x, y);
+                sT[2 * i * DV] = x, sT[(2 * i + 1) * DV] = y;
+            }
         }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -680,14 +679,13 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     if (!encode_heads(&p.tq, a.q, a.T, hk, a.qs) || !encode_heads(&p.tk, a.k, a.T, hk, a.ks) ||
         !encode_heads(&p.tv, a.v, a.T, a.H, a.vs))
         return cudaErrorInvalidValue;
-    p.wide_o = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
     cudaError_t e = cudaFuncSetAttribute(prep::kda_gated_delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, prep::SMEM);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(walk::kda_gated_delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, walk::SMEM);
     if (e != cudaSuccess) return e;
     prep::kda_gated_delta_prepare_kernel<<<static_cast<unsigned>(p.slots * a.H), prep::THREADS, prep::SMEM, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    walk::kda_gated_delta_chunk_kernel<<<static_cast<unsigned>(a.N) * a.H * walk::SLICES, walk::THREADS, walk::SMEM, stream>>>(p);
+    walk::kda_gated_delta_chunk_kernel<<<static_cast<unsigned>(a.N) * a.H, walk::THREADS, walk::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 

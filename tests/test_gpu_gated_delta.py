@@ -2,7 +2,8 @@
 
 Bounds element by element: oracle/delta.py derives them; o adds its own rounding, 2^-8 of itself. Over all elements (2-norms):
 errors of many roundings add up like independent ones. o: bf16 of itself (half a step is 2^-8 at most, 2^-8 / sqrt(3) on average over
-a step and less over values) and of the chunk's responses: below 2^-8. Final state: five operands of two bf16 terms, each at most
+a step and less, 2^-8 / 2.3, over values), of the chunk's responses, of Z and of the state that q multiplies: sqrt(4) / 2.3 = 0.87 of 2^-8
+at most: below 2^-8. Final state: five operands of two bf16 terms, each at most
 2^-16 and on average a fifth of it off: below 2^-16; the recurrence is fp32: below 2^-20.
 """
 import numpy as np
