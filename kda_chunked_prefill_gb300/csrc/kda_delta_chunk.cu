@@ -48,6 +48,12 @@ __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7
 // Workspace slots of chunks: those of sequence n begin at cu[n] / 64 + n, which leaves each as many as it can need.
 __device__ __forceinline__ int64_t slot_base(int64_t bos, int64_t n) { return bos / C + n; }
 
+__device__ __forceinline__ uint64_t evict_normal() {  // (the second launch reads them again)
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 struct ChunkParams {
     Params a;
     CUtensorMap tq, tk, tv;
@@ -58,17 +64,27 @@ struct ChunkParams {
 // ------------------------------------------------------------------ first launch: T, P T and the decays of each chunk
 namespace prep {
 
-constexpr int THREADS = 256;
-constexpr int LD = 68;  // floats of a row of A and T in shared memory
-constexpr int OFF_K = 0, OFF_Q = C * 256;          // k and q, rows of 256 bytes; then, over them, A and T
-constexpr int OFF_A = 0, OFF_TF = C * LD * 4;
-constexpr int OFF_M = 2 * C * LD * 4;              // 32 x LD floats: A21 T11
-constexpr int OFF_IMG = OFF_M + 32 * LD * 4;
-constexpr int OFF_G = OFF_IMG + IMAGE;             // float2 [64]: log2 prefix in two terms; beta
-constexpr int SMEM = OFF_G + C * 8 + C * 4;
-static_assert(OFF_M >= 2 * C * 256 && OFF_IMG % 128 == 0, "layout");
+// Four warps to a chunk and head, each with 16 rows of A and P, in blocks of 16 x 16 that stay in registers as fragments. T's
+// diagonal blocks by substitution in fp32; below it, T_ij = -T_ii sum_{j <= k < i} A_ik T_kj, one block diagonal after another, on
+// operands of two bf16 terms (three products: 2^-16). Scaled by beta from the start: (T diag(beta))_kj does as well for T_kj.
+constexpr int THREADS = 128;
+constexpr int PER_SM = 5;
+constexpr int SB = 16, BLOCKS = C / SB;
+constexpr int LD = 20;                                   // floats of a row of a diagonal block
+constexpr int OFF_K = 0, OFF_Q = 2 * TILE, OFF_IMG = 0;  // k and q, two panels of 64 channels each; over them, what leaves
+constexpr int OFF_MISC = 4 * TILE;
+static_assert(IMAGE <= OFF_MISC, "layout");
 
-__device__ __forceinline__ int kq_at(int r, int c) { return r * 256 + ((c & 8) << 4) + (((c ^ r) & 7) << 4); }  // 16-byte group c
+struct Misc {
+    alignas(16) float diag[BLOCKS][SB * LD];
+    float2 G[C];                        // log2 prefix in two terms
+    float beta[C];
+    float row[C];                       // e^{G_i - (G before i's block)}
+    float col[BLOCKS - 1][C - SB];      // e^{(G before block b + 1) - G_j}
+    uint64_t full;
+};
+constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(SMEM * PER_SM <= 227 * 1024, "shared memory");
 
 // The sequence whose slots hold `slot`: the last n with slot_base(cu[n], n) <= slot (whole warp).
 __device__ __forceinline__ int find_sequence(const Params &p, int64_t slot, int lane) {
@@ -86,15 +102,47 @@ __device__ __forceinline__ int find_sequence(const Params &p, int64_t slot, int 
 
 // 2^(x + y), |y| far below 1
 __device__ __forceinline__ float ex2_2(float x, float y) { return ex2(x) * fmaf(y, 0.6931471805599453f, 1.f); }
+// 2^(a - b)
+__device__ __forceinline__ float ex2_diff(float2 a, float2 b) { return ex2((a.x - b.x) + (a.y - b.y)); }
 
-__global__ void __launch_bounds__(THREADS, 3) kda_gated_delta_prepare_kernel(const __grid_constant__ ChunkParams cp) {
+__device__ __forceinline__ uint32_t transpose(uint32_t a) {  // an 8 x 8 matrix of 16-bit elements
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// two values in two bf16 terms
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16(x, y);
+    const float2 f = unpack_bf16(hi);
+    lo = pack_bf16(x - f.x, y - f.y);
+}
+// A 16 x 16 block as the tensor core's left operand: first and second terms. c[0..1]: rows g and g + 8 of columns 2 q, 2 q + 1 in the
+// accumulators' order; c[2..3] of columns 8 further.
+struct Left {
+    uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ void to_left(Left &f, const float (&a)[4], const float (&b)[4]) {
+    split_pair(a[0], a[1], f.hi[0], f.lo[0]);
+    split_pair(a[2], a[3], f.hi[1], f.lo[1]);
+    split_pair(b[0], b[1], f.hi[2], f.lo[2]);
+    split_pair(b[2], b[3], f.hi[3], f.lo[3]);
+}
+// d += left x (hi + lo), without the product of the second terms; hi, lo: right operand's fragments of two tiles of 8 columns
+__device__ __forceinline__ void product(float (&d)[2][4], const Left &f, const uint32_t (&hi)[4], const uint32_t (&lo)[4]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        mma16816(d[u], f.hi, hi[2 * u], hi[2 * u + 1]);
+        mma16816(d[u], f.hi, lo[2 * u], lo[2 * u + 1]);
+        mma16816(d[u], f.lo, hi[2 * u], hi[2 * u + 1]);
+    }
+}
+
+__global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kernel(const __grid_constant__ ChunkParams cp) {
     const Params &p = cp.a;
-    extern __shared__ __align__(128) unsigned char smem[];
-    float *A = reinterpret_cast<float *>(smem + OFF_A), *T = reinterpret_cast<float *>(smem + OFF_TF);
-    float *M = reinterpret_cast<float *>(smem + OFF_M);
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char *img = smem + OFF_IMG;
-    float2 *G = reinterpret_cast<float2 *>(smem + OFF_G);
-    float *beta = reinterpret_cast<float *>(smem + OFF_G + C * 8);
+    Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t slot = blockIdx.x / p.H;
     const int h = static_cast<int>(blockIdx.x % p.H), hk = h / p.rep;
@@ -107,15 +155,21 @@ __global__ void __launch_bounds__(THREADS, 3) kda_gated_delta_prepare_kernel(con
     }
     const int64_t t0 = bos + (slot - slot_base(bos, n)) * C;
     if (t0 < bos || t0 >= eos) return;
-    const int left = eos - t0 < C ? static_cast<int>(eos - t0) : C;
+    const int left = eos - t0 < C ? static_cast<int>(eos - t0) : C;  // rows behind are anything: what they enter is set to zero
 
+    if (tid == 0) {
+        mbar_init(&m->full, 1);
+        mbar_fence_init();
+        mbar_arrive_expect_tx(&m->full, 4 * TILE);
+        const uint64_t keep = evict_normal();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int idx = tid + i * THREADS, r = (idx >> 4) & 63, c = idx & 15;
-        const bool is_q = idx >= 1024, in = r < left;
-        const __nv_bfloat16 *src = is_q ? p.q + (t0 + (in ? r : 0)) * p.qs : p.k + (t0 + (in ? r : 0)) * p.ks;
-        cp_async16(smem + (is_q ? OFF_Q : OFF_K) + kq_at(r, c), src + hk * DK + 8 * c, in ? 16 : 0);
+        for (int c = 0; c < 2; ++c) {
+            lin::tma_load_3d(smem + OFF_K + c * TILE, &cp.tk, 64 * c, hk, static_cast<int>(t0), &m->full, keep);
+            lin::tma_load_3d(smem + OFF_Q + c * TILE, &cp.tq, 64 * c, hk, static_cast<int>(t0), &m->full, keep);
+        }
     }
+    float decays[4];  // of tokens 2 lane, 2 lane + 1: to the token, after it (warp 0)
+    float whole = 0.f, less = 0.f;
     if (warp == 0) {  // log2 decays, summed in 64 bits: differences of far sums keep their last bits
         double x[2];
         bool bad = false;
@@ -123,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, 3) kda_gated_delta_prepare_kernel(con
         for (int i = 0; i < 2; ++i) {
             const int t = 2 * lane + i;
             const float g = t < left ? p.g[(t0 + t) * p.H + h] : 0.f;
-            beta[t] = t < left ? p.beta[(t0 + t) * p.H + h] : 0.f;
+            m->beta[t] = t < left ? p.beta[(t0 + t) * p.H + h] : 0.f;
             bad |= !(g <= 0.f);
             x[i] = (g < -138.f ? -200.0 : static_cast<double>(g) * 1.4426950408889634);  // (2^-200 is 0 in fp32)
         }
@@ -134,202 +188,219 @@ __global__ void __launch_bounds__(THREADS, 3) kda_gated_delta_prepare_kernel(con
             if (lane >= d) s += y;
         }
         const double end = __shfl_sync(0xffffffffu, s, 31);
-        const double g1 = s, g0 = s - x[1];
-        Decays *d = reinterpret_cast<Decays *>(img + OFF_DECAYS);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const double gt = i ? g1 : g0, rest = end - gt;
-            const float hi = static_cast<float>(gt), lo = static_cast<float>(gt - hi);
-            G[2 * lane + i] = make_float2(hi, lo);
-            d->upto[2 * lane + i] = ex2_2(hi, lo);
-            const float rhi = static_cast<float>(rest);
-            d->after[2 * lane + i] = ex2_2(rhi, static_cast<float>(rest - rhi));
+            const double gt = i ? s : s - x[1], rest = end - gt;
+            const float hi = static_cast<float>(gt), lo = static_cast<float>(gt - hi), rhi = static_cast<float>(rest);
+            m->G[2 * lane + i] = make_float2(hi, lo);
+            decays[i] = ex2_2(hi, lo);
+            decays[2 + i] = ex2_2(rhi, static_cast<float>(rest - rhi));
         }
-        if (lane == 0) {
-            const float hi = static_cast<float>(end), lo = static_cast<float>(end - hi);
-            d->whole = ex2_2(hi, lo);
-            d->less = expm1f(static_cast<float>(end * 0.6931471805599453));
-        }
+        const float hi = static_cast<float>(end), lo = static_cast<float>(end - hi);
+        whole = ex2_2(hi, lo);
+        less = expm1f(static_cast<float>(end * 0.6931471805599453));
         if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, KDA_ERR_GATE_RANGE);
     }
-    cp_async_commit();
-    cp_async_wait_all();
-    __syncthreads();
+    __syncthreads();  // (the barrier is set up, G is there)
+    {                 // decays between blocks, in two factors that meet at the row's block
+        const float2 zero = make_float2(0.f, 0.f);
+        for (int i = tid; i < C + SB * 6; i += THREADS) {
+            if (i < C) {
+                m->row[i] = ex2_diff(m->G[i], i >= SB ? m->G[(i & ~(SB - 1)) - 1] : zero);
+            } else {
+                const int e = i - C, b = e < SB ? 0 : e < 3 * SB ? 1 : 2, j = e - (b == 0 ? 0 : b == 1 ? SB : 3 * SB);
+                m->col[b][j] = ex2_diff(m->G[SB * (b + 1) - 1], m->G[j]);
+            }
+        }
+    }
+    bool here = false;
+    for (int i = 0; i < 200000 && !here; ++i) here = lin::mbar_wait_some(&m->full, 0);
+    if (!__syncthreads_and(here)) {  // (never: the copies end at the latest with the kernel)
+        if (tid == 0) set_status(p.status, KDA_ERR_TIMEOUT);
+        return;
+    }
 
-    // rows 16 rb .. of K K^T (warps 0-3) or Q K^T (4-7), up to the diagonal
-    const int rb = warp & 3;
-    float acc[8][4];
+    // rows 16 w .. of K K^T and Q K^T, up to the diagonal
+    const int w = warp, g = lane >> 2, q2 = 2 * (lane & 3);
+    auto kq_at = [](int r, int c) { return (c >> 3) * TILE + swz(r, c & 7); };  // 16-byte group c of row r
+    float sk[2 * BLOCKS][4], sq[2 * BLOCKS][4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 2 * BLOCKS; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+        for (int i = 0; i < 4; ++i) sk[j][i] = sq[j][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < DK / 16; ++kk) {
+        uint32_t a[4], c[4];
+        ldsm_x4(a, smem + OFF_K + kq_at(SB * w + (lane & 15), 2 * kk + (lane >> 4)));
+        ldsm_x4(c, smem + OFF_Q + kq_at(SB * w + (lane & 15), 2 * kk + (lane >> 4)));
+#pragma unroll
+        for (int j = 0; j < BLOCKS; ++j) {
+            if (j > w) continue;
+            uint32_t b[4];
+            ldsm_x4(b, smem + OFF_K + kq_at(SB * j + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
+            mma16816(sk[2 * j], a, b[0], b[1]);
+            mma16816(sk[2 * j + 1], a, b[2], b[3]);
+            mma16816(sq[2 * j], c, b[0], b[1]);
+            mma16816(sq[2 * j + 1], c, b[2], b[3]);
+        }
+    }
+    const int i0 = SB * w + g;
+    const float bi[2] = {m->beta[i0], m->beta[i0 + 8]};
+    const bool in[2] = {i0 < left, i0 + 8 < left};
+    Left A[BLOCKS - 1], P[BLOCKS];
     {
-        const unsigned char *rows = smem + (warp < 4 ? OFF_K : OFF_Q);
+        const float rf[2] = {m->row[i0], m->row[i0 + 8]};
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) {
-            uint32_t a[4];
-            ldsm_x4(a, rows + kq_at(16 * rb + (lane & 15), 2 * kk + (lane >> 4)));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (j > rb) continue;
-                uint32_t b[4];
-                ldsm_x4(b, smem + OFF_K + kq_at(16 * j + (lane & 7) + ((lane >> 4) << 3), 2 * kk + ((lane >> 3) & 1)));
-                mma16816(acc[2 * j], a, b[0], b[1]);
-                mma16816(acc[2 * j + 1], a, b[2], b[3]);
-            }
-        }
-    }
-    const int i0 = 16 * rb + (lane >> 2);
-    const float2 gi[2] = {G[i0], G[i0 + 8]};
-    const float mul[2] = {warp < 4 ? beta[i0] : p.scale, warp < 4 ? beta[i0 + 8] : p.scale};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int i = i0 + (c >> 1) * 8, s = 8 * j + 2 * (lane & 3) + (c & 1);
-            const float2 gs = G[s];
-            const float d = (gi[c >> 1].x - gs.x) + (gi[c >> 1].y - gs.y);
-            const bool in = warp < 4 ? s < i : s <= i;
-            acc[j][c] = in ? mul[c >> 1] * ex2(d) * acc[j][c] : 0.f;
-        }
-    }
-    __syncthreads();  // (k and q have been read: A and T go over them)
-    if (warp < 4) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<float2 *>(A + (i0 + 8 * c) * LD + 8 * j + 2 * (lane & 3)) =
-                    make_float2(acc[j][2 * c], acc[j][2 * c + 1]);
-        __syncwarp();
-        // the diagonal block of these rows, inverted by substitution: a lane has a column
-        if (lane < 16) {
-            const float *a = A + 16 * rb * LD + 16 * rb;
-            float x[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                float s0 = r == lane ? 1.f : 0.f, s1 = 0.f;
-#pragma unroll
-                for (int m = 0; m < r; m += 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(a + r * LD + m);
-                    s0 = fmaf(-v.x, x[m], s0);
-                    if (m + 1 < r) s1 = fmaf(-v.y, x[m + 1], s1);
-                    if (m + 2 < r) s0 = fmaf(-v.z, x[m + 2], s0);
-                    if (m + 3 < r) s1 = fmaf(-v.w, x[m + 3], s1);
-                }
-                x[r] = s0 + s1;
-                T[(16 * rb + r) * LD + 16 * rb + lane] = x[r];
-            }
-        }
-    }
-    __syncthreads();
-    {  // the blocks below the diagonal of both halves: -T22 (A21 T11), 16 x 16
-        const int half = tid >> 7, i = (tid >> 3) & 15, j = 2 * (tid & 7);
-        const float *a = A + (32 * half + 16) * LD + 32 * half, *t11 = T + 32 * half * LD + 32 * half;
-        float *m = M + 16 * half * LD;
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float av = a[i * LD + k];
-            const float2 t = *reinterpret_cast<const float2 *>(t11 + k * LD + j);
-            s0 = fmaf(av, t.x, s0);
-            s1 = fmaf(av, t.y, s1);
-        }
-        *reinterpret_cast<float2 *>(m + i * LD + j) = make_float2(s0, s1);
-        __syncthreads();
-        const float *t22 = T + (32 * half + 16) * LD + 32 * half + 16;
-        s0 = s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const float av = t22[i * LD + k];
-            const float2 t = *reinterpret_cast<const float2 *>(m + k * LD + j);
-            s0 = fmaf(-av, t.x, s0);
-            s1 = fmaf(-av, t.y, s1);
-        }
-        *reinterpret_cast<float2 *>(T + (32 * half + 16 + i) * LD + 32 * half + j) = make_float2(s0, s1);
-        // (above the diagonal blocks: zeros, that the next step multiplies)
-        *reinterpret_cast<float2 *>(T + (32 * half + i) * LD + 32 * half + 16 + j) = make_float2(0.f, 0.f);
-        __syncthreads();
-    }
-    {  // and of the whole, 32 x 32
-        const int i = tid >> 3, j = 4 * (tid & 7);
-        auto product = [&](const float *a, const float *b) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int k = 0; k < 32; ++k) {
-                const float av = a[i * LD + k];
-                const float4 t = *reinterpret_cast<const float4 *>(b + k * LD + j);
-                s.x = fmaf(av, t.x, s.x);
-                s.y = fmaf(av, t.y, s.y);
-                s.z = fmaf(av, t.z, s.z);
-                s.w = fmaf(av, t.w, s.w);
-            }
-            return s;
-        };
-        *reinterpret_cast<float4 *>(M + i * LD + j) = product(A + 32 * LD, T);
-        __syncthreads();
-        const float4 s = product(T + 32 * LD + 32, M);
-        *reinterpret_cast<float4 *>(T + (32 + i) * LD + j) = make_float4(-s.x, -s.y, -s.z, -s.w);
-        __syncthreads();
-    }
-    {  // T diag(beta) in two bf16 terms
-        const int r = tid >> 2, c0 = 16 * (tid & 3);
-#pragma unroll
-        for (int c = 0; c < 16; c += 8) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int s = c0 + c + 2 * j;
-                const float2 t = *reinterpret_cast<const float2 *>(T + r * LD + s);
-                const float x = s <= r ? t.x * beta[s] : 0.f, y = s + 1 <= r ? t.y * beta[s + 1] : 0.f;
-                hi[j] = pack_bf16(x, y);
-                const float2 f = unpack_bf16(hi[j]);
-                lo[j] = pack_bf16(x - f.x, y - f.y);
-            }
-            const int at = swz(r, (c0 + c) / 8);
-            *reinterpret_cast<uint4 *>(img + OFF_T + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(img + OFF_TLO + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-    }
-    __syncthreads();
-    if (warp >= 4) {  // P T, rows 16 rb ..: P's accumulators are its fragments, both factors in two terms
-        float pt[8][4];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pt[j][i] = 0.f;
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-            if (kb > rb) continue;
-            uint32_t ph[4], pl[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float *v = &acc[2 * kb + (i >> 1)][2 * (i & 1)];
-                ph[i] = pack_bf16(v[0], v[1]);
-                const float2 f = unpack_bf16(ph[i]);
-                pl[i] = pack_bf16(v[0] - f.x, v[1] - f.y);
-            }
-#pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                if (nb > kb) continue;
-                uint32_t bh[4], bl[4];
-                const int at = swz(16 * kb + (lane & 15), 2 * nb + (lane >> 4));
-                ldsm_x4_t(bh, img + OFF_T + at);
-                ldsm_x4_t(bl, img + OFF_TLO + at);
+        for (int j = 0; j < BLOCKS; ++j) {
+            if (j > w) continue;
+            if (j < w) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    mma16816(pt[2 * nb + u], ph, bh[2 * u], bh[2 * u + 1]);
-                    mma16816(pt[2 * nb + u], ph, bl[2 * u], bl[2 * u + 1]);
-                    mma16816(pt[2 * nb + u], pl, bh[2 * u], bh[2 * u + 1]);
+                    const float2 cf = *reinterpret_cast<const float2 *>(&m->col[w - 1][SB * j + 8 * u + q2]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float l = rf[c >> 1] * ((c & 1) ? cf.y : cf.x);
+                        sk[2 * j + u][c] = in[c >> 1] ? bi[c >> 1] * l * sk[2 * j + u][c] : 0.f;
+                        sq[2 * j + u][c] = in[c >> 1] ? p.scale * l * sq[2 * j + u][c] : 0.f;
+                    }
                 }
+                to_left(A[j < BLOCKS - 1 ? j : 0], sk[2 * j], sk[2 * j + 1]);
+            } else {
+                const float2 gi[2] = {m->G[i0], m->G[i0 + 8]};
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int r = g + 8 * (c >> 1), s = 8 * u + q2 + (c & 1);
+                        const float l = ex2_diff(gi[c >> 1], m->G[SB * w + s]);
+                        sk[2 * j + u][c] = in[c >> 1] && s < r ? bi[c >> 1] * l * sk[2 * j + u][c] : 0.f;
+                        sq[2 * j + u][c] = in[c >> 1] && s <= r ? p.scale * l * sq[2 * j + u][c] : 0.f;
+                    }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<float2 *>(&m->diag[w][(g + 8 * c) * LD + 8 * u + q2]) =
+                            make_float2(sk[2 * j + u][2 * c], sk[2 * j + u][2 * c + 1]);
+            }
+            to_left(P[j], sq[2 * j], sq[2 * j + 1]);
+        }
+    }
+    __syncthreads();  // (k and q have been read: what leaves goes over them)
+    Left D;           // -T_ww
+    {
+        float *a = m->diag[w];
+        float x[SB];
+        if (lane < SB) {  // a column each
+#pragma unroll
+            for (int r = 0; r < SB; ++r) {
+                float s0 = r == lane ? 1.f : 0.f, s1 = 0.f;
+#pragma unroll
+                for (int k = 0; k < r; k += 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(a + r * LD + k);
+                    s0 = fmaf(-v.x, x[k], s0);
+                    if (k + 1 < r) s1 = fmaf(-v.y, x[k + 1], s1);
+                    if (k + 2 < r) s0 = fmaf(-v.z, x[k + 2], s0);
+                    if (k + 3 < r) s1 = fmaf(-v.w, x[k + 3], s1);
+                }
+                x[r] = s0 + s1;
             }
         }
+        __syncwarp();
+        if (lane < SB) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+            for (int r = 0; r < SB; ++r) a[r * LD + lane] = r >= lane ? x[r] : 0.f;
+        }
+        __syncwarp();
+        float t[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float2 be = *reinterpret_cast<const float2 *>(&m->beta[SB * w + 8 * u + q2]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float2 v = *reinterpret_cast<const float2 *>(a + (g + 8 * c) * LD + 8 * u + q2);
+                t[u][2 * c] = -v.x, t[u][2 * c + 1] = -v.y;
+                uint32_t hi, lo;
+                split_pair(v.x * be.x, v.y * be.y, hi, lo);
+                const int at = swz(i0 + 8 * c, 2 * w + u) + 2 * q2;
+                *reinterpret_cast<uint32_t *>(img + OFF_T + at) = hi;
+                *reinterpret_cast<uint32_t *>(img + OFF_TLO + at) = lo;
+            }
+        }
+        to_left(D, t[0], t[1]);
+        for (int c = 2 * w + 2; c < 2 * BLOCKS; ++c) {  // above the diagonal: zeros
+            const int tile = lane < 16 ? OFF_T : OFF_TLO;
+            *reinterpret_cast<uint4 *>(img + tile + swz(SB * w + (lane & 15), c)) = make_uint4(0, 0, 0, 0);
+            if (lane < 16) *reinterpret_cast<uint4 *>(img + OFF_PT + swz(SB * w + lane, c)) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    if (warp == 0) {
+        Decays *d = reinterpret_cast<Decays *>(img + OFF_DECAYS);
+        *reinterpret_cast<float2 *>(&d->upto[2 * lane]) = make_float2(decays[0], decays[1]);
+        *reinterpret_cast<float2 *>(&d->after[2 * lane]) = make_float2(decays[2], decays[3]);
+        if (lane == 0) d->whole = whole, d->less = less;
+    }
+    __syncthreads();
+    // the right operand's fragments of block (k, j) of T
+    auto load_t = [&](int k, int j, uint32_t(&hi)[4], uint32_t(&lo)[4]) {
+        const int at = swz(SB * k + (lane & 15), 2 * j + (lane >> 4));
+        ldsm_x4_t(hi, img + OFF_T + at);
+        ldsm_x4_t(lo, img + OFF_TLO + at);
+    };
+#pragma unroll
+    for (int d = 1; d < BLOCKS; ++d) {
+        if (w >= d) {
+            const int j = w - d;
+            float r[2][4] = {};
+#pragma unroll
+            for (int k = 0; k < BLOCKS - 1; ++k) {
+                if (k < j || k >= w) continue;
+                uint32_t hi[4], lo[4];
+                load_t(k, j, hi, lo);
+                product(r, A[k], hi, lo);
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x, y;
+                    split_pair(r[u][2 * c], r[u][2 * c + 1], x, y);
+                    hi[2 * u + c] = transpose(x);
+                    lo[2 * u + c] = transpose(y);
+                }
+            float t[2][4] = {};
+            product(t, D, hi, lo);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x, y;
+                    split_pair(t[u][2 * c], t[u][2 * c + 1], x, y);
+                    const int at = swz(i0 + 8 * c, 2 * j + u) + 2 * q2;
+                    *reinterpret_cast<uint32_t *>(img + OFF_T + at) = x;
+                    *reinterpret_cast<uint32_t *>(img + OFF_TLO + at) = y;
+                }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j) {  // P T
+        if (j > w) continue;
+        float t[2][4] = {};
+#pragma unroll
+        for (int k = j; k < BLOCKS; ++k) {
+            if (k > w) continue;
+            uint32_t hi[4], lo[4];
+            load_t(k, j, hi, lo);
+            product(t, P[k], hi, lo);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<uint32_t *>(img + OFF_PT + swz(i0 + 8 * c, j) + 4 * (lane & 3)) =
-                    pack_bf16(pt[j][2 * c], pt[j][2 * c + 1]);
+                *reinterpret_cast<uint32_t *>(img + OFF_PT + swz(i0 + 8 * c, 2 * j + u) + 2 * q2) =
+                    pack_bf16(t[u][2 * c], t[u][2 * c + 1]);
     }
     fence_proxy_async_shared();
     __syncthreads();
