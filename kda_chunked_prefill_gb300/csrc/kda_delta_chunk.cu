@@ -33,6 +33,7 @@ constexpr int C = 64;  // tokens of a chunk
 // What the first launch leaves of a chunk and head. The tiles are rows of 64 bf16 (128 bytes), 128-byte swizzled.
 struct Decays {
     float upto[C];    // e^{G_t}
+    float out[C];     // scale e^{G_t}
     float after[C];   // e^{G_end - G_t}
     float whole, less;  // e^{G_end}, and minus 1
     float pad[30];
@@ -54,14 +55,193 @@ __device__ __forceinline__ uint64_t evict_normal() {  // (the second launch read
     return p;
 }
 
+// A part of a sequence that a CTA walks: chunks c0 .. c0 + len - 1 of sequence n.
+struct Segment {
+    int32_t n, c0, len;
+    int32_t from;   // the state it begins with: after a cut, its number; -1: the sequence's initial one; -2 - i: cut i's copy of it
+    int32_t to;     // of the pass over the states: the cut that its state goes to
+    int32_t kind;   // 0: outputs and the sequence's last state, 3: outputs; of the pass over the states, 1: the state, 2: its map
+};
+// The cuts of a sequence: numbers first .. first + count - 1.
+struct Cuts {
+    int32_t n, first, count;
+};
+
 struct ChunkParams {
     Params a;
     CUtensorMap tq, tk, tv;
     unsigned char *images;  // [slot][head]
     int64_t slots;
+    // sequences that are cut (device memory in the workspace)
+    int32_t shortest;       // shortest cut that the workspace is sized for, in chunks; 0: none is cut
+    int32_t sms;
+    int32_t most_segs, most_cuts;  // that the workspace holds
+    int32_t *counts;        // [0] segments, [1] those of the pass over the states, [2] sequences to join
+    Segment *segs, *segs_s;
+    Cuts *cuts;
+    // [cut][head][2][128][128]: the state after it (from zero; joined: the true one); the map of the part before it, transposed, or, for a
+    // sequence's first cut, the initial state (which the last part may have overwritten when the first begins with it)
+    float *states;
 };
 
-// ------------------------------------------------------------------ first launch: T, P T and the decays of each chunk
+// ------------------------------------------------------------------ which sequences are cut, and where
+namespace plan {
+
+// Cuts that are estimated: the shortest times these, over 2; and none.
+constexpr int CUTS = 8;
+__host__ __device__ constexpr int cut_length(int i, int shortest) {
+    constexpr int twice[CUTS] = {2, 3, 4, 6, 8, 12, 16, 24};
+    return shortest * twice[i] / 2;
+}
+struct Work {
+    int32_t jobs, longest;
+    int64_t chunks;
+    int32_t cuts;
+};
+__host__ __device__ inline void add(Work &w, int64_t count, int len) {
+    if (count < 1) return;
+    w.jobs += static_cast<int32_t>(count);
+    w.chunks += count * len;
+    if (len > w.longest) w.longest = len;
+}
+// A sequence of `chunks` cut to `len` or less: its parts' length, and how many.
+__host__ __device__ inline void parts_of(int chunks, int len, int &one, int &k) {
+    one = chunks;
+    k = 1;
+    if (chunks <= len) return;
+    one = (chunks - 1) / ((chunks - 1) / len + 1) + 1;
+    k = (chunks - 1) / one + 1;
+}
+// Its jobs in the outputs' pass, and in the pass over the states: all parts but the last, the state from zero and, but for the first, the
+// map.
+__host__ __device__ inline void add_sequence(Work &out, Work &states, int &most, int chunks, int len) {
+    int one, k;
+    parts_of(chunks, len, one, k);
+    add(out, k, one);
+    if (k > 1) add(states, 2 * k - 3, one);
+    states.cuts += k - 1;
+    if (k > most) most = k;
+}
+// The time of a pass on `sms` CTAs, in chunks: a job takes its own and two for its start and end.
+__host__ __device__ inline float pass_time(const Work &w, int heads, int sms) {
+    const float jobs = static_cast<float>(w.jobs) * heads, one = w.longest + 2.f;
+    const float even = (static_cast<float>(w.chunks) * heads + 2.f * jobs) / sms + (jobs > sms ? 0.5f * one : 0.f);
+    const float rounds = ceilf(jobs / sms) * one;
+    const float t = even < rounds ? even : rounds;
+    return w.jobs == 0 ? 0.f : t > one ? t : one;
+}
+// With the join (a quarter of a chunk's time a part) and two more launches.
+__host__ __device__ inline float time_of(const Work &out, const Work &states, int most, int heads, int sms) {
+    return pass_time(out, heads, sms) + (most > 1 ? pass_time(states, heads, sms) + 0.25f * most + 2.f : 0.f);
+}
+
+constexpr int THREADS = 128, BUCKETS = 64;
+struct Shared {
+    Work out[CUTS + 1], states[CUTS + 1];
+    int32_t most[CUTS + 1];
+    int32_t bucket[2][BUCKETS];  // first segments of each length, long ones first: of the outputs' pass, of the states'
+    int32_t cuts, joined, len, longest, none;
+};
+
+__device__ __forceinline__ int chunks_of(const Params &p, int n) {  // -1: bounds that are none
+    const int64_t b = p.cu[n], e = p.cu[n + 1];
+    if (b < 0 || e < b || e > p.T || p.cu[0] != 0) return -1;
+    return static_cast<int>((e - b + C - 1) / C);
+}
+
+// One CTA: the cut by estimates from the lengths, and the segments of both passes, long ones first.
+__device__ void make(const ChunkParams &cp, Shared *sh) {
+    const Params &p = cp.a;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < 2 * BUCKETS; i += THREADS) sh->bucket[i / BUCKETS][i % BUCKETS] = 0;
+    if (tid <= CUTS) sh->out[tid] = sh->states[tid] = Work{0, 0, 0, 0}, sh->most[tid] = 0;
+    if (tid == 0) sh->cuts = sh->joined = 0;
+    __syncthreads();
+    const int candidates = cp.shortest ? CUTS + 1 : 1;  // the last: none is cut
+    for (int c = 0; c < candidates; ++c) {
+        const int len = c == candidates - 1 ? 0x7fffffff : cut_length(c, cp.shortest);
+        Work out{0, 0, 0, 0}, states{0, 0, 0, 0};
+        int most = 0;
+        for (int n = tid; n < p.N; n += THREADS) {
+            const int chunks = chunks_of(p, n);
+            if (chunks < 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
+            else add_sequence(out, states, most, chunks, len);
+        }
+        auto gather = [](Work &to, const Work &w) {
+            atomicAdd(&to.jobs, w.jobs);
+            atomicMax(&to.longest, w.longest);
+            atomicAdd(&to.cuts, w.cuts);
+            atomicAdd(reinterpret_cast<unsigned long long *>(&to.chunks), static_cast<unsigned long long>(w.chunks));
+        };
+        gather(sh->out[c], out);
+        gather(sh->states[c], states);
+        atomicMax(&sh->most[c], most);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int best = candidates - 1;
+        float least = 3.0e38f;
+        for (int c = candidates - 1; c >= 0; --c) {
+            // (bad bounds may overlap, and then hold more than the workspace)
+            if (c < candidates - 1 && (sh->out[c].jobs > cp.most_segs || sh->states[c].cuts > cp.most_cuts)) continue;
+            const float t = time_of(sh->out[c], sh->states[c], sh->most[c], p.H, cp.sms);
+            if (t < least) least = t, best = c;
+        }
+        sh->len = best == candidates - 1 ? 0x7fffffff : cut_length(best, cp.shortest);
+        sh->longest = sh->out[best].longest > 0 ? sh->out[best].longest : 1;
+    }
+    __syncthreads();
+    auto bucket_of = [&](int len) { return BUCKETS - 1 - static_cast<int>(static_cast<int64_t>(len) * (BUCKETS - 1) / sh->longest); };
+    auto for_each = [&](auto &&f) {
+        for (int n = tid; n < p.N; n += THREADS) {
+            const int chunks = chunks_of(p, n);
+            if (chunks < 0) continue;
+            int one, k;
+            parts_of(chunks, sh->len, one, k);
+            f(n, chunks, k, one);
+        }
+    };
+    for_each([&](int, int chunks, int k, int one) {
+        for (int i = 0; i < k; ++i) {
+            const int rest = chunks - i * one, len = rest < one ? rest : one;
+            atomicAdd(&sh->bucket[0][bucket_of(len)], 1);
+            if (i < k - 1) atomicAdd(&sh->bucket[1][bucket_of(len)], i ? 2 : 1);
+        }
+    });
+    __syncthreads();
+    if (tid < 2) {
+        int sum = 0;
+        for (int b = 0; b < BUCKETS; ++b) {
+            const int c = sh->bucket[tid][b];
+            sh->bucket[tid][b] = sum;
+            sum += c;
+        }
+        cp.counts[tid] = sum;
+    }
+    __syncthreads();
+    for_each([&](int n, int chunks, int k, int one) {
+        int first = -1;
+        if (k > 1) {
+            first = atomicAdd(&sh->cuts, k - 1);
+            cp.cuts[atomicAdd(&sh->joined, 1)] = {n, first, k - 1};
+        }
+        for (int i = 0; i < k; ++i) {
+            const int rest = chunks - i * one, len = rest < one ? rest : one, b = bucket_of(len);
+            cp.segs[atomicAdd(&sh->bucket[0][b], 1)] = {n, i * one, len, i ? first + i - 1 : k > 1 ? -2 - first : -1, -1,
+                                                         i == k - 1 ? 0 : 3};
+            if (i == k - 1) continue;
+            const int at = atomicAdd(&sh->bucket[1][b], i ? 2 : 1);
+            cp.segs_s[at] = {n, i * one, len, -1, first + i, 1};
+            if (i) cp.segs_s[at + 1] = {n, i * one, len, -1, first + i, 2};
+        }
+    });
+    __syncthreads();
+    if (tid == 0) cp.counts[2] = sh->joined;
+}
+
+}  // namespace plan
+
+// ------------------------------------------------------------------ first launch: T, P T and the decays of each chunk; the plan
 namespace prep {
 
 // Four warps to a chunk and head, each with 16 rows of A and P, in blocks of 16 x 16 that stay in registers as fragments. T's
@@ -74,6 +254,7 @@ constexpr int LD = 20;                                   // floats of a row of a
 constexpr int OFF_K = 0, OFF_Q = 2 * TILE, OFF_IMG = 0;  // k and q, two panels of 64 channels each; over them, what leaves
 constexpr int OFF_MISC = 4 * TILE;
 static_assert(IMAGE <= OFF_MISC, "layout");
+static_assert(sizeof(plan::Shared) <= OFF_MISC && plan::THREADS == THREADS, "the plan's CTA");
 
 struct Misc {
     alignas(16) float diag[BLOCKS][SB * LD];
@@ -144,8 +325,12 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     unsigned char *img = smem + OFF_IMG;
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t slot = blockIdx.x / p.H;
-    const int h = static_cast<int>(blockIdx.x % p.H), hk = h / p.rep;
+    if (blockIdx.x == 0) {
+        plan::make(cp, reinterpret_cast<plan::Shared *>(smem));
+        return;
+    }
+    const int64_t slot = (blockIdx.x - 1) / p.H;
+    const int h = static_cast<int>((blockIdx.x - 1) % p.H), hk = h / p.rep;
 
     const int n = find_sequence(p, slot, lane);
     const int64_t bos = p.cu[n], eos = p.cu[n + 1];
@@ -337,6 +522,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     if (warp == 0) {
         Decays *d = reinterpret_cast<Decays *>(img + OFF_DECAYS);
         *reinterpret_cast<float2 *>(&d->upto[2 * lane]) = make_float2(decays[0], decays[1]);
+        *reinterpret_cast<float2 *>(&d->out[2 * lane]) = make_float2(p.scale * decays[0], p.scale * decays[1]);
         *reinterpret_cast<float2 *>(&d->after[2 * lane]) = make_float2(decays[2], decays[3]);
         if (lane == 0) d->whole = whole, d->less = less;
     }
@@ -407,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     if (tid == 0) {
         bulk_s2g(cp.images + (slot * p.H + h) * IMAGE, img, IMAGE);
         bulk_commit();
-        bulk_wait_all();
+        bulk_wait_read();
     }
 }
 
@@ -490,20 +676,21 @@ __device__ __forceinline__ void store_split(uint32_t hi, uint32_t lo, const f2 (
     tc_fence_before();
 }
 
+// STATES: the pass over the states of cut sequences.
+template <bool STATES>
 __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const __grid_constant__ ChunkParams cp) {
     const Params &p = cp.a;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t chain = blockIdx.x;
-    const int n = static_cast<int>(chain / p.H), h = static_cast<int>(chain % p.H), hk = h / p.rep;
-    const int64_t bos = p.cu[n], eos = p.cu[n + 1];
-    if (bos < 0 || eos < bos || eos > p.T || p.cu[0] != 0) {
-        if (tid == 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
-        return;
-    }
-    const int chunks = static_cast<int>((eos - bos + C - 1) / C);
+    const int job = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H), hk = h / p.rep;
+    if (job >= cp.counts[STATES ? 1 : 0]) return;
+    const Segment seg = (STATES ? cp.segs_s : cp.segs)[job];
+    const bool is_map = STATES && seg.kind == 2;
+    const int64_t chain = static_cast<int64_t>(seg.n) * p.H + h;
+    const int64_t begin = p.cu[seg.n], bos = begin + static_cast<int64_t>(seg.c0) * C, eos = p.cu[seg.n + 1];  // from the segment on
+    const int chunks = seg.len;
 
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], WARPS + 1);
@@ -521,7 +708,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 
     if (warp == WARP_LOAD) {
         if (lane == 0) {
-            const unsigned char *images = cp.images + (slot_base(bos, n) * p.H + h) * IMAGE;
+            const unsigned char *images = cp.images + ((slot_base(begin, seg.n) + seg.c0) * p.H + h) * IMAGE;
             bool ok = true;
             int it = 0;
             for (; it < chunks; ++it) {
@@ -543,11 +730,12 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) wait_drain(&m->full[i % STAGES], (i / STAGES) & 1);
         }
     } else if (warp == WARP_MMA) {
+        // Issued by one thread, whose instructions count: descriptors by one addition each.
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t ID = lin::idesc_bf16(false, false, 128, 128), ID_LO = lin::idesc_bf16(false, false, 128, 64),
+        constexpr uint32_t ID = lin::idesc_bf16(false, false, 128, 128), ID_64 = lin::idesc_bf16(false, false, 128, 64),
                            ID_U = lin::idesc_bf16(false, true, 128, 128);
         bool ok = true;
-        for (int it = 0; it < chunks; ++it) {
+        for (int it = 0; ok && it < chunks; ++it) {
             const int st = it % STAGES;
             const uint32_t ph = it & 1, s = base + st * STAGE;
             if (!(ok = wait_warp(m, &m->full[st], (it / STAGES) & 1))) break;
@@ -561,51 +749,44 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 fence_proxy_async_shared();
                 __syncwarp();
             }
-            auto kq_at = [&](int k) { return umma_desc_sw128(s + OFF_KQ + (k >> 2) * PANEL + (k & 3) * 32, 16, 1024); };
+            if (lane == 0) {
+                const uint64_t kq = umma_desc_sw128(s + OFF_KQ, 16, 1024), tt = umma_desc_sw128(s + OFF_TT, 16, 1024);
+                const uint64_t kt = umma_desc_sw128(s + OFF_KQ, PANEL, 1024);
+                // (additions to the address field: bytes / 16)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!(ok = wait_warp(m, &m->s[half], ph))) break;
-                tc_fence_after();
-                if (lane == 0) {
+                for (int half = 0; half < 2; ++half) {
+                    if (!ok || !(ok = wait(m, &m->s[half], ph))) continue;
+                    tc_fence_after();
 #pragma unroll
                     for (int k = 4 * half; k < 4 * half + 4; ++k) {
-                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 8 * k, kq_at(k), ID, k > 0);
-                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 8 * k, kq_at(k), ID, 1);
+                        const uint64_t b = kq + ((k >> 2) * PANEL + (k & 3) * 32) / 16;
+                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 8 * k, b, ID, k > 0);
+                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 8 * k, b, ID, 1);
                     }
                 }
-                __syncwarp();
-            }
-            if (!ok) break;
-            if (lane == 0) {
-                umma_commit(&m->ks);
-            }
-            __syncwarp();
-            if (!(ok = wait_warp(m, &m->z, ph))) break;
-            tc_fence_after();
-            if (lane == 0) {
-                auto t_at = [&](int off, int k) { return umma_desc_sw128(s + off + k * 32, 16, 1024); };
+                if (ok) umma_commit(&m->ks);
+                if (ok && (ok = wait(m, &m->z, ph))) {
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, t_at(OFF_TT, k), ID, k > 0);
-                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k + 8, t_at(OFF_TT, k), ID, 1);
-                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, t_at(OFF_TL, k), ID_LO, 1);
+                    for (int k = 0; k < 4; ++k) {
+                        lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + k * 2, ID, k > 0);
+                        lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k + 8, tt + k * 2, ID, 1);
+                        lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + (OFF_TL - OFF_TT) / 16 + k * 2, ID_64, 1);
+                    }
+                    umma_commit(&m->xs);
                 }
-                umma_commit(&m->xs);
-            }
-            __syncwarp();
-            if (!(ok = wait_warp(m, &m->x, ph))) break;
-            tc_fence_after();
-            if (lane == 0) {
+                if (ok && (ok = wait(m, &m->x, ph))) {
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint64_t b = umma_desc_sw128(s + OFF_KQ + k * 2048, PANEL, 1024);
-                    lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k, b, ID_U, k > 0);
-                    lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k + 8, b, ID_U, 1);
+                    for (int k = 0; k < 4; ++k) {
+                        lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k, kt + k * 128, ID_U, k > 0);
+                        lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k + 8, kt + k * 128, ID_U, 1);
+                    }
+                    umma_commit(&m->u);
+                    umma_commit(&m->empty[st]);
                 }
-                umma_commit(&m->u);
-                umma_commit(&m->empty[st]);
             }
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
         }
         if (!ok && lane == 0) {
             umma_commit(&m->drained);
@@ -618,10 +799,18 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
         const uint32_t t = tmem + (static_cast<uint32_t>(32 * quad) << 16);
         const int k0 = KEYS * part, t0 = TOKS * part;
         f2 S[KEYS / 2];  // keys k0 + 2 i, k0 + 2 i + 1
+        constexpr size_t STATE = DK * DV;
         {
-            const float *s0 = p.s0 ? p.s0 + static_cast<size_t>(chain) * (DK * DV) + k0 * DV + val : nullptr;
+            const float *s0 = STATES ? (seg.c0 == 0 ? p.s0 : nullptr) : p.s0;
+            if (s0) s0 += chain * STATE;
+            if (!STATES && seg.from >= 0) s0 = cp.states + (static_cast<size_t>(seg.from) * p.H + h) * 2 * STATE;
+            if (!STATES && seg.from < -1 && s0) s0 = cp.states + (static_cast<size_t>(-2 - seg.from) * p.H + h) * 2 * STATE + STATE;
+            if (s0) s0 += k0 * DV + val;
 #pragma unroll
-            for (int i = 0; i < KEYS / 2; ++i) S[i] = s0 ? pair(s0[2 * i * DV], s0[(2 * i + 1) * DV]) : 0;
+            for (int i = 0; i < KEYS / 2; ++i) {
+                S[i] = s0 ? pair(s0[2 * i * DV], s0[(2 * i + 1) * DV]) : 0;
+                if (is_map) S[i] = pair(k0 + 2 * i == val ? 1.f : 0.f, k0 + 2 * i + 1 == val ? 1.f : 0.f);
+            }
         }
         bool ok = true;
         for (int it = 0; it < chunks; ++it) {
@@ -642,7 +831,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                     return static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(v + i * 128 + ((c ^ (i & 7)) << 4))) << 16;
                 };
 #pragma unroll
-                for (int i = 0; i < TOKS / 2; ++i) z[i] = pair(at(2 * i), at(2 * i + 1));
+                for (int i = 0; i < TOKS / 2; ++i) z[i] = is_map ? 0 : pair(at(2 * i), at(2 * i + 1));
             }
             const float whole = d->whole, less = d->less;
             uint32_t r[16];
@@ -679,17 +868,25 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             mask(w);
             store_split(t + COL_X + t0, t + COL_X + t0 + 8, w);
             arrive_warp(&m->x);
-            {
+            if (!STATES) {
                 uint32_t q[16];
                 tmem_ld16(t + COL_QS + t0, q);
                 tmem_ld16(t + COL_O + t0, r);
                 tmem_wait_ld();
                 tc_fence_before();
-                __nv_bfloat16 *o = p.o + ((bos + static_cast<int64_t>(it) * C + t0) * p.H + h) * DV + val;
+                // Two tokens of two neighbouring columns lie in two lanes: each stores both columns of one token.
+                const bool odd = lane & 1;
+                const int64_t ld = static_cast<int64_t>(p.H) * DV;
+                __nv_bfloat16 *o = p.o + (bos + static_cast<int64_t>(it) * C + t0 + odd) * ld + h * DV + (val & ~1);
+                const int mine = left - t0 - odd;  // tokens from this lane's first on
 #pragma unroll
-                for (int i = 0; i < TOKS; ++i) {
-                    const float x = fmaf(p.scale * d->upto[t0 + i], __uint_as_float(q[i]), __uint_as_float(r[i]));
-                    if (t0 + i < left) o[static_cast<int64_t>(i) * p.H * DV] = __float2bfloat16_rn(x);
+                for (int i = 0; i < TOKS / 2; ++i) {
+                    const float2 e = *reinterpret_cast<const float2 *>(&d->out[t0 + 2 * i]);
+                    const uint32_t a = lin::bf16_of(lin::fma2(pair(e.x, e.y), pair(q[2 * i], q[2 * i + 1]), pair(r[2 * i], r[2 * i + 1])));
+                    const uint32_t b = __shfl_xor_sync(0xffffffffu, a, 1);
+                    const uint32_t x = odd ? __byte_perm(b, a, 0x7632) : __byte_perm(a, b, 0x5410);
+                    if (2 * i < mine) *reinterpret_cast<uint32_t *>(o) = x;
+                    o += 2 * ld;
                 }
             }
             arrive_warp(&m->empty[st]);
@@ -708,8 +905,21 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::add2(S[i], lin::fma2(S[i], f, pair(u[2 * i], u[2 * i + 1])));
             }
         }
-        if (p.sT && ok) {
-            float *sT = p.sT + static_cast<size_t>(chain) * (DK * DV) + k0 * DV + val;
+        if (is_map) {  // by the columns that it maps from
+            if (ok) {
+                float *sT = cp.states + ((static_cast<size_t>(seg.to) * p.H + h) * 2 + 1) * STATE + val * DK + k0;
+#pragma unroll
+                for (int i = 0; i < KEYS / 2; i += 2) {
+                    float4 x;
+                    split(S[i], x.x, x.y);
+                    split(S[i + 1], x.z, x.w);
+                    *reinterpret_cast<float4 *>(sT + 2 * i) = x;
+                }
+            }
+        } else if (float *sT = STATES ? cp.states + (static_cast<size_t>(seg.to) * p.H + h) * 2 * STATE
+                                      : seg.kind == 0 && p.sT ? p.sT + chain * STATE : nullptr;
+                   sT && ok) {
+            sT += k0 * DV + val;
 #pragma unroll
             for (int i = 0; i < KEYS / 2; ++i) {
                 float x, y;
@@ -728,6 +938,51 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 
 }  // namespace walk
 
+// ------------------------------------------------------------------ between the passes: the states that the parts begin with
+namespace join {
+
+constexpr int COLS = 8, PARTS = DV / COLS, THREADS = DK;
+
+// After a cut, E = F E' + N, with E' the state after the cut before, F the map of the part between them and N its state from zero. One
+// CTA has 8 value columns of a sequence and head, a thread a key: fp32 throughout, the sums in one order.
+__global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __grid_constant__ ChunkParams cp) {
+    __shared__ alignas(16) float E[2][DK][COLS];
+    const int part = blockIdx.x % PARTS, h = static_cast<int>(blockIdx.x / PARTS % cp.a.H), key = threadIdx.x;
+    const int64_t i = blockIdx.x / PARTS / cp.a.H;
+    if (i >= cp.counts[2]) return;
+    const Cuts cuts = cp.cuts[i];
+    constexpr size_t STATE = DK * DV;
+    float *at = cp.states + (static_cast<size_t>(cuts.first) * cp.a.H + h) * 2 * STATE;
+    if (const float *s0 = cp.a.s0) {
+        s0 += (static_cast<int64_t>(cuts.n) * cp.a.H + h) * STATE + key * DV + COLS * part;
+        float4 *copy = reinterpret_cast<float4 *>(at + STATE + key * DV + COLS * part);
+        copy[0] = reinterpret_cast<const float4 *>(s0)[0];
+        copy[1] = reinterpret_cast<const float4 *>(s0)[1];
+    }
+    for (int s = 0; s < cuts.count; ++s, at += 2 * STATE * cp.a.H) {
+        float *n = at + key * DV + COLS * part;
+        float4 x = reinterpret_cast<const float4 *>(n)[0], y = reinterpret_cast<const float4 *>(n)[1];
+        if (s > 0) {
+            const float *f = at + STATE + key;
+            const float(&e)[DK][COLS] = E[(s - 1) & 1];
+#pragma unroll 16
+            for (int j = 0; j < DK; ++j) {
+                const float a = __ldcg(f + j * DK);
+                const float4 u = *reinterpret_cast<const float4 *>(&e[j][0]), v = *reinterpret_cast<const float4 *>(&e[j][4]);
+                x.x = fmaf(a, u.x, x.x), x.y = fmaf(a, u.y, x.y), x.z = fmaf(a, u.z, x.z), x.w = fmaf(a, u.w, x.w);
+                y.x = fmaf(a, v.x, y.x), y.y = fmaf(a, v.y, y.y), y.z = fmaf(a, v.z, y.z), y.w = fmaf(a, v.w, y.w);
+            }
+            reinterpret_cast<float4 *>(n)[0] = x;
+            reinterpret_cast<float4 *>(n)[1] = y;
+        }
+        *reinterpret_cast<float4 *>(&E[s & 1][key][0]) = x;
+        *reinterpret_cast<float4 *>(&E[s & 1][key][4]) = y;
+        __syncthreads();
+    }
+}
+
+}  // namespace join
+
 // [tokens][heads][128] bf16 with a token stride; boxes of 64 channels x 1 head x 64 tokens
 bool encode_heads(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int heads, int64_t stride) {
     const cuuint64_t dims[3] = {DK, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
@@ -736,27 +991,88 @@ bool encode_heads(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int he
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, 3, dims, strides, box);
 }
 
+// The shortest cut worth a try, an SM's share of all chunks; 0 where no sequence can be longer, or there is one, as fast whole.
+int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
+    const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
+    int64_t len = (all + sms - 1) / sms;
+    if (len < 4) len = 4;
+    if (longest <= len) return 0;
+    if (N == 1) {
+        auto time = [&](int cut) {
+            plan::Work out{0, 0, 0, 0}, states{0, 0, 0, 0};
+            int most = 0;
+            plan::add_sequence(out, states, most, static_cast<int>(longest), cut);
+            return plan::time_of(out, states, most, static_cast<int>(H), sms);
+        };
+        bool pays = false;
+        for (int i = 0; i < plan::CUTS; ++i) pays |= time(plan::cut_length(i, static_cast<int>(len))) < time(0x7fffffff);
+        if (!pays) return 0;
+    }
+    return static_cast<int>(len);
+}
+
+struct Layout {
+    int64_t slots, segs, cuts;  // of chunks; parts: ceil(c / L) <= c' / L + 1 summed over the sequences; cuts: (c - 1) / L
+    size_t images, seg, seg_s, cut, states, bytes;
+};
+Layout layout_of(int64_t N, int64_t T, int64_t H, int shortest) {
+    Layout l;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.slots = T / C + N;
+    l.cuts = shortest ? T / (static_cast<int64_t>(C) * shortest) : 0;
+    l.segs = N + l.cuts;
+    l.images = 256;
+    l.seg = up(l.images + static_cast<size_t>(l.slots * H) * IMAGE);
+    l.seg_s = up(l.seg + sizeof(Segment) * l.segs);
+    l.cut = up(l.seg_s + sizeof(Segment) * 2 * l.cuts);
+    l.states = up(l.cut + sizeof(Cuts) * l.cuts);
+    l.bytes = l.states + sizeof(float) * 2 * DK * DV * static_cast<size_t>(l.cuts * H);
+    return l;
+}
+
 }  // namespace
 
-size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) { return static_cast<size_t>((T / C + N) * H) * IMAGE; }
+size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
+    const int sms = sm_count();
+    return sms < 1 ? 0 : layout_of(N, T, H, shortest_cut(N, T, H, sms)).bytes;
+}
 
 cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream) {
     if (a.T < 1) return launch_recurrent(a, stream);  // (states pass through)
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
     ChunkParams p{};
     p.a = a;
-    p.images = static_cast<unsigned char *>(workspace);
-    p.slots = a.T / C + a.N;
     const int hk = a.H / a.rep;
     if (!encode_heads(&p.tq, a.q, a.T, hk, a.qs) || !encode_heads(&p.tk, a.k, a.T, hk, a.ks) ||
         !encode_heads(&p.tv, a.v, a.T, a.H, a.vs))
         return cudaErrorInvalidValue;
+    p.shortest = shortest_cut(a.N, a.T, a.H, sms);
+    const Layout l = layout_of(a.N, a.T, a.H, p.shortest);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    p.counts = reinterpret_cast<int32_t *>(ws);
+    p.images = ws + l.images;
+    p.slots = l.slots;
+    p.sms = sms;
+    p.most_segs = static_cast<int32_t>(l.segs);
+    p.most_cuts = static_cast<int32_t>(l.cuts);
+    p.segs = reinterpret_cast<Segment *>(ws + l.seg);
+    p.segs_s = reinterpret_cast<Segment *>(ws + l.seg_s);
+    p.cuts = reinterpret_cast<Cuts *>(ws + l.cut);
+    p.states = reinterpret_cast<float *>(ws + l.states);
     cudaError_t e = cudaFuncSetAttribute(prep::kda_gated_delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, prep::SMEM);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(walk::kda_gated_delta_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, walk::SMEM);
+    e = cudaFuncSetAttribute(walk::kda_gated_delta_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk::SMEM);
     if (e != cudaSuccess) return e;
-    prep::kda_gated_delta_prepare_kernel<<<static_cast<unsigned>(p.slots * a.H), prep::THREADS, prep::SMEM, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    walk::kda_gated_delta_chunk_kernel<<<static_cast<unsigned>(a.N) * a.H, walk::THREADS, walk::SMEM, stream>>>(p);
+    prep::kda_gated_delta_prepare_kernel<<<static_cast<unsigned>(1 + l.slots * a.H), prep::THREADS, prep::SMEM, stream>>>(p);
+    if (p.shortest) {
+        e = cudaFuncSetAttribute(walk::kda_gated_delta_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk::SMEM);
+        if (e != cudaSuccess) return e;
+        walk::kda_gated_delta_chunk_kernel<true><<<static_cast<unsigned>(2 * l.cuts * a.H), walk::THREADS, walk::SMEM, stream>>>(p);
+        const int64_t joined = l.cuts < a.N ? l.cuts : a.N;
+        join::kda_gated_delta_join_kernel<<<static_cast<unsigned>(joined * a.H * join::PARTS), join::THREADS, 0, stream>>>(p);
+    }
+    walk::kda_gated_delta_chunk_kernel<false><<<static_cast<unsigned>(l.segs * a.H), walk::THREADS, walk::SMEM, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -257,6 +257,24 @@ def test_prompt_in_place_on_slices_and_another_stream():
     assert torch.equal(o, want[0]) and torch.equal(d["s0"], want[1])
 
 
+def test_cut_sequences_with_states_in_place():
+    """Long sequences in parts, beside short and empty ones; the state's buffer updated. The last part of a sequence may end before the
+    first begins: it must not find the final state."""
+    for lens, H in (([3000, 40, 0, 1700], 2), ([64 * 5, 6000], 1), ([9000], 4)):
+        x = make(lens, H, H, seed=55, rate=0.1)
+        d = dev(x)
+        want = kda.gated_delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["cu"], d["s0"], check=True)
+        check(x, *want)
+        o = torch.empty_like(d["v"])
+        kda.kda_gated_delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["cu"], d["s0"], x["scale"], o, d["s0"])
+        assert torch.equal(o, want[0]) and torch.equal(d["s0"], want[1])
+    x = make([5000, 30], 2, 2, seed=56, state=False, rate=0.1)
+    check(x, *chunk(x))
+    o, fs = chunk(x, output_final_state=False)
+    assert fs is None
+    check(x, o, None)
+
+
 def test_bad_lengths_are_skipped():
     """cu_seqlens that run backwards or past the rows: reported, the other sequences are right."""
     x = make([100, 50, 80], 2, 2, seed=36, extra=20)
