@@ -55,6 +55,10 @@ __device__ __forceinline__ uint64_t evict_normal() {  // (the second launch read
     return p;
 }
 
+// A launch may be set up while the one before ends: what that one wrote is read behind this.
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A part of a sequence that a CTA walks: chunks c0 .. c0 + len - 1 of sequence n.
 struct Segment {
     int32_t n, c0, len;
@@ -325,6 +329,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     unsigned char *img = smem + OFF_IMG;
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    let_next_launch();
     if (blockIdx.x == 0) {
         plan::make(cp, reinterpret_cast<plan::Shared *>(smem));
         return;
@@ -684,14 +689,6 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int job = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H), hk = h / p.rep;
-    if (job >= cp.counts[STATES ? 1 : 0]) return;
-    const Segment seg = (STATES ? cp.segs_s : cp.segs)[job];
-    const bool is_map = STATES && seg.kind == 2;
-    const int64_t chain = static_cast<int64_t>(seg.n) * p.H + h;
-    const int64_t begin = p.cu[seg.n], bos = begin + static_cast<int64_t>(seg.c0) * C, eos = p.cu[seg.n + 1];  // from the segment on
-    const int chunks = seg.len;
-
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], WARPS + 1);
         for (int i = 0; i < 2; ++i) mbar_init(&m->s[i], WARPS / 2);
@@ -700,6 +697,16 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
         m->abort = 0;
         mbar_fence_init();
     }
+    const int job = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H), hk = h / p.rep;
+    wait_for_launch();
+    let_next_launch();
+    if (job >= cp.counts[STATES ? 1 : 0]) return;
+    const Segment seg = (STATES ? cp.segs_s : cp.segs)[job];  // (the plan's)
+    const bool is_map = STATES && seg.kind == 2;
+    const int64_t chain = static_cast<int64_t>(seg.n) * p.H + h;
+    const int64_t begin = p.cu[seg.n], bos = begin + static_cast<int64_t>(seg.c0) * C, eos = p.cu[seg.n + 1];  // from the segment on
+    const int chunks = seg.len;
+
     if (warp == WARP_MMA) tmem_alloc(&m->tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -941,43 +948,83 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 // ------------------------------------------------------------------ between the passes: the states that the parts begin with
 namespace join {
 
-constexpr int COLS = 8, PARTS = DV / COLS, THREADS = DK;
+constexpr int COLS = 8, PARTS = DV / COLS;
+constexpr int KEYS = 2, SHARES = 8, SHARE = DK / SHARES, THREADS = DK / KEYS * SHARES;
 
 // After a cut, E = F E' + N, with E' the state after the cut before, F the map of the part between them and N its state from zero. One
-// CTA has 8 value columns of a sequence and head, a thread a key: fp32 throughout, the sums in one order.
+// CTA has 8 value columns of a sequence and head; a thread two keys and an eighth of the sum's terms, whose factors it loads a cut
+// ahead. fp32 throughout, the sums in one order. Bound by latency: one cut waits for the one before.
 __global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __grid_constant__ ChunkParams cp) {
-    __shared__ alignas(16) float E[2][DK][COLS];
-    const int part = blockIdx.x % PARTS, h = static_cast<int>(blockIdx.x / PARTS % cp.a.H), key = threadIdx.x;
+    __shared__ alignas(16) float E[DK][COLS], sums[SHARES][DK][COLS];
+    const int part = blockIdx.x % PARTS, h = static_cast<int>(blockIdx.x / PARTS % cp.a.H);
+    const int key = threadIdx.x % (DK / KEYS), share = threadIdx.x / (DK / KEYS);  // keys key and key + 64
     const int64_t i = blockIdx.x / PARTS / cp.a.H;
+    wait_for_launch();
+    let_next_launch();
     if (i >= cp.counts[2]) return;
     const Cuts cuts = cp.cuts[i];
     constexpr size_t STATE = DK * DV;
+    const size_t step = 2 * STATE * cp.a.H;
     float *at = cp.states + (static_cast<size_t>(cuts.first) * cp.a.H + h) * 2 * STATE;
-    if (const float *s0 = cp.a.s0) {
-        s0 += (static_cast<int64_t>(cuts.n) * cp.a.H + h) * STATE + key * DV + COLS * part;
-        float4 *copy = reinterpret_cast<float4 *>(at + STATE + key * DV + COLS * part);
-        copy[0] = reinterpret_cast<const float4 *>(s0)[0];
-        copy[1] = reinterpret_cast<const float4 *>(s0)[1];
-    }
-    for (int s = 0; s < cuts.count; ++s, at += 2 * STATE * cp.a.H) {
-        float *n = at + key * DV + COLS * part;
-        float4 x = reinterpret_cast<const float4 *>(n)[0], y = reinterpret_cast<const float4 *>(n)[1];
-        if (s > 0) {
-            const float *f = at + STATE + key;
-            const float(&e)[DK][COLS] = E[(s - 1) & 1];
-#pragma unroll 16
-            for (int j = 0; j < DK; ++j) {
-                const float a = __ldcg(f + j * DK);
-                const float4 u = *reinterpret_cast<const float4 *>(&e[j][0]), v = *reinterpret_cast<const float4 *>(&e[j][4]);
-                x.x = fmaf(a, u.x, x.x), x.y = fmaf(a, u.y, x.y), x.z = fmaf(a, u.z, x.z), x.w = fmaf(a, u.w, x.w);
-                y.x = fmaf(a, v.x, y.x), y.y = fmaf(a, v.y, y.y), y.z = fmaf(a, v.z, y.z), y.w = fmaf(a, v.w, y.w);
-            }
-            reinterpret_cast<float4 *>(n)[0] = x;
-            reinterpret_cast<float4 *>(n)[1] = y;
-        }
-        *reinterpret_cast<float4 *>(&E[s & 1][key][0]) = x;
-        *reinterpret_cast<float4 *>(&E[s & 1][key][4]) = y;
+    const int mk = threadIdx.x / 4, mc = 2 * (threadIdx.x % 4);  // this thread's two columns of E and N
+    const size_t mine = static_cast<size_t>(mk) * DV + COLS * part + mc;
+    if (const float *s0 = cp.a.s0)
+        *reinterpret_cast<float2 *>(at + STATE + mine) =
+            *reinterpret_cast<const float2 *>(s0 + (static_cast<int64_t>(cuts.n) * cp.a.H + h) * STATE + mine);
+    float f[KEYS][SHARE], ahead[KEYS][SHARE];
+    float2 n = *reinterpret_cast<const float2 *>(at + mine), n_ahead;
+    auto load = [&](const float *state) {
+        n_ahead = *reinterpret_cast<const float2 *>(state + mine);
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j)
+#pragma unroll
+            for (int k = 0; k < KEYS; ++k) ahead[k][j] = __ldcg(state + STATE + (SHARE * share + j) * DK + key + k * (DK / KEYS));
+    };
+    if (cuts.count > 1) load(at + step);
+    *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
+#pragma unroll 1
+    for (int s = 1; s < cuts.count; ++s) {
+        at += step;
+        n = n_ahead;
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j)
+#pragma unroll
+            for (int k = 0; k < KEYS; ++k) f[k][j] = ahead[k][j];
+        if (s + 1 < cuts.count) load(at + step);
         __syncthreads();
+        f2 x[KEYS][COLS / 2];
+#pragma unroll
+        for (int k = 0; k < KEYS; ++k)
+#pragma unroll
+            for (int c = 0; c < COLS / 2; ++c) x[k][c] = 0;
+#pragma unroll
+        for (int j = 0; j < SHARE; ++j) {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][0]);
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][4]);
+#pragma unroll
+            for (int k = 0; k < KEYS; ++k) {
+                const f2 a = pair(f[k][j], f[k][j]);
+                x[k][0] = lin::fma2(a, u.x, x[k][0]);
+                x[k][1] = lin::fma2(a, u.y, x[k][1]);
+                x[k][2] = lin::fma2(a, v.x, x[k][2]);
+                x[k][3] = lin::fma2(a, v.y, x[k][3]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KEYS; ++k) {
+            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(&sums[share][key + k * (DK / KEYS)][0]);
+            to[0] = make_ulonglong2(x[k][0], x[k][1]);
+            to[1] = make_ulonglong2(x[k][2], x[k][3]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < SHARES; ++r) {
+            const float2 u = *reinterpret_cast<const float2 *>(&sums[r][mk][mc]);
+            n.x += u.x;
+            n.y += u.y;
+        }
+        *reinterpret_cast<float2 *>(at + mine) = n;
+        *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
     }
 }
 
@@ -1030,6 +1077,25 @@ Layout layout_of(int64_t N, int64_t T, int64_t H, int shortest) {
     return l;
 }
 
+// `after`: its CTAs may be set up while the launch before ends (they wait for it before they read what it wrote).
+cudaError_t launch(void (*kernel)(ChunkParams), int64_t ctas, int threads, int smem, bool after, const ChunkParams &p, cudaStream_t stream) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace
 
 size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
@@ -1060,20 +1126,14 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.segs_s = reinterpret_cast<Segment *>(ws + l.seg_s);
     p.cuts = reinterpret_cast<Cuts *>(ws + l.cut);
     p.states = reinterpret_cast<float *>(ws + l.states);
-    cudaError_t e = cudaFuncSetAttribute(prep::kda_gated_delta_prepare_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, prep::SMEM);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(walk::kda_gated_delta_chunk_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk::SMEM);
-    if (e != cudaSuccess) return e;
-    prep::kda_gated_delta_prepare_kernel<<<static_cast<unsigned>(1 + l.slots * a.H), prep::THREADS, prep::SMEM, stream>>>(p);
-    if (p.shortest) {
-        e = cudaFuncSetAttribute(walk::kda_gated_delta_chunk_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, walk::SMEM);
-        if (e != cudaSuccess) return e;
-        walk::kda_gated_delta_chunk_kernel<true><<<static_cast<unsigned>(2 * l.cuts * a.H), walk::THREADS, walk::SMEM, stream>>>(p);
+    cudaError_t e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H, prep::THREADS, prep::SMEM, false, p, stream);
+    if (e == cudaSuccess && p.shortest) {
+        e = launch(walk::kda_gated_delta_chunk_kernel<true>, 2 * l.cuts * a.H, walk::THREADS, walk::SMEM, true, p, stream);
         const int64_t joined = l.cuts < a.N ? l.cuts : a.N;
-        join::kda_gated_delta_join_kernel<<<static_cast<unsigned>(joined * a.H * join::PARTS), join::THREADS, 0, stream>>>(p);
+        if (e == cudaSuccess) e = launch(join::kda_gated_delta_join_kernel, joined * a.H * join::PARTS, join::THREADS, 0, true, p, stream);
     }
-    walk::kda_gated_delta_chunk_kernel<false><<<static_cast<unsigned>(l.segs * a.H), walk::THREADS, walk::SMEM, stream>>>(p);
-    return cudaGetLastError();
+    return e == cudaSuccess ? launch(walk::kda_gated_delta_chunk_kernel<false>, l.segs * a.H, walk::THREADS, walk::SMEM, true, p, stream)
+                            : e;
 }
 
 }  // namespace delta
