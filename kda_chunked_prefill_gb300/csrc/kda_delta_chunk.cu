@@ -285,6 +285,15 @@ __device__ __forceinline__ int find_sequence(const Params &p, int64_t slot, int 
     return lo;
 }
 
+// A sum in two terms, the second what the first leaves.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const float s = a.hi + b.hi, t = s - a.hi;
+    const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo), hi = s + e;
+    return {hi, e - (hi - s)};
+}
 // 2^(x + y), |y| far below 1
 __device__ __forceinline__ float ex2_2(float x, float y) { return ex2(x) * fmaf(y, 0.6931471805599453f, 1.f); }
 // 2^(a - b)
@@ -358,10 +367,13 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
             lin::tma_load_3d(smem + OFF_Q + c * TILE, &cp.tq, 64 * c, hk, static_cast<int>(t0), &m->full, keep);
         }
     }
+    __syncthreads();  // (the barrier is set up)
     float decays[4];  // of tokens 2 lane, 2 lane + 1: to the token, after it (warp 0)
     float whole = 0.f, less = 0.f;
-    if (warp == 0) {  // log2 decays, summed in 64 bits: differences of far sums keep their last bits
-        double x[2];
+    if (warp == 0) {
+        // log2 decays, summed in two fp32 terms: differences of far sums keep their last bits. (In 64 bits, floating or fixed point, the
+        // sums took two to three times as long, and every warp waits for them.) Below -138 a gate counts as -inf: 2^-200 is 0 in fp32.
+        Two x[2];
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -369,46 +381,39 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
             const float g = t < left ? p.g[(t0 + t) * p.H + h] : 0.f;
             m->beta[t] = t < left ? p.beta[(t0 + t) * p.H + h] : 0.f;
             bad |= !(g <= 0.f);
-            x[i] = (g < -138.f ? -200.0 : static_cast<double>(g) * 1.4426950408889634);  // (2^-200 is 0 in fp32)
+            const float y = g * LOG2E;
+            x[i] = g < -138.f ? Two{-200.f, 0.f} : Two{y, fmaf(g, LOG2E, -y) + g * 1.925963e-8f};  // (log2 e beyond LOG2E)
         }
-        double s = x[0] + x[1];
+        Two s = add(x[0], x[1]);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, d);
-            if (lane >= d) s += y;
+            const Two y{__shfl_up_sync(0xffffffffu, s.hi, d), __shfl_up_sync(0xffffffffu, s.lo, d)};
+            if (lane >= d) s = add(s, y);
         }
-        const double end = __shfl_sync(0xffffffffu, s, 31);
+        const Two end{__shfl_sync(0xffffffffu, s.hi, 31), __shfl_sync(0xffffffffu, s.lo, 31)};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const double gt = i ? s : s - x[1], rest = end - gt;
-            const float hi = static_cast<float>(gt), lo = static_cast<float>(gt - hi), rhi = static_cast<float>(rest);
-            m->G[2 * lane + i] = make_float2(hi, lo);
-            decays[i] = ex2_2(hi, lo);
-            decays[2 + i] = ex2_2(rhi, static_cast<float>(rest - rhi));
+            const Two gt = i ? s : add(s, {-x[1].hi, -x[1].lo}), rest = add(end, {-gt.hi, -gt.lo});
+            m->G[2 * lane + i] = make_float2(gt.hi, gt.lo);
+            decays[i] = ex2_2(gt.hi, gt.lo);
+            decays[2 + i] = ex2_2(rest.hi, rest.lo);
         }
-        const float hi = static_cast<float>(end), lo = static_cast<float>(end - hi);
-        whole = ex2_2(hi, lo);
-        less = expm1f(static_cast<float>(end * 0.6931471805599453));
+        whole = ex2_2(end.hi, end.lo);
+        less = expm1f((end.hi + end.lo) * 0.6931471805599453f);
         if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, KDA_ERR_GATE_RANGE);
-    }
-    __syncthreads();  // (the barrier is set up, G is there)
-    {                 // decays between blocks, in two factors that meet at the row's block
+        __syncwarp();
+        // decays between blocks, in two factors that meet at the row's block
         const float2 zero = make_float2(0.f, 0.f);
-        for (int i = tid; i < C + SB * 6; i += THREADS) {
-            if (i < C) {
-                m->row[i] = ex2_diff(m->G[i], i >= SB ? m->G[(i & ~(SB - 1)) - 1] : zero);
-            } else {
-                const int e = i - C, b = e < SB ? 0 : e < 3 * SB ? 1 : 2, j = e - (b == 0 ? 0 : b == 1 ? SB : 3 * SB);
-                m->col[b][j] = ex2_diff(m->G[SB * (b + 1) - 1], m->G[j]);
-            }
+#pragma unroll
+        for (int i = 0; i < C; i += 32) m->row[i + lane] = ex2_diff(m->G[i + lane], i + lane >= SB ? m->G[((i + lane) & ~(SB - 1)) - 1] : zero);
+#pragma unroll
+        for (int i = 0; i < 6 * SB; i += 32) {
+            const int e = i + lane, b = e < SB ? 0 : e < 3 * SB ? 1 : 2, j = e - (b == 0 ? 0 : b == 1 ? SB : 3 * SB);
+            m->col[b][j] = ex2_diff(m->G[SB * (b + 1) - 1], m->G[j]);
         }
     }
     bool here = false;
     for (int i = 0; i < 200000 && !here; ++i) here = lin::mbar_wait_some(&m->full, 0);
-    if (!__syncthreads_and(here)) {  // (never: the copies end at the latest with the kernel)
-        if (tid == 0) set_status(p.status, KDA_ERR_TIMEOUT);
-        return;
-    }
 
     // rows 16 w .. of K K^T and Q K^T, up to the diagonal
     const int w = warp, g = lane >> 2, q2 = 2 * (lane & 3);
@@ -433,6 +438,11 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
             mma16816(sq[2 * j], c, b[0], b[1]);
             mma16816(sq[2 * j + 1], c, b[2], b[3]);
         }
+    }
+    // (the copies end at the latest with the kernel: never false)
+    if (!__syncthreads_and(here)) {
+        if (tid == 0) set_status(p.status, KDA_ERR_TIMEOUT);
+        return;
     }
     const int i0 = SB * w + g;
     const float bi[2] = {m->beta[i0], m->beta[i0 + 8]};
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
             to_left(P[j], sq[2 * j], sq[2 * j + 1]);
         }
     }
-    __syncthreads();  // (k and q have been read: what leaves goes over them)
+    // (k and q have been read: what leaves goes over them)
     Left D;           // -T_ww
     {
         float *a = m->diag[w];
@@ -518,10 +528,12 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
             }
         }
         to_left(D, t[0], t[1]);
-        for (int c = 2 * w + 2; c < 2 * BLOCKS; ++c) {  // above the diagonal: zeros
-            const int tile = lane < 16 ? OFF_T : OFF_TLO;
-            *reinterpret_cast<uint4 *>(img + tile + swz(SB * w + (lane & 15), c)) = make_uint4(0, 0, 0, 0);
-            if (lane < 16) *reinterpret_cast<uint4 *>(img + OFF_PT + swz(SB * w + lane, c)) = make_uint4(0, 0, 0, 0);
+    }
+    {  // above the diagonal blocks: zeros
+        const int r = tid & (C - 1), second = tid / C;
+        for (int c = 2 * (r / SB) + 2; c < 2 * BLOCKS; ++c) {
+            *reinterpret_cast<uint4 *>(img + (second ? OFF_TLO : OFF_T) + swz(r, c)) = make_uint4(0, 0, 0, 0);
+            if ((c & 1) == second) *reinterpret_cast<uint4 *>(img + OFF_PT + swz(r, c)) = make_uint4(0, 0, 0, 0);
         }
     }
     if (warp == 0) {
@@ -593,13 +605,11 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
                 *reinterpret_cast<uint32_t *>(img + OFF_PT + swz(i0 + 8 * c, 2 * j + u) + 2 * q2) =
                     pack_bf16(t[u][2 * c], t[u][2 * c + 1]);
     }
-    fence_proxy_async_shared();
     __syncthreads();
-    if (tid == 0) {
-        bulk_s2g(cp.images + (slot * p.H + h) * IMAGE, img, IMAGE);
-        bulk_commit();
-        bulk_wait_read();
-    }
+    // (by all threads: a bulk copy would hold the CTA for 2000 cycles more)
+    uint4 *to = reinterpret_cast<uint4 *>(cp.images + (slot * p.H + h) * IMAGE);
+#pragma unroll 4
+    for (int i = tid; i < IMAGE / 16; i += THREADS) to[i] = reinterpret_cast<const uint4 *>(img)[i];
 }
 
 }  // namespace prep
