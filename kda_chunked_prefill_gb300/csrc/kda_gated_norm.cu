@@ -3,11 +3,12 @@
 //
 //     n = x / sqrt(mean(x^2) + eps) * w * act(gate);  y_scale = max|n| / 448;  y = e4m3(n / y_scale)
 //
-// Sum and maximum come from one reduction: max|n| = max|x w act(gate)| / sqrt(mean(x^2) + eps), so a row is read once and
-// stays in registers. Sixteen lanes take a row, eight channels each (one 16-byte access of x, gate and, half as wide, y); the
-// weight's eight values stay in registers for the two rows that a half warp takes.
+// Sum and maximum come from one reduction: with m = x w act(gate), the codes are e4m3(m 448 / max|m|) and the scale is max|m| / sqrt(
+// mean(x^2) + eps) / 448, so a row is read once and stays in registers. Sixteen lanes take a row, eight channels each (one 16-byte
+// access of x, gate and, half as wide, y); the weight's eight values stay in registers for the two rows that a half warp takes.
 //
-// Bound by memory: 5 bytes per channel with bf16 x (2 + 2 in, 1 out), 7 with fp32.
+// Bound by memory: 5 bytes per channel with bf16 x (2 + 2 in, 1 out), 7 with fp32. The sigmoid is the hardware's 2^x and reciprocal (a
+// few units in the last place; expf and an IEEE division made the kernel wait for its instructions, 53 an element).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,11 +46,18 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
-template <typename X>
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// STRIDED: the gate's tokens lie gate_stride elements apart; otherwise like x.
+template <typename X, bool STRIDED, bool SILU>
 __global__ void __launch_bounds__(THREADS)
     kda_gated_rms_norm_kernel(const X *__restrict__ x, const __nv_bfloat16 *__restrict__ gate, int64_t gate_stride,
-                              const float *__restrict__ weight, int64_t rows, int32_t heads, float eps, bool silu,
-                              uint8_t *__restrict__ y, float *__restrict__ y_scale) {
+                              const float *__restrict__ weight, int32_t rows, int32_t heads, float eps, uint8_t *__restrict__ y,
+                              float *__restrict__ y_scale) {
     const int c = 8 * (threadIdx.x & 15);
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * CTA_ROWS + threadIdx.x / 16;
     float w[8], v[ROWS][8], g[ROWS][8];
@@ -60,9 +68,13 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = g[i][j] = 0.f;
         if (row >= rows) continue;
-        const int64_t t = row / heads;
         load8(x + row * DV + c, v[i]);
-        load8(gate + t * gate_stride + (row - t * heads) * DV + c, g[i]);
+        int64_t at = row * DV;
+        if (STRIDED) {
+            const uint32_t t = static_cast<uint32_t>(row) / static_cast<uint32_t>(heads);
+            at = t * gate_stride + static_cast<int64_t>(static_cast<uint32_t>(row) - t * heads) * DV;
+        }
+        load8(gate + at + c, g[i]);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -71,8 +83,8 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             sum = fmaf(v[i][j], v[i][j], sum);
-            const float sig = 1.f / (1.f + expf(-g[i][j]));
-            v[i][j] *= w[j] * (silu ? g[i][j] * sig : sig);
+            const float sig = rcp(1.f + ex2(g[i][j] * -LOG2E));  // (2^x infinite: closed)
+            v[i][j] *= w[j] * (SILU ? g[i][j] * sig : sig);
             mx = max_abs_nan(mx, v[i][j]);
         }
 #pragma unroll
@@ -81,18 +93,20 @@ __global__ void __launch_bounds__(THREADS)
             mx = max_abs_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
         }
         if (row >= rows) continue;  // (a whole half warp)
-        // (a sum that is not finite, by a NaN, an infinity or an overflow, marks the whole row)
-        const float rstd = sum <= 3.402823466e38f ? 1.f / sqrtf(sum / static_cast<float>(DV) + eps) : __int_as_float(0x7fc00000);
-        const float amax = max_abs_nan(0.f, mx * rstd);  // max|n|; NaN or infinite once anything in the row is
-        const bool tiny = amax < TINY;
-        float mul = tiny ? 0.f : rstd * (E4M3_MAX / amax);
-        if (mul > 3.402823466e38f) {  // small elements and a small eps: in two factors
+        // A sum that is not finite, by a NaN, an infinity or an overflow, marks the whole row; so does an infinite product.
+        const bool fine = sum <= 3.402823466e38f && mx <= 3.402823466e38f;
+        const float rstd = rsqrtf(sum * (1.f / DV) + eps), amax = fine ? mx * rstd : __int_as_float(0x7fc00000);
+        const bool good = amax <= 3.402823466e38f, tiny = amax < TINY;
+        float mul = E4M3_MAX * rcp(mx);
+        if (!(mx > 1e-30f && mx < 1e30f)) {  // where the quotient, or its reciprocal, is out of range: in two factors
+            const float first = mx < 1.f ? 0x1p80f : 0x1p-80f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
-            mul = E4M3_MAX / amax;
+            for (int j = 0; j < 8; ++j) v[i][j] *= first;
+            mul = E4M3_MAX / (mx * first);
         }
-        if (!(amax <= 3.402823466e38f)) mul = __int_as_float(0x7fc00000);
-        if (c == 0) y_scale[row] = tiny ? 0.f : amax <= 3.402823466e38f ? amax / E4M3_MAX : __int_as_float(0x7fc00000);
+        if (tiny) mul = 0.f;
+        if (!good) mul = __int_as_float(0x7fc00000);
+        if (c == 0) y_scale[row] = tiny ? 0.f : good ? amax * (1.f / E4M3_MAX) : mul;
         const uint32_t a = e4m3x4(v[i][0] * mul, v[i][1] * mul, v[i][2] * mul, v[i][3] * mul);
         const uint32_t b = e4m3x4(v[i][4] * mul, v[i][5] * mul, v[i][6] * mul, v[i][7] * mul);
         *reinterpret_cast<uint2 *>(y + row * DV + c) = make_uint2(a, b);
@@ -100,10 +114,15 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 template <typename X>
-void launch(const X *x, const __nv_bfloat16 *gate, int64_t gs, const float *w, int64_t rows, int heads, float eps, bool silu,
+void launch(const X *x, const __nv_bfloat16 *gate, int64_t gs, const float *w, int rows, int heads, float eps, bool silu,
             uint8_t *y, float *ys, cudaStream_t s) {
-    const int grid = static_cast<int>((rows - 1) / CTA_ROWS + 1);
-    kda_gated_rms_norm_kernel<X><<<grid, THREADS, 0, s>>>(x, gate, gs, w, rows, heads, eps, silu, y, ys);
+    const int grid = (rows - 1) / CTA_ROWS + 1;
+    const bool strided = gs != static_cast<int64_t>(heads) * DV;
+    auto run = [&](auto kernel) { kernel<<<grid, THREADS, 0, s>>>(x, gate, gs, w, rows, heads, eps, y, ys); };
+    if (strided)
+        silu ? run(kda_gated_rms_norm_kernel<X, true, true>) : run(kda_gated_rms_norm_kernel<X, true, false>);
+    else
+        silu ? run(kda_gated_rms_norm_kernel<X, false, true>) : run(kda_gated_rms_norm_kernel<X, false, false>);
 }
 
 }  // namespace gatednorm
@@ -115,7 +134,7 @@ extern "C" kda_status_t kda_gated_rms_norm(const void *x, const void *gate, int6
     using kda::checks::aligned;
     if (head_dim_v != KDA_HEAD_DIM) return KDA_ERR_UNSUPPORTED;
     if (tokens < 0 || num_heads < 1 || (x_fp32 != 0 && x_fp32 != 1) || (silu != 0 && silu != 1)) return KDA_ERR_INVALID_ARG;
-    if (tokens > (int64_t{1} << 33) / num_heads) return KDA_ERR_UNSUPPORTED;  // (2^40 elements)
+    if (tokens > 0x7fffffffLL / num_heads) return KDA_ERR_UNSUPPORTED;
     if (!(eps > 0.f && eps < 3.0e38f)) return KDA_ERR_INVALID_ARG;
     if (gate_token_stride < static_cast<int64_t>(num_heads) * KDA_HEAD_DIM || gate_token_stride % 8) return KDA_ERR_INVALID_ARG;
     if (tokens == 0) return KDA_OK;
@@ -125,7 +144,7 @@ extern "C" kda_status_t kda_gated_rms_norm(const void *x, const void *gate, int6
         return KDA_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const auto *gb = static_cast<const __nv_bfloat16 *>(gate);
-    const int64_t rows = tokens * num_heads;
+    const int rows = static_cast<int>(tokens * num_heads);
     if (x_fp32)
         kda::gatednorm::launch(static_cast<const float *>(x), gb, gate_token_stride, weight, rows, num_heads, eps, silu != 0,
                                static_cast<uint8_t *>(y), y_scale, s);

@@ -28,12 +28,8 @@
 namespace kda {
 namespace mm {
 
-using lin::f2;
-using lin::fma2;
 using lin::mbar_arrive;
 using lin::mbar_wait_some;
-using lin::pair;
-using lin::split;
 
 constexpr int LANES = 128;  // of an accumulator
 constexpr int KB = 128;     // channels of a block: a row of a stage's tile is 128 bytes
@@ -143,7 +139,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 }
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[8]) { tmem_ld8(t, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[16]) { tmem_ld16(t, r); }
-__device__ __forceinline__ void tmem_ld(uint32_t t, uint32_t (&r)[32]) { lin::tmem_ld32(t, r); }
 __device__ __forceinline__ void cluster_sync() {  // all threads of the cluster's CTAs
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -284,15 +279,15 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         const int e = warp - FIRST_SUM_WARP, quad = warp & 3, half = e >> 2;
         const int my_lane = 32 * quad + lane, col0 = half * C::COLS;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + col0;
-        constexpr int LD = C::COLS < 16 ? C::COLS : C::CTAS == 2 ? 16 : 32;  // columns read at a time
+        constexpr int LD = C::COLS < 16 ? C::COLS : 16;  // columns read at a time
         uint32_t it = 0;
         bool ok = true;
         for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
             int lt, ct;
             tile_at(p, tile, lt, ct);
-            f2 acc[C::COLS / 2];
+            float acc[C::COLS];
 #pragma unroll
-            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < C::COLS; ++i) acc[i] = 0.f;
             for (int b = b0; b < b1; ++b, ++it) {
                 const uint32_t buf = it & 1, slot = it % SCALES;
                 if (!(ok = wait_warp(m, &m->sfull[slot], (it / SCALES) & 1) && wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
@@ -300,22 +295,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                 const float *s = scales + slot * C::SCALE_FLOATS;
                 float mine = 0.f;
                 if (!SWAP) mine = s[(col0 / KB) * LANES + my_lane];
-                const f2 mine2 = pair(mine, mine);
+                uint32_t d[2][LD];
+                tmem_ld(taddr + buf * BN, d[0]);
 #pragma unroll
-                for (int c = 0; c < C::COLS; c += LD) {
-                    uint32_t d[LD];
-                    tmem_ld(taddr + buf * BN + c, d);
+                for (int c = 0; c < C::COLS; c += LD) {  // (the next columns come while these are added)
+                    const uint32_t(&x)[LD] = d[c / LD & 1];
                     tmem_wait_ld();
+                    if (c + LD < C::COLS) tmem_ld(taddr + buf * BN + c + LD, d[c / LD + 1 & 1]);
 #pragma unroll
                     for (int i = 0; i < LD; i += 4) {
-                        f2 s0 = mine2, s1 = mine2;
-                        if (SWAP) {
-                            const float4 x = *reinterpret_cast<const float4 *>(s + col0 + c + i);
-                            s0 = pair(x.x, x.y);
-                            s1 = pair(x.z, x.w);
-                        }
-                        acc[(c + i) / 2] = fma2(pair(d[i], d[i + 1]), s0, acc[(c + i) / 2]);
-                        acc[(c + i) / 2 + 1] = fma2(pair(d[i + 2], d[i + 3]), s1, acc[(c + i) / 2 + 1]);
+                        float4 f = make_float4(mine, mine, mine, mine);
+                        if (SWAP) f = *reinterpret_cast<const float4 *>(s + col0 + c + i);
+                        acc[c + i] = fmaf(__uint_as_float(x[i]), f.x, acc[c + i]);
+                        acc[c + i + 1] = fmaf(__uint_as_float(x[i + 1]), f.y, acc[c + i + 1]);
+                        acc[c + i + 2] = fmaf(__uint_as_float(x[i + 2]), f.z, acc[c + i + 2]);
+                        acc[c + i + 3] = fmaf(__uint_as_float(x[i + 3]), f.w, acc[c + i + 3]);
                     }
                 }
                 tc_fence_before();
@@ -326,23 +320,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
             if (splits > 1) {  // (one tile a CTA; the stages are done with)
                 float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-                for (int i = 0; i < C::COLS / 2; ++i) {
-                    float x, y;
-                    split(acc[i], x, y);
-                    red[(col0 + 2 * i) * C::RED_LD + my_lane] = x;
-                    red[(col0 + 2 * i + 1) * C::RED_LD + my_lane] = y;
-                }
+                for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + my_lane] = acc[i];
             } else if (SWAP) {
                 const int64_t n = static_cast<int64_t>(lt) * LANES + my_lane;
 #pragma unroll
-                for (int i = 0; i < C::COLS / 2; ++i) {
-                    float v[2];
-                    split(acc[i], v[0], v[1]);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int64_t t = static_cast<int64_t>(ct) * BN + col0 + 2 * i + j;
-                        if (n < p.outs && t < p.rows) p.out[t * p.outs + n] = __float2bfloat16_rn(v[j]);
-                    }
+                for (int i = 0; i < C::COLS; ++i) {
+                    const int64_t t = static_cast<int64_t>(ct) * BN + col0 + i;
+                    if (n < p.outs && t < p.rows) p.out[t * p.outs + n] = __float2bfloat16_rn(acc[i]);
                 }
             } else {
                 // the warp's own 32 rows of y, as panels of PANEL columns, swizzled
@@ -353,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                 for (int c = 0; c < C::COLS; c += 8) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = lin::bf16_of(acc[c / 2 + j]);
+                    for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
                     *reinterpret_cast<uint4 *>(staging + C::staged(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 fence_proxy_async_shared();
