@@ -649,6 +649,7 @@ static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 // waits of up to 0.1 ms each before a role gives up; and before one that has given up takes its own copies for complete
 constexpr int WAITS = 20000, WAITS_DRAIN = 100;
 __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     int i = 0;
 #pragma unroll 1
     while (!lin::mbar_wait_some(bar, parity)) {
@@ -747,15 +748,16 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) wait_drain(&m->full[i % STAGES], (i / STAGES) & 1);
         }
     } else if (warp == WARP_MMA) {
-        // Issued by one thread, whose instructions count: descriptors by one addition each.
+        // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues.
         const uint32_t base = smem_u32(smem);
         constexpr uint32_t ID = lin::idesc_bf16(false, false, 128, 128), ID_64 = lin::idesc_bf16(false, false, 128, 64),
                            ID_U = lin::idesc_bf16(false, true, 128, 128);
         bool ok = true;
-        for (int it = 0; ok && it < chunks; ++it) {
-            const int st = it % STAGES;
+        uint32_t st = 0, use = 0;
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
             const uint32_t ph = it & 1, s = base + st * STAGE;
-            if (!(ok = wait_warp(m, &m->full[st], (it / STAGES) & 1))) break;
+            if (!(ok = wait_warp(m, &m->full[st], use & 1))) break;
             const int64_t left = eos - bos - static_cast<int64_t>(it) * C;
             if (left < C) {  // the rows of K behind are another sequence's, or anything: as zeros
                 unsigned char *kq = smem + st * STAGE + OFF_KQ;
@@ -766,45 +768,53 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 fence_proxy_async_shared();
                 __syncwarp();
             }
-            if (lane == 0) {
-                const uint64_t kq = umma_desc_sw128(s + OFF_KQ, 16, 1024), tt = umma_desc_sw128(s + OFF_TT, 16, 1024);
-                const uint64_t kt = umma_desc_sw128(s + OFF_KQ, PANEL, 1024);
-                // (additions to the address field: bytes / 16)
+            const uint64_t kq = umma_desc_sw128(s + OFF_KQ, 16, 1024), tt = umma_desc_sw128(s + OFF_TT, 16, 1024);
+            const uint64_t kt = umma_desc_sw128(s + OFF_KQ, PANEL, 1024);
+            // (additions to the address field: bytes / 16)
+            if (!(ok = wait_warp(m, &m->s[0], ph))) break;
+            tc_fence_after();
+            if (lin::elect_one()) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (!ok || !(ok = wait(m, &m->s[half], ph))) continue;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 4 * half; k < 4 * half + 4; ++k) {
-                        const uint64_t b = kq + ((k >> 2) * PANEL + (k & 3) * 32) / 16;
-                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 8 * k, b, ID, k > 0);
-                        lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 8 * k, b, ID, 1);
-                    }
-                }
-                if (ok) umma_commit(&m->ks);
-                if (ok && (ok = wait(m, &m->z, ph))) {
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + k * 2, ID, k > 0);
-                        lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k + 8, tt + k * 2, ID, 1);
-                        lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + (OFF_TL - OFF_TT) / 16 + k * 2, ID_64, 1);
-                    }
-                    umma_commit(&m->xs);
-                }
-                if (ok && (ok = wait(m, &m->x, ph))) {
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k, kt + k * 128, ID_U, k > 0);
-                        lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k + 8, kt + k * 128, ID_U, 1);
-                    }
-                    umma_commit(&m->u);
-                    umma_commit(&m->empty[st]);
+                for (int k = 0; k < 4; ++k) {
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 8 * k, kq + k * 2, ID, k > 0);
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 8 * k, kq + k * 2, ID, 1);
                 }
             }
-            ok = __all_sync(0xffffffffu, ok);
+            if (!(ok = wait_warp(m, &m->s[1], ph))) break;
+            tc_fence_after();
+            if (lin::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 32 + 8 * k, kq + PANEL / 16 + k * 2, ID, 1);
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 96 + 8 * k, kq + PANEL / 16 + k * 2, ID, 1);
+                }
+                umma_commit(&m->ks);
+            }
+            if (!(ok = wait_warp(m, &m->z, ph))) break;
+            tc_fence_after();
+            if (lin::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + k * 2, ID, k > 0);
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k + 8, tt + k * 2, ID, 1);
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + (OFF_TL - OFF_TT) / 16 + k * 2, ID_64, 1);
+                }
+                umma_commit(&m->xs);
+            }
+            if (!(ok = wait_warp(m, &m->x, ph))) break;
+            tc_fence_after();
+            if (lin::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k, kt + k * 128, ID_U, k > 0);
+                    lin::umma_ts(tmem + COL_U, tmem + COL_X + 16 * k + 8, kt + k * 128, ID_U, 1);
+                }
+                umma_commit(&m->u);
+                umma_commit(&m->empty[st]);
+            }
+            if (++st == STAGES) st = 0, ++use;
         }
+        __syncwarp();
         if (!ok && lane == 0) {
             umma_commit(&m->drained);
             wait_drain(&m->drained, 0);

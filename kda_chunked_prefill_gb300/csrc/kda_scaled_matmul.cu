@@ -8,14 +8,14 @@
 //
 // A CTA makes tiles of 128 lanes x BN columns of the accumulator. Roles:
 //   load    one thread: 128-byte wide tiles of both operands by TMA into a ring of stages
-//   MMAs    one thread
+//   MMAs    two threads, every second block each: waiting for its operands and issuing takes one as long as the tensor core
 //   scales  one warp: xs ws of each block, to shared memory, a few blocks ahead
 //   sums    eight warps: a lane and half of the columns each; then y
 //
 // Which operand takes the lanes. For more than 64 rows the rows of x do, columns are outputs: a thread needs one scale a block
 // (its 128 columns share the weight's), and y leaves by tiled stores. For up to 64 rows (decode) the weight's rows do and x's are
 // the columns, as few as 16: no lane of the tensor core idles, and the weight, which is what bounds these calls, is read by
-// as many CTAs as there are. Where tiles are fewer than the SMs, the CTAs of a cluster share a tile: each takes a part of the
+// as many CTAs as there are. Where these tiles are fewer than the SMs, the CTAs of a cluster share one: each takes a part of the
 // channels, and they add up their sums through distributed shared memory, in the order of their ranks.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,8 +35,8 @@ constexpr int LANES = 128;  // of an accumulator
 constexpr int KB = 128;     // channels of a block: a row of a stage's tile is 128 bytes
 constexpr int THREADS = 384;
 constexpr int SUM_WARPS = 8, FIRST_SUM_WARP = 4;
-constexpr int SCALES = 8;   // blocks' scales in shared memory
-constexpr int AHEAD = 4;    // of them loaded at a time
+constexpr int AHEAD = 4;    // blocks whose scales are loaded and handed on at a time (a wait a block for them was a third of the sums' time)
+constexpr int SCALES = 2;   // such groups in shared memory
 constexpr int MAX_SPLITS = 8;
 constexpr int SWAP_ROWS = 64;
 // waits of up to 0.1 ms each before a role gives up; and before one that has given up takes its own copies for complete
@@ -59,7 +59,7 @@ struct Cfg {
     static constexpr int RED_LD = LANES + 1;                   // a column of the sums that a cluster adds up
     static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
     static constexpr int OFF_STAGING = STAGES * STAGE, OFF_SCALES = OFF_STAGING + STAGING;
-    static constexpr int OFF_MISC = OFF_SCALES + SCALES * SCALE_FLOATS * 4;
+    static constexpr int OFF_MISC = OFF_SCALES + SCALES * AHEAD * SCALE_FLOATS * 4;
     // registers of the sums' warps and the others, where an even share is too few
     static constexpr bool UNEVEN = BN == 256;
     static constexpr int REGS_SUM = 208, REGS_AUX = 80, REGS = 168;
@@ -69,8 +69,8 @@ struct Cfg {
 struct Misc {
     uint64_t full[5], empty[5];              // a stage
     uint64_t tfull[2], tempty[2];            // an accumulator
-    uint64_t sfull[SCALES], sempty[SCALES];  // a block's scales
-    uint64_t drained;
+    uint64_t sfull[SCALES], sempty[SCALES];  // a group's scales
+    uint64_t drained[2];
     uint32_t tmem;
     int32_t abort;
 };
@@ -91,6 +91,7 @@ struct Params {
 };
 
 __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     int i = 0;
 #pragma unroll 1
     while (!mbar_wait_some(bar, parity)) {
@@ -105,6 +106,7 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
     }
 }
 __device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait(m, bar, parity));
 }
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         for (int i = 0; i < C::STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&m->tfull[i], 1), mbar_init(&m->tempty[i], SUM_WARPS);
         for (int i = 0; i < SCALES; ++i) mbar_init(&m->sfull[i], 1), mbar_init(&m->sempty[i], SUM_WARPS);
-        mbar_init(&m->drained, 1);
+        mbar_init(&m->drained[0], 1), mbar_init(&m->drained[1], 1);
         m->abort = 0;
         mbar_fence_init();
     }
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
     const uint32_t tmem = m->tmem;
 
     // this CTA's tiles, and its part of their blocks
-    const int splits = p.splits, rank = splits > 1 ? static_cast<int>(blockIdx.x) % splits : 0;
+    const int splits = SWAP ? p.splits : 1, rank = splits > 1 ? static_cast<int>(blockIdx.x) % splits : 0;
     const int64_t tile0 = blockIdx.x / splits, tile_step = gridDim.x / splits;
     const int b0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / splits);
     const int b1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / splits);
@@ -211,26 +213,37 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         if (!ok)  // what is in flight lands before the CTA ends
             for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
                 wait_drain(&m->full[i % C::STAGES], (i / C::STAGES) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 || warp == 3) {
+        // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues. Its instructions
+        // count: the sums' push them out of the first instruction cache.
         constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(LANES >> 4) << 24);
-        uint32_t it = 0;
+        const uint32_t buf = static_cast<uint32_t>(warp >> 1), d = tmem + buf * BN;
+        const uint64_t a0 = umma_desc_sw128(smem_u32(smem), 16, 1024);
+        const int64_t tiles = tile0 < p.tiles ? (p.tiles - 1 - tile0) / tile_step + 1 : 0;
+        const int64_t blocks = tiles * (b1 - b0);  // in all; every second is this thread's
+        uint32_t st = buf % C::STAGES, use = buf / C::STAGES, n = 0;
         bool ok = true;
-        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
-            for (int b = b0; b < b1; ++b, ++it) {
-                const uint32_t st = it % C::STAGES, buf = it & 1;
-                if (!(ok = wait(m, &m->full[st], (it / C::STAGES) & 1) && wait(m, &m->tempty[buf], ((it >> 1) & 1) ^ 1))) break;
-                tc_fence_after();
-                const uint32_t s = smem_u32(smem + st * C::STAGE);
-                const uint64_t da = umma_desc_sw128(s, 16, 1024), db = umma_desc_sw128(s + C::A_BYTES, 16, 1024);
+#pragma unroll 1
+        for (int64_t it = buf; it < blocks; it += 2, ++n) {
+            // In this order: that the sums are through with block it - 2, and so with every block before, says that this stage's
+            // last use, perhaps the other warp's, is over. Its parity alone would take the phase before last for this one.
+            if (!(ok = wait_warp(m, &m->tempty[buf], (n & 1) ^ 1) && wait_warp(m, &m->full[st], use & 1))) break;
+            tc_fence_after();
+            const uint64_t a = a0 + st * (C::STAGE / 16), b = a + C::A_BYTES / 16;
+            if (lin::elect_one()) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_e4m3(tmem + buf * BN, da + 2 * k, db + 2 * k, ID, k > 0);
+                for (int k = 0; k < 4; ++k) umma_e4m3(d, a + 2 * k, b + 2 * k, ID, k > 0);
                 umma_commit(&m->empty[st]);
                 umma_commit(&m->tfull[buf]);
             }
+            st += 2;
+            if (st >= C::STAGES) st -= C::STAGES, ++use;
         }
+        __syncwarp();
         if (!ok) {
-            umma_commit(&m->drained);
-            wait_drain(&m->drained, 0);
+            if (lin::elect_one()) umma_commit(&m->drained[buf]);
+            __syncwarp();
+            wait_drain(&m->drained[buf], 0);
         }
     } else if (warp == 2) {
         uint32_t it = 0;
@@ -257,20 +270,18 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                         ws[a][g] = out_block + g < out_blocks
                                        ? __ldg(p.ws + static_cast<int64_t>(out_block + g) * p.blocks + bb) : 0.f;
                 }
+                const uint32_t slot = it % SCALES;
+                if (!(ok = wait_warp(m, &m->sempty[slot], ((it / SCALES) & 1) ^ 1))) break;
+                float *s = scales + slot * (AHEAD * C::SCALE_FLOATS);
 #pragma unroll
-                for (int a = 0; a < AHEAD; ++a) {
-                    if (!ok || b + a >= b1) continue;
-                    const uint32_t slot = it % SCALES;
-                    if (!(ok = wait_warp(m, &m->sempty[slot], ((it / SCALES) & 1) ^ 1))) continue;
-                    float *s = scales + slot * C::SCALE_FLOATS;
+                for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
                     for (int g = 0; g < C::GROUPS; ++g)
 #pragma unroll
                         for (int i = 0; i < PER; ++i)
-                            if (!SWAP || BN >= 32 || lane < BN) s[g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
-                    arrive_warp(&m->sfull[slot]);
-                    ++it;
-                }
+                            if (!SWAP || BN >= 32 || lane < BN) s[a * C::SCALE_FLOATS + g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
+                arrive_warp(&m->sfull[slot]);
+                ++it;
             }
         }
     }
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         const int my_lane = 32 * quad + lane, col0 = half * C::COLS;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + col0;
         constexpr int LD = C::COLS < 16 ? C::COLS : 16;  // columns read at a time
-        uint32_t it = 0;
+        uint32_t it = 0, group = 0;
         bool ok = true;
         for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
             int lt, ct;
@@ -288,13 +299,22 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
             float acc[C::COLS];
 #pragma unroll
             for (int i = 0; i < C::COLS; ++i) acc[i] = 0.f;
+            float mine[AHEAD];
             for (int b = b0; b < b1; ++b, ++it) {
-                const uint32_t buf = it & 1, slot = it % SCALES;
-                if (!(ok = wait_warp(m, &m->sfull[slot], (it / SCALES) & 1) && wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
+                const uint32_t buf = it & 1, slot = group % SCALES, in = (b - b0) % AHEAD;
+                const float *s = scales + slot * (AHEAD * C::SCALE_FLOATS);
+                if (in == 0) {
+                    if (!(ok = wait_warp(m, &m->sfull[slot], (group / SCALES) & 1))) break;
+                    if (!SWAP) {
+#pragma unroll
+                        for (int a = 0; a < AHEAD; ++a) mine[a] = s[a * C::SCALE_FLOATS + (col0 / KB) * LANES + my_lane];
+                        arrive_warp(&m->sempty[slot]);
+                        ++group;
+                    }
+                }
+                if (!(ok = wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
                 tc_fence_after();
-                const float *s = scales + slot * C::SCALE_FLOATS;
-                float mine = 0.f;
-                if (!SWAP) mine = s[(col0 / KB) * LANES + my_lane];
+                const float one = in == 0 ? mine[0] : in == 1 ? mine[1] : in == 2 ? mine[2] : mine[3];
                 uint32_t d[2][LD];
                 tmem_ld(taddr + buf * BN, d[0]);
 #pragma unroll
@@ -304,8 +324,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                     if (c + LD < C::COLS) tmem_ld(taddr + buf * BN + c + LD, d[c / LD + 1 & 1]);
 #pragma unroll
                     for (int i = 0; i < LD; i += 4) {
-                        float4 f = make_float4(mine, mine, mine, mine);
-                        if (SWAP) f = *reinterpret_cast<const float4 *>(s + col0 + c + i);
+                        float4 f = make_float4(one, one, one, one);
+                        if (SWAP) f = *reinterpret_cast<const float4 *>(s + in * C::SCALE_FLOATS + col0 + c + i);
                         acc[c + i] = fmaf(__uint_as_float(x[i]), f.x, acc[c + i]);
                         acc[c + i + 1] = fmaf(__uint_as_float(x[i + 1]), f.y, acc[c + i + 1]);
                         acc[c + i + 2] = fmaf(__uint_as_float(x[i + 2]), f.z, acc[c + i + 2]);
@@ -314,10 +334,13 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                 }
                 tc_fence_before();
                 arrive_warp(&m->tempty[buf]);
-                if (lane == 0) mbar_arrive(&m->sempty[slot]);
+                if (SWAP && (in == AHEAD - 1 || b == b1 - 1)) {
+                    if (lane == 0) mbar_arrive(&m->sempty[slot]);
+                    ++group;
+                }
             }
             if (!ok) break;
-            if (splits > 1) {  // (one tile a CTA; the stages are done with)
+            if (SWAP && splits > 1) {  // (one tile a CTA; the stages are done with)
                 float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
                 for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + my_lane] = acc[i];
@@ -367,20 +390,25 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
 
     // (every thread comes here, one that has given up as well)
     __syncwarp();
-    if (splits > 1) {
+    if (SWAP && splits > 1) {
         cluster_sync();
         if (warp >= FIRST_SUM_WARP) {
             int lt, ct;
             tile_at(p, tile0, lt, ct);
             const int c0 = BN * rank / splits, n = BN * (rank + 1) / splits - c0;
             const uint32_t red = smem_u32(smem);
+#pragma unroll 4
             for (int i = threadIdx.x - 32 * FIRST_SUM_WARP; i < n * LANES; i += 32 * SUM_WARPS) {
-                const int c = c0 + (SWAP ? i / LANES : i % n), l = SWAP ? i % LANES : i / n;
-                const int64_t t = SWAP ? static_cast<int64_t>(ct) * BN + c : static_cast<int64_t>(lt) * LANES + l;
-                const int64_t o = SWAP ? static_cast<int64_t>(lt) * LANES + l : static_cast<int64_t>(ct) * BN + c;
+                const int c = c0 + i / LANES, l = i % LANES;
+                const int64_t t = static_cast<int64_t>(ct) * BN + c, o = static_cast<int64_t>(lt) * LANES + l;
                 if (t >= p.rows || o >= p.outs) continue;
-                float s = 0.f;
-                for (int r = 0; r < splits; ++r) s += ld_cluster(red + 4 * (c * C::RED_LD + l), r);
+                float part[MAX_SPLITS], s = 0.f;
+#pragma unroll
+                for (int r = 0; r < MAX_SPLITS; ++r)
+                    if (r < splits) part[r] = ld_cluster(red + 4 * (c * C::RED_LD + l), r);
+#pragma unroll
+                for (int r = 0; r < MAX_SPLITS; ++r)
+                    if (r < splits) s += part[r];
                 p.out[t * p.outs + o] = __float2bfloat16_rn(s);
             }
         }
@@ -398,7 +426,9 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
     using C = Cfg<BN, SWAP>;
     constexpr int SMEM = C::OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
     static_assert(SMEM * C::CTAS <= 227 * 1024, "shared memory");
-    static_assert(SWAP || BN <= 128 ? BN * C::RED_LD * 4 <= C::STAGES * C::STAGE : true, "a cluster's sums lie over the stages");
+    static_assert(AHEAD == 4, "a block's scale is picked among four");
+    static_assert(C::STAGES >= 2 && C::STAGES * C::STAGE / 16 < 0x3fff, "see the MMAs' warps");
+    static_assert(!SWAP || BN * C::RED_LD * 4 <= C::STAGES * C::STAGE, "a cluster's sums lie over the stages");
     const auto kernel = kda_scaled_matmul_kernel<BN, SWAP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
@@ -411,7 +441,7 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
     };
     if (!operand(&p.a, SWAP ? w : x, lanes, LANES) || !operand(&p.b, SWAP ? x : w, cols, BN)) return cudaErrorInvalidValue;
     p.tiled_y = 0;
-    if (!SWAP && splits == 1 && p.outs % 8 == 0) {
+    if (!SWAP && p.outs % 8 == 0) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.outs), static_cast<cuuint64_t>(p.rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.outs) * 2};
         const cuuint32_t box[2] = {static_cast<cuuint32_t>(C::PANEL), 32};
@@ -445,29 +475,30 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
 struct Choice {
     int bn, splits;
 };
-// The least estimated time over tile widths and splits: waves of CTAs x (a start and an end + blocks x the time of one), in
-// cycles. A block of 256 columns takes the tensor core 512, of 128 its operands' way from shared memory 270, of 64 the same for
-// A alone.
+// The least estimated time, in cycles, from measurements (8192 rows, 2048 channels to 6144 outputs: tiles of 256 columns 91 us, of 128
+// 118, of 64 139; 256 rows to 6176: 11.3, 8.8 and 10.1 us): rounds of CTAs x (blocks x a block's time + a tile's start and end). Up to 64
+// rows, the splits of a tile that keep the busiest SM's blocks fewest (7 rows, 12288 to 12288: one 30.2 us, two 28.5, three 27.8, four 33.0).
 Choice choose(int64_t rows, int64_t outs, int blocks, int sms) {
+    auto over = [](int64_t a, int64_t b) { return (a - 1) / b + 1; };
     Choice best{0, 1};
     double least = 0;
-    auto consider = [&](int bn, int per_sm, int64_t tiles, double block) {
-        for (int s = 1; s <= MAX_SPLITS && s <= blocks; ++s) {
-            if (s > 1 && (bn == 256 || tiles * s > 2 * static_cast<int64_t>(sms) * per_sm)) break;
-            const int64_t slots = static_cast<int64_t>(sms) * per_sm, waves = (tiles * s - 1) / slots + 1;
-            const double each = s == 1 ? 1500 : 4000, t = 3000 + waves * (each + ((blocks - 1) / s + 1) * block * per_sm);
-            if (!best.bn || t < least) best = {bn, s}, least = t;
-        }
+    auto offer = [&](int bn, int splits, double t) {
+        if (!best.bn || t < least) best = {bn, splits}, least = t;
     };
-    auto over = [](int64_t a, int64_t b) { return (a - 1) / b + 1; };
     if (rows <= SWAP_ROWS) {
         const int bn = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-        consider(bn, 2, over(outs, LANES), 150);
-    } else {
-        consider(256, 1, over(rows, LANES) * over(outs, 256), 530);
-        consider(128, 1, over(rows, LANES) * over(outs, 128), 300);
-        consider(64, 2, over(rows, LANES) * over(outs, 64), 200);
+        const int64_t tiles = over(outs, LANES);
+        for (int s = 1; s <= MAX_SPLITS && s <= blocks && (s == 1 || tiles * s <= 2 * static_cast<int64_t>(sms)); ++s)
+            offer(bn, s, static_cast<double>(over(tiles * s, sms)) * over(blocks, s) * 500. + (s > 1 ? 2500. : 0.));
+        return best;
     }
+    auto wide = [&](int bn, int64_t slots, int64_t tiles, double block) {
+        offer(bn, 1, static_cast<double>(over(tiles, slots)) * (blocks * block + 1200.));
+    };
+    const int64_t high = over(rows, LANES), t64 = high * over(outs, 64);
+    wide(256, sms, high * over(outs, 256), 1030.);
+    wide(128, sms, high * over(outs, 128), 680.);
+    wide(64, 2 * sms, t64, t64 <= sms ? 560. : 830.);
     return best;
 }
 
