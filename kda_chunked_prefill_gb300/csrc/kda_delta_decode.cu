@@ -2,18 +2,18 @@
 // token, state in and out:
 //     S <- e^{g_t} S;  d = beta_t (v_t - S^T k_t);  S <- S + k_t d^T;  o_t = scale S^T q_t
 //
-// A warp owns 32 value columns of one (sequence, head): column j of S, d and o
+// A warp owns 16 value columns of one (sequence, head): column j of S, d and o
 // depends on column j of the state alone, so no warp waits for another and there
-// is no barrier. A lane holds 32 key rows x 4 columns in registers. A token costs one
+// is no barrier. A lane holds 16 key rows x 4 columns in registers. A token costs one
 // reduction: k^T S and q^T S come from the state before the update, and
 //     o = scale (e^g q^T S + (q.k) d)
-// needs no second pass over it. The eight sums of a lane are reduced over the four
-// lanes that share its columns by halves (4 + 2 shuffles), which leaves each of
-// them with two. Everything is fp32; o is rounded once.
+// needs no second pass over it. The eight sums of a lane are reduced over the eight
+// lanes that share its columns by halves (4 + 2 + 1 shuffles), which leaves each of
+// them with one. Everything is fp32; o is rounded once.
 //
 // Bound by memory: 64 KB of state read and written per (sequence, head) and
-// call. A warp reads 4 rows x 128 bytes per access, 32 accesses in flight. (With 16
-// columns a warp, 64 bytes a row and half the registers: 7 % slower.)
+// call. A warp reads 8 rows x 64 bytes per access, 16 accesses in flight. (32 columns a warp, 4 rows x 128 bytes per access and half
+// as many warps: 8 % slower.) 256 sequences x 1 token, 16 heads: 82 us, a copy's time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,24 +32,28 @@ using lin::mul2;
 using lin::pair;
 using lin::split;
 
-constexpr int THREADS = 128;
-constexpr int COLS = 32;  // value columns of a warp
-constexpr int ROWS = 32;  // key rows of a lane
-static_assert(ROWS * 4 == DK && COLS * THREADS / 32 == DV, "four lanes share a column, a CTA has a state");
+constexpr int THREADS = 64;
+constexpr int PER_SM = 8;  // 128 registers: 16 warps an SM; with the 158 the compiler takes otherwise, 12, and 94 us instead of 82
+constexpr int COLS = 16;                                 // value columns of a warp
+constexpr int CTA_COLS = COLS * THREADS / 32;
+constexpr int PARTS = DV / CTA_COLS;                     // CTAs of a (sequence, head)
+constexpr int ROWS = 16;                                 // key rows of a lane
+static_assert(ROWS * 8 == DK, "eight lanes share a column");
 
 struct Token {
-    uint4 k[4], q[4];  // 32 rows each
+    uint4 k[2], q[2];  // 16 rows each
     uint2 v;           // 4 columns
     float g, beta;
 };
 
 template <bool VARLEN>
-__global__ void __launch_bounds__(THREADS, 2) kda_gated_delta_recurrent_kernel(const Params p) {
+__global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_recurrent_kernel(const Params p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t chain = blockIdx.x;  // n * H + h
+    const int part = blockIdx.x % PARTS;
+    const int64_t chain = blockIdx.x / PARTS;  // n * H + h
     const int n = static_cast<int>(chain / p.H), h = static_cast<int>(chain % p.H), hk = h / p.rep;
-    const int rg = lane >> 3;                       // rows 32 rg ..
-    const int col = COLS * warp + 4 * (lane & 7);  // columns col .. col + 3
+    const int rg = lane >> 2;                                        // rows 16 rg ..
+    const int col = CTA_COLS * part + COLS * warp + 4 * (lane & 3);  // columns col .. col + 3
 
     int64_t bos, len;
     if (VARLEN) {
@@ -77,8 +81,8 @@ __global__ void __launch_bounds__(THREADS, 2) kda_gated_delta_recurrent_kernel(c
     auto load = [&](int64_t t) {
         const uint4 *k = reinterpret_cast<const uint4 *>(p.k + t * p.ks + hk * DK + ROWS * rg);
         const uint4 *q = reinterpret_cast<const uint4 *>(p.q + t * p.qs + hk * DK + ROWS * rg);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) next.k[i] = k[i], next.q[i] = q[i];
+        next.k[0] = k[0], next.k[1] = k[1];
+        next.q[0] = q[0], next.q[1] = q[1];
         next.v = *reinterpret_cast<const uint2 *>(p.v + t * p.vs + h * DV + col);
         next.g = p.g[t * p.H + h];
         next.beta = p.beta[t * p.H + h];
@@ -88,15 +92,13 @@ __global__ void __launch_bounds__(THREADS, 2) kda_gated_delta_recurrent_kernel(c
     for (int64_t t = bos; t < bos + len; ++t) {
         const Token x = next;
         if (t + 1 < bos + len) load(t + 1);
-        auto word = [](const uint4(&u)[4], int i) {  // rows 2 i, 2 i + 1
-            const uint4 &v = u[i >> 2];
-            return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
-        };
+        const uint32_t kw[8] = {x.k[0].x, x.k[0].y, x.k[0].z, x.k[0].w, x.k[1].x, x.k[1].y, x.k[1].z, x.k[1].w};
+        const uint32_t qw[8] = {x.q[0].x, x.q[0].y, x.q[0].z, x.q[0].w, x.q[1].x, x.q[1].y, x.q[1].z, x.q[1].w};
         f2 a0 = 0, a1 = 0, o0 = 0, o1 = 0;
         float qk = 0.f;
 #pragma unroll
         for (int i = 0; i < ROWS / 2; ++i) {
-            const float2 kk = unpack_bf16(word(x.k, i)), qq = unpack_bf16(word(x.q, i));
+            const float2 kk = unpack_bf16(kw[i]), qq = unpack_bf16(qw[i]);
             qk = fmaf(qq.x, kk.x, qk);
             qk = fmaf(qq.y, kk.y, qk);
             a0 = fma2(pair(kk.x, kk.x), S[2 * i][0], a0);
@@ -108,20 +110,21 @@ __global__ void __launch_bounds__(THREADS, 2) kda_gated_delta_recurrent_kernel(c
             o0 = fma2(pair(qq.y, qq.y), S[2 * i + 1][0], o0);
             o1 = fma2(pair(qq.y, qq.y), S[2 * i + 1][1], o1);
         }
-        // over the four row groups: lane bit 4 keeps k^T S or q^T S, bit 3 two of the four columns
+        // over the eight row groups: lane 16 bit 4 keeps k^T S or q^T S, bits 3 and 2 one of the four columns
         float s[8];
         split(a0, s[0], s[1]);
         split(a1, s[2], s[3]);
         split(o0, s[4], s[5]);
         split(o1, s[6], s[7]);
-        const bool b4 = lane & 16, b3 = lane & 8;
-        float r4[4], r2[2];
+        const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+        float r4[4], r2[2], r1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) r4[j] = (b4 ? s[4 + j] : s[j]) + __shfl_xor_sync(0xffffffffu, b4 ? s[j] : s[4 + j], 16);
 #pragma unroll
         for (int j = 0; j < 2; ++j) r2[j] = (b3 ? r4[2 + j] : r4[j]) + __shfl_xor_sync(0xffffffffu, b3 ? r4[j] : r4[2 + j], 8);
+        r1 = (b2 ? r2[1] : r2[0]) + __shfl_xor_sync(0xffffffffu, b2 ? r2[0] : r2[1], 4);
 #pragma unroll
-        for (int m = 8; m <= 16; m <<= 1) qk += __shfl_xor_sync(0xffffffffu, qk, m);
+        for (int m = 4; m <= 16; m <<= 1) qk += __shfl_xor_sync(0xffffffffu, qk, m);
 
         gate_bad |= !(x.g <= 0.f);
         const float d = expf(x.g);  // 0 for -inf
@@ -130,15 +133,16 @@ __global__ void __launch_bounds__(THREADS, 2) kda_gated_delta_recurrent_kernel(c
         float w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            w[j] = x.beta * fmaf(-d, __shfl_sync(0xffffffffu, r2[j & 1], 8 * (j >> 1) + (lane & 7)), v[j]);
+            w[j] = x.beta * fmaf(-d, __shfl_sync(0xffffffffu, r1, 4 * j + (lane & 3)), v[j]);
+        const float mine = b3 ? (b2 ? w[3] : w[2]) : (b2 ? w[1] : w[0]);
         if (b4) {
-            const float oa = p.scale * fmaf(d, r2[0], qk * (b3 ? w[2] : w[0])), ob = p.scale * fmaf(d, r2[1], qk * (b3 ? w[3] : w[1]));
-            *reinterpret_cast<uint32_t *>(p.o + (t * p.H + h) * DV + col + (b3 ? 2 : 0)) = pack_bf16(oa, ob);
+            const float o = p.scale * fmaf(d, r1, qk * mine);
+            p.o[(t * p.H + h) * DV + col + (rg & 3)] = __float2bfloat16_rn(o);
         }
         const f2 d2 = pair(d, d), w0 = pair(w[0], w[1]), w1 = pair(w[2], w[3]);
 #pragma unroll
         for (int i = 0; i < ROWS / 2; ++i) {
-            const float2 kk = unpack_bf16(word(x.k, i));
+            const float2 kk = unpack_bf16(kw[i]);
             S[2 * i][0] = fma2(pair(kk.x, kk.x), w0, mul2(d2, S[2 * i][0]));
             S[2 * i][1] = fma2(pair(kk.x, kk.x), w1, mul2(d2, S[2 * i][1]));
             S[2 * i + 1][0] = fma2(pair(kk.y, kk.y), w0, mul2(d2, S[2 * i + 1][0]));
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, 2) kda_gated_delta_recurrent_kernel(c
 }  // namespace dec
 
 cudaError_t launch_recurrent(const Params &p, cudaStream_t stream) {
-    const int grid = p.N * p.H;  // the caller has checked that this fits
+    const int grid = p.N * p.H * dec::PARTS;  // the caller has checked that this fits
     if (p.cu)
         dec::kda_gated_delta_recurrent_kernel<true><<<grid, dec::THREADS, 0, stream>>>(p);
     else

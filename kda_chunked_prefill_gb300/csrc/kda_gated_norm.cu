@@ -5,7 +5,7 @@
 //
 // Sum and maximum come from one reduction: with m = x w act(gate), the codes are e4m3(m 448 / max|m|) and the scale is max|m| / sqrt(
 // mean(x^2) + eps) / 448, so a row is read once and stays in registers. Sixteen lanes take a row, eight channels each (one 16-byte
-// access of x, gate and, half as wide, y); the weight's eight values stay in registers for the two rows that a half warp takes.
+// access of x, gate and, half as wide, y), a row each: what hides the memory's latency is the number of warps.
 //
 // Bound by memory: 5 bytes per channel with bf16 x (2 + 2 in, 1 out), 7 with fp32. The sigmoid is the hardware's 2^x and reciprocal (a
 // few units in the last place; expf and an IEEE division made the kernel wait for its instructions, 53 an element).
@@ -15,15 +15,23 @@
 #include "kda.h"
 #include "kda_checks.h"
 #include "kda_common.cuh"
+#include "kda_linear.cuh"
 
 namespace kda {
 namespace gatednorm {
 
 constexpr float TINY = 7.888609052210118e-31f;  // 2^-100: below it a row counts as zero
 constexpr float E4M3_MAX = 448.f;
-constexpr int THREADS = 256;
-constexpr int ROWS = 2;                              // of a half warp
-constexpr int CTA_ROWS = THREADS / 16 * ROWS;
+constexpr int THREADS = 128, PER_SM = 16;  // every warp an SM has; two rows a half warp and half the warps: 22.6 us
+constexpr int CTA_ROWS = THREADS / 16;
+
+using lin::add2;
+using lin::f2;
+using lin::fma2;
+using lin::mul2;
+using lin::of_bf16;
+using lin::pair;
+using lin::split;
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;  // saturating, round to nearest even; NaN stays NaN
@@ -31,21 +39,21 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+// eight channels, in pairs
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, f2 (&v)[4]) {
     const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_bf16(w[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+    v[0] = of_bf16(u.x), v[1] = of_bf16(u.y), v[2] = of_bf16(u.z), v[3] = of_bf16(u.w);
 }
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void load8(const float *p, f2 (&v)[4]) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
 }
-
+using kda::max_abs_nan;
+__device__ __forceinline__ float max_abs_nan(float m, float x, float y) {  // NaN once any is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(x)), "f"(fabsf(y)));
+    return r;
+}
 __device__ __forceinline__ float rcp(float x) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -54,63 +62,64 @@ __device__ __forceinline__ float rcp(float x) {
 
 // STRIDED: the gate's tokens lie gate_stride elements apart; otherwise like x.
 template <typename X, bool STRIDED, bool SILU>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, PER_SM)
     kda_gated_rms_norm_kernel(const X *__restrict__ x, const __nv_bfloat16 *__restrict__ gate, int64_t gate_stride,
                               const float *__restrict__ weight, int32_t rows, int32_t heads, float eps, uint8_t *__restrict__ y,
                               float *__restrict__ y_scale) {
     const int c = 8 * (threadIdx.x & 15);
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * CTA_ROWS + threadIdx.x / 16;
-    float w[8], v[ROWS][8], g[ROWS][8];
-    load8(weight + c, w);
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int64_t row = row0 + i * (THREADS / 16);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = g[i][j] = 0.f;
-        if (row >= rows) continue;
-        load8(x + row * DV + c, v[i]);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * CTA_ROWS + threadIdx.x / 16;
+    f2 v[4] = {}, g[4] = {}, w[4];
+    if (row < rows) {
+        load8(x + row * DV + c, v);
         int64_t at = row * DV;
         if (STRIDED) {
             const uint32_t t = static_cast<uint32_t>(row) / static_cast<uint32_t>(heads);
             at = t * gate_stride + static_cast<int64_t>(static_cast<uint32_t>(row) - t * heads) * DV;
         }
-        load8(gate + at + c, g[i]);
+        load8(gate + at + c, g);
     }
+    load8(weight + c, w);
+    f2 sums = 0;
+    float mx = 0.f;
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const int64_t row = row0 + i * (THREADS / 16);
-        float sum = 0.f, mx = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            sum = fmaf(v[i][j], v[i][j], sum);
-            const float sig = rcp(1.f + ex2(g[i][j] * -LOG2E));  // (2^x infinite: closed)
-            v[i][j] *= w[j] * (SILU ? g[i][j] * sig : sig);
-            mx = max_abs_nan(mx, v[i][j]);
-        }
-#pragma unroll
-        for (int s = 8; s; s >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, s);
-            mx = max_abs_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-        }
-        if (row >= rows) continue;  // (a whole half warp)
-        // A sum that is not finite, by a NaN, an infinity or an overflow, marks the whole row; so does an infinite product.
-        const bool fine = sum <= 3.402823466e38f && mx <= 3.402823466e38f;
-        const float rstd = rsqrtf(sum * (1.f / DV) + eps), amax = fine ? mx * rstd : __int_as_float(0x7fc00000);
-        const bool good = amax <= 3.402823466e38f, tiny = amax < TINY;
-        float mul = E4M3_MAX * rcp(mx);
-        if (!(mx > 1e-30f && mx < 1e30f)) {  // where the quotient, or its reciprocal, is out of range: in two factors
-            const float first = mx < 1.f ? 0x1p80f : 0x1p-80f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= first;
-            mul = E4M3_MAX / (mx * first);
-        }
-        if (tiny) mul = 0.f;
-        if (!good) mul = __int_as_float(0x7fc00000);
-        if (c == 0) y_scale[row] = tiny ? 0.f : good ? amax * (1.f / E4M3_MAX) : mul;
-        const uint32_t a = e4m3x4(v[i][0] * mul, v[i][1] * mul, v[i][2] * mul, v[i][3] * mul);
-        const uint32_t b = e4m3x4(v[i][4] * mul, v[i][5] * mul, v[i][6] * mul, v[i][7] * mul);
-        *reinterpret_cast<uint2 *>(y + row * DV + c) = make_uint2(a, b);
+    for (int j = 0; j < 4; ++j) {
+        sums = fma2(v[j], v[j], sums);
+        float a, b;
+        split(mul2(g[j], pair(-LOG2E, -LOG2E)), a, b);
+        split(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);  // (2^x infinite: closed)
+        f2 act = pair(rcp(a), rcp(b));
+        if (SILU) act = mul2(act, g[j]);
+        v[j] = mul2(v[j], mul2(w[j], act));
+        split(v[j], a, b);
+        mx = max_abs_nan(mx, a, b);
     }
+    float sum, half;
+    split(sums, sum, half);
+    sum += half;
+#pragma unroll
+    for (int s = 8; s; s >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        mx = max_abs_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    }
+    if (row >= rows) return;  // (a whole half warp)
+    // A sum that is not finite, by a NaN, an infinity or an overflow, marks the whole row; so does an infinite product.
+    const bool fine = sum <= 3.402823466e38f && mx <= 3.402823466e38f;
+    const float rstd = rsqrtf(sum * (1.f / DV) + eps), amax = fine ? mx * rstd : __int_as_float(0x7fc00000);
+    const bool good = amax <= 3.402823466e38f, tiny = amax < TINY;
+    float mul = E4M3_MAX * rcp(mx);
+    if (!(mx > 1e-30f && mx < 1e30f)) {  // where the quotient, or its reciprocal, is out of range: in two factors
+        const float first = mx < 1.f ? 0x1p80f : 0x1p-80f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], pair(first, first));
+        mul = E4M3_MAX / (mx * first);
+    }
+    if (tiny) mul = 0.f;
+    if (!good) mul = __int_as_float(0x7fc00000);
+    if (c == 0) y_scale[row] = tiny ? 0.f : good ? amax * (1.f / E4M3_MAX) : mul;
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(mul2(v[j], pair(mul, mul)), q[2 * j], q[2 * j + 1]);
+    *reinterpret_cast<uint2 *>(y + row * DV + c) = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
 template <typename X>
