@@ -803,18 +803,63 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, in_place: bool = False,
 
 
 # ------------------------------------------------------------------ the delta rule with one decay per head
-def _delta_args(q, k, v, g, beta, o, initial_state, final_state, num_seqs, status):
-    """The checks kda_gated_delta_chunk_fwd and kda_gated_delta_decode_fwd share."""
+# (Of the calls from here on, those that allocate their outputs do not check them: a small call's host time is its time.)
+def _delta_inputs(q, k, v, g, beta, initial_state, num_seqs):
+    """The checks of what kda_gated_delta_chunk_fwd and kda_gated_delta_decode_fwd read, and what they pass on."""
+    index = _device_of(q)
+    shape = q.shape
+    if len(shape) != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must have shape (tokens, heads, head_dim)")
+    T, Hk, D = shape
+    _, H, V = v.shape
+    qs, ks, vs = _heads_view(q, "q", T, index), _heads_view(k, "k", T, index), _heads_view(v, "v", T, index)
+    if k.shape != shape:
+        raise ValueError(f"k must have q's shape {tuple(shape)}, got {tuple(k.shape)}")
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"the number of value heads ({H}) must be a multiple of the query/key heads ({Hk})")
     if g.dim() != 2:
         raise ValueError(f"g must have shape (tokens, heads), got {tuple(g.shape)}")
-    args = _linear_args(q, k, v, g, o, initial_state, final_state, num_seqs, status)
-    _need(beta, "beta", _F32, g.shape, args[0])
-    return args[:-1]
+    _need(g, "g", _F32, (T, H), index)
+    _need(beta, "beta", _F32, (T, H), index)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", _F32, (num_seqs, H, D, V), index)
+    return index, T, H, Hk, D, V, qs, ks, vs
+
+
+def _delta_outputs(inputs, o, final_state, status, num_seqs):
+    index, T, H, _, D, V = inputs[:6]
+    _need(o, "o", _BF16, (T, H, V), index)
+    if final_state is not None:
+        _need(final_state, "final_state", _F32, (num_seqs, H, D, V), index)
+    if status is not None:
+        _need(status, "status", _I32, (1,), index)
 
 
 def gated_delta_workspace_size(num_seqs: int, total_tokens: int, num_heads: int) -> int:
     """Workspace bytes ``kda_gated_delta_chunk_fwd`` needs on the current CUDA device (0: none)."""
     return int(load_library().kda_gated_delta_chunk_fwd_workspace_size(int(num_seqs), int(total_tokens), int(num_heads)))
+
+
+def _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, final_state, status, stream, workspace):
+    index, T, H, Hk, D, V, qs, ks, vs = inputs
+    N = cu_seqlens.shape[0] - 1
+    _need(cu_seqlens, "cu_seqlens", _I32, (N + 1,), index)
+    lib = load_library()
+    if workspace is None:
+        if _current_device() == index:
+            need = lib.kda_gated_delta_chunk_fwd_workspace_size(N, T, H)
+        else:
+            with torch.cuda.device(index):
+                need = lib.kda_gated_delta_chunk_fwd_workspace_size(N, T, H)
+        if need:
+            with _on(stream):
+                workspace = torch.empty(need, dtype=_U8, device=q.device)
+    elif workspace.get_device() != index or workspace.dtype is not _U8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return _call(lib.kda_gated_delta_chunk_fwd, "kda_gated_delta_chunk_fwd", index,
+                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk,
+                  D, V, qs, ks, vs, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
+                  0 if workspace is None else workspace.numel()), stream)
 
 
 def kda_gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state, scale: float, o, final_state, status=None,
@@ -830,21 +875,9 @@ def kda_gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state, scale
     on a host-side error; returns ``KDA_OK`` once queued.
     """
     N = cu_seqlens.shape[0] - 1
-    index, T, H, Hk, D, V, qs, ks, vs = _delta_args(q, k, v, g, beta, o, initial_state, final_state, N, status)
-    _need(cu_seqlens, "cu_seqlens", _I32, (N + 1,), index)
-    lib = load_library()
-    if workspace is None:
-        with torch.cuda.device(index) if _current_device() != index else _here:
-            need = lib.kda_gated_delta_chunk_fwd_workspace_size(N, T, H)
-        if need:
-            with _on(stream):
-                workspace = torch.empty(need, dtype=_U8, device=q.device)
-    elif workspace.get_device() != index or workspace.dtype is not _U8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    return _call(lib.kda_gated_delta_chunk_fwd, "kda_gated_delta_chunk_fwd", index,
-                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk,
-                  D, V, qs, ks, vs, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
-                  0 if workspace is None else workspace.numel()), stream)
+    inputs = _delta_inputs(q, k, v, g, beta, initial_state, N)
+    _delta_outputs(inputs, o, final_state, status, N)
+    return _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, final_state, status, stream, workspace)
 
 
 def gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state=None, scale: Optional[float] = None,
@@ -856,18 +889,33 @@ def gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state=None, scal
     and a device-detected error raises ``KdaError``. Rows of ``o`` behind the last
     sequence are not written.
     """
-    dev, shape = q.device, v.shape
-    if scale is None:
-        scale = q.shape[2] ** -0.5
+    N = cu_seqlens.shape[0] - 1
+    inputs = _delta_inputs(q, k, v, g, beta, initial_state, N)
+    _, T, H, _, D, V = inputs[:6]
+    dev = q.device
     with _on(stream):
-        o = torch.empty(shape, dtype=_BF16, device=dev)
-        fs = (torch.empty((cu_seqlens.shape[0] - 1, shape[1], q.shape[2], shape[2]), dtype=_F32, device=dev)
-              if output_final_state else None)
+        o = torch.empty((T, H, V), dtype=_BF16, device=dev)
+        fs = torch.empty((N, H, D, V), dtype=_F32, device=dev) if output_final_state else None
         status = _status(check, dev)
-    kda_gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state, scale, o, fs, status, stream)
+    _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, D ** -0.5 if scale is None else scale, o, fs, status, stream,
+                 None)
     if check:
         _raise_device(status, stream, "kda_gated_delta_chunk_fwd")
     return o, fs
+
+
+def _steps(q, num_seqs):
+    N, T = int(num_seqs), q.shape[0]
+    if N < 0 or (N == 0 and T != 0) or (N > 0 and T % N != 0):
+        raise ValueError("q must hold the same number of tokens for every sequence")
+    return N, T // N if N else 0
+
+
+def _delta_decode(inputs, q, k, v, g, beta, N, steps, initial_state, scale, o, final_state, status, stream):
+    index, _, H, Hk, D, V, qs, ks, vs = inputs
+    return _call(load_library().kda_gated_delta_decode_fwd, "kda_gated_delta_decode_fwd", index,
+                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N, steps, H, Hk, D, V, qs, ks, vs,
+                  _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status)), stream)
 
 
 def kda_gated_delta_decode_fwd(q, k, v, g, beta, num_seqs: int, initial_state, scale: float, o, final_state, status=None,
@@ -875,30 +923,27 @@ def kda_gated_delta_decode_fwd(q, k, v, g, beta, num_seqs: int, initial_state, s
     """Call the C entry point ``kda_gated_delta_decode_fwd`` with caller-allocated
     outputs: sequence n's tokens are rows n*Tn .. n*Tn+Tn-1 of q, k, v, g, beta and
     o; tensors as in ``kda_gated_delta_chunk_fwd``."""
-    N = int(num_seqs)
-    T = q.shape[0]
-    if N < 0 or (N == 0 and T != 0) or (N > 0 and T % N != 0):
-        raise ValueError("q must hold the same number of tokens for every sequence")
-    index, T, H, Hk, D, V, qs, ks, vs = _delta_args(q, k, v, g, beta, o, initial_state, final_state, N, status)
-    return _call(load_library().kda_gated_delta_decode_fwd, "kda_gated_delta_decode_fwd", index,
-                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), N, T // N if N else 0, H, Hk, D, V,
-                  qs, ks, vs, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status)), stream)
+    N, steps = _steps(q, num_seqs)
+    inputs = _delta_inputs(q, k, v, g, beta, initial_state, N)
+    _delta_outputs(inputs, o, final_state, status, N)
+    return _delta_decode(inputs, q, k, v, g, beta, N, steps, initial_state, scale, o, final_state, status, stream)
 
 
 def gated_delta_decode_fwd(q, k, v, g, beta, num_seqs: int, state=None, scale: Optional[float] = None,
                            in_place: bool = False, check: bool = False, stream=None):
     """Run ``kda_gated_delta_decode_fwd``; returns ``(o, final_state)``. With
     ``in_place`` the given ``state`` tensor is updated and returned as ``final_state``."""
-    dev, shape = q.device, v.shape
-    if scale is None:
-        scale = q.shape[2] ** -0.5
+    N, steps = _steps(q, num_seqs)
+    inputs = _delta_inputs(q, k, v, g, beta, state, N)
+    _, T, H, _, D, V = inputs[:6]
     if in_place and state is None:
         raise ValueError("in_place needs a state tensor")
+    dev = q.device
     with _on(stream):
-        o = torch.empty(shape, dtype=_BF16, device=dev)
-        fs = state if in_place else torch.empty((int(num_seqs), shape[1], q.shape[2], shape[2]), dtype=_F32, device=dev)
+        o = torch.empty((T, H, V), dtype=_BF16, device=dev)
+        fs = state if in_place else torch.empty((N, H, D, V), dtype=_F32, device=dev)
         status = _status(check, dev)
-    kda_gated_delta_decode_fwd(q, k, v, g, beta, num_seqs, state, scale, o, fs, status, stream)
+    _delta_decode(inputs, q, k, v, g, beta, N, steps, state, D ** -0.5 if scale is None else scale, o, fs, status, stream)
     if check:
         _raise_device(status, stream, "kda_gated_delta_decode_fwd")
     return o, fs
@@ -908,77 +953,98 @@ def gated_delta_decode_fwd(q, k, v, g, beta, num_seqs: int, state=None, scale: O
 _ACTIVATIONS = {"sigmoid": 0, "silu": 1}
 
 
+def _gate_inputs(x, gate, weight, activation):
+    index, shape, kind = _device_of(x), x.shape, x.dtype
+    if len(shape) != 3:
+        raise ValueError(f"x must have shape (tokens, heads, head_dim), got {tuple(shape)}")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(_ACTIVATIONS)}, got {activation!r}")
+    if kind is not _BF16 and kind is not _F32:
+        raise TypeError(f"x must be {_BF16} or {_F32}, got {kind}")
+    T, H, D = shape
+    _need(x, "x", kind, shape, index)
+    gs = _heads_view(gate, "gate", T, index)
+    if gate.shape != shape:
+        raise ValueError(f"gate must have x's shape {tuple(shape)}, got {tuple(gate.shape)}")
+    _need(weight, "weight", _F32, (D,), index)
+    return index, T, H, D, gs, 1 if kind is _F32 else 0, _ACTIVATIONS[activation]
+
+
+def _gate_call(inputs, x, gate, weight, eps, y, y_scale, stream):
+    index, T, H, D, gs, fp32, silu = inputs
+    return _call(load_library().kda_gated_rms_norm, "kda_gated_rms_norm", index,
+                 (x.data_ptr(), gate.data_ptr(), gs, weight.data_ptr(), T, H, D, eps, fp32, silu, y.data_ptr(), y_scale.data_ptr()),
+                 stream)
+
+
 def kda_gated_rms_norm(x, gate, weight, eps: float, y, y_scale, activation: str = "sigmoid", stream=None) -> int:
     """Call the C entry point ``kda_gated_rms_norm``: x bf16 or fp32 [T,H,128];
     gate bf16 [T,H,128] (tokens may be strided); weight fp32 [128]; y
     float8_e4m3fn [T,H*128]; y_scale fp32 [T,H]; activation "sigmoid" or "silu"."""
-    index = _device_of(x)
-    if x.dim() != 3:
-        raise ValueError(f"x must have shape (tokens, heads, head_dim), got {tuple(x.shape)}")
-    if activation not in _ACTIVATIONS:
-        raise ValueError(f"activation must be one of {tuple(_ACTIVATIONS)}, got {activation!r}")
-    T, H, D = x.shape
-    kind = x.dtype
-    if kind is not _BF16 and kind is not _F32:
-        raise TypeError(f"x must be {_BF16} or {_F32}, got {kind}")
-    _need(x, "x", kind, (T, H, D), index)
-    gs = _heads_view(gate, "gate", T, index)
-    if gate.shape != x.shape:
-        raise ValueError(f"gate must have x's shape {tuple(x.shape)}, got {tuple(gate.shape)}")
-    _need(weight, "weight", _F32, (D,), index)
+    inputs = _gate_inputs(x, gate, weight, activation)
+    index, T, H, D = inputs[:4]
     _need(y, "y", _F8, (T, H * D), index)
     _need(y_scale, "y_scale", _F32, (T, H), index)
-    return _call(load_library().kda_gated_rms_norm, "kda_gated_rms_norm", index,
-                 (x.data_ptr(), gate.data_ptr(), gs, weight.data_ptr(), T, H, D, eps, 1 if kind is _F32 else 0,
-                  _ACTIVATIONS[activation], y.data_ptr(), y_scale.data_ptr()), stream)
+    return _gate_call(inputs, x, gate, weight, eps, y, y_scale, stream)
 
 
 def gated_rms_norm(x, gate, weight, eps: float = 1e-5, activation: str = "sigmoid", stream=None):
     """Run ``kda_gated_rms_norm`` on an attention output x [T,H,128]; returns
     ``(y, y_scale)``, float8_e4m3fn [T,H*128] and fp32 [T,H]."""
+    inputs = _gate_inputs(x, gate, weight, activation)
+    _, T, H, D = inputs[:4]
     dev = x.device
-    if x.dim() != 3:
-        raise ValueError(f"x must have shape (tokens, heads, head_dim), got {tuple(x.shape)}")
-    T, H, D = x.shape
     with _on(stream):
         y = torch.empty((T, H * D), dtype=_F8, device=dev)
         y_scale = torch.empty((T, H), dtype=_F32, device=dev)
-    kda_gated_rms_norm(x, gate, weight, eps, y, y_scale, activation, stream)
+    _gate_call(inputs, x, gate, weight, eps, y, y_scale, stream)
     return y, y_scale
 
 
 # ------------------------------------------------------------------ e4m3 product with scales
-def kda_scaled_matmul(x, x_scale, weight, weight_scale, y, status=None, stream=None) -> int:
-    """Call the C entry point ``kda_scaled_matmul``: x float8_e4m3fn [..., K] with
-    x_scale fp32 [...] or [..., ceil(K/128)]; weight float8_e4m3fn [N,K] with
-    weight_scale fp32 [ceil(N/128), ceil(K/128)]; y bf16 [..., N]; status: int32 [1] or None."""
+def _product_inputs(x, x_scale, weight, weight_scale):
     index, shape = _device_of(x), x.shape
     if len(shape) < 1 or weight.dim() != 2:
         raise ValueError("x must have shape (..., width) and weight (outs, width)")
     N, K = weight.shape
+    lead = shape[:-1]
     blocks = (K + 127) // 128
     per_block = x_scale.dim() == len(shape)
-    _need(x, "x", _F8, (*shape[:-1], K), index)
+    _need(x, "x", _F8, (*lead, K), index)
     _need(weight, "weight", _F8, (N, K), index)
-    _need(x_scale, "x_scale", _F32, (*shape[:-1], blocks) if per_block else shape[:-1], index)
+    _need(x_scale, "x_scale", _F32, (*lead, blocks) if per_block else lead, index)
     _need(weight_scale, "weight_scale", _F32, ((N + 127) // 128, blocks), index)
-    _need(y, "y", _BF16, (*shape[:-1], N), index)
+    return index, lead, K, N, int(per_block)
+
+
+def _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream):
+    index, lead, K, N, per_block = inputs
+    return _call(load_library().kda_scaled_matmul, "kda_scaled_matmul", index,
+                 (x.data_ptr(), x_scale.data_ptr(), per_block, weight.data_ptr(), weight_scale.data_ptr(), lead.numel(), K, N,
+                  y.data_ptr(), _p(status)), stream)
+
+
+def kda_scaled_matmul(x, x_scale, weight, weight_scale, y, status=None, stream=None) -> int:
+    """Call the C entry point ``kda_scaled_matmul``: x float8_e4m3fn [..., K] with
+    x_scale fp32 [...] or [..., ceil(K/128)]; weight float8_e4m3fn [N,K] with
+    weight_scale fp32 [ceil(N/128), ceil(K/128)]; y bf16 [..., N]; status: int32 [1] or None."""
+    inputs = _product_inputs(x, x_scale, weight, weight_scale)
+    index, lead, _, N, _ = inputs
+    _need(y, "y", _BF16, (*lead, N), index)
     if status is not None:
         _need(status, "status", _I32, (1,), index)
-    rows = y.numel() // N if N else 0
-    return _call(load_library().kda_scaled_matmul, "kda_scaled_matmul", index,
-                 (x.data_ptr(), x_scale.data_ptr(), int(per_block), weight.data_ptr(), weight_scale.data_ptr(), rows, K, N,
-                  y.data_ptr(), _p(status)), stream)
+    return _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream)
 
 
 def scaled_matmul(x, x_scale, weight, weight_scale, check: bool = False, stream=None):
     """Run ``kda_scaled_matmul``; returns y bf16 [..., N]. With ``check=True`` the
     device status word is read back (a synchronising copy)."""
+    inputs = _product_inputs(x, x_scale, weight, weight_scale)
     dev = x.device
     with _on(stream):
-        y = torch.empty((*x.shape[:-1], weight.shape[0]), dtype=_BF16, device=dev)
+        y = torch.empty((*inputs[1], inputs[3]), dtype=_BF16, device=dev)
         status = _status(check, dev)
-    kda_scaled_matmul(x, x_scale, weight, weight_scale, y, status, stream)
+    _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream)
     if check:
         _raise_device(status, stream, "kda_scaled_matmul")
     return y
