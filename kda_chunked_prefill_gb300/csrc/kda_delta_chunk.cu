@@ -32,7 +32,7 @@ constexpr int C = 64;  // tokens of a chunk
 
 // What the first launch leaves of a chunk and head. The tiles are rows of 64 bf16 (128 bytes), 128-byte swizzled.
 struct Decays {
-    float upto[C];    // e^{G_t}
+    float minus[C];   // -e^{G_t}
     float out[C];     // scale e^{G_t}
     float after[C];   // e^{G_end - G_t}
     float whole, less;  // e^{G_end}, and minus 1
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     }
     if (warp == 0) {
         Decays *d = reinterpret_cast<Decays *>(img + OFF_DECAYS);
-        *reinterpret_cast<float2 *>(&d->upto[2 * lane]) = make_float2(decays[0], decays[1]);
+        *reinterpret_cast<float2 *>(&d->minus[2 * lane]) = make_float2(-decays[0], -decays[1]);
         *reinterpret_cast<float2 *>(&d->out[2 * lane]) = make_float2(p.scale * decays[0], p.scale * decays[1]);
         *reinterpret_cast<float2 *>(&d->after[2 * lane]) = make_float2(decays[2], decays[3]);
         if (lane == 0) d->whole = whole, d->less = less;
@@ -638,7 +638,7 @@ constexpr uint32_t COL_S = 0, COL_KS = 128, COL_QS = 192, COL_X = 256, COL_O = 3
 struct Misc {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t s[2], z, x;           // written; S by halves of the keys
-    uint64_t ks, xs, u;            // MMAs complete: K S and Q S; T Z and P T Z; the update
+    uint64_t ks, xs, o, u;         // MMAs complete: K S; T Z; Q S and P T Z; the update
     uint64_t drained;
     uint32_t tmem;
     int32_t abort;
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
     if (tid == 0) {
         for (int i = 0; i < STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], WARPS + 1);
         for (int i = 0; i < 2; ++i) mbar_init(&m->s[i], WARPS / 2);
-        mbar_init(&m->z, WARPS), mbar_init(&m->x, WARPS), mbar_init(&m->ks, 1), mbar_init(&m->xs, 1), mbar_init(&m->u, 1);
+        mbar_init(&m->z, WARPS), mbar_init(&m->x, WARPS), mbar_init(&m->ks, 1), mbar_init(&m->xs, 1), mbar_init(&m->o, 1), mbar_init(&m->u, 1);
         mbar_init(&m->drained, 1);
         m->abort = 0;
         mbar_fence_init();
@@ -750,8 +750,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
     } else if (warp == WARP_MMA) {
         // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues.
         const uint32_t base = smem_u32(smem);
-        constexpr uint32_t ID = lin::idesc_bf16(false, false, 128, 128), ID_64 = lin::idesc_bf16(false, false, 128, 64),
-                           ID_U = lin::idesc_bf16(false, true, 128, 128);
+        constexpr uint32_t ID = lin::idesc_bf16(false, false, 128, 64), ID_U = lin::idesc_bf16(false, true, 128, 128);
         bool ok = true;
         uint32_t st = 0, use = 0;
 #pragma unroll 1
@@ -771,6 +770,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             const uint64_t kq = umma_desc_sw128(s + OFF_KQ, 16, 1024), tt = umma_desc_sw128(s + OFF_TT, 16, 1024);
             const uint64_t kt = umma_desc_sw128(s + OFF_KQ, PANEL, 1024);
             // (additions to the address field: bytes / 16)
+            // What the chain waits for goes first, N = 64 (an MMA takes 45 to 50 cycles then, 65 to 70 with N = 128); Q S and P T Z follow
+            // while the warps make Z and X.
             if (!(ok = wait_warp(m, &m->s[0], ph))) break;
             tc_fence_after();
             if (lin::elect_one()) {
@@ -789,6 +790,14 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                     lin::umma_ts(tmem + COL_KS, tmem + COL_S + 96 + 8 * k, kq + PANEL / 16 + k * 2, ID, 1);
                 }
                 umma_commit(&m->ks);
+                if (!STATES) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t q = kq + TILE / 16 + (k >> 2) * (PANEL / 16) + (k & 3) * 2;
+                        lin::umma_ts(tmem + COL_QS, tmem + COL_S + 8 * k, q, ID, k > 0);
+                        lin::umma_ts(tmem + COL_QS, tmem + COL_S + 64 + 8 * k, q, ID, 1);
+                    }
+                }
             }
             if (!(ok = wait_warp(m, &m->z, ph))) break;
             tc_fence_after();
@@ -797,9 +806,17 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 for (int k = 0; k < 4; ++k) {
                     lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + k * 2, ID, k > 0);
                     lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k + 8, tt + k * 2, ID, 1);
-                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + (OFF_TL - OFF_TT) / 16 + k * 2, ID_64, 1);
+                    lin::umma_ts(tmem + COL_X, tmem + COL_KS + 16 * k, tt + (OFF_TL - OFF_TT) / 16 + k * 2, ID, 1);
                 }
                 umma_commit(&m->xs);
+                if (!STATES) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        lin::umma_ts(tmem + COL_O, tmem + COL_KS + 16 * k, tt + TILE / 16 + k * 2, ID, k > 0);
+                        lin::umma_ts(tmem + COL_O, tmem + COL_KS + 16 * k + 8, tt + TILE / 16 + k * 2, ID, 1);
+                    }
+                    umma_commit(&m->o);
+                }
             }
             if (!(ok = wait_warp(m, &m->x, ph))) break;
             tc_fence_after();
@@ -850,7 +867,18 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             store_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
             arrive_warp(&m->s[half]);
             if (!(ok = wait_warp(m, &m->full[st], (it / STAGES) & 1))) break;
-            f2 z[TOKS / 2], w[TOKS / 2];
+            // (what does not depend on the MMAs is done while they run)
+            const float whole = d->whole, less = d->less;
+            if (less < -0.5f) {
+                const f2 f = pair(whole, whole);
+#pragma unroll
+                for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::mul2(S[i], f);
+            } else {  // (a slow decay is not rounded away chunk after chunk)
+                const f2 f = pair(less, less);
+#pragma unroll
+                for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::fma2(S[i], f, S[i]);
+            }
+            f2 z[TOKS / 2], e[TOKS / 2];
             {
                 const unsigned char *v = stage + OFF_V + (val >> 6) * TILE + t0 * 128 + (val & 7) * 2;
                 const int c = (val & 63) >> 3;
@@ -860,17 +888,13 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 #pragma unroll
                 for (int i = 0; i < TOKS / 2; ++i) z[i] = is_map ? 0 : pair(at(2 * i), at(2 * i + 1));
             }
-            const float whole = d->whole, less = d->less;
-            uint32_t r[16];
-            if (!(ok = wait_warp(m, &m->ks, ph))) break;
-            tc_fence_after();
-            tmem_ld16(t + COL_KS + t0, r);
-            tmem_wait_ld();
+            auto load_decays = [&](const float *x) {
 #pragma unroll
-            for (int i = 0; i < TOKS / 2; ++i) {
-                const float2 e = *reinterpret_cast<const float2 *>(&d->upto[t0 + 2 * i]);
-                z[i] = lin::fma2(pair(-e.x, -e.y), pair(r[2 * i], r[2 * i + 1]), z[i]);
-            }
+                for (int i = 0; i < TOKS / 4; ++i) {
+                    const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(x + t0 + 4 * i);
+                    e[2 * i] = u.x, e[2 * i + 1] = u.y;
+                }
+            };
             auto mask = [&](f2(&v)[TOKS / 2]) {  // tokens behind the sequence: zeros, whatever they are
                 if (left == C) return;
 #pragma unroll
@@ -880,22 +904,31 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                     v[i] = pair(t0 + 2 * i < left ? x : 0.f, t0 + 2 * i + 1 < left ? y : 0.f);
                 }
             };
+            load_decays(d->minus);
+            uint32_t r[16];
+            if (!(ok = wait_warp(m, &m->ks, ph))) break;
+            tc_fence_after();
+            tmem_ld16(t + COL_KS + t0, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::fma2(e[i], pair(r[2 * i], r[2 * i + 1]), z[i]);
             mask(z);
             store_split(t + COL_KS + t0, t + COL_KS + t0 + 8, z);
             arrive_warp(&m->z);
+            load_decays(d->after);
             if (!(ok = wait_warp(m, &m->xs, ph))) break;
             tc_fence_after();
             tmem_ld16(t + COL_X + t0, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < TOKS / 2; ++i) {
-                const float2 e = *reinterpret_cast<const float2 *>(&d->after[t0 + 2 * i]);
-                w[i] = lin::mul2(pair(e.x, e.y), pair(r[2 * i], r[2 * i + 1]));
-            }
-            mask(w);
-            store_split(t + COL_X + t0, t + COL_X + t0 + 8, w);
+            for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::mul2(e[i], pair(r[2 * i], r[2 * i + 1]));
+            mask(z);
+            store_split(t + COL_X + t0, t + COL_X + t0 + 8, z);
             arrive_warp(&m->x);
             if (!STATES) {
+                load_decays(d->out);
+                if (!(ok = wait_warp(m, &m->o, ph))) break;
+                tc_fence_after();
                 uint32_t q[16];
                 tmem_ld16(t + COL_QS + t0, q);
                 tmem_ld16(t + COL_O + t0, r);
@@ -908,8 +941,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
                 const int mine = left - t0 - odd;  // tokens from this lane's first on
 #pragma unroll
                 for (int i = 0; i < TOKS / 2; ++i) {
-                    const float2 e = *reinterpret_cast<const float2 *>(&d->out[t0 + 2 * i]);
-                    const uint32_t a = lin::bf16_of(lin::fma2(pair(e.x, e.y), pair(q[2 * i], q[2 * i + 1]), pair(r[2 * i], r[2 * i + 1])));
+                    const uint32_t a = lin::bf16_of(lin::fma2(e[i], pair(q[2 * i], q[2 * i + 1]), pair(r[2 * i], r[2 * i + 1])));
                     const uint32_t b = __shfl_xor_sync(0xffffffffu, a, 1);
                     const uint32_t x = odd ? __byte_perm(b, a, 0x7632) : __byte_perm(a, b, 0x5410);
                     if (2 * i < mine) *reinterpret_cast<uint32_t *>(o) = x;
@@ -922,15 +954,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             uint32_t u[32];
             lin::tmem_ld32(t + COL_U + k0, u);
             tmem_wait_ld();
-            if (less < -0.5f) {
-                const f2 f = pair(whole, whole);
 #pragma unroll
-                for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::fma2(S[i], f, pair(u[2 * i], u[2 * i + 1]));
-            } else {  // (a slow decay is not rounded away chunk after chunk)
-                const f2 f = pair(less, less);
-#pragma unroll
-                for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::add2(S[i], lin::fma2(S[i], f, pair(u[2 * i], u[2 * i + 1])));
-            }
+            for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::add2(S[i], pair(u[2 * i], u[2 * i + 1]));
         }
         if (is_map) {  // by the columns that it maps from
             if (ok) {
