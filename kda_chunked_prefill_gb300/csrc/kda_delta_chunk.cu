@@ -675,21 +675,22 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[8]) { tmem_st8(t, r); }
-__device__ __forceinline__ void tmem_st(uint32_t t, const uint32_t (&r)[16]) { tmem_st16(t, r); }
-// v in two bf16 terms: N columns of pairs at `hi` and at `lo`, and on to the MMAs
-template <int N>
-__device__ __forceinline__ void store_split(uint32_t hi, uint32_t lo, const f2 (&v)[N]) {
-    uint32_t h[N], l[N];
+// 16 values in two bf16 terms: 8 columns of pairs at `hi` and at `lo`
+__device__ __forceinline__ void put_split(uint32_t hi, uint32_t lo, const f2 *v) {
+    uint32_t h[8], l[8];
     const f2 minus = pair(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) h[i] = lin::bf16_of(v[i]);
-    tmem_st(hi, h);
+    for (int i = 0; i < 8; ++i) h[i] = lin::bf16_of(v[i]);
+    tmem_st8(hi, h);
 #pragma unroll
-    for (int i = 0; i < N; ++i) l[i] = lin::bf16_of(lin::fma2(lin::of_bf16(h[i]), minus, v[i]));
-    tmem_st(lo, l);
+    for (int i = 0; i < 8; ++i) l[i] = lin::bf16_of(lin::fma2(lin::of_bf16(h[i]), minus, v[i]));
+    tmem_st8(lo, l);
+}
+// what this warp has put is there for the MMAs
+__device__ __forceinline__ void hand_on(uint64_t *bar) {
     tmem_wait_st();
     tc_fence_before();
+    arrive_warp(bar);
 }
 
 // STATES: the pass over the states of cut sequences.
@@ -857,16 +858,20 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             }
         }
         bool ok = true;
-        for (int it = 0; it < chunks; ++it) {
-            const int st = it % STAGES;
+        if (chunks > 0) {
+            put_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
+            put_split(t + COL_S + k0 / 2 + 8, t + COL_S + 72 + k0 / 2, S + 8);
+            hand_on(&m->s[half]);
+        }
+        int rest = static_cast<int>(eos - bos);  // tokens, from this chunk on
+        uint32_t st = 0, use = 0;
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it, rest -= C) {
             const uint32_t ph = it & 1;
-            const int64_t rest = eos - bos - static_cast<int64_t>(it) * C;
-            const int left = rest < C ? static_cast<int>(rest) : C;
+            const int left = rest < C ? rest : C;
             const unsigned char *stage = smem + st * STAGE;
             const Decays *d = reinterpret_cast<const Decays *>(stage + OFF_D);
-            store_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
-            arrive_warp(&m->s[half]);
-            if (!(ok = wait_warp(m, &m->full[st], (it / STAGES) & 1))) break;
+            if (!(ok = wait_warp(m, &m->full[st], use & 1))) break;
             // (what does not depend on the MMAs is done while they run)
             const float whole = d->whole, less = d->less;
             if (less < -0.5f) {
@@ -913,8 +918,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 #pragma unroll
             for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::fma2(e[i], pair(r[2 * i], r[2 * i + 1]), z[i]);
             mask(z);
-            store_split(t + COL_KS + t0, t + COL_KS + t0 + 8, z);
-            arrive_warp(&m->z);
+            put_split(t + COL_KS + t0, t + COL_KS + t0 + 8, z);
+            hand_on(&m->z);
             load_decays(d->after);
             if (!(ok = wait_warp(m, &m->xs, ph))) break;
             tc_fence_after();
@@ -923,8 +928,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 #pragma unroll
             for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::mul2(e[i], pair(r[2 * i], r[2 * i + 1]));
             mask(z);
-            store_split(t + COL_X + t0, t + COL_X + t0 + 8, z);
-            arrive_warp(&m->x);
+            put_split(t + COL_X + t0, t + COL_X + t0 + 8, z);
+            hand_on(&m->x);
             if (!STATES) {
                 load_decays(d->out);
                 if (!(ok = wait_warp(m, &m->o, ph))) break;
@@ -951,11 +956,23 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             arrive_warp(&m->empty[st]);
             if (!(ok = wait_warp(m, &m->u, ph))) break;
             tc_fence_after();
-            uint32_t u[32];
-            lin::tmem_ld32(t + COL_U + k0, u);
+            // the update, and the next chunk's operand: the second half of the keys is read while the first is split
+            uint32_t u[2][16];
+            tmem_ld16(t + COL_U + k0, u[0]);
+            tmem_wait_ld();
+            tmem_ld16(t + COL_U + k0 + 16, u[1]);
+            const bool more = it + 1 < chunks;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) S[i] = lin::add2(S[i], pair(u[0][2 * i], u[0][2 * i + 1]));
+            if (more) put_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < KEYS / 2; ++i) S[i] = lin::add2(S[i], pair(u[2 * i], u[2 * i + 1]));
+            for (int i = 0; i < 8; ++i) S[8 + i] = lin::add2(S[8 + i], pair(u[1][2 * i], u[1][2 * i + 1]));
+            if (more) {
+                put_split(t + COL_S + k0 / 2 + 8, t + COL_S + 72 + k0 / 2, S + 8);
+                hand_on(&m->s[half]);
+            }
+            if (++st == STAGES) st = 0, ++use;
         }
         if (is_map) {  // by the columns that it maps from
             if (ok) {
