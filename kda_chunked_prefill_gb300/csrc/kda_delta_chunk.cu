@@ -675,15 +675,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+// x - a, y - b for the pair (a, b) of bf16
+__device__ __forceinline__ uint32_t rest_of(f2 v, uint32_t h) {
+    float x, y;
+    split(v, x, y);
+    asm("{\n\t.reg .b16 a, b, m;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 m, 0xBF80;\n\t"  // -1
+        "fma.rn.f32.bf16 %0, a, m, %0;\n\tfma.rn.f32.bf16 %1, b, m, %1;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "r"(h));
+    return pack_bf16(x, y);
+}
 // 16 values in two bf16 terms: 8 columns of pairs at `hi` and at `lo`
 __device__ __forceinline__ void put_split(uint32_t hi, uint32_t lo, const f2 *v) {
     uint32_t h[8], l[8];
-    const f2 minus = pair(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = lin::bf16_of(v[i]);
     tmem_st8(hi, h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = lin::bf16_of(lin::fma2(lin::of_bf16(h[i]), minus, v[i]));
+    for (int i = 0; i < 8; ++i) l[i] = rest_of(v[i], h[i]);
     tmem_st8(lo, l);
 }
 // what this warp has put is there for the MMAs
