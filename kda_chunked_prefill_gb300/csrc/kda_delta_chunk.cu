@@ -139,105 +139,119 @@ __host__ __device__ inline float time_of(const Work &out, const Work &states, in
     return pass_time(out, heads, sms) + (most > 1 ? pass_time(states, heads, sms) + 0.25f * most + 2.f : 0.f);
 }
 
-constexpr int THREADS = 128, BUCKETS = 64;
+constexpr int THREADS = 128, BUCKETS = 64, HELD = 4096;
 struct Shared {
     Work out[CUTS + 1], states[CUTS + 1];
     int32_t most[CUTS + 1];
     int32_t bucket[2][BUCKETS];  // first segments of each length, long ones first: of the outputs' pass, of the states'
-    int32_t cuts, joined, len, longest, none;
+    int32_t cuts, joined, len, longest;
+    int32_t held[HELD];          // chunks of the first sequences; -1: bounds that are none
 };
 
-__device__ __forceinline__ int chunks_of(const Params &p, int n) {  // -1: bounds that are none
+__device__ __forceinline__ int chunks_of(const Params &p, int n) {
     const int64_t b = p.cu[n], e = p.cu[n + 1];
     if (b < 0 || e < b || e > p.T || p.cu[0] != 0) return -1;
     return static_cast<int>((e - b + C - 1) / C);
 }
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ Work warp_work(Work w) {
+    long long chunks = w.chunks;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) chunks += __shfl_xor_sync(0xffffffffu, chunks, d);
+    return {warp_sum(w.jobs), warp_max(w.longest), chunks, warp_sum(w.cuts)};
+}
 
-// One CTA: the cut by estimates from the lengths, and the segments of both passes, long ones first.
+// One CTA: the cut by estimates from the lengths, and the segments of both passes, long ones first. (The other CTAs' chunks take longer
+// than this only if it is quick: lengths are read once, a warp estimates a cut.)
 __device__ void make(const ChunkParams &cp, Shared *sh) {
     const Params &p = cp.a;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < 2 * BUCKETS; i += THREADS) sh->bucket[i / BUCKETS][i % BUCKETS] = 0;
-    if (tid <= CUTS) sh->out[tid] = sh->states[tid] = Work{0, 0, 0, 0}, sh->most[tid] = 0;
     if (tid == 0) sh->cuts = sh->joined = 0;
+    for (int n = tid; n < p.N; n += THREADS) {
+        const int chunks = chunks_of(p, n);
+        if (chunks < 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
+        if (n < HELD) sh->held[n] = chunks;
+    }
     __syncthreads();
+    auto length = [&](int n) { return n < HELD ? sh->held[n] : chunks_of(p, n); };
     const int candidates = cp.shortest ? CUTS + 1 : 1;  // the last: none is cut
-    for (int c = 0; c < candidates; ++c) {
+    for (int c = warp; c < candidates; c += THREADS / 32) {
         const int len = c == candidates - 1 ? 0x7fffffff : cut_length(c, cp.shortest);
         Work out{0, 0, 0, 0}, states{0, 0, 0, 0};
         int most = 0;
-        for (int n = tid; n < p.N; n += THREADS) {
-            const int chunks = chunks_of(p, n);
-            if (chunks < 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
-            else add_sequence(out, states, most, chunks, len);
+        for (int n = lane; n < p.N; n += 32) {
+            const int chunks = length(n);
+            if (chunks >= 0) add_sequence(out, states, most, chunks, len);
         }
-        auto gather = [](Work &to, const Work &w) {
-            atomicAdd(&to.jobs, w.jobs);
-            atomicMax(&to.longest, w.longest);
-            atomicAdd(&to.cuts, w.cuts);
-            atomicAdd(reinterpret_cast<unsigned long long *>(&to.chunks), static_cast<unsigned long long>(w.chunks));
-        };
-        gather(sh->out[c], out);
-        gather(sh->states[c], states);
-        atomicMax(&sh->most[c], most);
+        out = warp_work(out), states = warp_work(states), most = warp_max(most);
+        if (lane == 0) sh->out[c] = out, sh->states[c] = states, sh->most[c] = most;
     }
     __syncthreads();
-    if (tid == 0) {
-        int best = candidates - 1;
-        float least = 3.0e38f;
-        for (int c = candidates - 1; c >= 0; --c) {
-            // (bad bounds may overlap, and then hold more than the workspace)
-            if (c < candidates - 1 && (sh->out[c].jobs > cp.most_segs || sh->states[c].cuts > cp.most_cuts)) continue;
-            const float t = time_of(sh->out[c], sh->states[c], sh->most[c], p.H, cp.sms);
-            if (t < least) least = t, best = c;
+    if (warp == 0) {
+        float t = 3.0e38f;
+        // (bad bounds may overlap, and then hold more than the workspace)
+        if (lane < candidates && (lane == candidates - 1 || (sh->out[lane].jobs <= cp.most_segs && sh->states[lane].cuts <= cp.most_cuts)))
+            t = time_of(sh->out[lane], sh->states[lane], sh->most[lane], p.H, cp.sms);
+        float least = t;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
+        const int best = 31 - __clz(__ballot_sync(0xffffffffu, t == least && lane < candidates));
+        if (lane == 0) {
+            sh->len = best == candidates - 1 ? 0x7fffffff : cut_length(best, cp.shortest);
+            sh->longest = sh->out[best].longest > 0 ? sh->out[best].longest : 1;
         }
-        sh->len = best == candidates - 1 ? 0x7fffffff : cut_length(best, cp.shortest);
-        sh->longest = sh->out[best].longest > 0 ? sh->out[best].longest : 1;
     }
     __syncthreads();
     auto bucket_of = [&](int len) { return BUCKETS - 1 - static_cast<int>(static_cast<int64_t>(len) * (BUCKETS - 1) / sh->longest); };
     auto for_each = [&](auto &&f) {
         for (int n = tid; n < p.N; n += THREADS) {
-            const int chunks = chunks_of(p, n);
+            const int chunks = length(n);
             if (chunks < 0) continue;
             int one, k;
             parts_of(chunks, sh->len, one, k);
             f(n, chunks, k, one);
         }
     };
-    for_each([&](int, int chunks, int k, int one) {
-        for (int i = 0; i < k; ++i) {
-            const int rest = chunks - i * one, len = rest < one ? rest : one;
-            atomicAdd(&sh->bucket[0][bucket_of(len)], 1);
-            if (i < k - 1) atomicAdd(&sh->bucket[1][bucket_of(len)], i ? 2 : 1);
+    for_each([&](int, int chunks, int k, int one) {  // (all parts but the last are of one length)
+        const int whole = bucket_of(one), last = bucket_of(chunks - (k - 1) * one);
+        if (k > 1) {
+            atomicAdd(&sh->bucket[0][whole], k - 1);
+            atomicAdd(&sh->bucket[1][whole], 2 * k - 3);
         }
+        atomicAdd(&sh->bucket[0][last], 1);
     });
     __syncthreads();
-    if (tid < 2) {
-        int sum = 0;
-        for (int b = 0; b < BUCKETS; ++b) {
-            const int c = sh->bucket[tid][b];
-            sh->bucket[tid][b] = sum;
-            sum += c;
+    if (warp < 2) {
+        int *bucket = sh->bucket[warp];
+        const int x = bucket[2 * lane], y = bucket[2 * lane + 1];
+        int sum = x + y;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += z;
         }
-        cp.counts[tid] = sum;
+        bucket[2 * lane] = sum - x - y;
+        bucket[2 * lane + 1] = sum - y;
+        if (lane == 31) cp.counts[warp] = sum;
     }
     __syncthreads();
     for_each([&](int n, int chunks, int k, int one) {
-        int first = -1;
+        int first = -1, at = 0, at_s = 0;
         if (k > 1) {
             first = atomicAdd(&sh->cuts, k - 1);
             cp.cuts[atomicAdd(&sh->joined, 1)] = {n, first, k - 1};
+            at = atomicAdd(&sh->bucket[0][bucket_of(one)], k - 1);
+            at_s = atomicAdd(&sh->bucket[1][bucket_of(one)], 2 * k - 3);
         }
-        for (int i = 0; i < k; ++i) {
-            const int rest = chunks - i * one, len = rest < one ? rest : one, b = bucket_of(len);
-            cp.segs[atomicAdd(&sh->bucket[0][b], 1)] = {n, i * one, len, i ? first + i - 1 : k > 1 ? -2 - first : -1, -1,
-                                                         i == k - 1 ? 0 : 3};
-            if (i == k - 1) continue;
-            const int at = atomicAdd(&sh->bucket[1][b], i ? 2 : 1);
-            cp.segs_s[at] = {n, i * one, len, -1, first + i, 1};
-            if (i) cp.segs_s[at + 1] = {n, i * one, len, -1, first + i, 2};
+        for (int i = 0; i < k - 1; ++i) {
+            cp.segs[at++] = {n, i * one, one, i ? first + i - 1 : -2 - first, -1, 3};
+            cp.segs_s[at_s++] = {n, i * one, one, -1, first + i, 1};
+            if (i) cp.segs_s[at_s++] = {n, i * one, one, -1, first + i, 2};
         }
+        const int c0 = (k - 1) * one, len = chunks - c0;
+        cp.segs[atomicAdd(&sh->bucket[0][bucket_of(len)], 1)] = {n, c0, len, k > 1 ? first + k - 2 : -1, -1, 0};
     });
     __syncthreads();
     if (tid == 0) cp.counts[2] = sh->joined;
