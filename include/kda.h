@@ -604,7 +604,9 @@ kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *
  * varlen-packed prompts, for layers that share KDA's state [N,H,128,128],
  * packing and serving path:
  *       S <- e^{g_t} S;   S <- S + beta_t k_t (v_t - S^T k_t)^T;   o_t = scale * S^T q_t
- * (Not part of the method's pages.)
+ * It is computed chunk by chunk (64 tokens) on the tensor cores. Long sequences
+ * are cut where there are few: the last bits of a sequence's results depend on
+ * what is beside it in the batch. (Not part of the method's pages.)
  *   q, k          bf16, num_qk_heads heads of 128 channels per token; value head
  *                 h reads query/key head h / (num_heads / num_qk_heads), so
  *                 num_qk_heads divides num_heads. As with KDA, normalising the
@@ -613,7 +615,8 @@ kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *
  *   *_token_stride  elements from one token to the next (>= heads x 128, a
  *                 multiple of 8): q, k and v may be slices of one projection.
  *   g, beta       fp32 [total_tokens, num_heads]: natural-log decay, g <= 0 (-inf
- *                 forgets everything), and the strength of erasing and writing.
+ *                 forgets everything, and a g below -138 counts as -inf),
+ *                 and the strength of erasing and writing.
  *   cu_seqlens    int32 [num_seqs + 1]: cu[0] = 0, nondecreasing, cu[num_seqs] <=
  *                 total_tokens. Rows of o behind the last sequence are left as
  *                 they were, and q, k, v, g, beta there are not used.
@@ -628,8 +631,15 @@ kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *
  *                 sequence is skipped), KDA_ERR_TIMEOUT.
  *   workspace     kda_gated_delta_chunk_fwd_workspace_size(...) bytes, 256-byte
  *                 aligned (NULL when that is 0); not shared by calls that overlap.
+ * Precision: products of bf16 operands with fp32 accumulation; the state is kept
+ * and updated in fp32. What depends on it, and the chunk's inverse, enter products
+ * in two bf16 terms (relative error of final_state about 6e-6); the decayed scores
+ * that reach o are rounded once to bf16, as o is.
+ * The workspace takes 400 bytes a token and head (25.8 KB a chunk), and twice a
+ * state for each cut, of which there are at most about as many as SMs.
  * q, k, v, g, beta must be finite (g may be -inf): another value may reach every
- * output of its sequence and head from the start of its chunk on. Alignment: q, k, v, o and the
+ * output of its sequence and head from the start of its chunk on (a long
+ * sequence's: of all of it). Alignment: q, k, v, o and the
  * states 16 bytes, g, beta, cu_seqlens and status_dev 4.
  */
 kda_status_t kda_gated_delta_chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
@@ -639,6 +649,27 @@ kda_status_t kda_gated_delta_chunk_fwd(const void *q, const void *k, const void 
                                        const float *initial_state, float scale, void *o, float *final_state,
                                        int32_t *status_dev, void *workspace, size_t workspace_bytes,
                                        kda_stream_t stream);
+
+/*
+ * kda_gated_delta_chunk_fwd_debug, kda_scaled_matmul_debug — the calls for
+ * testing the failure detection without a GPU fault. withhold is the number of
+ * the chunk, counted from 0 in each thread block, or of the group of four blocks
+ * of 128 channels, of which an operand or its scales are not handed on (-1: none
+ * withheld, the plain call; below that KDA_ERR_INVALID_ARG). What waits for
+ * it gives up after 20000 waits of up to 0.1 ms each, the device reports
+ * KDA_ERR_TIMEOUT in status_dev, every block leaves and the context stays
+ * usable; the outputs are then unspecified. Blocks with fewer withhold nothing.
+ */
+kda_status_t kda_gated_delta_chunk_fwd_debug(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                             const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                             int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k,
+                                             int32_t head_dim_v, int64_t q_token_stride, int64_t k_token_stride,
+                                             int64_t v_token_stride, const float *initial_state, float scale, void *o,
+                                             float *final_state, int32_t *status_dev, void *workspace,
+                                             size_t workspace_bytes, kda_stream_t stream, int32_t withhold);
+kda_status_t kda_scaled_matmul_debug(const void *x, const float *x_scale, int32_t x_scale_per_block, const void *weight,
+                                     const float *weight_scale, int64_t rows, int32_t width, int32_t outs, void *y,
+                                     int32_t *status_dev, kda_stream_t stream, int32_t withhold);
 
 /* Workspace bytes of kda_gated_delta_chunk_fwd for these sizes on the current
  * device (0: none needed, or invalid arguments). */

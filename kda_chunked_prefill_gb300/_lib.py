@@ -41,8 +41,8 @@ EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_stat
             "kda_chunk_fwd_host_buffer_size", "kda_decode_fwd",
             "kda_chunk_fwd_launches", "kda_linear_chunk_fwd", "kda_linear_chunk_fwd_debug", "kda_linear_chunk_fwd_workspace_size",
             "kda_linear_decode_fwd", "kda_state_store", "kda_state_load", "kda_add_rms_norm",
-            "kda_gated_delta_chunk_fwd", "kda_gated_delta_chunk_fwd_workspace_size", "kda_gated_delta_decode_fwd",
-            "kda_gated_rms_norm", "kda_scaled_matmul",
+            "kda_gated_delta_chunk_fwd", "kda_gated_delta_chunk_fwd_debug", "kda_gated_delta_chunk_fwd_workspace_size", "kda_gated_delta_decode_fwd",
+            "kda_gated_rms_norm", "kda_scaled_matmul", "kda_scaled_matmul_debug",
             "kda_status_string", "kda_version")
 DECODE_MAX_TOKENS = 64
 NORM_MAX_WIDTH = 32768
@@ -123,6 +123,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_gated_delta_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, i64, i64, i64, vp,
                                                   f32, vp, vp, vp, vp, ctypes.c_size_t, vp]
         lib.kda_gated_delta_chunk_fwd.restype = ctypes.c_int
+        lib.kda_gated_delta_chunk_fwd_debug.argtypes = lib.kda_gated_delta_chunk_fwd.argtypes + [i32]
+        lib.kda_gated_delta_chunk_fwd_debug.restype = ctypes.c_int
         lib.kda_gated_delta_chunk_fwd_workspace_size.argtypes = [i32, i64, i32]
         lib.kda_gated_delta_chunk_fwd_workspace_size.restype = ctypes.c_size_t
         lib.kda_gated_delta_decode_fwd.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64, i64, i64, vp, f32,
@@ -132,6 +134,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_gated_rms_norm.restype = ctypes.c_int
         lib.kda_scaled_matmul.argtypes = [vp, vp, i32, vp, vp, i64, i32, i32, vp, vp, vp]
         lib.kda_scaled_matmul.restype = ctypes.c_int
+        lib.kda_scaled_matmul_debug.argtypes = lib.kda_scaled_matmul.argtypes + [i32]
+        lib.kda_scaled_matmul_debug.restype = ctypes.c_int
         lib.kda_chunk_fwd_workspace_size.argtypes = [i32, i32]
         lib.kda_chunk_fwd_workspace_size.restype = ctypes.c_size_t
         lib.kda_chunk_fwd_launches.argtypes = [i32, i64, i32]
@@ -840,7 +844,8 @@ def gated_delta_workspace_size(num_seqs: int, total_tokens: int, num_heads: int)
     return int(load_library().kda_gated_delta_chunk_fwd_workspace_size(int(num_seqs), int(total_tokens), int(num_heads)))
 
 
-def _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, final_state, status, stream, workspace):
+def _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, final_state, status, stream, workspace,
+                 withhold=None):
     index, T, H, Hk, D, V, qs, ks, vs = inputs
     N = cu_seqlens.shape[0] - 1
     _need(cu_seqlens, "cu_seqlens", _I32, (N + 1,), index)
@@ -856,14 +861,17 @@ def _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, 
                 workspace = torch.empty(need, dtype=_U8, device=q.device)
     elif workspace.get_device() != index or workspace.dtype is not _U8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
-    return _call(lib.kda_gated_delta_chunk_fwd, "kda_gated_delta_chunk_fwd", index,
-                 (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk,
-                  D, V, qs, ks, vs, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
-                  0 if workspace is None else workspace.numel()), stream)
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk,
+            D, V, qs, ks, vs, _p(initial_state), scale, o.data_ptr(), _p(final_state), _p(status), _p(workspace),
+            0 if workspace is None else workspace.numel())
+    if withhold is not None:
+        debug = lib.kda_gated_delta_chunk_fwd_debug
+        return _call(lambda *a: debug(*a, withhold), "kda_gated_delta_chunk_fwd_debug", index, args, stream)
+    return _call(lib.kda_gated_delta_chunk_fwd, "kda_gated_delta_chunk_fwd", index, args, stream)
 
 
 def kda_gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state, scale: float, o, final_state, status=None,
-                              stream=None, workspace=None) -> int:
+                              stream=None, workspace=None, withhold: Optional[int] = None) -> int:
     """Call the C entry point ``kda_gated_delta_chunk_fwd`` with caller-allocated outputs.
 
     q, k: bf16 [T,Hk,128]; v: bf16 [T,H,128], H a multiple of Hk (tokens may be
@@ -871,13 +879,15 @@ def kda_gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state, scale
     final_state: fp32 [N,H,128,128] or None (may be the same tensor); o: bf16
     [T,H,128]; status: int32 [1] or None; workspace: uint8 tensor of
     ``gated_delta_workspace_size(N, T, H)`` bytes (default: a new one from torch's
-    allocator for the call's stream). All on one CUDA device. Raises ``KdaError``
-    on a host-side error; returns ``KDA_OK`` once queued.
+    allocator for the call's stream). All on one CUDA device. ``withhold`` calls
+    ``kda_gated_delta_chunk_fwd_debug`` with this number. Raises ``KdaError`` on a
+    host-side error; returns ``KDA_OK`` once queued.
     """
     N = cu_seqlens.shape[0] - 1
     inputs = _delta_inputs(q, k, v, g, beta, initial_state, N)
     _delta_outputs(inputs, o, final_state, status, N)
-    return _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, final_state, status, stream, workspace)
+    return _delta_chunk(inputs, q, k, v, g, beta, cu_seqlens, initial_state, scale, o, final_state, status, stream, workspace,
+                        withhold)
 
 
 def gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state=None, scale: Optional[float] = None,
@@ -1017,23 +1027,27 @@ def _product_inputs(x, x_scale, weight, weight_scale):
     return index, lead, K, N, int(per_block)
 
 
-def _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream):
+def _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream, withhold=None):
     index, lead, K, N, per_block = inputs
-    return _call(load_library().kda_scaled_matmul, "kda_scaled_matmul", index,
-                 (x.data_ptr(), x_scale.data_ptr(), per_block, weight.data_ptr(), weight_scale.data_ptr(), lead.numel(), K, N,
-                  y.data_ptr(), _p(status)), stream)
+    lib = load_library()
+    args = (x.data_ptr(), x_scale.data_ptr(), per_block, weight.data_ptr(), weight_scale.data_ptr(), lead.numel(), K, N,
+            y.data_ptr(), _p(status))
+    if withhold is not None:
+        return _call(lambda *a: lib.kda_scaled_matmul_debug(*a, withhold), "kda_scaled_matmul_debug", index, args, stream)
+    return _call(lib.kda_scaled_matmul, "kda_scaled_matmul", index, args, stream)
 
 
-def kda_scaled_matmul(x, x_scale, weight, weight_scale, y, status=None, stream=None) -> int:
+def kda_scaled_matmul(x, x_scale, weight, weight_scale, y, status=None, stream=None, withhold: Optional[int] = None) -> int:
     """Call the C entry point ``kda_scaled_matmul``: x float8_e4m3fn [..., K] with
     x_scale fp32 [...] or [..., ceil(K/128)]; weight float8_e4m3fn [N,K] with
-    weight_scale fp32 [ceil(N/128), ceil(K/128)]; y bf16 [..., N]; status: int32 [1] or None."""
+    weight_scale fp32 [ceil(N/128), ceil(K/128)]; y bf16 [..., N]; status: int32 [1] or
+    None. ``withhold`` calls ``kda_scaled_matmul_debug`` with this number."""
     inputs = _product_inputs(x, x_scale, weight, weight_scale)
     index, lead, _, N, _ = inputs
     _need(y, "y", _BF16, (*lead, N), index)
     if status is not None:
         _need(status, "status", _I32, (1,), index)
-    return _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream)
+    return _product_call(inputs, x, x_scale, weight, weight_scale, y, status, stream, withhold)
 
 
 def scaled_matmul(x, x_scale, weight, weight_scale, check: bool = False, stream=None):

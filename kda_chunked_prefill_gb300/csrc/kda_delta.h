@@ -27,8 +27,9 @@ struct Params {
 // the recurrence, token after token (few tokens per sequence)
 cudaError_t launch_recurrent(const Params &p, cudaStream_t stream);
 
-// chunk by chunk on the tensor cores
-cudaError_t launch_chunked(const Params &p, void *workspace, cudaStream_t stream);
+// chunk by chunk on the tensor cores; withhold, for tests of the failure detection: the number of the chunk of each CTA whose operand
+// is not handed on to the tensor cores (-1: none)
+cudaError_t launch_chunked(const Params &p, void *workspace, cudaStream_t stream, int withhold);
 size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H);
 
 }  // namespace delta

@@ -54,17 +54,11 @@ kda_status_t delta_args(const void *q, const void *k, const void *v, const float
     return KDA_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-kda_status_t kda_gated_delta_chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
-                                       const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
-                                       int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
-                                       int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
-                                       const float *initial_state, float scale, void *o, float *final_state,
-                                       int32_t *status_dev, void *workspace, size_t workspace_bytes,
-                                       kda_stream_t stream) {
+kda_status_t chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta, const int32_t *cu_seqlens,
+                       int32_t num_seqs, int64_t total_tokens, int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k,
+                       int32_t head_dim_v, int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                       const float *initial_state, float scale, void *o, float *final_state, int32_t *status_dev,
+                       void *workspace, size_t workspace_bytes, kda_stream_t stream, int32_t withhold) {
     kda::delta::Params p;
     const kda_status_t rc = delta_args(q, k, v, g, beta, num_seqs, total_tokens, num_heads, num_qk_heads, head_dim_k,
                                        head_dim_v, q_token_stride, k_token_stride, v_token_stride, initial_state, scale,
@@ -77,7 +71,36 @@ kda_status_t kda_gated_delta_chunk_fwd(const void *q, const void *k, const void 
     if (status_dev && cudaMemsetAsync(status_dev, 0, sizeof(int32_t), s) != cudaSuccess) return KDA_ERR_CUDA;
     if (num_seqs == 0) return KDA_OK;
     p.cu = cu_seqlens;
-    return kda::delta::launch_chunked(p, workspace, s) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return kda::delta::launch_chunked(p, workspace, s, withhold) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_gated_delta_chunk_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                       const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                       int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k, int32_t head_dim_v,
+                                       int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                       const float *initial_state, float scale, void *o, float *final_state,
+                                       int32_t *status_dev, void *workspace, size_t workspace_bytes,
+                                       kda_stream_t stream) {
+    return chunk_fwd(q, k, v, g, beta, cu_seqlens, num_seqs, total_tokens, num_heads, num_qk_heads, head_dim_k, head_dim_v,
+                     q_token_stride, k_token_stride, v_token_stride, initial_state, scale, o, final_state, status_dev,
+                     workspace, workspace_bytes, stream, -1);
+}
+
+kda_status_t kda_gated_delta_chunk_fwd_debug(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                                             const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                             int32_t num_heads, int32_t num_qk_heads, int32_t head_dim_k,
+                                             int32_t head_dim_v, int64_t q_token_stride, int64_t k_token_stride,
+                                             int64_t v_token_stride, const float *initial_state, float scale, void *o,
+                                             float *final_state, int32_t *status_dev, void *workspace,
+                                             size_t workspace_bytes, kda_stream_t stream, int32_t withhold) {
+    if (withhold < -1) return KDA_ERR_INVALID_ARG;
+    return chunk_fwd(q, k, v, g, beta, cu_seqlens, num_seqs, total_tokens, num_heads, num_qk_heads, head_dim_k, head_dim_v,
+                     q_token_stride, k_token_stride, v_token_stride, initial_state, scale, o, final_state, status_dev,
+                     workspace, workspace_bytes, stream, withhold);
 }
 
 size_t kda_gated_delta_chunk_fwd_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t num_heads) {

@@ -77,6 +77,7 @@ struct ChunkParams {
     unsigned char *images;  // [slot][head]
     int64_t slots;
     // sequences that are cut (device memory in the workspace)
+    int32_t withhold;       // tests: the chunk of each CTA whose Z is not handed on (-1: none)
     int32_t shortest;       // shortest cut that the workspace is sized for, in chunks; 0: none is cut
     int32_t sms;
     int32_t most_segs, most_cuts;  // that the workspace holds
@@ -134,9 +135,9 @@ __host__ __device__ inline float pass_time(const Work &w, int heads, int sms) {
     const float t = even < rounds ? even : rounds;
     return w.jobs == 0 ? 0.f : t > one ? t : one;
 }
-// With the join (a quarter of a chunk's time a part) and two more launches.
+// With the join (0.6 of a chunk's time a part) and two more launches.
 __host__ __device__ inline float time_of(const Work &out, const Work &states, int most, int heads, int sms) {
-    return pass_time(out, heads, sms) + (most > 1 ? pass_time(states, heads, sms) + 0.25f * most + 2.f : 0.f);
+    return pass_time(out, heads, sms) + (most > 1 ? pass_time(states, heads, sms) + 0.6f * most + 2.f : 0.f);
 }
 
 constexpr int THREADS = 128, BUCKETS = 64, HELD = 4096;
@@ -942,7 +943,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::fma2(e[i], pair(r[2 * i], r[2 * i + 1]), z[i]);
             mask(z);
             put_split(t + COL_KS + t0, t + COL_KS + t0 + 8, z);
-            hand_on(&m->z);
+            if (it != cp.withhold) hand_on(&m->z);
             load_decays(d->after);
             if (!(ok = wait_warp(m, &m->xs, ph))) break;
             tc_fence_after();
@@ -1188,7 +1189,7 @@ size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
     return sms < 1 ? 0 : layout_of(N, T, H, shortest_cut(N, T, H, sms)).bytes;
 }
 
-cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream) {
+cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream, int withhold) {
     if (a.T < 1) return launch_recurrent(a, stream);  // (states pass through)
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
@@ -1198,6 +1199,7 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     if (!encode_heads(&p.tq, a.q, a.T, hk, a.qs) || !encode_heads(&p.tk, a.k, a.T, hk, a.ks) ||
         !encode_heads(&p.tv, a.v, a.T, a.H, a.vs))
         return cudaErrorInvalidValue;
+    p.withhold = withhold;
     p.shortest = shortest_cut(a.N, a.T, a.H, sms);
     const Layout l = layout_of(a.N, a.T, a.H, p.shortest);
     unsigned char *ws = static_cast<unsigned char *>(workspace);

@@ -86,6 +86,7 @@ struct Params {
     int64_t tiles;
     int32_t splits;   // CTAs of a cluster that share a tile
     int32_t tiled_y;  // y leaves by tiled stores
+    int32_t withhold; // tests: the group of blocks of each CTA whose scales are not handed on (-1: none)
     __nv_bfloat16 *out;
     int32_t *status;
 };
@@ -194,97 +195,97 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
     const int b1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / splits);
 
     if (warp < FIRST_SUM_WARP) {
-    if (C::UNEVEN) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
-    if (warp == 0 && lane == 0) {
-        uint32_t it = 0;
-        bool ok = true;
-        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
-            int lt, ct;
-            tile_at(p, tile, lt, ct);
-            for (int b = b0; b < b1; ++b, ++it) {
-                const uint32_t st = it % C::STAGES, use = it / C::STAGES;
-                if (!(ok = wait(m, &m->empty[st], (use & 1) ^ 1))) break;
-                unsigned char *s = smem + st * C::STAGE;
-                mbar_arrive_expect_tx(&m->full[st], C::STAGE);
-                tma_load_2d(s, &p.a, b * KB, lt * LANES, &m->full[st]);
-                tma_load_2d(s + C::A_BYTES, &p.b, b * KB, ct * BN, &m->full[st]);
-            }
-        }
-        if (!ok)  // what is in flight lands before the CTA ends
-            for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
-                wait_drain(&m->full[i % C::STAGES], (i / C::STAGES) & 1);
-    } else if (warp == 1 || warp == 3) {
-        // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues. Its instructions
-        // count: the sums' push them out of the first instruction cache.
-        constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(LANES >> 4) << 24);
-        const uint32_t buf = static_cast<uint32_t>(warp >> 1), d = tmem + buf * BN;
-        const uint64_t a0 = umma_desc_sw128(smem_u32(smem), 16, 1024);
-        const int64_t tiles = tile0 < p.tiles ? (p.tiles - 1 - tile0) / tile_step + 1 : 0;
-        const int64_t blocks = tiles * (b1 - b0);  // in all; every second is this thread's
-        uint32_t st = buf % C::STAGES, use = buf / C::STAGES, n = 0;
-        bool ok = true;
-#pragma unroll 1
-        for (int64_t it = buf; it < blocks; it += 2, ++n) {
-            // In this order: that the sums are through with block it - 2, and so with every block before, says that this stage's
-            // last use, perhaps the other warp's, is over. Its parity alone would take the phase before last for this one.
-            if (!(ok = wait_warp(m, &m->tempty[buf], (n & 1) ^ 1) && wait_warp(m, &m->full[st], use & 1))) break;
-            tc_fence_after();
-            const uint64_t a = a0 + st * (C::STAGE / 16), b = a + C::A_BYTES / 16;
-            if (lin::elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) umma_e4m3(d, a + 2 * k, b + 2 * k, ID, k > 0);
-                umma_commit(&m->empty[st]);
-                umma_commit(&m->tfull[buf]);
-            }
-            st += 2;
-            if (st >= C::STAGES) st -= C::STAGES, ++use;
-        }
-        __syncwarp();
-        if (!ok) {
-            if (lin::elect_one()) umma_commit(&m->drained[buf]);
-            __syncwarp();
-            wait_drain(&m->drained[buf], 0);
-        }
-    } else if (warp == 2) {
-        uint32_t it = 0;
-        bool ok = true;
-        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
-            int lt, ct;
-            tile_at(p, tile, lt, ct);
-            const int row0 = SWAP ? ct * BN : lt * LANES;
-            const int out_block = SWAP ? lt : ct * BN / KB;
-            const int out_blocks = (p.outs + KB - 1) / KB;
-            constexpr int PER = SWAP ? (BN + 31) / 32 : LANES / 32;  // rows of a lane
-            for (int b = b0; ok && b < b1; b += AHEAD) {
-                float xs[AHEAD][PER], ws[AHEAD][C::GROUPS];
-#pragma unroll
-                for (int a = 0; a < AHEAD; ++a) {
-                    const int bb = b + a < b1 ? b + a : b1 - 1;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int64_t row = row0 + 32 * i + lane;
-                        xs[a][i] = row < p.rows ? __ldg(p.xs + row * p.xs_row + static_cast<int64_t>(bb) * p.xs_block) : 0.f;
-                    }
-#pragma unroll
-                    for (int g = 0; g < C::GROUPS; ++g)
-                        ws[a][g] = out_block + g < out_blocks
-                                       ? __ldg(p.ws + static_cast<int64_t>(out_block + g) * p.blocks + bb) : 0.f;
+        if (C::UNEVEN) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
+        if (warp == 0 && lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+                int lt, ct;
+                tile_at(p, tile, lt, ct);
+                for (int b = b0; b < b1; ++b, ++it) {
+                    const uint32_t st = it % C::STAGES, use = it / C::STAGES;
+                    if (!(ok = wait(m, &m->empty[st], (use & 1) ^ 1))) break;
+                    unsigned char *s = smem + st * C::STAGE;
+                    mbar_arrive_expect_tx(&m->full[st], C::STAGE);
+                    tma_load_2d(s, &p.a, b * KB, lt * LANES, &m->full[st]);
+                    tma_load_2d(s + C::A_BYTES, &p.b, b * KB, ct * BN, &m->full[st]);
                 }
-                const uint32_t slot = it % SCALES;
-                if (!(ok = wait_warp(m, &m->sempty[slot], ((it / SCALES) & 1) ^ 1))) break;
-                float *s = scales + slot * (AHEAD * C::SCALE_FLOATS);
+            }
+            if (!ok)  // what is in flight lands before the CTA ends
+                for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
+                    wait_drain(&m->full[i % C::STAGES], (i / C::STAGES) & 1);
+        } else if (warp == 1 || warp == 3) {
+            // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues. Its instructions
+            // count: the sums' push them out of the first instruction cache.
+            constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(LANES >> 4) << 24);
+            const uint32_t buf = static_cast<uint32_t>(warp >> 1), d = tmem + buf * BN;
+            const uint64_t a0 = umma_desc_sw128(smem_u32(smem), 16, 1024);
+            const int64_t tiles = tile0 < p.tiles ? (p.tiles - 1 - tile0) / tile_step + 1 : 0;
+            const int64_t blocks = tiles * (b1 - b0);  // in all; every second is this thread's
+            uint32_t st = buf % C::STAGES, use = buf / C::STAGES, n = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int64_t it = buf; it < blocks; it += 2, ++n) {
+                // In this order: that the sums are through with block it - 2, and so with every block before, says that this stage's
+                // last use, perhaps the other warp's, is over. Its parity alone would take the phase before last for this one.
+                if (!(ok = wait_warp(m, &m->tempty[buf], (n & 1) ^ 1) && wait_warp(m, &m->full[st], use & 1))) break;
+                tc_fence_after();
+                const uint64_t a = a0 + st * (C::STAGE / 16), b = a + C::A_BYTES / 16;
+                if (lin::elect_one()) {
 #pragma unroll
-                for (int a = 0; a < AHEAD; ++a)
+                    for (int k = 0; k < 4; ++k) umma_e4m3(d, a + 2 * k, b + 2 * k, ID, k > 0);
+                    umma_commit(&m->empty[st]);
+                    umma_commit(&m->tfull[buf]);
+                }
+                st += 2;
+                if (st >= C::STAGES) st -= C::STAGES, ++use;
+            }
+            __syncwarp();
+            if (!ok) {
+                if (lin::elect_one()) umma_commit(&m->drained[buf]);
+                __syncwarp();
+                wait_drain(&m->drained[buf], 0);
+            }
+        } else if (warp == 2) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+                int lt, ct;
+                tile_at(p, tile, lt, ct);
+                const int row0 = SWAP ? ct * BN : lt * LANES;
+                const int out_block = SWAP ? lt : ct * BN / KB;
+                const int out_blocks = (p.outs + KB - 1) / KB;
+                constexpr int PER = SWAP ? (BN + 31) / 32 : LANES / 32;  // rows of a lane
+                for (int b = b0; ok && b < b1; b += AHEAD) {
+                    float xs[AHEAD][PER], ws[AHEAD][C::GROUPS];
 #pragma unroll
-                    for (int g = 0; g < C::GROUPS; ++g)
+                    for (int a = 0; a < AHEAD; ++a) {
+                        const int bb = b + a < b1 ? b + a : b1 - 1;
 #pragma unroll
-                        for (int i = 0; i < PER; ++i)
-                            if (!SWAP || BN >= 32 || lane < BN) s[a * C::SCALE_FLOATS + g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
-                arrive_warp(&m->sfull[slot]);
-                ++it;
+                        for (int i = 0; i < PER; ++i) {
+                            const int64_t row = row0 + 32 * i + lane;
+                            xs[a][i] = row < p.rows ? __ldg(p.xs + row * p.xs_row + static_cast<int64_t>(bb) * p.xs_block) : 0.f;
+                        }
+#pragma unroll
+                        for (int g = 0; g < C::GROUPS; ++g)
+                            ws[a][g] = out_block + g < out_blocks
+                                           ? __ldg(p.ws + static_cast<int64_t>(out_block + g) * p.blocks + bb) : 0.f;
+                    }
+                    const uint32_t slot = it % SCALES;
+                    if (!(ok = wait_warp(m, &m->sempty[slot], ((it / SCALES) & 1) ^ 1))) break;
+                    float *s = scales + slot * (AHEAD * C::SCALE_FLOATS);
+#pragma unroll
+                    for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+                        for (int g = 0; g < C::GROUPS; ++g)
+#pragma unroll
+                            for (int i = 0; i < PER; ++i)
+                                if (!SWAP || BN >= 32 || lane < BN) s[a * C::SCALE_FLOATS + g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
+                    if (static_cast<int32_t>(it) != p.withhold) arrive_warp(&m->sfull[slot]);
+                    ++it;
+                }
             }
         }
-    }
     } else {
         if (C::UNEVEN) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SUM));
         const int e = warp - FIRST_SUM_WARP, quad = warp & 3, half = e >> 2;
@@ -432,6 +433,13 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
     const auto kernel = kda_scaled_matmul_kernel<BN, SWAP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
+    if (C::UNEVEN) {
+        static const int regs = [] {
+            cudaFuncAttributes f{};
+            return cudaFuncGetAttributes(&f, kda_scaled_matmul_kernel<BN, SWAP>) == cudaSuccess ? f.numRegs : 0;
+        }();
+        if (regs != C::REGS) return cudaErrorInvalidConfiguration;  // the warps' register split adds up to this
+    }
     const int lanes = SWAP ? p.outs : p.rows, cols = SWAP ? p.rows : p.outs;
     auto operand = [&](CUtensorMap *m, const void *at, int64_t n, int box_rows) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(n)};
@@ -505,9 +513,9 @@ Choice choose(int64_t rows, int64_t outs, int blocks, int sms) {
 }  // namespace mm
 }  // namespace kda
 
-extern "C" kda_status_t kda_scaled_matmul(const void *x, const float *x_scale, int32_t x_scale_per_block, const void *weight,
-                                          const float *weight_scale, int64_t rows, int32_t width, int32_t outs, void *y,
-                                          int32_t *status_dev, kda_stream_t stream) {
+static kda_status_t scaled_matmul(const void *x, const float *x_scale, int32_t x_scale_per_block, const void *weight,
+                                  const float *weight_scale, int64_t rows, int32_t width, int32_t outs, void *y,
+                                  int32_t *status_dev, kda_stream_t stream, int32_t withhold) {
     using kda::checks::aligned;
     if (rows < 0 || width < 1 || outs < 1 || (x_scale_per_block != 0 && x_scale_per_block != 1)) return KDA_ERR_INVALID_ARG;
     if (width % 16 != 0) return KDA_ERR_UNSUPPORTED;
@@ -533,6 +541,7 @@ extern "C" kda_status_t kda_scaled_matmul(const void *x, const float *x_scale, i
     p.outs = outs;
     p.out = static_cast<__nv_bfloat16 *>(y);
     p.status = status_dev;
+    p.withhold = withhold;
     const kda::mm::Choice c = kda::mm::choose(rows, outs, p.blocks, sms);
     cudaError_t e;
     if (rows <= kda::mm::SWAP_ROWS)
@@ -544,4 +553,18 @@ extern "C" kda_status_t kda_scaled_matmul(const void *x, const float *x_scale, i
             : c.bn == 128 ? kda::mm::launch<128, false>(p, x, weight, width, c.splits, sms, s)
                           : kda::mm::launch<256, false>(p, x, weight, width, c.splits, sms, s);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+extern "C" kda_status_t kda_scaled_matmul(const void *x, const float *x_scale, int32_t x_scale_per_block, const void *weight,
+                                          const float *weight_scale, int64_t rows, int32_t width, int32_t outs, void *y,
+                                          int32_t *status_dev, kda_stream_t stream) {
+    return scaled_matmul(x, x_scale, x_scale_per_block, weight, weight_scale, rows, width, outs, y, status_dev, stream, -1);
+}
+
+extern "C" kda_status_t kda_scaled_matmul_debug(const void *x, const float *x_scale, int32_t x_scale_per_block,
+                                                const void *weight, const float *weight_scale, int64_t rows, int32_t width,
+                                                int32_t outs, void *y, int32_t *status_dev, kda_stream_t stream,
+                                                int32_t withhold) {
+    if (withhold < -1) return KDA_ERR_INVALID_ARG;
+    return scaled_matmul(x, x_scale, x_scale_per_block, weight, weight_scale, rows, width, outs, y, status_dev, stream, withhold);
 }

@@ -275,6 +275,55 @@ def test_cut_sequences_with_states_in_place():
     check(x, o, None)
 
 
+def test_many_sequences():
+    """More sequences than the plan holds lengths of, empty ones among them, one long one."""
+    rng = np.random.default_rng(3)
+    lens = [int(n) for n in rng.integers(0, 4, 4300)]
+    lens[17], lens[4299] = 700, 65
+    x = make(lens, 1, 1, seed=57)
+    o, fs = chunk(x)
+    check(x, o, fs)
+
+
+@pytest.mark.parametrize("H,Hk", [(1, 1), (5, 1), (32, 4)])
+def test_lengths_around_chunks_and_cuts(H, Hk):
+    for lens in ([64 * 8 - 1, 64 * 8, 64 * 8 + 1], [1 + 64 * 30], [64 * 31, 2]):
+        x = make(lens, H, Hk, seed=H + len(lens), rate=0.3)
+        o, fs = chunk(x)
+        check(x, o, fs)
+
+
+def test_workspace_given_and_too_small():
+    x = make([300, 65], 2, 2, seed=58)
+    d = dev(x)
+    need = kda.gated_delta_workspace_size(2, 365, 2)
+    o, fs = torch.empty_like(d["v"]), torch.empty_like(d["s0"])
+    ws = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")
+    args = (d["q"], d["k"], d["v"], d["g"], d["beta"], d["cu"], d["s0"], x["scale"], o, fs)
+    kda.kda_gated_delta_chunk_fwd(*args, workspace=ws[:need])
+    check(x, o, fs)
+    assert bool((ws[need:] == 255).all())
+    for bad in (ws[:need - 1], ws[16:16 + need]):
+        with pytest.raises(kda.KdaError) as e:
+            kda.kda_gated_delta_chunk_fwd(*args, workspace=bad)
+        assert e.value.code == kda.KDA_ERR_INVALID_ARG
+
+
+def test_overlapping_lengths_stay_inside_the_workspace():
+    """Bounds that are each in range but run backwards hold more tokens than there are: reported, nothing outside is written."""
+    T, H = 4000, 1
+    x = make([T], H, H, seed=59, state=False)
+    d = dev(x)
+    cu = torch.tensor([0, T] * 40, dtype=torch.int32, device="cuda")
+    N = 79
+    need = kda.gated_delta_workspace_size(N, T, H)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    o, fs = torch.empty_like(d["v"]), torch.empty(N, H, D, D, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_gated_delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], cu, None, x["scale"], o, fs, status, workspace=ws[:need])
+    assert int(status) == kda.KDA_ERR_BAD_SEQLENS and bool((ws[need:] == 255).all())
+
+
 def test_bad_lengths_are_skipped():
     """cu_seqlens that run backwards or past the rows: reported, the other sequences are right."""
     x = make([100, 50, 80], 2, 2, seed=36, extra=20)

@@ -85,6 +85,13 @@ def test_product_refuses(lib, over, code):
     assert _product(lib, **over) == code
 
 
+@pytest.mark.parametrize("withhold", [-2, -2 ** 31])
+def test_debug_forms_refuse(lib, withhold):
+    args = [FAKE] * 6 + [2, 100, 4, 2, 128, 128, 256, 256, 512, None, 0.1, FAKE, None, None, None, 0, None]
+    assert lib.kda_gated_delta_chunk_fwd_debug(*args, withhold) == INVALID
+    assert lib.kda_scaled_matmul_debug(FAKE, FAKE, 1, FAKE, FAKE, 3, 256, 200, FAKE, None, None, withhold) == INVALID
+
+
 def test_calls_with_nothing_to_do(lib):
     assert _chunk(lib, N=0, T=0, q=None, k=None, v=None, g=None, beta=None, cu=None, o=None) == kda.KDA_OK
     assert _decode(lib, N=0, q=None, k=None, v=None, g=None, beta=None, o=None) == kda.KDA_OK
