@@ -604,8 +604,9 @@ kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *
  * varlen-packed prompts, for layers that share KDA's state [N,H,128,128],
  * packing and serving path:
  *       S <- e^{g_t} S;   S <- S + beta_t k_t (v_t - S^T k_t)^T;   o_t = scale * S^T q_t
- * It is computed chunk by chunk (64 tokens) on the tensor cores. Long sequences
- * are cut where there are few: the last bits of a sequence's results depend on
+ * It is computed chunk by chunk (64 tokens) on the tensor cores. Where sequences
+ * have few tokens (16 on average) those of up to 64 run the recurrence itself.
+ * Long sequences are cut where there are few: the last bits of a sequence's results depend on
  * what is beside it in the batch. (Not part of the method's pages.)
  *   q, k          bf16, num_qk_heads heads of 128 channels per token; value head
  *                 h reads query/key head h / (num_heads / num_qk_heads), so

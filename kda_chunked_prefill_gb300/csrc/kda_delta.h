@@ -16,6 +16,7 @@ struct Params {
     int32_t steps;
     int32_t N;
     int64_t T;
+    int64_t longest;  // the recurrence with cu: sequences of more tokens are left out (negative: none is)
     int32_t H, rep;  // value heads; value heads per query/key head
     const float *s0;
     float scale;

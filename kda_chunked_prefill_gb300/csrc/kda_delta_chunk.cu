@@ -46,7 +46,8 @@ static_assert(IMAGE % 128 == 0 && sizeof(Decays) % 16 == 0, "bulk copies");
 // 16-byte group c of row r of a tile
 __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-// Workspace slots of chunks: those of sequence n begin at cu[n] / 64 + n, which leaves each as many as it can need.
+// Workspace slots of chunks: those of sequence n begin at cu[n] / 64 + n, which leaves each as many as it can need. (Where only the long
+// sequences run in chunks: one after the other.)
 __device__ __forceinline__ int64_t slot_base(int64_t bos, int64_t n) { return bos / C + n; }
 
 __device__ __forceinline__ uint64_t evict_normal() {  // (the second launch reads them again)
@@ -62,6 +63,7 @@ __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol
 // A part of a sequence that a CTA walks: chunks c0 .. c0 + len - 1 of sequence n.
 struct Segment {
     int32_t n, c0, len;
+    int32_t slot;   // of its first chunk
     int32_t from;   // the state it begins with: after a cut, its number; -1: the sequence's initial one; -2 - i: cut i's copy of it
     int32_t to;     // of the pass over the states: the cut that its state goes to
     int32_t kind;   // 0: outputs and the sequence's last state, 3: outputs; of the pass over the states, 1: the state, 2: its map
@@ -77,6 +79,7 @@ struct ChunkParams {
     unsigned char *images;  // [slot][head]
     int64_t slots;
     // sequences that are cut (device memory in the workspace)
+    int32_t longer;         // sequences of no more tokens are left out (the recurrence runs them); -1: none is
     int32_t withhold;       // tests: the chunk of each CTA whose Z is not handed on (-1: none)
     int32_t shortest;       // shortest cut that the workspace is sized for, in chunks; 0: none is cut
     int32_t sms;
@@ -145,14 +148,37 @@ struct Shared {
     Work out[CUTS + 1], states[CUTS + 1];
     int32_t most[CUTS + 1];
     int32_t bucket[2][BUCKETS];  // first segments of each length, long ones first: of the outputs' pass, of the states'
-    int32_t cuts, joined, len, longest;
-    int32_t held[HELD];          // chunks of the first sequences; -1: bounds that are none
+    int32_t cuts, joined, len, longest, none;
+    int32_t sums[THREADS / 32];
+    int32_t held[HELD];          // chunks_of() of the first sequences
 };
 
-__device__ __forceinline__ int chunks_of(const Params &p, int n) {
+// -1: bounds that are none; -2: a sequence that is left out
+__device__ __forceinline__ int chunks_of(const ChunkParams &cp, int n) {
+    const Params &p = cp.a;
     const int64_t b = p.cu[n], e = p.cu[n + 1];
     if (b < 0 || e < b || e > p.T || p.cu[0] != 0) return -1;
-    return static_cast<int>((e - b + C - 1) / C);
+    return e - b <= cp.longer ? -2 : static_cast<int>((e - b + C - 1) / C);
+}
+// The sum of x over the CTA's threads before this one, on top of `carry`, which grows by the whole.
+__device__ __forceinline__ int scan(int x, int &carry, int (&sums)[THREADS / 32]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int sum = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    int before = carry + sum - x;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) before += sums[i];
+        carry += sums[i];
+    }
+    return before;
 }
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(0xffffffffu, x); }
@@ -171,12 +197,12 @@ __device__ void make(const ChunkParams &cp, Shared *sh) {
     for (int i = tid; i < 2 * BUCKETS; i += THREADS) sh->bucket[i / BUCKETS][i % BUCKETS] = 0;
     if (tid == 0) sh->cuts = sh->joined = 0;
     for (int n = tid; n < p.N; n += THREADS) {
-        const int chunks = chunks_of(p, n);
-        if (chunks < 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
+        const int chunks = chunks_of(cp, n);
+        if (chunks == -1) set_status(p.status, KDA_ERR_BAD_SEQLENS);
         if (n < HELD) sh->held[n] = chunks;
     }
     __syncthreads();
-    auto length = [&](int n) { return n < HELD ? sh->held[n] : chunks_of(p, n); };
+    auto length = [&](int n) { return n < HELD ? sh->held[n] : chunks_of(cp, n); };
     const int candidates = cp.shortest ? CUTS + 1 : 1;  // the last: none is cut
     for (int c = warp; c < candidates; c += THREADS / 32) {
         const int len = c == candidates - 1 ? 0x7fffffff : cut_length(c, cp.shortest);
@@ -199,12 +225,19 @@ __device__ void make(const ChunkParams &cp, Shared *sh) {
 #pragma unroll
         for (int d = 16; d; d >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
         const int best = 31 - __clz(__ballot_sync(0xffffffffu, t == least && lane < candidates));
+        // Bad bounds may overlap: then there may be more long sequences, or chunks of them, than there is room for. None is run.
+        const Work &all = sh->out[candidates - 1];
+        if (lane == 0) sh->none = cp.longer >= 0 && (all.jobs > cp.most_segs || all.chunks > cp.slots);
         if (lane == 0) {
             sh->len = best == candidates - 1 ? 0x7fffffff : cut_length(best, cp.shortest);
             sh->longest = sh->out[best].longest > 0 ? sh->out[best].longest : 1;
         }
     }
     __syncthreads();
+    if (sh->none) {
+        if (tid < 3) cp.counts[tid] = 0;
+        return;
+    }
     auto bucket_of = [&](int len) { return BUCKETS - 1 - static_cast<int>(static_cast<int64_t>(len) * (BUCKETS - 1) / sh->longest); };
     auto for_each = [&](auto &&f) {
         for (int n = tid; n < p.N; n += THREADS) {
@@ -238,8 +271,15 @@ __device__ void make(const ChunkParams &cp, Shared *sh) {
         if (lane == 31) cp.counts[warp] = sum;
     }
     __syncthreads();
-    for_each([&](int n, int chunks, int k, int one) {
-        int first = -1, at = 0, at_s = 0;
+    int slots = 0;
+    for (int n0 = 0; n0 < p.N; n0 += THREADS) {
+        const int n = n0 + tid, chunks = n < p.N ? length(n) : -1;
+        int slot = 0;
+        if (cp.longer >= 0) slot = scan(chunks > 0 ? chunks : 0, slots, sh->sums);
+        if (chunks < 0) continue;
+        if (cp.longer < 0) slot = static_cast<int>(slot_base(p.cu[n], n));
+        int one, k, first = -1, at = 0, at_s = 0;
+        parts_of(chunks, sh->len, one, k);
         if (k > 1) {
             first = atomicAdd(&sh->cuts, k - 1);
             cp.cuts[atomicAdd(&sh->joined, 1)] = {n, first, k - 1};
@@ -247,13 +287,14 @@ __device__ void make(const ChunkParams &cp, Shared *sh) {
             at_s = atomicAdd(&sh->bucket[1][bucket_of(one)], 2 * k - 3);
         }
         for (int i = 0; i < k - 1; ++i) {
-            cp.segs[at++] = {n, i * one, one, i ? first + i - 1 : -2 - first, -1, 3};
-            cp.segs_s[at_s++] = {n, i * one, one, -1, first + i, 1};
-            if (i) cp.segs_s[at_s++] = {n, i * one, one, -1, first + i, 2};
+            const int c0 = i * one;
+            cp.segs[at++] = {n, c0, one, slot + c0, i ? first + i - 1 : -2 - first, -1, 3};
+            cp.segs_s[at_s++] = {n, c0, one, slot + c0, -1, first + i, 1};
+            if (i) cp.segs_s[at_s++] = {n, c0, one, slot + c0, -1, first + i, 2};
         }
         const int c0 = (k - 1) * one, len = chunks - c0;
-        cp.segs[atomicAdd(&sh->bucket[0][bucket_of(len)], 1)] = {n, c0, len, k > 1 ? first + k - 2 : -1, -1, 0};
-    });
+        cp.segs[atomicAdd(&sh->bucket[0][bucket_of(len)], 1)] = {n, c0, len, slot + c0, k > 1 ? first + k - 2 : -1, -1, 0};
+    }
     __syncthreads();
     if (tid == 0) cp.counts[2] = sh->joined;
 }
@@ -282,6 +323,7 @@ struct Misc {
     float row[C];                       // e^{G_i - (G before i's block)}
     float col[BLOCKS - 1][C - SB];      // e^{(G before block b + 1) - G_j}
     uint64_t full;
+    int32_t sums[THREADS / 32], found[2];
 };
 constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(SMEM * PER_SM <= 227 * 1024, "shared memory");
@@ -309,6 +351,20 @@ __device__ __forceinline__ Two add(Two a, Two b) {
     const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo), hi = s + e;
     return {hi, e - (hi - s)};
 }
+// The same where only long sequences have slots, one after the other (whole CTA); -1: the slot is behind the last.
+__device__ __forceinline__ int find_long(const ChunkParams &cp, int slot, int &chunk, int (&sums)[THREADS / 32], int (&found)[2]) {
+    if (threadIdx.x == 0) found[0] = -1;
+    int slots = 0;
+    for (int n0 = 0; n0 < cp.a.N && slots <= slot; n0 += THREADS) {
+        const int n = n0 + threadIdx.x, c = n < cp.a.N ? plan::chunks_of(cp, n) : 0, chunks = c > 0 ? c : 0;
+        const int first = plan::scan(chunks, slots, sums);
+        if (slot >= first && slot < first + chunks) found[0] = n, found[1] = slot - first;
+    }
+    __syncthreads();
+    chunk = found[1];
+    return found[0];
+}
+
 // 2^(x + y), |y| far below 1
 __device__ __forceinline__ float ex2_2(float x, float y) { return ex2(x) * fmaf(y, 0.6931471805599453f, 1.f); }
 // 2^(a - b)
@@ -361,13 +417,16 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     const int64_t slot = (blockIdx.x - 1) / p.H;
     const int h = static_cast<int>((blockIdx.x - 1) % p.H), hk = h / p.rep;
 
-    const int n = find_sequence(p, slot, lane);
-    const int64_t bos = p.cu[n], eos = p.cu[n + 1];
-    if (bos < 0 || eos < bos || eos > p.T || p.cu[0] != 0) {
-        if (tid == 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
-        return;
+    int n, chunk = 0;
+    if (cp.longer >= 0) {
+        n = find_long(cp, static_cast<int>(slot), chunk, m->sums, m->found);
+        if (n < 0) return;
+    } else {
+        n = find_sequence(p, slot, lane);
     }
-    const int64_t t0 = bos + (slot - slot_base(bos, n)) * C;
+    const int64_t bos = p.cu[n], eos = p.cu[n + 1];
+    if (bos < 0 || eos < bos || eos > p.T || p.cu[0] != 0) return;  // (the plan reports it)
+    const int64_t t0 = bos + (cp.longer >= 0 ? chunk : slot - slot_base(bos, n)) * C;
     if (t0 < bos || t0 >= eos) return;
     const int left = eos - t0 < C ? static_cast<int>(eos - t0) : C;  // rows behind are anything: what they enter is set to zero
 
@@ -751,7 +810,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
 
     if (warp == WARP_LOAD) {
         if (lane == 0) {
-            const unsigned char *images = cp.images + ((slot_base(begin, seg.n) + seg.c0) * p.H + h) * IMAGE;
+            const unsigned char *images = cp.images + (static_cast<int64_t>(seg.slot) * p.H + h) * IMAGE;
             bool ok = true;
             int it = 0;
             for (; it < chunks; ++it) {
@@ -1144,15 +1203,26 @@ int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
     return static_cast<int>(len);
 }
 
+// Batches of few tokens a sequence run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 64.
+// 16 heads: 256 sequences of 16 tokens 260 us and 281 as chunks, of 24 369 and 286; 64 of 16: 73 and 82, 16 of 16: 21 and 23.
+// A batch of so few tokens on average may hold long sequences among many short ones (prompts among single tokens), and the host does
+// not know: those of more than FEW_LONGEST tokens run as chunks all the same, in launches that end at once where there are none.
+bool few_tokens(int64_t N, int64_t T) { return T <= 16 * N; }
+constexpr int FEW_LONGEST = KDA_DECODE_MAX_TOKENS;  // what the recurrence's own entry point takes
+int64_t most_long(int64_t N, int64_t T) { return T / (FEW_LONGEST + 1) < N ? T / (FEW_LONGEST + 1) : N; }
+
 struct Layout {
     int64_t slots, segs, cuts;  // of chunks; parts: ceil(c / L) <= c' / L + 1 summed over the sequences; cuts: (c - 1) / L
+    int shortest;
     size_t images, seg, seg_s, cut, states, bytes;
 };
-Layout layout_of(int64_t N, int64_t T, int64_t H, int shortest) {
+Layout layout_of(int64_t N, int64_t T, int64_t H, int sms) {
     Layout l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    if (few_tokens(N, T)) N = most_long(N, T);
+    l.shortest = shortest_cut(N, T, H, sms);
     l.slots = T / C + N;
-    l.cuts = shortest ? T / (static_cast<int64_t>(C) * shortest) : 0;
+    l.cuts = l.shortest ? T / (static_cast<int64_t>(C) * l.shortest) : 0;
     l.segs = N + l.cuts;
     l.images = 256;
     l.seg = up(l.images + static_cast<size_t>(l.slots * H) * IMAGE);
@@ -1162,6 +1232,8 @@ Layout layout_of(int64_t N, int64_t T, int64_t H, int shortest) {
     l.bytes = l.states + sizeof(float) * 2 * DK * DV * static_cast<size_t>(l.cuts * H);
     return l;
 }
+// nothing runs as chunks
+bool recurrence_only(int64_t N, int64_t T) { return T < 1 || (few_tokens(N, T) && T <= FEW_LONGEST); }
 
 // `after`: its CTAs may be set up while the launch before ends (they wait for it before they read what it wrote).
 cudaError_t launch(void (*kernel)(ChunkParams), int64_t ctas, int threads, int smem, bool after, const ChunkParams &p, cudaStream_t stream) {
@@ -1186,11 +1258,11 @@ cudaError_t launch(void (*kernel)(ChunkParams), int64_t ctas, int threads, int s
 
 size_t chunked_workspace_bytes(int64_t N, int64_t T, int64_t H) {
     const int sms = sm_count();
-    return sms < 1 ? 0 : layout_of(N, T, H, shortest_cut(N, T, H, sms)).bytes;
+    return sms < 1 || recurrence_only(N, T) ? 0 : layout_of(N, T, H, sms).bytes;
 }
 
 cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream, int withhold) {
-    if (a.T < 1) return launch_recurrent(a, stream);  // (states pass through)
+    if (recurrence_only(a.N, a.T)) return launch_recurrent(a, stream);
     const int sms = sm_count();
     if (sms < 1) return cudaErrorInvalidDevice;
     ChunkParams p{};
@@ -1200,8 +1272,16 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
         !encode_heads(&p.tv, a.v, a.T, a.H, a.vs))
         return cudaErrorInvalidValue;
     p.withhold = withhold;
-    p.shortest = shortest_cut(a.N, a.T, a.H, sms);
-    const Layout l = layout_of(a.N, a.T, a.H, p.shortest);
+    const bool few = few_tokens(a.N, a.T);
+    p.longer = few ? FEW_LONGEST : -1;
+    if (few) {
+        Params short_ones = a;
+        short_ones.longest = FEW_LONGEST;
+        const cudaError_t e = launch_recurrent(short_ones, stream);
+        if (e != cudaSuccess) return e;
+    }
+    const Layout l = layout_of(a.N, a.T, a.H, sms);
+    p.shortest = l.shortest;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.counts = reinterpret_cast<int32_t *>(ws);
     p.images = ws + l.images;

@@ -285,6 +285,36 @@ def test_many_sequences():
     check(x, o, fs)
 
 
+@pytest.mark.parametrize("lens,H", [([1] * 255 + [2049], 2), ([0] * 60 + [300, 64, 65, 1] + [2] * 5, 3), ([7] * 30 + [0, 90] + [1] * 3, 2),
+                                    ([16] * 20, 2), ([64, 0, 0, 0, 0, 0, 0, 0], 2), ([0] * 7 + [65, 0], 2),
+                                    ([0] * 800 + [6000, 1, 900], 1)])
+def test_long_sequences_among_short_ones(lens, H):
+    """Few tokens a sequence on average, but not in every one: the long ones run as chunks. States in place."""
+    x = make(lens, H, H, seed=42, extra=5)
+    x["g"][sum(lens):] = float("nan")
+    d = dev(x)
+    o = torch.full_like(d["v"], 7.0)
+    status = torch.ones(1, dtype=torch.int32, device="cuda")
+    kda.kda_gated_delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], d["cu"], d["s0"], x["scale"], o, d["s0"], status)
+    x["g"][sum(lens):] = 0
+    check(x, o, d["s0"])
+    assert int(status) == 0 and bool((o[sum(lens):] == 7.0).all())
+
+
+def test_overlapping_long_sequences_among_short_ones():
+    """Bounds that run backwards in a batch of few tokens a sequence: reported, nothing outside the workspace is written."""
+    T, N = 600, 200
+    x = make([T], 1, 1, seed=60, state=False)
+    d = dev(x)
+    cu = torch.tensor([0, 100] * (N // 2) + [T], dtype=torch.int32, device="cuda")
+    need = kda.gated_delta_workspace_size(N, T, 1)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    o, fs = torch.empty_like(d["v"]), torch.empty(N, 1, D, D, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kda.kda_gated_delta_chunk_fwd(d["q"], d["k"], d["v"], d["g"], d["beta"], cu, None, x["scale"], o, fs, status, workspace=ws[:need])
+    assert int(status) == kda.KDA_ERR_BAD_SEQLENS and bool((ws[need:] == 255).all())
+
+
 @pytest.mark.parametrize("H,Hk", [(1, 1), (5, 1), (32, 4)])
 def test_lengths_around_chunks_and_cuts(H, Hk):
     for lens in ([64 * 8 - 1, 64 * 8, 64 * 8 + 1], [1 + 64 * 30], [64 * 31, 2]):
