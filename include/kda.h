@@ -702,12 +702,14 @@ kda_status_t kda_gated_delta_decode_fwd(const void *q, const void *k, const void
  *   gate          bf16, num_heads heads of 128 channels per token, gate_token_stride
  *                 elements from one token to the next (>= heads x 128, a multiple of 8)
  *   weight        fp32 [128]
- *   silu          act(gate): 0 sigmoid(gate), 1 gate * sigmoid(gate)
+ *   eps           at least 1e-40 (below, squares of the size of eps have too few bits)
+ *   silu          act(gate): 0 sigmoid(gate), 1 gate * sigmoid(gate); a sigmoid
+ *                 below 2^-126 counts as 0
  *   y             e4m3 [tokens, num_heads, 128];  y_scale  fp32 [tokens, num_heads]
  * y and y_scale are the activations of kda_scaled_matmul with one scale per 128
  * channels. Sums and norms are fp32. A row whose max|n| is below 2^-100 gets scale
- * 0 and codes 0; a row with a NaN or an infinite n, or whose sum of squares
- * overflows fp32, gets scale NaN and codes NaN. Alignment: x, gate, weight, y 16 bytes,
+ * 0 and codes 0; a row with a NaN or an infinite n (formed in the order above), or
+ * whose sum of squares overflows fp32, gets scale NaN and codes NaN. Alignment: x, gate, weight, y 16 bytes,
  * y_scale 4. One launch, asynchronous on `stream`.
  */
 kda_status_t kda_gated_rms_norm(const void *x, const void *gate, int64_t gate_token_stride, const float *weight,
@@ -727,8 +729,9 @@ kda_status_t kda_gated_rms_norm(const void *x, const void *gate, int64_t gate_to
  *   y             bf16 [rows, outs]
  *   status_dev    optional device int32, zeroed on the stream; KDA_ERR_TIMEOUT
  * Products and sums of a block on the tensor cores in fp32, over the blocks in
- * fp32 registers; y is rounded once. A NaN code or scale makes NaN what it
- * enters. All tensors contiguous. Alignment: x, weight, y 16 bytes, the others 4.
+ * fp32 registers; y is rounded once. The two scales are multiplied first, in
+ * fp32: where that overflows, y is infinite or NaN. A NaN code or scale makes NaN
+ * what it enters. All tensors contiguous. Alignment: x, weight, y 16 bytes, the others 4.
  * One launch, asynchronous on `stream`, no workspace; the same inputs give the same bits.
  */
 #define KDA_MATMUL_MAX 16777216

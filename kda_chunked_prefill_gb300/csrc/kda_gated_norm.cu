@@ -4,7 +4,8 @@
 //     n = x / sqrt(mean(x^2) + eps) * w * act(gate);  y_scale = max|n| / 448;  y = e4m3(n / y_scale)
 //
 // Sum and maximum come from one reduction: with m = x w act(gate), the codes are e4m3(m 448 / max|m|) and the scale is max|m| / sqrt(
-// mean(x^2) + eps) / 448, so a row is read once and stays in registers. Sixteen lanes take a row, eight channels each (one 16-byte
+// mean(x^2) + eps) / 448, so a row is read once and stays in registers (where max|m| is far from 1, which n need not be, it is read
+// again and n formed in the order above). Sixteen lanes take a row, eight channels each (one 16-byte
 // access of x, gate and, half as wide, y), a row each: what hides the memory's latency is the number of warps.
 //
 // Bound by memory: 5 bytes per channel with bf16 x (2 + 2 in, 1 out), 7 with fp32. The sigmoid is the hardware's 2^x and reciprocal (a
@@ -60,6 +61,20 @@ __device__ __forceinline__ float rcp(float x) {
     return r;
 }
 
+template <bool SILU>
+__device__ __forceinline__ f2 act(f2 gate) {
+    float a, b;
+    split(mul2(gate, pair(-LOG2E, -LOG2E)), a, b);
+    split(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);  // (2^x infinite: closed)
+    const f2 s = pair(rcp(a), rcp(b));
+    return SILU ? mul2(s, gate) : s;
+}
+__device__ __forceinline__ float max_abs_nan(float m, f2 x) {
+    float a, b;
+    split(x, a, b);
+    return max_abs_nan(m, a, b);
+}
+
 // STRIDED: the gate's tokens lie gate_stride elements apart; otherwise like x.
 template <typename X, bool STRIDED, bool SILU>
 __global__ void __launch_bounds__(THREADS, PER_SM)
@@ -69,7 +84,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM)
     const int c = 8 * (threadIdx.x & 15);
     const int64_t row = static_cast<int64_t>(blockIdx.x) * CTA_ROWS + threadIdx.x / 16;
     f2 v[4] = {}, g[4] = {}, w[4];
-    if (row < rows) {
+    auto load_row = [&] {
         load8(x + row * DV + c, v);
         int64_t at = row * DV;
         if (STRIDED) {
@@ -77,21 +92,16 @@ __global__ void __launch_bounds__(THREADS, PER_SM)
             at = t * gate_stride + static_cast<int64_t>(static_cast<uint32_t>(row) - t * heads) * DV;
         }
         load8(gate + at + c, g);
-    }
+    };
+    if (row < rows) load_row();
     load8(weight + c, w);
     f2 sums = 0;
     float mx = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         sums = fma2(v[j], v[j], sums);
-        float a, b;
-        split(mul2(g[j], pair(-LOG2E, -LOG2E)), a, b);
-        split(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);  // (2^x infinite: closed)
-        f2 act = pair(rcp(a), rcp(b));
-        if (SILU) act = mul2(act, g[j]);
-        v[j] = mul2(v[j], mul2(w[j], act));
-        split(v[j], a, b);
-        mx = max_abs_nan(mx, a, b);
+        v[j] = mul2(v[j], mul2(w[j], act<SILU>(g[j])));
+        mx = max_abs_nan(mx, v[j]);
     }
     float sum, half;
     split(sums, sum, half);
@@ -102,17 +112,23 @@ __global__ void __launch_bounds__(THREADS, PER_SM)
         mx = max_abs_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     }
     if (row >= rows) return;  // (a whole half warp)
-    // A sum that is not finite, by a NaN, an infinity or an overflow, marks the whole row; so does an infinite product.
-    const bool fine = sum <= 3.402823466e38f && mx <= 3.402823466e38f;
-    const float rstd = rsqrtf(sum * (1.f / DV) + eps), amax = fine ? mx * rstd : __int_as_float(0x7fc00000);
-    const bool good = amax <= 3.402823466e38f, tiny = amax < TINY;
-    float mul = E4M3_MAX * rcp(mx);
-    if (!(mx > 1e-30f && mx < 1e30f)) {  // where the quotient, or its reciprocal, is out of range: in two factors
-        const float first = mx < 1.f ? 0x1p80f : 0x1p-80f;
+    const float rstd = rsqrtf(sum * (1.f / DV) + eps);
+    float amax = mx * rstd, mul = E4M3_MAX * rcp(mx);
+    if (!(mx > 1e-30f && mx < 1e30f)) {  // the products, or a quotient by them, may be out of range where n is not
+        load_row();
+        load8(weight + c, w);
+        amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], pair(first, first));
-        mul = E4M3_MAX / (mx * first);
+        for (int j = 0; j < 4; ++j) {
+            v[j] = mul2(mul2(mul2(v[j], pair(rstd, rstd)), w[j]), act<SILU>(g[j]));
+            amax = max_abs_nan(amax, v[j]);
+        }
+#pragma unroll
+        for (int s = 8; s; s >>= 1) amax = max_abs_nan(amax, __shfl_xor_sync(0xffffu << (threadIdx.x & 16), amax, s));
+        mul = E4M3_MAX / amax;
     }
+    // A sum that is not finite, by a NaN, an infinity or an overflow, marks the whole row; so does an infinite n.
+    const bool good = sum <= 3.402823466e38f && amax <= 3.402823466e38f, tiny = good && amax < TINY;
     if (tiny) mul = 0.f;
     if (!good) mul = __int_as_float(0x7fc00000);
     if (c == 0) y_scale[row] = tiny ? 0.f : good ? amax * (1.f / E4M3_MAX) : mul;
@@ -144,7 +160,7 @@ extern "C" kda_status_t kda_gated_rms_norm(const void *x, const void *gate, int6
     if (head_dim_v != KDA_HEAD_DIM) return KDA_ERR_UNSUPPORTED;
     if (tokens < 0 || num_heads < 1 || (x_fp32 != 0 && x_fp32 != 1) || (silu != 0 && silu != 1)) return KDA_ERR_INVALID_ARG;
     if (tokens > 0x7fffffffLL / num_heads) return KDA_ERR_UNSUPPORTED;
-    if (!(eps > 0.f && eps < 3.0e38f)) return KDA_ERR_INVALID_ARG;
+    if (!(eps >= 1e-40f && eps < 3.0e38f)) return KDA_ERR_INVALID_ARG;
     if (gate_token_stride < static_cast<int64_t>(num_heads) * KDA_HEAD_DIM || gate_token_stride % 8) return KDA_ERR_INVALID_ARG;
     if (tokens == 0) return KDA_OK;
     if (gate_token_stride > (int64_t{1} << 40) / tokens) return KDA_ERR_UNSUPPORTED;

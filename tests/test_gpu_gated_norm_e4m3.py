@@ -62,6 +62,15 @@ def test_sizes(size, eps):
     check(x, g, w, eps, False, y, scale)
 
 
+@pytest.mark.parametrize("size,weight,eps", [(1e17, 1e21, 1e-5), (1e-18, 1e-21, 1e-40), (1e-5, 1e38, 1e-5), (1e-15, 1e25, 1e-5)])
+def test_products_out_of_range(size, weight, eps):
+    """x * weight overflows or underflows fp32 where n does not; or 448 / n may."""
+    x, g, w = make(9, 2, 10, fp32=True, size=size)
+    w = w * weight
+    y, scale = kda.gated_rms_norm(x.cuda(), g.cuda(), w.cuda(), eps)
+    check(x, g, w, eps, False, y, scale)
+
+
 def test_zero_rows_closed_gates_and_what_is_not_finite():
     x, g, w = make(8, 2, 9)
     x[0, 0] = 0

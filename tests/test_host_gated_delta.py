@@ -63,7 +63,7 @@ def _norm(lib, **over):
 
 @pytest.mark.parametrize("over,code", [
     ({"dv": 64}, UNSUPPORTED), ({"T": -1}, INVALID), ({"T": 2 ** 40}, UNSUPPORTED), ({"H": 0}, INVALID), ({"eps": 0.0}, INVALID),
-    ({"eps": NAN}, INVALID), ({"fp32": 2}, INVALID), ({"silu": -1}, INVALID), ({"gs": 504}, INVALID), ({"gs": 516}, INVALID),
+    ({"eps": NAN}, INVALID), ({"eps": 1e-42}, INVALID), ({"fp32": 2}, INVALID), ({"silu": -1}, INVALID), ({"gs": 504}, INVALID), ({"gs": 516}, INVALID),
     ({"gs": 2 ** 40}, UNSUPPORTED), ({"x": None}, INVALID), ({"gate": OFF8}, INVALID), ({"w": OFF8}, INVALID), ({"y": OFF8}, INVALID),
     ({"ys": OFF2}, INVALID), ({"ys": None}, INVALID)])
 def test_norm_refuses(lib, over, code):
