@@ -1186,24 +1186,25 @@ bool encode_heads(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int he
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, 3, dims, strides, box);
 }
 
-// The shortest cut worth a try, an SM's share of all chunks; 0 where no sequence can be longer, or there is one, as fast whole.
+// The shortest cut worth a try, an SM's share of all chunks; 0 where none pays, which spares two launches (8 us of the 122 of
+// 4 x 2048 tokens and 16 heads, where the host cannot rule it out). Cuts gain most where one sequence holds all tokens: if none pays for
+// that one, none is tried.
 int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
     const int64_t longest = (T + C - 1) / C, all = (T / C + N) * H;
     int64_t len = (all + sms - 1) / sms;
     if (len < 4) len = 4;
-    if (longest <= len) return 0;
-    if (N == 1) {
-        auto time = [&](int cut) {
-            plan::Work out{0, 0, 0, 0}, states{0, 0, 0, 0};
-            int most = 0;
-            plan::add_sequence(out, states, most, static_cast<int>(longest), cut);
-            return plan::time_of(out, states, most, static_cast<int>(H), sms);
-        };
-        bool pays = false;
-        for (int i = 0; i < plan::CUTS; ++i) pays |= time(plan::cut_length(i, static_cast<int>(len))) < time(0x7fffffff);
-        if (!pays) return 0;
+    auto time = [&](int cut) {
+        plan::Work out{0, 0, 0, 0}, states{0, 0, 0, 0};
+        int most = 0;
+        plan::add_sequence(out, states, most, static_cast<int>(longest), cut);
+        return plan::time_of(out, states, most, static_cast<int>(H), sms);
+    };
+    bool pays = false;
+    for (int i = 0; i < plan::CUTS; ++i) {
+        const int cut = plan::cut_length(i, static_cast<int>(len));
+        pays |= cut < longest && time(cut) < time(0x7fffffff);
     }
-    return static_cast<int>(len);
+    return pays ? static_cast<int>(len) : 0;
 }
 
 // Batches of few tokens a sequence run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 64.
