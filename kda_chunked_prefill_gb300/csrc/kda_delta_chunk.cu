@@ -779,37 +779,23 @@ __device__ __forceinline__ void hand_on(uint64_t *bar) {
     arrive_warp(bar);
 }
 
-// STATES: the pass over the states of cut sequences.
+__device__ __forceinline__ void set_up(Misc *m) {
+    for (int i = 0; i < STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], WARPS + 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&m->s[i], WARPS / 2);
+    mbar_init(&m->z, WARPS), mbar_init(&m->x, WARPS), mbar_init(&m->ks, 1), mbar_init(&m->xs, 1), mbar_init(&m->o, 1), mbar_init(&m->u, 1);
+    mbar_init(&m->drained, 1);
+    mbar_fence_init();
+}
+
+// A segment, by the whole CTA. STATES: of the pass over the states of cut sequences.
 template <bool STATES>
-__global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const __grid_constant__ ChunkParams cp) {
+__device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, int h, unsigned char *smem, Misc *m, uint32_t tmem) {
     const Params &p = cp.a;
-    extern __shared__ unsigned char raw[];
-    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int i = 0; i < STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], WARPS + 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&m->s[i], WARPS / 2);
-        mbar_init(&m->z, WARPS), mbar_init(&m->x, WARPS), mbar_init(&m->ks, 1), mbar_init(&m->xs, 1), mbar_init(&m->o, 1), mbar_init(&m->u, 1);
-        mbar_init(&m->drained, 1);
-        m->abort = 0;
-        mbar_fence_init();
-    }
-    const int job = static_cast<int>(blockIdx.x / p.H), h = static_cast<int>(blockIdx.x % p.H), hk = h / p.rep;
-    wait_for_launch();
-    let_next_launch();
-    if (job >= cp.counts[STATES ? 1 : 0]) return;
-    const Segment seg = (STATES ? cp.segs_s : cp.segs)[job];  // (the plan's)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hk = h / p.rep;
     const bool is_map = STATES && seg.kind == 2;
     const int64_t chain = static_cast<int64_t>(seg.n) * p.H + h;
     const int64_t begin = p.cu[seg.n], bos = begin + static_cast<int64_t>(seg.c0) * C, eos = p.cu[seg.n + 1];  // from the segment on
     const int chunks = seg.len;
-
-    if (warp == WARP_MMA) tmem_alloc(&m->tmem, 512);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = m->tmem;
 
     if (warp == WARP_LOAD) {
         if (lane == 0) {
@@ -833,6 +819,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             }
             if (!ok)  // what is in flight lands before the CTA ends
                 for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) wait_drain(&m->full[i % STAGES], (i / STAGES) & 1);
+            else if (STATES)  // the barriers are set up anew for the next segment: no arrival is left out
+                for (int i = it < STAGES ? 0 : it - STAGES; i < it && ok; ++i) ok = wait(m, &m->empty[i % STAGES], (i / STAGES) & 1);
         }
     } else if (warp == WARP_MMA) {
         // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues.
@@ -1087,7 +1075,51 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid == 0 && m->abort) set_status(p.status, KDA_ERR_TIMEOUT);
+}
+
+// The outputs' CTAs have a segment each; those of the pass over the states, no more of them than SMs, one in each round, there and back,
+// as long ones are listed first. (Where no sequence is cut, this launch and the join's end at once, the sooner the fewer CTAs they have:
+// with one for each segment and for each part of the join's columns they took 4.9 us of 16 x 64 tokens and 16 heads, 9.6 of 8 x 1024 and
+// 7.6 of 4 x 2048, and as many as SMs 2.5, 4.8 and 6.0. The outputs' CTAs in rounds as well took 9 to 18 % longer for a chunk: the loop
+// costs registers.)
+template <bool STATES>
+__global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const __grid_constant__ ChunkParams cp) {
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    Misc *m = reinterpret_cast<Misc *>(smem + OFF_MISC);
+    const int tid = threadIdx.x, warp = tid >> 5, H = cp.a.H;
+    if (tid == 0) {
+        set_up(m);
+        m->abort = 0;
+    }
+    int index = static_cast<int>(blockIdx.x);
+    wait_for_launch();
+    let_next_launch();
+    const Segment *segs = STATES ? cp.segs_s : cp.segs;  // (the plan's)
+    const int jobs = cp.counts[STATES ? 1 : 0] * H;
+    if (index >= jobs) return;
+    Segment seg = segs[index / H];
+    if (warp == WARP_MMA) tmem_alloc(&m->tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = m->tmem;
+    walk<STATES>(cp, seg, index % H, smem, m, tmem);
+    if (STATES) {
+#pragma unroll 1
+        for (int round = 1;; ++round) {
+            index = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (index >= jobs || m->abort) break;
+            if (tid == 0) {  // (every arrival has come)
+                for (uint64_t *bar = m->full; bar <= &m->drained; ++bar) lin::mbar_inval(bar);
+                set_up(m);
+            }
+            seg = segs[index / H];
+            __syncthreads();
+            walk<STATES>(cp, seg, index % H, smem, m, tmem);
+        }
+    }
+    if (tid == 0 && m->abort) set_status(cp.a.status, KDA_ERR_TIMEOUT);
     if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
 }
 
@@ -1098,81 +1130,84 @@ namespace join {
 
 constexpr int COLS = 8, PARTS = DV / COLS;
 constexpr int KEYS = 2, SHARES = 8, SHARE = DK / SHARES, THREADS = DK / KEYS * SHARES;
+constexpr int PER_SM = 1;  // CTAs, which take more in turn
 
 // After a cut, E = F E' + N, with E' the state after the cut before, F the map of the part between them and N its state from zero. One
 // CTA has 8 value columns of a sequence and head; a thread two keys and an eighth of the sum's terms, whose factors it loads a cut
 // ahead. fp32 throughout, the sums in one order. Bound by latency: one cut waits for the one before.
 __global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __grid_constant__ ChunkParams cp) {
     __shared__ alignas(16) float E[DK][COLS], sums[SHARES][DK][COLS];
-    const int part = blockIdx.x % PARTS, h = static_cast<int>(blockIdx.x / PARTS % cp.a.H);
     const int key = threadIdx.x % (DK / KEYS), share = threadIdx.x / (DK / KEYS);  // keys key and key + 64
-    const int64_t i = blockIdx.x / PARTS / cp.a.H;
-    wait_for_launch();
-    let_next_launch();
-    if (i >= cp.counts[2]) return;
-    const Cuts cuts = cp.cuts[i];
+    const int mk = threadIdx.x / 4, mc = 2 * (threadIdx.x % 4);  // this thread's two columns of E and N
     constexpr size_t STATE = DK * DV;
     const size_t step = 2 * STATE * cp.a.H;
-    float *at = cp.states + (static_cast<size_t>(cuts.first) * cp.a.H + h) * 2 * STATE;
-    const int mk = threadIdx.x / 4, mc = 2 * (threadIdx.x % 4);  // this thread's two columns of E and N
-    const size_t mine = static_cast<size_t>(mk) * DV + COLS * part + mc;
-    if (const float *s0 = cp.a.s0)
-        *reinterpret_cast<float2 *>(at + STATE + mine) =
-            *reinterpret_cast<const float2 *>(s0 + (static_cast<int64_t>(cuts.n) * cp.a.H + h) * STATE + mine);
-    float f[KEYS][SHARE], ahead[KEYS][SHARE];
-    float2 n = *reinterpret_cast<const float2 *>(at + mine), n_ahead;
-    auto load = [&](const float *state) {
-        n_ahead = *reinterpret_cast<const float2 *>(state + mine);
-#pragma unroll
-        for (int j = 0; j < SHARE; ++j)
-#pragma unroll
-            for (int k = 0; k < KEYS; ++k) ahead[k][j] = __ldcg(state + STATE + (SHARE * share + j) * DK + key + k * (DK / KEYS));
-    };
-    if (cuts.count > 1) load(at + step);
-    *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
+    wait_for_launch();
+    let_next_launch();
+    const int64_t jobs = static_cast<int64_t>(cp.counts[2]) * cp.a.H * PARTS;
 #pragma unroll 1
-    for (int s = 1; s < cuts.count; ++s) {
-        at += step;
-        n = n_ahead;
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int part = static_cast<int>(job % PARTS), h = static_cast<int>(job / PARTS % cp.a.H);
+        const Cuts cuts = cp.cuts[job / PARTS / cp.a.H];
+        float *at = cp.states + (static_cast<size_t>(cuts.first) * cp.a.H + h) * 2 * STATE;
+        const size_t mine = static_cast<size_t>(mk) * DV + COLS * part + mc;
+        if (const float *s0 = cp.a.s0)
+            *reinterpret_cast<float2 *>(at + STATE + mine) =
+                *reinterpret_cast<const float2 *>(s0 + (static_cast<int64_t>(cuts.n) * cp.a.H + h) * STATE + mine);
+        float f[KEYS][SHARE], ahead[KEYS][SHARE];
+        float2 n = *reinterpret_cast<const float2 *>(at + mine), n_ahead;
+        auto load = [&](const float *state) {
+            n_ahead = *reinterpret_cast<const float2 *>(state + mine);
 #pragma unroll
-        for (int j = 0; j < SHARE; ++j)
+            for (int j = 0; j < SHARE; ++j)
 #pragma unroll
-            for (int k = 0; k < KEYS; ++k) f[k][j] = ahead[k][j];
-        if (s + 1 < cuts.count) load(at + step);
-        __syncthreads();
-        f2 x[KEYS][COLS / 2];
+                for (int k = 0; k < KEYS; ++k) ahead[k][j] = __ldcg(state + STATE + (SHARE * share + j) * DK + key + k * (DK / KEYS));
+        };
+        if (cuts.count > 1) load(at + step);
+        *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
+#pragma unroll 1
+        for (int s = 1; s < cuts.count; ++s) {
+            at += step;
+            n = n_ahead;
 #pragma unroll
-        for (int k = 0; k < KEYS; ++k)
+            for (int j = 0; j < SHARE; ++j)
 #pragma unroll
-            for (int c = 0; c < COLS / 2; ++c) x[k][c] = 0;
+                for (int k = 0; k < KEYS; ++k) f[k][j] = ahead[k][j];
+            if (s + 1 < cuts.count) load(at + step);
+            __syncthreads();
+            f2 x[KEYS][COLS / 2];
 #pragma unroll
-        for (int j = 0; j < SHARE; ++j) {
-            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][0]);
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][4]);
+            for (int k = 0; k < KEYS; ++k)
+#pragma unroll
+                for (int c = 0; c < COLS / 2; ++c) x[k][c] = 0;
+#pragma unroll
+            for (int j = 0; j < SHARE; ++j) {
+                const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][0]);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][4]);
+#pragma unroll
+                for (int k = 0; k < KEYS; ++k) {
+                    const f2 a = pair(f[k][j], f[k][j]);
+                    x[k][0] = lin::fma2(a, u.x, x[k][0]);
+                    x[k][1] = lin::fma2(a, u.y, x[k][1]);
+                    x[k][2] = lin::fma2(a, v.x, x[k][2]);
+                    x[k][3] = lin::fma2(a, v.y, x[k][3]);
+                }
+            }
 #pragma unroll
             for (int k = 0; k < KEYS; ++k) {
-                const f2 a = pair(f[k][j], f[k][j]);
-                x[k][0] = lin::fma2(a, u.x, x[k][0]);
-                x[k][1] = lin::fma2(a, u.y, x[k][1]);
-                x[k][2] = lin::fma2(a, v.x, x[k][2]);
-                x[k][3] = lin::fma2(a, v.y, x[k][3]);
+                ulonglong2 *to = reinterpret_cast<ulonglong2 *>(&sums[share][key + k * (DK / KEYS)][0]);
+                to[0] = make_ulonglong2(x[k][0], x[k][1]);
+                to[1] = make_ulonglong2(x[k][2], x[k][3]);
             }
-        }
+            __syncthreads();
 #pragma unroll
-        for (int k = 0; k < KEYS; ++k) {
-            ulonglong2 *to = reinterpret_cast<ulonglong2 *>(&sums[share][key + k * (DK / KEYS)][0]);
-            to[0] = make_ulonglong2(x[k][0], x[k][1]);
-            to[1] = make_ulonglong2(x[k][2], x[k][3]);
+            for (int r = 0; r < SHARES; ++r) {
+                const float2 u = *reinterpret_cast<const float2 *>(&sums[r][mk][mc]);
+                n.x += u.x;
+                n.y += u.y;
+            }
+            *reinterpret_cast<float2 *>(at + mine) = n;
+            *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
         }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < SHARES; ++r) {
-            const float2 u = *reinterpret_cast<const float2 *>(&sums[r][mk][mc]);
-            n.x += u.x;
-            n.y += u.y;
-        }
-        *reinterpret_cast<float2 *>(at + mine) = n;
-        *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
     }
 }
 
@@ -1186,7 +1221,7 @@ bool encode_heads(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int he
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, 3, dims, strides, box);
 }
 
-// The shortest cut worth a try, an SM's share of all chunks; 0 where none pays, which spares two launches (8 us of the 122 of
+// The shortest cut worth a try, an SM's share of all chunks; 0 where none pays, which spares two launches (6 us of the 121 of
 // 4 x 2048 tokens and 16 heads, where the host cannot rule it out). Cuts gain most where one sequence holds all tokens: if none pays for
 // that one, none is tried.
 int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
@@ -1299,9 +1334,10 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.states = reinterpret_cast<float *>(ws + l.states);
     cudaError_t e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H, prep::THREADS, prep::SMEM, false, p, stream);
     if (e == cudaSuccess && p.shortest) {
-        e = launch(walk::kda_gated_delta_chunk_kernel<true>, 2 * l.cuts * a.H, walk::THREADS, walk::SMEM, true, p, stream);
-        const int64_t joined = l.cuts < a.N ? l.cuts : a.N;
-        if (e == cudaSuccess) e = launch(join::kda_gated_delta_join_kernel, joined * a.H * join::PARTS, join::THREADS, 0, true, p, stream);
+        const int64_t parts = 2 * l.cuts * a.H, joins = (l.cuts < a.N ? l.cuts : a.N) * a.H * join::PARTS, most = join::PER_SM * sms;
+        e = launch(walk::kda_gated_delta_chunk_kernel<true>, parts < sms ? parts : sms, walk::THREADS, walk::SMEM, true, p, stream);
+        if (e == cudaSuccess)
+            e = launch(join::kda_gated_delta_join_kernel, joins < most ? joins : most, join::THREADS, 0, true, p, stream);
     }
     return e == cudaSuccess ? launch(walk::kda_gated_delta_chunk_kernel<false>, l.segs * a.H, walk::THREADS, walk::SMEM, true, p, stream)
                             : e;
