@@ -1130,13 +1130,31 @@ namespace join {
 
 constexpr int COLS = 8, PARTS = DV / COLS;
 constexpr int KEYS = 2, SHARES = 8, SHARE = DK / SHARES, THREADS = DK / KEYS * SHARES;
-constexpr int PER_SM = 1;  // CTAs, which take more in turn
+constexpr int STAGES = 2;
+struct Shared {
+    alignas(16) float F[STAGES][DK][DK];         // maps, transposed
+    alignas(16) float E[DK][COLS];
+    alignas(16) float sums[SHARES][2][DK][COLS / 2];  // by halves of the columns: neighbouring keys are neighbours
+};
+static_assert(COLS == 8, "two halves of four columns");
+
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_groups() {  // for all but the last N
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // After a cut, E = F E' + N, with E' the state after the cut before, F the map of the part between them and N its state from zero. One
-// CTA has 8 value columns of a sequence and head; a thread two keys and an eighth of the sum's terms, whose factors it loads a cut
-// ahead. fp32 throughout, the sums in one order. Bound by latency: one cut waits for the one before.
-__global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __grid_constant__ ChunkParams cp) {
-    __shared__ alignas(16) float E[DK][COLS], sums[SHARES][DK][COLS];
+// CTA has 8 value columns of a sequence and head, and an SM's registers; a thread two keys and an eighth of the sum's terms. fp32
+// throughout, the sums in one order. One cut waits for the one before; F (64 KB) comes two cuts ahead. 37 cuts of 4 heads: 58 us, 1.6 a
+// cut, the time of a thread's 260 instructions at four warps a scheduler. (F in registers, one cut ahead: 65 us. Three tf32 products on
+// mma.sync, with F split by each CTA: 74.)
+__global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_join_kernel(const __grid_constant__ ChunkParams cp) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    Shared *m = reinterpret_cast<Shared *>(raw);
     const int key = threadIdx.x % (DK / KEYS), share = threadIdx.x / (DK / KEYS);  // keys key and key + 64
     const int mk = threadIdx.x / 4, mc = 2 * (threadIdx.x % 4);  // this thread's two columns of E and N
     constexpr size_t STATE = DK * DV;
@@ -1153,27 +1171,29 @@ __global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __g
         if (const float *s0 = cp.a.s0)
             *reinterpret_cast<float2 *>(at + STATE + mine) =
                 *reinterpret_cast<const float2 *>(s0 + (static_cast<int64_t>(cuts.n) * cp.a.H + h) * STATE + mine);
-        float f[KEYS][SHARE], ahead[KEYS][SHARE];
-        float2 n = *reinterpret_cast<const float2 *>(at + mine), n_ahead;
-        auto load = [&](const float *state) {
-            n_ahead = *reinterpret_cast<const float2 *>(state + mine);
+        auto load = [&](int s) {  // cut s's map
+            if (s < cuts.count) {
+                const float *from = at + step * s + STATE + 4 * threadIdx.x;
+                float *to = &m->F[s % STAGES][0][0] + 4 * threadIdx.x;
 #pragma unroll
-            for (int j = 0; j < SHARE; ++j)
-#pragma unroll
-                for (int k = 0; k < KEYS; ++k) ahead[k][j] = __ldcg(state + STATE + (SHARE * share + j) * DK + key + k * (DK / KEYS));
+                for (int i = 0; i < DK * DK / 4 / THREADS; ++i) copy16(to + 4 * THREADS * i, from + 4 * THREADS * i);
+            }
+            end_group();
         };
-        if (cuts.count > 1) load(at + step);
-        *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
+        auto load_n = [&](int s) {
+            return s < cuts.count ? *reinterpret_cast<const float2 *>(at + step * s + mine) : make_float2(0.f, 0.f);
+        };
+        load(1);
+        load(2);
+        float2 n = load_n(0), ahead = load_n(1);
+        *reinterpret_cast<float2 *>(&m->E[mk][mc]) = n;
 #pragma unroll 1
         for (int s = 1; s < cuts.count; ++s) {
-            at += step;
-            n = n_ahead;
-#pragma unroll
-            for (int j = 0; j < SHARE; ++j)
-#pragma unroll
-                for (int k = 0; k < KEYS; ++k) f[k][j] = ahead[k][j];
-            if (s + 1 < cuts.count) load(at + step);
+            n = ahead;
+            ahead = load_n(s + 1);
+            wait_groups<1>();
             __syncthreads();
+            const float(*F)[DK] = m->F[s % STAGES] + SHARE * share;
             f2 x[KEYS][COLS / 2];
 #pragma unroll
             for (int k = 0; k < KEYS; ++k)
@@ -1181,11 +1201,12 @@ __global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __g
                 for (int c = 0; c < COLS / 2; ++c) x[k][c] = 0;
 #pragma unroll
             for (int j = 0; j < SHARE; ++j) {
-                const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][0]);
-                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&E[SHARE * share + j][4]);
+                const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&m->E[SHARE * share + j][0]);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&m->E[SHARE * share + j][4]);
 #pragma unroll
                 for (int k = 0; k < KEYS; ++k) {
-                    const f2 a = pair(f[k][j], f[k][j]);
+                    const float f = F[j][key + k * (DK / KEYS)];
+                    const f2 a = pair(f, f);
                     x[k][0] = lin::fma2(a, u.x, x[k][0]);
                     x[k][1] = lin::fma2(a, u.y, x[k][1]);
                     x[k][2] = lin::fma2(a, v.x, x[k][2]);
@@ -1193,20 +1214,21 @@ __global__ void __launch_bounds__(THREADS) kda_gated_delta_join_kernel(const __g
                 }
             }
 #pragma unroll
-            for (int k = 0; k < KEYS; ++k) {
-                ulonglong2 *to = reinterpret_cast<ulonglong2 *>(&sums[share][key + k * (DK / KEYS)][0]);
-                to[0] = make_ulonglong2(x[k][0], x[k][1]);
-                to[1] = make_ulonglong2(x[k][2], x[k][3]);
-            }
+            for (int k = 0; k < KEYS; ++k)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    *reinterpret_cast<ulonglong2 *>(m->sums[share][half][key + k * (DK / KEYS)]) =
+                        make_ulonglong2(x[k][2 * half], x[k][2 * half + 1]);
             __syncthreads();
+            load(s + 2);
 #pragma unroll
             for (int r = 0; r < SHARES; ++r) {
-                const float2 u = *reinterpret_cast<const float2 *>(&sums[r][mk][mc]);
+                const float2 u = *reinterpret_cast<const float2 *>(&m->sums[r][mc / 4][mk][mc % 4]);
                 n.x += u.x;
                 n.y += u.y;
             }
-            *reinterpret_cast<float2 *>(at + mine) = n;
-            *reinterpret_cast<float2 *>(&E[mk][mc]) = n;
+            *reinterpret_cast<float2 *>(at + step * s + mine) = n;
+            *reinterpret_cast<float2 *>(&m->E[mk][mc]) = n;
         }
     }
 }
@@ -1334,10 +1356,10 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.states = reinterpret_cast<float *>(ws + l.states);
     cudaError_t e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H, prep::THREADS, prep::SMEM, false, p, stream);
     if (e == cudaSuccess && p.shortest) {
-        const int64_t parts = 2 * l.cuts * a.H, joins = (l.cuts < a.N ? l.cuts : a.N) * a.H * join::PARTS, most = join::PER_SM * sms;
+        const int64_t parts = 2 * l.cuts * a.H, joins = (l.cuts < a.N ? l.cuts : a.N) * a.H * join::PARTS;
         e = launch(walk::kda_gated_delta_chunk_kernel<true>, parts < sms ? parts : sms, walk::THREADS, walk::SMEM, true, p, stream);
         if (e == cudaSuccess)
-            e = launch(join::kda_gated_delta_join_kernel, joins < most ? joins : most, join::THREADS, 0, true, p, stream);
+            e = launch(join::kda_gated_delta_join_kernel, joins < sms ? joins : sms, join::THREADS, sizeof(join::Shared), true, p, stream);
     }
     return e == cudaSuccess ? launch(walk::kda_gated_delta_chunk_kernel<false>, l.segs * a.H, walk::THREADS, walk::SMEM, true, p, stream)
                             : e;
