@@ -9,7 +9,8 @@
 // access of x, gate and, half as wide, y), a row each: what hides the memory's latency is the number of warps.
 //
 // Bound by memory: 5 bytes per channel with bf16 x (2 + 2 in, 1 out), 7 with fp32. The sigmoid is the hardware's 2^x and reciprocal (a
-// few units in the last place; expf and an IEEE division made the kernel wait for its instructions, 53 an element).
+// few units in the last place; expf and an IEEE division made the kernel wait for its instructions, 53 an element). 8192 tokens, 16 heads,
+// bf16: 17.4 us, 4.9 TB/s of a copy's 6.65, in 6.7 waves of CTAs that each load, reduce and store once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
