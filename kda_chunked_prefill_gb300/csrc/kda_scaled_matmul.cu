@@ -32,6 +32,7 @@
 namespace kda {
 namespace mm {
 
+using lin::f2;
 using lin::mbar_arrive;
 using lin::mbar_wait_some;
 
@@ -104,6 +105,15 @@ __device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
         if (*reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
     }
     return true;
+}
+__device__ __forceinline__ bool is_complete(uint64_t *bar, uint32_t parity) {  // (does not wait)
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
 #pragma unroll 1
@@ -297,64 +307,86 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + col0;
         constexpr int LD = C::COLS < 16 ? C::COLS : 16;  // columns read at a time
         uint32_t it = 0, group = 0;
-        bool ok = true;
+        bool ok = true, ready = false;  // ready: the next block's sum is there
         for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
             int lt, ct;
             tile_at(p, tile, lt, ct);
-            float acc[C::COLS];
+            f2 acc[C::COLS / 2];  // of neighbouring columns
 #pragma unroll
-            for (int i = 0; i < C::COLS; ++i) acc[i] = 0.f;
+            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
             float mine[AHEAD];
-            for (int b = b0; b < b1; ++b, ++it) {
-                const uint32_t buf = it & 1, slot = group % SCALES, in = (b - b0) % AHEAD;
-                const float *s = scales + slot * (AHEAD * C::SCALE_FLOATS);
-                if (in == 0) {
+            const float *s = scales;  // the block's
+            int handed = 0;           // blocks of this group to come
+#pragma unroll 1
+            for (int left = b1 - b0; left > 0; --left, ++it) {
+                const uint32_t buf = it & 1, slot = group % SCALES;
+                if (handed == 0) {
                     if (!(ok = wait_warp(m, &m->sfull[slot], (group / SCALES) & 1))) break;
+                    handed = AHEAD;
+                    s = scales + slot * (AHEAD * C::SCALE_FLOATS);
                     if (!SWAP) {
 #pragma unroll
                         for (int a = 0; a < AHEAD; ++a) mine[a] = s[a * C::SCALE_FLOATS + (col0 / KB) * LANES + my_lane];
-                        arrive_warp(&m->sempty[slot]);
+                        __syncwarp();
+                        lin::mbar_arrive_if(&m->sempty[slot], lane == 0);
                         ++group;
                     }
                 }
-                if (!(ok = wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
+                --handed;
+                if (!__all_sync(0xffffffffu, ready) && !(ok = wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
                 tc_fence_after();
-                const float one = in == 0 ? mine[0] : in == 1 ? mine[1] : in == 2 ? mine[2] : mine[3];
                 uint32_t d[2][LD];
                 tmem_ld(taddr + buf * BN, d[0]);
+                const float one = mine[0];
+#pragma unroll
+                for (int a = 0; a + 1 < AHEAD; ++a) mine[a] = mine[a + 1];
 #pragma unroll
                 for (int c = 0; c < C::COLS; c += LD) {  // (the next columns come while these are added)
                     const uint32_t(&x)[LD] = d[c / LD & 1];
                     tmem_wait_ld();
-                    if (c + LD < C::COLS) tmem_ld(taddr + buf * BN + c + LD, d[c / LD + 1 & 1]);
+                    if (c + LD < C::COLS) {
+                        tmem_ld(taddr + buf * BN + c + LD, d[c / LD + 1 & 1]);
+                    } else {  // all is read: the accumulator is handed back, and the other one asked for, before the last columns are added
+                        tc_fence_before();
+                        __syncwarp();
+                        lin::mbar_arrive_if(&m->tempty[buf], lane == 0);
+                        ready = is_complete(&m->tfull[buf ^ 1], ((it + 1) >> 1) & 1);
+                    }
 #pragma unroll
                     for (int i = 0; i < LD; i += 4) {
                         float4 f = make_float4(one, one, one, one);
-                        if (SWAP) f = *reinterpret_cast<const float4 *>(s + in * C::SCALE_FLOATS + col0 + c + i);
-                        acc[c + i] = fmaf(__uint_as_float(x[i]), f.x, acc[c + i]);
-                        acc[c + i + 1] = fmaf(__uint_as_float(x[i + 1]), f.y, acc[c + i + 1]);
-                        acc[c + i + 2] = fmaf(__uint_as_float(x[i + 2]), f.z, acc[c + i + 2]);
-                        acc[c + i + 3] = fmaf(__uint_as_float(x[i + 3]), f.w, acc[c + i + 3]);
+                        if (SWAP) f = *reinterpret_cast<const float4 *>(s + col0 + c + i);
+                        f2 &a0 = acc[(c + i) / 2], &a1 = acc[(c + i) / 2 + 1];
+                        a0 = lin::fma2(lin::pair(x[i], x[i + 1]), lin::pair(f.x, f.y), a0);
+                        a1 = lin::fma2(lin::pair(x[i + 2], x[i + 3]), lin::pair(f.z, f.w), a1);
                     }
                 }
-                tc_fence_before();
-                arrive_warp(&m->tempty[buf]);
-                if (SWAP && (in == AHEAD - 1 || b == b1 - 1)) {
-                    if (lane == 0) mbar_arrive(&m->sempty[slot]);
+                s += C::SCALE_FLOATS;
+                if (SWAP && (handed == 0 || left == 1)) {
+                    __syncwarp();
+                    lin::mbar_arrive_if(&m->sempty[slot], lane == 0);
                     ++group;
+                    handed = 0;
                 }
             }
             if (!ok) break;
             if (SWAP && splits > 1) {  // (one tile a CTA; the stages are done with)
                 float *red = reinterpret_cast<float *>(smem);
 #pragma unroll
-                for (int i = 0; i < C::COLS; ++i) red[(col0 + i) * C::RED_LD + my_lane] = acc[i];
+                for (int i = 0; i < C::COLS; i += 2) {
+                    float u, v;
+                    lin::split(acc[i / 2], u, v);
+                    red[(col0 + i) * C::RED_LD + my_lane] = u;
+                    red[(col0 + i + 1) * C::RED_LD + my_lane] = v;
+                }
             } else if (SWAP) {
                 const int64_t n = static_cast<int64_t>(lt) * LANES + my_lane;
 #pragma unroll
                 for (int i = 0; i < C::COLS; ++i) {
                     const int64_t t = static_cast<int64_t>(ct) * BN + col0 + i;
-                    if (n < p.outs && t < p.rows) p.out[t * p.outs + n] = __float2bfloat16_rn(acc[i]);
+                    float u, v;
+                    lin::split(acc[i / 2], u, v);
+                    if (n < p.outs && t < p.rows) p.out[t * p.outs + n] = __float2bfloat16_rn(i & 1 ? v : u);
                 }
             } else {
                 // the warp's own 32 rows of y, as panels of PANEL columns, swizzled
@@ -365,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                 for (int c = 0; c < C::COLS; c += 8) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[c + 2 * j], acc[c + 2 * j + 1]);
+                    for (int j = 0; j < 4; ++j) w[j] = lin::bf16_of(acc[c / 2 + j]);
                     *reinterpret_cast<uint4 *>(staging + C::staged(lane, c)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 fence_proxy_async_shared();
