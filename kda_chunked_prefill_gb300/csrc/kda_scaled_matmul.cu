@@ -18,9 +18,11 @@
 // as many CTAs as there are. Where these tiles are fewer than the SMs, the CTAs of a cluster share one: each takes a part of the
 // channels, and they add up their sums through distributed shared memory, in the order of their ranks.
 //
-// What bounds it. Many rows: the sums' warps, which read each block's accumulators from tensor memory and add them, 1030 cycles for
-// 128 x 256 of them where the MMAs take 512 (8192 rows, 2048 channels to 6144 outputs 88 us, 2.3 PFLOP/s, the tensor pipe busy in 48 % of
-// the cycles). Few rows: reading the weight (7 rows, 12288 to 12288: 28 us, 5.4 TB/s).
+// What bounds it. Many rows: an SM's way into shared memory, 48 KB for a block of a 128 x 256 tile at 54 bytes a cycle, as measured by
+// loads alone: 920 cycles, where the MMAs take 512 (8192 rows, 2048 channels to 6144 outputs 86 us, 2.4 PFLOP/s; 80 without the sums). A
+// tile of a pair of CTAs needs 32 KB of each, but then the round trip of the two accumulators that tensor memory has room for bounds it
+// (88 us; 73 without the sums, 64 without MMAs as well). Sixteen warps for the sums instead of eight: 93 us. Few rows: reading the weight
+// (7 rows, 12288 to 12288: 28 us, 5.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
