@@ -275,6 +275,12 @@ def test_cut_sequences_with_states_in_place():
     check(x, o, None)
 
 
+def test_parts_and_joins_in_rounds():
+    """More parts of cut sequences, and more columns to join, than an SM each."""
+    x = make([6000, 7000], 8, 4, seed=61, rate=0.1)
+    check(x, *chunk(x))
+
+
 def test_many_sequences():
     """More sequences than the plan holds lengths of, empty ones among them, one long one."""
     rng = np.random.default_rng(3)

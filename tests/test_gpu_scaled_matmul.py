@@ -94,3 +94,17 @@ def test_replayed_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(y, first)
     check(x, xs, w, ws, first)
+
+
+def test_two_at_once():
+    """Wide, narrow and clustered tiles beside one another on two streams: each holds tensor memory of the SMs that it shares."""
+    cases = [make(2500, 2304, 640, True, 11), make(40, 2048, 2048, False, 12), make(300, 640, 640, True, 13)]
+    d = [[t.cuda() for t in c] for c in cases]
+    want = [kda.scaled_matmul(*c, check=True) for c in d]
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    got = [[kda.scaled_matmul(*d[(i + j) % 3], stream=s) for i in range(6)] for j, s in enumerate(streams)]
+    torch.cuda.synchronize()
+    for j in range(3):
+        for i in range(6):
+            assert torch.equal(got[j][i], want[(i + j) % 3])
