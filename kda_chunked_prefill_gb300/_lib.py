@@ -3,7 +3,8 @@
 Argument marshalling only: tensors are checked for dtype, device, shape and
 contiguity and turned into raw pointers; every step of the computation runs
 in the library's CUDA kernels. There is no fallback: if the library is
-missing or fails to load, these functions raise.
+missing or fails to load, these functions raise. (``_native.so``, where it is
+built, does the same for some plain calls in less host time.)
 """
 from __future__ import annotations
 
@@ -49,6 +50,7 @@ NORM_MAX_WIDTH = 32768
 
 _lock = threading.Lock()
 _lib = None
+_native = None  # the plain calls as native code, once the library is loaded and if they are built
 
 
 class KdaError(RuntimeError):
@@ -144,8 +146,28 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_version.argtypes = []
         lib.kda_version.restype = i32
+        _load_native(lib)
         _lib = lib
         return lib
+
+
+def _load_native(lib):
+    global _native
+    try:
+        from . import _native as native
+    except ImportError:  # not built, or for another torch: every call takes its general path
+        return
+    native.set_entry(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.kda_gated_rms_norm, lib.kda_scaled_matmul, lib.kda_gated_delta_decode_fwd, lib.kda_gated_delta_chunk_fwd,
+        lib.kda_gated_delta_chunk_fwd_workspace_size)))
+    _native = native
+
+
+def _done(result, what):
+    """What a native call returned: an error code, or the outputs."""
+    if type(result) is int:
+        raise KdaError(result, what)
+    return result
 
 
 def status_string(code: int) -> str:
@@ -807,7 +829,8 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, in_place: bool = False,
 
 
 # ------------------------------------------------------------------ the delta rule with one decay per head
-# (Of the calls from here on, those that allocate their outputs do not check them: a small call's host time is its time.)
+# (Of the calls from here on, those that allocate their outputs do not check them, and the plain ones, without a stream or a check, are
+# one native call: a small call's host time is its time. What that does not take, a refused argument among it, goes the general way.)
 def _delta_inputs(q, k, v, g, beta, initial_state, num_seqs):
     """The checks of what kda_gated_delta_chunk_fwd and kda_gated_delta_decode_fwd read, and what they pass on."""
     index = _device_of(q)
@@ -899,6 +922,10 @@ def gated_delta_chunk_fwd(q, k, v, g, beta, cu_seqlens, initial_state=None, scal
     and a device-detected error raises ``KdaError``. Rows of ``o`` behind the last
     sequence are not written.
     """
+    if stream is None and not check and _native is not None:
+        r = _native.gated_delta_chunk(q, k, v, g, beta, cu_seqlens, initial_state, scale, True if output_final_state else False)
+        if r is not None:
+            return _done(r, "kda_gated_delta_chunk_fwd")
     N = cu_seqlens.shape[0] - 1
     inputs = _delta_inputs(q, k, v, g, beta, initial_state, N)
     _, T, H, _, D, V = inputs[:6]
@@ -943,6 +970,10 @@ def gated_delta_decode_fwd(q, k, v, g, beta, num_seqs: int, state=None, scale: O
                            in_place: bool = False, check: bool = False, stream=None):
     """Run ``kda_gated_delta_decode_fwd``; returns ``(o, final_state)``. With
     ``in_place`` the given ``state`` tensor is updated and returned as ``final_state``."""
+    if stream is None and not check and _native is not None:
+        r = _native.gated_delta_decode(q, k, v, g, beta, num_seqs, state, scale, True if in_place else False)
+        if r is not None:
+            return _done(r, "kda_gated_delta_decode_fwd")
     N, steps = _steps(q, num_seqs)
     inputs = _delta_inputs(q, k, v, g, beta, state, N)
     _, T, H, _, D, V = inputs[:6]
@@ -1001,6 +1032,10 @@ def kda_gated_rms_norm(x, gate, weight, eps: float, y, y_scale, activation: str 
 def gated_rms_norm(x, gate, weight, eps: float = 1e-5, activation: str = "sigmoid", stream=None):
     """Run ``kda_gated_rms_norm`` on an attention output x [T,H,128]; returns
     ``(y, y_scale)``, float8_e4m3fn [T,H*128] and fp32 [T,H]."""
+    if stream is None and _native is not None and activation in _ACTIVATIONS:
+        r = _native.gated_rms_norm(x, gate, weight, eps, _ACTIVATIONS[activation])
+        if r is not None:
+            return _done(r, "kda_gated_rms_norm")
     inputs = _gate_inputs(x, gate, weight, activation)
     _, T, H, D = inputs[:4]
     dev = x.device
@@ -1053,6 +1088,10 @@ def kda_scaled_matmul(x, x_scale, weight, weight_scale, y, status=None, stream=N
 def scaled_matmul(x, x_scale, weight, weight_scale, check: bool = False, stream=None):
     """Run ``kda_scaled_matmul``; returns y bf16 [..., N]. With ``check=True`` the
     device status word is read back (a synchronising copy)."""
+    if stream is None and not check and _native is not None:
+        r = _native.scaled_matmul(x, x_scale, weight, weight_scale)
+        if r is not None:
+            return _done(r, "kda_scaled_matmul")
     inputs = _product_inputs(x, x_scale, weight, weight_scale)
     dev = x.device
     with _on(stream):

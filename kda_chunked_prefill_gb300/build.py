@@ -2,7 +2,10 @@
 
 Each ``csrc/*.cu`` file is compiled to an object in parallel, then linked
 into ``kda_chunked_prefill_gb300/libkda.so``. No CMake, no torch extension
-machinery: the library has a plain C ABI (``include/kda.h``).
+machinery: the library has a plain C ABI (``include/kda.h``). Beside it, g++
+compiles ``csrc/kda_binding.cpp`` into ``_native.so``, the plain calls of the
+binding as native code; it depends on the installed torch, and the binding works
+without it (slower on the host).
 """
 from __future__ import annotations
 
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libkda.so")
+NATIVE_SOURCE = os.path.join(CSRC, "kda_binding.cpp")
+NATIVE_PATH = os.path.join(PKG, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -78,8 +83,54 @@ def kernel_stamp(source: str) -> str:
     return h.hexdigest()
 
 
+def build_native(force: bool = False) -> bool:
+    """Compile ``_native.so`` against the installed torch; skipped when nothing has
+    changed. False, with a note on stderr, where that does not work."""
+    import sysconfig
+
+    import torch
+
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    where = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, *(f for d in ("include", "include/torch/csrc/api/include") for f in ("-isystem", os.path.join(where, d))),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], NATIVE_SOURCE,
+           "-L" + os.path.join(where, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+    h = hashlib.sha256((torch.__version__ + sys.version + " ".join(cmd)).encode())
+    for f in (NATIVE_SOURCE, os.path.join(INCLUDE, "kda.h")):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    stamp_file = os.path.join(BUILD_DIR, "native_stamp")
+    if not force and os.path.exists(NATIVE_PATH) and os.path.exists(stamp_file) and open(stamp_file).read() == h.hexdigest():
+        return True
+    try:
+        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+        failed = r.stderr if r.returncode != 0 else None
+    except OSError as e:
+        failed = str(e)
+    if failed is not None:
+        if os.path.exists(NATIVE_PATH):
+            os.remove(NATIVE_PATH)
+        sys.stderr.write(f"_native.so is left out:\n{failed}\n")
+        return False
+    os.replace(tmp, NATIVE_PATH)
+    with open(stamp_file, "w") as fh:
+        fh.write(h.hexdigest())
+    return True
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; skipped when the sources are unchanged since the last build."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        native = ex.submit(build_native, force)
+        path = _build_library(force, verbose)
+        native.result()
+    return path
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     stamp_file = os.path.join(BUILD_DIR, "stamp")
     stamp = _stamp()

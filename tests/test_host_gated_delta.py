@@ -119,6 +119,24 @@ def test_binding_refuses():
         kda.scaled_matmul(x, torch.ones(4), x, torch.ones(1, 2))
 
 
+def test_native_calls_leave_what_is_not_plain(lib):
+    """The native form of a plain call gives back what it does not take; the general one then says why."""
+    if _lib._native is None:
+        pytest.skip("the native calls are not built")
+    t, g = torch.zeros(4, 2, 128, dtype=torch.bfloat16), torch.zeros(4, 2)
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    x = torch.zeros(4, 256, dtype=torch.float8_e4m3fn)
+    n = _lib._native
+    assert n.gated_delta_chunk(t, t, t, g, g, cu, None, None, True) is None
+    assert n.gated_delta_chunk(None, t, t, g, g, 7, None, "x", True) is None
+    assert n.gated_delta_decode(t, t, t, g, g, 4, None, None, False) is None
+    assert n.gated_delta_decode(t, t, t, g, g, 2 ** 70, None, None, False) is None
+    assert n.gated_rms_norm(t, t, torch.ones(128), 1e-5, 0) is None
+    assert n.scaled_matmul(x, torch.ones(4), x, torch.ones(1, 2)) is None
+    with pytest.raises(TypeError):
+        n.scaled_matmul(x, x)
+
+
 def test_oracle_recurrence_closed_forms():
     """With g = 0, beta = 1 and unit keys a token reads back what it wrote, repeated keys replace, orthogonal ones add up; beta =
     0 leaves the decayed state; the chunk's matrix form gives the same."""
