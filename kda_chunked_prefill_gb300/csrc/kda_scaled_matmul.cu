@@ -18,11 +18,14 @@
 // as many CTAs as there are. Where these tiles are fewer than the SMs, the CTAs of a cluster share one: each takes a part of the
 // channels, and they add up their sums through distributed shared memory, in the order of their ranks.
 //
-// What bounds it. Many rows: an SM's way into shared memory, 48 KB for a block of a 128 x 256 tile at 54 bytes a cycle, as measured by
-// loads alone: 920 cycles, where the MMAs take 512 (8192 rows, 2048 channels to 6144 outputs 86 us, 2.4 PFLOP/s; 80 without the sums). A
-// tile of a pair of CTAs needs 32 KB of each, but then the round trip of the two accumulators that tensor memory has room for bounds it
-// (88 us; 73 without the sums, 64 without MMAs as well). Sixteen warps for the sums instead of eight: 93 us. Few rows: reading the weight
-// (7 rows, 12288 to 12288: 28 us, 5.4 TB/s).
+// Wide tiles are a pair's: two CTAs make 256 x 256, each has its 128 lanes' accumulators and half of the columns' operand. An SM takes
+// 54 bytes a cycle into shared memory (measured by loads alone): a tile of 128 x 256 by one CTA needs 48 KB a block, 920 cycles, where its
+// MMAs take 512; of a pair, each CTA needs 32 KB, 610. The two halves of the columns have barriers of their own.
+//
+// What bounds it. Many rows: the round trip of the accumulators, two of which fill tensor memory (read by the sums' warps, arrival at the
+// first CTA, MMAs, commit to both), 800 cycles a block: 8192 rows, 2048 channels to 6144 outputs 78 us, 2.65 PFLOP/s. (Columns in one
+// piece 88 us; one CTA's tiles 86; the pair without the sums 73; sixteen warps for the sums 92; arrivals with release semantics at cluster
+// scope 169.) Few rows: reading the weight (7 rows, 12288 to 12288: 28 us, 5.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -51,9 +54,12 @@ constexpr int WAITS = 20000, WAITS_DRAIN = 100;
 
 template <int BN, bool SWAP>
 struct Cfg {
-    static constexpr int A_BYTES = LANES * KB, B_BYTES = BN * KB, STAGE = A_BYTES + B_BYTES;
+    // of a pair's columns, each CTA has the first or the second 64 of both halves
+    static constexpr bool PAIR = BN == 256;
+    static constexpr int HALVES = PAIR ? 2 : 1;  // of the columns: accumulators with barriers of their own
+    static constexpr int A_BYTES = LANES * KB, B_BOX = PAIR ? BN / 4 : BN, B_BYTES = HALVES * B_BOX * KB, STAGE = A_BYTES + B_BYTES;
     static constexpr int CTAS = BN <= 64 ? 2 : 1;  // per SM
-    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 5 : SWAP ? (BN == 64 ? 4 : 5) : 3;
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 5 : SWAP ? (BN == 64 ? 4 : 5) : 3;
     static constexpr int GROUPS = BN == 256 ? 2 : 1;  // column groups with a weight scale of their own
     static constexpr int SCALE_FLOATS = SWAP ? BN : GROUPS * LANES;
     static constexpr int STAGING = SWAP ? 0 : LANES * BN * 2;  // y's tile, a warp's part after another's
@@ -75,7 +81,7 @@ struct Cfg {
 
 struct Misc {
     uint64_t full[5], empty[5];              // a stage
-    uint64_t tfull[2], tempty[2];            // an accumulator
+    uint64_t tfull[4], tempty[4];            // an accumulator
     uint64_t sfull[SCALES], sempty[SCALES];  // a group's scales
     uint64_t drained[2];
     uint32_t tmem;
@@ -89,8 +95,7 @@ struct Params {
     int32_t xs_block; // and from one block's to the next (0: one scale a row)
     int32_t blocks;   // of channels
     int32_t rows, outs;
-    int32_t lane_tiles;
-    int64_t tiles;
+    int32_t lane_tiles, col_tiles, tiles;
     int32_t splits;   // CTAs of a cluster that share a tile
     int32_t tiled_y;  // y leaves by tiled stores
     int32_t withhold; // tests: the group of blocks of each CTA whose scales are not handed on (-1: none)
@@ -143,13 +148,68 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
                  "r"(c0), "r"(c1), "r"(smem_u32(src))
                  : "memory");
 }
-// kind::f8f6f4 with e4m3 A and B (K-major) and fp32 D: 32 channels
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// the same address in the first CTA of a pair
+__device__ __forceinline__ uint32_t in_leader(const void *p) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+// a CTA's half of a pair's stage: its bytes count at the first CTA's barrier
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t leader_bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(leader_bar)
         : "memory");
+}
+__device__ __forceinline__ void arrive_remote_if(uint32_t bar, bool yes) {  // (no branch)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(yes))
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void alloc(uint32_t *slot, uint32_t ncols) {  // whole warp
+    if (!PAIR) {
+        tmem_alloc(slot, ncols);
+        return;
+    }
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        tmem_dealloc(taddr, ncols);
+}
+// kind::f8f6f4 with e4m3 A and B (K-major) and fp32 D: 32 channels
+template <bool PAIR>
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// arrives at `bar`, of a pair at the barriers of this address of the CTAs in `mask`, once the MMAs so far are complete
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar, uint16_t mask = 3) {
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+            "h"(mask)
+            : "memory");
+    else
+        umma_commit(bar);
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -170,16 +230,16 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-// Tiles in the order they are made: bands of 16 lane tiles, in a band column after column, so that what runs at one time shares
-// few rows of both operands.
-__device__ __forceinline__ void tile_at(const Params &p, int64_t i, int &lane_tile, int &col_tile) {
-    constexpr int BAND = 16;
-    const int64_t col_tiles = p.tiles / p.lane_tiles;
-    const int64_t band = i / (BAND * col_tiles), in = i - band * BAND * col_tiles;
-    const int first = static_cast<int>(band) * BAND;
-    const int height = p.lane_tiles - first < BAND ? p.lane_tiles - first : BAND;
-    lane_tile = first + static_cast<int>(in % height);
-    col_tile = static_cast<int>(in / height);
+// Tiles in the order they are made: bands of BAND lanes, in a band column after column, so that what runs at one time shares few rows of
+// both operands.
+constexpr uint32_t BAND = 2048;
+template <bool PAIR>
+__device__ __forceinline__ void tile_at(const Params &p, int32_t i, int &lane_tile, int &col_tile) {
+    constexpr uint32_t MOST = BAND / LANES / (PAIR ? 2 : 1);
+    const uint32_t wide = MOST * static_cast<uint32_t>(p.col_tiles), band = static_cast<uint32_t>(i) / wide, in = i - band * wide;
+    const uint32_t first = band * MOST, rest = p.lane_tiles - first, height = rest < MOST ? rest : MOST, col = in / height;
+    lane_tile = static_cast<int>(first + in - col * height);
+    col_tile = static_cast<int>(col);
 }
 
 template <int BN, bool SWAP>
@@ -192,21 +252,23 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) mbar_init(&m->full[i], 1), mbar_init(&m->empty[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&m->tfull[i], 1), mbar_init(&m->tempty[i], SUM_WARPS);
+        for (int i = 0; i < 2 * C::HALVES; ++i) mbar_init(&m->tfull[i], 1), mbar_init(&m->tempty[i], SUM_WARPS);
         for (int i = 0; i < SCALES; ++i) mbar_init(&m->sfull[i], 1), mbar_init(&m->sempty[i], SUM_WARPS);
         mbar_init(&m->drained[0], 1), mbar_init(&m->drained[1], 1);
         m->abort = 0;
         mbar_fence_init();
     }
-    if (warp == 3) tmem_alloc(&m->tmem, C::TMEM);
+    if (warp == 3) alloc<C::PAIR>(&m->tmem, C::TMEM);
     tc_fence_before();
     __syncthreads();
+    if (C::PAIR) cluster_sync();  // (both CTAs' barriers are set up)
     tc_fence_after();
     const uint32_t tmem = m->tmem;
 
-    // this CTA's tiles, and its part of their blocks
+    // this CTA's tiles, and its part of their blocks or, of a pair, of their lanes
     const int splits = SWAP ? p.splits : 1, rank = splits > 1 ? static_cast<int>(blockIdx.x) % splits : 0;
-    const int64_t tile0 = blockIdx.x / splits, tile_step = gridDim.x / splits;
+    const int peer = C::PAIR ? static_cast<int>(blockIdx.x) & 1 : 0;
+    const int32_t tile0 = C::PAIR ? blockIdx.x / 2 : blockIdx.x / splits, tile_step = C::PAIR ? gridDim.x / 2 : gridDim.x / splits;
     const int b0 = static_cast<int>(static_cast<int64_t>(p.blocks) * rank / splits);
     const int b1 = static_cast<int>(static_cast<int64_t>(p.blocks) * (rank + 1) / splits);
 
@@ -215,59 +277,82 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         if (warp == 0 && lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            for (int32_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
                 int lt, ct;
-                tile_at(p, tile, lt, ct);
+                tile_at<C::PAIR>(p, tile, lt, ct);
+                if (C::PAIR) lt = 2 * lt + peer;
                 for (int b = b0; b < b1; ++b, ++it) {
                     const uint32_t st = it % C::STAGES, use = it / C::STAGES;
                     if (!(ok = wait(m, &m->empty[st], (use & 1) ^ 1))) break;
                     unsigned char *s = smem + st * C::STAGE;
-                    mbar_arrive_expect_tx(&m->full[st], C::STAGE);
-                    tma_load_2d(s, &p.a, b * KB, lt * LANES, &m->full[st]);
-                    tma_load_2d(s + C::A_BYTES, &p.b, b * KB, ct * BN, &m->full[st]);
+                    if (C::PAIR) {
+                        const uint32_t bar = in_leader(&m->full[st]);
+                        if (!peer) mbar_arrive_expect_tx(&m->full[st], 2 * C::STAGE);
+                        tma_load_2d_pair(s, &p.a, b * KB, lt * LANES, bar);
+#pragma unroll
+                        for (int h = 0; h < C::HALVES; ++h)
+                            tma_load_2d_pair(s + C::A_BYTES + h * C::B_BOX * KB, &p.b, b * KB, ct * BN + (2 * h + peer) * C::B_BOX, bar);
+                    } else {
+                        mbar_arrive_expect_tx(&m->full[st], C::STAGE);
+                        tma_load_2d(s, &p.a, b * KB, lt * LANES, &m->full[st]);
+                        tma_load_2d(s + C::A_BYTES, &p.b, b * KB, ct * BN, &m->full[st]);
+                    }
                 }
             }
-            if (!ok)  // what is in flight lands before the CTA ends
+            if (C::PAIR)  // the first CTA's commits arrive here: none may be on its way when this CTA ends
+                for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; ok && i < it; ++i)
+                    ok = wait(m, &m->empty[i % C::STAGES], (i / C::STAGES) & 1);
+            if (!ok && !peer)  // what is in flight lands before the CTA, or both of a pair, end
                 for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
                     wait_drain(&m->full[i % C::STAGES], (i / C::STAGES) & 1);
-        } else if (warp == 1 || warp == 3) {
+        } else if ((warp == 1 || warp == 3) && !peer) {
             // The whole warp goes through the loop, so that descriptors are made in uniform registers; one lane issues. Its instructions
             // count: the sums' push them out of the first instruction cache.
-            constexpr uint32_t ID = (1u << 4) | (static_cast<uint32_t>(BN >> 3) << 17) | (static_cast<uint32_t>(LANES >> 4) << 24);
+            constexpr uint32_t M = C::PAIR ? 2 * LANES : LANES, N = BN / C::HALVES, ID = (1u << 4) | (N >> 3 << 17) | (M >> 4 << 24);
             const uint32_t buf = static_cast<uint32_t>(warp >> 1), d = tmem + buf * BN;
             const uint64_t a0 = umma_desc_sw128(smem_u32(smem), 16, 1024);
-            const int64_t tiles = tile0 < p.tiles ? (p.tiles - 1 - tile0) / tile_step + 1 : 0;
-            const int64_t blocks = tiles * (b1 - b0);  // in all; every second is this thread's
+            const int32_t tiles = tile0 < p.tiles ? (p.tiles - 1 - tile0) / tile_step + 1 : 0;
+            const int64_t blocks = static_cast<int64_t>(tiles) * (b1 - b0);  // in all; every second is this thread's
             uint32_t st = buf % C::STAGES, use = buf / C::STAGES, n = 0;
             bool ok = true;
 #pragma unroll 1
             for (int64_t it = buf; it < blocks; it += 2, ++n) {
-                // In this order: that the sums are through with block it - 2, and so with every block before, says that this stage's
-                // last use, perhaps the other warp's, is over. Its parity alone would take the phase before last for this one.
-                if (!(ok = wait_warp(m, &m->tempty[buf], (n & 1) ^ 1) && wait_warp(m, &m->full[st], use & 1))) break;
-                tc_fence_after();
                 const uint64_t a = a0 + st * (C::STAGE / 16), b = a + C::A_BYTES / 16;
-                if (lin::elect_one()) {
+                // The accumulators first: that the sums are through with block it - 2, and so with every block before, says that this stage's
+                // last use, perhaps the other warp's, is over. Its parity alone would take the phase before last for this one. (Of a pair, each
+                // of these warps has stages of its own, and asks for the operands ahead.)
+                if (C::PAIR && !(ok = wait_warp(m, &m->full[st], use & 1))) break;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_e4m3(d, a + 2 * k, b + 2 * k, ID, k > 0);
-                    umma_commit(&m->empty[st]);
-                    umma_commit(&m->tfull[buf]);
+                for (int h = 0; h < C::HALVES; ++h) {
+                    const uint32_t i = buf * C::HALVES + h;
+                    ok = wait_warp(m, &m->tempty[i], (n & 1) ^ 1) && (C::PAIR || wait_warp(m, &m->full[st], use & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lin::elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_e4m3<C::PAIR>(d + h * (BN / 2), a + 2 * k, b + h * (C::B_BOX * KB / 16) + 2 * k, ID, k > 0);
+                        if (h == C::HALVES - 1) commit<C::PAIR>(&m->empty[st]);
+                        commit<C::PAIR>(&m->tfull[i]);
+                    }
                 }
+                if (!ok) break;
                 st += 2;
                 if (st >= C::STAGES) st -= C::STAGES, ++use;
             }
             __syncwarp();
             if (!ok) {
-                if (lin::elect_one()) umma_commit(&m->drained[buf]);
+                if (lin::elect_one()) commit<C::PAIR>(&m->drained[buf], 1);
                 __syncwarp();
                 wait_drain(&m->drained[buf], 0);
             }
         } else if (warp == 2) {
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+            for (int32_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
                 int lt, ct;
-                tile_at(p, tile, lt, ct);
+                tile_at<C::PAIR>(p, tile, lt, ct);
+                if (C::PAIR) lt = 2 * lt + peer;
                 const int row0 = SWAP ? ct * BN : lt * LANES;
                 const int out_block = SWAP ? lt : ct * BN / KB;
                 const int out_blocks = (p.outs + KB - 1) / KB;
@@ -296,7 +381,8 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                         for (int g = 0; g < C::GROUPS; ++g)
 #pragma unroll
                             for (int i = 0; i < PER; ++i)
-                                if (!SWAP || BN >= 32 || lane < BN) s[a * C::SCALE_FLOATS + g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
+                                if (!SWAP || BN >= 32 || lane < BN)
+                                    s[a * C::SCALE_FLOATS + g * LANES + 32 * i + lane] = xs[a][i] * ws[a][g];
                     if (static_cast<int32_t>(it) != p.withhold) arrive_warp(&m->sfull[slot]);
                     ++it;
                 }
@@ -307,12 +393,14 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         const int e = warp - FIRST_SUM_WARP, quad = warp & 3, half = e >> 2;
         const int my_lane = 32 * quad + lane, col0 = half * C::COLS;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * quad) << 16) + col0;
+        const uint32_t tempty = C::PAIR ? in_leader(&m->tempty[0]) : 0, mine_of = C::PAIR ? half : 0;  // its accumulator of a buffer's
         constexpr int LD = C::COLS < 16 ? C::COLS : 16;  // columns read at a time
         uint32_t it = 0, group = 0;
         bool ok = true, ready = false;  // ready: the next block's sum is there
-        for (int64_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
+        for (int32_t tile = tile0; ok && tile < p.tiles; tile += tile_step) {
             int lt, ct;
-            tile_at(p, tile, lt, ct);
+            tile_at<C::PAIR>(p, tile, lt, ct);
+            if (C::PAIR) lt = 2 * lt + peer;
             f2 acc[C::COLS / 2];  // of neighbouring columns
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
@@ -335,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                     }
                 }
                 --handed;
-                if (!__all_sync(0xffffffffu, ready) && !(ok = wait_warp(m, &m->tfull[buf], (it >> 1) & 1))) break;
+                if (!__all_sync(0xffffffffu, ready) && !(ok = wait_warp(m, &m->tfull[buf * C::HALVES + mine_of], (it >> 1) & 1))) break;
                 tc_fence_after();
                 uint32_t d[2][LD];
                 tmem_ld(taddr + buf * BN, d[0]);
@@ -351,8 +439,11 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
                     } else {  // all is read: the accumulator is handed back, and the other one asked for, before the last columns are added
                         tc_fence_before();
                         __syncwarp();
-                        lin::mbar_arrive_if(&m->tempty[buf], lane == 0);
-                        ready = is_complete(&m->tfull[buf ^ 1], ((it + 1) >> 1) & 1);
+                        if (C::PAIR)
+                            arrive_remote_if(tempty + 8 * (buf * C::HALVES + mine_of), lane == 0);
+                        else
+                            lin::mbar_arrive_if(&m->tempty[buf], lane == 0);
+                        ready = is_complete(&m->tfull[(buf ^ 1) * C::HALVES + mine_of], ((it + 1) >> 1) & 1);
                     }
 #pragma unroll
                     for (int i = 0; i < LD; i += 4) {
@@ -433,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
         cluster_sync();
         if (warp >= FIRST_SUM_WARP) {
             int lt, ct;
-            tile_at(p, tile0, lt, ct);
+            tile_at<C::PAIR>(p, tile0, lt, ct);
             const int c0 = BN * rank / splits, n = BN * (rank + 1) / splits - c0;
             const uint32_t red = smem_u32(smem);
 #pragma unroll 4
@@ -455,9 +546,10 @@ __global__ void __launch_bounds__(THREADS, Cfg<BN, SWAP>::CTAS) kda_scaled_matmu
     }
     tc_fence_before();
     __syncthreads();
+    if (C::PAIR) cluster_sync();  // (the pair's products have read this CTA's tiles, and nothing arrives at its barriers any more)
     tc_fence_after();
     if (threadIdx.x == 0 && m->abort) set_status(p.status, KDA_ERR_TIMEOUT);
-    if (warp == 3) tmem_dealloc(tmem, C::TMEM);
+    if (warp == 3) dealloc<C::PAIR>(tmem, C::TMEM);
 }
 
 template <int BN, bool SWAP>
@@ -466,7 +558,7 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
     constexpr int SMEM = C::OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
     static_assert(SMEM * C::CTAS <= 227 * 1024, "shared memory");
     static_assert(AHEAD == 4, "a block's scale is picked among four");
-    static_assert(C::STAGES >= 2 && C::STAGES * C::STAGE / 16 < 0x3fff, "see the MMAs' warps");
+    static_assert(C::STAGES >= 2 && (!C::PAIR || C::STAGES % 2 == 0) && C::STAGES * C::STAGE / 16 < 0x3fff, "see the MMAs' warps");
     static_assert(!SWAP || BN * C::RED_LD * 4 <= C::STAGES * C::STAGE, "a cluster's sums lie over the stages");
     const auto kernel = kda_scaled_matmul_kernel<BN, SWAP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
@@ -485,7 +577,7 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
         const cuuint32_t box[2] = {KB, static_cast<cuuint32_t>(box_rows)};
         return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, at, 2, dims, strides, box);
     };
-    if (!operand(&p.a, SWAP ? w : x, lanes, LANES) || !operand(&p.b, SWAP ? x : w, cols, BN)) return cudaErrorInvalidValue;
+    if (!operand(&p.a, SWAP ? w : x, lanes, LANES) || !operand(&p.b, SWAP ? x : w, cols, C::B_BOX)) return cudaErrorInvalidValue;
     p.tiled_y = 0;
     if (!SWAP && p.outs % 8 == 0) {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.outs), static_cast<cuuint64_t>(p.rows)};
@@ -496,22 +588,25 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
             return cudaErrorInvalidValue;
         p.tiled_y = 1;
     }
-    p.lane_tiles = (lanes - 1) / LANES + 1;
-    p.tiles = static_cast<int64_t>(p.lane_tiles) * ((cols - 1) / BN + 1);
+    p.lane_tiles = (lanes - 1) / (C::PAIR ? 2 * LANES : LANES) + 1;
+    p.col_tiles = (cols - 1) / BN + 1;
+    const int64_t tiles = static_cast<int64_t>(p.lane_tiles) * p.col_tiles;
+    if (tiles > 0x7fffffffLL / 16) return cudaErrorInvalidValue;  // (y would be larger than any memory)
+    p.tiles = static_cast<int32_t>(tiles);
     p.splits = splits;
-    if (splits == 1) {
+    if (splits == 1 && !C::PAIR) {
         const int64_t most = static_cast<int64_t>(sms) * C::CTAS;
-        kernel<<<static_cast<int>(p.tiles < most ? p.tiles : most), THREADS, SMEM, stream>>>(p);
+        kernel<<<static_cast<int>(tiles < most ? tiles : most), THREADS, SMEM, stream>>>(p);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.tiles * splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(C::PAIR ? 2 * (p.tiles < sms / 2 ? p.tiles : sms / 2) : p.tiles * splits));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = static_cast<unsigned>(splits);
+    at.val.clusterDim.x = static_cast<unsigned>(C::PAIR ? 2 : splits);
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
@@ -521,7 +616,7 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
 struct Choice {
     int bn, splits;
 };
-// The least estimated time, in cycles, from measurements (8192 rows, 2048 channels to 6144 outputs: tiles of 256 columns 91 us, of 128
+// The least estimated time, in cycles, from measurements (8192 rows, 2048 channels to 6144 outputs: pairs' tiles of 256 columns 78 us, of 128
 // 118, of 64 139; 256 rows to 6176: 11.3, 8.8 and 10.1 us): rounds of CTAs x (blocks x a block's time + a tile's start and end). Up to 64
 // rows, the splits of a tile that keep the busiest SM's blocks fewest (7 rows, 12288 to 12288: one 30.2 us, two 28.5, three 27.8, four 33.0).
 Choice choose(int64_t rows, int64_t outs, int blocks, int sms) {
@@ -542,7 +637,7 @@ Choice choose(int64_t rows, int64_t outs, int blocks, int sms) {
         offer(bn, 1, static_cast<double>(over(tiles, slots)) * (blocks * block + 1200.));
     };
     const int64_t high = over(rows, LANES), t64 = high * over(outs, 64);
-    wide(256, sms, high * over(outs, 256), 1030.);
+    if (sms > 1) wide(256, sms / 2, over(rows, 2 * LANES) * over(outs, 256), 800.);
     wide(128, sms, high * over(outs, 128), 680.);
     wide(64, 2 * sms, t64, t64 <= sms ? 560. : 830.);
     return best;
