@@ -44,7 +44,7 @@ def _sources():
 
 def _stamp() -> str:
     h = hashlib.sha256()
-    for f in _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+    for f in _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + \
             sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [__file__]:
         h.update(os.path.relpath(f, ROOT).encode())
         with open(f, "rb") as fh:
