@@ -1101,8 +1101,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
         m->abort = 0;
     }
     int index = static_cast<int>(blockIdx.x);
-    wait_for_launch();
     let_next_launch();
+    wait_for_launch();
     const Segment *segs = STATES ? cp.segs_s : cp.segs;  // (the plan's)
     const int jobs = cp.counts[STATES ? 1 : 0] * H;
     if (index >= jobs) return;
@@ -1167,8 +1167,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_join_kernel(const 
     const int mk = threadIdx.x / 4, mc = 2 * (threadIdx.x % 4);  // this thread's two columns of E and N
     constexpr size_t STATE = DK * DV;
     const size_t step = 2 * STATE * cp.a.H;
-    wait_for_launch();
     let_next_launch();
+    wait_for_launch();
     const int64_t jobs = static_cast<int64_t>(cp.counts[2]) * cp.a.H * PARTS;
 #pragma unroll 1
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
