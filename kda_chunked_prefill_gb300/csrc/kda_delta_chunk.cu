@@ -716,8 +716,8 @@ constexpr int STAGE = OFF_D + 1024;
 static_assert(sizeof(Decays) <= 1024, "stage");
 constexpr int STAGE_BYTES = 2 * PANEL + 2 * TILE + IMAGE;  // that arrive
 constexpr int OFF_MISC = STAGES * STAGE;
-// Tensor memory columns: S (first terms of 128 keys, then second); (K S)^T, under it Z, and (Q S)^T; X^T, under it X in two terms, and
-// (P T Z)^T; the update (K^T X)^T. Of Z and X, 16 tokens take 8 columns of first terms and 8 of second, over their sums.
+// Tensor memory columns: S; (K S)^T, under it Z, and (Q S)^T; X^T, under it X, and (P T Z)^T; the update (K^T X)^T. Of S, Z and X, 16 keys
+// or tokens take 8 columns of first terms and 8 of second.
 constexpr uint32_t COL_S = 0, COL_KS = 128, COL_QS = 192, COL_X = 256, COL_O = 320, COL_U = 384;
 
 struct Misc {
@@ -749,16 +749,12 @@ __device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
     }
 }
 __device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // (the warp stays together)
     return __all_sync(0xffffffffu, wait(m, bar, parity));
 }
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) lin::mbar_arrive(bar);
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+    lin::mbar_arrive_if(bar, (threadIdx.x & 31) == 0);
 }
 // x - a, y - b for the pair (a, b) of bf16
 __device__ __forceinline__ uint32_t rest_of(f2 v, uint32_t h) {
@@ -770,15 +766,14 @@ __device__ __forceinline__ uint32_t rest_of(f2 v, uint32_t h) {
         : "r"(h));
     return pack_bf16(x, y);
 }
-// 16 values in two bf16 terms: 8 columns of pairs at `hi` and at `lo`
-__device__ __forceinline__ void put_split(uint32_t hi, uint32_t lo, const f2 *v) {
-    uint32_t h[8], l[8];
+// 16 values in two bf16 terms: 8 columns of pairs and 8 more (by two stores of 8 columns: 2 % slower)
+__device__ __forceinline__ void put_split(uint32_t at, const f2 *v) {
+    uint32_t x[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = lin::bf16_of(v[i]);
-    tmem_st8(hi, h);
+    for (int i = 0; i < 8; ++i) x[i] = lin::bf16_of(v[i]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = rest_of(v[i], h[i]);
-    tmem_st8(lo, l);
+    for (int i = 0; i < 8; ++i) x[8 + i] = rest_of(v[i], x[i]);
+    tmem_st16(at, x);
 }
 // what this warp has put is there for the MMAs
 __device__ __forceinline__ void hand_on(uint64_t *bar) {
@@ -860,8 +855,8 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
             if (lin::elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 8 * k, kq + k * 2, ID, k > 0);
-                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 8 * k, kq + k * 2, ID, 1);
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 16 * k, kq + k * 2, ID, k > 0);
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 16 * k + 8, kq + k * 2, ID, 1);
                 }
             }
             if (!(ok = wait_warp(m, &m->s[1], ph))) break;
@@ -869,16 +864,16 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
             if (lin::elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 32 + 8 * k, kq + PANEL / 16 + k * 2, ID, 1);
-                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 96 + 8 * k, kq + PANEL / 16 + k * 2, ID, 1);
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 64 + 16 * k, kq + PANEL / 16 + k * 2, ID, 1);
+                    lin::umma_ts(tmem + COL_KS, tmem + COL_S + 72 + 16 * k, kq + PANEL / 16 + k * 2, ID, 1);
                 }
                 umma_commit(&m->ks);
                 if (!STATES) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const uint64_t q = kq + TILE / 16 + (k >> 2) * (PANEL / 16) + (k & 3) * 2;
-                        lin::umma_ts(tmem + COL_QS, tmem + COL_S + 8 * k, q, ID, k > 0);
-                        lin::umma_ts(tmem + COL_QS, tmem + COL_S + 64 + 8 * k, q, ID, 1);
+                        lin::umma_ts(tmem + COL_QS, tmem + COL_S + 16 * k, q, ID, k > 0);
+                        lin::umma_ts(tmem + COL_QS, tmem + COL_S + 16 * k + 8, q, ID, 1);
                     }
                 }
             }
@@ -941,8 +936,8 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
         }
         bool ok = true;
         if (chunks > 0) {
-            put_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
-            put_split(t + COL_S + k0 / 2 + 8, t + COL_S + 72 + k0 / 2, S + 8);
+            put_split(t + COL_S + k0, S);
+            put_split(t + COL_S + k0 + 16, S + 8);
             hand_on(&m->s[half]);
         }
         int rest = static_cast<int>(eos - bos);  // tokens, from this chunk on
@@ -974,6 +969,14 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
                 };
 #pragma unroll
                 for (int i = 0; i < TOKS / 2; ++i) z[i] = is_map ? 0 : pair(at(2 * i), at(2 * i + 1));
+                if (left < C) {  // tokens behind the sequence: zeros, whatever they are; so are their rows of T and of K, and then of X
+#pragma unroll
+                    for (int i = 0; i < TOKS / 2; ++i) {
+                        float x, y;
+                        split(z[i], x, y);
+                        z[i] = pair(t0 + 2 * i < left ? x : 0.f, t0 + 2 * i + 1 < left ? y : 0.f);
+                    }
+                }
             }
             auto load_decays = [&](const float *x) {
 #pragma unroll
@@ -982,25 +985,15 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
                     e[2 * i] = u.x, e[2 * i + 1] = u.y;
                 }
             };
-            auto mask = [&](f2(&v)[TOKS / 2]) {  // tokens behind the sequence: zeros, whatever they are
-                if (left == C) return;
-#pragma unroll
-                for (int i = 0; i < TOKS / 2; ++i) {
-                    float x, y;
-                    split(v[i], x, y);
-                    v[i] = pair(t0 + 2 * i < left ? x : 0.f, t0 + 2 * i + 1 < left ? y : 0.f);
-                }
-            };
-            load_decays(d->minus);
             uint32_t r[16];
             if (!(ok = wait_warp(m, &m->ks, ph))) break;
             tc_fence_after();
             tmem_ld16(t + COL_KS + t0, r);
+            load_decays(d->minus);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::fma2(e[i], pair(r[2 * i], r[2 * i + 1]), z[i]);
-            mask(z);
-            put_split(t + COL_KS + t0, t + COL_KS + t0 + 8, z);
+            put_split(t + COL_KS + t0, z);
             if (it != cp.withhold) hand_on(&m->z);
             load_decays(d->after);
             if (!(ok = wait_warp(m, &m->xs, ph))) break;
@@ -1009,16 +1002,15 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < TOKS / 2; ++i) z[i] = lin::mul2(e[i], pair(r[2 * i], r[2 * i + 1]));
-            mask(z);
-            put_split(t + COL_X + t0, t + COL_X + t0 + 8, z);
+            put_split(t + COL_X + t0, z);
             hand_on(&m->x);
             if (!STATES) {
-                load_decays(d->out);
                 if (!(ok = wait_warp(m, &m->o, ph))) break;
                 tc_fence_after();
                 uint32_t q[16];
                 tmem_ld16(t + COL_QS + t0, q);
                 tmem_ld16(t + COL_O + t0, r);
+                load_decays(d->out);
                 tmem_wait_ld();
                 tc_fence_before();
                 // Two tokens of two neighbouring columns lie in two lanes: each stores both columns of one token.
@@ -1046,12 +1038,12 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
             const bool more = it + 1 < chunks;
 #pragma unroll
             for (int i = 0; i < 8; ++i) S[i] = lin::add2(S[i], pair(u[0][2 * i], u[0][2 * i + 1]));
-            if (more) put_split(t + COL_S + k0 / 2, t + COL_S + 64 + k0 / 2, S);
+            if (more) put_split(t + COL_S + k0, S);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i) S[8 + i] = lin::add2(S[8 + i], pair(u[1][2 * i], u[1][2 * i + 1]));
             if (more) {
-                put_split(t + COL_S + k0 / 2 + 8, t + COL_S + 72 + k0 / 2, S + 8);
+                put_split(t + COL_S + k0 + 16, S + 8);
                 hand_on(&m->s[half]);
             }
             if (++st == STAGES) st = 0, ++use;
