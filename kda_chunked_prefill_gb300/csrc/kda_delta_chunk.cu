@@ -12,12 +12,12 @@
 // head: K S, T Z and K^T X one after the other, Q S and P T Z beside them. Where there are few sequences, long ones are cut: a pass over
 // the parts' states from zero and their maps, and a join, come before the walk (see plan).
 //
-// Bound by latency. 4 x 2048 tokens, 16 heads: 36 us for the 2112 chunks (5 CTAs an SM, 12 us each: substitutions and products of 16
-// rows that wait for one another), 78 for 32 chunks one after the other on 64 SMs, 2.3 us each: three products of 45 to 70 cycles an MMA,
+// Bound by latency. 4 x 2048 tokens, 16 heads: 35 us for the 2112 chunks (5 CTAs an SM, 12 us each: substitutions and products of 16
+// rows that wait for one another), 72 for 32 chunks one after the other on 64 SMs, 2.1 us each: three products of 45 to 70 cycles an MMA,
 // and after each the accumulators' way through registers, split in two bf16 terms, back to tensor memory. The tensor pipe is busy in
-// 44 % of a walking SM's cycles. In all 118 us; 1 x 65536 tokens, 4 heads: 63, states 129, join 58, walk 75, in all 336.
+// 46 % of a walking SM's cycles. In all 111 us; 1 x 65536 tokens, 4 heads: 60, states 119, join 58, walk 71, in all 315.
 // (Z, X and S in halves, so that MMAs start on the first: 3 % slower, as each half's hand-over costs what it hides. Operands through shared
-// memory with 64 value columns a CTA: 5300 cycles a chunk for half of the columns, against 4750 for all.)
+// memory with 64 value columns a CTA: 5300 cycles a chunk for half of the columns, against 4400 for all.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -138,7 +138,7 @@ __host__ __device__ inline void add_sequence(Work &out, Work &states, int &most,
     states.cuts += k - 1;
     if (k > most) most = k;
 }
-// The time of a pass on `sms` CTAs, in chunks (2.3 us): a job takes its own and 1.2 for its start and end.
+// The time of a pass on `sms` CTAs, in chunks (2.1 us): a job takes its own and 1.2 for its start and end.
 __host__ __device__ inline float pass_time(const Work &w, int heads, int sms) {
     const float jobs = static_cast<float>(w.jobs) * heads, one = w.longest + 1.2f;
     const float even = (static_cast<float>(w.chunks) * heads + 1.2f * jobs) / sms + (jobs > sms ? 0.5f * one : 0.f);
@@ -1245,7 +1245,7 @@ bool encode_heads(CUtensorMap *m, const __nv_bfloat16 *x, int64_t tokens, int he
     return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, 3, dims, strides, box);
 }
 
-// The shortest cut worth a try, an SM's share of all chunks; 0 where none pays, which spares two launches (6 us of the 121 of
+// The shortest cut worth a try, an SM's share of all chunks; 0 where none pays, which spares two launches (3 us of the 112 of
 // 4 x 2048 tokens and 16 heads, where the host cannot rule it out). Cuts gain most where one sequence holds all tokens: if none pays for
 // that one, none is tried.
 int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
