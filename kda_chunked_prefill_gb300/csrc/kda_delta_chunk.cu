@@ -138,18 +138,18 @@ __host__ __device__ inline void add_sequence(Work &out, Work &states, int &most,
     states.cuts += k - 1;
     if (k > most) most = k;
 }
-// The time of a pass on `sms` CTAs, in chunks (2.1 us): a job takes its own and 1.2 for its start and end.
+// The time of a pass on `sms` CTAs, in chunks (2.1 us): a job takes its own and one for its start and end.
 __host__ __device__ inline float pass_time(const Work &w, int heads, int sms) {
-    const float jobs = static_cast<float>(w.jobs) * heads, one = w.longest + 1.2f;
-    const float even = (static_cast<float>(w.chunks) * heads + 1.2f * jobs) / sms + (jobs > sms ? 0.5f * one : 0.f);
+    const float jobs = static_cast<float>(w.jobs) * heads, one = w.longest + 1.f;
+    const float even = (static_cast<float>(w.chunks) * heads + jobs) / sms + (jobs > sms ? 0.5f * one : 0.f);
     const float rounds = ceilf(jobs / sms) * one;
     const float t = even < rounds ? even : rounds;
     return w.jobs == 0 ? 0.f : t > one ? t : one;
 }
-// With the join (0.9 of a chunk's time a part) and two more launches. With these three figures the cut taken was within 4 % of the best
-// of those tried in 14 batches. 1 sequence of 65,536 tokens: 1 head in parts of 14, 21, 28, 54 chunks 222, 203, 218, 298 us and 2253
-// whole; 4 heads 27, 40, 54: 340, 392, 356 and 2376. 16 of 1 to 3853 tokens, 16 heads: the longest in 3 parts 187, whole 207. 4 of
-// 2048, 16 heads: in 2 parts 136, whole 122.
+// With the join (0.9 of a chunk's time a part) and two more launches. With these three figures the cut taken was within 5 % of the best
+// of those tried in 28 batches. 1 sequence of 65,536 tokens: 1 head in parts of 14, 21, 28, 54 chunks 216, 198, 206, 280 us and 2124
+// whole; 4 heads 27, 40, 54: 315, 372, 329 and 2174. 16 of 1 to 3853 tokens, 16 heads: the longest in 3 parts 176, whole 191. 4 of
+// 2048, 16 heads: in 2 parts 125, whole 112.
 __host__ __device__ inline float time_of(const Work &out, const Work &states, int most, int heads, int sms) {
     return pass_time(out, heads, sms) + (most > 1 ? pass_time(states, heads, sms) + 0.9f * most + 2.f : 0.f);
 }
