@@ -628,8 +628,12 @@ kda_status_t kda_add_rms_norm(const void *x, const void *residual, const float *
  *                 pointer as initial_state. An empty sequence's final state is
  *                 its initial state.
  *   status_dev    optional device int32, zeroed on the stream, then the first of
- *                 KDA_ERR_GATE_RANGE (some g > 0 or NaN), KDA_ERR_BAD_SEQLENS (that
- *                 sequence is skipped), KDA_ERR_TIMEOUT.
+ *                 KDA_ERR_GATE_RANGE (some g > 0 or NaN), KDA_ERR_BAD_SEQLENS,
+ *                 KDA_ERR_TIMEOUT. A sequence whose bounds run backwards or out of
+ *                 range is skipped (its state in final_state stays as it was), all of
+ *                 them where cu[0] is not 0; every other one gets its own results, in a
+ *                 form that takes much longer. Where such bounds make sequences
+ *                 overlap, a row of o that several have holds the output of one.
  *   workspace     kda_gated_delta_chunk_fwd_workspace_size(...) bytes, 256-byte
  *                 aligned (NULL when that is 0); not shared by calls that overlap.
  * Precision: products of bf16 operands with fp32 accumulation; the state is kept

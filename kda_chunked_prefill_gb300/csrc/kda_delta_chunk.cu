@@ -85,13 +85,12 @@ struct ChunkParams {
     Params a;
     CUtensorMap tq, tk, tv;
     unsigned char *images;  // [slot][head]
-    int64_t slots;
+    int64_t slots;          // of chunks
     // sequences that are cut (device memory in the workspace)
     int32_t longer;         // sequences of no more tokens are left out (the recurrence runs them); -1: none is
     int32_t withhold;       // tests: the chunk of each CTA whose Z is not handed on (-1: none)
     int32_t shortest;       // shortest cut that the workspace is sized for, in chunks; 0: none is cut
     int32_t sms;
-    int32_t most_segs, most_cuts;  // that the workspace holds
     int32_t *counts;        // [0] segments, [1] those of the pass over the states, [2] sequences to join
     Segment *segs, *segs_s;
     Cuts *cuts;
@@ -159,7 +158,7 @@ struct Shared {
     Work out[CUTS + 1], states[CUTS + 1];
     int32_t most[CUTS + 1];
     int32_t bucket[2][BUCKETS];  // first segments of each length, long ones first: of the outputs' pass, of the states'
-    int32_t cuts, joined, len, longest, none;
+    int32_t cuts, joined, len, longest;
     int32_t sums[THREADS / 32];
     int32_t held[HELD];          // chunks_of() of the first sequences
 };
@@ -208,12 +207,18 @@ __device__ __noinline__ void make(const ChunkParams &cp, Shared *sh) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < 2 * BUCKETS; i += THREADS) sh->bucket[i / BUCKETS][i % BUCKETS] = 0;
     if (tid == 0) sh->cuts = sh->joined = 0;
+    bool bad = false;
     for (int n = tid; n < p.N; n += THREADS) {
         const int chunks = chunks_of(cp, n);
-        if (chunks == -1) set_status(p.status, KDA_ERR_BAD_SEQLENS);
+        bad |= chunks == -1;
         if (n < HELD) sh->held[n] = chunks;
     }
-    __syncthreads();
+    // Slots of chunks are found, and the workspace is large enough, where bounds are in order; otherwise this launch runs what it can itself.
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
+        if (tid < 3) cp.counts[tid] = 0;
+        return;
+    }
     auto length = [&](int n) { return n < HELD ? sh->held[n] : chunks_of(cp, n); };
     const int candidates = cp.shortest ? CUTS + 1 : 1;  // the last: none is cut
     for (int c = warp; c < candidates; c += THREADS / 32) {
@@ -229,27 +234,17 @@ __device__ __noinline__ void make(const ChunkParams &cp, Shared *sh) {
     }
     __syncthreads();
     if (warp == 0) {
-        float t = 3.0e38f;
-        // (bad bounds may overlap, and then hold more than the workspace)
-        if (lane < candidates && (lane == candidates - 1 || (sh->out[lane].jobs <= cp.most_segs && sh->states[lane].cuts <= cp.most_cuts)))
-            t = time_of(sh->out[lane], sh->states[lane], sh->most[lane], p.H, cp.sms);
+        const float t = lane < candidates ? time_of(sh->out[lane], sh->states[lane], sh->most[lane], p.H, cp.sms) : 3.0e38f;
         float least = t;
 #pragma unroll
         for (int d = 16; d; d >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, d));
         const int best = 31 - __clz(__ballot_sync(0xffffffffu, t == least && lane < candidates));
-        // Bad bounds may overlap: then there may be more long sequences, or chunks of them, than there is room for. None is run.
-        const Work &all = sh->out[candidates - 1];
-        if (lane == 0) sh->none = cp.longer >= 0 && (all.jobs > cp.most_segs || all.chunks > cp.slots);
         if (lane == 0) {
             sh->len = best == candidates - 1 ? 0x7fffffff : cut_length(best, cp.shortest);
             sh->longest = sh->out[best].longest > 0 ? sh->out[best].longest : 1;
         }
     }
     __syncthreads();
-    if (sh->none) {
-        if (tid < 3) cp.counts[tid] = 0;
-        return;
-    }
     auto bucket_of = [&](int len) { return BUCKETS - 1 - static_cast<int>(static_cast<int64_t>(len) * (BUCKETS - 1) / sh->longest); };
     auto for_each = [&](auto &&f) {
         for (int n = tid; n < p.N; n += THREADS) {
@@ -414,6 +409,75 @@ __device__ __forceinline__ void product(float (&d)[2][4], const Left &f, const u
     }
 }
 
+// Malformed batches: the last CTAs of this launch look through all bounds, and where some are not in order run the sequences whose own are, token
+// after token by the recurrence's formulas in fp32: 32 value columns of a sequence and head, a lane a column, a warp 32 keys of it; one
+// sum over the warps a token, about 1 us. Nothing in the workspace is used, as where a chunk's images lie presupposes order. (The
+// same code in the walk's kernel, never called, took 2 to 3 % of every well-formed call; here 0 to 1 %.)
+__device__ __noinline__ void malformed(const ChunkParams &cp, int first, int ctas, float *sums) {
+    const Params &p = cp.a;
+    constexpr int PARTS = THREADS / 32, KEYS = DK / PARTS, BLOCKS = DV / 32, BUF = PARTS * 65;  // k^T S, q^T S and q.k by parts of the keys
+    const int part = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bool bad = false;
+    for (int n = threadIdx.x; n < p.N; n += THREADS) bad |= plan::chunks_of(cp, n) == -1;
+    if (!__syncthreads_or(bad)) return;
+    const int64_t jobs = static_cast<int64_t>(p.N) * p.H * BLOCKS;
+    uint32_t buf = 0;
+#pragma unroll 1
+    for (int64_t job = first; job < jobs; job += ctas) {
+        const int val = 32 * static_cast<int>(job % BLOCKS) + lane, h = static_cast<int>(job / BLOCKS % p.H), n = static_cast<int>(job / BLOCKS / p.H);
+        if (plan::chunks_of(cp, n) < 0) continue;  // (its own bounds are bad, or the recurrence runs it)
+        const int64_t bos = p.cu[n], eos = p.cu[n + 1];
+        const size_t state = (static_cast<size_t>(n) * p.H + h) * (DK * DV) + static_cast<size_t>(KEYS * part) * DV + val;
+        const int c = h / p.rep * DK + KEYS * part;
+        float S[KEYS];
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) S[i] = p.s0 ? p.s0[state + i * DV] : 0.f;
+#pragma unroll 1
+        for (int64_t t = bos; t < eos; ++t, buf ^= 1) {
+            float *at = sums + buf * BUF;  // (its last use was read before the barrier of the token before)
+            const uint4 *kp = reinterpret_cast<const uint4 *>(p.k + t * p.ks + c), *qp = reinterpret_cast<const uint4 *>(p.q + t * p.qs + c);
+            uint32_t k[KEYS / 2];
+            float ks = 0.f, qs = 0.f, qk = 0.f;
+#pragma unroll
+            for (int i = 0; i < KEYS / 8; ++i) {
+                const uint4 x = kp[i], y = qp[i];
+                const uint32_t q[4] = {y.x, y.y, y.z, y.w};
+                k[4 * i] = x.x, k[4 * i + 1] = x.y, k[4 * i + 2] = x.z, k[4 * i + 3] = x.w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 kk = unpack_bf16(k[4 * i + j]), qq = unpack_bf16(q[j]);
+                    const float s0 = S[8 * i + 2 * j], s1 = S[8 * i + 2 * j + 1];
+                    ks = fmaf(kk.y, s1, fmaf(kk.x, s0, ks));
+                    qs = fmaf(qq.y, s1, fmaf(qq.x, s0, qs));
+                    qk = fmaf(qq.y, kk.y, fmaf(qq.x, kk.x, qk));
+                }
+            }
+            at[65 * part + lane] = ks;
+            at[65 * part + 32 + lane] = qs;
+            if (lane == 0) at[65 * part + 64] = qk;
+            __syncthreads();
+            ks = qs = qk = 0.f;
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) ks += at[65 * i + lane], qs += at[65 * i + 32 + lane], qk += at[65 * i + 64];
+            const float d = expf(p.g[t * p.H + h]), v = __bfloat162float(p.v[t * p.vs + h * DV + val]);
+            const float x = p.beta[t * p.H + h] * fmaf(-d, ks, v);
+            if (part == 0) p.o[(t * p.H + h) * DV + val] = __float2bfloat16_rn(p.scale * fmaf(d, qs, qk * x));
+#pragma unroll
+            for (int i = 0; i < KEYS / 2; ++i) {
+                const float2 kk = unpack_bf16(k[i]);
+                S[2 * i] = fmaf(kk.x, x, d * S[2 * i]);
+                S[2 * i + 1] = fmaf(kk.y, x, d * S[2 * i + 1]);
+            }
+        }
+        if (p.sT) {
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) p.sT[state + i * DV] = S[i];
+        }
+    }
+}
+// their number: an SM each, and no more than they have jobs
+int malformed_ctas(int64_t N, int64_t H, int sms) { return static_cast<int>(4 * N * H < sms ? 4 * N * H : sms); }
+
 __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kernel(const __grid_constant__ ChunkParams cp) {
     const Params &p = cp.a;
     extern __shared__ unsigned char raw[];
@@ -424,6 +488,11 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     let_next_launch();
     if (blockIdx.x == 0) {
         plan::make(cp, reinterpret_cast<plan::Shared *>(smem));
+        return;
+    }
+    if (blockIdx.x > cp.slots * p.H) {
+        const int first = static_cast<int>(1 + cp.slots * p.H);
+        malformed(cp, static_cast<int>(blockIdx.x) - first, static_cast<int>(gridDim.x) - first, reinterpret_cast<float *>(smem));
         return;
     }
     const int64_t slot = (blockIdx.x - 1) / p.H;
@@ -437,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
         n = find_sequence(p, slot, lane);
     }
     const int64_t bos = p.cu[n], eos = p.cu[n + 1];
-    if (bos < 0 || eos < bos || eos > p.T || p.cu[0] != 0) return;  // (the plan reports it)
+    if (bos < 0 || eos < bos || eos > p.T || p.cu[0] != 0) return;  // (the batch is malformed: the plan reports it)
     const int64_t t0 = bos + (cp.longer >= 0 ? chunk : slot - slot_base(bos, n)) * C;
     if (t0 < bos || t0 >= eos) return;
     const int left = eos - t0 < C ? static_cast<int>(eos - t0) : C;  // rows behind are anything: what they enter is set to zero
@@ -1350,13 +1419,11 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.images = ws + l.images;
     p.slots = l.slots;
     p.sms = sms;
-    p.most_segs = static_cast<int32_t>(l.segs);
-    p.most_cuts = static_cast<int32_t>(l.cuts);
     p.segs = reinterpret_cast<Segment *>(ws + l.seg);
     p.segs_s = reinterpret_cast<Segment *>(ws + l.seg_s);
     p.cuts = reinterpret_cast<Cuts *>(ws + l.cut);
     p.states = reinterpret_cast<float *>(ws + l.states);
-    cudaError_t e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H, prep::THREADS, prep::SMEM, false, p, stream);
+    cudaError_t e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H + prep::malformed_ctas(a.N, a.H, sms), prep::THREADS, prep::SMEM, false, p, stream);
     if (e == cudaSuccess && p.shortest) {
         const int64_t parts = 2 * l.cuts * a.H, joins = (l.cuts < a.N ? l.cuts : a.N) * a.H * join::PARTS;
         e = launch(walk::kda_gated_delta_chunk_kernel<true>, parts < sms ? parts : sms, walk::THREADS, walk::SMEM, true, p, stream);
