@@ -8,6 +8,8 @@
 namespace kda {
 namespace delta {
 
+constexpr int CHUNK = 64;  // tokens of a chunk
+
 struct Params {
     const __nv_bfloat16 *q, *k, *v;
     int64_t qs, ks, vs;  // elements from one token to the next
@@ -16,7 +18,10 @@ struct Params {
     int32_t steps;
     int32_t N;
     int64_t T;
-    int64_t longest;  // the recurrence with cu: sequences of more tokens are left out (negative: none is)
+    int64_t longest;  // the recurrence with cu: sequences of more tokens are left out (negative: none is), but listed:
+    int32_t *listed;  // [0] their chunks (of CHUNK tokens) in all, [1] 1 where some bounds are not in order, else 0
+    int2 *list;       // the sequence and number of each of these chunks, a sequence's one after the other
+    int64_t most;     // that there is room for (enough, where bounds are in order)
     int32_t H, rep;  // value heads; value heads per query/key head
     const float *s0;
     float scale;

@@ -45,6 +45,9 @@ kda_status_t delta_args(const void *q, const void *k, const void *v, const float
     p->N = num_seqs;
     p->T = tokens;
     p->longest = -1;
+    p->listed = nullptr;
+    p->list = nullptr;
+    p->most = 0;
     p->H = num_heads;
     p->rep = num_heads / num_qk_heads;
     p->s0 = s0;

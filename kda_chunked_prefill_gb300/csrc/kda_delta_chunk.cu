@@ -36,7 +36,7 @@ using lin::f2;
 using lin::pair;
 using lin::split;
 
-constexpr int C = 64;  // tokens of a chunk
+constexpr int C = CHUNK;
 
 // What the first launch leaves of a chunk and head. The tiles are rows of 64 bf16 (128 bytes), 128-byte swizzled.
 struct Decays {
@@ -55,7 +55,7 @@ static_assert(IMAGE % 128 == 0 && sizeof(Decays) % 16 == 0, "bulk copies");
 __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 // Workspace slots of chunks: those of sequence n begin at cu[n] / 64 + n, which leaves each as many as it can need. (Where only the long
-// sequences run in chunks: one after the other.)
+// sequences run in chunks, the recurrence's launch before these has listed their chunks, one after the other.)
 __device__ __forceinline__ int64_t slot_base(int64_t bos, int64_t n) { return bos / C + n; }
 
 __device__ __forceinline__ uint64_t evict_normal() {  // (the second launch reads them again)
@@ -87,11 +87,14 @@ struct ChunkParams {
     unsigned char *images;  // [slot][head]
     int64_t slots;          // of chunks
     // sequences that are cut (device memory in the workspace)
-    int32_t longer;         // sequences of no more tokens are left out (the recurrence runs them); -1: none is
+    int32_t longer;         // sequences of no more tokens are left out (the recurrence runs them, and lists the others); -1: none is
     int32_t withhold;       // tests: the chunk of each CTA whose Z is not handed on (-1: none)
     int32_t shortest;       // shortest cut that the workspace is sized for, in chunks; 0: none is cut
     int32_t sms;
+    int32_t from;           // first of the outputs' jobs that are run in rounds
     int32_t *counts;        // [0] segments, [1] those of the pass over the states, [2] sequences to join
+    const int32_t *listed;  // the long sequences' chunks, where only those run here: see Params
+    const int2 *list;
     Segment *segs, *segs_s;
     Cuts *cuts;
     // [cut][head][2][128][128]: the state after it (from zero; joined: the true one); the map of the part before it, transposed, or, for a
@@ -159,36 +162,15 @@ struct Shared {
     int32_t most[CUTS + 1];
     int32_t bucket[2][BUCKETS];  // first segments of each length, long ones first: of the outputs' pass, of the states'
     int32_t cuts, joined, len, longest;
-    int32_t sums[THREADS / 32];
-    int32_t held[HELD];          // chunks_of() of the first sequences
+    int32_t held[HELD];          // chunks of the first items
 };
 
-// -1: bounds that are none; -2: a sequence that is left out
+// -1: bounds that are not in order; -2: a sequence that is left out
 __device__ __forceinline__ int chunks_of(const ChunkParams &cp, int n) {
     const Params &p = cp.a;
     const int64_t b = p.cu[n], e = p.cu[n + 1];
     if (b < 0 || e < b || e > p.T || p.cu[0] != 0) return -1;
     return e - b <= cp.longer ? -2 : static_cast<int>((e - b + C - 1) / C);
-}
-// The sum of x over the CTA's threads before this one, on top of `carry`, which grows by the whole.
-__device__ __forceinline__ int scan(int x, int &carry, int (&sums)[THREADS / 32]) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int sum = x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += y;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = sum;
-    __syncthreads();
-    int before = carry + sum - x;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-        if (i < warp) before += sums[i];
-        carry += sums[i];
-    }
-    return before;
 }
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 __device__ __forceinline__ int warp_max(int x) { return __reduce_max_sync(0xffffffffu, x); }
@@ -199,6 +181,16 @@ __device__ __forceinline__ Work warp_work(Work w) {
     return {warp_sum(w.jobs), warp_max(w.longest), chunks, warp_sum(w.cuts)};
 }
 
+// Some bounds of the batch are not in order (whole CTA).
+__device__ __forceinline__ bool malformed(const ChunkParams &cp) {
+    bool bad = false;
+    if (cp.longer >= 0)
+        bad = cp.listed[1];
+    else
+        for (int n = threadIdx.x; n < cp.a.N; n += blockDim.x) bad |= chunks_of(cp, n) == -1;
+    return __syncthreads_or(bad);
+}
+
 // One CTA: the cut by estimates from the lengths, and the segments of both passes, long ones first. (The other CTAs' chunks take longer
 // than this only if it is quick: lengths are read once, a warp estimates a cut. 5 to 11 us; as code of its own, out of the chunks' way, a call
 // takes 1 to 3 % less.)
@@ -207,26 +199,27 @@ __device__ __noinline__ void make(const ChunkParams &cp, Shared *sh) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < 2 * BUCKETS; i += THREADS) sh->bucket[i / BUCKETS][i % BUCKETS] = 0;
     if (tid == 0) sh->cuts = sh->joined = 0;
-    bool bad = false;
-    for (int n = tid; n < p.N; n += THREADS) {
-        const int chunks = chunks_of(cp, n);
-        bad |= chunks == -1;
-        if (n < HELD) sh->held[n] = chunks;
-    }
     // Slots of chunks are found, and the workspace is large enough, where bounds are in order; otherwise this launch runs what it can itself.
-    if (__syncthreads_or(bad)) {
+    if (malformed(cp)) {
         if (tid == 0) set_status(p.status, KDA_ERR_BAD_SEQLENS);
         if (tid < 3) cp.counts[tid] = 0;
         return;
     }
-    auto length = [&](int n) { return n < HELD ? sh->held[n] : chunks_of(cp, n); };
+    // items: the sequences, or the long ones' chunks, of which the first stands for its sequence
+    const bool listed = cp.longer >= 0;
+    const int items = listed ? cp.listed[0] : p.N;
+    auto sequence = [&](int i) { return listed ? cp.list[i].x : i; };
+    auto chunks_at = [&](int i) { return listed && cp.list[i].y != 0 ? -2 : chunks_of(cp, sequence(i)); };
+    for (int i = tid; i < items && i < HELD; i += THREADS) sh->held[i] = chunks_at(i);
+    __syncthreads();
+    auto length = [&](int i) { return i < HELD ? sh->held[i] : chunks_at(i); };
     const int candidates = cp.shortest ? CUTS + 1 : 1;  // the last: none is cut
     for (int c = warp; c < candidates; c += THREADS / 32) {
         const int len = c == candidates - 1 ? 0x7fffffff : cut_length(c, cp.shortest);
         Work out{0, 0, 0, 0}, states{0, 0, 0, 0};
         int most = 0;
-        for (int n = lane; n < p.N; n += 32) {
-            const int chunks = length(n);
+        for (int i = lane; i < items; i += 32) {
+            const int chunks = length(i);
             if (chunks >= 0) add_sequence(out, states, most, chunks, len);
         }
         out = warp_work(out), states = warp_work(states), most = warp_max(most);
@@ -247,12 +240,12 @@ __device__ __noinline__ void make(const ChunkParams &cp, Shared *sh) {
     __syncthreads();
     auto bucket_of = [&](int len) { return BUCKETS - 1 - static_cast<int>(static_cast<int64_t>(len) * (BUCKETS - 1) / sh->longest); };
     auto for_each = [&](auto &&f) {
-        for (int n = tid; n < p.N; n += THREADS) {
-            const int chunks = length(n);
+        for (int i = tid; i < items; i += THREADS) {
+            const int chunks = length(i);
             if (chunks < 0) continue;
             int one, k;
             parts_of(chunks, sh->len, one, k);
-            f(n, chunks, k, one);
+            f(i, chunks, k, one);
         }
     };
     for_each([&](int, int chunks, int k, int one) {  // (all parts but the last are of one length)
@@ -278,15 +271,9 @@ __device__ __noinline__ void make(const ChunkParams &cp, Shared *sh) {
         if (lane == 31) cp.counts[warp] = sum;
     }
     __syncthreads();
-    int slots = 0;
-    for (int n0 = 0; n0 < p.N; n0 += THREADS) {
-        const int n = n0 + tid, chunks = n < p.N ? length(n) : -1;
-        int slot = 0;
-        if (cp.longer >= 0) slot = scan(chunks > 0 ? chunks : 0, slots, sh->sums);
-        if (chunks < 0) continue;
-        if (cp.longer < 0) slot = static_cast<int>(slot_base(p.cu[n], n));
-        int one, k, first = -1, at = 0, at_s = 0;
-        parts_of(chunks, sh->len, one, k);
+    for_each([&](int item, int chunks, int k, int one) {
+        const int n = sequence(item), slot = listed ? item : static_cast<int>(slot_base(p.cu[n], n));
+        int first = -1, at = 0, at_s = 0;
         if (k > 1) {
             first = atomicAdd(&sh->cuts, k - 1);
             cp.cuts[atomicAdd(&sh->joined, 1)] = {n, first, k - 1};
@@ -301,7 +288,7 @@ __device__ __noinline__ void make(const ChunkParams &cp, Shared *sh) {
         }
         const int c0 = (k - 1) * one, len = chunks - c0;
         cp.segs[atomicAdd(&sh->bucket[0][bucket_of(len)], 1)] = {n, c0, len, slot + c0, k > 1 ? first + k - 2 : -1, -1, 0};
-    }
+    });
     __syncthreads();
     if (tid == 0) cp.counts[2] = sh->joined;
 }
@@ -330,7 +317,6 @@ struct Misc {
     float row[C];                       // e^{G_i - (G before i's block)}
     float col[BLOCKS - 1][C - SB];      // e^{(G before block b + 1) - G_j}
     uint64_t full;
-    int32_t sums[THREADS / 32], found[2];
 };
 constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(SMEM * PER_SM <= 227 * 1024, "shared memory");
@@ -358,20 +344,6 @@ __device__ __forceinline__ Two add(Two a, Two b) {
     const float e = ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo), hi = s + e;
     return {hi, e - (hi - s)};
 }
-// The same where only long sequences have slots, one after the other (whole CTA); -1: the slot is behind the last.
-__device__ __forceinline__ int find_long(const ChunkParams &cp, int slot, int &chunk, int (&sums)[THREADS / 32], int (&found)[2]) {
-    if (threadIdx.x == 0) found[0] = -1;
-    int slots = 0;
-    for (int n0 = 0; n0 < cp.a.N && slots <= slot; n0 += THREADS) {
-        const int n = n0 + threadIdx.x, c = n < cp.a.N ? plan::chunks_of(cp, n) : 0, chunks = c > 0 ? c : 0;
-        const int first = plan::scan(chunks, slots, sums);
-        if (slot >= first && slot < first + chunks) found[0] = n, found[1] = slot - first;
-    }
-    __syncthreads();
-    chunk = found[1];
-    return found[0];
-}
-
 // 2^(x + y), |y| far below 1
 __device__ __forceinline__ float ex2_2(float x, float y) { return ex2(x) * fmaf(y, 0.6931471805599453f, 1.f); }
 // 2^(a - b)
@@ -409,17 +381,15 @@ __device__ __forceinline__ void product(float (&d)[2][4], const Left &f, const u
     }
 }
 
-// Malformed batches: the last CTAs of this launch look through all bounds, and where some are not in order run the sequences whose own are, token
+// Malformed batches: the last CTAs of this launch run the sequences whose own bounds are in order, token
 // after token by the recurrence's formulas in fp32: 32 value columns of a sequence and head, a lane a column, a warp 32 keys of it; one
 // sum over the warps a token, about 1 us. Nothing in the workspace is used, as where a chunk's images lie presupposes order. (The
 // same code in the walk's kernel, never called, took 2 to 3 % of every well-formed call; here 0 to 1 %.)
-__device__ __noinline__ void malformed(const ChunkParams &cp, int first, int ctas, float *sums) {
+__device__ __noinline__ void token_by_token(const ChunkParams &cp, int first, int ctas, float *sums) {
     const Params &p = cp.a;
     constexpr int PARTS = THREADS / 32, KEYS = DK / PARTS, BLOCKS = DV / 32, BUF = PARTS * 65;  // k^T S, q^T S and q.k by parts of the keys
     const int part = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    bool bad = false;
-    for (int n = threadIdx.x; n < p.N; n += THREADS) bad |= plan::chunks_of(cp, n) == -1;
-    if (!__syncthreads_or(bad)) return;
+    if (!plan::malformed(cp)) return;
     const int64_t jobs = static_cast<int64_t>(p.N) * p.H * BLOCKS;
     uint32_t buf = 0;
 #pragma unroll 1
@@ -476,7 +446,7 @@ __device__ __noinline__ void malformed(const ChunkParams &cp, int first, int cta
     }
 }
 // their number: an SM each, and no more than they have jobs
-int malformed_ctas(int64_t N, int64_t H, int sms) { return static_cast<int>(4 * N * H < sms ? 4 * N * H : sms); }
+int spare_ctas(int64_t N, int64_t H, int sms) { return static_cast<int>(4 * N * H < sms ? 4 * N * H : sms); }
 
 __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kernel(const __grid_constant__ ChunkParams cp) {
     const Params &p = cp.a;
@@ -492,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
     }
     if (blockIdx.x > cp.slots * p.H) {
         const int first = static_cast<int>(1 + cp.slots * p.H);
-        malformed(cp, static_cast<int>(blockIdx.x) - first, static_cast<int>(gridDim.x) - first, reinterpret_cast<float *>(smem));
+        token_by_token(cp, static_cast<int>(blockIdx.x) - first, static_cast<int>(gridDim.x) - first, reinterpret_cast<float *>(smem));
         return;
     }
     const int64_t slot = (blockIdx.x - 1) / p.H;
@@ -500,8 +470,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) kda_gated_delta_prepare_kerne
 
     int n, chunk = 0;
     if (cp.longer >= 0) {
-        n = find_long(cp, static_cast<int>(slot), chunk, m->sums, m->found);
-        if (n < 0) return;
+        if (slot >= cp.listed[0]) return;
+        const int2 at = cp.list[slot];
+        n = at.x, chunk = at.y;
     } else {
         n = find_sequence(p, slot, lane);
     }
@@ -862,7 +833,8 @@ __device__ __forceinline__ void set_up(Misc *m) {
 }
 
 // A segment, by the whole CTA. STATES: of the pass over the states of cut sequences.
-template <bool STATES>
+// ROUNDS: another segment may follow.
+template <bool STATES, bool ROUNDS>
 __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, int h, unsigned char *smem, Misc *m, uint32_t tmem) {
     const Params &p = cp.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hk = h / p.rep;
@@ -893,7 +865,7 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
             }
             if (!ok)  // what is in flight lands before the CTA ends
                 for (int i = it < STAGES ? 0 : it - STAGES; i < it; ++i) wait_drain(&m->full[i % STAGES], (i / STAGES) & 1);
-            else if (STATES)  // the barriers are set up anew for the next segment: no arrival is left out
+            else if (ROUNDS)  // the barriers are set up anew for the next segment: no arrival is left out
                 for (int i = it < STAGES ? 0 : it - STAGES; i < it && ok; ++i) ok = wait(m, &m->empty[i % STAGES], (i / STAGES) & 1);
         }
     } else if (warp == WARP_MMA) {
@@ -1149,11 +1121,12 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
 }
 
 // The outputs' CTAs have a segment each; those of the pass over the states, no more of them than SMs, one in each round, there and back,
-// as long ones are listed first. (Where no sequence is cut, this launch and the join's end at once, the sooner the fewer CTAs they have:
+// as long ones are listed first. So have those of the outputs' jobs from `from` on: where most sequences run token after token, and the host
+// does not know how many do not, only the first jobs have a CTA each (16,384 that end at once take 75 us). (Where no sequence is cut, this launch and the join's end at once, the sooner the fewer CTAs they have:
 // with one for each segment and for each part of the join's columns they took 4.9 us of 16 x 64 tokens and 16 heads, 9.6 of 8 x 1024 and
 // 7.6 of 4 x 2048, and as many as SMs 2.5, 4.8 and 6.0. The outputs' CTAs in rounds as well took 9 to 18 % longer for a chunk: the loop
 // costs registers.)
-template <bool STATES>
+template <bool STATES, bool ROUNDS>
 __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const __grid_constant__ ChunkParams cp) {
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -1163,7 +1136,8 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
         set_up(m);
         m->abort = 0;
     }
-    int index = static_cast<int>(blockIdx.x);
+    const int from = ROUNDS && !STATES ? cp.from : 0;
+    int index = from + static_cast<int>(blockIdx.x);
     let_next_launch();
     wait_for_launch();
     const Segment *segs = STATES ? cp.segs_s : cp.segs;  // (the plan's)
@@ -1175,11 +1149,11 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = m->tmem;
-    walk<STATES>(cp, seg, index % H, smem, m, tmem);
-    if (STATES) {
+    walk<STATES, ROUNDS>(cp, seg, index % H, smem, m, tmem);
+    if (ROUNDS) {
 #pragma unroll 1
         for (int round = 1;; ++round) {
-            index = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            index = from + round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
             if (index >= jobs || m->abort) break;
             if (tid == 0) {  // (every arrival has come)
                 for (uint64_t *bar = m->full; bar <= &m->drained; ++bar) lin::mbar_inval(bar);
@@ -1187,7 +1161,7 @@ __global__ void __launch_bounds__(THREADS, 1) kda_gated_delta_chunk_kernel(const
             }
             seg = segs[index / H];
             __syncthreads();
-            walk<STATES>(cp, seg, index % H, smem, m, tmem);
+            walk<STATES, ROUNDS>(cp, seg, index % H, smem, m, tmem);
         }
     }
     if (tid == 0 && m->abort) set_status(cp.a.status, KDA_ERR_TIMEOUT);
@@ -1338,26 +1312,30 @@ int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
 // Batches of few tokens a sequence run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 64.
 // 16 heads: 256 sequences of 16 tokens 260 us and 281 as chunks, of 24 369 and 286; 64 of 16: 73 and 82, 16 of 16: 21 and 23.
 // A batch of so few tokens on average may hold long sequences among many short ones (prompts among single tokens), and the host does
-// not know: those of more than FEW_LONGEST tokens run as chunks all the same, in launches that end at once where there are none.
+// not know: those of more than FEW_LONGEST tokens run as chunks all the same. The recurrence's launch lists their chunks; where there are none,
+// the launches behind it take 5 us of 16 sequences of 16 tokens, 17 of 256 and 50 of 4096 (16 heads; the sequences themselves 21, 260 and 3990).
 bool few_tokens(int64_t N, int64_t T) { return T <= 16 * N; }
 constexpr int FEW_LONGEST = KDA_DECODE_MAX_TOKENS;  // what the recurrence's own entry point takes
+constexpr int OWN_CTAS = 4;  // of the outputs' pass with a segment of their own, an SM
 int64_t most_long(int64_t N, int64_t T) { return T / (FEW_LONGEST + 1) < N ? T / (FEW_LONGEST + 1) : N; }
 
 struct Layout {
     int64_t slots, segs, cuts;  // of chunks; parts: ceil(c / L) <= c' / L + 1 summed over the sequences; cuts: (c - 1) / L
     int shortest;
-    size_t images, seg, seg_s, cut, states, bytes;
+    size_t images, list, seg, seg_s, cut, states, bytes;
 };
 Layout layout_of(int64_t N, int64_t T, int64_t H, int sms) {
     Layout l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    if (few_tokens(N, T)) N = most_long(N, T);
+    const bool few = few_tokens(N, T);
+    if (few) N = most_long(N, T);
     l.shortest = shortest_cut(N, T, H, sms);
     l.slots = T / C + N;
     l.cuts = l.shortest ? T / (static_cast<int64_t>(C) * l.shortest) : 0;
     l.segs = N + l.cuts;
     l.images = 256;
-    l.seg = up(l.images + static_cast<size_t>(l.slots * H) * IMAGE);
+    l.list = up(l.images + static_cast<size_t>(l.slots * H) * IMAGE);
+    l.seg = up(l.list + (few ? sizeof(int2) * l.slots : 0));
     l.seg_s = up(l.seg + sizeof(Segment) * l.segs);
     l.cut = up(l.seg_s + sizeof(Segment) * 2 * l.cuts);
     l.states = up(l.cut + sizeof(Cuts) * l.cuts);
@@ -1406,16 +1384,14 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.withhold = withhold;
     const bool few = few_tokens(a.N, a.T);
     p.longer = few ? FEW_LONGEST : -1;
-    if (few) {
-        Params short_ones = a;
-        short_ones.longest = FEW_LONGEST;
-        const cudaError_t e = launch_recurrent(short_ones, stream);
-        if (e != cudaSuccess) return e;
-    }
     const Layout l = layout_of(a.N, a.T, a.H, sms);
     p.shortest = l.shortest;
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     p.counts = reinterpret_cast<int32_t *>(ws);
+    int32_t *listed = p.counts + 4;
+    int2 *list = reinterpret_cast<int2 *>(ws + l.list);
+    p.listed = listed;
+    p.list = list;
     p.images = ws + l.images;
     p.slots = l.slots;
     p.sms = sms;
@@ -1423,15 +1399,31 @@ cudaError_t launch_chunked(const Params &a, void *workspace, cudaStream_t stream
     p.segs_s = reinterpret_cast<Segment *>(ws + l.seg_s);
     p.cuts = reinterpret_cast<Cuts *>(ws + l.cut);
     p.states = reinterpret_cast<float *>(ws + l.states);
-    cudaError_t e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H + prep::malformed_ctas(a.N, a.H, sms), prep::THREADS, prep::SMEM, false, p, stream);
+    cudaError_t e = cudaSuccess;
+    if (few) {
+        Params rest = a;
+        rest.longest = FEW_LONGEST;
+        rest.listed = listed;
+        rest.list = list;
+        rest.most = l.slots;
+        e = launch_recurrent(rest, stream);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch(prep::kda_gated_delta_prepare_kernel, 1 + l.slots * a.H + prep::spare_ctas(a.N, a.H, sms), prep::THREADS, prep::SMEM, false, p, stream);
     if (e == cudaSuccess && p.shortest) {
         const int64_t parts = 2 * l.cuts * a.H, joins = (l.cuts < a.N ? l.cuts : a.N) * a.H * join::PARTS;
-        e = launch(walk::kda_gated_delta_chunk_kernel<true>, parts < sms ? parts : sms, walk::THREADS, walk::SMEM, true, p, stream);
+        e = launch(walk::kda_gated_delta_chunk_kernel<true, true>, parts < sms ? parts : sms, walk::THREADS, walk::SMEM, true, p, stream);
         if (e == cudaSuccess)
             e = launch(join::kda_gated_delta_join_kernel, joins < sms ? joins : sms, join::THREADS, sizeof(join::Shared), true, p, stream);
     }
-    return e == cudaSuccess ? launch(walk::kda_gated_delta_chunk_kernel<false>, l.segs * a.H, walk::THREADS, walk::SMEM, true, p, stream)
-                            : e;
+    // (a long sequence among many short ones needs few of the CTAs that there might have to be)
+    const int64_t jobs = l.segs * a.H, own = few && jobs > OWN_CTAS * sms ? OWN_CTAS * sms : jobs;
+    if (e == cudaSuccess) e = launch(walk::kda_gated_delta_chunk_kernel<false, false>, own, walk::THREADS, walk::SMEM, true, p, stream);
+    if (e == cudaSuccess && own < jobs) {
+        p.from = static_cast<int32_t>(own);
+        e = launch(walk::kda_gated_delta_chunk_kernel<false, true>, sms, walk::THREADS, walk::SMEM, true, p, stream);
+    }
+    return e;
 }
 
 }  // namespace delta
