@@ -953,8 +953,9 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
             if (++st == STAGES) st = 0, ++use;
         }
         __syncwarp();
-        if (!ok && lane == 0) {
-            umma_commit(&m->drained);
+        if (!ok) {
+            if (lin::elect_one()) umma_commit(&m->drained);  // (by the lane that issued the MMAs: a commit tracks its own thread's)
+            __syncwarp();
             wait_drain(&m->drained, 0);
         }
         __syncwarp();
