@@ -17,3 +17,10 @@ def test_a_role_that_gives_up_commits_by_the_lane_that_issued(name):
     for line in commits:
         assert re.match(r"\s*if \(lin::elect_one\(\)\) ", line), line
     assert "lane == 0) {\n            umma_commit" not in text
+
+
+def test_no_arrival_is_relaxed():
+    """Who waits on a barrier may rely on what the arriving thread did before: no kernel hands anything over by an arrival without release."""
+    for name in sorted(os.listdir(CSRC)):
+        text = open(os.path.join(CSRC, name), encoding="utf-8").read()
+        assert not re.search(r"mbarrier\.arrive[\w.:]*\.relaxed", text), name
