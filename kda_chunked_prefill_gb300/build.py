@@ -86,30 +86,36 @@ def kernel_stamp(source: str) -> str:
 def build_native(force: bool = False) -> bool:
     """Compile ``_native.so`` against the installed torch; skipped when nothing has
     changed. False, with a note on stderr, where that does not work."""
+    import importlib.util
     import sysconfig
 
-    import torch
-
     os.makedirs(BUILD_DIR, exist_ok=True)
-    where = os.path.dirname(torch.__file__)
-    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, *(f for d in ("include", "include/torch/csrc/api/include") for f in ("-isystem", os.path.join(where, d))),
-           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], NATIVE_SOURCE,
-           "-L" + os.path.join(where, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
-    h = hashlib.sha256((torch.__version__ + sys.version + " ".join(cmd)).encode())
-    for f in (NATIVE_SOURCE, os.path.join(INCLUDE, "kda.h")):
-        with open(f, "rb") as fh:
-            h.update(fh.read())
-    stamp_file = os.path.join(BUILD_DIR, "native_stamp")
-    if not force and os.path.exists(NATIVE_PATH) and os.path.exists(stamp_file) and open(stamp_file).read() == h.hexdigest():
-        return True
-    try:
-        r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
-        failed = r.stderr if r.returncode != 0 else None
-    except OSError as e:
-        failed = str(e)
+    spec = importlib.util.find_spec("torch")  # (found, not imported: an unchanged build does not pay for that)
+    if spec is not None and spec.origin:
+        where = os.path.dirname(spec.origin)
+        cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+        tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", INCLUDE,
+               *(f for d in ("include", "include/torch/csrc/api/include") for f in ("-isystem", os.path.join(where, d))),
+               "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], NATIVE_SOURCE,
+               "-L" + os.path.join(where, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+        h = hashlib.sha256((sys.version + " ".join(cmd)).encode())
+        for f in (NATIVE_SOURCE, os.path.join(INCLUDE, "kda.h"), os.path.join(where, "version.py")):
+            if os.path.exists(f):
+                with open(f, "rb") as fh:
+                    h.update(fh.read())
+        stamp_file = os.path.join(BUILD_DIR, "native_stamp")
+        if not force and os.path.exists(NATIVE_PATH) and os.path.exists(stamp_file) and open(stamp_file).read() == h.hexdigest():
+            return True
+        try:
+            import torch
+            abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+            r = subprocess.run([*cmd, abi, "-o", tmp], capture_output=True, text=True)
+            failed = r.stderr if r.returncode != 0 else None
+        except (OSError, ImportError) as e:
+            failed = str(e)
+    else:
+        failed = "torch is not installed"
     if failed is not None:
         if os.path.exists(NATIVE_PATH):
             os.remove(NATIVE_PATH)
