@@ -16,9 +16,11 @@ length) and f = 2^-24:
                      out) are off by w each, x by w again, and fp32 sums of 128 terms twice by 130 f, together taken as 2^-15:
                      |E_t| <= |k_t| 2^-15 (|x_t| + beta_t (|k| s + 4 |z_t| + 4 |k_t| sum_{s<t} beta_s |k_s| |z_s|)) + 8 f s.
 
-The output adds its own products (the same counts), and in chunks one rounding to bf16 (2^-8) of each of its two operands: the
-response of o_t to z_s, at most |q_t| beta_s |k_s|, with z's second terms (2^-8 of z) left out, and the entry state that q_t
-multiplies, whose column's rounding is at most 2^-8 of it, |q_t| 2^-8 s.
+The output adds its own products (the same counts). In chunks it has two: q_t with the entry state, in two bf16 terms (w of it, |q_t| w s),
+and P T with z, in two terms too (w). P T, the response of o_t to z_s, at most |q_t| beta_s |k_s|, is the one operand that is rounded once to
+bf16 (2^-8); before that P's and T's terms and the product of their second ones, left out, are w each (T's own error is in x's, and so in E).
+Sums of 128 to 256 terms in fp32, truncated, are 2^-15. Together 2^-8 and at most 8 w of the response, here 1.02 x 2^-8 + 4 w (9 w), and 3
+w of the entry state's part, here 4 w: w = 2^-16, 4 w = 2^-14.
 """
 from __future__ import annotations
 
@@ -58,7 +60,7 @@ def recurrence(q, k, v, g, beta, lens, state, scale, chunk=0):
                 z = np.abs(v[t]) + kk * entry
                 local = kk * 2.0 ** -15 * (np.abs(x) + b * (kk * entry + 4 * z + 4 * kk * resp)) + 8 * F * s
                 resp = resp + b * kk * z
-                more = (2.0 ** -8 * 1.02) * (2 * resp + entry) + 2.0 ** -14 * (entry + resp)
+                more = (2.0 ** -8 * 1.02) * resp + 2.0 ** -14 * (entry + resp)
             else:
                 local = F * (8 * s + 150 * b * kk * kk * s + 8 * b * kk * np.abs(v[t]))
                 more = 160 * F * (s + kk * np.abs(x))
