@@ -155,7 +155,9 @@ def _load_native(lib):
     global _native
     try:
         from . import _native as native
-    except ImportError:  # not built, or for another torch: every call takes its general path
+    except ImportError:  # not built: every call takes its general path
+        return
+    if getattr(native, "torch_version", None) != torch.__version__:  # (built against another torch: it would misread tensors)
         return
     native.set_entry(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.kda_gated_rms_norm, lib.kda_scaled_matmul, lib.kda_gated_delta_decode_fwd, lib.kda_gated_delta_chunk_fwd,

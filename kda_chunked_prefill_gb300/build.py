@@ -110,7 +110,8 @@ def build_native(force: bool = False) -> bool:
         try:
             import torch
             abi = f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
-            r = subprocess.run([*cmd, abi, "-o", tmp], capture_output=True, text=True)
+            version = f'-DKDA_TORCH_VERSION="{torch.__version__}"'  # (the binding uses it with no other)
+            r = subprocess.run([*cmd, abi, version, "-o", tmp], capture_output=True, text=True)
             failed = r.stderr if r.returncode != 0 else None
         except (OSError, ImportError) as e:
             failed = str(e)

@@ -47,3 +47,34 @@ def test_a_compiler_that_fails_leaves_the_native_calls_out(tmp_path):
     assert run(tmp_path)[0].startswith("the library True")
     out, err = run(tmp_path, 'Done.returncode, Done.stderr = 1, "no such header"\nopen(os.path.join(b.BUILD_DIR, "native_stamp"), "w").close()')
     assert out == "the library False True False" and "no such header" in err
+
+
+def test_native_calls_of_another_torch_are_not_used():
+    """What was compiled against one torch reads tensors by that one's layout: beside another the general calls are taken."""
+    script = """
+import sys, types, torch
+import kda_chunked_prefill_gb300 as kda
+from kda_chunked_prefill_gb300 import _lib
+used = []
+native = types.ModuleType("kda_chunked_prefill_gb300._native")
+native.set_entry = lambda *a: used.append(len(a))
+{version}
+sys.modules["kda_chunked_prefill_gb300._native"] = kda._native = native
+_lib.load_library(build_if_missing=True)
+print(used, _lib._native is native)
+"""
+    for version, want in (("native.torch_version = torch.__version__", "[5] True"), ("native.torch_version = '1.0.0'", "[] False"),
+                          ("", "[] False")):
+        r = subprocess.run([sys.executable, "-c", script.format(version=version)], capture_output=True, text=True, cwd=ROOT)
+        assert r.returncode == 0 and r.stdout.strip() == want, (version, r.stdout, r.stderr)
+
+
+def test_native_calls_name_their_torch():
+    import pytest
+    import torch
+
+    from kda_chunked_prefill_gb300 import _lib
+    _lib.load_library(build_if_missing=True)
+    if _lib._native is None:
+        pytest.skip("the native calls are not built")
+    assert _lib._native.torch_version == torch.__version__
