@@ -21,6 +21,7 @@
 #include "kda.h"
 #include "kda_checks.h"
 #include "kda_common.cuh"
+#include "kda_e4m3.cuh"
 
 namespace kda {
 namespace addnorm {
@@ -28,13 +29,6 @@ namespace addnorm {
 constexpr float TINY = 7.888609052210118e-31f;  // 2^-100: below it a row counts as zero
 constexpr float E4M3_MAX = 448.f;
 constexpr int NARROW = 4;  // rows of a CTA where a warp takes one
-
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    uint16_t lo, hi;  // saturating, round to nearest even; NaN stays NaN
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
 
 __device__ __forceinline__ void load_weight(const float *p, float (&v)[8]) {
     const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];

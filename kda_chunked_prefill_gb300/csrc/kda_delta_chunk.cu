@@ -26,6 +26,7 @@
 #include "kda_delta.h"
 #include "kda_linear.cuh"
 #include "kda_tensor_map.h"
+#include "kda_waits.cuh"
 
 namespace kda {
 namespace delta {
@@ -773,27 +774,6 @@ struct Misc {
 constexpr int SMEM = OFF_MISC + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(SMEM <= 227 * 1024, "one CTA's shared memory");
 
-// waits of up to 0.1 ms each before a role gives up; and before one that has given up takes its own copies for complete
-constexpr int WAITS = 20000, WAITS_DRAIN = 100;
-__device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    int i = 0;
-#pragma unroll 1
-    while (!lin::mbar_wait_some(bar, parity)) {
-        if (++i == WAITS) *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
-        if (*reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
-    }
-    return true;
-}
-__device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < WAITS_DRAIN && !lin::mbar_wait_some(bar, parity); ++i) {
-    }
-}
-__device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;  // (the warp stays together)
-    return __all_sync(0xffffffffu, wait(m, bar, parity));
-}
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     __syncwarp();
     lin::mbar_arrive_if(bar, (threadIdx.x & 31) == 0);

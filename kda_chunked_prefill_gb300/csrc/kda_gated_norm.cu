@@ -18,6 +18,7 @@
 #include "kda.h"
 #include "kda_checks.h"
 #include "kda_common.cuh"
+#include "kda_e4m3.cuh"
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -36,12 +37,6 @@ using lin::of_bf16;
 using lin::pair;
 using lin::split;
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    uint16_t lo, hi;  // saturating, round to nearest even; NaN stays NaN
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-}
 // read once: past the first cache (4 % less time in turn, 11 % of a call)
 __device__ __forceinline__ uint4 load_once(const void *p) {
     uint4 u;

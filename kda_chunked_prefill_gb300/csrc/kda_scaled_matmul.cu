@@ -33,13 +33,13 @@
 #include "kda_checks.h"
 #include "kda_linear.cuh"
 #include "kda_tensor_map.h"
+#include "kda_waits.cuh"
 
 namespace kda {
 namespace mm {
 
 using lin::f2;
 using lin::mbar_arrive;
-using lin::mbar_wait_some;
 
 constexpr int LANES = 128;  // of an accumulator
 constexpr int KB = 128;     // channels of a block: a row of a stage's tile is 128 bytes
@@ -49,8 +49,6 @@ constexpr int AHEAD = 4;    // blocks whose scales are loaded and handed on at a
 constexpr int SCALES = 2;   // such groups in shared memory
 constexpr int MAX_SPLITS = 8;
 constexpr int SWAP_ROWS = 64;
-// waits of up to 0.1 ms each before a role gives up; and before one that has given up takes its own copies for complete
-constexpr int WAITS = 20000, WAITS_DRAIN = 100;
 
 template <int BN, bool SWAP>
 struct Cfg {
@@ -103,16 +101,6 @@ struct Params {
     int32_t *status;
 };
 
-__device__ __forceinline__ bool wait(Misc *m, uint64_t *bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    int i = 0;
-#pragma unroll 1
-    while (!mbar_wait_some(bar, parity)) {
-        if (++i == WAITS) *reinterpret_cast<volatile int32_t *>(&m->abort) = 1;
-        if (*reinterpret_cast<volatile int32_t *>(&m->abort)) return false;
-    }
-    return true;
-}
 __device__ __forceinline__ bool is_complete(uint64_t *bar, uint32_t parity) {  // (does not wait)
     uint32_t ok;
     asm volatile(
@@ -121,15 +109,6 @@ __device__ __forceinline__ bool is_complete(uint64_t *bar, uint32_t parity) {  /
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
-}
-__device__ __forceinline__ void wait_drain(uint64_t *bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < WAITS_DRAIN && !mbar_wait_some(bar, parity); ++i) {
-    }
-}
-__device__ __forceinline__ bool wait_warp(Misc *m, uint64_t *bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, wait(m, bar, parity));
 }
 __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     __syncwarp();
