@@ -95,3 +95,39 @@ def test_short_sequences_take_the_recurrences_time():
     chunk = best_of(lambda: kda.kda_gated_delta_chunk_fwd(*args, x["cu"], x["s0"], D ** -0.5, o, fs))
     steps = best_of(lambda: kda.kda_gated_delta_decode_fwd(*args, N, x["s0"], D ** -0.5, o, fs))
     assert chunk <= 1.35 * steps, (chunk, steps)
+
+
+def test_a_captured_call_finds_the_long_ones_anew():
+    """The same graph on other bounds: which sequences are long, whether any is, and whether bounds are in order, is found at each replay. Two
+    graphs with workspaces of their own, replayed at once on two streams."""
+    T, N, H = 1500, 300, 2
+    rng = np.random.default_rng(3)
+    batch = lambda *long: [*long, *rng.multinomial(T - sum(long), np.full(N - len(long), 1 / (N - len(long)))).tolist()]
+    batches = [batch(900, 130, 65), batch(), batch(64, 66, 700), [0] * (N - 1) + [T], batch(65)]
+    x = make(batches[0], H, seed=7)
+    names = ("q", "k", "v", "g", "beta")
+    cu = [torch.tensor(np.concatenate([[0], np.cumsum(b)]), dtype=torch.int32, device="cuda") for b in batches]
+    assert all(sum(b) == T and len(b) == N for b in batches)
+    want = [kda.gated_delta_chunk_fwd(*(x[n] for n in names), c, x["s0"], check=True) for c in cu]
+    held, graphs = [cu[0].clone(), cu[1].clone()], []
+    torch.cuda.synchronize()
+    for h in held:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = kda.gated_delta_chunk_fwd(*(x[n] for n in names), h, x["s0"])
+        graphs.append((g, out))
+    bad = cu[2].clone()
+    bad[150] = 10 ** 6
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for i in range(2 * len(cu)):
+        at = [(i + j) % len(cu) for j in range(2)]
+        for h, a in zip(held, at):
+            h.copy_(bad if i == 3 else cu[a])
+        torch.cuda.synchronize()
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, out), a in zip(graphs, at):
+            if i != 3:
+                assert torch.equal(out[0], want[a][0]) and torch.equal(out[1], want[a][1])
