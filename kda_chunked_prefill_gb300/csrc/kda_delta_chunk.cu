@@ -1103,7 +1103,8 @@ __device__ __forceinline__ void walk(const ChunkParams &cp, const Segment &seg, 
 
 // The outputs' CTAs have a segment each; those of the pass over the states, no more of them than SMs, one in each round, there and back,
 // as long ones are listed first. So have those of the outputs' jobs from `from` on: where most sequences run token after token, and the host
-// does not know how many do not, only the first jobs have a CTA each (16,384 that end at once take 75 us). (Where no sequence is cut, this launch and the join's end at once, the sooner the fewer CTAs they have:
+// does not know how many do not, only the first jobs have a CTA each (16,384 that end at once take 75 us). (Where no sequence is cut, this
+// launch and the join's end at once, the sooner the fewer CTAs they have:
 // with one for each segment and for each part of the join's columns they took 4.9 us of 16 x 64 tokens and 16 heads, 9.6 of 8 x 1024 and
 // 7.6 of 4 x 2048, and as many as SMs 2.5, 4.8 and 6.0. The outputs' CTAs in rounds as well took 9 to 18 % longer for a chunk: the loop
 // costs registers.)
@@ -1290,8 +1291,10 @@ int shortest_cut(int64_t N, int64_t T, int64_t H, int sms) {
     return pays ? static_cast<int>(len) : 0;
 }
 
-// Batches of few tokens a sequence run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 64.
-// 16 heads: 256 sequences of 16 tokens 260 us and 281 as chunks, of 24 369 and 286; 64 of 16: 73 and 82, 16 of 16: 21 and 23.
+// Batches of few tokens a sequence run the recurrence, which takes a time for each token where a chunk takes the same for 1 as for 64. In
+// us, the recurrence and chunks: 256 sequences of 8 tokens, 4 heads 47 and 72, of 16 79 and 74, of 24 112 and 75; 16 heads 168 and 262, 275
+// and 268, 386 and 274; 32 heads 315 and 522, 523 and 529, 745 and 534. 1024 of 16, 16 heads 1022 and 1041; 64 of 16, 1, 16 and 96 heads 17
+// and 19, 77 and 70, 397 and 410; 16 of 16, 16 heads 27 and 23 (the furthest from the better).
 // A batch of so few tokens on average may hold long sequences among many short ones (prompts among single tokens), and the host does
 // not know: those of more than FEW_LONGEST tokens run as chunks all the same. The recurrence's launch lists their chunks; where there are none,
 // the launches behind it take 5 us of 16 sequences of 16 tokens, 17 of 256 and 50 of 4096 (16 heads; the sequences themselves 21, 260 and 3990).

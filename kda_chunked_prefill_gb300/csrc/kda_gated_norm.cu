@@ -10,8 +10,8 @@
 //
 // Bound by memory: 5 bytes per channel with bf16 x (2 + 2 in, 1 out), 7 with fp32. The sigmoid is the hardware's 2^x and reciprocal (a
 // few units in the last place; expf and an IEEE division made the kernel wait for its instructions, 53 an element). 8192 tokens, 16 heads,
-// bf16, in turn on six sets of tensors: 14.6 us, 5.8 TB/s of a copy's 6.65, in 6.7 waves of CTAs that each load, reduce and store once
-// (CTAs of 256 threads 15.8, of 512 16.5).
+// bf16, in turn on six sets of tensors: 16.2 us, 5.2 TB/s of a copy's 6.65 (on one set, partly from L2, 13.5; fp32 20.8 and 17.6), in 6.7
+// waves of CTAs that each load, reduce and store once (CTAs of 256 threads were 8 % slower, of 512 13 %).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -23,7 +23,8 @@
 // MMAs take 512; of a pair, each CTA needs 32 KB, 610. The two halves of the columns have barriers of their own.
 //
 // What bounds it. Many rows: the round trip of the accumulators, two of which fill tensor memory (read by the sums' warps, arrival at the
-// first CTA, MMAs, commit to both), 800 cycles a block: 8192 rows, 2048 channels to 6144 outputs 78 us, 2.65 PFLOP/s. (Columns in one
+// first CTA, MMAs, commit to both), 800 cycles a block: 8192 rows, 2048 channels to 6144 outputs 78 us at 2070 MHz, 2.65 PFLOP/s, and 85 to 88
+// after some tens of milliseconds of it, when the power cap holds the SMs at 1800 to 1940 MHz, replayed or not. (At the full clock: columns in one
 // piece 88 us; one CTA's tiles 86; the pair without the sums 73; sixteen warps for the sums 92.) Few rows: reading the weight (7 rows, 12288
 // to 12288: 28 us, 5.4 TB/s).
 #include <cuda_bf16.h>
@@ -600,9 +601,20 @@ cudaError_t launch(Params &p, const void *x, const void *w, int64_t width, int s
 struct Choice {
     int bn, splits;
 };
-// The least estimated time, in cycles, from measurements (8192 rows, 2048 channels to 6144 outputs: pairs' tiles of 256 columns 78 us, of 128
-// 118, of 64 139; 256 rows to 6176: 11.3, 8.8 and 10.1 us): rounds of CTAs x (blocks x a block's time + a tile's start and end). Up to 64
-// rows, the splits of a tile that keep the busiest SM's blocks fewest (7 rows, 12288 to 12288: one 30.2 us, two 28.5, three 27.8, four 33.0).
+// The least estimated time, in cycles: rounds of CTAs x (blocks x a block's time + a tile's start and end). It is there to order the choices
+// and is below what a call takes, most of all for few rows, where reading the weight is not in it. Measured, us a call, in turn on sets of
+// tensors larger than L2, * what is taken:
+//   rows, channels to outputs    tiles of 64   128    256      rows, channels to outputs    splits 1    2     3     4     5     6     8
+//   8192,  2048 to  6144            134.2   111.2   80.5*        7, 12288 to 12288             31.0  29.9  28.7*
+//   8192,  2048 to  2048             49.4    40.4   33.0*        7,  8192 to  1024             17.0  11.8   9.4   8.0   7.5   6.9   6.0*
+//  16384,  1024 to  1024             29.3    24.8   21.9*       16,  4096 to  4096             11.3   9.6   8.7   8.2*  9.0   9.2   8.9
+//   3000,  1024 to 12288             58.7    49.7   38.3*       30, 12288 to  2048             26.5  17.5  13.7  12.0  11.1  10.6  11.2*
+//   1024,  2048 to  6144             23.2    20.0   20.1*       32,  4096 to  4096             12.1  10.7   9.4   8.9*  9.8   9.8   9.6
+//   1024,  2048 to  2048             10.5     9.4*  11.8        64, 12288 to  2048             34.0  22.8  17.1  14.5  13.1  12.4  13.4*
+//    512,  2048 to  2048              8.8*    8.7   10.9        64,  2048 to 12288             11.4* 14.6  13.4
+//    256,  2048 to  6176             11.1     9.6*  13.0        64,  2048 to  6176             10.3  11.0  11.5* 10.3  10.1  14.3
+//    128, 12288 to  2048             37.1*   31.1   43.0        50,  8192 to  8192             25.2  21.3* 20.0  18.8
+// At most 8 % from the best but for the last two of the right and the last of the left (13 to 19 %).
 Choice choose(int64_t rows, int64_t outs, int blocks, int sms) {
     auto over = [](int64_t a, int64_t b) { return (a - 1) / b + 1; };
     Choice best{0, 1};
